@@ -224,8 +224,7 @@ def prepare(case, seed):
     s["workspace"] = None
     if own:
         import gated_deltanet_delta_gb300 as gdn
-        s["workspace"] = torch.empty(gdn.attn_paged_workspace_size(case["seqs"], sum(new), case["hq"], case["hkv"], case["dim"]),
-                                     dtype=torch.uint8, device="cuda")
+        s["workspace"] = torch.empty(gdn.attn_paged_workspace_size(case["dim"]), dtype=torch.uint8, device="cuda")
     return s
 
 
