@@ -582,3 +582,229 @@ extern "C" gdn_status gdn_prefill_chunked_noalloc(const void* q, const void* k, 
                                num_seqs, T, Hk, Hv, K, V, chunk_size, scale, out, g_scratch_ptr[dev],
                                kNoallocScratchBytes, dev_status, stream);
 }
+
+// ------------------------------------------------------------------------------------------------
+// the paged attention cache, attention over it, and draft verification
+static bool attn_dim_ok(int D) { return D == 64 || D == 128 || D == 256; }
+
+// What attn_cache_write, attn_cache_read and attn_paged ask of their cache.
+static gdn_status cache_check(const char* fn, const void* kc, const void* vc, const float* ks, const float* vs,
+                              gdn_dtype cache_dtype, gdn_dtype dtype, int64_t num_pages, int page_size, int Hkv,
+                              int D, const int32_t* dev_status, size_t* bytes) {
+    REQUIRE(dtype == GDN_BF16 || dtype == GDN_F16, GDN_ERR_INVALID_ARG, "%s: dtype must be GDN_BF16 or GDN_F16", fn);
+    REQUIRE(cache_dtype == dtype || cache_dtype == GDN_E4M3, GDN_ERR_INVALID_ARG,
+            "%s: cache_dtype must be dtype or GDN_E4M3", fn);
+    REQUIRE(attn_dim_ok(D), GDN_ERR_UNSUPPORTED, "%s: D must be 64, 128 or 256 (got %d)", fn, D);
+    REQUIRE(Hkv <= 65535, GDN_ERR_UNSUPPORTED, "%s: at most 65535 heads (got %d)", fn, Hkv);
+    REQUIRE(kc && vc && dev_status, GDN_ERR_INVALID_ARG, "%s: null pointer", fn);
+    REQUIRE(aligned(kc, 16) && aligned(vc, 16) && aligned(dev_status, 4), GDN_ERR_INVALID_ARG,
+            "%s: caches must be 16-byte aligned", fn);
+    if (cache_dtype == GDN_E4M3)
+        REQUIRE(ks && vs && aligned(ks, 4) && aligned(vs, 4), GDN_ERR_INVALID_ARG,
+                "%s: an 8-bit cache needs k_scale and v_scale", fn);
+    else
+        REQUIRE(!ks && !vs, GDN_ERR_INVALID_ARG, "%s: a cache of dtype has no scales", fn);
+    const long long rows_per_page = static_cast<long long>(Hkv) * page_size;
+    REQUIRE(num_pages <= (1LL << 52) / (rows_per_page * D), GDN_ERR_UNSUPPORTED, "%s: cache too large", fn);
+    *bytes = static_cast<size_t>(num_pages) * rows_per_page * D * (cache_dtype == GDN_E4M3 ? 1 : 2);
+    return GDN_OK;
+}
+
+extern "C" gdn_status attn_cache_write(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                                       gdn_dtype dtype, const int64_t* slots, int64_t T, void* k_cache,
+                                       void* v_cache, float* k_scale, float* v_scale, gdn_dtype cache_dtype,
+                                       int64_t num_pages, int page_size, int Hkv, int D, int32_t* dev_status,
+                                       gdn_stream_t stream) {
+    const char* fn = "attn_cache_write";
+    REQUIRE(T >= 0 && num_pages >= 0 && page_size >= 1 && Hkv >= 1, GDN_ERR_INVALID_ARG,
+            "%s: sizes must be T, num_pages >= 0 and page_size, Hkv >= 1", fn);
+    if (T == 0) return GDN_OK;
+    size_t cb = 0;
+    const gdn_status s = cache_check(fn, k_cache, v_cache, k_scale, v_scale, cache_dtype, dtype, num_pages, page_size,
+                                     Hkv, D, dev_status, &cb);
+    if (s != GDN_OK) return s;
+    REQUIRE(k && v && slots, GDN_ERR_INVALID_ARG, "%s: null pointer", fn);
+    const long long row = static_cast<long long>(Hkv) * D;
+    REQUIRE(k_stride >= row && v_stride >= row && k_stride % 8 == 0 && v_stride % 8 == 0, GDN_ERR_INVALID_ARG,
+            "%s: token strides must be multiples of 8 and at least Hkv * D", fn);
+    REQUIRE(aligned(k, 16) && aligned(v, 16) && aligned(slots, 8), GDN_ERR_INVALID_ARG,
+            "%s: k and v must be 16-byte aligned", fn);
+    REQUIRE(T < (1LL << 31) && k_stride < (1LL << 31) && v_stride < (1LL << 31), GDN_ERR_UNSUPPORTED,
+            "%s: T and the strides must be below 2^31", fn);
+    const size_t kb = (static_cast<size_t>(T - 1) * k_stride + row) * 2, vb = (static_cast<size_t>(T - 1) * v_stride + row) * 2;
+    REQUIRE(!any_overlap(k_cache, cb, v_cache, cb) && !any_overlap(k, kb, k_cache, cb) && !any_overlap(k, kb, v_cache, cb) &&
+                !any_overlap(v, vb, k_cache, cb) && !any_overlap(v, vb, v_cache, cb),
+            GDN_ERR_INVALID_ARG, "%s: the caches overlap each other or the sources", fn);
+    gdn::CacheMoveArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.k_in = static_cast<const uint16_t*>(k);
+    a.v_in = static_cast<const uint16_t*>(v);
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.kc = k_cache;
+    a.vc = v_cache;
+    a.ks = k_scale;
+    a.vs = v_scale;
+    a.slots = slots;
+    a.status = dev_status;
+    a.T = T;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.H = Hkv;
+    gdn::launch_cache_write(a, D, dtype == GDN_F16, cache_dtype == GDN_E4M3, static_cast<cudaStream_t>(stream));
+    return launched(fn);
+}
+
+extern "C" gdn_status attn_cache_read(const void* k_cache, const void* v_cache, const float* k_scale,
+                                      const float* v_scale, gdn_dtype cache_dtype, int64_t num_pages, int page_size,
+                                      const int64_t* page_table, int max_pages, const int64_t* cu_seqlens,
+                                      int num_seqs, int64_t T, int Hkv, int D, void* k, void* v, gdn_dtype dtype,
+                                      int32_t* dev_status, gdn_stream_t stream) {
+    const char* fn = "attn_cache_read";
+    REQUIRE(T >= 0 && num_seqs >= 0 && num_pages >= 0 && max_pages >= 0 && page_size >= 1 && Hkv >= 1,
+            GDN_ERR_INVALID_ARG, "%s: sizes must be T, num_seqs, num_pages, max_pages >= 0 and page_size, Hkv >= 1", fn);
+    if (T == 0 || num_seqs == 0) return GDN_OK;
+    size_t cb = 0;
+    const gdn_status s = cache_check(fn, k_cache, v_cache, k_scale, v_scale, cache_dtype, dtype, num_pages, page_size,
+                                     Hkv, D, dev_status, &cb);
+    if (s != GDN_OK) return s;
+    REQUIRE(k && v && cu_seqlens && (page_table || max_pages == 0), GDN_ERR_INVALID_ARG, "%s: null pointer", fn);
+    REQUIRE(aligned(k, 16) && aligned(v, 16) && aligned(cu_seqlens, 8) && aligned(page_table, 8), GDN_ERR_INVALID_ARG,
+            "%s: k and v must be 16-byte aligned", fn);
+    REQUIRE(T < (1LL << 31), GDN_ERR_UNSUPPORTED, "%s: T must be below 2^31", fn);
+    const size_t ob = static_cast<size_t>(T) * Hkv * D * 2;
+    REQUIRE(!any_overlap(k, ob, v, ob) && !any_overlap(k, ob, k_cache, cb) && !any_overlap(k, ob, v_cache, cb) &&
+                !any_overlap(v, ob, k_cache, cb) && !any_overlap(v, ob, v_cache, cb),
+            GDN_ERR_INVALID_ARG, "%s: the outputs overlap each other or the caches", fn);
+    gdn::CacheMoveArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.k_out = static_cast<uint16_t*>(k);
+    a.v_out = static_cast<uint16_t*>(v);
+    a.kc = const_cast<void*>(k_cache);
+    a.vc = const_cast<void*>(v_cache);
+    a.ks = const_cast<float*>(k_scale);
+    a.vs = const_cast<float*>(v_scale);
+    a.table = page_table;
+    a.cu = cu_seqlens;
+    a.status = dev_status;
+    a.T = T;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.max_pages = max_pages;
+    a.num_seqs = num_seqs;
+    a.H = Hkv;
+    gdn::launch_cache_read(a, D, dtype == GDN_F16, cache_dtype == GDN_E4M3, static_cast<cudaStream_t>(stream));
+    return launched(fn);
+}
+
+extern "C" size_t attn_paged_workspace_size(int D) { return attn_dim_ok(D) ? gdn::attn_workspace_bytes(D) : 0; }
+
+extern "C" gdn_status attn_paged(const void* q, int64_t q_stride, gdn_dtype dtype, const void* k_cache,
+                                 const void* v_cache, const float* k_scale, const float* v_scale,
+                                 gdn_dtype cache_dtype, int64_t num_pages, int page_size, const int64_t* page_table,
+                                 int max_pages, const int64_t* kv_lens, const int64_t* cu_seqlens, int num_seqs,
+                                 int64_t T, int64_t max_q, int Hq, int Hkv, int D, float scale, void* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, int32_t* dev_status, gdn_stream_t stream) {
+    const char* fn = "attn_paged";
+    REQUIRE(T >= 0 && num_seqs >= 0 && num_pages >= 0 && max_pages >= 0 && max_q >= 0 && page_size >= 1 && Hq >= 1 &&
+                Hkv >= 1,
+            GDN_ERR_INVALID_ARG,
+            "%s: sizes must be T, max_q, num_seqs, num_pages, max_pages >= 0 and page_size, Hq, Hkv >= 1", fn);
+    REQUIRE(Hq % Hkv == 0, GDN_ERR_INVALID_ARG, "%s: Hq (%d) must be a multiple of Hkv (%d)", fn, Hq, Hkv);
+    REQUIRE(Hq / Hkv <= 16, GDN_ERR_UNSUPPORTED, "%s: Hq / Hkv must be at most 16 (got %d)", fn, Hq / Hkv);
+    if (T == 0 || num_seqs == 0) return GDN_OK;
+    size_t cb = 0;
+    const gdn_status s = cache_check(fn, k_cache, v_cache, k_scale, v_scale, cache_dtype, dtype, num_pages, page_size,
+                                     Hkv, D, dev_status, &cb);
+    if (s != GDN_OK) return s;
+    REQUIRE(q && out && kv_lens && cu_seqlens && (page_table || max_pages == 0), GDN_ERR_INVALID_ARG,
+            "%s: null pointer", fn);
+    REQUIRE(q_stride >= static_cast<int64_t>(Hq) * D && q_stride % 8 == 0 && q_stride < (1LL << 31), GDN_ERR_INVALID_ARG,
+            "%s: q_stride must be a multiple of 8, at least Hq * D and below 2^31", fn);
+    REQUIRE(aligned(q, 16) && aligned(out, 16) && aligned(lse, 4) && aligned(kv_lens, 8) && aligned(cu_seqlens, 8) &&
+                aligned(page_table, 8),
+            GDN_ERR_INVALID_ARG, "%s: q and out must be 16-byte aligned", fn);
+    REQUIRE(T < (1LL << 30) && static_cast<long long>(max_pages) * page_size < (1LL << 31), GDN_ERR_UNSUPPORTED,
+            "%s: T must be below 2^30 and max_pages * page_size below 2^31", fn);
+    const size_t need = gdn::attn_workspace_bytes(D);
+    REQUIRE(workspace && workspace_bytes >= need, GDN_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed (got %zu)", fn,
+            need, workspace ? workspace_bytes : size_t(0));
+    REQUIRE(aligned(workspace, 16), GDN_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
+    const size_t ob = static_cast<size_t>(T) * Hq * D * 2, lb = lse ? static_cast<size_t>(T) * Hq * 4 : 0;
+    const size_t qb = (static_cast<size_t>(T - 1) * q_stride + static_cast<size_t>(Hq) * D) * 2;
+    REQUIRE(!any_overlap(out, ob, q, qb) && !any_overlap(out, ob, workspace, need) && !any_overlap(out, ob, lse, lb) &&
+                !any_overlap(out, ob, k_cache, cb) && !any_overlap(out, ob, v_cache, cb) &&
+                !any_overlap(lse, lb, workspace, need) && !any_overlap(workspace, need, q, qb) &&
+                !any_overlap(workspace, need, k_cache, cb) && !any_overlap(workspace, need, v_cache, cb),
+            GDN_ERR_INVALID_ARG, "%s: out, lse or workspace overlaps another buffer", fn);
+    gdn::AttnArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.q = static_cast<const uint16_t*>(q);
+    a.q_stride = q_stride;
+    a.kc = k_cache;
+    a.vc = v_cache;
+    a.ks = k_scale;
+    a.vs = v_scale;
+    a.table = page_table;
+    a.kv_lens = kv_lens;
+    a.cu = cu_seqlens;
+    a.out = out;
+    a.lse = lse;
+    a.part = static_cast<float*>(workspace);
+    a.status = dev_status;
+    a.T = T;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.max_pages = max_pages;
+    a.num_seqs = num_seqs;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.G = Hq / Hkv;
+    a.f16 = dtype == GDN_F16;
+    a.scale_log2 = scale * 1.44269504088896340736f;
+    int sh = 0;
+    while ((1LL << sh) < page_size) ++sh;
+    a.page_mul = static_cast<uint32_t>(((1ULL << (31 + sh)) + page_size - 1) / page_size);
+    a.page_shift = 31 + sh;
+    const cudaError_t e =
+        gdn::launch_attn(a, D, cache_dtype == GDN_E4M3, max_q, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+    return launched(fn);
+}
+
+extern "C" gdn_status draft_verify(const float* target_p, const float* draft_p, const int64_t* drafts,
+                                   const int64_t* num_drafts, const float* u_accept, const float* u_sample, int N,
+                                   int T, int V, int64_t* accepted, int64_t* tokens, int32_t* dev_status,
+                                   gdn_stream_t stream) {
+    const char* fn = "draft_verify";
+    REQUIRE(N >= 0 && T >= 0 && V >= 1, GDN_ERR_INVALID_ARG, "%s: sizes must be N, T >= 0 and V >= 1", fn);
+    REQUIRE(V <= (1 << 20), GDN_ERR_UNSUPPORTED, "%s: V must be at most 2^20 (got %d)", fn, V);
+    REQUIRE(N < (1 << 28), GDN_ERR_UNSUPPORTED, "%s: N must be below 2^28", fn);
+    if (N == 0) return GDN_OK;
+    REQUIRE(target_p && u_sample && accepted && tokens && dev_status && (T == 0 || (draft_p && drafts && u_accept)),
+            GDN_ERR_INVALID_ARG, "%s: null pointer", fn);
+    REQUIRE(aligned(target_p, 4) && aligned(draft_p, 4) && aligned(drafts, 8) && aligned(num_drafts, 8) &&
+                aligned(u_accept, 4) && aligned(u_sample, 4) && aligned(accepted, 8) && aligned(tokens, 8) &&
+                aligned(dev_status, 4),
+            GDN_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+    const size_t tb = static_cast<size_t>(N) * (T + 1) * 8;
+    REQUIRE(!any_overlap(tokens, tb, drafts, static_cast<size_t>(N) * T * 8) &&
+                !any_overlap(tokens, tb, accepted, static_cast<size_t>(N) * 8),
+            GDN_ERR_INVALID_ARG, "%s: tokens overlaps drafts or accepted", fn);
+    gdn::VerifyArgs a;
+    a.target = target_p;
+    a.draft = draft_p;
+    a.drafts = drafts;
+    a.num_drafts = num_drafts;
+    a.u_accept = u_accept;
+    a.u_sample = u_sample;
+    a.accepted = accepted;
+    a.tokens = tokens;
+    a.status = dev_status;
+    a.N = N;
+    a.T = T;
+    a.V = V;
+    const cudaError_t e = gdn::launch_verify(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+    return launched(fn);
+}

@@ -1,0 +1,95 @@
+// attn.cu -- launch of attention over a paged cache: choice of the kernel and of its grid.
+#include <algorithm>
+#include <atomic>
+
+#include "attn_rows.cuh"
+#include "launch.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kMaxDevices = 64;
+constexpr int kMaxCtas = 608;  // the workspace has two partial slots for each
+std::atomic<int> g_sms[kMaxDevices];
+
+cudaError_t sm_count(int* n) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    *n = g_sms[dev].load(std::memory_order_acquire);
+    if (*n == 0) {
+        e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        g_sms[dev].store(*n, std::memory_order_release);
+    }
+    return cudaSuccess;
+}
+
+// Raises a kernel's shared-memory limit once per device.
+template <typename K>
+cudaError_t raise_smem(K kernel, int bytes, std::atomic<unsigned long long>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (done.load(std::memory_order_acquire) >> dev & 1) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(1ull << dev, std::memory_order_release);
+    return e;
+}
+
+// The joining kernel starts while the main kernel still runs (programmatic dependent launch) and waits
+// for it before it reads the partials.
+template <int BN>
+cudaError_t launch_combine(const AttnArgs& a, int R, int D, int grid, cudaStream_t stream) {
+    const int RB = 4;
+    if (grid < 2) return cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid - 1, (R + RB - 1) / RB);
+    cfg.blockDim = dim3(attn::kCombineThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn::attn_combine_kernel<BN>, a, R, D, RB, grid);
+}
+
+template <int D, bool F16, bool F8>
+cudaError_t launch_rows(AttnArgs a, cudaStream_t stream) {
+    using C = attn::RowsCfg<D, F8>;
+    static std::atomic<unsigned long long> done{0};
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e == cudaSuccess) e = raise_smem(attn::attn_rows_kernel<D, F16, F8>, C::SMEM, done);
+    if (e != cudaSuccess) return e;
+    a.tq = std::max(1, attn::kRowsTile / a.G);
+    a.min_tiles = 2;
+    const int grid = std::min(sms * C::OCC, kMaxCtas);
+    attn::attn_rows_kernel<D, F16, F8><<<grid, attn::kRowsNT, C::SMEM, stream>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_combine<attn::kRowsBN>(a, attn::kRowsTile, D, grid, stream);
+}
+
+template <int D>
+cudaError_t launch_d(const AttnArgs& a, bool f8, cudaStream_t stream) {
+    if (a.f16) return f8 ? launch_rows<D, true, true>(a, stream) : launch_rows<D, true, false>(a, stream);
+    return f8 ? launch_rows<D, false, true>(a, stream) : launch_rows<D, false, false>(a, stream);
+}
+}  // namespace
+
+size_t attn_workspace_bytes(int D) {
+    return static_cast<size_t>(kMaxCtas) * 2 * attn::kRowsTile * (D + 2) * sizeof(float);
+}
+
+cudaError_t launch_attn(const AttnArgs& a, int D, bool f8, int max_q, cudaStream_t stream) {
+    (void)max_q;
+    if (D == 64) return launch_d<64>(a, f8, stream);
+    if (D == 128) return launch_d<128>(a, f8, stream);
+    return launch_d<256>(a, f8, stream);
+}
+
+}  // namespace gdn

@@ -1,0 +1,377 @@
+// attn_rows.cuh -- attn_paged for few query rows per key head (single tokens): tiles of 16 rows.
+//
+// Bound: the cache is read once from HBM and each key row meets at most 16 query rows, about 16
+// operations per byte, so the time is the bytes' time.  What the kernel has to do is keep enough of
+// them in flight and stay out of their way.  Hence: four independent warps per CTA, each with its own
+// ring of cp.async stages of 16 keys (no block barrier inside a unit); warp w takes keys 16 w .. 16 w + 15
+// of each 64-key tile and keeps its own reference, sum and accumulator, joined once per unit through
+// shared memory.  The products run on mma.sync m16n8k16: its 16 rows are the whole tile, whereas a
+// tcgen05.mma would compute 128 rows for them and add a TMEM round trip per tile.
+//
+// 8-bit caches (F8): e4m3 values widen exactly to binary16, so both products run on binary16 operands.
+// A query row is first multiplied by a power of two that brings its largest element to 2^13 .. 2^14
+// (bf16 elements down to 2^-27 of the row's largest stay exact); the power, the key's scale and the
+// softmax scale multiply the fp32 product.  The value's scale moves into the exponent,
+//     p'_j = 2^{y_j + log2(vs_j) - ref},   l = sum p'_j / vs_j,   acc = sum p'_j v_j,
+// so that p' fits binary16 whatever the scales' sizes are.
+#pragma once
+
+#include "attn.cuh"
+#include "attn_mma.cuh"
+
+namespace gdn {
+namespace attn {
+
+constexpr int kRowsTile = 16;   // rows per query tile
+constexpr int kRowsBN = 64;     // keys per tile: 16 per warp
+constexpr int kRowsNT = 128;
+
+template <int D, bool F8>
+struct RowsCfg {
+    static constexpr int ROWB = F8 ? D : 2 * D;               // bytes per cached row
+    static constexpr int CH = ROWB / 16;                      // 16-byte chunks per row
+    static constexpr int STAGE = 2 * 16 * ROWB + (F8 ? 128 : 0);  // K rows, V rows, scales
+    // stages per warp: about 100 KB per CTA, two CTAs per SM
+    static constexpr int NS = D == 256 ? (F8 ? 3 : 3) : (D == 128 ? (F8 ? 4 : 3) : (F8 ? 6 : 4));
+    static constexpr int RING = NS * STAGE * 4;
+    static constexpr int MERGE = 4 * 16 * D * 4;
+    static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+    static constexpr int OCC = D == 256 ? (F8 ? 2 : 1) : (D == 128 ? (F8 ? 3 : 2) : 3);
+};
+
+// 16-byte chunk c of row r of a stage: rows are XOR-swizzled so that eight rows at one chunk column, or
+// eight consecutive chunks, fall on different banks.
+template <int CH>
+__device__ __forceinline__ int rows_swz(int r, int c) {
+    return CH >= 8 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3));
+}
+
+template <int D, bool F16, bool F8>
+__global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel(const __grid_constant__ AttnArgs a) {
+    using C = RowsCfg<D, F8>;
+    constexpr bool MF16 = F16 || F8;  // operand type of the products
+    constexpr int BN = kRowsBN, NS = C::NS, CH = C::CH, KS = D / 16;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ PlanSmem plan;
+    __shared__ float m_s[4][16], l_s[4][16];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;  // fragment row and column group
+
+    long long w0;
+    const long long W = plan_total<BN, kRowsNT>(a, plan, w0, blockIdx.x == 0);
+    pdl_launch();
+    const long long per = max((W + gridDim.x - 1) / static_cast<long long>(gridDim.x), static_cast<long long>(a.min_tiles));
+    long long at = blockIdx.x * per;
+    if (at >= W) return;
+    const long long end = min(at + per, W);
+    Place p = locate<BN, kRowsNT>(a, plan, w0, at);
+
+    uint8_t* ring = smem + warp * (NS * C::STAGE);
+    const uint32_t ring_a = smem_addr(ring);
+    float* merge = reinterpret_cast<float*>(smem);
+
+    for (;;) {
+        const int t0 = p.tile;
+        const int t1 = static_cast<int>(min(static_cast<long long>(p.nk), t0 + (end - at)));
+        const int i0 = p.qt * a.tq;
+        const int ntok = min(a.tq, p.s.m - i0), rows = ntok * a.G;
+        const int vis0 = p.s.L - p.s.m + i0 + 1;      // keys that token i0 sees
+        const int kend = min(t1 * BN, vis0 + ntok - 1);  // one past the last key of this segment
+
+        // ---- query fragments: rows g and g + 8 ----
+        uint32_t qf[KS][4];
+        float rscale[2];
+        int vis[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int r = g + 8 * half;
+            const bool live = r < rows;
+            const int tok = live ? r / a.G : 0;
+            vis[half] = live ? vis0 + tok : 0;
+            const uint16_t* src = a.q + (p.s.q0 + i0 + tok) * a.q_stride + static_cast<long long>(p.h * a.G + (live ? r - tok * a.G : 0)) * D;
+            rscale[half] = a.scale_log2;
+            if constexpr (!F8) {
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    const uint32_t* s32 = reinterpret_cast<const uint32_t*>(src + k * 16 + t * 2);
+                    qf[k][half] = live ? s32[0] : 0u;
+                    qf[k][half + 2] = live ? s32[4] : 0u;
+                }
+            } else {
+                // K step 4 kk + j holds, in thread column group t, features kk 64 + t 16 + 4 j + 0 .. 3
+                float mx = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < D / 64; ++kk) {
+                    uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                    if (live) {
+                        w[0] = *reinterpret_cast<const uint4*>(src + kk * 64 + t * 16);
+                        w[1] = *reinterpret_cast<const uint4*>(src + kk * 64 + t * 16 + 8);
+                    }
+                    const uint32_t* x = reinterpret_cast<const uint32_t*>(w);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        qf[4 * kk + j][half] = x[2 * j];
+                        qf[4 * kk + j][half + 2] = x[2 * j + 1];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float2 f = unpack2<F16>(x[2 * j + i]);
+                            mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+                        }
+                    }
+                }
+                mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 2));
+                const float up = row_up(mx);
+                rscale[half] *= 1.f / up;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 f = unpack2<F16>(qf[k][half + 2 * i]);
+                        qf[k][half + 2 * i] = pack2<true>(f.x * up, f.y * up);
+                    }
+                }
+            }
+        }
+
+        float o[D / 8][4];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        float ref[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
+
+        // ---- this warp's steps: keys (t0 + s) 64 + warp 16 .. + 15, while any is below kend ----
+        const int first = t0 * BN + warp * 16;
+        const int steps = kend > first ? (kend - first + BN - 1) / BN : 0;
+        auto fetch_off = [&](int s) -> long long {  // row offset of this lane's key of step s
+            const int pos = first + s * BN + (lane & 15);
+            return s < steps && pos < kend ? row_of(a, p.n, p.h, pos) : -1;
+        };
+        long long off = fetch_off(0);
+        auto issue = [&](int s) {
+            if (s < steps) {
+                const uint32_t dst = ring_a + (s % NS) * C::STAGE;
+                if constexpr (F8) {
+                    const float* sc = lane < 16 ? a.ks : a.vs;
+                    cp_async4(dst + 32 * C::ROWB + lane * 4, sc + (off < 0 ? 0 : off), off >= 0);
+                }
+#pragma unroll
+                for (int i = 0; i < CH / 2; ++i) {
+                    const int idx = i * 32 + lane, r = idx / CH, c = idx % CH;
+                    const long long ro = __shfl_sync(kFullMask, off, r);
+                    const long long byte = (ro < 0 ? 0 : ro * C::ROWB) + c * 16;
+                    const uint32_t d = dst + r * C::ROWB + rows_swz<CH>(r, c) * 16;
+                    cp_async16(d, static_cast<const uint8_t*>(a.kc) + byte, ro >= 0);
+                    cp_async16(d + 16 * C::ROWB, static_cast<const uint8_t*>(a.vc) + byte, ro >= 0);
+                }
+                off = fetch_off(s + 1);
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int s = 0; s < NS - 1; ++s) issue(s);
+
+        for (int s = 0; s < steps; ++s) {
+            cp_async_wait<NS - 2>();
+            __syncwarp();
+            issue(s + NS - 1);  // into the stage that the previous step has read
+            const uint32_t kst = ring_a + (s % NS) * C::STAGE, vst = kst + 16 * C::ROWB;
+
+            float sc[2][4] = {};
+            if constexpr (!F8) {
+                const int mi = lane >> 3, tok = (mi >> 1) * 8 + (lane & 7);
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    uint32_t b[4];
+                    ldsm4(b, kst + tok * C::ROWB + rows_swz<CH>(tok, 2 * k + (mi & 1)) * 16);
+                    mma16816<MF16>(sc[0], qf[k], b[0], b[1]);
+                    mma16816<MF16>(sc[1], qf[k], b[2], b[3]);
+                }
+            } else {
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const int tok = nt * 8 + g;
+#pragma unroll
+                    for (int kk = 0; kk < D / 64; ++kk) {
+                        uint4 w = lds128(kst + tok * C::ROWB + rows_swz<CH>(tok, kk * 4 + t) * 16);
+                        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma16816<true>(sc[nt], qf[4 * kk + j], e4m3x2_f16x2(x[j]), e4m3x2_f16x2(x[j] >> 16));
+                    }
+                }
+            }
+
+            // ---- y = s log2(e), masked; 8-bit values: plus log2 of the value's scale ----
+            const int base = first + s * BN;
+            float lv[2][2], iv[2][2];
+            if constexpr (F8) {
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int tok = nt * 8 + 2 * t + i;
+                        const float ks = lds32(kst + 32 * C::ROWB + tok * 4), vs = lds32(kst + 32 * C::ROWB + 64 + tok * 4);
+                        // the stage's rows past the segment's end hold zeros, scale included
+                        const bool in = base + tok < kend;
+                        lv[nt][i] = in ? log2f(vs) : 0.f;
+                        iv[nt][i] = in ? 1.f / vs : 0.f;
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+                            sc[nt][2 * half + i] = fmaf(sc[nt][2 * half + i] * rscale[half], ks, lv[nt][i]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sc[nt][i] *= a.scale_log2;
+            }
+            if (base + 16 > vis0 || base + 16 > kend) {
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int pos = base + nt * 8 + 2 * t + (i & 1);
+                        if (pos >= vis[i >> 1] || pos >= kend) sc[nt][i] = -INFINITY;
+                    }
+            }
+            float mx[2], use[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float x = fmaxf(fmaxf(sc[0][2 * half], sc[0][2 * half + 1]), fmaxf(sc[1][2 * half], sc[1][2 * half + 1]));
+                x = fmaxf(x, __shfl_xor_sync(kFullMask, x, 1));
+                mx[half] = fmaxf(x, __shfl_xor_sync(kFullMask, x, 2));
+            }
+            // rows move their reference when a score is kRefSlack above it (the first time: above -inf)
+            const bool up = mx[0] > ref[0] + kRefSlack || mx[1] > ref[1] + kRefSlack;
+            if (__any_sync(kFullMask, up)) {
+                float f[2];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const float to = fmaxf(ref[half], mx[half]);
+                    f[half] = to == -INFINITY ? 1.f : fast_exp2(ref[half] - to);
+                    ref[half] = to;
+                    lsum[half] *= f[half];
+                }
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    o[i][0] *= f[0];
+                    o[i][1] *= f[0];
+                    o[i][2] *= f[1];
+                    o[i][3] *= f[1];
+                }
+            }
+            use[0] = ref[0] == -INFINITY ? 0.f : ref[0];
+            use[1] = ref[1] == -INFINITY ? 0.f : ref[1];
+            uint32_t pf[4];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const float x = fast_exp2(sc[nt][2 * half] - use[half]), y = fast_exp2(sc[nt][2 * half + 1] - use[half]);
+                    if constexpr (F8) lsum[half] = fmaf(x, iv[nt][0], fmaf(y, iv[nt][1], lsum[half]));
+                    else lsum[half] += x + y;
+                    pf[2 * nt + half] = pack2<MF16>(x, y);
+                }
+            }
+
+            const int mi = lane >> 3, vtok = (mi & 1) * 8 + (lane & 7);
+            if constexpr (!F8) {
+#pragma unroll
+                for (int dc = 0; dc < D / 16; ++dc) {
+                    uint32_t b[4];
+                    ldsm4t(b, vst + vtok * C::ROWB + rows_swz<CH>(vtok, 2 * dc + (mi >> 1)) * 16);
+                    mma16816<MF16>(o[2 * dc], pf, b[0], b[1]);
+                    mma16816<MF16>(o[2 * dc + 1], pf, b[2], b[3]);
+                }
+            } else {
+                // a chunk's even features make one 8-column tile, its odd features another
+#pragma unroll
+                for (int c2 = 0; c2 < D / 32; ++c2) {
+                    uint32_t b[4];
+                    ldsm4t(b, vst + vtok * C::ROWB + rows_swz<CH>(vtok, 2 * c2 + (mi >> 1)) * 16);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t lo = __byte_perm(b[2 * i], 0, 0x3120), hi = __byte_perm(b[2 * i + 1], 0, 0x3120);
+                        mma16816<true>(o[4 * c2 + 2 * i], pf, e4m3x2_f16x2(lo), e4m3x2_f16x2(hi));
+                        mma16816<true>(o[4 * c2 + 2 * i + 1], pf, e4m3x2_f16x2(lo >> 16), e4m3x2_f16x2(hi >> 16));
+                    }
+                }
+            }
+        }
+        cp_async_wait<0>();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            lsum[half] += __shfl_xor_sync(kFullMask, lsum[half], 1);
+            lsum[half] += __shfl_xor_sync(kFullMask, lsum[half], 2);
+        }
+
+        // ---- join the four warps: accumulators through shared memory (the rings are drained) ----
+        __syncthreads();
+        if (t == 0) {
+            m_s[warp][g] = ref[0];
+            m_s[warp][g + 8] = ref[1];
+            l_s[warp][g] = lsum[0];
+            l_s[warp][g + 8] = lsum[1];
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float* dst = merge + (warp * 16 + g + 8 * half) * D;
+            if constexpr (!F8) {
+#pragma unroll
+                for (int nt = 0; nt < D / 8; ++nt)
+                    *reinterpret_cast<float2*>(dst + ((nt * 8 + 2 * t) ^ (g << 2 & 24))) = make_float2(o[nt][2 * half], o[nt][2 * half + 1]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c)
+                    *reinterpret_cast<float4*>(dst + ((c * 16 + 4 * t) ^ (g << 2 & 24))) =
+                        make_float4(o[2 * c][2 * half], o[2 * c + 1][2 * half], o[2 * c][2 * half + 1], o[2 * c + 1][2 * half + 1]);
+            }
+        }
+        __syncthreads();
+        const bool whole = t0 == 0 && t1 == p.nk;
+        float* part = a.part + (static_cast<long long>(blockIdx.x) * 2 + (t0 > 0 ? 0 : 1)) * (16LL * (D + 2));
+        constexpr int TPR = D / 4;  // threads per row, four columns each
+        for (int r = tid / TPR; r < rows; r += kRowsNT / TPR) {
+            const int col = (tid % TPR) * 4;
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) top = fmaxf(top, m_s[w][r]);
+            const float zero = top == -INFINITY ? 0.f : top;
+            float l = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float f = fast_exp2(m_s[w][r] - zero);
+                const float4 v = *reinterpret_cast<const float4*>(merge + (w * 16 + r) * D + (col ^ ((r & 7) << 2 & 24)));
+                l = fmaf(f, l_s[w][r], l);
+                acc.x = fmaf(f, v.x, acc.x);
+                acc.y = fmaf(f, v.y, acc.y);
+                acc.z = fmaf(f, v.z, acc.z);
+                acc.w = fmaf(f, v.w, acc.w);
+            }
+            if (whole) {
+                const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+                const long long row = (p.s.q0 + i0 + r / a.G) * a.Hq + p.h * a.G + r % a.G;
+                uint2 w;
+                w.x = pack2<F16>(acc.x * inv, acc.y * inv);
+                w.y = pack2<F16>(acc.z * inv, acc.w * inv);
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * D + col) = w;
+                if (a.lse && col == 0) a.lse[row] = l == 0.f ? -INFINITY : (zero + log2f(l)) * kLn2;
+            } else {
+                *reinterpret_cast<float4*>(part + r * D + col) = acc;
+                if (col == 0) {
+                    part[16 * D + r] = top;
+                    part[16 * (D + 1) + r] = l;
+                }
+            }
+        }
+        at += t1 - t0;
+        if (at >= end) break;
+        next_unit<BN>(a, p);
+        __syncthreads();  // the rings are written again
+    }
+}
+
+}  // namespace attn
+}  // namespace gdn

@@ -1,0 +1,182 @@
+// cache.cuh -- rows into a paged attention cache, quantised on the way, and back out of it.
+//
+// Both are copies: each value is read once and written once, and the bound is HBM.  A row (one token,
+// one head, D values) belongs to a group of D / 8 lanes, eight values per lane: 16-byte accesses on the
+// 16-bit side, 8-byte accesses on the 8-bit side.  A CTA takes kTokens consecutive tokens of one head of
+// K or of V, so that its accesses to the cache run along the tokens of a page; a group has all its rows'
+// loads in flight before the first is used.
+//
+// Quantisation (cache type e4m3): per row, scale = the least power of two s with max |x| <= 448 s, and
+// the value e4m3(x / s), to nearest, ties to even.  A power of two, because a floating-point type loses
+// nothing by it (its relative step is the same at every scale), x / s and value * s are exact, and the
+// dequantised value is itself a bf16 (or binary16) number: reading back rounds nothing.  s is at least
+// 2^-100.  A row of zeros gets scale 1.  Elements that are not finite become e4m3's NaN and do not
+// count for the scale.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "kernel_args.h"
+
+namespace gdn {
+namespace cache {
+
+constexpr int kThreads = 256;
+
+template <bool F16>
+__device__ __forceinline__ float2 widen2(uint32_t w) {
+    if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
+    if constexpr (F16) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        return pack_bf16x2(lo, hi);
+    }
+}
+
+// Two floats to two e4m3 values (nearest even), the first in the low byte; NaN for what is not finite.
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+    const float nan = __int_as_float(0x7fffffff);
+    if (!(fabsf(lo) < INFINITY)) lo = nan;
+    if (!(fabsf(hi) < INFINITY)) hi = nan;
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+// kv: 0 moves keys, 1 values (blockIdx.z).
+template <int D, bool F16, bool F8, int TOKENS>
+__global__ void __launch_bounds__(kThreads) attn_cache_write_kernel(const __grid_constant__ CacheMoveArgs a) {
+    constexpr int LANES = D / 8, GROUPS = kThreads / LANES, ROWS = (TOKENS + GROUPS - 1) / GROUPS;
+    const int h = blockIdx.y, kv = blockIdx.z, lane = threadIdx.x % LANES;
+    const long long first = static_cast<long long>(blockIdx.x) * TOKENS + threadIdx.x / LANES;
+    const long long last = min(static_cast<long long>(blockIdx.x + 1) * TOKENS, a.T);
+    const uint16_t* src = (kv ? a.v_in + first * a.v_stride : a.k_in + first * a.k_stride) + h * D + lane * 8;
+    const long long step = GROUPS * (kv ? a.v_stride : a.k_stride);
+    uint4 x[ROWS];
+    long long slot[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const bool on = first + i * GROUPS < last;
+        x[i] = on ? __ldcs(reinterpret_cast<const uint4*>(src + i * step)) : make_uint4(0, 0, 0, 0);
+        slot[i] = on ? a.slots[first + i * GROUPS] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        float f[8], scale = 1.f;
+        uint2 q = make_uint2(0, 0);
+        if constexpr (F8) {
+            float mx = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 p = widen2<F16>(w[j]);
+                f[2 * j] = p.x;
+                f[2 * j + 1] = p.y;
+                if (fabsf(p.x) < INFINITY) mx = fmaxf(mx, fabsf(p.x));
+                if (fabsf(p.y) < INFINITY) mx = fmaxf(mx, fabsf(p.y));
+            }
+            mx = fmaxf(mx, 0.f);
+#pragma unroll
+            for (int o = LANES / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, o));
+            // 448 = 1.75 2^8: the exponent is mx's less 8, less 7 where mx's significand is over 1.75
+            const uint32_t u = __float_as_uint(mx);
+            int e = static_cast<int>(u >> 23) - 127 - ((u & 0x7fffffu) > 0x600000u ? 7 : 8);
+            e = max(e, -100);
+            if (mx == 0.f) e = 0;
+            scale = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+            const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] *= inv;
+            q.x = to_e4m3x2(f[0], f[1]) | to_e4m3x2(f[2], f[3]) << 16;
+            q.y = to_e4m3x2(f[4], f[5]) | to_e4m3x2(f[6], f[7]) << 16;
+        }
+        if (first + i * GROUPS >= last || slot[i] < 0) continue;  // a negative slot: the token is not kept
+        const long long page = slot[i] / a.page_size;
+        if (page >= a.num_pages) {
+            if (lane == 0) atomicOr(a.status, kStatusBadCacheIndex);
+            continue;
+        }
+        const long long row = (page * a.H + h) * a.page_size + (slot[i] - page * a.page_size);
+        if constexpr (F8) {
+            uint8_t* dst = static_cast<uint8_t*>(kv ? a.vc : a.kc);
+            *reinterpret_cast<uint2*>(dst + row * D + lane * 8) = q;
+            if (lane == 0) (kv ? a.vs : a.ks)[row] = scale;
+        } else {
+            uint16_t* dst = static_cast<uint16_t*>(kv ? a.vc : a.kc);
+            *reinterpret_cast<uint4*>(dst + row * D + lane * 8) = x[i];
+        }
+    }
+}
+
+template <int D, bool F16, bool F8, int TOKENS>
+__global__ void __launch_bounds__(kThreads) attn_cache_read_kernel(const __grid_constant__ CacheMoveArgs a) {
+    constexpr int LANES = D / 8, GROUPS = kThreads / LANES, ROWS = (TOKENS + GROUPS - 1) / GROUPS;
+    __shared__ long long rows_s[TOKENS];
+    const int h = blockIdx.y, kv = blockIdx.z, lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+    const long long t0 = static_cast<long long>(blockIdx.x) * TOKENS;
+    if (threadIdx.x < TOKENS) {  // the cached row of each token (-1: none)
+        const long long t = t0 + threadIdx.x;
+        long long row = -1;
+        if (t < a.T) {
+            // the last sequence that begins at or before t
+            int lo = 0, hi = a.num_seqs;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (a.cu[mid] <= t) lo = mid;
+                else hi = mid;
+            }
+            const long long b = a.cu[lo], e = a.cu[lo + 1], pos = t - b;
+            const bool fits = e - b <= static_cast<long long>(a.max_pages) * a.page_size;
+            if (b < 0 || e > a.T || !fits) atomicOr(a.status, kStatusBadSeqlens);
+            if (b >= 0 && t < e && e <= a.T && pos >= 0 && fits) {
+                const long long pg = pos / a.page_size;
+                const long long page = a.table[static_cast<long long>(lo) * a.max_pages + pg];
+                if (page >= 0 && page < a.num_pages) row = (page * a.H + h) * a.page_size + (pos - pg * a.page_size);
+                else atomicOr(a.status, kStatusBadCacheIndex);
+            }
+        }
+        rows_s[threadIdx.x] = row;
+    }
+    __syncthreads();
+    long long row[ROWS];
+    uint4 x[ROWS];
+    float s[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int k = group + i * GROUPS;
+        row[i] = k < TOKENS ? rows_s[k] : -1;
+        if constexpr (F8) {
+            const uint8_t* src = static_cast<const uint8_t*>(kv ? a.vc : a.kc);
+            const uint2 w = row[i] >= 0 ? __ldcs(reinterpret_cast<const uint2*>(src + row[i] * D + lane * 8)) : make_uint2(0, 0);
+            x[i] = make_uint4(w.x, w.y, 0, 0);
+            s[i] = row[i] >= 0 ? (kv ? a.vs : a.ks)[row[i]] : 0.f;
+        } else {
+            const uint16_t* src = static_cast<const uint16_t*>(kv ? a.vc : a.kc);
+            x[i] = row[i] >= 0 ? __ldcs(reinterpret_cast<const uint4*>(src + row[i] * D + lane * 8)) : make_uint4(0, 0, 0, 0);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        if (row[i] < 0) continue;  // nothing cached for this token: its row is not written
+        if constexpr (F8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t two = (j < 2 ? x[i].x : x[i].y) >> (16 * (j & 1)) & 0xffffu;
+                const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+                const float2 f = __half22float2(__half2(hr));
+                w[j] = narrow2<F16>(f.x * s[i], f.y * s[i]);
+            }
+            x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        uint16_t* dst = kv ? a.v_out : a.k_out;
+        __stcs(reinterpret_cast<uint4*>(dst + ((t0 + group + i * GROUPS) * a.H + h) * D + lane * 8), x[i]);
+    }
+}
+
+}  // namespace cache
+}  // namespace gdn

@@ -168,4 +168,67 @@ constexpr int kWinD = 128;       // head dim
 constexpr int kWinThreads = 128;
 constexpr int kWinMaxTok = 8;
 
+// Bits of the device status word (GDN_STATUS_* of gdn.h).
+constexpr int kStatusBadCacheIndex = 1, kStatusBadSeqlens = 2, kStatusTimeout = 4, kStatusBadProbs = 8,
+              kStatusBadToken = 16;
+
+// Attention over a paged cache.  Caches [num_pages, Hkv, page_size, D], scales [num_pages, Hkv, page_size]
+// (null: not quantised), table [num_seqs, max_pages].
+struct AttnArgs {
+    const uint16_t* q;   // [T, Hq, D], rows q_stride elements apart
+    long long q_stride;
+    const void* kc;
+    const void* vc;
+    const float* ks;
+    const float* vs;
+    const int64_t* table;
+    const int64_t* kv_lens;
+    const int64_t* cu;
+    void* out;           // [T, Hq, D]
+    float* lse;          // [T, Hq] or null
+    float* part;         // partial results of units that span CTAs
+    int32_t* status;
+    long long T, num_pages;
+    int page_size, max_pages, num_seqs;
+    int Hq, Hkv, G;      // G = Hq / Hkv
+    int tq;              // tokens per query tile
+    int min_tiles;       // fewest key tiles per CTA
+    int f16;             // q and out are binary16 (else bf16)
+    float scale_log2;    // scale * log2(e)
+    uint32_t page_mul;   // division by page_size
+    int page_shift;
+};
+
+// Cache rows moved by the write and read kernels.
+struct CacheMoveArgs {
+    const uint16_t* k_in;  // write: [T, H, D] sources
+    const uint16_t* v_in;
+    long long k_stride, v_stride;
+    uint16_t* k_out;       // read: [T, H, D] results
+    uint16_t* v_out;
+    void* kc;
+    void* vc;
+    float* ks;
+    float* vs;
+    const int64_t* slots;  // write: flat slot per token
+    const int64_t* table;  // read: page table and bounds
+    const int64_t* cu;
+    int32_t* status;
+    long long T, num_pages;
+    int page_size, max_pages, num_seqs, H;
+};
+
+struct VerifyArgs {
+    const float* target;   // [N, T + 1, V]
+    const float* draft;    // [N, T, V]
+    const int64_t* drafts; // [N, T]
+    const int64_t* num_drafts;  // [N] or null
+    const float* u_accept; // [N, T]
+    const float* u_sample; // [N]
+    int64_t* accepted;     // [N]
+    int64_t* tokens;       // [N, T + 1]
+    int32_t* status;
+    int N, T, V;
+};
+
 }  // namespace gdn

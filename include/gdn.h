@@ -14,6 +14,11 @@
  *   comba_prefill_chunked  varlen chunkwise-WY prefill of the Comba recurrence over a pooled state
  *   gdn_window_fused     fused decode window: conv + SiLU, L2 norm, gates, recurrence over ntok
  *                        tokens, gated RMSNorm, with verify / commit / partial commit
+ * and the operations of the attention layers and of the drafted decoding around them:
+ *   attn_paged           causal attention of each sequence's new tokens over its paged cache
+ *   attn_cache_write     keys and values into the paged cache, quantised to 8 bits or as they are
+ *   attn_cache_read      cached keys and values back to dense rows
+ *   draft_verify         which drafted tokens the target accepts, and the token that follows them
  *
  * Conventions shared by every entry point
  *   - Every tensor argument is a DEVICE pointer to dense, contiguous, row-major memory in the layout
@@ -57,15 +62,22 @@ typedef enum gdn_status {
     GDN_ERR_TIMEOUT = 4      /* reserved for bounded device-side waits that gave up */
 } gdn_status;
 
-typedef enum gdn_dtype { GDN_BF16 = 0, GDN_F32 = 1 } gdn_dtype;
+typedef enum gdn_dtype {
+    GDN_BF16 = 0,
+    GDN_F32 = 1,
+    GDN_F16 = 2, /* IEEE binary16 */
+    GDN_E4M3 = 3 /* 8-bit float: 4 exponent bits, 3 of significand, largest 448, no infinity */
+} gdn_dtype;
 
 /* A cudaStream_t, passed opaquely so that this header needs no CUDA header. */
 typedef void* gdn_stream_t;
 
-/* Bits of the device status word of gdn_prefill_chunked and gdn_decode_step_pooled. */
-#define GDN_STATUS_BAD_CACHE_INDEX 1 /* a cache_indices entry outside [0, pool_size) */
-#define GDN_STATUS_BAD_SEQLENS 2     /* cu_seqlens[n] < 0, decreasing, or beyond T */
+/* Bits of the device status word (the entry points that take dev_status). */
+#define GDN_STATUS_BAD_CACHE_INDEX 1 /* a cache_indices entry outside [0, pool_size); a page or slot outside the cache */
+#define GDN_STATUS_BAD_SEQLENS 2     /* cu_seqlens[n] < 0, decreasing, or beyond T; a length its page table cannot hold */
 #define GDN_STATUS_TIMEOUT 4         /* a bounded wait for the tensor core or a copy gave up */
+#define GDN_STATUS_BAD_PROBS 8       /* draft_verify: a distribution to draw from has no mass */
+#define GDN_STATUS_BAD_TOKEN 16      /* draft_verify: a drafted token outside [0, V) */
 
 /*
  * gdn_decode_step -- one GDN decode step for B sequences.  [gated_delta.rs] "Recurrence per step":
@@ -355,6 +367,119 @@ gdn_status gdn_window_fused(float* state, const float* hist, float* hist_out, co
  * the built-in limits.  Process-wide; it applies to calls launched after it returns.
  */
 void gdn_prefill_set_wait_limit(uint32_t polls);
+
+/*
+ * The paged attention cache.  Keys and values of all sequences live in pages of page_size tokens:
+ *   k_cache, v_cache   [num_pages, Hkv, page_size, D] of cache_dtype
+ *   k_scale, v_scale   f32 [num_pages, Hkv, page_size]   cache_dtype GDN_E4M3 only (else NULL): a cached
+ *                      element stands for value * scale of its (token, head)
+ *   page_table         int64 [num_seqs, max_pages]   token t of sequence n is in page
+ *                      page_table[n][t / page_size] at t % page_size; only the entries that a
+ *                      sequence's length reaches are read
+ * page_size is any positive number.  A page or slot outside the cache sets GDN_STATUS_BAD_CACHE_INDEX
+ * and is not accessed.  dev_status is a device int32, zeroed by the caller; the kernels OR bits in.
+ */
+
+/*
+ * attn_cache_write -- T tokens' keys and values into the cache.
+ *   k, v       [T, Hkv, D] of dtype (GDN_BF16 or GDN_F16); token t begins k_stride (v_stride) elements
+ *              after token t - 1 (a slice of a fused projection needs no copy); 16-byte aligned, strides
+ *              multiples of 8
+ *   slots      int64 [T]   where token t goes: page * page_size + offset; a negative slot leaves the token
+ *              out; distinct (of two tokens with one slot either may stay)
+ *   cache_dtype  dtype (rows are copied), or GDN_E4M3: per (token, head) row the scale is the least power
+ *              of two s >= 2^-100 with max |x| <= 448 s (1 for a row of zeros) and the stored value
+ *              e4m3(x / s), to nearest even.  x / s is exact, and so is value * s in bf16.  Elements that
+ *              are not finite are stored as NaN and do not count for the scale.
+ * The sources must not overlap the cache.  Supported: D in {64, 128, 256}, Hkv <= 65535.
+ */
+gdn_status attn_cache_write(const void* k, const void* v, int64_t k_stride, int64_t v_stride, gdn_dtype dtype,
+                            const int64_t* slots, int64_t T, void* k_cache, void* v_cache, float* k_scale,
+                            float* v_scale, gdn_dtype cache_dtype, int64_t num_pages, int page_size, int Hkv,
+                            int D, int32_t* dev_status, gdn_stream_t stream);
+
+/*
+ * attn_cache_read -- the cached tokens of num_seqs sequences as dense rows.
+ *   cu_seqlens int64 [num_seqs + 1]   token t of sequence n is row cu_seqlens[n] + t
+ *   k, v       [T, Hkv, D] of dtype, 16-byte aligned, T = cu_seqlens[num_seqs]; rows that no sequence
+ *              covers, and rows whose page is outside the cache, are not written
+ *   cache_dtype  dtype, or GDN_E4M3: value * scale in fp32, rounded to dtype (exact in bf16 for scales that
+ *              attn_cache_write made)
+ * Supported: D in {64, 128, 256}, Hkv <= 65535.
+ */
+gdn_status attn_cache_read(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                           gdn_dtype cache_dtype, int64_t num_pages, int page_size, const int64_t* page_table,
+                           int max_pages, const int64_t* cu_seqlens, int num_seqs, int64_t T, int Hkv, int D,
+                           void* k, void* v, gdn_dtype dtype, int32_t* dev_status, gdn_stream_t stream);
+
+/*
+ * attn_paged_workspace_size -- bytes of device workspace that attn_paged needs for heads of D features
+ * (it depends on D alone); 0 for a D that it does not support.  Pure host function.
+ */
+size_t attn_paged_workspace_size(int D);
+
+/*
+ * attn_paged -- causal attention of new tokens over a paged cache that already holds their keys and
+ * values.  Sequence n has L = kv_lens[n] cached tokens; its m = cu_seqlens[n+1] - cu_seqlens[n] queries
+ * are the last m of them: query i stands at position L - m + i and sees keys 0 .. L - m + i.  Query head
+ * h reads key head h / (Hq / Hkv):
+ *     s_j = scale q.k_j;   out = sum_j e^{s_j} v_j / sum_j e^{s_j};   lse = ln sum_j e^{s_j}.
+ * One token per sequence is a decode step; a few are a window of drafted tokens; m = L is a whole prompt.
+ *
+ *   q          [T, Hq, D] of dtype (GDN_BF16 or GDN_F16), token t q_stride elements after token t - 1;
+ *              16-byte aligned, q_stride a multiple of 8
+ *   kv_lens    int64 [num_seqs]
+ *   cu_seqlens int64 [num_seqs + 1]
+ *   max_q      the largest m, as far as the caller knows it: it chooses the kernel and changes no result
+ *              beyond rounding
+ *   out        [T, Hq, D] of dtype, 16-byte aligned
+ *   lse        f32 [T, Hq], natural logarithm; may be NULL
+ *   workspace  attn_paged_workspace_size(D) bytes, 16-byte aligned, contents need not be initialised;
+ *              calls that share it must not overlap on the GPU
+ * A query that sees no key (L < m - i) gets out = 0, lse = -infinity.  Memory of the cache past a
+ * sequence's length is never used, whatever it holds.  Keys and values that some query of a sequence's
+ * chunk sees must be finite: the products with them also run, with weight zero, for the chunk's earlier
+ * queries.  Scales must be positive and finite.  A sequence with malformed bounds sets
+ * GDN_STATUS_BAD_SEQLENS and is skipped (its rows are not written); one with a page outside the cache sets
+ * GDN_STATUS_BAD_CACHE_INDEX and its rows hold no meaningful value.
+ * Products take 16-bit operands (dtype; binary16 for an 8-bit cache, which its values and the scaled
+ * queries fit exactly), weights are rounded to that type for the second product; scores, sums and
+ * outputs accumulate in f32.  Results do not depend on timing.
+ * Supported: D in {64, 128, 256}, Hq % Hkv == 0, Hq / Hkv <= 16, cache_dtype dtype or GDN_E4M3,
+ * max_pages * page_size < 2^31, T < 2^30.
+ */
+gdn_status attn_paged(const void* q, int64_t q_stride, gdn_dtype dtype, const void* k_cache, const void* v_cache,
+                      const float* k_scale, const float* v_scale, gdn_dtype cache_dtype, int64_t num_pages,
+                      int page_size, const int64_t* page_table, int max_pages, const int64_t* kv_lens,
+                      const int64_t* cu_seqlens, int num_seqs, int64_t T, int64_t max_q, int Hq, int Hkv, int D,
+                      float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                      int32_t* dev_status, gdn_stream_t stream);
+
+/*
+ * draft_verify -- verification of drafted tokens by rejection sampling, from given random numbers.
+ * Drafted token t of sequence n is accepted while u_accept * draft_p[x] < target_p[x] (x the token, rows
+ * t).  At the first rejection r the next token is drawn from max(target_p[r] - draft_p[r], 0); with all T
+ * accepted from target_p[T].  With P = floor(clamp(p, 0, 1) 2^36) entry by entry, Q likewise:
+ *     w_i = max(P_i - Q_i, 0) (P_i where all of these are 0, or nothing was rejected);
+ *     mark = floor(sum w * floor(u_sample 2^24) / 2^24);  the token is the least i with w_0 + .. + w_i > mark,
+ * so results are a function of the inputs alone.  The count is what gdn_window_fused commits: a window over
+ * the last sampled token and T drafts commits after its token accepted + 1 (0x100 | accepted + 1).
+ *
+ *   target_p   f32 [N, T + 1, V]     probabilities
+ *   draft_p    f32 [N, T, V]
+ *   drafts     int64 [N, T]
+ *   num_drafts int64 [N] or NULL     drafts of each sequence where they are fewer than T (clamped to 0 .. T)
+ *   u_accept   f32 [N, T]            uniform in [0, 1)
+ *   u_sample   f32 [N]               uniform in [0, 1)
+ *   accepted   int64 [N]
+ *   tokens     int64 [N, T + 1]      the accepted drafts, the drawn token, then -1
+ *   dev_status device int32, zeroed by the caller: GDN_STATUS_BAD_TOKEN where a draft is outside [0, V)
+ *              (it counts as rejected), GDN_STATUS_BAD_PROBS where a row to draw from has no mass (token 0)
+ * Supported: T >= 0, 1 <= V <= 2^20.
+ */
+gdn_status draft_verify(const float* target_p, const float* draft_p, const int64_t* drafts,
+                        const int64_t* num_drafts, const float* u_accept, const float* u_sample, int N, int T,
+                        int V, int64_t* accepted, int64_t* tokens, int32_t* dev_status, gdn_stream_t stream);
 
 /* Static description of a status code. */
 const char* gdn_status_string(gdn_status status);
