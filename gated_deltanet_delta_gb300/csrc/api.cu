@@ -711,7 +711,7 @@ extern "C" gdn_status attn_paged(const void* q, int64_t q_stride, gdn_dtype dtyp
             GDN_ERR_INVALID_ARG,
             "%s: sizes must be T, max_q, num_seqs, num_pages, max_pages >= 0 and page_size, Hq, Hkv >= 1", fn);
     REQUIRE(Hq % Hkv == 0, GDN_ERR_INVALID_ARG, "%s: Hq (%d) must be a multiple of Hkv (%d)", fn, Hq, Hkv);
-    REQUIRE(Hq / Hkv <= 16, GDN_ERR_UNSUPPORTED, "%s: Hq / Hkv must be at most 16 (got %d)", fn, Hq / Hkv);
+    REQUIRE(Hq / Hkv <= 128, GDN_ERR_UNSUPPORTED, "%s: Hq / Hkv must be at most 128 (got %d)", fn, Hq / Hkv);
     if (T == 0 || num_seqs == 0) return GDN_OK;
     size_t cb = 0;
     const gdn_status s = cache_check(fn, k_cache, v_cache, k_scale, v_scale, cache_dtype, dtype, num_pages, page_size,
@@ -767,7 +767,7 @@ extern "C" gdn_status attn_paged(const void* q, int64_t q_stride, gdn_dtype dtyp
     a.page_mul = static_cast<uint32_t>(((1ULL << (31 + sh)) + page_size - 1) / page_size);
     a.page_shift = 31 + sh;
     const cudaError_t e =
-        gdn::launch_attn(a, D, cache_dtype == GDN_E4M3, max_q, static_cast<cudaStream_t>(stream));
+        gdn::launch_attn(a, D, cache_dtype == GDN_E4M3, static_cast<int>(max_q < T ? max_q : T), static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
     return launched(fn);
 }

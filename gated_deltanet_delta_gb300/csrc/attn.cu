@@ -3,13 +3,15 @@
 #include <atomic>
 
 #include "attn_rows.cuh"
+#include "attn_tiles.cuh"
 #include "launch.h"
 
 namespace gdn {
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int kMaxCtas = 608;  // the workspace has two partial slots for each
+constexpr int kMaxCtas = 608;      // of the row kernel; the workspace has two partial slots for each
+constexpr int kMaxTileCtas = 160;  // of the tile kernel, likewise
 std::atomic<int> g_sms[kMaxDevices];
 
 cudaError_t sm_count(int* n) {
@@ -42,8 +44,7 @@ cudaError_t raise_smem(K kernel, int bytes, std::atomic<unsigned long long>& don
 // The joining kernel starts while the main kernel still runs (programmatic dependent launch) and waits
 // for it before it reads the partials.
 template <int BN>
-cudaError_t launch_combine(const AttnArgs& a, int R, int D, int grid, cudaStream_t stream) {
-    const int RB = 4;
+cudaError_t launch_combine(const AttnArgs& a, int R, int D, int RB, int grid, cudaStream_t stream) {
     if (grid < 2) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid - 1, (R + RB - 1) / RB);
@@ -71,25 +72,51 @@ cudaError_t launch_rows(AttnArgs a, cudaStream_t stream) {
     attn::attn_rows_kernel<D, F16, F8><<<grid, attn::kRowsNT, C::SMEM, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_combine<attn::kRowsBN>(a, attn::kRowsTile, D, grid, stream);
+    return launch_combine<attn::kRowsBN>(a, attn::kRowsTile, D, 4, grid, stream);
+}
+
+template <int D, bool F16, bool F8>
+cudaError_t launch_tiles(AttnArgs a, cudaStream_t stream) {
+    using C = attn::TilesCfg<D, F8>;
+    static std::atomic<unsigned long long> done{0};
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e == cudaSuccess) e = raise_smem(attn::attn_tiles_kernel<D, F16, F8>, C::SMEM, done);
+    if (e != cudaSuccess) return e;
+    a.tq = C::R / a.G;
+    a.min_tiles = 1;
+    const int grid = std::min(sms, kMaxTileCtas);
+    attn::attn_tiles_kernel<D, F16, F8><<<grid, attn::kTilesNT, C::SMEM, stream>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_combine<C::BN>(a, C::R, D, 16, grid, stream);
+}
+
+template <int D, bool F16, bool F8>
+cudaError_t launch_any(const AttnArgs& a, int max_q, cudaStream_t stream) {
+    // One 16-row tile holds the rows that share a key head: the row kernel.  Beyond that it would read
+    // every key once per 16 rows.
+    return static_cast<long long>(std::max(max_q, 1)) * a.G <= attn::kRowsTile ? launch_rows<D, F16, F8>(a, stream)
+                                                                  : launch_tiles<D, F16, F8>(a, stream);
 }
 
 template <int D>
-cudaError_t launch_d(const AttnArgs& a, bool f8, cudaStream_t stream) {
-    if (a.f16) return f8 ? launch_rows<D, true, true>(a, stream) : launch_rows<D, true, false>(a, stream);
-    return f8 ? launch_rows<D, false, true>(a, stream) : launch_rows<D, false, false>(a, stream);
+cudaError_t launch_d(const AttnArgs& a, bool f8, int max_q, cudaStream_t stream) {
+    if (a.f16) return f8 ? launch_any<D, true, true>(a, max_q, stream) : launch_any<D, true, false>(a, max_q, stream);
+    return f8 ? launch_any<D, false, true>(a, max_q, stream) : launch_any<D, false, false>(a, max_q, stream);
 }
 }  // namespace
 
 size_t attn_workspace_bytes(int D) {
-    return static_cast<size_t>(kMaxCtas) * 2 * attn::kRowsTile * (D + 2) * sizeof(float);
+    const size_t rows = static_cast<size_t>(kMaxCtas) * attn::kRowsTile;
+    const size_t tiles = static_cast<size_t>(kMaxTileCtas) * (D == 256 ? attn::TilesCfg<256, false>::R : attn::TilesCfg<128, false>::R);
+    return std::max(rows, tiles) * 2 * (D + 2) * sizeof(float);
 }
 
 cudaError_t launch_attn(const AttnArgs& a, int D, bool f8, int max_q, cudaStream_t stream) {
-    (void)max_q;
-    if (D == 64) return launch_d<64>(a, f8, stream);
-    if (D == 128) return launch_d<128>(a, f8, stream);
-    return launch_d<256>(a, f8, stream);
+    if (D == 64) return launch_d<64>(a, f8, max_q, stream);
+    if (D == 128) return launch_d<128>(a, f8, max_q, stream);
+    return launch_d<256>(a, f8, max_q, stream);
 }
 
 }  // namespace gdn

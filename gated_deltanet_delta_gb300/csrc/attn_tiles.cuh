@@ -1,0 +1,572 @@
+// attn_tiles.cuh -- attn_paged for many query rows per key head (drafted windows, chunks, prompts): tiles
+// of 128 rows on the tensor cores (tcgen05, accumulators in TMEM).
+//
+// Per key tile of BN keys and 128 rows:  S = Q K^T (128 x BN x D),  P = 2^{y - ref},  O += P V
+// (128 x D x BN).  S, P (over S's columns) and O live in TMEM; Q, K and V tiles in shared memory in the
+// 128-byte-swizzled operand layouts; a row's reference and sum in its thread's registers.
+// Two S buffers keep the tensor core busy while one of them is exponentiated.  D <= 128: a unit has up to
+// 256 rows, two row tiles ("slots") with an accumulator each that share every K and V tile; a unit of at
+// most 128 rows uses the slots for alternate key tiles, and the two accumulators are added at its end.
+// D = 256: one row tile and one accumulator (256 columns), key tiles of 64 in two S buffers.
+// So operation s (s = 0, 1, ..) works in buffer s & 1 on key tile s / 2 (two row tiles) or s.
+//
+// Roles, 512 threads: two softmax warpgroups (one per buffer; thread i owns TMEM lane i, a row), a loader
+// warpgroup, and a warp whose lane 0 issues every MMA:  S(0) S(1) | P(0)? PV(0) S(2) | P(1)? PV(1) S(3) ..
+// Operations of one issuing thread run in order, so S(s + 2) overwrites a buffer only after PV(s) has
+// read P from it.
+// The loader gathers rows by page with cp.async (any page size; rows past the keys are zero-filled, so
+// nothing stale meets a weight of zero), three groups in flight.  8-bit caches go through a staging ring,
+// private per thread, and are widened into the tile; attn_rows.cuh says how their scales are applied.
+//
+// Every wait is bounded: one that runs out sets GDN_STATUS_TIMEOUT and the CTA's abort flag, on which
+// all roles leave; copies and MMAs in flight are waited for (bounded) before the CTA ends.
+#pragma once
+
+#include "attn.cuh"
+#include "attn_mma.cuh"
+#include "tcgen05.cuh"
+
+namespace gdn {
+namespace attn {
+
+constexpr int kTilesNT = 512;
+constexpr uint32_t kTilesWait = 1u << 22;  // polls before a wait gives up (seconds)
+
+template <int D, bool F8>
+struct TilesCfg {
+    static constexpr int BN = D == 256 ? 64 : 128;         // keys per tile
+    static constexpr int SLOTS = D == 256 ? 1 : 2;         // row tiles per unit
+    static constexpr int R = 128 * SLOTS;                  // rows per unit
+    static constexpr int HALVES = D / 64;                  // 64-feature halves of an operand tile
+    static constexpr uint32_t QTILE = 128u * D * 2, TILE = static_cast<uint32_t>(BN) * D * 2;
+    static constexpr uint32_t RAW = F8 ? TILE / 2 : 0;
+    // K and V tiles in shared memory.  8 bits: with 3, a K tile's place is its second predecessor's V tile's,
+    // so two slots for the keys' scales are enough.
+    static constexpr int NST = F8 ? 3 : (D == 64 ? 8 : 5);
+    // copy groups in flight behind the newest.  16 bits: at most NST - 2, as S(s + 2) needs its K tile before
+    // the V tile before it is released.
+    static constexpr int LAG = F8 ? (D == 64 ? 5 : 2) : 3;
+    static constexpr int NRAW = F8 ? LAG + 1 : 0;
+    static constexpr uint32_t OFF_KV = SLOTS * QTILE;
+    static constexpr uint32_t OFF_RAW = OFF_KV + NST * TILE;
+    static constexpr uint32_t OFF_RSC = OFF_RAW + NRAW * RAW;            // raw scales of a stage: K, V
+    static constexpr uint32_t OFF_SC = OFF_RSC + NRAW * (F8 ? 1024 : 0);  // ks, log2 vs, 1 / vs of two tiles
+    static constexpr uint32_t OFF_RS = OFF_SC + (F8 ? 2 * 3 * 128 * 4 : 0);  // row scales of two units
+    static constexpr uint32_t USED = OFF_RS + (F8 ? 2 * R * 4 : 0);
+    static constexpr uint32_t SMEM = USED + 1024;          // 1024-byte alignment
+    static constexpr uint32_t TM_S = 0, TM_O = 256, TM_SB = BN;  // TMEM columns
+};
+
+enum : int { TB_QF = 0, TB_QE, TB_S0, TB_S1, TB_P0, TB_P1, TB_OD0, TB_OD1, TB_OF0, TB_OF1, TB_MF, TB_ME, TB_SC0, TB_SC1, TB_DRAIN, TB_KV };
+
+__device__ __forceinline__ void tm_ld32(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+template <int D, bool F16, bool F8>
+__global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_constant__ AttnArgs a) {
+    using C = TilesCfg<D, F8>;
+    constexpr bool MF16 = F16 || F8;
+    constexpr int BN = C::BN, NST = C::NST, LAG = C::LAG, SLOTS = C::SLOTS;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ PlanSmem plan;
+    __shared__ uint64_t bars[TB_KV + 2 * NST];
+    __shared__ float ml_s[128][2];
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int abort_flag;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = tid >> 7;
+
+    long long w0;
+    const long long W = plan_total<BN, kTilesNT>(a, plan, w0, blockIdx.x == 0);
+    pdl_launch();
+    const long long per = max((W + gridDim.x - 1) / static_cast<long long>(gridDim.x), static_cast<long long>(a.min_tiles));
+    long long at = blockIdx.x * per;
+    if (at >= W) return;
+    const long long end = min(at + per, W);
+    Place p = locate<BN, kTilesNT>(a, plan, w0, at);
+
+    uint8_t* sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sb = smem_addr(sm);
+    if (warp == 12) tc::tmem_alloc(&tmem_slot, 512);
+    if (tid == 0) {
+        for (int i = 0; i < TB_KV + 2 * NST; ++i) {
+            const bool by_warps = i == TB_QF || i == TB_P0 || i == TB_P1 || i == TB_OF0 || i == TB_OF1 || i == TB_MF ||
+                                  i == TB_ME || i == TB_SC0 || i == TB_SC1 || (i >= TB_KV && i < TB_KV + NST);
+            tc::mbar_init(&bars[i], by_warps ? 4 : 1);
+        }
+        abort_flag = 0;
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tm = tmem_slot;
+    constexpr int KV_FULL = TB_KV, KV_EMPTY = TB_KV + NST;
+
+    auto wait = [&](int i, uint32_t parity) -> bool {
+        if (tc::mbar_wait_or_abort(&bars[i], parity, kTilesWait, &abort_flag)) return true;
+        abort_flag = 1;
+        return false;
+    };
+    auto warp_wait = [&](int i, uint32_t parity) -> bool {
+        const bool ok = __all_sync(kFullMask, wait(i, parity));
+        tc::fence_after();
+        return ok;
+    };
+    // one arrival for the warp, after all of its lanes' writes
+    auto warp_arrive = [&](int i) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars[i]);
+    };
+
+    if (wg == 2) {
+        // ------------------------------------------------------------ loader
+        // warp w moves rows w RW .. w RW + RW - 1 of every tile; lane l holds the cache offset of one of them
+        constexpr int RW = BN / 4;
+        constexpr int CHR = (F8 ? D : 2 * D) / 16;  // 16-byte chunks per cached row
+        constexpr int PER = RW * CHR / 32;          // chunks per lane and tile
+        const int tl = tid & 127, r0 = (warp & 3) * RW, mine = r0 + lane % RW;
+        uint32_t open = 0, item = 0, made = 0, pend = 0, unit = 0;
+        bool ok = true;
+        // the oldest group has landed: (8 bits: widen it and) hand it over
+        auto finish = [&](uint32_t what) {
+            if constexpr (F8) {
+                const uint32_t stage = made % NST, ring = made % C::NRAW;
+                if (!warp_wait(KV_EMPTY + stage, (made / NST & 1) ^ 1)) {
+                    ok = false;
+                    return;
+                }
+                if (!(made & 1)) {  // a K tile: its keys' scales, for the softmax
+                    if (lane < RW) {
+                        const uint32_t rsc = sb + C::OFF_RSC + ring * 1024 + mine * 4;
+                        float* sc = reinterpret_cast<float*>(sm + C::OFF_SC) + (made >> 1 & 1) * 384 + mine;
+                        const float ks = lds32(rsc), vs = lds32(rsc + 512);
+                        const bool none = vs == 0.f;  // past the keys: zero-filled
+                        sc[0] = ks;
+                        sc[128] = none ? 0.f : log2f(vs);
+                        sc[256] = none ? 0.f : 1.f / vs;
+                    }
+                    warp_arrive(TB_SC0 + (made >> 1 & 1));
+                }
+                const uint32_t raw = sb + C::OFF_RAW + ring * C::RAW + (warp & 3) * (PER * 512) + lane * 16;
+                const uint32_t dst = sb + C::OFF_KV + stage * C::TILE;
+#pragma unroll 4
+                for (int i = 0; i < PER; ++i) {
+                    const int idx = i * 32 + lane, r = r0 + idx / CHR, c = idx % CHR;
+                    const uint4 w = lds128(raw + i * 512);
+                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t y[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        y[2 * j] = e4m3x2_f16x2(x[j]);
+                        y[2 * j + 1] = e4m3x2_f16x2(x[j] >> 16);
+                    }
+                    sts128(dst + tc::sw_chunk(r, 2 * c, BN), make_uint4(y[0], y[1], y[2], y[3]));
+                    sts128(dst + tc::sw_chunk(r, 2 * c + 1, BN), make_uint4(y[4], y[5], y[6], y[7]));
+                }
+                tc::fence_proxy_async();
+                warp_arrive(KV_FULL + stage);
+                ++made;
+            } else {
+                tc::fence_proxy_async();
+                warp_arrive(what);
+            }
+        };
+        auto push = [&](uint32_t what) {  // closes a copy group, which fills what barrier `what` stands for
+            cp_async_commit();
+            pend = pend << 8 | what;
+            if (open == LAG) {
+                cp_async_wait<LAG>();
+                finish(F8 ? 0u : pend >> (8 * (LAG & 3)) & 0xff);
+            } else {
+                ++open;
+            }
+        };
+        auto flush = [&]() {
+            cp_async_wait<0>();
+            for (; open > 0 && ok; --open) finish(F8 ? 0u : pend >> (8 * (open - 1)) & 0xff);
+        };
+        for (;;) {
+            const int t0 = p.tile, t1 = static_cast<int>(min(static_cast<long long>(p.nk), t0 + (end - at)));
+            const int i0 = p.qt * a.tq, ntok = min(a.tq, p.s.m - i0), rows = ntok * a.G;
+            const int kend = min(t1 * BN, p.s.L - p.s.m + i0 + ntok);
+            const int qrows = rows > 128 ? 256 : 128;
+            // ---- queries
+            ok = warp_wait(TB_QE, (unit & 1) ^ 1);
+            if (!ok) break;
+            if constexpr (!F8) {
+                for (int idx = tl; idx < qrows * (D / 8); idx += 128) {
+                    const int r = idx / (D / 8), c = idx % (D / 8);
+                    const bool on = r < rows;
+                    const int tok = on ? r / a.G : 0;
+                    const uint16_t* src = a.q + (p.s.q0 + i0 + tok) * a.q_stride +
+                                          static_cast<long long>(p.h * a.G + (on ? r - tok * a.G : 0)) * D + c * 8;
+                    cp_async16(sb + (r >> 7) * C::QTILE + tc::sw_chunk(r & 127, c, 128), src, on);
+                }
+                push(TB_QF);
+            } else {
+                for (int r = tl; r < qrows; r += 128) {
+                    const bool on = r < rows;
+                    const int tok = on ? r / a.G : 0;
+                    const uint4* src = reinterpret_cast<const uint4*>(
+                        a.q + (p.s.q0 + i0 + tok) * a.q_stride + static_cast<long long>(p.h * a.G + (on ? r - tok * a.G : 0)) * D);
+                    float mx = 0.f;
+#pragma unroll 4
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint4 w = on ? src[c] : make_uint4(0, 0, 0, 0);
+                        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 f = unpack2<F16>(x[j]);
+                            mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+                        }
+                    }
+                    const float up = row_up(mx);
+#pragma unroll 4
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint4 w = on ? src[c] : make_uint4(0, 0, 0, 0);
+                        uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 f = unpack2<F16>(x[j]);
+                            x[j] = pack2<true>(f.x * up, f.y * up);
+                        }
+                        sts128(sb + (r >> 7) * C::QTILE + tc::sw_chunk(r & 127, c, 128), make_uint4(x[0], x[1], x[2], x[3]));
+                    }
+                    reinterpret_cast<float*>(sm + C::OFF_RS)[(unit & 1) * C::R + r] = a.scale_log2 * (1.f / up);
+                }
+                tc::fence_proxy_async();
+                warp_arrive(TB_QF);
+            }
+            // ---- keys and values, tile by tile
+            for (int t = t0; t < t1 && ok; ++t) {
+                const int pos = t * BN + mine;
+                const long long off = pos < kend ? row_of(a, p.n, p.h, pos) : -1;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    uint32_t dst;
+                    if constexpr (F8) {
+                        const uint32_t ring = item % C::NRAW;
+                        dst = sb + C::OFF_RAW + ring * C::RAW + (warp & 3) * (PER * 512) + lane * 16;
+                        if (kv == 0 && lane < RW) {
+                            const uint32_t rsc = sb + C::OFF_RSC + ring * 1024 + mine * 4;
+                            cp_async4(rsc, a.ks + (off < 0 ? 0 : off), off >= 0);
+                            cp_async4(rsc + 512, a.vs + (off < 0 ? 0 : off), off >= 0);
+                        }
+                    } else {
+                        const uint32_t stage = item % NST;
+                        if (!warp_wait(KV_EMPTY + stage, (item / NST & 1) ^ 1)) {
+                            ok = false;
+                            break;
+                        }
+                        dst = sb + C::OFF_KV + stage * C::TILE;
+                    }
+                    const uint8_t* base = static_cast<const uint8_t*>(kv ? a.vc : a.kc);
+#pragma unroll 8
+                    for (int i = 0; i < PER; ++i) {
+                        const int idx = i * 32 + lane, rl = idx / CHR, c = idx % CHR;
+                        const long long ro = __shfl_sync(kFullMask, off, rl);
+                        const uint8_t* src = base + (ro < 0 ? 0 : ro * (CHR * 16)) + c * 16;
+                        cp_async16(F8 ? dst + i * 512 : dst + tc::sw_chunk(r0 + rl, c, BN), src, ro >= 0);
+                    }
+                    push(F8 ? 0u : static_cast<uint32_t>(KV_FULL) + item % NST);
+                    ++item;
+                    if (!ok) break;
+                }
+            }
+            // the MMAs of this unit, which free the query tiles, need all of its keys
+            if (ok) flush();
+            if (!ok) break;
+            at += t1 - t0;
+            ++unit;
+            if (at >= end) break;
+            next_unit<BN>(a, p);
+        }
+        cp_async_wait<0>();
+    } else if (warp == 12) {
+        // ------------------------------------------------------------ MMA issue
+        if (lane == 0) {
+            constexpr uint32_t FMT = MF16 ? 0u : (1u << 7) | (1u << 10);
+            constexpr uint32_t ID_S = (tc::idesc_bf16(128, BN, 0, 0, 0) & ~((1u << 7) | (1u << 10))) | FMT;
+            constexpr uint32_t ID_O = (tc::idesc_bf16(128, D, 0, 1, 0) & ~((1u << 7) | (1u << 10))) | FMT;
+            uint32_t base = 0, unit = 0, np[2] = {0, 0};
+            bool ok = true;
+            for (;;) {
+                const int t0 = p.tile, t1 = static_cast<int>(min(static_cast<long long>(p.nk), t0 + (end - at)));
+                const int rows = min(a.tq, p.s.m - p.qt * a.tq) * a.G;
+                const bool full = SLOTS == 2 && rows > 128;
+                const int nops = full ? 2 * (t1 - t0) : t1 - t0;
+                auto issue_s = [&](int s) {
+                    const int b = s & 1, tile = full ? s >> 1 : s;
+                    const uint32_t it = base + 2 * tile, stage = it % NST;
+                    if (!wait(KV_FULL + stage, it / NST & 1)) return false;
+                    tc::fence_after();
+                    const uint32_t qa = sb + (full ? b * C::QTILE : 0u), ka = sb + C::OFF_KV + stage * C::TILE;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        tc::mma_bf16(tm + C::TM_S + b * C::TM_SB, tc::sdesc(qa + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024),
+                                     tc::sdesc(ka + (k >> 2) * (BN * 128) + (k & 3) * 32, 16, 1024), ID_S, k > 0);
+                    tc::commit(&bars[TB_S0 + b]);
+                    if (!full || b) tc::commit(&bars[KV_EMPTY + stage]);
+                    if (s == nops - 1) tc::commit(&bars[TB_QE]);
+                    return true;
+                };
+                ok = wait(TB_QF, unit & 1);
+                tc::fence_after();
+                ok = ok && issue_s(0) && (nops < 2 || issue_s(1));
+                for (int s = 0; s < nops && ok; ++s) {
+                    const int b = s & 1, tile = full ? s >> 1 : s, o = SLOTS == 2 ? b : 0;
+                    const bool fresh = SLOTS == 2 ? s < 2 : s == 0;
+                    const uint32_t it = base + 2 * tile + 1, stage = it % NST;
+                    ok = wait(TB_P0 + b, np[b] & 1) && wait(KV_FULL + stage, it / NST & 1) &&
+                         (!fresh || wait(TB_OF0 + o, (unit & 1) ^ 1));
+                    if (!ok) break;
+                    ++np[b];
+                    tc::fence_after();
+                    const uint32_t va = sb + C::OFF_KV + stage * C::TILE;
+#pragma unroll
+                    for (int k = 0; k < BN / 16; ++k)
+                        tc::mma_bf16_ts(tm + C::TM_O + o * D, tm + C::TM_S + b * C::TM_SB + 8 * k,
+                                        tc::sdesc(va + k * 2048, BN * 128, 1024), ID_O, !fresh || k > 0);
+                    tc::commit(&bars[TB_OD0 + o]);
+                    if (!full || b) tc::commit(&bars[KV_EMPTY + stage]);
+                    if (s + 2 < nops) ok = issue_s(s + 2);
+                }
+                if (!ok) break;
+                base += 2 * (t1 - t0);
+                ++unit;
+                at += t1 - t0;
+                if (at >= end) break;
+                next_unit<BN>(a, p);
+            }
+            // nothing of this CTA's may be in flight when it ends, its barriers' arrivals included
+            tc::commit(&bars[TB_DRAIN]);
+            tc::mbar_wait(&bars[TB_DRAIN], 0, kTilesWait);
+        }
+    } else if (wg < SLOTS) {
+        // ------------------------------------------------------------ softmax: one row per thread
+        const int row = tid & 127;
+        const uint32_t trow = tm + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        uint32_t unit = 0, ns[2] = {0, 0}, od[2] = {0, 0}, nml = 0, tiles = 0;
+        (void)tiles;
+        for (;;) {
+            const int t0 = p.tile, t1 = static_cast<int>(min(static_cast<long long>(p.nk), t0 + (end - at)));
+            const int i0 = p.qt * a.tq, rows = min(a.tq, p.s.m - i0) * a.G;
+            const bool full = SLOTS == 2 && rows > 128;
+            const int nops = full ? 2 * (t1 - t0) : t1 - t0;
+            const int r = (full ? wg * 128 : 0) + row;
+            const bool live = r < rows, some = __any_sync(kFullMask, live);
+            const int vis = live ? p.s.L - p.s.m + i0 + r / a.G + 1 : 0;  // keys that this row sees
+            float c = a.scale_log2;
+            if constexpr (F8) {
+                if (!warp_wait(TB_QF, unit & 1)) break;
+                c = reinterpret_cast<const float*>(sm + C::OFF_RS)[(unit & 1) * C::R + r];
+            }
+            float ref = -INFINITY, l = 0.f;
+            bool ok = true;
+            int done = 0;  // this slot's operations of the unit
+            for (int s = SLOTS == 2 ? wg : 0; s < nops; s += SLOTS, ++done) {
+                const int b = s & 1, tile = full ? s >> 1 : s, o = SLOTS == 2 ? b : 0;
+                const uint32_t ts = trow + C::TM_S + b * C::TM_SB;
+                const float* sc = nullptr;
+                if constexpr (F8) {
+                    const uint32_t ti = tiles + tile;
+                    ok = warp_wait(TB_SC0 + (ti & 1), ti >> 1 & 1);
+                    if (!ok) break;
+                    sc = reinterpret_cast<const float*>(sm + C::OFF_SC) + (ti & 1) * 384;
+                }
+                ok = warp_wait(TB_S0 + b, ns[b] & 1);
+                if (!ok) break;
+                ++ns[b];
+                if (some) {
+                    const int lim = vis - (t0 + tile) * BN;  // visible keys of the tile
+                    const bool mask = __any_sync(kFullMask, lim < BN);
+                    auto scores = [&](int ch, float (&y)[32]) {  // y of keys ch 32 .. ch 32 + 31 (raw loaded)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            if constexpr (F8) {
+                                const float4 ks = *reinterpret_cast<const float4*>(sc + ch * 32 + i);
+                                const float4 lv = *reinterpret_cast<const float4*>(sc + 128 + ch * 32 + i);
+                                y[i] = fmaf(y[i] * c, ks.x, lv.x);
+                                y[i + 1] = fmaf(y[i + 1] * c, ks.y, lv.y);
+                                y[i + 2] = fmaf(y[i + 2] * c, ks.z, lv.z);
+                                y[i + 3] = fmaf(y[i + 3] * c, ks.w, lv.w);
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) y[i + j] *= c;
+                            }
+                        }
+                        if (mask) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (ch * 32 + i >= lim) y[i] = -INFINITY;
+                        }
+                    };
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int ch = 0; ch < BN / 32; ++ch) {
+                        float y[32];
+                        tm_ld32(ts + ch * 32, y);
+                        tc::wait_ld();
+                        scores(ch, y);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(y[i], y[i + 1]));
+                    }
+                    if (__any_sync(kFullMask, mx > ref + kRefSlack)) {
+                        const float to = fmaxf(ref, mx);
+                        const float f = to == -INFINITY ? 1.f : fast_exp2(ref - to);
+                        ref = to;
+                        l *= f;
+                        if (done > 0) {  // what has been accumulated so far
+                            ok = warp_wait(TB_OD0 + o, (od[o] + done - 1) & 1);
+                            if (!ok) break;
+#pragma unroll
+                            for (int ch = 0; ch < D / 16; ++ch) {
+                                float v[16];
+                                tc::ld16(trow + C::TM_O + o * D + ch * 16, v);
+                                tc::wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) v[i] *= f;
+                                tc::st16(trow + C::TM_O + o * D + ch * 16, v);
+                            }
+                        }
+                    }
+                    const float use = ref == -INFINITY ? 0.f : ref;
+#pragma unroll
+                    for (int ch = 0; ch < BN / 32; ++ch) {
+                        float y[32];
+                        uint32_t w[16];
+                        tm_ld32(ts + ch * 32, y);
+                        tc::wait_ld();
+                        scores(ch, y);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            float x[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) x[j] = fast_exp2(y[i + j] - use);
+                            if constexpr (F8) {
+                                const float4 iv = *reinterpret_cast<const float4*>(sc + 256 + ch * 32 + i);
+                                l = fmaf(x[0], iv.x, fmaf(x[1], iv.y, fmaf(x[2], iv.z, fmaf(x[3], iv.w, l))));
+                            } else {
+                                l += (x[0] + x[1]) + (x[2] + x[3]);
+                            }
+                            w[i / 2] = pack2<MF16>(x[0], x[1]);
+                            w[i / 2 + 1] = pack2<MF16>(x[2], x[3]);
+                        }
+                        tm_st16(ts + ch * 16, w);
+                    }
+                    tc::wait_st();
+                }
+                tc::fence_before();
+                warp_arrive(TB_P0 + b);
+            }
+            if (!ok) break;
+            // operations of the two accumulators up to the unit's end
+            od[0] += SLOTS == 2 ? (nops + 1) / 2 : nops;
+            od[1] += SLOTS == 2 ? nops / 2 : 0;
+            tiles += t1 - t0;
+
+            // ---- the unit's rows
+            const bool both = SLOTS == 2 && !full;  // the slots hold two parts of the same rows
+            float f0 = 1.f, f1 = 0.f;
+            if (both && wg == 1) {
+                ok = warp_wait(TB_ME, (nml & 1) ^ 1);
+                if (!ok) break;
+                ml_s[row][0] = ref;
+                ml_s[row][1] = l;
+                warp_arrive(TB_MF);
+            } else {
+                if (both) {
+                    ok = warp_wait(TB_MF, nml & 1);
+                    if (!ok) break;
+                    const float ref1 = ml_s[row][0], l1 = ml_s[row][1];
+                    warp_arrive(TB_ME);
+                    const float top = fmaxf(ref, ref1);
+                    if (top != -INFINITY) {
+                        f0 = fast_exp2(ref - top);
+                        f1 = fast_exp2(ref1 - top);
+                    }
+                    l = l * f0 + l1 * f1;
+                    ref = top;
+                }
+                const int o = SLOTS == 2 ? wg : 0;
+                ok = warp_wait(TB_OD0 + o, (od[o] - 1) & 1) && (!both || nops < 2 || warp_wait(TB_OD0 + 1, (od[1] - 1) & 1));
+                if (!ok) break;
+                if (some) {
+                    const bool whole = t0 == 0 && t1 == p.nk;
+                    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+                    const long long orow = (p.s.q0 + i0 + r / a.G) * a.Hq + p.h * a.G + r % a.G;
+                    float* part = a.part + (static_cast<long long>(blockIdx.x) * 2 + (t0 > 0 ? 0 : 1)) *
+                                               (static_cast<long long>(C::R) * (D + 2));
+#pragma unroll 1
+                    for (int ch = 0; ch < D / 32; ++ch) {
+                        float v[32];
+                        tm_ld32(trow + C::TM_O + o * D + ch * 32, v);
+                        tc::wait_ld();
+                        if (both && nops > 1) {
+                            float u[32];
+                            tm_ld32(trow + C::TM_O + D + ch * 32, u);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = fmaf(f1, u[i], f0 * v[i]);
+                        }
+                        if (live && whole) {
+                            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D + ch * 32);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                dst[i] = make_uint4(pack2<F16>(v[8 * i] * inv, v[8 * i + 1] * inv), pack2<F16>(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
+                                                    pack2<F16>(v[8 * i + 4] * inv, v[8 * i + 5] * inv), pack2<F16>(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
+                        } else if (live) {
+                            float4* dst = reinterpret_cast<float4*>(part + static_cast<long long>(r) * D + ch * 32);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                        }
+                        __syncwarp();
+                    }
+                    if (live) {
+                        if (!whole) {
+                            part[static_cast<long long>(C::R) * D + r] = ref;
+                            part[static_cast<long long>(C::R) * (D + 1) + r] = l;
+                        } else if (a.lse) {
+                            a.lse[orow] = l == 0.f ? -INFINITY : ((ref == -INFINITY ? 0.f : ref) + log2f(l)) * kLn2;
+                        }
+                    }
+                }
+                tc::fence_before();
+                warp_arrive(TB_OF0 + o);
+                if (both) warp_arrive(TB_OF0 + 1);
+            }
+            if (both) ++nml;
+            ++unit;
+            at += t1 - t0;
+            if (at >= end) break;
+            next_unit<BN>(a, p);
+        }
+    }
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 12) tc::tmem_dealloc(tm, 512);
+    if (tid == 0 && abort_flag) atomicOr(a.status, kStatusTimeout);
+}
+
+}  // namespace attn
+}  // namespace gdn

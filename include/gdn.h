@@ -445,7 +445,7 @@ size_t attn_paged_workspace_size(int D);
  * Products take 16-bit operands (dtype; binary16 for an 8-bit cache, which its values and the scaled
  * queries fit exactly), weights are rounded to that type for the second product; scores, sums and
  * outputs accumulate in f32.  Results do not depend on timing.
- * Supported: D in {64, 128, 256}, Hq % Hkv == 0, Hq / Hkv <= 16, cache_dtype dtype or GDN_E4M3,
+ * Supported: D in {64, 128, 256}, Hq % Hkv == 0, Hq / Hkv <= 128, cache_dtype dtype or GDN_E4M3,
  * max_pages * page_size < 2^31, T < 2^30.
  */
 gdn_status attn_paged(const void* q, int64_t q_stride, gdn_dtype dtype, const void* k_cache, const void* v_cache,

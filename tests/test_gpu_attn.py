@@ -99,7 +99,8 @@ FORMS = [
     ([5, 2], [3, 40], 4, 2),                           # more queries than cached keys: empty rows first
     ([33, 1, 70], [33, 500, 130], 4, 1),               # chunks of several query tiles beside a single token
     ([130, 257], [300, 257], 6, 2),                    # long chunks
-    ([3], [90], 16, 1),                                # 16 heads on a key head
+    ([3], [90], 16, 1), ([2], [300], 40, 2),           # wide groups: 16 and 20 heads on a key head
+    ([2, 1], [70, 9], 128, 1),                         # the widest
 ]
 
 
