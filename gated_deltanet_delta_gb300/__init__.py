@@ -49,6 +49,8 @@ _lib = None
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libgdn.so (once) and declare the C signatures.  Raises OSError if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -126,9 +128,15 @@ def _check(status: int, what: str) -> None:
 # ------------------------------------------------------------------------------------------------
 # torch marshalling helpers (torch is imported lazily so that the ABI can be loaded without it)
 # ------------------------------------------------------------------------------------------------
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t) -> int | None:
@@ -136,12 +144,14 @@ def _ptr(t) -> int | None:
 
 
 def _stream(device) -> int:
-    torch = _torch()
-    return torch.cuda.current_stream(device).cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
 def _want(t, name: str, dtype, shape=None):
     torch = _torch()
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:

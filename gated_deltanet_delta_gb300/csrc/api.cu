@@ -750,7 +750,6 @@ extern "C" gdn_status attn_paged(const void* q, int64_t q_stride, gdn_dtype dtyp
     a.cu = cu_seqlens;
     a.out = out;
     a.lse = lse;
-    a.part = static_cast<float*>(workspace);
     a.status = dev_status;
     a.T = T;
     a.num_pages = num_pages;
@@ -767,7 +766,7 @@ extern "C" gdn_status attn_paged(const void* q, int64_t q_stride, gdn_dtype dtyp
     a.page_mul = static_cast<uint32_t>(((1ULL << (31 + sh)) + page_size - 1) / page_size);
     a.page_shift = 31 + sh;
     const cudaError_t e =
-        gdn::launch_attn(a, D, cache_dtype == GDN_E4M3, static_cast<int>(max_q < T ? max_q : T), static_cast<cudaStream_t>(stream));
+        gdn::launch_attn(a, workspace, D, cache_dtype == GDN_E4M3, static_cast<int>(max_q < T ? max_q : T), static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
     return launched(fn);
 }

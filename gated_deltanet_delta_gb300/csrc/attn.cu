@@ -12,6 +12,8 @@ namespace {
 constexpr int kMaxDevices = 64;
 constexpr int kMaxCtas = 608;      // of the row kernel; the workspace has two partial slots for each
 constexpr int kMaxTileCtas = 160;  // of the tile kernel, likewise
+constexpr size_t kJoinBytes = kMaxCtas * sizeof(AttnJoin);  // at the workspace's start
+static_assert(kJoinBytes % 16 == 0, "the partials are read by 16 bytes");
 std::atomic<int> g_sms[kMaxDevices];
 
 cudaError_t sm_count(int* n) {
@@ -43,11 +45,10 @@ cudaError_t raise_smem(K kernel, int bytes, std::atomic<unsigned long long>& don
 
 // The joining kernel starts while the main kernel still runs (programmatic dependent launch) and waits
 // for it before it reads the partials.
-template <int BN>
-cudaError_t launch_combine(const AttnArgs& a, int R, int D, int RB, int grid, cudaStream_t stream) {
-    if (grid < 2) return cudaSuccess;
+template <int D>
+cudaError_t launch_combine(const AttnArgs& a, int R, int RB, int grid, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid - 1, (R + RB - 1) / RB);
+    cfg.gridDim = dim3(grid, (R + RB - 1) / RB);
     cfg.blockDim = dim3(attn::kCombineThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -55,7 +56,7 @@ cudaError_t launch_combine(const AttnArgs& a, int R, int D, int RB, int grid, cu
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn::attn_combine_kernel<BN>, a, R, D, RB, grid);
+    return cudaLaunchKernelEx(&cfg, attn::attn_combine_kernel<D>, a, R, RB);
 }
 
 template <int D, bool F16, bool F8>
@@ -72,7 +73,7 @@ cudaError_t launch_rows(AttnArgs a, cudaStream_t stream) {
     attn::attn_rows_kernel<D, F16, F8><<<grid, attn::kRowsNT, C::SMEM, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_combine<attn::kRowsBN>(a, attn::kRowsTile, D, 4, grid, stream);
+    return launch_combine<D>(a, attn::kRowsTile, attn::kRowsTile, grid, stream);
 }
 
 template <int D, bool F16, bool F8>
@@ -83,13 +84,22 @@ cudaError_t launch_tiles(AttnArgs a, cudaStream_t stream) {
     cudaError_t e = sm_count(&sms);
     if (e == cudaSuccess) e = raise_smem(attn::attn_tiles_kernel<D, F16, F8>, C::SMEM, done);
     if (e != cudaSuccess) return e;
+    // the split of registers among roles waits forever where the launch has fewer than it adds up to
+    static std::atomic<int> regs{0};
+    if (regs.load(std::memory_order_relaxed) == 0) {
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, attn::attn_tiles_kernel<D, F16, F8>);
+        if (e != cudaSuccess) return e;
+        regs.store(fa.numRegs, std::memory_order_relaxed);
+    }
+    if (regs.load(std::memory_order_relaxed) < attn::kRegsLaunch) return cudaErrorInvalidConfiguration;
     a.tq = C::R / a.G;
     a.min_tiles = 1;
     const int grid = std::min(sms, kMaxTileCtas);
     attn::attn_tiles_kernel<D, F16, F8><<<grid, attn::kTilesNT, C::SMEM, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_combine<C::BN>(a, C::R, D, 16, grid, stream);
+    return launch_combine<D>(a, C::R, 32, grid, stream);
 }
 
 template <int D, bool F16, bool F8>
@@ -110,10 +120,13 @@ cudaError_t launch_d(const AttnArgs& a, bool f8, int max_q, cudaStream_t stream)
 size_t attn_workspace_bytes(int D) {
     const size_t rows = static_cast<size_t>(kMaxCtas) * attn::kRowsTile;
     const size_t tiles = static_cast<size_t>(kMaxTileCtas) * (D == 256 ? attn::TilesCfg<256, false>::R : attn::TilesCfg<128, false>::R);
-    return std::max(rows, tiles) * 2 * (D + 2) * sizeof(float);
+    return kJoinBytes + std::max(rows, tiles) * 2 * (D + 2) * sizeof(float);
 }
 
-cudaError_t launch_attn(const AttnArgs& a, int D, bool f8, int max_q, cudaStream_t stream) {
+cudaError_t launch_attn(const AttnArgs& args, void* workspace, int D, bool f8, int max_q, cudaStream_t stream) {
+    AttnArgs a = args;
+    a.joins = static_cast<AttnJoin*>(workspace);
+    a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kJoinBytes);
     if (D == 64) return launch_d<64>(a, f8, max_q, stream);
     if (D == 128) return launch_d<128>(a, f8, max_q, stream);
     return launch_d<256>(a, f8, max_q, stream);

@@ -21,6 +21,7 @@
 // The lengths are on the device; every CTA finds its range from them itself.
 #pragma once
 
+#include "attn_mma.cuh"
 #include "common.cuh"
 #include "kernel_args.h"
 
@@ -195,71 +196,100 @@ __device__ __forceinline__ long long row_of(const AttnArgs& a, int n, int h, int
     return (page * a.Hkv + h) * a.page_size + (pos - pg * a.page_size);
 }
 
-__device__ __forceinline__ void store_out(const AttnArgs& a, long long at, float x) {
-    uint16_t* o = static_cast<uint16_t*>(a.out);
-    o[at] = a.f16 ? __half_as_ushort(__float2half_rn(x)) : f32_to_bf16_rne(x);
-}
-
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Joins the partials of one unit that spans CTAs: block (c, y) looks at the boundary at entry c per.
-// Where that is the first boundary inside a unit, its partials are slot 1 of CTA c - 1 and slot 0 of
-// CTAs c .. (end - 1) / per; the block joins rows y RB .. of the tile.  Otherwise it has nothing to do.
-// A slot holds R rows of D sums, then R references, then R values of l.
-constexpr int kCombineThreads = 128;
-template <int BN>
-__global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const __grid_constant__ AttnArgs a, int R, int D,
-                                                                       int RB, int grid_main) {
-    __shared__ PlanSmem sm;
-    const int tid = threadIdx.x;
-    long long w0;
-    const long long W = plan_total<BN, kCombineThreads>(a, sm, w0, false);
-    const long long per = max((W + grid_main - 1) / grid_main, static_cast<long long>(a.min_tiles));
-    const long long c = blockIdx.x + 1, at = c * per;
-    if (at >= W) return;
-    const Place p = locate<BN, kCombineThreads>(a, sm, w0, at);
-    const long long u0 = at - p.tile, u1 = u0 + p.nk;
-    if (p.tile == 0 || u0 < at - per) return;
-    const int i0 = p.qt * a.tq, rows = min(a.tq, p.s.m - i0) * a.G;
-    const int r0 = blockIdx.y * RB;
-    if (r0 >= rows) return;
-    const int parts = 1 + static_cast<int>((u1 - 1) / per - c + 1);
+// What a CTA leaves for attn_combine_kernel: parts = 0, or the unit that begins in its range and goes on
+// in the next parts - 1 CTAs'.
+__device__ __forceinline__ void leave_join(const AttnArgs& a, const Place& p, int t0, int t1, long long per) {
+    AttnJoin j;
+    const int i0 = p.qt * a.tq;
+    j.parts = t0 > 0 || t1 == p.nk ? 0 : 1 + static_cast<int>((p.nk - t1 + per - 1) / per);
+    j.rows = min(a.tq, p.s.m - i0) * a.G;
+    j.h = p.h;
+    j.pad = 0;
+    j.token = p.s.q0 + i0;
+    a.joins[blockIdx.x] = j;
+}
+__device__ __forceinline__ void leave_no_join(const AttnArgs& a) { a.joins[blockIdx.x].parts = 0; }
+
+// Joins the partials of the unit that begins in CTA blockIdx.x of the main kernel and ends in a later one:
+// slot 1 of that CTA and slot 0 of the parts - 1 after it, in that order.  A slot holds R rows of D sums,
+// then R references, then R values of l.  D / 4 threads make a group, which owns a row (four columns per
+// thread); with more groups than rows, several groups share a row's partials.  blockIdx.y: rows RB ..
+constexpr int kCombineThreads = 512;
+__device__ __forceinline__ void weigh(float f, float lp, const float4& v, float& l, float4& acc) {
+    l = fmaf(f, lp, l);
+    acc.x = fmaf(f, v.x, acc.x);
+    acc.y = fmaf(f, v.y, acc.y);
+    acc.z = fmaf(f, v.z, acc.z);
+    acc.w = fmaf(f, v.w, acc.w);
+}
+template <int D>
+__global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const __grid_constant__ AttnArgs a, int R, int RB) {
+    constexpr int TPR = D / 4, GROUPS = kCombineThreads / TPR;
+    __shared__ float4 acc_s[kCombineThreads];
+    __shared__ float2 rl_s[GROUPS];
     pdl_wait();
+    const AttnJoin j = a.joins[blockIdx.x];
+    const int r0 = blockIdx.y * RB, nr = min(RB, j.rows - r0);
+    if (j.parts < 2 || nr <= 0) return;
+    const int g = threadIdx.x / TPR, lane = threadIdx.x % TPR, col = lane * 4;
+    const int slices = max(1, min(j.parts, GROUPS / nr));
     const long long slot = static_cast<long long>(R) * (D + 2);
-    const float* first = a.part + ((c - 1) * 2 + 1) * slot;
-    const float* rest = a.part + c * 2 * slot;
-    // one group of D / 4 threads per row, four columns each
-    const int per_row = D / 4, groups = kCombineThreads / per_row, col = (tid % per_row) * 4;
-    for (int r = r0 + tid / per_row; r < min(r0 + RB, rows); r += groups) {
-        float ref = -INFINITY;
-        for (int i = 0; i < parts; ++i) {
-            const float* s = i == 0 ? first : rest + (i - 1) * 2 * slot;
-            ref = fmaxf(ref, s[static_cast<long long>(R) * D + r]);
-        }
+    const float* first = a.part + (blockIdx.x * 2LL + 1) * slot;
+    const float* rest = a.part + (blockIdx.x + 1) * 2LL * slot - 2 * slot;  // partial i >= 1 at rest + 2 i slot
+    // partials sl, sl + slices, .. of row r
+    auto gather = [&](int r, int sl, float& ref, float& l, float4& acc) {
+        ref = -INFINITY;
+#pragma unroll 8
+        for (int i = sl; i < j.parts; i += slices)
+            ref = fmaxf(ref, (i == 0 ? first : rest + i * 2 * slot)[static_cast<long long>(R) * D + r]);
         const float base = ref == -INFINITY ? 0.f : ref;
-        float l = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        l = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int i = 0; i < parts; ++i) {
-            const float* s = i == 0 ? first : rest + (i - 1) * 2 * slot;
-            const float f = exp2f(s[static_cast<long long>(R) * D + r] - base);
+        for (int i = sl; i < j.parts; i += slices) {
+            const float* s = i == 0 ? first : rest + i * 2 * slot;
             const float4 v = *reinterpret_cast<const float4*>(s + static_cast<long long>(r) * D + col);
-            l = fmaf(f, s[static_cast<long long>(R) * (D + 1) + r], l);
-            acc.x = fmaf(f, v.x, acc.x);
-            acc.y = fmaf(f, v.y, acc.y);
-            acc.z = fmaf(f, v.z, acc.z);
-            acc.w = fmaf(f, v.w, acc.w);
+            weigh(exp2f(s[static_cast<long long>(R) * D + r] - base), s[static_cast<long long>(R) * (D + 1) + r], v, l, acc);
         }
+    };
+    auto finish = [&](int r, float ref, float l, const float4& acc) {
         const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-        const long long row = (p.s.q0 + i0 + r / a.G) * a.Hq + p.h * a.G + r % a.G;
-        const long long o = row * D + col;
-        store_out(a, o, acc.x * inv);
-        store_out(a, o + 1, acc.y * inv);
-        store_out(a, o + 2, acc.z * inv);
-        store_out(a, o + 3, acc.w * inv);
-        if (a.lse && col == 0) a.lse[row] = l == 0.f ? -INFINITY : (base + log2f(l)) * kLn2;
+        const long long row = (j.token + r / a.G) * a.Hq + j.h * a.G + r % a.G;
+        uint2 w;
+        w.x = a.f16 ? pack2<true>(acc.x * inv, acc.y * inv) : pack2<false>(acc.x * inv, acc.y * inv);
+        w.y = a.f16 ? pack2<true>(acc.z * inv, acc.w * inv) : pack2<false>(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * D + col) = w;
+        if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : ((ref == -INFINITY ? 0.f : ref) + log2f(l)) * kLn2;
+    };
+    float ref, l;
+    float4 acc;
+    if (slices == 1) {
+        for (int r = g; r < nr; r += GROUPS) {
+            gather(r0 + r, 0, ref, l, acc);
+            finish(r0 + r, ref, l, acc);
+        }
+        return;
     }
+    if (g < nr * slices) {
+        gather(r0 + g % nr, g / nr, ref, l, acc);
+        acc_s[threadIdx.x] = acc;
+        if (lane == 0) rl_s[g] = make_float2(ref, l);
+    }
+    __syncthreads();
+    if (g >= nr) return;
+    float top = -INFINITY;
+    for (int k = 0; k < slices; ++k) top = fmaxf(top, rl_s[k * nr + g].x);
+    const float base = top == -INFINITY ? 0.f : top;
+    l = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < slices; ++k) {
+        const float2 rl = rl_s[k * nr + g];
+        weigh(exp2f(rl.x - base), rl.y, acc_s[(k * nr + g) * TPR + lane], l, acc);
+    }
+    finish(r0 + g, top, l, acc);
 }
 
 }  // namespace attn

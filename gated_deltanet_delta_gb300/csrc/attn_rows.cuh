@@ -62,7 +62,10 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
     pdl_launch();
     const long long per = max((W + gridDim.x - 1) / static_cast<long long>(gridDim.x), static_cast<long long>(a.min_tiles));
     long long at = blockIdx.x * per;
-    if (at >= W) return;
+    if (at >= W) {
+        if (tid == 0) leave_no_join(a);
+        return;
+    }
     const long long end = min(at + per, W);
     Place p = locate<BN, kRowsNT>(a, plan, w0, at);
 
@@ -367,7 +370,10 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
             }
         }
         at += t1 - t0;
-        if (at >= end) break;
+        if (at >= end) {
+            if (tid == 0) leave_join(a, p, t0, t1, per);
+            break;
+        }
         next_unit<BN>(a, p);
         __syncthreads();  // the rings are written again
     }

@@ -59,7 +59,7 @@ struct TilesCfg {
 
 enum : int { TB_QF = 0, TB_QE, TB_S0, TB_S1, TB_P0, TB_P1, TB_OD0, TB_OD1, TB_OF0, TB_OF1, TB_MF, TB_ME, TB_SC0, TB_SC1, TB_DRAIN, TB_KV };
 
-__device__ __forceinline__ void tm_ld32(uint32_t taddr, float (&v)[32]) {
+__device__ __forceinline__ void tm_ld32(uint32_t taddr, float* v) {
     uint32_t r[32];
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -82,6 +82,52 @@ __device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&r)[16])
         : "memory");
 }
 
+// Pairs of fp32 operations in one instruction (f32x2).
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float x, float y) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpair(f32x2 p, float* x) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x[0]), "=f"(x[1]) : "l"(p)); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// x <- 2^(x times + plus), both elements
+__device__ __forceinline__ void pair_exp2(float* x, float times, float plus) {
+    unpair(fma2(pair(x[0], x[1]), pair(times, times), pair(plus, plus)), x);
+    x[0] = fast_exp2(x[0]);
+    x[1] = fast_exp2(x[1]);
+}
+// y <- x c k + v
+__device__ __forceinline__ void pair_fma(float* y, const float* x, float c, float k0, float k1, float v0, float v1) {
+    unpair(fma2(mul2(pair(x[0], x[1]), pair(c, c)), pair(k0, k1), pair(v0, v1)), y);
+}
+__device__ __forceinline__ void pair_add(float* s, const float* x) { unpair(add2(pair(s[0], s[1]), pair(x[0], x[1])), s); }
+__device__ __forceinline__ void pair_mac(float* s, const float* x, float k0, float k1) {
+    unpair(fma2(pair(x[0], x[1]), pair(k0, k1), pair(s[0], s[1])), s);
+}
+
+// Registers per thread after the roles part: the softmax holds a row of S (the launch's 512 x 128 registers
+// are 128 x (184 + 184 + 72 + 72)).
+constexpr int kRegsLaunch = 128, kRegsSoftmax = 184, kRegsOther = 72;
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 template <int D, bool F16, bool F8>
 __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_constant__ AttnArgs a) {
     using C = TilesCfg<D, F8>;
@@ -100,7 +146,10 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
     pdl_launch();
     const long long per = max((W + gridDim.x - 1) / static_cast<long long>(gridDim.x), static_cast<long long>(a.min_tiles));
     long long at = blockIdx.x * per;
-    if (at >= W) return;
+    if (at >= W) {
+        if (tid == 256) leave_no_join(a);
+        return;
+    }
     const long long end = min(at + per, W);
     Place p = locate<BN, kTilesNT>(a, plan, w0, at);
 
@@ -138,6 +187,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
     };
 
     if (wg == 2) {
+        regs_down<kRegsOther>();
         // ------------------------------------------------------------ loader
         // warp w moves rows w RW .. w RW + RW - 1 of every tile; lane l holds the cache offset of one of them
         constexpr int RW = BN / 4;
@@ -146,6 +196,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
         const int tl = tid & 127, r0 = (warp & 3) * RW, mine = r0 + lane % RW;
         uint32_t open = 0, item = 0, made = 0, pend = 0, unit = 0;
         bool ok = true;
+        if (tl == 0) leave_no_join(a);  // stands if this CTA gives up
         // the oldest group has landed: (8 bits: widen it and) hand it over
         auto finish = [&](uint32_t what) {
             if constexpr (F8) {
@@ -297,13 +348,17 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             if (!ok) break;
             at += t1 - t0;
             ++unit;
-            if (at >= end) break;
+            if (at >= end) {
+                if (tl == 0) leave_join(a, p, t0, t1, per);
+                break;
+            }
             next_unit<BN>(a, p);
         }
         cp_async_wait<0>();
-    } else if (warp == 12) {
+    } else if (wg == 3) {
         // ------------------------------------------------------------ MMA issue
-        if (lane == 0) {
+        regs_down<kRegsOther>();
+        if (warp == 12 && lane == 0) {
             constexpr uint32_t FMT = MF16 ? 0u : (1u << 7) | (1u << 10);
             constexpr uint32_t ID_S = (tc::idesc_bf16(128, BN, 0, 0, 0) & ~((1u << 7) | (1u << 10))) | FMT;
             constexpr uint32_t ID_O = (tc::idesc_bf16(128, D, 0, 1, 0) & ~((1u << 7) | (1u << 10))) | FMT;
@@ -363,6 +418,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
         }
     } else if (wg < SLOTS) {
         // ------------------------------------------------------------ softmax: one row per thread
+        regs_up<kRegsSoftmax>();
         const int row = tid & 127;
         const uint32_t trow = tm + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         uint32_t unit = 0, ns[2] = {0, 0}, od[2] = {0, 0}, nml = 0, tiles = 0;
@@ -399,37 +455,41 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                 if (some) {
                     const int lim = vis - (t0 + tile) * BN;  // visible keys of the tile
                     const bool mask = __any_sync(kFullMask, lim < BN);
-                    auto scores = [&](int ch, float (&y)[32]) {  // y of keys ch 32 .. ch 32 + 31 (raw loaded)
+                    float y[BN];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            if constexpr (F8) {
-                                const float4 ks = *reinterpret_cast<const float4*>(sc + ch * 32 + i);
-                                const float4 lv = *reinterpret_cast<const float4*>(sc + 128 + ch * 32 + i);
-                                y[i] = fmaf(y[i] * c, ks.x, lv.x);
-                                y[i + 1] = fmaf(y[i + 1] * c, ks.y, lv.y);
-                                y[i + 2] = fmaf(y[i + 2] * c, ks.z, lv.z);
-                                y[i + 3] = fmaf(y[i + 3] * c, ks.w, lv.w);
-                            } else {
+                    for (int ch = 0; ch < BN / 32; ++ch) tm_ld32(ts + ch * 32, y + ch * 32);
+                    tc::wait_ld();
+                    // y_j = raw_j times `times`, which is not negative
+                    float times = fabsf(c);
+                    if constexpr (F8) {
+                        times = 1.f;
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) y[i + j] *= c;
-                            }
+                        for (int i = 0; i < BN; i += 4) {
+                            const float4 ks = *reinterpret_cast<const float4*>(sc + i);
+                            const float4 lv = *reinterpret_cast<const float4*>(sc + 128 + i);
+                            pair_fma(y + i, y + i, c, ks.x, ks.y, lv.x, lv.y);
+                            pair_fma(y + i + 2, y + i + 2, c, ks.z, ks.w, lv.z, lv.w);
                         }
                         if (mask) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (ch * 32 + i >= lim) y[i] = -INFINITY;
+                            for (int i = 0; i < BN; ++i)
+                                if (i >= lim) y[i] = -INFINITY;
                         }
-                    };
-                    float mx = -INFINITY;
+                    } else if (mask) {
+                        times = 1.f;
 #pragma unroll
-                    for (int ch = 0; ch < BN / 32; ++ch) {
-                        float y[32];
-                        tm_ld32(ts + ch * 32, y);
-                        tc::wait_ld();
-                        scores(ch, y);
+                        for (int i = 0; i < BN; ++i) y[i] = i >= lim ? -INFINITY : y[i] * c;
+                    } else if (c < 0.f) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(y[i], y[i + 1]));
+                        for (int i = 0; i < BN; ++i) y[i] = -y[i];
                     }
+                    float m4[4] = {y[0], y[1], y[2], y[3]};
+#pragma unroll
+                    for (int i = 4; i < BN; i += 8) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) m4[j] = i + 4 + j < BN ? fmaxf(fmaxf(m4[j], y[i + j]), y[i + 4 + j]) : fmaxf(m4[j], y[i + j]);
+                    }
+                    const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * times;
                     if (__any_sync(kFullMask, mx > ref + kRefSlack)) {
                         const float to = fmaxf(ref, mx);
                         const float f = to == -INFINITY ? 1.f : fast_exp2(ref - to);
@@ -438,7 +498,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                         if (done > 0) {  // what has been accumulated so far
                             ok = warp_wait(TB_OD0 + o, (od[o] + done - 1) & 1);
                             if (!ok) break;
-#pragma unroll
+#pragma unroll 1
                             for (int ch = 0; ch < D / 16; ++ch) {
                                 float v[16];
                                 tc::ld16(trow + C::TM_O + o * D + ch * 16, v);
@@ -450,29 +510,29 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                         }
                     }
                     const float use = ref == -INFINITY ? 0.f : ref;
+                    float l2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int ch = 0; ch < BN / 32; ++ch) {
-                        float y[32];
                         uint32_t w[16];
-                        tm_ld32(ts + ch * 32, y);
-                        tc::wait_ld();
-                        scores(ch, y);
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
-                            float x[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) x[j] = fast_exp2(y[i + j] - use);
+                            float* x = y + ch * 32 + i;
+                            pair_exp2(x, times, -use);
+                            pair_exp2(x + 2, times, -use);
                             if constexpr (F8) {
                                 const float4 iv = *reinterpret_cast<const float4*>(sc + 256 + ch * 32 + i);
-                                l = fmaf(x[0], iv.x, fmaf(x[1], iv.y, fmaf(x[2], iv.z, fmaf(x[3], iv.w, l))));
+                                pair_mac(l2, x, iv.x, iv.y);
+                                pair_mac(l2 + 2, x + 2, iv.z, iv.w);
                             } else {
-                                l += (x[0] + x[1]) + (x[2] + x[3]);
+                                pair_add(l2, x);
+                                pair_add(l2 + 2, x + 2);
                             }
                             w[i / 2] = pack2<MF16>(x[0], x[1]);
                             w[i / 2 + 1] = pack2<MF16>(x[2], x[3]);
                         }
                         tm_st16(ts + ch * 16, w);
                     }
+                    l += (l2[0] + l2[1]) + (l2[2] + l2[3]);
                     tc::wait_st();
                 }
                 tc::fence_before();

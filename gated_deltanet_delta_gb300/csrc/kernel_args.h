@@ -172,6 +172,11 @@ constexpr int kWinMaxTok = 8;
 constexpr int kStatusBadCacheIndex = 1, kStatusBadSeqlens = 2, kStatusTimeout = 4, kStatusBadProbs = 8,
               kStatusBadToken = 16;
 
+struct AttnJoin {  // see attn.cuh
+    int parts, rows, h, pad;
+    long long token;
+};
+
 // Attention over a paged cache.  Caches [num_pages, Hkv, page_size, D], scales [num_pages, Hkv, page_size]
 // (null: not quantised), table [num_seqs, max_pages].
 struct AttnArgs {
@@ -186,6 +191,7 @@ struct AttnArgs {
     const int64_t* cu;
     void* out;           // [T, Hq, D]
     float* lse;          // [T, Hq] or null
+    AttnJoin* joins;     // one per CTA
     float* part;         // partial results of units that span CTAs
     int32_t* status;
     long long T, num_pages;

@@ -6,8 +6,10 @@ namespace gdn {
 
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream) {
     const int chunks = (a.V + verify::kChunk - 1) / verify::kChunk;
-    int C = 8;
-    // a CTA has 16 warps: no more CTAs than the row has chunks for
+    // Four CTAs fit an SM.  Eight per sequence while they all run at once (64 sequences of 131072: 18.7 us,
+    // with four 19.3); beyond that four (255 sequences of 100003: 47.0 us, with eight 51.1, with two 47.7).
+    int C = a.N <= 76 ? 8 : 4;
+    // a CTA has 8 warps: no more CTAs than the row has chunks for
     while (C > 1 && chunks < C * 8) C /= 2;
     const int per = (chunks + C - 1) / C + 1;
     cudaLaunchConfig_t cfg = {};

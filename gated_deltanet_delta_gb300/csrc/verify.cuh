@@ -11,8 +11,8 @@
 //
 // Bound: one row of p, and of q after a rejection, is read once: HBM for a batch, latency for one
 // sequence.  A cluster of CTAs takes a sequence: each sums its part of the row by chunks of 256
-// entries, the parts' sums cross the cluster's shared memory, and the one CTA whose part holds the mark
-// finds the chunk and reads its 256 entries again (from L2).  One launch, no workspace, no atomics.
+// entries and writes its sum into every CTA's shared memory, and the one CTA whose part holds the mark
+// finds the chunk and reads its 256 entries again (from L2) while the others are already gone.  One launch, no workspace, no atomics.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -23,23 +23,32 @@
 namespace gdn {
 namespace verify {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kChunk = 256;            // entries per chunk: eight per lane
-constexpr int kMaxChunks = 4096;       // per CTA
 typedef unsigned long long u64;
 
-__device__ __forceinline__ u64 units(float p) {
-    return __float2ull_rz(fminf(fmaxf(p, 0.f), 1.f) * 68719476736.f);  // NaN counts as 0
+// P = floor(x 2^36) of a value in [0, 1] as P = hi 2^18 + lo, each plus 0x4B000000 (the bits of 2^23):
+// adding 2^23 with truncation leaves a number's whole part in the significand.  Float additions run at
+// full rate; a conversion to 64-bit integers took 50 cycles per warp and four fifths of the kernel's time.
+struct Units {
+    int hi, lo;
+};
+__device__ __forceinline__ Units units(float x) {
+    const float h = __fmaf_rz(x, 262144.f, 8388608.f);
+    const float rest = __fmaf_rn(x, 262144.f, 8388608.f - h);  // exact, in [0, 1)
+    return {__float_as_int(h), __float_as_int(__fmaf_rz(rest, 262144.f, 8388608.f))};
 }
-__device__ __forceinline__ u64 weight(float p, float q) {
-    const u64 a = units(p), b = units(q);
-    return a > b ? a - b : 0;
+// Adds max(P - Q, 0) to hi 2^18 + lo.  x > y implies P >= Q; NaN counts as 0.
+__device__ __forceinline__ void add_weight(float x, float y, int& hi, int& lo) {
+    x = __saturatef(x);
+    y = __saturatef(y);
+    const Units a = units(x), b = units(y);
+    if (x > y) {
+        hi += a.hi - b.hi;
+        lo += a.lo - b.lo;
+    }
 }
-__device__ __forceinline__ u64 warp_sum(u64 x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFullMask, x, o);
-    return x;
-}
+__device__ __forceinline__ u64 joined(int hi, int lo) { return static_cast<u64>((static_cast<long long>(hi) << 18) + lo); }
 __device__ __forceinline__ u64 warp_scan(u64 x, int lane) {  // inclusive
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -49,11 +58,11 @@ __device__ __forceinline__ u64 warp_scan(u64 x, int lane) {  // inclusive
     return x;
 }
 
-__global__ void __launch_bounds__(kThreads) draft_verify_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const __grid_constant__ VerifyArgs a) {
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     extern __shared__ u64 sums[];        // this CTA's chunks
-    __shared__ u64 total_s[2];
+    __shared__ u64 total_s[2][8];        // every CTA's total, by rank, of the two passes
     __shared__ int count_s, drafts_s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
@@ -100,20 +109,31 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const __grid_con
     u64 mine = 0, all = 0, before = 0;
     for (int pass = 0; pass < 2; ++pass) {
         mine = 0;
-        for (int c = c0 + warp; c < c1; c += kThreads / 32) {
-            float x[8], y[8];
+        // one chunk ahead: a warp's next sixteen loads are in flight while it adds up this one's
+        float x[8], y[8], xn[8], yn[8];
+        auto load = [&](int c, float (&u)[8], float (&v)[8]) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int i = c * kChunk + j * 32 + lane;
-                x[j] = i < a.V ? p[i] : 0.f;
-                y[j] = q && i < a.V ? q[i] : 0.f;
+                const bool in = c < c1 && i < a.V;
+                u[j] = in ? p[i] : 0.f;
+                v[j] = q && in ? q[i] : 0.f;
             }
-            u64 s = 0;
+        };
+        load(c0 + warp, x, y);
+        for (int c = c0 + warp; c < c1; c += kThreads / 32) {
+            load(c + kThreads / 32, xn, yn);
+            int hi = 0, lo = 0;  // 256 entries of at most 2^18: no overflow
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s += weight(x[j], y[j]);
-            s = warp_sum(s);
+            for (int j = 0; j < 8; ++j) add_weight(x[j], y[j], hi, lo);
+            const u64 s = joined(__reduce_add_sync(kFullMask, hi), __reduce_add_sync(kFullMask, lo));
             if (lane == 0) sums[c - c0] = s;
             mine += s;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[j] = xn[j];
+                y[j] = yn[j];
+            }
         }
         __shared__ u64 warp_s[kThreads / 32];
         if (lane == 0) warp_s[warp] = mine;
@@ -121,11 +141,11 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const __grid_con
         mine = 0;
 #pragma unroll
         for (int i = 0; i < kThreads / 32; ++i) mine += warp_s[i];
-        if (tid == 0) total_s[pass] = mine;
+        if (tid < C) *cluster.map_shared_rank(&total_s[pass][rank], tid) = mine;
         cluster.sync();
         all = before = 0;
         for (int r = 0; r < C; ++r) {
-            const u64 s = *cluster.map_shared_rank(&total_s[pass], r);
+            const u64 s = total_s[pass][r];
             all += s;
             if (r < rank) before += s;
         }
@@ -159,7 +179,9 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const __grid_con
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int i = i0 + j * 32 + lane;
-            w[j] = i < a.V ? weight(p[i], q ? q[i] : 0.f) : 0;
+            int hi = 0, lo = 0;
+            if (i < a.V) add_weight(p[i], q ? q[i] : 0.f, hi, lo);
+            w[j] = joined(hi, lo);
         }
         int token = -1;
 #pragma unroll
@@ -184,7 +206,6 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const __grid_con
         for (int t = tid; t <= a.T; t += kThreads)
             if (t != count) out[t] = t < count ? a.drafts[static_cast<long long>(n) * a.T + t] : -1;
     }
-    cluster.sync();  // a CTA's totals stay readable until all have read them
 }
 
 }  // namespace verify
