@@ -120,6 +120,18 @@ __device__ __forceinline__ void pair_mac(float* s, const float* x, float k0, flo
     unpair(fma2(pair(x[0], x[1]), pair(k0, k1), pair(s[0], s[1])), s);
 }
 
+// The same value in every lane, as the compiler sees it too.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(kFullMask, x, 0); }
+__device__ __forceinline__ uint64_t uniform(uint64_t x) {
+    return static_cast<uint64_t>(uniform(static_cast<uint32_t>(x >> 32))) << 32 | uniform(static_cast<uint32_t>(x));
+}
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect() {
+    uint32_t one;
+    asm volatile("{.reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p;}" : "=r"(one));
+    return one != 0;
+}
+
 // Registers per thread after the roles part: the softmax holds a row of S (the launch's 512 x 128 registers
 // are 128 x (184 + 184 + 72 + 72)).
 constexpr int kRegsLaunch = 128, kRegsSoftmax = 184, kRegsOther = 72;
@@ -357,64 +369,84 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
         cp_async_wait<0>();
     } else if (wg == 3) {
         // ------------------------------------------------------------ MMA issue
+        // The whole warp runs the loop, and one elected lane issues: descriptors stay warp-uniform (an MMA
+        // takes them from uniform registers; issued from a branch on the lane index, each one's operands are
+        // moved there first, which made the issue twice as long as the products).
         regs_down<kRegsOther>();
-        if (warp == 12 && lane == 0) {
+        if (warp == 12) {
             constexpr uint32_t FMT = MF16 ? 0u : (1u << 7) | (1u << 10);
             constexpr uint32_t ID_S = (tc::idesc_bf16(128, BN, 0, 0, 0) & ~((1u << 7) | (1u << 10))) | FMT;
             constexpr uint32_t ID_O = (tc::idesc_bf16(128, D, 0, 1, 0) & ~((1u << 7) | (1u << 10))) | FMT;
-            uint32_t base = 0, unit = 0, np[2] = {0, 0};
+            const uint32_t tmu = uniform(tm);
+            const uint64_t dq = uniform(tc::sdesc(sb, 16, 1024)), dk = uniform(tc::sdesc(sb + C::OFF_KV, 16, 1024));
+            const uint64_t dv = uniform(tc::sdesc(sb + C::OFF_KV, BN * 128, 1024));
+            uint32_t unit = 0, np[2] = {0, 0};
+            uint32_t ks = 0, kp = 0, vs = 1, vp = 0;  // stage and parity of the next K tile, of the next V tile
+            auto step = [](uint32_t& stage, uint32_t& parity) {
+                stage += 2;
+                if (stage >= NST) {
+                    stage -= NST;
+                    parity ^= 1;
+                }
+            };
             bool ok = true;
             for (;;) {
                 const int t0 = p.tile, t1 = static_cast<int>(min(static_cast<long long>(p.nk), t0 + (end - at)));
                 const int rows = min(a.tq, p.s.m - p.qt * a.tq) * a.G;
-                const bool full = SLOTS == 2 && rows > 128;
-                const int nops = full ? 2 * (t1 - t0) : t1 - t0;
+                const bool full = uniform(SLOTS == 2 && rows > 128 ? 1u : 0u) != 0;
+                const int nops = static_cast<int>(uniform(static_cast<uint32_t>(full ? 2 * (t1 - t0) : t1 - t0)));
                 auto issue_s = [&](int s) {
-                    const int b = s & 1, tile = full ? s >> 1 : s;
-                    const uint32_t it = base + 2 * tile, stage = it % NST;
-                    if (!wait(KV_FULL + stage, it / NST & 1)) return false;
-                    tc::fence_after();
-                    const uint32_t qa = sb + (full ? b * C::QTILE : 0u), ka = sb + C::OFF_KV + stage * C::TILE;
+                    const int b = s & 1;
+                    if (!warp_wait(KV_FULL + ks, kp)) return false;
+                    const uint64_t qa = dq + (full && b ? C::QTILE >> 4 : 0u), ka = dk + ks * (C::TILE >> 4);
+                    const bool last = !full || b;  // of this K tile's products
+                    if (elect()) {
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        tc::mma_bf16(tm + C::TM_S + b * C::TM_SB, tc::sdesc(qa + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024),
-                                     tc::sdesc(ka + (k >> 2) * (BN * 128) + (k & 3) * 32, 16, 1024), ID_S, k > 0);
-                    tc::commit(&bars[TB_S0 + b]);
-                    if (!full || b) tc::commit(&bars[KV_EMPTY + stage]);
-                    if (s == nops - 1) tc::commit(&bars[TB_QE]);
+                        for (int k = 0; k < D / 16; ++k)
+                            tc::mma_bf16(tmu + C::TM_S + b * C::TM_SB, qa + ((k >> 2) * 16384 + (k & 3) * 32) / 16,
+                                         ka + ((k >> 2) * (BN * 128) + (k & 3) * 32) / 16, ID_S, k > 0);
+                        tc::commit(&bars[TB_S0 + b]);
+                        if (last) tc::commit(&bars[KV_EMPTY + ks]);
+                        if (s == nops - 1) tc::commit(&bars[TB_QE]);
+                    }
+                    __syncwarp();
+                    if (last) step(ks, kp);
                     return true;
                 };
-                ok = wait(TB_QF, unit & 1);
-                tc::fence_after();
+                ok = warp_wait(TB_QF, unit & 1);
                 ok = ok && issue_s(0) && (nops < 2 || issue_s(1));
                 for (int s = 0; s < nops && ok; ++s) {
-                    const int b = s & 1, tile = full ? s >> 1 : s, o = SLOTS == 2 ? b : 0;
-                    const bool fresh = SLOTS == 2 ? s < 2 : s == 0;
-                    const uint32_t it = base + 2 * tile + 1, stage = it % NST;
-                    ok = wait(TB_P0 + b, np[b] & 1) && wait(KV_FULL + stage, it / NST & 1) &&
-                         (!fresh || wait(TB_OF0 + o, (unit & 1) ^ 1));
+                    const int b = s & 1, o = SLOTS == 2 ? b : 0;
+                    const bool fresh = SLOTS == 2 ? s < 2 : s == 0, last = !full || b;
+                    ok = warp_wait(KV_FULL + vs, vp) && (!fresh || warp_wait(TB_OF0 + o, (unit & 1) ^ 1)) &&
+                         warp_wait(TB_P0 + b, np[b] & 1);
                     if (!ok) break;
                     ++np[b];
-                    tc::fence_after();
-                    const uint32_t va = sb + C::OFF_KV + stage * C::TILE;
+                    const uint64_t va = dv + vs * (C::TILE >> 4);
+                    if (elect()) {
 #pragma unroll
-                    for (int k = 0; k < BN / 16; ++k)
-                        tc::mma_bf16_ts(tm + C::TM_O + o * D, tm + C::TM_S + b * C::TM_SB + 8 * k,
-                                        tc::sdesc(va + k * 2048, BN * 128, 1024), ID_O, !fresh || k > 0);
-                    tc::commit(&bars[TB_OD0 + o]);
-                    if (!full || b) tc::commit(&bars[KV_EMPTY + stage]);
+                        for (int k = 0; k < BN / 16; ++k)
+                            tc::mma_bf16_ts(tmu + C::TM_O + o * D, tmu + C::TM_S + b * C::TM_SB + 8 * k, va + k * (2048 / 16), ID_O,
+                                            !fresh || k > 0);
+                        tc::commit(&bars[TB_OD0 + o]);
+                        if (last) tc::commit(&bars[KV_EMPTY + vs]);
+                    }
+                    __syncwarp();
+                    if (last) step(vs, vp);
                     if (s + 2 < nops) ok = issue_s(s + 2);
                 }
                 if (!ok) break;
-                base += 2 * (t1 - t0);
                 ++unit;
                 at += t1 - t0;
                 if (at >= end) break;
                 next_unit<BN>(a, p);
             }
             // nothing of this CTA's may be in flight when it ends, its barriers' arrivals included
-            tc::commit(&bars[TB_DRAIN]);
-            tc::mbar_wait(&bars[TB_DRAIN], 0, kTilesWait);
+            if (elect()) {
+                tc::commit(&bars[TB_DRAIN]);
+                tc::mbar_wait(&bars[TB_DRAIN], 0, kTilesWait);
+            }
+            __syncwarp();
         }
     } else if (wg < SLOTS) {
         // ------------------------------------------------------------ softmax: one row per thread
