@@ -1,6 +1,10 @@
 // attn.cu -- launch of attention over a paged cache: choice of the kernel and of its grid.
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <atomic>
+#include <cstring>
+#include <mutex>
 
 #include "attn_rows.cuh"
 #include "attn_tiles.cuh"
@@ -41,6 +45,35 @@ cudaError_t raise_smem(K kernel, int bytes, std::atomic<unsigned long long>& don
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess) done.fetch_or(1ull << dev, std::memory_order_release);
     return e;
+}
+
+// cuTensorMapEncodeTiled through the runtime's driver entry point (no link against libcuda).
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static std::once_flag once;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+// A cache as rows of D elements.  16 bits: boxes of 64 features, 128-byte swizzle (an operand tile's rows);
+// 8 bits: boxes of whole rows, as they are.
+bool encode_cache(CUtensorMap* map, const void* base, long long rows, int D, int box, bool f8, bool f16) {
+    const auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * (f8 ? 1 : 2)};
+    const cuuint32_t shape[2] = {static_cast<cuuint32_t>(f8 ? D : 64), static_cast<cuuint32_t>(box)};
+    const cuuint32_t step[2] = {1, 1};
+    const CUtensorMapDataType type = f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : (f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+    return fn(map, type, 2, const_cast<void*>(base), dims, strides, shape, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The joining kernel starts while the main kernel still runs (programmatic dependent launch) and waits
@@ -95,8 +128,16 @@ cudaError_t launch_tiles(AttnArgs a, cudaStream_t stream) {
     if (regs.load(std::memory_order_relaxed) < attn::kRegsLaunch) return cudaErrorInvalidConfiguration;
     a.tq = C::R / a.G;
     a.min_tiles = 1;
+    // Boxes of at least 8 rows (the swizzle's period) that divide a page; coordinates are 32-bit
+    AttnMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    const long long cached = a.num_pages * a.Hkv * a.page_size;
+    a.box = std::min(a.page_size & -a.page_size, C::BOX);
+    if (a.box < 8 || cached < a.box || cached >= 1LL << 31) a.box = 0;
+    if (a.box && !(encode_cache(&maps.k, a.kc, cached, D, a.box, F8, F16) && encode_cache(&maps.v, a.vc, cached, D, a.box, F8, F16)))
+        return cudaErrorInvalidValue;
     const int grid = std::min(sms, kMaxTileCtas);
-    attn::attn_tiles_kernel<D, F16, F8><<<grid, attn::kTilesNT, C::SMEM, stream>>>(a);
+    attn::attn_tiles_kernel<D, F16, F8><<<grid, attn::kTilesNT, C::SMEM, stream>>>(a, maps);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_combine<D>(a, C::R, 32, grid, stream);

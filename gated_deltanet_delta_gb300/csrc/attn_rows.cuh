@@ -101,7 +101,8 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
                     qf[k][half + 2] = live ? s32[4] : 0u;
                 }
             } else {
-                // K step 4 kk + j holds, in thread column group t, features kk 64 + t 16 + 4 j + 0 .. 3
+                // K step 4 kk + j holds, in thread column group t, features kk 64 + t 16 + 4 j + 0, 2, 1, 3 (the
+                // order in which a word's bytes are widened)
                 float mx = 0.f;
 #pragma unroll
                 for (int kk = 0; kk < D / 64; ++kk) {
@@ -113,8 +114,8 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
                     const uint32_t* x = reinterpret_cast<const uint32_t*>(w);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        qf[4 * kk + j][half] = x[2 * j];
-                        qf[4 * kk + j][half + 2] = x[2 * j + 1];
+                        qf[4 * kk + j][half] = __byte_perm(x[2 * j], x[2 * j + 1], 0x5410);
+                        qf[4 * kk + j][half + 2] = __byte_perm(x[2 * j], x[2 * j + 1], 0x7632);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const float2 f = unpack2<F16>(x[2 * j + i]);
@@ -125,7 +126,7 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
                 mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 2));
                 const float up = row_up(mx);
-                rscale[half] *= 1.f / up;
+                rscale[half] *= kE4m3Up / up;
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
 #pragma unroll
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
                         const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            mma16816<true>(sc[nt], qf[4 * kk + j], e4m3x2_f16x2(x[j]), e4m3x2_f16x2(x[j] >> 16));
+                            mma16816<true>(sc[nt], qf[4 * kk + j], e4m3_even(x[j]), e4m3_odd(x[j]));
                     }
                 }
             }
@@ -295,9 +296,8 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
                     ldsm4t(b, vst + vtok * C::ROWB + rows_swz<CH>(vtok, 2 * c2 + (mi >> 1)) * 16);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const uint32_t lo = __byte_perm(b[2 * i], 0, 0x3120), hi = __byte_perm(b[2 * i + 1], 0, 0x3120);
-                        mma16816<true>(o[4 * c2 + 2 * i], pf, e4m3x2_f16x2(lo), e4m3x2_f16x2(hi));
-                        mma16816<true>(o[4 * c2 + 2 * i + 1], pf, e4m3x2_f16x2(lo >> 16), e4m3x2_f16x2(hi >> 16));
+                        mma16816<true>(o[4 * c2 + 2 * i], pf, e4m3_even(b[2 * i]), e4m3_even(b[2 * i + 1]));
+                        mma16816<true>(o[4 * c2 + 2 * i + 1], pf, e4m3_odd(b[2 * i]), e4m3_odd(b[2 * i + 1]));
                     }
                 }
             }
@@ -328,7 +328,8 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c)
                     *reinterpret_cast<float4*>(dst + ((c * 16 + 4 * t) ^ (g << 2 & 24))) =
-                        make_float4(o[2 * c][2 * half], o[2 * c + 1][2 * half], o[2 * c][2 * half + 1], o[2 * c + 1][2 * half + 1]);
+                        make_float4(o[2 * c][2 * half] * kE4m3Up, o[2 * c + 1][2 * half] * kE4m3Up, o[2 * c][2 * half + 1] * kE4m3Up,
+                                    o[2 * c + 1][2 * half + 1] * kE4m3Up);
             }
         }
         __syncthreads();

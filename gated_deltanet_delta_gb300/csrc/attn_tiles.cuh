@@ -14,9 +14,9 @@
 // warpgroup, and a warp whose lane 0 issues every MMA:  S(0) S(1) | P(0)? PV(0) S(2) | P(1)? PV(1) S(3) ..
 // Operations of one issuing thread run in order, so S(s + 2) overwrites a buffer only after PV(s) has
 // read P from it.
-// The loader gathers rows by page with cp.async (any page size; rows past the keys are zero-filled, so
-// nothing stale meets a weight of zero), three groups in flight.  8-bit caches go through a staging ring,
-// private per thread, and are widened into the tile; attn_rows.cuh says how their scales are applied.
+// The loader gathers rows by page: whole boxes of rows by TMA, the ragged end of the keys by cp.async with
+// zero fill (nothing stale may meet a weight of zero).  8-bit caches go through a staging ring, a part per
+// loader warp, and are widened into the tile; attn_rows.cuh says how their scales are applied.
 //
 // Every wait is bounded: one that runs out sets GDN_STATUS_TIMEOUT and the CTA's abort flag, on which
 // all roles leave; copies and MMAs in flight are waited for (bounded) before the CTA ends.
@@ -47,6 +47,7 @@ struct TilesCfg {
     // the V tile before it is released.
     static constexpr int LAG = F8 ? (D == 64 ? 5 : 2) : 3;
     static constexpr int NRAW = F8 ? LAG + 1 : 0;
+    static constexpr int BOX = BN / 4;                     // most rows of one TMA box: a loader warp's rows
     static constexpr uint32_t OFF_KV = SLOTS * QTILE;
     static constexpr uint32_t OFF_RAW = OFF_KV + NST * TILE;
     static constexpr uint32_t OFF_RSC = OFF_RAW + NRAW * RAW;            // raw scales of a stage: K, V
@@ -57,7 +58,7 @@ struct TilesCfg {
     static constexpr uint32_t TM_S = 0, TM_O = 256, TM_SB = BN;  // TMEM columns
 };
 
-enum : int { TB_QF = 0, TB_QE, TB_S0, TB_S1, TB_P0, TB_P1, TB_OD0, TB_OD1, TB_OF0, TB_OF1, TB_MF, TB_ME, TB_SC0, TB_SC1, TB_DRAIN, TB_KV };
+enum : int { TB_QF = 0, TB_QE, TB_S0, TB_S1, TB_P0, TB_P1, TB_OD0, TB_OD1, TB_OF0, TB_OF1, TB_MF, TB_ME, TB_SC0, TB_SC1, TB_DRAIN, TB_KV };  // then KV_FULL, KV_EMPTY and (8 bits) RAW_FULL of every loader warp
 
 __device__ __forceinline__ void tm_ld32(uint32_t taddr, float* v) {
     uint32_t r[32];
@@ -132,6 +133,14 @@ __device__ __forceinline__ bool elect() {
     return one != 0;
 }
 
+// TMA: a 2-D box at column x, row y of the cache seen as rows of D elements.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, int x, int y, uint64_t* mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(tc::smem_u32(mbar))
+        : "memory");
+}
+
 // Registers per thread after the roles part: the softmax holds a row of S (the launch's 512 x 128 registers
 // are 128 x (184 + 184 + 72 + 72)).
 constexpr int kRegsLaunch = 128, kRegsSoftmax = 184, kRegsOther = 72;
@@ -141,13 +150,14 @@ template <int N>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 template <int D, bool F16, bool F8>
-__global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnMaps maps) {
     using C = TilesCfg<D, F8>;
     constexpr bool MF16 = F16 || F8;
     constexpr int BN = C::BN, NST = C::NST, LAG = C::LAG, SLOTS = C::SLOTS;
     extern __shared__ uint8_t smem_raw[];
     __shared__ PlanSmem plan;
-    __shared__ uint64_t bars[TB_KV + 2 * NST];
+    constexpr int NBAR = TB_KV + 2 * NST + 4 * C::NRAW;
+    __shared__ uint64_t bars[NBAR];
     __shared__ float ml_s[128][2];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
@@ -169,7 +179,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
     const uint32_t sb = smem_addr(sm);
     if (warp == 12) tc::tmem_alloc(&tmem_slot, 512);
     if (tid == 0) {
-        for (int i = 0; i < TB_KV + 2 * NST; ++i) {
+        for (int i = 0; i < NBAR; ++i) {
             const bool by_warps = i == TB_QF || i == TB_P0 || i == TB_P1 || i == TB_OF0 || i == TB_OF1 || i == TB_MF ||
                                   i == TB_ME || i == TB_SC0 || i == TB_SC1 || (i >= TB_KV && i < TB_KV + NST);
             tc::mbar_init(&bars[i], by_warps ? 4 : 1);
@@ -180,7 +190,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
     __syncthreads();
     tc::fence_after();
     const uint32_t tm = tmem_slot;
-    constexpr int KV_FULL = TB_KV, KV_EMPTY = TB_KV + NST;
+    constexpr int KV_FULL = TB_KV, KV_EMPTY = TB_KV + NST, RAW_FULL = TB_KV + 2 * NST;
 
     auto wait = [&](int i, uint32_t parity) -> bool {
         if (tc::mbar_wait_or_abort(&bars[i], parity, kTilesWait, &abort_flag)) return true;
@@ -189,6 +199,11 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
     };
     auto warp_wait = [&](int i, uint32_t parity) -> bool {
         const bool ok = __all_sync(kFullMask, wait(i, parity));
+        tc::fence_after();
+        return ok;
+    };
+    auto one_wait = [&](int i, uint32_t parity) -> bool {
+        const bool ok = wait(i, parity);
         tc::fence_after();
         return ok;
     };
@@ -206,13 +221,24 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
         constexpr int CHR = (F8 ? D : 2 * D) / 16;  // 16-byte chunks per cached row
         constexpr int PER = RW * CHR / 32;          // chunks per lane and tile
         const int tl = tid & 127, r0 = (warp & 3) * RW, mine = r0 + lane % RW;
+        // rows that lie within the keys come by TMA, in boxes of a.box rows that never straddle a page; a
+        // warp with a row past the keys (or a page size without a factor of 8) uses cp.async and zero-fills
+        const int box = a.box, boxes = box ? RW / box : 0;
         uint32_t open = 0, item = 0, made = 0, pend = 0, unit = 0;
+        uint32_t raw_tma = 0, raw_phase = 0;  // 8 bits: ring slots filled by TMA, and their barriers' parities
         bool ok = true;
         if (tl == 0) leave_no_join(a);  // stands if this CTA gives up
         // the oldest group has landed: (8 bits: widen it and) hand it over
         auto finish = [&](uint32_t what) {
             if constexpr (F8) {
                 const uint32_t stage = made % NST, ring = made % C::NRAW;
+                if (raw_tma >> ring & 1) {
+                    if (!warp_wait(RAW_FULL + 4 * ring + (warp & 3), raw_phase >> ring & 1)) {
+                        ok = false;
+                        return;
+                    }
+                    raw_phase ^= 1u << ring;
+                }
                 if (!warp_wait(KV_EMPTY + stage, (made / NST & 1) ^ 1)) {
                     ok = false;
                     return;
@@ -239,8 +265,8 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                     uint32_t y[8];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        y[2 * j] = e4m3x2_f16x2(x[j]);
-                        y[2 * j + 1] = e4m3x2_f16x2(x[j] >> 16);
+                        y[2 * j] = e4m3_even(x[j]);
+                        y[2 * j + 1] = e4m3_odd(x[j]);
                     }
                     sts128(dst + tc::sw_chunk(r, 2 * c, BN), make_uint4(y[0], y[1], y[2], y[3]));
                     sts128(dst + tc::sw_chunk(r, 2 * c + 1, BN), make_uint4(y[4], y[5], y[6], y[7]));
@@ -312,9 +338,12 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                             const float2 f = unpack2<F16>(x[j]);
                             x[j] = pack2<true>(f.x * up, f.y * up);
                         }
-                        sts128(sb + (r >> 7) * C::QTILE + tc::sw_chunk(r & 127, c, 128), make_uint4(x[0], x[1], x[2], x[3]));
+                        // features 0, 2, 1, 3 of every four, as the keys' are widened
+                        sts128(sb + (r >> 7) * C::QTILE + tc::sw_chunk(r & 127, c, 128),
+                               make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[0], x[1], 0x7632),
+                                          __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[2], x[3], 0x7632)));
                     }
-                    reinterpret_cast<float*>(sm + C::OFF_RS)[(unit & 1) * C::R + r] = a.scale_log2 * (1.f / up);
+                    reinterpret_cast<float*>(sm + C::OFF_RS)[(unit & 1) * C::R + r] = a.scale_log2 * (kE4m3Up / up);
                 }
                 tc::fence_proxy_async();
                 warp_arrive(TB_QF);
@@ -323,37 +352,58 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             for (int t = t0; t < t1 && ok; ++t) {
                 const int pos = t * BN + mine;
                 const long long off = pos < kend ? row_of(a, p.n, p.h, pos) : -1;
+                const bool tma = box && __all_sync(kFullMask, off >= 0);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    uint32_t dst;
+                    const uint32_t stage = item % NST, ring = F8 ? item % C::NRAW : 0;
+                    uint32_t dst;  // of this warp's rows
                     if constexpr (F8) {
-                        const uint32_t ring = item % C::NRAW;
-                        dst = sb + C::OFF_RAW + ring * C::RAW + (warp & 3) * (PER * 512) + lane * 16;
+                        dst = sb + C::OFF_RAW + ring * C::RAW + (warp & 3) * (PER * 512);
                         if (kv == 0 && lane < RW) {
                             const uint32_t rsc = sb + C::OFF_RSC + ring * 1024 + mine * 4;
                             cp_async4(rsc, a.ks + (off < 0 ? 0 : off), off >= 0);
                             cp_async4(rsc + 512, a.vs + (off < 0 ? 0 : off), off >= 0);
                         }
                     } else {
-                        const uint32_t stage = item % NST;
                         if (!warp_wait(KV_EMPTY + stage, (item / NST & 1) ^ 1)) {
                             ok = false;
                             break;
                         }
-                        dst = sb + C::OFF_KV + stage * C::TILE;
+                        dst = sb + C::OFF_KV + stage * C::TILE + r0 * 128;
                     }
-                    const uint8_t* base = static_cast<const uint8_t*>(kv ? a.vc : a.kc);
-#pragma unroll 8
-                    for (int i = 0; i < PER; ++i) {
-                        const int idx = i * 32 + lane, rl = idx / CHR, c = idx % CHR;
-                        const long long ro = __shfl_sync(kFullMask, off, rl);
-                        const uint8_t* src = base + (ro < 0 ? 0 : ro * (CHR * 16)) + c * 16;
-                        cp_async16(F8 ? dst + i * 512 : dst + tc::sw_chunk(r0 + rl, c, BN), src, ro >= 0);
+                    if (tma) {
+                        constexpr int COLS = F8 ? 1 : D / 64;  // boxes side by side
+                        uint64_t* bar = &bars[F8 ? RAW_FULL + 4 * ring + (warp & 3) : KV_FULL + stage];
+                        if (lane == 0) tc::mbar_expect_tx(bar, RW * CHR * 16);
+                        __syncwarp();
+                        for (int i = lane; i < (boxes * COLS + 31) / 32 * 32; i += 32) {
+                            const int rb = i / COLS * box, x = i % COLS;
+                            const long long ro = __shfl_sync(kFullMask, off, rb % RW);
+                            if (i < boxes * COLS)
+                                tma_load_2d(F8 ? dst + rb * CHR * 16 : dst + x * (BN * 128) + rb * 128, kv ? &maps.v : &maps.k,
+                                            x * 64, static_cast<int>(ro), bar);
+                        }
+                    } else {
+                        const uint8_t* base = static_cast<const uint8_t*>(kv ? a.vc : a.kc);
+#pragma unroll 4
+                        for (int i = 0; i < PER; ++i) {
+                            const int idx = i * 32 + lane, rl = idx / CHR, c = idx % CHR;
+                            const long long ro = __shfl_sync(kFullMask, off, rl);
+                            const uint8_t* src = base + (ro < 0 ? 0 : ro * (CHR * 16)) + c * 16;
+                            cp_async16(F8 ? dst + idx * 16 : dst - r0 * 128 + tc::sw_chunk(r0 + rl, c, BN), src, ro >= 0);
+                        }
                     }
-                    push(F8 ? 0u : static_cast<uint32_t>(KV_FULL) + item % NST);
+                    if constexpr (F8) {
+                        raw_tma = (raw_tma & ~(1u << ring)) | (tma ? 1u << ring : 0u);
+                        push(0);
+                    } else if (!tma) {
+                        push(KV_FULL + stage);
+                    }
                     ++item;
                     if (!ok) break;
                 }
+                // the queries, copied meanwhile, are handed over behind two tiles' copies
+                if (!F8 && box && t == t0 + 1 && ok) flush();
             }
             // the MMAs of this unit, which free the query tiles, need all of its keys
             if (ok) flush();
@@ -367,19 +417,22 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             next_unit<BN>(a, p);
         }
         cp_async_wait<0>();
+        if (!ok) {  // gave up: leave what TMA copies are in flight (microseconds) a millisecond
+            for (int i = 0; i < 100; ++i) __nanosleep(10000);
+        }
     } else if (wg == 3) {
         // ------------------------------------------------------------ MMA issue
         // The whole warp runs the loop, and one elected lane issues: descriptors stay warp-uniform (an MMA
         // takes them from uniform registers; issued from a branch on the lane index, each one's operands are
         // moved there first, which made the issue twice as long as the products).
         regs_down<kRegsOther>();
-        if (warp == 12) {
+        if (warp == 12 && elect()) {
             constexpr uint32_t FMT = MF16 ? 0u : (1u << 7) | (1u << 10);
             constexpr uint32_t ID_S = (tc::idesc_bf16(128, BN, 0, 0, 0) & ~((1u << 7) | (1u << 10))) | FMT;
             constexpr uint32_t ID_O = (tc::idesc_bf16(128, D, 0, 1, 0) & ~((1u << 7) | (1u << 10))) | FMT;
-            const uint32_t tmu = uniform(tm);
-            const uint64_t dq = uniform(tc::sdesc(sb, 16, 1024)), dk = uniform(tc::sdesc(sb + C::OFF_KV, 16, 1024));
-            const uint64_t dv = uniform(tc::sdesc(sb + C::OFF_KV, BN * 128, 1024));
+            const uint32_t tmu = tm;
+            const uint64_t dq = (tc::sdesc(sb, 16, 1024)), dk = (tc::sdesc(sb + C::OFF_KV, 16, 1024));
+            const uint64_t dv = (tc::sdesc(sb + C::OFF_KV, BN * 128, 1024));
             uint32_t unit = 0, np[2] = {0, 0};
             uint32_t ks = 0, kp = 0, vs = 1, vp = 0;  // stage and parity of the next K tile, of the next V tile
             auto step = [](uint32_t& stage, uint32_t& parity) {
@@ -393,14 +446,14 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             for (;;) {
                 const int t0 = p.tile, t1 = static_cast<int>(min(static_cast<long long>(p.nk), t0 + (end - at)));
                 const int rows = min(a.tq, p.s.m - p.qt * a.tq) * a.G;
-                const bool full = uniform(SLOTS == 2 && rows > 128 ? 1u : 0u) != 0;
-                const int nops = static_cast<int>(uniform(static_cast<uint32_t>(full ? 2 * (t1 - t0) : t1 - t0)));
+                const bool full = (SLOTS == 2 && rows > 128 ? 1u : 0u) != 0;
+                const int nops = static_cast<int>((static_cast<uint32_t>(full ? 2 * (t1 - t0) : t1 - t0)));
                 auto issue_s = [&](int s) {
                     const int b = s & 1;
-                    if (!warp_wait(KV_FULL + ks, kp)) return false;
+                    if ((!full || !b) && !one_wait(KV_FULL + ks, kp)) return false;  // its tile's first product
                     const uint64_t qa = dq + (full && b ? C::QTILE >> 4 : 0u), ka = dk + ks * (C::TILE >> 4);
                     const bool last = !full || b;  // of this K tile's products
-                    if (elect()) {
+                    {
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
                             tc::mma_bf16(tmu + C::TM_S + b * C::TM_SB, qa + ((k >> 2) * 16384 + (k & 3) * 32) / 16,
@@ -409,21 +462,20 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                         if (last) tc::commit(&bars[KV_EMPTY + ks]);
                         if (s == nops - 1) tc::commit(&bars[TB_QE]);
                     }
-                    __syncwarp();
                     if (last) step(ks, kp);
                     return true;
                 };
-                ok = warp_wait(TB_QF, unit & 1);
+                ok = one_wait(TB_QF, unit & 1);
                 ok = ok && issue_s(0) && (nops < 2 || issue_s(1));
                 for (int s = 0; s < nops && ok; ++s) {
                     const int b = s & 1, o = SLOTS == 2 ? b : 0;
                     const bool fresh = SLOTS == 2 ? s < 2 : s == 0, last = !full || b;
-                    ok = warp_wait(KV_FULL + vs, vp) && (!fresh || warp_wait(TB_OF0 + o, (unit & 1) ^ 1)) &&
-                         warp_wait(TB_P0 + b, np[b] & 1);
+                    ok = ((full && b) || one_wait(KV_FULL + vs, vp)) && (!fresh || one_wait(TB_OF0 + o, (unit & 1) ^ 1)) &&
+                         one_wait(TB_P0 + b, np[b] & 1);
                     if (!ok) break;
                     ++np[b];
                     const uint64_t va = dv + vs * (C::TILE >> 4);
-                    if (elect()) {
+                    {
 #pragma unroll
                         for (int k = 0; k < BN / 16; ++k)
                             tc::mma_bf16_ts(tmu + C::TM_O + o * D, tmu + C::TM_S + b * C::TM_SB + 8 * k, va + k * (2048 / 16), ID_O,
@@ -431,7 +483,6 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                         tc::commit(&bars[TB_OD0 + o]);
                         if (last) tc::commit(&bars[KV_EMPTY + vs]);
                     }
-                    __syncwarp();
                     if (last) step(vs, vp);
                     if (s + 2 < nops) ok = issue_s(s + 2);
                 }
@@ -442,11 +493,10 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                 next_unit<BN>(a, p);
             }
             // nothing of this CTA's may be in flight when it ends, its barriers' arrivals included
-            if (elect()) {
+            {
                 tc::commit(&bars[TB_DRAIN]);
                 tc::mbar_wait(&bars[TB_DRAIN], 0, kTilesWait);
             }
-            __syncwarp();
         }
     } else if (wg < SLOTS) {
         // ------------------------------------------------------------ softmax: one row per thread
@@ -619,6 +669,16 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                             tc::wait_ld();
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] = fmaf(f1, u[i], f0 * v[i]);
+                        }
+                        if constexpr (F8) {  // columns hold features 0, 2, 1, 3 of every four, times 2^-8
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                const float x = v[i + 1] * kE4m3Up;
+                                v[i] *= kE4m3Up;
+                                v[i + 1] = v[i + 2] * kE4m3Up;
+                                v[i + 2] = x;
+                                v[i + 3] *= kE4m3Up;
+                            }
                         }
                         if (live && whole) {
                             uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D + ch * 32);

@@ -203,6 +203,12 @@ struct AttnArgs {
     float scale_log2;    // scale * log2(e)
     uint32_t page_mul;   // division by page_size
     int page_shift;
+    int box;             // rows per TMA box, a divisor of page_size; 0: no TMA
+};
+
+// The caches as rows of D elements.
+struct AttnMaps {
+    CUtensorMap k, v;
 };
 
 // Cache rows moved by the write and read kernels.
