@@ -65,6 +65,17 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The two e4m3 values in the low (high) half of a word as two binary16 (exact).
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t x) {
+    uint32_t r;
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t x) {
+    uint32_t r;
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(r) : "r"(x));
+    return r;
+}
 // Four e4m3 values of a word as binary16, times 2^-8: bytes 0 and 2, bytes 1 and 3 (the lower byte in the
 // low half).  Sign, exponent and significand move to binary16's places; the exponents' biases, 7 and 15,
 // leave the factor, which the callers' scales take up.  Exact, subnormal values included (NaN comes out

@@ -38,27 +38,33 @@ struct TilesCfg {
     static constexpr int SLOTS = D == 256 ? 1 : 2;         // row tiles per unit
     static constexpr int R = 128 * SLOTS;                  // rows per unit
     static constexpr int HALVES = D / 64;                  // 64-feature halves of an operand tile
+    static constexpr bool QTM = D == 256;                  // queries in TMEM, not in shared memory
+    static constexpr bool DUAL = F8 && D == 256;           // warpgroup 1, idle else, loads the values
     static constexpr uint32_t QTILE = 128u * D * 2, TILE = static_cast<uint32_t>(BN) * D * 2;
     static constexpr uint32_t RAW = F8 ? TILE / 2 : 0;
-    // K and V tiles in shared memory.  8 bits: with 3, a K tile's place is its second predecessor's V tile's,
-    // so two slots for the keys' scales are enough.
-    static constexpr int NST = F8 ? 3 : (D == 64 ? 8 : 5);
+    // K and V tiles in shared memory.  8 bits, one loader: 3, so a K tile takes the place of its second
+    // predecessor's V tile, and two slots for the keys' scales are enough.  Two loaders: 4, so that each has
+    // places of its own; a K tile takes its second predecessor's, whose product follows the softmax of the
+    // tile two before that: four slots.
+    static constexpr int NST = F8 ? (DUAL ? 4 : 3) : (D == 64 ? 8 : (D == 128 ? 5 : 6));
+    static constexpr uint32_t SCN = DUAL ? 4 : 2;
     // copy groups in flight behind the newest.  16 bits: at most NST - 2, as S(s + 2) needs its K tile before
     // the V tile before it is released.
-    static constexpr int LAG = F8 ? (D == 64 ? 5 : 2) : 3;
-    static constexpr int NRAW = F8 ? LAG + 1 : 0;
+    static constexpr int LAG = F8 ? (D == 64 ? 5 : (DUAL ? 1 : 2)) : 3;
+    static constexpr int NRAW = F8 ? LAG + 1 : 0;          // staging slots of a loader
+    static constexpr int RINGS = F8 ? (DUAL ? 2 : 1) * NRAW : 0;
     static constexpr int BOX = BN / 4;                     // most rows of one TMA box: a loader warp's rows
-    static constexpr uint32_t OFF_KV = SLOTS * QTILE;
+    static constexpr uint32_t OFF_KV = QTM ? 0 : SLOTS * QTILE;
     static constexpr uint32_t OFF_RAW = OFF_KV + NST * TILE;
-    static constexpr uint32_t OFF_RSC = OFF_RAW + NRAW * RAW;            // raw scales of a stage: K, V
-    static constexpr uint32_t OFF_SC = OFF_RSC + NRAW * (F8 ? 1024 : 0);  // ks, log2 vs, 1 / vs of two tiles
-    static constexpr uint32_t OFF_RS = OFF_SC + (F8 ? 2 * 3 * 128 * 4 : 0);  // row scales of two units
-    static constexpr uint32_t USED = OFF_RS + (F8 ? 2 * R * 4 : 0);
+    static constexpr uint32_t OFF_RSC = OFF_RAW + RINGS * RAW;            // raw scales of a stage: K, V
+    static constexpr uint32_t OFF_SC = OFF_RSC + NRAW * (F8 ? 1024 : 0);  // ks, log2 vs, 1 / vs of SCN tiles
+    static constexpr uint32_t OFF_RS = OFF_SC + (F8 ? SCN * 3 * BN * 4 : 0);  // row scales of two units
+    static constexpr uint32_t USED = OFF_RS + (F8 && !QTM ? 2 * R * 4 : 0);
     static constexpr uint32_t SMEM = USED + 1024;          // 1024-byte alignment
-    static constexpr uint32_t TM_S = 0, TM_O = 256, TM_SB = BN;  // TMEM columns
+    static constexpr uint32_t TM_S = 0, TM_Q = 128, TM_O = 256, TM_SB = BN;  // TMEM columns
 };
 
-enum : int { TB_QF = 0, TB_QE, TB_S0, TB_S1, TB_P0, TB_P1, TB_OD0, TB_OD1, TB_OF0, TB_OF1, TB_MF, TB_ME, TB_SC0, TB_SC1, TB_DRAIN, TB_KV };  // then KV_FULL, KV_EMPTY and (8 bits) RAW_FULL of every loader warp
+enum : int { TB_QF = 0, TB_QE, TB_S0, TB_S1, TB_P0, TB_P1, TB_OD0, TB_OD1, TB_OF0, TB_OF1, TB_MF, TB_ME, TB_SC0, TB_SC3 = TB_SC0 + 3, TB_DRAIN, TB_KV };  // then KV_FULL, KV_EMPTY and (8 bits) RAW_FULL of every loader warp
 
 __device__ __forceinline__ void tm_ld32(uint32_t taddr, float* v) {
     uint32_t r[32];
@@ -156,7 +162,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
     constexpr int BN = C::BN, NST = C::NST, LAG = C::LAG, SLOTS = C::SLOTS;
     extern __shared__ uint8_t smem_raw[];
     __shared__ PlanSmem plan;
-    constexpr int NBAR = TB_KV + 2 * NST + 4 * C::NRAW;
+    constexpr int NBAR = TB_KV + 2 * NST + 4 * C::RINGS;
     __shared__ uint64_t bars[NBAR];
     __shared__ float ml_s[128][2];
     __shared__ uint32_t tmem_slot;
@@ -181,7 +187,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
     if (tid == 0) {
         for (int i = 0; i < NBAR; ++i) {
             const bool by_warps = i == TB_QF || i == TB_P0 || i == TB_P1 || i == TB_OF0 || i == TB_OF1 || i == TB_MF ||
-                                  i == TB_ME || i == TB_SC0 || i == TB_SC1 || (i >= TB_KV && i < TB_KV + NST);
+                                  i == TB_ME || (i >= TB_SC0 && i <= TB_SC3) || (i >= TB_KV && i < TB_KV + NST);
             tc::mbar_init(&bars[i], by_warps ? 4 : 1);
         }
         abort_flag = 0;
@@ -213,7 +219,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
         if (lane == 0) tc::mbar_arrive(&bars[i]);
     };
 
-    if (wg == 2) {
+    if (wg == 2 || (C::DUAL && wg == 1)) {
         regs_down<kRegsOther>();
         // ------------------------------------------------------------ loader
         // warp w moves rows w RW .. w RW + RW - 1 of every tile; lane l holds the cache offset of one of them
@@ -224,16 +230,19 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
         // rows that lie within the keys come by TMA, in boxes of a.box rows that never straddle a page; a
         // warp with a row past the keys (or a page size without a factor of 8) uses cp.async and zero-fills
         const int box = a.box, boxes = box ? RW / box : 0;
-        uint32_t open = 0, item = 0, made = 0, pend = 0, unit = 0;
+        // tiles are numbered K 0, V 1, K 2, ..; a loader has all of them, or (DUAL) the even or the odd ones
+        const uint32_t lg = C::DUAL && wg == 1 ? 1 : 0;
+        constexpr uint32_t STEP = C::DUAL ? 2 : 1;
+        uint32_t open = 0, item = lg, made = lg, pend = 0, unit = 0;
         uint32_t raw_tma = 0, raw_phase = 0;  // 8 bits: ring slots filled by TMA, and their barriers' parities
         bool ok = true;
-        if (tl == 0) leave_no_join(a);  // stands if this CTA gives up
+        if (tid == 256) leave_no_join(a);  // stands if this CTA gives up
         // the oldest group has landed: (8 bits: widen it and) hand it over
         auto finish = [&](uint32_t what) {
             if constexpr (F8) {
-                const uint32_t stage = made % NST, ring = made % C::NRAW;
+                const uint32_t stage = made % NST, ring = made / STEP % C::NRAW;
                 if (raw_tma >> ring & 1) {
-                    if (!warp_wait(RAW_FULL + 4 * ring + (warp & 3), raw_phase >> ring & 1)) {
+                    if (!warp_wait(RAW_FULL + 4 * (lg * C::NRAW + ring) + (warp & 3), raw_phase >> ring & 1)) {
                         ok = false;
                         return;
                     }
@@ -246,16 +255,16 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                 if (!(made & 1)) {  // a K tile: its keys' scales, for the softmax
                     if (lane < RW) {
                         const uint32_t rsc = sb + C::OFF_RSC + ring * 1024 + mine * 4;
-                        float* sc = reinterpret_cast<float*>(sm + C::OFF_SC) + (made >> 1 & 1) * 384 + mine;
+                        float* sc = reinterpret_cast<float*>(sm + C::OFF_SC) + made / 2 % C::SCN * (3 * BN) + mine;
                         const float ks = lds32(rsc), vs = lds32(rsc + 512);
                         const bool none = vs == 0.f;  // past the keys: zero-filled
                         sc[0] = ks;
-                        sc[128] = none ? 0.f : log2f(vs);
-                        sc[256] = none ? 0.f : 1.f / vs;
+                        sc[BN] = none ? 0.f : log2f(vs);
+                        sc[2 * BN] = none ? 0.f : 1.f / vs;
                     }
-                    warp_arrive(TB_SC0 + (made >> 1 & 1));
+                    warp_arrive(TB_SC0 + made / 2 % C::SCN);
                 }
-                const uint32_t raw = sb + C::OFF_RAW + ring * C::RAW + (warp & 3) * (PER * 512) + lane * 16;
+                const uint32_t raw = sb + C::OFF_RAW + (lg * C::NRAW + ring) * C::RAW + (warp & 3) * (PER * 512) + lane * 16;
                 const uint32_t dst = sb + C::OFF_KV + stage * C::TILE;
 #pragma unroll 4
                 for (int i = 0; i < PER; ++i) {
@@ -265,15 +274,19 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                     uint32_t y[8];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        y[2 * j] = e4m3_even(x[j]);
-                        y[2 * j + 1] = e4m3_odd(x[j]);
+                        y[2 * j] = e4m3_lo(x[j]);
+                        y[2 * j + 1] = e4m3_hi(x[j]);
                     }
-                    sts128(dst + tc::sw_chunk(r, 2 * c, BN), make_uint4(y[0], y[1], y[2], y[3]));
-                    sts128(dst + tc::sw_chunk(r, 2 * c + 1, BN), make_uint4(y[4], y[5], y[6], y[7]));
+                    // chunks 2 c and 2 c + 1 of the row; lanes of odd 64-feature halves store theirs in the other
+                    // order, so that eight lanes' stores fall on different banks
+                    const bool odd = CHR > 4 && (c & 4);
+                    const uint4 y0 = make_uint4(y[0], y[1], y[2], y[3]), y1 = make_uint4(y[4], y[5], y[6], y[7]);
+                    sts128(dst + tc::sw_chunk(r, 2 * c + (odd ? 1 : 0), BN), odd ? y1 : y0);
+                    sts128(dst + tc::sw_chunk(r, 2 * c + (odd ? 0 : 1), BN), odd ? y0 : y1);
                 }
                 tc::fence_proxy_async();
                 warp_arrive(KV_FULL + stage);
-                ++made;
+                made += STEP;
             } else {
                 tc::fence_proxy_async();
                 warp_arrive(what);
@@ -297,11 +310,15 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             const int t0 = p.tile, t1 = static_cast<int>(min(static_cast<long long>(p.nk), t0 + (end - at)));
             const int i0 = p.qt * a.tq, ntok = min(a.tq, p.s.m - i0), rows = ntok * a.G;
             const int kend = min(t1 * BN, p.s.L - p.s.m + i0 + ntok);
-            const int qrows = rows > 128 ? 256 : 128;
             // ---- queries
-            ok = warp_wait(TB_QE, (unit & 1) ^ 1);
-            if (!ok) break;
-            if constexpr (!F8) {
+            const int qrows = C::QTM ? 0 : (rows > 128 ? 256 : 128);
+            if (!C::QTM) {
+                ok = warp_wait(TB_QE, (unit & 1) ^ 1);
+                if (!ok) break;
+            }
+            if constexpr (C::QTM) {
+                (void)qrows;
+            } else if constexpr (!F8) {
                 for (int idx = tl; idx < qrows * (D / 8); idx += 128) {
                     const int r = idx / (D / 8), c = idx % (D / 8);
                     const bool on = r < rows;
@@ -338,12 +355,9 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                             const float2 f = unpack2<F16>(x[j]);
                             x[j] = pack2<true>(f.x * up, f.y * up);
                         }
-                        // features 0, 2, 1, 3 of every four, as the keys' are widened
-                        sts128(sb + (r >> 7) * C::QTILE + tc::sw_chunk(r & 127, c, 128),
-                               make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[0], x[1], 0x7632),
-                                          __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[2], x[3], 0x7632)));
+                        sts128(sb + (r >> 7) * C::QTILE + tc::sw_chunk(r & 127, c, 128), make_uint4(x[0], x[1], x[2], x[3]));
                     }
-                    reinterpret_cast<float*>(sm + C::OFF_RS)[(unit & 1) * C::R + r] = a.scale_log2 * (kE4m3Up / up);
+                    reinterpret_cast<float*>(sm + C::OFF_RS)[(unit & 1) * C::R + r] = a.scale_log2 * (1.f / up);
                 }
                 tc::fence_proxy_async();
                 warp_arrive(TB_QF);
@@ -355,10 +369,11 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                 const bool tma = box && __all_sync(kFullMask, off >= 0);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    const uint32_t stage = item % NST, ring = F8 ? item % C::NRAW : 0;
+                    if (C::DUAL && kv != static_cast<int>(lg)) continue;
+                    const uint32_t stage = item % NST, ring = F8 ? item / STEP % C::NRAW : 0;
                     uint32_t dst;  // of this warp's rows
                     if constexpr (F8) {
-                        dst = sb + C::OFF_RAW + ring * C::RAW + (warp & 3) * (PER * 512);
+                        dst = sb + C::OFF_RAW + (lg * C::NRAW + ring) * C::RAW + (warp & 3) * (PER * 512);
                         if (kv == 0 && lane < RW) {
                             const uint32_t rsc = sb + C::OFF_RSC + ring * 1024 + mine * 4;
                             cp_async4(rsc, a.ks + (off < 0 ? 0 : off), off >= 0);
@@ -373,7 +388,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                     }
                     if (tma) {
                         constexpr int COLS = F8 ? 1 : D / 64;  // boxes side by side
-                        uint64_t* bar = &bars[F8 ? RAW_FULL + 4 * ring + (warp & 3) : KV_FULL + stage];
+                        uint64_t* bar = &bars[F8 ? RAW_FULL + 4 * (lg * C::NRAW + ring) + (warp & 3) : KV_FULL + stage];
                         if (lane == 0) tc::mbar_expect_tx(bar, RW * CHR * 16);
                         __syncwarp();
                         for (int i = lane; i < (boxes * COLS + 31) / 32 * 32; i += 32) {
@@ -399,11 +414,11 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                     } else if (!tma) {
                         push(KV_FULL + stage);
                     }
-                    ++item;
+                    item += STEP;
                     if (!ok) break;
                 }
                 // the queries, copied meanwhile, are handed over behind two tiles' copies
-                if (!F8 && box && t == t0 + 1 && ok) flush();
+                if (!F8 && !C::QTM && box && t == t0 + 1 && ok) flush();
             }
             // the MMAs of this unit, which free the query tiles, need all of its keys
             if (ok) flush();
@@ -411,7 +426,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             at += t1 - t0;
             ++unit;
             if (at >= end) {
-                if (tl == 0) leave_join(a, p, t0, t1, per);
+                if (tid == 256) leave_join(a, p, t0, t1, per);
                 break;
             }
             next_unit<BN>(a, p);
@@ -456,11 +471,12 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                     {
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
-                            tc::mma_bf16(tmu + C::TM_S + b * C::TM_SB, qa + ((k >> 2) * 16384 + (k & 3) * 32) / 16,
+                            if constexpr (C::QTM) tc::mma_bf16_ts(tmu + C::TM_S + b * C::TM_SB, tmu + C::TM_Q + 8 * k, ka + ((k >> 2) * (BN * 128) + (k & 3) * 32) / 16, ID_S, k > 0);
+                            else tc::mma_bf16(tmu + C::TM_S + b * C::TM_SB, qa + ((k >> 2) * 16384 + (k & 3) * 32) / 16,
                                          ka + ((k >> 2) * (BN * 128) + (k & 3) * 32) / 16, ID_S, k > 0);
                         tc::commit(&bars[TB_S0 + b]);
                         if (last) tc::commit(&bars[KV_EMPTY + ks]);
-                        if (s == nops - 1) tc::commit(&bars[TB_QE]);
+                        if (!C::QTM && s == nops - 1) tc::commit(&bars[TB_QE]);
                     }
                     if (last) step(ks, kp);
                     return true;
@@ -514,7 +530,53 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             const bool live = r < rows, some = __any_sync(kFullMask, live);
             const int vis = live ? p.s.L - p.s.m + i0 + r / a.G + 1 : 0;  // keys that this row sees
             float c = a.scale_log2;
-            if constexpr (F8) {
+            if constexpr (C::QTM) {
+                // this row's query into TMEM (the last unit's products with it are done: S of all of them was read)
+                if (some) {
+                    const uint4* src = reinterpret_cast<const uint4*>(a.q + (p.s.q0 + i0 + (live ? r / a.G : 0)) * a.q_stride +
+                                                                      static_cast<long long>(p.h * a.G + (live ? r % a.G : 0)) * D);
+                    float up = 1.f;
+                    if constexpr (F8) {
+                        float mx = 0.f;
+#pragma unroll 8
+                        for (int i = 0; i < D / 8; ++i) {
+                            const uint4 q4 = live ? src[i] : make_uint4(0, 0, 0, 0);
+                            const uint32_t x[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float2 f = unpack2<F16>(x[j]);
+                                mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+                            }
+                        }
+                        up = row_up(mx);
+                        c *= 1.f / up;
+                    }
+#pragma unroll 2
+                    for (int i = 0; i < D / 32; ++i) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint4 q4 = live ? src[4 * i + k] : make_uint4(0, 0, 0, 0);
+                            w[4 * k] = q4.x;
+                            w[4 * k + 1] = q4.y;
+                            w[4 * k + 2] = q4.z;
+                            w[4 * k + 3] = q4.w;
+                        }
+                        if constexpr (F8) {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const float2 f = unpack2<F16>(w[k]);
+                                w[k] = pack2<true>(f.x * up, f.y * up);
+                            }
+                        }
+                        __syncwarp();
+                        tm_st16(trow + C::TM_Q + i * 16, w);
+                    }
+                    tc::wait_st();
+                }
+                tc::fence_before();
+                warp_arrive(TB_QF);
+            } else if constexpr (F8) {
                 if (!warp_wait(TB_QF, unit & 1)) break;
                 c = reinterpret_cast<const float*>(sm + C::OFF_RS)[(unit & 1) * C::R + r];
             }
@@ -527,9 +589,9 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                 const float* sc = nullptr;
                 if constexpr (F8) {
                     const uint32_t ti = tiles + tile;
-                    ok = warp_wait(TB_SC0 + (ti & 1), ti >> 1 & 1);
+                    ok = warp_wait(TB_SC0 + ti % C::SCN, ti / C::SCN & 1);
                     if (!ok) break;
-                    sc = reinterpret_cast<const float*>(sm + C::OFF_SC) + (ti & 1) * 384;
+                    sc = reinterpret_cast<const float*>(sm + C::OFF_SC) + ti % C::SCN * (3 * BN);
                 }
                 ok = warp_wait(TB_S0 + b, ns[b] & 1);
                 if (!ok) break;
@@ -548,7 +610,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
 #pragma unroll
                         for (int i = 0; i < BN; i += 4) {
                             const float4 ks = *reinterpret_cast<const float4*>(sc + i);
-                            const float4 lv = *reinterpret_cast<const float4*>(sc + 128 + i);
+                            const float4 lv = *reinterpret_cast<const float4*>(sc + BN + i);
                             pair_fma(y + i, y + i, c, ks.x, ks.y, lv.x, lv.y);
                             pair_fma(y + i + 2, y + i + 2, c, ks.z, ks.w, lv.z, lv.w);
                         }
@@ -602,7 +664,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                             pair_exp2(x, times, -use);
                             pair_exp2(x + 2, times, -use);
                             if constexpr (F8) {
-                                const float4 iv = *reinterpret_cast<const float4*>(sc + 256 + ch * 32 + i);
+                                const float4 iv = *reinterpret_cast<const float4*>(sc + 2 * BN + ch * 32 + i);
                                 pair_mac(l2, x, iv.x, iv.y);
                                 pair_mac(l2 + 2, x + 2, iv.z, iv.w);
                             } else {
@@ -669,16 +731,6 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                             tc::wait_ld();
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] = fmaf(f1, u[i], f0 * v[i]);
-                        }
-                        if constexpr (F8) {  // columns hold features 0, 2, 1, 3 of every four, times 2^-8
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const float x = v[i + 1] * kE4m3Up;
-                                v[i] *= kE4m3Up;
-                                v[i + 1] = v[i + 2] * kE4m3Up;
-                                v[i + 2] = x;
-                                v[i + 3] *= kE4m3Up;
-                            }
                         }
                         if (live && whole) {
                             uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D + ch * 32);
