@@ -79,7 +79,8 @@ bool encode_cache(CUtensorMap* map, const void* base, long long rows, int D, int
 // The joining kernel starts while the main kernel still runs (programmatic dependent launch) and waits
 // for it before it reads the partials.
 template <int D>
-cudaError_t launch_combine(const AttnArgs& a, int R, int RB, int grid, cudaStream_t stream) {
+cudaError_t launch_combine(const AttnArgs& a, int R, int grid, cudaStream_t stream) {
+    const int RB = std::min(R, attn::kCombineThreads / (D / 4));  // a row per group of threads
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, (R + RB - 1) / RB);
     cfg.blockDim = dim3(attn::kCombineThreads);
@@ -101,12 +102,13 @@ cudaError_t launch_rows(AttnArgs a, cudaStream_t stream) {
     if (e == cudaSuccess) e = raise_smem(attn::attn_rows_kernel<D, F16, F8>, C::SMEM, done);
     if (e != cudaSuccess) return e;
     a.tq = std::max(1, attn::kRowsTile / a.G);
-    a.min_tiles = 2;
+    a.ov = 1;
+    a.min_per = 3;
     const int grid = std::min(sms * C::OCC, kMaxCtas);
     attn::attn_rows_kernel<D, F16, F8><<<grid, attn::kRowsNT, C::SMEM, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_combine<D>(a, attn::kRowsTile, attn::kRowsTile, grid, stream);
+    return launch_combine<D>(a, attn::kRowsTile, grid, stream);
 }
 
 template <int D, bool F16, bool F8>
@@ -127,7 +129,8 @@ cudaError_t launch_tiles(AttnArgs a, cudaStream_t stream) {
     }
     if (regs.load(std::memory_order_relaxed) < attn::kRegsLaunch) return cudaErrorInvalidConfiguration;
     a.tq = C::R / a.G;
-    a.min_tiles = 1;
+    a.ov = 4;
+    a.min_per = 6;
     // Boxes of at least 8 rows (the swizzle's period) that divide a page; coordinates are 32-bit
     AttnMaps maps;
     std::memset(&maps, 0, sizeof(maps));
@@ -140,7 +143,7 @@ cudaError_t launch_tiles(AttnArgs a, cudaStream_t stream) {
     attn::attn_tiles_kernel<D, F16, F8><<<grid, attn::kTilesNT, C::SMEM, stream>>>(a, maps);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_combine<D>(a, C::R, 32, grid, stream);
+    return launch_combine<D>(a, C::R, grid, stream);
 }
 
 template <int D, bool F16, bool F8>

@@ -12,13 +12,15 @@
 //
 // Division of the work.  The G heads that share a key head are rows of one tile: row r of a query tile
 // is token i0 + r / G and head h G + r % G, so a key row is read once for all of them.  A unit is
-// (sequence, key head, query tile); it costs as many key tiles as its last token sees.  All units'
-// key tiles form one list (sequences, then heads, then query tiles, then key tiles), and CTA c takes
-// entries [c per, (c+1) per): every CTA has the same work whatever the lengths are, one long sequence
-// included.  A unit that spans CTAs leaves one partial (acc, ref, l) per CTA in the workspace (at most
-// two per CTA: of the unit that its range begins inside, and of the one that it ends inside), and
-// attn_combine_kernel joins them in the order of the keys, so results do not depend on timing.
-// The lengths are on the device; every CTA finds its range from them itself.
+// (sequence, key head, query tile); it takes as many key tiles as its last token sees.  Its cost, counted
+// in products of 128 (16) rows with a key tile, is wt per key tile (2 where it has two row tiles) plus ov for
+// starting and ending it.  All units' costs form one line (sequences, then heads, then query tiles), and
+// CTA c takes the stretch [c per, (c+1) per): every CTA has the same work whatever the lengths are, one
+// long sequence included.  A stretch's end inside a unit cuts it between two key tiles.  A unit that spans
+// CTAs leaves one partial (acc, ref, l) per CTA in the workspace (at most two per CTA: of the unit that its
+// stretch begins inside, and of the one that it ends inside), and attn_combine_kernel joins them in the
+// order of the keys, so results do not depend on timing.  The lengths are on the device; every CTA finds
+// its stretch from them itself.
 #pragma once
 
 #include "attn_mma.cuh"
@@ -47,31 +49,62 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int n, bool* bad) {
     return s;
 }
 
+// How a kernel tiles: BN keys, SL row tiles of ROWS rows per unit.
+template <int BN_, int SL_, int ROWS_>
+struct Tiling {
+    static constexpr int BN = BN_, SL = SL_, ROWS = ROWS_;
+};
+
+// sum_{i < n} floor((a i + b) / m), all not negative: the steps of Euclid's algorithm (lattice points
+// under a line).
+__device__ __forceinline__ long long floor_sum(long long n, unsigned m, unsigned a, unsigned b) {
+    long long sum = 0;
+    while (n > 0) {
+        sum += (n - 1) * n / 2 * (a / m) + n * (b / m);
+        a %= m;
+        b %= m;
+        const unsigned long long top = static_cast<unsigned long long>(a) * n + b;
+        n = static_cast<long long>(top / m);
+        b = static_cast<unsigned>(top % m);
+        const unsigned x = m;
+        m = a;
+        a = x;
+    }
+    return sum;
+}
+
 // Key tiles of query tile qt: what its last token sees, at least one (a tile that sees nothing still
 // has to write its zeros).
-template <int BN>
+template <class T>
 __device__ __forceinline__ int unit_tiles(const AttnArgs& a, const Seq& s, int qt) {
     const int last = min((qt + 1) * a.tq, s.m);
-    return max(1, (s.L - s.m + last + BN - 1) / BN);
+    return max(1, (s.L - s.m + last + T::BN - 1) / T::BN);
 }
-template <int BN>
-__device__ __forceinline__ long long seq_tiles(const AttnArgs& a, const Seq& s) {
-    long long w = 0;
-    const int nq = (s.m + a.tq - 1) / a.tq;
-    for (int qt = 0; qt < nq; ++qt) w += unit_tiles<BN>(a, s, qt);
-    return w;
+// Cost per key tile of query tile qt.
+template <class T>
+__device__ __forceinline__ int unit_wt(const AttnArgs& a, const Seq& s, int qt) {
+    return T::SL == 2 && min(a.tq, s.m - qt * a.tq) * a.G > T::ROWS ? 2 : 1;
+}
+// Cost of query tiles 0 .. k - 1, none of them the sequence's last.
+template <class T>
+__device__ __forceinline__ long long cost_before(const AttnArgs& a, const Seq& s, int k) {
+    if (k == 0) return 0;
+    // tile i's last token sees base + (i + 1) tq keys; the first `ones` of them at most one tile
+    const int base = s.L - s.m;
+    const int ones = min(k, max(0, T::BN - base) / a.tq);
+    const long long tiles = ones + floor_sum(k - ones, T::BN, a.tq, base + (ones + 1) * a.tq + T::BN - 1);
+    return tiles * unit_wt<T>(a, s, 0) + static_cast<long long>(k) * a.ov;
+}
+template <class T>
+__device__ __forceinline__ long long seq_cost(const AttnArgs& a, const Seq& s) {
+    if (s.m == 0) return 0;
+    const int last = (s.m - 1) / a.tq;
+    return cost_before<T>(a, s, last) + unit_tiles<T>(a, s, last) * unit_wt<T>(a, s, last) + a.ov;
 }
 
 __device__ __forceinline__ long long shfl_up_ll(long long v, int d) {
     return static_cast<long long>(__shfl_up_sync(kFullMask, static_cast<unsigned long long>(v), d));
 }
-
-// Position of an entry of the work list.
-struct Place {
-    int n, h, qt, tile;
-    Seq s;
-    int nk;  // key tiles of the unit
-};
 
 struct PlanSmem {
     long long warp[32];
@@ -79,105 +112,128 @@ struct PlanSmem {
     int n;
 };
 
-// Total weight of the list: the sum over sequences, times Hkv.  `w0` receives the weight of sequence
-// threadIdx.x (the first chunk of locate()).  status bits are set by the CTA with report = true.
-template <int BN, int NT>
-__device__ __forceinline__ long long plan_total(const AttnArgs& a, PlanSmem& sm, long long& w0, bool report) {
-    const int tid = threadIdx.x;
-    long long sum = 0;
-    w0 = 0;
+// A CTA's walk along its stretch: the unit it is in, and the unit's key tiles t0 .. t1 - 1 that are its.
+struct Walk {
+    int n, h, qt;
+    Seq s;
+    int nk, wt;            // the unit's key tiles and their cost
+    int t0, t1;
+    long long begin, end;  // the unit's begin; the stretch's end
+};
+
+__device__ __forceinline__ int cut(const AttnArgs& a, const Walk& w, long long at) {  // key tiles before `at`
+    const long long x = at - w.begin - a.ov;
+    return x <= 0 ? 0 : static_cast<int>(min(static_cast<long long>(w.nk), (x + w.wt - 1) / w.wt));
+}
+template <class T>
+__device__ __forceinline__ void enter(const AttnArgs& a, Walk& w, long long from) {
+    w.nk = unit_tiles<T>(a, w.s, w.qt);
+    w.wt = unit_wt<T>(a, w.s, w.qt);
+    w.t0 = cut(a, w, from);
+    w.t1 = cut(a, w, w.end);
+}
+// On to the next unit that has tiles for this CTA; false at the stretch's end.
+template <class T>
+__device__ __forceinline__ bool advance(const AttnArgs& a, Walk& w) {
+    do {
+        const long long past = w.begin + static_cast<long long>(w.nk) * w.wt + a.ov;
+        if (w.end <= past) return false;
+        w.begin = past;
+        if ((w.qt + 1) * a.tq < w.s.m) {
+            ++w.qt;
+        } else {
+            w.qt = 0;
+            if (++w.h == a.Hkv) {
+                w.h = 0;
+                bool bad;
+                do w.s = load_seq(a, ++w.n, &bad);
+                while (w.s.m == 0);
+            }
+        }
+        enter<T>(a, w, w.begin);
+    } while (w.t0 >= w.t1);
+    return true;
+}
+
+// This CTA's stretch and its first unit; false where it has no work.  All threads of the block call it.
+// status bits are set by CTA 0.
+template <class T, int NT>
+__device__ __forceinline__ bool plan(const AttnArgs& a, PlanSmem& sm, Walk& w, long long& per) {
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    long long sum = 0, first = 0;  // costs of this thread's sequences; of the first one
     for (int n = tid; n < a.num_seqs; n += NT) {
         bool bad;
         const Seq s = load_seq(a, n, &bad);
-        if (bad && report) atomicOr(a.status, kStatusBadSeqlens);
-        const long long w = seq_tiles<BN>(a, s) * a.Hkv;
-        if (n == tid) w0 = w;
-        sum += w;
+        if (bad && blockIdx.x == 0) atomicOr(a.status, kStatusBadSeqlens);
+        const long long c = seq_cost<T>(a, s) * a.Hkv;
+        if (n == tid) first = c;
+        sum += c;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         sum += static_cast<long long>(__shfl_xor_sync(kFullMask, static_cast<unsigned long long>(sum), o));
-    if ((tid & 31) == 0) sm.warp[tid >> 5] = sum;
+    if (lane == 0) sm.warp[wid] = sum;
     __syncthreads();
     long long total = 0;
 #pragma unroll
     for (int i = 0; i < NT / 32; ++i) total += sm.warp[i];
-    __syncthreads();
-    return total;
-}
-
-// The place of entry `at` (0 <= at < total).  All threads of the block call it.
-template <int BN, int NT>
-__device__ __forceinline__ Place locate(const AttnArgs& a, PlanSmem& sm, long long w0, long long at) {
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    per = max((total + gridDim.x - 1) / static_cast<long long>(gridDim.x), static_cast<long long>(a.min_per));
+    const long long at = blockIdx.x * per;
+    if (at >= total) return false;
+    // the sequence that `at` falls in
     long long base = 0;
     for (int n0 = 0; n0 < a.num_seqs; n0 += NT) {
-        long long w = 0;
-        if (n0 == 0) {
-            w = w0;
-        } else if (n0 + tid < a.num_seqs) {
-            bool bad;
-            const Seq s = load_seq(a, n0 + tid, &bad);
-            w = seq_tiles<BN>(a, s) * a.Hkv;
+        long long c = first;
+        if (n0 > 0) {
+            c = 0;
+            if (n0 + tid < a.num_seqs) {
+                bool bad;
+                const Seq s = load_seq(a, n0 + tid, &bad);
+                c = seq_cost<T>(a, s) * a.Hkv;
+            }
         }
-        long long inc = w;
+        long long inc = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long u = shfl_up_ll(inc, o);
             if (lane >= o) inc += u;
         }
+        __syncthreads();  // sm.warp has been read
         if (lane == 31) sm.warp[wid] = inc;
         __syncthreads();
-        long long before = base, total = base;
+        long long before = base, all = base;
 #pragma unroll
         for (int i = 0; i < NT / 32; ++i) {
             const long long x = sm.warp[i];
             if (i < wid) before += x;
-            total += x;
+            all += x;
         }
-        const long long lo = before + inc - w;
-        if (at >= lo && at < lo + w) {
+        const long long lo = before + inc - c;
+        if (at >= lo && at < lo + c) {
             sm.n = n0 + tid;
             sm.rem = at - lo;
         }
-        __syncthreads();
-        if (at < total) break;
-        base = total;
+        if (at < all) break;
+        base = all;
     }
-    Place p;
-    p.n = sm.n;
+    __syncthreads();
+    w.n = sm.n;
+    w.end = min(at + per, total);
     bool bad;
-    p.s = load_seq(a, p.n, &bad);
-    const long long per_head = seq_tiles<BN>(a, p.s);
-    const long long rem = sm.rem;
-    p.h = static_cast<int>(rem / per_head);
-    long long r = rem - p.h * per_head;
-    p.qt = 0;
-    p.nk = unit_tiles<BN>(a, p.s, 0);
-    while (r >= p.nk) {
-        r -= p.nk;
-        p.nk = unit_tiles<BN>(a, p.s, ++p.qt);
+    w.s = load_seq(a, w.n, &bad);
+    const long long rem = sm.rem, head = seq_cost<T>(a, w.s);
+    w.h = static_cast<int>(rem / head);
+    const long long r = rem - w.h * head;
+    int lo = 0, hi = (w.s.m - 1) / a.tq;  // the last query tile that begins at or before r
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (cost_before<T>(a, w.s, mid) <= r) lo = mid;
+        else hi = mid - 1;
     }
-    p.tile = static_cast<int>(r);
-    return p;
-}
-
-// The first entry of the unit after p's (which must exist).
-template <int BN>
-__device__ __forceinline__ void next_unit(const AttnArgs& a, Place& p) {
-    p.tile = 0;
-    if ((p.qt + 1) * a.tq < p.s.m) {
-        ++p.qt;
-    } else {
-        p.qt = 0;
-        if (++p.h == a.Hkv) {
-            p.h = 0;
-            bool bad;
-            do p.s = load_seq(a, ++p.n, &bad);
-            while (p.s.m == 0);
-        }
-    }
-    p.nk = unit_tiles<BN>(a, p.s, p.qt);
+    w.qt = lo;
+    w.begin = at - (r - cost_before<T>(a, w.s, lo));
+    enter<T>(a, w, at);
+    return w.t0 < w.t1 || advance<T>(a, w);
 }
 
 // pos / page_size for 0 <= pos < 2^31: page_mul = ceil(2^(31 + s) / page_size), 2^s >= page_size.
@@ -199,16 +255,18 @@ __device__ __forceinline__ long long row_of(const AttnArgs& a, int n, int h, int
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// What a CTA leaves for attn_combine_kernel: parts = 0, or the unit that begins in its range and goes on
-// in the next parts - 1 CTAs'.
-__device__ __forceinline__ void leave_join(const AttnArgs& a, const Place& p, int t0, int t1, long long per) {
+// What a CTA leaves for attn_combine_kernel: parts = 0, or the unit that begins in its stretch and goes on
+// in the next parts - 1 CTAs' (those whose stretch begins before the unit's last key tile).
+__device__ __forceinline__ void leave_join(const AttnArgs& a, const Walk& w, long long per) {
     AttnJoin j;
-    const int i0 = p.qt * a.tq;
-    j.parts = t0 > 0 || t1 == p.nk ? 0 : 1 + static_cast<int>((p.nk - t1 + per - 1) / per);
-    j.rows = min(a.tq, p.s.m - i0) * a.G;
-    j.h = p.h;
+    const int i0 = w.qt * a.tq;
+    j.parts = 0;
+    if (w.t0 == 0 && w.t1 < w.nk)
+        j.parts = 1 + static_cast<int>((w.begin + a.ov + static_cast<long long>(w.nk - 1) * w.wt) / per - blockIdx.x);
+    j.rows = min(a.tq, w.s.m - i0) * a.G;
+    j.h = w.h;
     j.pad = 0;
-    j.token = p.s.q0 + i0;
+    j.token = w.s.q0 + i0;
     a.joins[blockIdx.x] = j;
 }
 __device__ __forceinline__ void leave_no_join(const AttnArgs& a) { a.joins[blockIdx.x].parts = 0; }
@@ -239,20 +297,30 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const __g
     const long long slot = static_cast<long long>(R) * (D + 2);
     const float* first = a.part + (blockIdx.x * 2LL + 1) * slot;
     const float* rest = a.part + (blockIdx.x + 1) * 2LL * slot - 2 * slot;  // partial i >= 1 at rest + 2 i slot
-    // partials sl, sl + slices, .. of row r
+    // partials sl, sl + slices, .. of row r, four at a time (their loads in flight together)
     auto gather = [&](int r, int sl, float& ref, float& l, float4& acc) {
         ref = -INFINITY;
-#pragma unroll 8
-        for (int i = sl; i < j.parts; i += slices)
-            ref = fmaxf(ref, (i == 0 ? first : rest + i * 2 * slot)[static_cast<long long>(R) * D + r]);
-        const float base = ref == -INFINITY ? 0.f : ref;
         l = 0.f;
         acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int i = sl; i < j.parts; i += slices) {
-            const float* s = i == 0 ? first : rest + i * 2 * slot;
-            const float4 v = *reinterpret_cast<const float4*>(s + static_cast<long long>(r) * D + col);
-            weigh(exp2f(s[static_cast<long long>(R) * D + r] - base), s[static_cast<long long>(R) * (D + 1) + r], v, l, acc);
+        for (int i0 = sl; i0 < j.parts; i0 += 4 * slices) {
+            float rf[4], lp[4];
+            float4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = i0 + k * slices;
+                const float* s = i == 0 ? first : rest + i * 2 * slot;
+                const bool on = i < j.parts;
+                rf[k] = on ? s[static_cast<long long>(R) * D + r] : -INFINITY;
+                lp[k] = on ? s[static_cast<long long>(R) * (D + 1) + r] : 0.f;
+                v[k] = on ? *reinterpret_cast<const float4*>(s + static_cast<long long>(r) * D + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            const float top = fmaxf(fmaxf(fmaxf(rf[0], rf[1]), fmaxf(rf[2], rf[3])), ref);
+            const float base = top == -INFINITY ? 0.f : top, f = exp2f(ref - base);
+            l *= f;
+            acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) weigh(exp2f(rf[k] - base), lp[k], v[k], l, acc);
+            ref = top;
         }
     };
     auto finish = [&](int r, float ref, float l, const float4& acc) {

@@ -76,15 +76,6 @@ __device__ __forceinline__ uint32_t e4m3_hi(uint32_t x) {
     asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(r) : "r"(x));
     return r;
 }
-// Four e4m3 values of a word as binary16, times 2^-8: bytes 0 and 2, bytes 1 and 3 (the lower byte in the
-// low half).  Sign, exponent and significand move to binary16's places; the exponents' biases, 7 and 15,
-// leave the factor, which the callers' scales take up.  Exact, subnormal values included (NaN comes out
-// as 480 2^-8).  Seven logic operations for four values: the hardware conversion (cvt.rn.f16x2.e4m3x2)
-// takes two per instruction, but a warp's takes about 16 cycles and held the row kernel at 59 % of HBM.
-constexpr float kE4m3Up = 256.f;
-__device__ __forceinline__ uint32_t e4m3_even(uint32_t w) { return ((w << 7) & 0x3f803f80u) | ((w << 8) & 0x80008000u); }
-__device__ __forceinline__ uint32_t e4m3_odd(uint32_t w) { return ((w >> 1) & 0x3f803f80u) | (w & 0x80008000u); }
-
 // Two 16-bit elements to floats, and back (round to nearest even), the first in the low half.
 template <bool F16>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {

@@ -25,6 +25,7 @@ namespace attn {
 constexpr int kRowsTile = 16;   // rows per query tile
 constexpr int kRowsBN = 64;     // keys per tile: 16 per warp
 constexpr int kRowsNT = 128;
+typedef Tiling<kRowsBN, 1, kRowsTile> RowsTiling;
 
 template <int D, bool F8>
 struct RowsCfg {
@@ -52,30 +53,26 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
     constexpr bool MF16 = F16 || F8;  // operand type of the products
     constexpr int BN = kRowsBN, NS = C::NS, CH = C::CH, KS = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ PlanSmem plan;
+    __shared__ PlanSmem plan_s;
     __shared__ float m_s[4][16], l_s[4][16];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;  // fragment row and column group
 
-    long long w0;
-    const long long W = plan_total<BN, kRowsNT>(a, plan, w0, blockIdx.x == 0);
+    Walk p;
+    long long per;
+    const bool busy = plan<RowsTiling, kRowsNT>(a, plan_s, p, per);
     pdl_launch();
-    const long long per = max((W + gridDim.x - 1) / static_cast<long long>(gridDim.x), static_cast<long long>(a.min_tiles));
-    long long at = blockIdx.x * per;
-    if (at >= W) {
+    if (!busy) {
         if (tid == 0) leave_no_join(a);
         return;
     }
-    const long long end = min(at + per, W);
-    Place p = locate<BN, kRowsNT>(a, plan, w0, at);
 
     uint8_t* ring = smem + warp * (NS * C::STAGE);
     const uint32_t ring_a = smem_addr(ring);
     float* merge = reinterpret_cast<float*>(smem);
 
     for (;;) {
-        const int t0 = p.tile;
-        const int t1 = static_cast<int>(min(static_cast<long long>(p.nk), t0 + (end - at)));
+        const int t0 = p.t0, t1 = p.t1;
         const int i0 = p.qt * a.tq;
         const int ntok = min(a.tq, p.s.m - i0), rows = ntok * a.G;
         const int vis0 = p.s.L - p.s.m + i0 + 1;      // keys that token i0 sees
@@ -101,8 +98,7 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
                     qf[k][half + 2] = live ? s32[4] : 0u;
                 }
             } else {
-                // K step 4 kk + j holds, in thread column group t, features kk 64 + t 16 + 4 j + 0, 2, 1, 3 (the
-                // order in which a word's bytes are widened)
+                // K step 4 kk + j holds, in thread column group t, features kk 64 + t 16 + 4 j + 0 .. 3
                 float mx = 0.f;
 #pragma unroll
                 for (int kk = 0; kk < D / 64; ++kk) {
@@ -114,8 +110,8 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
                     const uint32_t* x = reinterpret_cast<const uint32_t*>(w);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        qf[4 * kk + j][half] = __byte_perm(x[2 * j], x[2 * j + 1], 0x5410);
-                        qf[4 * kk + j][half + 2] = __byte_perm(x[2 * j], x[2 * j + 1], 0x7632);
+                        qf[4 * kk + j][half] = x[2 * j];
+                        qf[4 * kk + j][half + 2] = x[2 * j + 1];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const float2 f = unpack2<F16>(x[2 * j + i]);
@@ -126,7 +122,7 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
                 mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 2));
                 const float up = row_up(mx);
-                rscale[half] *= kE4m3Up / up;
+                rscale[half] *= 1.f / up;
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
 #pragma unroll
@@ -200,7 +196,7 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
                         const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            mma16816<true>(sc[nt], qf[4 * kk + j], e4m3_even(x[j]), e4m3_odd(x[j]));
+                            mma16816<true>(sc[nt], qf[4 * kk + j], e4m3_lo(x[j]), e4m3_hi(x[j]));
                     }
                 }
             }
@@ -296,8 +292,9 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
                     ldsm4t(b, vst + vtok * C::ROWB + rows_swz<CH>(vtok, 2 * c2 + (mi >> 1)) * 16);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        mma16816<true>(o[4 * c2 + 2 * i], pf, e4m3_even(b[2 * i]), e4m3_even(b[2 * i + 1]));
-                        mma16816<true>(o[4 * c2 + 2 * i + 1], pf, e4m3_odd(b[2 * i]), e4m3_odd(b[2 * i + 1]));
+                        const uint32_t lo = __byte_perm(b[2 * i], 0, 0x3120), hi = __byte_perm(b[2 * i + 1], 0, 0x3120);
+                        mma16816<true>(o[4 * c2 + 2 * i], pf, e4m3_lo(lo), e4m3_lo(hi));
+                        mma16816<true>(o[4 * c2 + 2 * i + 1], pf, e4m3_hi(lo), e4m3_hi(hi));
                     }
                 }
             }
@@ -328,8 +325,8 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c)
                     *reinterpret_cast<float4*>(dst + ((c * 16 + 4 * t) ^ (g << 2 & 24))) =
-                        make_float4(o[2 * c][2 * half] * kE4m3Up, o[2 * c + 1][2 * half] * kE4m3Up, o[2 * c][2 * half + 1] * kE4m3Up,
-                                    o[2 * c + 1][2 * half + 1] * kE4m3Up);
+                        make_float4(o[2 * c][2 * half], o[2 * c + 1][2 * half], o[2 * c][2 * half + 1],
+                                    o[2 * c + 1][2 * half + 1]);
             }
         }
         __syncthreads();
@@ -370,12 +367,8 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
                 }
             }
         }
-        at += t1 - t0;
-        if (at >= end) {
-            if (tid == 0) leave_join(a, p, t0, t1, per);
-            break;
-        }
-        next_unit<BN>(a, p);
+        if (tid == 0) leave_join(a, p, per);  // the last unit's stands
+        if (!advance<RowsTiling>(a, p)) break;
         __syncthreads();  // the rings are written again
     }
 }

@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
     constexpr bool MF16 = F16 || F8;
     constexpr int BN = C::BN, NST = C::NST, LAG = C::LAG, SLOTS = C::SLOTS;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ PlanSmem plan;
+    __shared__ PlanSmem plan_s;
     constexpr int NBAR = TB_KV + 2 * NST + 4 * C::RINGS;
     __shared__ uint64_t bars[NBAR];
     __shared__ float ml_s[128][2];
@@ -169,17 +169,15 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
     __shared__ volatile int abort_flag;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = tid >> 7;
 
-    long long w0;
-    const long long W = plan_total<BN, kTilesNT>(a, plan, w0, blockIdx.x == 0);
+    typedef Tiling<BN, SLOTS, 128> T;
+    Walk p;
+    long long per;
+    const bool busy = plan<T, kTilesNT>(a, plan_s, p, per);
     pdl_launch();
-    const long long per = max((W + gridDim.x - 1) / static_cast<long long>(gridDim.x), static_cast<long long>(a.min_tiles));
-    long long at = blockIdx.x * per;
-    if (at >= W) {
+    if (!busy) {
         if (tid == 256) leave_no_join(a);
         return;
     }
-    const long long end = min(at + per, W);
-    Place p = locate<BN, kTilesNT>(a, plan, w0, at);
 
     uint8_t* sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t sb = smem_addr(sm);
@@ -307,7 +305,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             for (; open > 0 && ok; --open) finish(F8 ? 0u : pend >> (8 * (open - 1)) & 0xff);
         };
         for (;;) {
-            const int t0 = p.tile, t1 = static_cast<int>(min(static_cast<long long>(p.nk), t0 + (end - at)));
+            const int t0 = p.t0, t1 = p.t1;
             const int i0 = p.qt * a.tq, ntok = min(a.tq, p.s.m - i0), rows = ntok * a.G;
             const int kend = min(t1 * BN, p.s.L - p.s.m + i0 + ntok);
             // ---- queries
@@ -363,9 +361,14 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                 warp_arrive(TB_QF);
             }
             // ---- keys and values, tile by tile
-            for (int t = t0; t < t1 && ok; ++t) {
+            auto lookup = [&](int t) -> long long {  // a tile ahead: the page table is some hundred cycles away
                 const int pos = t * BN + mine;
-                const long long off = pos < kend ? row_of(a, p.n, p.h, pos) : -1;
+                return t < t1 && pos < kend ? row_of(a, p.n, p.h, pos) : -1;
+            };
+            long long next = lookup(t0);
+            for (int t = t0; t < t1 && ok; ++t) {
+                const long long off = next;
+                next = lookup(t + 1);
                 const bool tma = box && __all_sync(kFullMask, off >= 0);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
@@ -423,13 +426,9 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             // the MMAs of this unit, which free the query tiles, need all of its keys
             if (ok) flush();
             if (!ok) break;
-            at += t1 - t0;
             ++unit;
-            if (at >= end) {
-                if (tid == 256) leave_join(a, p, t0, t1, per);
-                break;
-            }
-            next_unit<BN>(a, p);
+            if (tid == 256) leave_join(a, p, per);  // the last unit's stands
+            if (!advance<T>(a, p)) break;
         }
         cp_async_wait<0>();
         if (!ok) {  // gave up: leave what TMA copies are in flight (microseconds) a millisecond
@@ -459,7 +458,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             };
             bool ok = true;
             for (;;) {
-                const int t0 = p.tile, t1 = static_cast<int>(min(static_cast<long long>(p.nk), t0 + (end - at)));
+                const int t0 = p.t0, t1 = p.t1;
                 const int rows = min(a.tq, p.s.m - p.qt * a.tq) * a.G;
                 const bool full = (SLOTS == 2 && rows > 128 ? 1u : 0u) != 0;
                 const int nops = static_cast<int>((static_cast<uint32_t>(full ? 2 * (t1 - t0) : t1 - t0)));
@@ -504,9 +503,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                 }
                 if (!ok) break;
                 ++unit;
-                at += t1 - t0;
-                if (at >= end) break;
-                next_unit<BN>(a, p);
+                if (!advance<T>(a, p)) break;
             }
             // nothing of this CTA's may be in flight when it ends, its barriers' arrivals included
             {
@@ -522,7 +519,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
         uint32_t unit = 0, ns[2] = {0, 0}, od[2] = {0, 0}, nml = 0, tiles = 0;
         (void)tiles;
         for (;;) {
-            const int t0 = p.tile, t1 = static_cast<int>(min(static_cast<long long>(p.nk), t0 + (end - at)));
+            const int t0 = p.t0, t1 = p.t1;
             const int i0 = p.qt * a.tq, rows = min(a.tq, p.s.m - i0) * a.G;
             const bool full = SLOTS == 2 && rows > 128;
             const int nops = full ? 2 * (t1 - t0) : t1 - t0;
@@ -712,7 +709,9 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                     ref = top;
                 }
                 const int o = SLOTS == 2 ? wg : 0;
-                ok = warp_wait(TB_OD0 + o, (od[o] - 1) & 1) && (!both || nops < 2 || warp_wait(TB_OD0 + 1, (od[1] - 1) & 1));
+                // One accumulator for both buffers: the last two products may both be pending, and a barrier is
+                // waited for one phase at a time (what was read of S says that those before them are done)
+                ok = (SLOTS == 2 || warp_wait(TB_OD0, od[0] & 1)) && warp_wait(TB_OD0 + o, (od[o] - 1) & 1) && (!both || nops < 2 || warp_wait(TB_OD0 + 1, (od[1] - 1) & 1));
                 if (!ok) break;
                 if (some) {
                     const bool whole = t0 == 0 && t1 == p.nk;
@@ -760,9 +759,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             }
             if (both) ++nml;
             ++unit;
-            at += t1 - t0;
-            if (at >= end) break;
-            next_unit<BN>(a, p);
+            if (!advance<T>(a, p)) break;
         }
     }
     __syncwarp();

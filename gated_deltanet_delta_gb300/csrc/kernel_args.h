@@ -198,7 +198,7 @@ struct AttnArgs {
     int page_size, max_pages, num_seqs;
     int Hq, Hkv, G;      // G = Hq / Hkv
     int tq;              // tokens per query tile
-    int min_tiles;       // fewest key tiles per CTA
+    int ov, min_per;     // a unit's fixed cost; the least cost per CTA (attn.cuh)
     int f16;             // q and out are binary16 (else bf16)
     float scale_log2;    // scale * log2(e)
     uint32_t page_mul;   // division by page_size

@@ -194,6 +194,22 @@ def test_repeats_bit_for_bit(gdn, max_q):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("max_q", [1, 64])
+def test_same_bits_with_cold_and_warm_caches(gdn, max_q, dim, f8):
+    # copies that come late or early, and in another order, change no bit
+    x = make(15, [8, 8, 30], [900, 1500, 300], 8, 2, dim, 64, torch.bfloat16, f8)
+    flush = torch.empty(300 << 20, dtype=torch.uint8, device="cuda")
+    first = call(gdn, x, 0.07, max_q=max_q)
+    check(x, first[0], first[1], 0.07)
+    for i in range(24):
+        if i % 2 == 0:
+            flush.fill_(i)
+        again = call(gdn, x, 0.07, max_q=max_q)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1]), i
+
+
 @pytest.mark.parametrize("max_q", [1, 64])
 def test_many_sequences(gdn, max_q):
     # more sequences than a block has threads, most of them tiny
