@@ -129,8 +129,8 @@ cudaError_t launch_tiles(AttnArgs a, cudaStream_t stream) {
     }
     if (regs.load(std::memory_order_relaxed) < attn::kRegsLaunch) return cudaErrorInvalidConfiguration;
     a.tq = C::R / a.G;
-    a.ov = 4;
-    a.min_per = 6;
+    a.ov = 6;
+    a.min_per = 8;
     // Boxes of at least 8 rows (the swizzle's period) that divide a page; coordinates are 32-bit
     AttnMaps maps;
     std::memset(&maps, 0, sizeof(maps));

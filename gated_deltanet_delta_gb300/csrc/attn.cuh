@@ -64,8 +64,14 @@ __device__ __forceinline__ long long floor_sum(long long n, unsigned m, unsigned
         a %= m;
         b %= m;
         const unsigned long long top = static_cast<unsigned long long>(a) * n + b;
-        n = static_cast<long long>(top / m);
-        b = static_cast<unsigned>(top % m);
+        if (top < m) break;
+        if (top >> 32) {
+            n = static_cast<long long>(top / m);
+            b = static_cast<unsigned>(top % m);
+        } else {
+            n = static_cast<unsigned>(top) / m;
+            b = static_cast<unsigned>(top) % m;
+        }
         const unsigned x = m;
         m = a;
         a = x;
@@ -224,14 +230,16 @@ __device__ __forceinline__ bool plan(const AttnArgs& a, PlanSmem& sm, Walk& w, l
     const long long rem = sm.rem, head = seq_cost<T>(a, w.s);
     w.h = static_cast<int>(rem / head);
     const long long r = rem - w.h * head;
-    int lo = 0, hi = (w.s.m - 1) / a.tq;  // the last query tile that begins at or before r
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (cost_before<T>(a, w.s, mid) <= r) lo = mid;
-        else hi = mid - 1;
+    // the last query tile that begins at or before r: costs rise, so count the tiles that do
+    const int tiles = (w.s.m + a.tq - 1) / a.tq;
+    int count = 0;
+    for (int q0 = 0; q0 < tiles; q0 += NT) {
+        const int c = __syncthreads_count(q0 + tid < tiles && cost_before<T>(a, w.s, q0 + tid) <= r);
+        count += c;
+        if (c < NT) break;
     }
-    w.qt = lo;
-    w.begin = at - (r - cost_before<T>(a, w.s, lo));
+    w.qt = count - 1;
+    w.begin = at - (r - cost_before<T>(a, w.s, w.qt));
     enter<T>(a, w, at);
     return w.t0 < w.t1 || advance<T>(a, w);
 }

@@ -13,7 +13,8 @@
 // Roles, 512 threads: two softmax warpgroups (one per buffer; thread i owns TMEM lane i, a row), a loader
 // warpgroup, and a warp whose lane 0 issues every MMA:  S(0) S(1) | P(0)? PV(0) S(2) | P(1)? PV(1) S(3) ..
 // Operations of one issuing thread run in order, so S(s + 2) overwrites a buffer only after PV(s) has
-// read P from it.
+// read P from it.  P is handed over in two halves, so that its products begin while the second half is
+// exponentiated: the chain S, softmax, PV of a slot is what bounds long chunks.
 // The loader gathers rows by page: whole boxes of rows by TMA, the ragged end of the keys by cp.async with
 // zero fill (nothing stale may meet a weight of zero).  8-bit caches go through a staging ring, a part per
 // loader warp, and are widened into the tile; attn_rows.cuh says how their scales are applied.
@@ -64,7 +65,7 @@ struct TilesCfg {
     static constexpr uint32_t TM_S = 0, TM_Q = 128, TM_O = 256, TM_SB = BN;  // TMEM columns
 };
 
-enum : int { TB_QF = 0, TB_QE, TB_S0, TB_S1, TB_P0, TB_P1, TB_OD0, TB_OD1, TB_OF0, TB_OF1, TB_MF, TB_ME, TB_SC0, TB_SC3 = TB_SC0 + 3, TB_DRAIN, TB_KV };  // then KV_FULL, KV_EMPTY and (8 bits) RAW_FULL of every loader warp
+enum : int { TB_QF = 0, TB_QE, TB_S0, TB_S1, TB_P0, TB_P1, TB_OD0, TB_OD1, TB_OF0, TB_OF1, TB_MF, TB_ME, TB_SC0, TB_SC3 = TB_SC0 + 3, TB_H0, TB_H1, TB_DRAIN, TB_KV };  // then KV_FULL, KV_EMPTY and (8 bits) RAW_FULL of every loader warp
 
 __device__ __forceinline__ void tm_ld32(uint32_t taddr, float* v) {
     uint32_t r[32];
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
     if (tid == 0) {
         for (int i = 0; i < NBAR; ++i) {
             const bool by_warps = i == TB_QF || i == TB_P0 || i == TB_P1 || i == TB_OF0 || i == TB_OF1 || i == TB_MF ||
-                                  i == TB_ME || (i >= TB_SC0 && i <= TB_SC3) || (i >= TB_KV && i < TB_KV + NST);
+                                  i == TB_ME || i == TB_H0 || i == TB_H1 || (i >= TB_SC0 && i <= TB_SC3) || (i >= TB_KV && i < TB_KV + NST);
             tc::mbar_init(&bars[i], by_warps ? 4 : 1);
         }
         abort_flag = 0;
@@ -486,15 +487,19 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                     const int b = s & 1, o = SLOTS == 2 ? b : 0;
                     const bool fresh = SLOTS == 2 ? s < 2 : s == 0, last = !full || b;
                     ok = ((full && b) || one_wait(KV_FULL + vs, vp)) && (!fresh || one_wait(TB_OF0 + o, (unit & 1) ^ 1)) &&
-                         one_wait(TB_P0 + b, np[b] & 1);
+                         one_wait((SLOTS == 2 ? TB_H0 : TB_P0) + b, np[b] & 1);
                     if (!ok) break;
                     ++np[b];
                     const uint64_t va = dv + vs * (C::TILE >> 4);
                     {
 #pragma unroll
-                        for (int k = 0; k < BN / 16; ++k)
+                        for (int k = 0; k < BN / 16; ++k) {
+                            // the first half of P came first; now the rest
+                            if (SLOTS == 2 && k == BN / 32 && !(ok = one_wait(TB_P0 + b, np[b] - 1 & 1))) break;
                             tc::mma_bf16_ts(tmu + C::TM_O + o * D, tmu + C::TM_S + b * C::TM_SB + 8 * k, va + k * (2048 / 16), ID_O,
                                             !fresh || k > 0);
+                        }
+                        if (!ok) break;
                         tc::commit(&bars[TB_OD0 + o]);
                         if (last) tc::commit(&bars[KV_EMPTY + vs]);
                     }
@@ -672,9 +677,16 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                             w[i / 2 + 1] = pack2<MF16>(x[2], x[3]);
                         }
                         tm_st16(ts + ch * 16, w);
+                        if (SLOTS == 2 && ch == BN / 64 - 1) {  // half of P: its products can start
+                            tc::wait_st();
+                            tc::fence_before();
+                            warp_arrive(TB_H0 + b);
+                        }
                     }
                     l += (l2[0] + l2[1]) + (l2[2] + l2[3]);
                     tc::wait_st();
+                } else if (SLOTS == 2) {
+                    warp_arrive(TB_H0 + b);
                 }
                 tc::fence_before();
                 warp_arrive(TB_P0 + b);
