@@ -61,19 +61,34 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// A cache as rows of D elements.  16 bits: boxes of 64 features, 128-byte swizzle (an operand tile's rows);
-// 8 bits: boxes of whole rows, as they are.
-bool encode_cache(CUtensorMap* map, const void* base, long long rows, int D, int box, bool f8, bool f16) {
+// A cache as rows of D elements, in boxes of `box` rows and `line` bytes (a row, or 128 bytes of it), with the
+// swizzle of that width, or none.
+bool encode_cache(CUtensorMap* map, const void* base, long long rows, int D, int box, int line, bool swizzle, bool f8, bool f16) {
     const auto fn = encode_fn();
     if (!fn) return false;
+    const int size = f8 ? 1 : 2;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * (f8 ? 1 : 2)};
-    const cuuint32_t shape[2] = {static_cast<cuuint32_t>(f8 ? D : 64), static_cast<cuuint32_t>(box)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * size};
+    const cuuint32_t shape[2] = {static_cast<cuuint32_t>(line / size), static_cast<cuuint32_t>(box)};
     const cuuint32_t step[2] = {1, 1};
     const CUtensorMapDataType type = f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : (f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
-    return fn(map, type, 2, const_cast<void*>(base), dims, strides, shape, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const CUtensorMapSwizzle sw = !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : (line == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+    return fn(map, type, 2, const_cast<void*>(base), dims, strides, shape, step, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Chooses a.box, the rows of a box: a power of two up to `most` that divides a page; 0 (no TMA) where that is
+// below `least`, or where a row's number passes the coordinates' 32 bits.  Makes the maps.
+cudaError_t make_maps(AttnArgs& a, AttnMaps& maps, int D, bool f8, int least, int most, int line, bool swizzle) {
+    std::memset(&maps, 0, sizeof(maps));
+    const long long rows = a.num_pages * a.Hkv * a.page_size;
+    a.box = std::min(a.page_size & -a.page_size, most);
+    if (a.box < least || rows < a.box || rows >= 1LL << 31) a.box = 0;
+    if (a.box == 0) return cudaSuccess;
+    return encode_cache(&maps.k, a.kc, rows, D, a.box, line, swizzle, f8, a.f16) &&
+                   encode_cache(&maps.v, a.vc, rows, D, a.box, line, swizzle, f8, a.f16)
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
 }
 
 // The joining kernel starts while the main kernel still runs (programmatic dependent launch) and waits
@@ -104,8 +119,18 @@ cudaError_t launch_rows(AttnArgs a, cudaStream_t stream) {
     a.tq = std::max(1, attn::kRowsTile / a.G);
     a.ov = 1;
     a.min_per = 3;
+    AttnMaps maps;
+    // the scales of a box come by copies that begin on 16-byte boundaries
+    const bool tma = F8 && (reinterpret_cast<uintptr_t>(a.ks) | reinterpret_cast<uintptr_t>(a.vs)) % 16 == 0;
+    if (tma) {
+        e = make_maps(a, maps, D, F8, 16, C::TK, C::LINE, true);
+        if (e != cudaSuccess) return e;
+    } else {
+        std::memset(&maps, 0, sizeof(maps));
+        a.box = 0;
+    }
     const int grid = std::min(sms * C::OCC, kMaxCtas);
-    attn::attn_rows_kernel<D, F16, F8><<<grid, attn::kRowsNT, C::SMEM, stream>>>(a);
+    attn::attn_rows_kernel<D, F16, F8><<<grid, attn::kRowsNT, C::SMEM, stream>>>(a, maps);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_combine<D>(a, attn::kRowsTile, grid, stream);
@@ -131,14 +156,10 @@ cudaError_t launch_tiles(AttnArgs a, cudaStream_t stream) {
     a.tq = C::R / a.G;
     a.ov = 6;
     a.min_per = 8;
-    // Boxes of at least 8 rows (the swizzle's period) that divide a page; coordinates are 32-bit
+    // boxes of at least 8 rows, the swizzle's period; 8 bits: whole rows, unswizzled, into the staging ring
     AttnMaps maps;
-    std::memset(&maps, 0, sizeof(maps));
-    const long long cached = a.num_pages * a.Hkv * a.page_size;
-    a.box = std::min(a.page_size & -a.page_size, C::BOX);
-    if (a.box < 8 || cached < a.box || cached >= 1LL << 31) a.box = 0;
-    if (a.box && !(encode_cache(&maps.k, a.kc, cached, D, a.box, F8, F16) && encode_cache(&maps.v, a.vc, cached, D, a.box, F8, F16)))
-        return cudaErrorInvalidValue;
+    e = make_maps(a, maps, D, F8, 8, C::BOX, F8 ? D : 128, !F8);
+    if (e != cudaSuccess) return e;
     const int grid = std::min(sms, kMaxTileCtas);
     attn::attn_tiles_kernel<D, F16, F8><<<grid, attn::kTilesNT, C::SMEM, stream>>>(a, maps);
     e = cudaGetLastError();

@@ -49,6 +49,12 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int n, bool* bad) {
     return s;
 }
 
+// a / b for a >= 0, b > 0: 64-bit division takes some hundred cycles, 32-bit a few tens.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+    if (static_cast<unsigned long long>(a | b) >> 32) return a / b;
+    return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+}
+
 // How a kernel tiles: BN keys, SL row tiles of ROWS rows per unit.
 template <int BN_, int SL_, int ROWS_>
 struct Tiling {
@@ -65,13 +71,8 @@ __device__ __forceinline__ long long floor_sum(long long n, unsigned m, unsigned
         b %= m;
         const unsigned long long top = static_cast<unsigned long long>(a) * n + b;
         if (top < m) break;
-        if (top >> 32) {
-            n = static_cast<long long>(top / m);
-            b = static_cast<unsigned>(top % m);
-        } else {
-            n = static_cast<unsigned>(top) / m;
-            b = static_cast<unsigned>(top) % m;
-        }
+        n = divide(static_cast<long long>(top), m);
+        b = static_cast<unsigned>(top - static_cast<unsigned long long>(n) * m);
         const unsigned x = m;
         m = a;
         a = x;
@@ -129,7 +130,7 @@ struct Walk {
 
 __device__ __forceinline__ int cut(const AttnArgs& a, const Walk& w, long long at) {  // key tiles before `at`
     const long long x = at - w.begin - a.ov;
-    return x <= 0 ? 0 : static_cast<int>(min(static_cast<long long>(w.nk), (x + w.wt - 1) / w.wt));
+    return x <= 0 ? 0 : static_cast<int>(min(static_cast<long long>(w.nk), (x + w.wt - 1) >> (w.wt - 1)));  // wt: 1 or 2
 }
 template <class T>
 __device__ __forceinline__ void enter(const AttnArgs& a, Walk& w, long long from) {
@@ -183,7 +184,7 @@ __device__ __forceinline__ bool plan(const AttnArgs& a, PlanSmem& sm, Walk& w, l
     long long total = 0;
 #pragma unroll
     for (int i = 0; i < NT / 32; ++i) total += sm.warp[i];
-    per = max((total + gridDim.x - 1) / static_cast<long long>(gridDim.x), static_cast<long long>(a.min_per));
+    per = max(divide(total + gridDim.x - 1, gridDim.x), static_cast<long long>(a.min_per));
     const long long at = blockIdx.x * per;
     if (at >= total) return false;
     // the sequence that `at` falls in
@@ -228,7 +229,7 @@ __device__ __forceinline__ bool plan(const AttnArgs& a, PlanSmem& sm, Walk& w, l
     bool bad;
     w.s = load_seq(a, w.n, &bad);
     const long long rem = sm.rem, head = seq_cost<T>(a, w.s);
-    w.h = static_cast<int>(rem / head);
+    w.h = static_cast<int>(divide(rem, head));
     const long long r = rem - w.h * head;
     // the last query tile that begins at or before r: costs rise, so count the tiles that do
     const int tiles = (w.s.m + a.tq - 1) / a.tq;
@@ -270,7 +271,7 @@ __device__ __forceinline__ void leave_join(const AttnArgs& a, const Walk& w, lon
     const int i0 = w.qt * a.tq;
     j.parts = 0;
     if (w.t0 == 0 && w.t1 < w.nk)
-        j.parts = 1 + static_cast<int>((w.begin + a.ov + static_cast<long long>(w.nk - 1) * w.wt) / per - blockIdx.x);
+        j.parts = 1 + static_cast<int>(divide(w.begin + a.ov + static_cast<long long>(w.nk - 1) * w.wt, per) - blockIdx.x);
     j.rows = min(a.tq, w.s.m - i0) * a.G;
     j.h = w.h;
     j.pad = 0;
@@ -283,7 +284,7 @@ __device__ __forceinline__ void leave_no_join(const AttnArgs& a) { a.joins[block
 // slot 1 of that CTA and slot 0 of the parts - 1 after it, in that order.  A slot holds R rows of D sums,
 // then R references, then R values of l.  D / 4 threads make a group, which owns a row (four columns per
 // thread); with more groups than rows, several groups share a row's partials.  blockIdx.y: rows RB ..
-constexpr int kCombineThreads = 512;
+constexpr int kCombineThreads = 256;
 __device__ __forceinline__ void weigh(float f, float lp, const float4& v, float& l, float4& acc) {
     l = fmaf(f, lp, l);
     acc.x = fmaf(f, v.x, acc.x);
@@ -292,7 +293,7 @@ __device__ __forceinline__ void weigh(float f, float lp, const float4& v, float&
     acc.w = fmaf(f, v.w, acc.w);
 }
 template <int D>
-__global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const __grid_constant__ AttnArgs a, int R, int RB) {
+__global__ void __launch_bounds__(kCombineThreads, 5) attn_combine_kernel(const __grid_constant__ AttnArgs a, int R, int RB) {
     constexpr int TPR = D / 4, GROUPS = kCombineThreads / TPR;
     __shared__ float4 acc_s[kCombineThreads];
     __shared__ float2 rl_s[GROUPS];
@@ -305,16 +306,16 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const __g
     const long long slot = static_cast<long long>(R) * (D + 2);
     const float* first = a.part + (blockIdx.x * 2LL + 1) * slot;
     const float* rest = a.part + (blockIdx.x + 1) * 2LL * slot - 2 * slot;  // partial i >= 1 at rest + 2 i slot
-    // partials sl, sl + slices, .. of row r, four at a time (their loads in flight together)
+    // partials sl, sl + slices, .. of row r, three at a time (their loads in flight together)
     auto gather = [&](int r, int sl, float& ref, float& l, float4& acc) {
         ref = -INFINITY;
         l = 0.f;
         acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i0 = sl; i0 < j.parts; i0 += 4 * slices) {
-            float rf[4], lp[4];
-            float4 v[4];
+        for (int i0 = sl; i0 < j.parts; i0 += 3 * slices) {
+            float rf[3], lp[3];
+            float4 v[3];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 3; ++k) {
                 const int i = i0 + k * slices;
                 const float* s = i == 0 ? first : rest + i * 2 * slot;
                 const bool on = i < j.parts;
@@ -322,12 +323,12 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const __g
                 lp[k] = on ? s[static_cast<long long>(R) * (D + 1) + r] : 0.f;
                 v[k] = on ? *reinterpret_cast<const float4*>(s + static_cast<long long>(r) * D + col) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            const float top = fmaxf(fmaxf(fmaxf(rf[0], rf[1]), fmaxf(rf[2], rf[3])), ref);
+            const float top = fmaxf(fmaxf(rf[0], rf[1]), fmaxf(rf[2], ref));
             const float base = top == -INFINITY ? 0.f : top, f = exp2f(ref - base);
             l *= f;
             acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) weigh(exp2f(rf[k] - base), lp[k], v[k], l, acc);
+            for (int k = 0; k < 3; ++k) weigh(exp2f(rf[k] - base), lp[k], v[k], l, acc);
             ref = top;
         }
     };

@@ -3,7 +3,7 @@
 // Bound: the cache is read once from HBM and each key row meets at most 16 query rows, about 16
 // operations per byte, so the time is the bytes' time.  What the kernel has to do is keep enough of
 // them in flight and stay out of their way.  Hence: four independent warps per CTA, each with its own
-// ring of cp.async stages of 16 keys (no block barrier inside a unit); warp w takes keys 16 w .. 16 w + 15
+// ring of stages of 16 or 32 keys (no block barrier inside a unit); warp w takes keys 16 w .. 16 w + 15
 // of each 64-key tile and keeps its own reference, sum and accumulator, joined once per unit through
 // shared memory.  The products run on mma.sync m16n8k16: its 16 rows are the whole tile, whereas a
 // tcgen05.mma would compute 128 rows for them and add a TMEM round trip per tile.
@@ -18,43 +18,54 @@
 
 #include "attn.cuh"
 #include "attn_mma.cuh"
+#include "tcgen05.cuh"
 
 namespace gdn {
 namespace attn {
 
 constexpr int kRowsTile = 16;   // rows per query tile
-constexpr int kRowsBN = 64;     // keys per tile: 16 per warp
 constexpr int kRowsNT = 128;
-typedef Tiling<kRowsBN, 1, kRowsTile> RowsTiling;
+constexpr uint32_t kRowsWait = 1u << 22;  // polls before a wait gives up (seconds)
 
 template <int D, bool F8>
 struct RowsCfg {
-    static constexpr int ROWB = F8 ? D : 2 * D;               // bytes per cached row
-    static constexpr int CH = ROWB / 16;                      // 16-byte chunks per row
-    static constexpr int STAGE = 2 * 16 * ROWB + (F8 ? 128 : 0);  // K rows, V rows, scales
-    // stages per warp: about 100 KB per CTA, two CTAs per SM
-    static constexpr int NS = D == 256 ? (F8 ? 3 : 3) : (D == 128 ? (F8 ? 4 : 3) : (F8 ? 6 : 4));
+    static constexpr int ROWB = F8 ? D : 2 * D;      // bytes per cached row
+    static constexpr int CH = ROWB / 16;             // 16-byte chunks per cached row
+    static constexpr int LINE = ROWB < 128 ? ROWB : 128;  // bytes of a row that stand together
+    static constexpr int COLS = ROWB / LINE;         // a stage's rows as COLS blocks of TK lines
+    // keys per step and warp.  8 bits: a step of 16 took 560 instructions, half of them not for its products
+    static constexpr int TK = F8 && D <= 128 ? 32 : 16;
+    static constexpr int BN = 4 * TK;                // keys per tile of the CTA
+    static constexpr int STAGE = 2 * TK * ROWB;      // K rows, V rows
+    // stages per warp: 64 to 100 KB per CTA, two or three CTAs per SM
+    static constexpr int NS = D == 256 ? 3 : (D == 128 ? (F8 ? 2 : 3) : (F8 ? 3 : 4));
     static constexpr int RING = NS * STAGE * 4;
+    static constexpr int SCALE = 8 * TK;             // a stage's scales: K, V
+    static constexpr int SCALES = F8 ? NS * 4 * SCALE : 0;
     static constexpr int MERGE = 4 * 16 * D * 4;
-    static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+    static constexpr int SMEM = (RING + SCALES > MERGE ? RING + SCALES : MERGE) + 1024;
     static constexpr int OCC = D == 256 ? (F8 ? 2 : 1) : (D == 128 ? (F8 ? 3 : 2) : 3);
 };
 
-// 16-byte chunk c of row r of a stage: rows are XOR-swizzled so that eight rows at one chunk column, or
-// eight consecutive chunks, fall on different banks.
-template <int CH>
-__device__ __forceinline__ int rows_swz(int r, int c) {
-    return CH >= 8 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3));
+// Byte offset of 16-byte chunk c of row r of a stage's rows: the layout that TMA writes with its 128-byte
+// (64-byte) swizzle, in which eight rows at one chunk column, or eight consecutive chunks, fall on
+// different banks.
+template <class C>
+__device__ __forceinline__ int rows_at(int r, int c) {
+    if constexpr (C::LINE == 128) return (c >> 3) * (C::TK * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    else return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
 template <int D, bool F16, bool F8>
-__global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnMaps maps) {
     using C = RowsCfg<D, F8>;
     constexpr bool MF16 = F16 || F8;  // operand type of the products
-    constexpr int BN = kRowsBN, NS = C::NS, CH = C::CH, KS = D / 16;
-    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int TK = C::TK, BN = C::BN, NS = C::NS, CH = C::CH, KS = D / 16, NT = TK / 8;
+    typedef Tiling<BN, 1, kRowsTile> RowsTiling;
+    extern __shared__ uint8_t smem_raw[];
     __shared__ PlanSmem plan_s;
     __shared__ float m_s[4][16], l_s[4][16];
+    __shared__ uint64_t full[4][NS];  // a stage filled by TMA
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;  // fragment row and column group
 
@@ -67,9 +78,17 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
         return;
     }
 
-    uint8_t* ring = smem + warp * (NS * C::STAGE);
-    const uint32_t ring_a = smem_addr(ring);
+    uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    const uint32_t ring_a = smem_addr(smem) + warp * (NS * C::STAGE);
+    const uint32_t scale_a = smem_addr(smem) + C::RING + warp * (NS * C::SCALE);
     float* merge = reinterpret_cast<float*>(smem);
+    if (lane == 0) {
+        for (int i = 0; i < NS; ++i) tc::mbar_init(&full[warp][i], 1);
+        tc::fence_proxy_async();
+    }
+    __syncwarp();
+    uint32_t phase = 0;     // of the stages' barriers
+    bool gave_up = false;
 
     for (;;) {
         const int t0 = p.t0, t1 = p.t1;
@@ -139,60 +158,103 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
         for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         float ref[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
 
-        // ---- this warp's steps: keys (t0 + s) 64 + warp 16 .. + 15, while any is below kend ----
-        const int first = t0 * BN + warp * 16;
-        const int steps = kend > first ? (kend - first + BN - 1) / BN : 0;
-        auto fetch_off = [&](int s) -> long long {  // row offset of this lane's key of step s
-            const int pos = first + s * BN + (lane & 15);
-            return s < steps && pos < kend ? row_of(a, p.n, p.h, pos) : -1;
+        // ---- this warp's steps: keys (t0 + s) BN + warp TK .. + TK - 1, while any is below kend ----
+        const int first = t0 * BN + warp * TK;
+        const int steps = kend > first && !gave_up ? (kend - first + BN - 1) / BN : 0;
+        // 8 bits, pages that 16 divides: TMA, by boxes of a.box rows, of which one page holds each; lane i looks
+        // up and copies box i.  Else (any page size) cp.async: every lane looks up a row, and rows past kend are
+        // zero-filled.  16-bit rows take that way always: it keeps as many bytes in flight, and is ready earlier
+        // (64 sequences of up to 8192 keys, 8 x 128: 184 us, by TMA 188).
+        const bool tma = F8 && a.box >= 16;
+        auto lookup = [&](int s) -> long long {
+            const int i = tma ? lane * a.box : lane & (TK - 1), pos = first + s * BN + i;
+            return s < steps && i < TK && pos < kend ? row_of(a, p.n, p.h, pos) : -1;
         };
-        long long off = fetch_off(0);
+        long long off = lookup(0);
         auto issue = [&](int s) {
             if (s < steps) {
-                const uint32_t dst = ring_a + (s % NS) * C::STAGE;
-                if constexpr (F8) {
-                    const float* sc = lane < 16 ? a.ks : a.vs;
-                    cp_async4(dst + 32 * C::ROWB + lane * 4, sc + (off < 0 ? 0 : off), off >= 0);
-                }
+                const int st = s % NS;
+                const uint32_t dst = ring_a + st * C::STAGE, sdst = scale_a + st * C::SCALE;
+                if (tma) {
+                    uint64_t* bar = &full[warp][st];
+                    const unsigned on = __ballot_sync(kFullMask, off >= 0);
+                    if (lane == 0) tc::mbar_expect_tx(bar, __popc(on) * a.box * (2 * C::ROWB + 8));
+                    __syncwarp();
+                    if (off >= 0) {
+                        const int r = lane * a.box;
 #pragma unroll
-                for (int i = 0; i < CH / 2; ++i) {
-                    const int idx = i * 32 + lane, r = idx / CH, c = idx % CH;
-                    const long long ro = __shfl_sync(kFullMask, off, r);
-                    const long long byte = (ro < 0 ? 0 : ro * C::ROWB) + c * 16;
-                    const uint32_t d = dst + r * C::ROWB + rows_swz<CH>(r, c) * 16;
-                    cp_async16(d, static_cast<const uint8_t*>(a.kc) + byte, ro >= 0);
-                    cp_async16(d + 16 * C::ROWB, static_cast<const uint8_t*>(a.vc) + byte, ro >= 0);
+                        for (int x = 0; x < C::COLS; ++x) {
+                            tma_load_2d(dst + x * (TK * 128) + r * C::LINE, &maps.k, x * C::LINE, static_cast<int>(off), bar);
+                            tma_load_2d(dst + TK * C::ROWB + x * (TK * 128) + r * C::LINE, &maps.v, x * C::LINE, static_cast<int>(off), bar);
+                        }
+                        tc::bulk_load(sdst + r * 4, a.ks + off, a.box * 4, bar);
+                        tc::bulk_load(sdst + TK * 4 + r * 4, a.vs + off, a.box * 4, bar);
+                    }
+                } else {
+                    if constexpr (F8) {
+                        if (lane < TK) {
+                            cp_async4(sdst + lane * 4, a.ks + (off < 0 ? 0 : off), off >= 0);
+                            cp_async4(sdst + TK * 4 + lane * 4, a.vs + (off < 0 ? 0 : off), off >= 0);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < CH * TK / 32; ++i) {
+                        const int idx = i * 32 + lane, r = idx / CH, c = idx % CH;
+                        const long long ro = __shfl_sync(kFullMask, off, r);
+                        const long long byte = (ro < 0 ? 0 : ro * C::ROWB) + c * 16;
+                        const uint32_t d = dst + rows_at<C>(r, c);
+                        cp_async16(d, static_cast<const uint8_t*>(a.kc) + byte, ro >= 0);
+                        cp_async16(d + TK * C::ROWB, static_cast<const uint8_t*>(a.vc) + byte, ro >= 0);
+                    }
                 }
-                off = fetch_off(s + 1);
+                off = lookup(s + 1);
             }
-            cp_async_commit();
+            if (!tma) cp_async_commit();
         };
 #pragma unroll
         for (int s = 0; s < NS - 1; ++s) issue(s);
 
         for (int s = 0; s < steps; ++s) {
-            cp_async_wait<NS - 2>();
-            __syncwarp();
+            const int st = s % NS, base = first + s * BN;
+            const uint32_t kst = ring_a + st * C::STAGE, vst = kst + TK * C::ROWB, sst = scale_a + st * C::SCALE;
+            if (tma) {
+                if (!tc::mbar_wait(&full[warp][st], phase >> st & 1, kRowsWait)) {
+                    atomicOr(a.status, kStatusTimeout);
+                    gave_up = true;
+                }
+                phase ^= 1u << st;
+                if (base + TK > kend) {  // what the page holds past the keys must not meet a weight of zero
+                    __syncwarp();
+                    for (int i = lane; i < TK * CH; i += 32)
+                        if (base + i / CH >= kend) sts128(vst + rows_at<C>(i / CH, i % CH), make_uint4(0, 0, 0, 0));
+                    tc::fence_proxy_async();  // before TMA writes here again
+                }
+            } else {
+                cp_async_wait<NS - 2>();
+            }
+            if (__any_sync(kFullMask, gave_up)) {
+                gave_up = true;
+                break;
+            }
+            __syncwarp();  // all lanes' copies and zeros are in place, and the previous step has read its stage
             issue(s + NS - 1);  // into the stage that the previous step has read
-            const uint32_t kst = ring_a + (s % NS) * C::STAGE, vst = kst + 16 * C::ROWB;
 
-            float sc[2][4] = {};
+            float sc[NT][4] = {};
             if constexpr (!F8) {
                 const int mi = lane >> 3, tok = (mi >> 1) * 8 + (lane & 7);
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
                     uint32_t b[4];
-                    ldsm4(b, kst + tok * C::ROWB + rows_swz<CH>(tok, 2 * k + (mi & 1)) * 16);
+                    ldsm4(b, kst + rows_at<C>(tok, 2 * k + (mi & 1)));
                     mma16816<MF16>(sc[0], qf[k], b[0], b[1]);
                     mma16816<MF16>(sc[1], qf[k], b[2], b[3]);
                 }
             } else {
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    const int tok = nt * 8 + g;
+                for (int kk = 0; kk < D / 64; ++kk) {
 #pragma unroll
-                    for (int kk = 0; kk < D / 64; ++kk) {
-                        uint4 w = lds128(kst + tok * C::ROWB + rows_swz<CH>(tok, kk * 4 + t) * 16);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint4 w = lds128(kst + rows_at<C>(nt * 8 + g, kk * 4 + t));
                         const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
@@ -202,43 +264,42 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
             }
 
             // ---- y = s log2(e), masked; 8-bit values: plus log2 of the value's scale ----
-            const int base = first + s * BN;
-            float lv[2][2], iv[2][2];
+            float iv[NT][2];
             if constexpr (F8) {
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float2 ks = lds64(sst + (nt * 8 + 2 * t) * 4), vs = lds64(sst + TK * 4 + (nt * 8 + 2 * t) * 4);
+                    const float lv[2] = {fast_log2(vs.x), fast_log2(vs.y)};
+                    iv[nt][0] = fast_rcp(vs.x);
+                    iv[nt][1] = fast_rcp(vs.y);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int tok = nt * 8 + 2 * t + i;
-                        const float ks = lds32(kst + 32 * C::ROWB + tok * 4), vs = lds32(kst + 32 * C::ROWB + 64 + tok * 4);
-                        // the stage's rows past the segment's end hold zeros, scale included
-                        const bool in = base + tok < kend;
-                        lv[nt][i] = in ? log2f(vs) : 0.f;
-                        iv[nt][i] = in ? 1.f / vs : 0.f;
-#pragma unroll
-                        for (int half = 0; half < 2; ++half)
-                            sc[nt][2 * half + i] = fmaf(sc[nt][2 * half + i] * rscale[half], ks, lv[nt][i]);
+                    for (int half = 0; half < 2; ++half) {
+                        sc[nt][2 * half] = fmaf(sc[nt][2 * half] * rscale[half], ks.x, lv[0]);
+                        sc[nt][2 * half + 1] = fmaf(sc[nt][2 * half + 1] * rscale[half], ks.y, lv[1]);
                     }
                 }
             } else {
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) sc[nt][i] *= a.scale_log2;
             }
-            if (base + 16 > vis0 || base + 16 > kend) {
+            if (base + TK > vis0 || base + TK > kend) {
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int pos = base + nt * 8 + 2 * t + (i & 1);
                         if (pos >= vis[i >> 1] || pos >= kend) sc[nt][i] = -INFINITY;
+                        if (F8 && pos >= kend) iv[nt][i & 1] = 0.f;  // no key, no scale
                     }
             }
             float mx[2], use[2];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                float x = fmaxf(fmaxf(sc[0][2 * half], sc[0][2 * half + 1]), fmaxf(sc[1][2 * half], sc[1][2 * half + 1]));
+                float x = fmaxf(sc[0][2 * half], sc[0][2 * half + 1]);
+#pragma unroll
+                for (int nt = 1; nt < NT; ++nt) x = fmaxf(x, fmaxf(sc[nt][2 * half], sc[nt][2 * half + 1]));
                 x = fmaxf(x, __shfl_xor_sync(kFullMask, x, 1));
                 mx[half] = fmaxf(x, __shfl_xor_sync(kFullMask, x, 2));
             }
@@ -263,43 +324,48 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
             }
             use[0] = ref[0] == -INFINITY ? 0.f : ref[0];
             use[1] = ref[1] == -INFINITY ? 0.f : ref[1];
-            uint32_t pf[4];
+            uint32_t pf[NT / 2][4];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
+            for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const float x = fast_exp2(sc[nt][2 * half] - use[half]), y = fast_exp2(sc[nt][2 * half + 1] - use[half]);
                     if constexpr (F8) lsum[half] = fmaf(x, iv[nt][0], fmaf(y, iv[nt][1], lsum[half]));
                     else lsum[half] += x + y;
-                    pf[2 * nt + half] = pack2<MF16>(x, y);
+                    pf[nt / 2][2 * (nt & 1) + half] = pack2<MF16>(x, y);
                 }
             }
 
-            const int mi = lane >> 3, vtok = (mi & 1) * 8 + (lane & 7);
-            if constexpr (!F8) {
+            const int mi = lane >> 3;
 #pragma unroll
-                for (int dc = 0; dc < D / 16; ++dc) {
-                    uint32_t b[4];
-                    ldsm4t(b, vst + vtok * C::ROWB + rows_swz<CH>(vtok, 2 * dc + (mi >> 1)) * 16);
-                    mma16816<MF16>(o[2 * dc], pf, b[0], b[1]);
-                    mma16816<MF16>(o[2 * dc + 1], pf, b[2], b[3]);
-                }
-            } else {
-                // a chunk's even features make one 8-column tile, its odd features another
+            for (int kg = 0; kg < TK / 16; ++kg) {
+                const int vtok = kg * 16 + (mi & 1) * 8 + (lane & 7);
+                if constexpr (!F8) {
 #pragma unroll
-                for (int c2 = 0; c2 < D / 32; ++c2) {
-                    uint32_t b[4];
-                    ldsm4t(b, vst + vtok * C::ROWB + rows_swz<CH>(vtok, 2 * c2 + (mi >> 1)) * 16);
+                    for (int dc = 0; dc < D / 16; ++dc) {
+                        uint32_t b[4];
+                        ldsm4t(b, vst + rows_at<C>(vtok, 2 * dc + (mi >> 1)));
+                        mma16816<MF16>(o[2 * dc], pf[kg], b[0], b[1]);
+                        mma16816<MF16>(o[2 * dc + 1], pf[kg], b[2], b[3]);
+                    }
+                } else {
+                    // a chunk's even features make one 8-column tile, its odd features another
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t lo = __byte_perm(b[2 * i], 0, 0x3120), hi = __byte_perm(b[2 * i + 1], 0, 0x3120);
-                        mma16816<true>(o[4 * c2 + 2 * i], pf, e4m3_lo(lo), e4m3_lo(hi));
-                        mma16816<true>(o[4 * c2 + 2 * i + 1], pf, e4m3_hi(lo), e4m3_hi(hi));
+                    for (int c2 = 0; c2 < D / 32; ++c2) {
+                        uint32_t b[4];
+                        ldsm4t(b, vst + rows_at<C>(vtok, 2 * c2 + (mi >> 1)));
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t lo = __byte_perm(b[2 * i], 0, 0x3120), hi = __byte_perm(b[2 * i + 1], 0, 0x3120);
+                            mma16816<true>(o[4 * c2 + 2 * i], pf[kg], e4m3_lo(lo), e4m3_lo(hi));
+                            mma16816<true>(o[4 * c2 + 2 * i + 1], pf[kg], e4m3_hi(lo), e4m3_hi(hi));
+                        }
                     }
                 }
             }
         }
         cp_async_wait<0>();
+        __syncwarp();
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             lsum[half] += __shfl_xor_sync(kFullMask, lsum[half], 1);
@@ -369,7 +435,11 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
         }
         if (tid == 0) leave_join(a, p, per);  // the last unit's stands
         if (!advance<RowsTiling>(a, p)) break;
+        tc::fence_proxy_async();
         __syncthreads();  // the rings are written again
+    }
+    if (gave_up) {  // leave the copies in flight (microseconds) a millisecond
+        for (int i = 0; i < 100; ++i) __nanosleep(10000);
     }
 }
 

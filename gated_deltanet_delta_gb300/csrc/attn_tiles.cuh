@@ -140,14 +140,6 @@ __device__ __forceinline__ bool elect() {
     return one != 0;
 }
 
-// TMA: a 2-D box at column x, row y of the cache seen as rows of D elements.
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, int x, int y, uint64_t* mbar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(tc::smem_u32(mbar))
-        : "memory");
-}
-
 // Registers per thread after the roles part: the softmax holds a row of S (the launch's 512 x 128 registers
 // are 128 x (184 + 184 + 72 + 72)).
 constexpr int kRegsLaunch = 128, kRegsSoftmax = 184, kRegsOther = 72;
