@@ -148,9 +148,9 @@ def _stream(device) -> int:
 
 
 def _want(t, name: str, dtype, shape=None):
-    torch = _torch()
-    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous()
-            and (shape is None or t.shape == shape)):
+    torch = _torch_module or _torch()
+    # the usual case first, in few steps: these checks are a good part of a small call's time
+    if type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.is_contiguous() and (shape is None or t.shape == shape):
         return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -476,53 +476,56 @@ def gdn_window_fused(state, hist, hist_out, qkv, alpha, beta, z, conv_w, dt, ssm
 # Attention over a paged cache, the cache itself, draft verification
 # ------------------------------------------------------------------------------------------------
 def _row_code(dtype, name: str) -> int:
-    torch = _torch()
-    if dtype == torch.bfloat16:
+    torch = _torch_module or _torch()
+    if dtype is torch.bfloat16:
         return GDN_BF16
-    if dtype == torch.float16:
+    if dtype is torch.float16:
         return GDN_F16
     raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {dtype}")
 
 
 def _want_rows(t, name: str, dtype, shape):
     """A [T, H, D] tensor whose tokens may stand apart (a slice of a wider row); returns its token stride."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    torch = _torch_module or _torch()
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.shape == shape):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     T, H, D = shape
     if T == 0:
         return H * D
-    s = t.stride()
-    if s[2] != 1 or (H > 1 and s[1] != D):
-        raise ValueError(f"{name}: a token's heads must be contiguous (strides {s})")
-    return s[0] if T > 1 else H * D
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (H > 1 and s1 != D):
+        raise ValueError(f"{name}: a token's heads must be contiguous (strides {t.stride()})")
+    return s0 if T > 1 else H * D
 
 
 def _want_cache(k_cache, v_cache, k_scale, v_scale, dtype):
-    """Checks the caches against rows of `dtype`; returns their type's code."""
-    torch = _torch()
-    if k_cache.dim() != 4:
-        raise ValueError(f"k_cache must be [num_pages,Hkv,page_size,D], got {tuple(k_cache.shape)}")
-    f8 = k_cache.dtype == torch.float8_e4m3fn
-    _want(k_cache, "k_cache", torch.float8_e4m3fn if f8 else dtype)
-    _want(v_cache, "v_cache", k_cache.dtype, k_cache.shape)
+    """Checks the caches against rows of `dtype`; returns their type's code and their shape."""
+    torch = _torch_module or _torch()
+    shape = k_cache.shape
+    if len(shape) != 4:
+        raise ValueError(f"k_cache must be [num_pages,Hkv,page_size,D], got {tuple(shape)}")
+    f8 = k_cache.dtype is torch.float8_e4m3fn
+    have = torch.float8_e4m3fn if f8 else dtype
+    _want(k_cache, "k_cache", have)
+    _want(v_cache, "v_cache", have, shape)
     if f8:
-        _want(k_scale, "k_scale", torch.float32, k_cache.shape[:3])
-        _want(v_scale, "v_scale", torch.float32, k_cache.shape[:3])
-        return GDN_E4M3
+        _want(k_scale, "k_scale", torch.float32, shape[:3])
+        _want(v_scale, "v_scale", torch.float32, shape[:3])
+        return GDN_E4M3, shape
     if k_scale is not None or v_scale is not None:
         raise ValueError(f"a {k_cache.dtype} cache has no scales")
-    return _row_code(dtype, "k_cache")
+    return _row_code(dtype, "k_cache"), shape
 
 
 def _want_status(dev_status, device):
-    torch = _torch()
+    torch = _torch_module or _torch()
     if dev_status is None:
         dev_status = torch.zeros(1, dtype=torch.int32, device=device)
     return _want(dev_status, "dev_status", torch.int32, (1,))
@@ -534,18 +537,18 @@ def attn_cache_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, 
     leave a token out; k_cache, v_cache [num_pages,Hkv,page_size,D] of k's dtype, or torch.float8_e4m3fn
     with k_scale, v_scale f32 [num_pages,Hkv,page_size]: each row is then quantised with a power-of-two
     scale of its own."""
-    torch = _torch()
-    code = _row_code(k.dtype, "k")
-    cache = _want_cache(k_cache, v_cache, k_scale, v_scale, k.dtype)
-    pages, H, page_size, D = k_cache.shape
-    T = k.shape[0]
-    ks = _want_rows(k, "k", k.dtype, (T, H, D))
-    vs = _want_rows(v, "v", k.dtype, (T, H, D))
+    torch = _torch_module or _torch()
+    dtype, device, T = k.dtype, k.device, k.shape[0]
+    code = _row_code(dtype, "k")
+    cache, (pages, H, page_size, D) = _want_cache(k_cache, v_cache, k_scale, v_scale, dtype)
+    rows = (T, H, D)
+    ks = _want_rows(k, "k", dtype, rows)
+    vs = _want_rows(v, "v", dtype, rows)
     _want(slots, "slots", torch.int64, (T,))
-    dev_status = _want_status(dev_status, k.device)
-    _check(load().attn_cache_write(_ptr(k), _ptr(v), ks, vs, code, _ptr(slots), T, _ptr(k_cache), _ptr(v_cache),
-                                   _ptr(k_scale), _ptr(v_scale), cache, pages, page_size, H, D, _ptr(dev_status),
-                                   _stream(k.device)), "attn_cache_write")
+    dev_status = _want_status(dev_status, device)
+    _check(load().attn_cache_write(k.data_ptr(), v.data_ptr(), ks, vs, code, slots.data_ptr(), T, k_cache.data_ptr(),
+                                   v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale), cache, pages, page_size, H, D,
+                                   dev_status.data_ptr(), _stream(device)), "attn_cache_write")
 
 
 def attn_cache_read(k_cache, v_cache, page_table, cu_seqlens, T: int, dtype=None, k_scale=None, v_scale=None,
@@ -553,25 +556,30 @@ def attn_cache_read(k_cache, v_cache, page_table, cu_seqlens, T: int, dtype=None
     """Cached keys and values as dense rows: token t of sequence n is row cu_seqlens[n] + t of k, v
     [T,Hkv,D], T = cu_seqlens[-1].  page_table int64 [N,max_pages]; cu_seqlens int64 [N+1]; dtype is the
     rows' (an 8-bit cache's default is bf16, another's its own).  Returns (k, v)."""
-    torch = _torch()
-    pages, H, page_size, D = k_cache.shape
+    torch = _torch_module or _torch()
+    device = k_cache.device
     if dtype is None:
-        dtype = torch.bfloat16 if k_cache.dtype == torch.float8_e4m3fn else k_cache.dtype
+        dtype = torch.bfloat16 if k_cache.dtype is torch.float8_e4m3fn else k_cache.dtype
     code = _row_code(dtype, "dtype")
-    cache = _want_cache(k_cache, v_cache, k_scale, v_scale, dtype)
+    cache, (pages, H, page_size, D) = _want_cache(k_cache, v_cache, k_scale, v_scale, dtype)
     N = cu_seqlens.shape[0] - 1
     _want(page_table, "page_table", torch.int64)
-    if page_table.dim() != 2 or page_table.shape[0] != N:
-        raise ValueError(f"page_table must be [{N},max_pages], got {tuple(page_table.shape)}")
+    table = page_table.shape
+    if len(table) != 2 or table[0] != N:
+        raise ValueError(f"page_table must be [{N},max_pages], got {tuple(table)}")
     _want(cu_seqlens, "cu_seqlens", torch.int64, (N + 1,))
-    k = torch.empty((T, H, D), dtype=dtype, device=k_cache.device) if k is None else k
-    v = torch.empty((T, H, D), dtype=dtype, device=k_cache.device) if v is None else v
-    _want(k, "k", dtype, (T, H, D))
-    _want(v, "v", dtype, (T, H, D))
-    dev_status = _want_status(dev_status, k_cache.device)
-    _check(load().attn_cache_read(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), cache, pages, page_size,
-                                  _ptr(page_table), page_table.shape[1], _ptr(cu_seqlens), N, T, H, D, _ptr(k),
-                                  _ptr(v), code, _ptr(dev_status), _stream(k_cache.device)), "attn_cache_read")
+    rows = (T, H, D)
+    if k is None:
+        k = torch.empty(rows, dtype=dtype, device=device)
+    if v is None:
+        v = torch.empty(rows, dtype=dtype, device=device)
+    _want(k, "k", dtype, rows)
+    _want(v, "v", dtype, rows)
+    dev_status = _want_status(dev_status, device)
+    _check(load().attn_cache_read(k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale), cache, pages,
+                                  page_size, page_table.data_ptr(), table[1], cu_seqlens.data_ptr(), N, T, H, D,
+                                  k.data_ptr(), v.data_ptr(), code, dev_status.data_ptr(), _stream(device)),
+           "attn_cache_read")
     return k, v
 
 
@@ -587,34 +595,35 @@ def attn_paged(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens, max_q: int,
     int64 [N,max_pages]; kv_lens int64 [N]: cached tokens, the new ones included; cu_seqlens int64 [N+1]:
     rows of q; max_q: the longest chunk (it only chooses the kernel).  Returns out [T,Hq,D]; lse (f32
     [T,Hq]) is filled where given.  scale defaults to D^-0.5."""
-    torch = _torch()
-    T, Hq, D = q.shape
-    code = _row_code(q.dtype, "q")
-    cache = _want_cache(k_cache, v_cache, k_scale, v_scale, q.dtype)
-    pages, Hkv, page_size, Dc = k_cache.shape
+    torch = _torch_module or _torch()
+    dtype, device, rows = q.dtype, q.device, q.shape
+    T, Hq, D = rows
+    code = _row_code(dtype, "q")
+    cache, (pages, Hkv, page_size, Dc) = _want_cache(k_cache, v_cache, k_scale, v_scale, dtype)
     if Dc != D:
         raise ValueError(f"q has heads of {D}, the cache of {Dc}")
-    q_stride = _want_rows(q, "q", q.dtype, (T, Hq, D))
+    q_stride = _want_rows(q, "q", dtype, rows)
     N = kv_lens.shape[0]
     _want(page_table, "page_table", torch.int64)
-    if page_table.dim() != 2 or page_table.shape[0] != N:
-        raise ValueError(f"page_table must be [{N},max_pages], got {tuple(page_table.shape)}")
+    table = page_table.shape
+    if len(table) != 2 or table[0] != N:
+        raise ValueError(f"page_table must be [{N},max_pages], got {tuple(table)}")
     _want(kv_lens, "kv_lens", torch.int64, (N,))
     _want(cu_seqlens, "cu_seqlens", torch.int64, (N + 1,))
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    _want(out, "out", q.dtype, (T, Hq, D))
+        out = torch.empty(rows, dtype=dtype, device=device)
+    else:
+        _want(out, "out", dtype, rows)
     if lse is not None:
         _want(lse, "lse", torch.float32, (T, Hq))
     if workspace is None:
-        workspace = torch.empty(attn_paged_workspace_size(D), dtype=torch.uint8, device=q.device)
-    dev_status = _want_status(dev_status, q.device)
-    scale = D ** -0.5 if scale is None else float(scale)
-    _check(load().attn_paged(_ptr(q), q_stride, code, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                             cache, pages, page_size, _ptr(page_table), page_table.shape[1], _ptr(kv_lens),
-                             _ptr(cu_seqlens), N, T, int(max_q), Hq, Hkv, D, scale, _ptr(out), _ptr(lse),
-                             _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status),
-                             _stream(q.device)), "attn_paged")
+        workspace = torch.empty(attn_paged_workspace_size(D), dtype=torch.uint8, device=device)
+    dev_status = _want_status(dev_status, device)
+    _check(load().attn_paged(q.data_ptr(), q_stride, code, k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
+                             _ptr(v_scale), cache, pages, page_size, page_table.data_ptr(), table[1],
+                             kv_lens.data_ptr(), cu_seqlens.data_ptr(), N, T, max_q, Hq, Hkv, D,
+                             D ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse), workspace.data_ptr(),
+                             workspace.nbytes, dev_status.data_ptr(), _stream(device)), "attn_paged")
     return out
 
 
@@ -624,24 +633,28 @@ def draft_verify(target_p, draft_p, drafts, u_accept, u_sample, num_drafts=None,
     u_accept f32 [N,T] and u_sample f32 [N] uniform in [0, 1); num_drafts int64 [N] where some sequences
     have fewer than T.  Returns (accepted int64 [N], tokens int64 [N,T+1]): the accepted drafts, the token
     drawn after them, then -1."""
-    torch = _torch()
+    torch = _torch_module or _torch()
+    device = target_p.device
     N, T1, V = target_p.shape
     T = T1 - 1
-    _want(target_p, "target_p", torch.float32)
-    _want(draft_p, "draft_p", torch.float32, (N, T, V))
-    _want(drafts, "drafts", torch.int64, (N, T))
-    _want(u_accept, "u_accept", torch.float32, (N, T))
-    _want(u_sample, "u_sample", torch.float32, (N,))
+    f32, i64 = torch.float32, torch.int64
+    _want(target_p, "target_p", f32)
+    _want(draft_p, "draft_p", f32, (N, T, V))
+    _want(drafts, "drafts", i64, (N, T))
+    _want(u_accept, "u_accept", f32, (N, T))
+    _want(u_sample, "u_sample", f32, (N,))
     if num_drafts is not None:
-        _want(num_drafts, "num_drafts", torch.int64, (N,))
+        _want(num_drafts, "num_drafts", i64, (N,))
     if accepted is None:
-        accepted = torch.empty((N,), dtype=torch.int64, device=target_p.device)
+        accepted = torch.empty((N,), dtype=i64, device=device)
+    else:
+        _want(accepted, "accepted", i64, (N,))
     if tokens is None:
-        tokens = torch.empty((N, T + 1), dtype=torch.int64, device=target_p.device)
-    _want(accepted, "accepted", torch.int64, (N,))
-    _want(tokens, "tokens", torch.int64, (N, T + 1))
-    dev_status = _want_status(dev_status, target_p.device)
-    _check(load().draft_verify(_ptr(target_p), _ptr(draft_p), _ptr(drafts), _ptr(num_drafts), _ptr(u_accept),
-                               _ptr(u_sample), N, T, V, _ptr(accepted), _ptr(tokens), _ptr(dev_status),
-                               _stream(target_p.device)), "draft_verify")
+        tokens = torch.empty((N, T1), dtype=i64, device=device)
+    else:
+        _want(tokens, "tokens", i64, (N, T1))
+    dev_status = _want_status(dev_status, device)
+    _check(load().draft_verify(target_p.data_ptr(), draft_p.data_ptr(), drafts.data_ptr(), _ptr(num_drafts),
+                               u_accept.data_ptr(), u_sample.data_ptr(), N, T, V, accepted.data_ptr(),
+                               tokens.data_ptr(), dev_status.data_ptr(), _stream(device)), "draft_verify")
     return accepted, tokens

@@ -51,19 +51,30 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
 template <int D, bool F16, bool F8, int TOKENS>
 __global__ void __launch_bounds__(kThreads) attn_cache_write_kernel(const __grid_constant__ CacheMoveArgs a) {
     constexpr int LANES = D / 8, GROUPS = kThreads / LANES, ROWS = (TOKENS + GROUPS - 1) / GROUPS;
-    const int h = blockIdx.y, kv = blockIdx.z, lane = threadIdx.x % LANES;
-    const long long first = static_cast<long long>(blockIdx.x) * TOKENS + threadIdx.x / LANES;
-    const long long last = min(static_cast<long long>(blockIdx.x + 1) * TOKENS, a.T);
-    const uint16_t* src = (kv ? a.v_in + first * a.v_stride : a.k_in + first * a.k_stride) + h * D + lane * 8;
-    const long long step = GROUPS * (kv ? a.v_stride : a.k_stride);
+    __shared__ long long rows_s[TOKENS];
+    const int h = blockIdx.y, kv = blockIdx.z, lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+    const long long t0 = static_cast<long long>(blockIdx.x) * TOKENS;
+    const uint16_t* src = (kv ? a.v_in + t0 * a.v_stride : a.k_in + t0 * a.k_stride) + h * D + lane * 8;
+    const long long stride = kv ? a.v_stride : a.k_stride;
     uint4 x[ROWS];
-    long long slot[ROWS];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-        const bool on = first + i * GROUPS < last;
-        x[i] = on ? __ldcs(reinterpret_cast<const uint4*>(src + i * step)) : make_uint4(0, 0, 0, 0);
-        slot[i] = on ? a.slots[first + i * GROUPS] : -1;
+        const int k = group + i * GROUPS;
+        x[i] = k < TOKENS && t0 + k < a.T ? __ldcs(reinterpret_cast<const uint4*>(src + k * stride)) : make_uint4(0, 0, 0, 0);
     }
+    // the cached row of each token (-1: none), once per token: a 64-bit division per row and lane took as long as
+    // the copy
+    if (threadIdx.x < TOKENS) {
+        const long long t = t0 + threadIdx.x, slot = t < a.T ? a.slots[t] : -1;
+        long long row = -1;
+        if (slot >= 0) {  // a negative slot: the token is not kept
+            const long long page = (slot | a.page_size) >> 32 ? slot / a.page_size : static_cast<unsigned>(slot) / static_cast<unsigned>(a.page_size);
+            if (page < a.num_pages) row = (page * a.H + h) * a.page_size + (slot - page * a.page_size);
+            else atomicOr(a.status, kStatusBadCacheIndex);
+        }
+        rows_s[threadIdx.x] = row;
+    }
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
@@ -94,13 +105,9 @@ __global__ void __launch_bounds__(kThreads) attn_cache_write_kernel(const __grid
             q.x = to_e4m3x2(f[0], f[1]) | to_e4m3x2(f[2], f[3]) << 16;
             q.y = to_e4m3x2(f[4], f[5]) | to_e4m3x2(f[6], f[7]) << 16;
         }
-        if (first + i * GROUPS >= last || slot[i] < 0) continue;  // a negative slot: the token is not kept
-        const long long page = slot[i] / a.page_size;
-        if (page >= a.num_pages) {
-            if (lane == 0) atomicOr(a.status, kStatusBadCacheIndex);
-            continue;
-        }
-        const long long row = (page * a.H + h) * a.page_size + (slot[i] - page * a.page_size);
+        const int k = group + i * GROUPS;
+        const long long row = k < TOKENS ? rows_s[k] : -1;
+        if (row < 0) continue;
         if constexpr (F8) {
             uint8_t* dst = static_cast<uint8_t*>(kv ? a.vc : a.kc);
             *reinterpret_cast<uint2*>(dst + row * D + lane * 8) = q;
