@@ -250,15 +250,18 @@ __device__ __forceinline__ int page_of(const AttnArgs& a, int pos) {
     return static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned>(pos)) * a.page_mul) >> a.page_shift);
 }
 
-// Element offset (in rows of D) of key `pos` of sequence n, head h; -1 where its page is outside the cache.
-__device__ __forceinline__ long long row_of(const AttnArgs& a, int n, int h, int pos) {
-    const int pg = page_of(a, pos);
-    const long long page = a.table[static_cast<long long>(n) * a.max_pages + pg];
+// The page table's entry for key `pos` of sequence n.  Looked at (row_of) only when it is needed: a check
+// right behind the load would wait for it.
+__device__ __forceinline__ long long page_entry(const AttnArgs& a, int n, int pos) {
+    return a.table[static_cast<long long>(n) * a.max_pages + page_of(a, pos)];
+}
+// Offset (in rows of D) of key `pos` of head h, which is in page `page`; -1 where that is outside the cache.
+__device__ __forceinline__ long long row_of(const AttnArgs& a, long long page, int h, int pos) {
     if (page < 0 || page >= a.num_pages) {
         atomicOr(a.status, kStatusBadCacheIndex);
         return -1;
     }
-    return (page * a.Hkv + h) * a.page_size + (pos - pg * a.page_size);
+    return (page * a.Hkv + h) * a.page_size + (pos - page_of(a, pos) * a.page_size);
 }
 
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

@@ -166,13 +166,17 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
         // zero-filled.  16-bit rows take that way always: it keeps as many bytes in flight, and is ready earlier
         // (64 sequences of up to 8192 keys, 8 x 128: 184 us, by TMA 188).
         const bool tma = F8 && a.box >= 16;
-        auto lookup = [&](int s) -> long long {
-            const int i = tma ? lane * a.box : lane & (TK - 1), pos = first + s * BN + i;
-            return s < steps && i < TK && pos < kend ? row_of(a, p.n, p.h, pos) : -1;
+        const int mine = tma ? lane * a.box : lane & (TK - 1);  // the row, or the first of a box, of this lane
+        auto entry = [&](int s) -> long long {
+            const int pos = first + s * BN + mine;
+            return s < steps && mine < TK && pos < kend ? page_entry(a, p.n, pos) : 0;
         };
-        long long off = lookup(0);
+        long long next = entry(0);
         auto issue = [&](int s) {
             if (s < steps) {
+                const int pos = first + s * BN + mine;
+                const long long off = mine < TK && pos < kend ? row_of(a, next, p.h, pos) : -1;
+                next = entry(s + 1);
                 const int st = s % NS;
                 const uint32_t dst = ring_a + st * C::STAGE, sdst = scale_a + st * C::SCALE;
                 if (tma) {
@@ -207,7 +211,6 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
                         cp_async16(d + TK * C::ROWB, static_cast<const uint8_t*>(a.vc) + byte, ro >= 0);
                     }
                 }
-                off = lookup(s + 1);
             }
             if (!tma) cp_async_commit();
         };

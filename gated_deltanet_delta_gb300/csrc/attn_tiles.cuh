@@ -257,10 +257,13 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                 }
                 const uint32_t raw = sb + C::OFF_RAW + (lg * C::NRAW + ring) * C::RAW + (warp & 3) * (PER * 512) + lane * 16;
                 const uint32_t dst = sb + C::OFF_KV + stage * C::TILE;
-#pragma unroll 4
+                uint4 held[PER];
+#pragma unroll
+                for (int i = 0; i < PER; ++i) held[i] = lds128(raw + i * 512);
+#pragma unroll
                 for (int i = 0; i < PER; ++i) {
                     const int idx = i * 32 + lane, r = r0 + idx / CHR, c = idx % CHR;
-                    const uint4 w = lds128(raw + i * 512);
+                    const uint4 w = held[i];
                     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
                     uint32_t y[8];
 #pragma unroll
@@ -354,14 +357,15 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                 warp_arrive(TB_QF);
             }
             // ---- keys and values, tile by tile
-            auto lookup = [&](int t) -> long long {  // a tile ahead: the page table is some hundred cycles away
+            auto entry = [&](int t) -> long long {
                 const int pos = t * BN + mine;
-                return t < t1 && pos < kend ? row_of(a, p.n, p.h, pos) : -1;
+                return t < t1 && pos < kend ? page_entry(a, p.n, pos) : 0;
             };
-            long long next = lookup(t0);
+            long long next = entry(t0);  // a tile ahead: the page table is some hundred cycles away
             for (int t = t0; t < t1 && ok; ++t) {
-                const long long off = next;
-                next = lookup(t + 1);
+                const int pos = t * BN + mine;
+                const long long off = pos < kend ? row_of(a, next, p.h, pos) : -1;
+                next = entry(t + 1);
                 const bool tma = box && __all_sync(kFullMask, off >= 0);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
