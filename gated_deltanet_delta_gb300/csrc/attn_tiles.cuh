@@ -40,32 +40,33 @@ struct TilesCfg {
     static constexpr int R = 128 * SLOTS;                  // rows per unit
     static constexpr int HALVES = D / 64;                  // 64-feature halves of an operand tile
     static constexpr bool QTM = D == 256;                  // queries in TMEM, not in shared memory
-    static constexpr bool DUAL = F8 && D == 256;           // warpgroup 1, idle else, loads the values
+    static constexpr bool DUAL = F8 && D == 256;           // warpgroup 1, idle else, widens the values
     static constexpr uint32_t QTILE = 128u * D * 2, TILE = static_cast<uint32_t>(BN) * D * 2;
     static constexpr uint32_t RAW = F8 ? TILE / 2 : 0;
-    // K and V tiles in shared memory.  8 bits, one loader: 3, so a K tile takes the place of its second
-    // predecessor's V tile, and two slots for the keys' scales are enough.  Two loaders: 4, so that each has
-    // places of its own; a K tile takes its second predecessor's, whose product follows the softmax of the
-    // tile two before that: four slots.
+    // K and V tiles in shared memory.  Two widening warpgroups: 4, so that each has places of its own.
     static constexpr int NST = F8 ? (DUAL ? 4 : 3) : (D == 64 ? 8 : (D == 128 ? 5 : 6));
-    static constexpr uint32_t SCN = DUAL ? 4 : 2;
-    // copy groups in flight behind the newest.  16 bits: at most NST - 2, as S(s + 2) needs its K tile before
-    // the V tile before it is released.
-    static constexpr int LAG = F8 ? (D == 64 ? 5 : (DUAL ? 1 : 2)) : 3;
-    static constexpr int NRAW = F8 ? LAG + 1 : 0;          // staging slots of a loader
-    static constexpr int RINGS = F8 ? (DUAL ? 2 : 1) * NRAW : 0;
+    // copy groups in flight behind the newest: at most NST - 2, as S(s + 2) needs its K tile before the V tile
+    // before it is released
+    static constexpr int LAG = 3;
+    // 8 bits: staging slots, one ring for all tiles or (DUAL) one for the keys' and one for the values'
+    static constexpr int NRAW = F8 ? (D == 64 ? 6 : (DUAL ? 2 : 3)) : 0, RINGS = (DUAL ? 2 : 1) * NRAW;
+    static constexpr uint32_t SCN = 4;                     // tiles whose keys' scales are held
     static constexpr int BOX = BN / 4;                     // most rows of one TMA box: a loader warp's rows
     static constexpr uint32_t OFF_KV = QTM ? 0 : SLOTS * QTILE;
     static constexpr uint32_t OFF_RAW = OFF_KV + NST * TILE;
-    static constexpr uint32_t OFF_RSC = OFF_RAW + RINGS * RAW;            // raw scales of a stage: K, V
-    static constexpr uint32_t OFF_SC = OFF_RSC + NRAW * (F8 ? 1024 : 0);  // ks, log2 vs, 1 / vs of SCN tiles
-    static constexpr uint32_t OFF_RS = OFF_SC + (F8 ? SCN * 3 * BN * 4 : 0);  // row scales of two units
+    static constexpr uint32_t OFF_SC = OFF_RAW + RINGS * RAW;             // ks, log2 vs, 1 / vs of SCN tiles
+    static constexpr uint32_t OFF_RS = OFF_SC + (F8 ? SCN * 3u * BN * 4 : 0);  // row scales of two units
     static constexpr uint32_t USED = OFF_RS + (F8 && !QTM ? 2 * R * 4 : 0);
     static constexpr uint32_t SMEM = USED + 1024;          // 1024-byte alignment
     static constexpr uint32_t TM_S = 0, TM_Q = 128, TM_O = 256, TM_SB = BN;  // TMEM columns
 };
 
-enum : int { TB_QF = 0, TB_QE, TB_S0, TB_S1, TB_P0, TB_P1, TB_OD0, TB_OD1, TB_OF0, TB_OF1, TB_MF, TB_ME, TB_SC0, TB_SC3 = TB_SC0 + 3, TB_H0, TB_H1, TB_DRAIN, TB_KV };  // then KV_FULL, KV_EMPTY and (8 bits) RAW_FULL of every loader warp
+// Barriers: queries full / empty, S, P (halves first), products with V done, accumulators read, (ref, l)
+// handed over / read, end; then KV_FULL and KV_EMPTY of every place and, for 8 bits, staging slots and scales
+// full / empty.
+enum : int {
+    TB_QF = 0, TB_QE, TB_S0, TB_S1, TB_P0, TB_P1, TB_H0, TB_H1, TB_OD0, TB_OD1, TB_OF0, TB_OF1, TB_MF, TB_ME, TB_DRAIN, TB_KV
+};
 
 __device__ __forceinline__ void tm_ld32(uint32_t taddr, float* v) {
     uint32_t r[32];
@@ -153,9 +154,11 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
     using C = TilesCfg<D, F8>;
     constexpr bool MF16 = F16 || F8;
     constexpr int BN = C::BN, NST = C::NST, LAG = C::LAG, SLOTS = C::SLOTS;
+    (void)LAG;
     extern __shared__ uint8_t smem_raw[];
     __shared__ PlanSmem plan_s;
-    constexpr int NBAR = TB_KV + 2 * NST + 4 * C::RINGS;
+    constexpr int KV_FULL = TB_KV, KV_EMPTY = TB_KV + NST, RAW_FULL = TB_KV + 2 * NST, RAW_EMPTY = RAW_FULL + C::RINGS,
+                  SC_FULL = RAW_EMPTY + C::RINGS, SC_EMPTY = SC_FULL + (F8 ? C::SCN : 0), NBAR = SC_EMPTY + (F8 ? C::SCN : 0);
     __shared__ uint64_t bars[NBAR];
     __shared__ float ml_s[128][2];
     __shared__ uint32_t tmem_slot;
@@ -177,9 +180,9 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
     if (warp == 12) tc::tmem_alloc(&tmem_slot, 512);
     if (tid == 0) {
         for (int i = 0; i < NBAR; ++i) {
-            const bool by_warps = i == TB_QF || i == TB_P0 || i == TB_P1 || i == TB_OF0 || i == TB_OF1 || i == TB_MF ||
-                                  i == TB_ME || i == TB_H0 || i == TB_H1 || (i >= TB_SC0 && i <= TB_SC3) || (i >= TB_KV && i < TB_KV + NST);
-            tc::mbar_init(&bars[i], by_warps ? 4 : 1);
+            const bool by_warps = i == TB_QF || (i >= TB_P0 && i <= TB_H1) || i == TB_OF0 || i == TB_OF1 || i == TB_MF ||
+                                  i == TB_ME || (i >= KV_FULL && i < KV_EMPTY) || (i >= RAW_EMPTY && i < SC_FULL);
+            tc::mbar_init(&bars[i], i >= SC_EMPTY ? 8 : (by_warps ? 4 : 1));
         }
         abort_flag = 0;
     }
@@ -187,7 +190,6 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
     __syncthreads();
     tc::fence_after();
     const uint32_t tm = tmem_slot;
-    constexpr int KV_FULL = TB_KV, KV_EMPTY = TB_KV + NST, RAW_FULL = TB_KV + 2 * NST;
 
     auto wait = [&](int i, uint32_t parity) -> bool {
         if (tc::mbar_wait_or_abort(&bars[i], parity, kTilesWait, &abort_flag)) return true;
@@ -210,120 +212,33 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
         if (lane == 0) tc::mbar_arrive(&bars[i]);
     };
 
-    if (wg == 2 || (C::DUAL && wg == 1)) {
+    constexpr int RW = BN / 4;                  // rows of a tile that a loader (widening) warp handles
+    constexpr int CHR = (F8 ? D : 2 * D) / 16;  // 16-byte chunks per cached row
+    constexpr int PER = RW * CHR / 32;          // chunks per lane and tile
+    if (F8 && (wg == 2 || (C::DUAL && wg == 1))) {
+        // ------------------------------------------------------------ 8 bits: queries, and widening
+        // Tiles are numbered K 0, V 1, K 2, ..; a warpgroup has all of them, or (DUAL) the even or the odd ones.
         regs_down<kRegsOther>();
-        // ------------------------------------------------------------ loader
-        // warp w moves rows w RW .. w RW + RW - 1 of every tile; lane l holds the cache offset of one of them
-        constexpr int RW = BN / 4;
-        constexpr int CHR = (F8 ? D : 2 * D) / 16;  // 16-byte chunks per cached row
-        constexpr int PER = RW * CHR / 32;          // chunks per lane and tile
-        const int tl = tid & 127, r0 = (warp & 3) * RW, mine = r0 + lane % RW;
-        // rows that lie within the keys come by TMA, in boxes of a.box rows that never straddle a page; a
-        // warp with a row past the keys (or a page size without a factor of 8) uses cp.async and zero-fills
-        const int box = a.box, boxes = box ? RW / box : 0;
-        // tiles are numbered K 0, V 1, K 2, ..; a loader has all of them, or (DUAL) the even or the odd ones
+        const int tl = tid & 127, r0 = (warp & 3) * RW;
         const uint32_t lg = C::DUAL && wg == 1 ? 1 : 0;
         constexpr uint32_t STEP = C::DUAL ? 2 : 1;
-        uint32_t open = 0, item = lg, made = lg, pend = 0, unit = 0;
-        uint32_t raw_tma = 0, raw_phase = 0;  // 8 bits: ring slots filled by TMA, and their barriers' parities
+        uint32_t stage = lg, par = 1, slot = 0, rpar = 0, unit = 0;  // the next place and its parity, the next staging slot
         bool ok = true;
         if (tid == 256) leave_no_join(a);  // stands if this CTA gives up
-        // the oldest group has landed: (8 bits: widen it and) hand it over
-        auto finish = [&](uint32_t what) {
-            if constexpr (F8) {
-                const uint32_t stage = made % NST, ring = made / STEP % C::NRAW;
-                if (raw_tma >> ring & 1) {
-                    if (!warp_wait(RAW_FULL + 4 * (lg * C::NRAW + ring) + (warp & 3), raw_phase >> ring & 1)) {
-                        ok = false;
-                        return;
-                    }
-                    raw_phase ^= 1u << ring;
-                }
-                if (!warp_wait(KV_EMPTY + stage, (made / NST & 1) ^ 1)) {
-                    ok = false;
-                    return;
-                }
-                if (!(made & 1)) {  // a K tile: its keys' scales, for the softmax
-                    if (lane < RW) {
-                        const uint32_t rsc = sb + C::OFF_RSC + ring * 1024 + mine * 4;
-                        float* sc = reinterpret_cast<float*>(sm + C::OFF_SC) + made / 2 % C::SCN * (3 * BN) + mine;
-                        const float ks = lds32(rsc), vs = lds32(rsc + 512);
-                        const bool none = vs == 0.f;  // past the keys: zero-filled
-                        sc[0] = ks;
-                        sc[BN] = none ? 0.f : log2f(vs);
-                        sc[2 * BN] = none ? 0.f : 1.f / vs;
-                    }
-                    warp_arrive(TB_SC0 + made / 2 % C::SCN);
-                }
-                const uint32_t raw = sb + C::OFF_RAW + (lg * C::NRAW + ring) * C::RAW + (warp & 3) * (PER * 512) + lane * 16;
-                const uint32_t dst = sb + C::OFF_KV + stage * C::TILE;
-                uint4 held[PER];
-#pragma unroll
-                for (int i = 0; i < PER; ++i) held[i] = lds128(raw + i * 512);
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int idx = i * 32 + lane, r = r0 + idx / CHR, c = idx % CHR;
-                    const uint4 w = held[i];
-                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t y[8];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        y[2 * j] = e4m3_lo(x[j]);
-                        y[2 * j + 1] = e4m3_hi(x[j]);
-                    }
-                    // chunks 2 c and 2 c + 1 of the row; lanes of odd 64-feature halves store theirs in the other
-                    // order, so that eight lanes' stores fall on different banks
-                    const bool odd = CHR > 4 && (c & 4);
-                    const uint4 y0 = make_uint4(y[0], y[1], y[2], y[3]), y1 = make_uint4(y[4], y[5], y[6], y[7]);
-                    sts128(dst + tc::sw_chunk(r, 2 * c + (odd ? 1 : 0), BN), odd ? y1 : y0);
-                    sts128(dst + tc::sw_chunk(r, 2 * c + (odd ? 0 : 1), BN), odd ? y0 : y1);
-                }
-                tc::fence_proxy_async();
-                warp_arrive(KV_FULL + stage);
-                made += STEP;
-            } else {
-                tc::fence_proxy_async();
-                warp_arrive(what);
-            }
-        };
-        auto push = [&](uint32_t what) {  // closes a copy group, which fills what barrier `what` stands for
-            cp_async_commit();
-            pend = pend << 8 | what;
-            if (open == LAG) {
-                cp_async_wait<LAG>();
-                finish(F8 ? 0u : pend >> (8 * (LAG & 3)) & 0xff);
-            } else {
-                ++open;
-            }
-        };
-        auto flush = [&]() {
-            cp_async_wait<0>();
-            for (; open > 0 && ok; --open) finish(F8 ? 0u : pend >> (8 * (open - 1)) & 0xff);
-        };
+        // Lanes 0 .. 3 of every eight take chunks of one row, 4 .. 7 the other half's of the next row: so eight lanes'
+        // 16-byte loads, and each of their two stores, fall on different banks.
+        const int sub = lane >> 2 & 1, q8 = lane >> 3;
+        int rl, cl;  // row within a pass over 32 chunks, and chunk
+        if constexpr (CHR == 16) rl = sub, cl = (lane & 3) + 4 * (q8 ^ sub);
+        else if constexpr (CHR == 8) rl = 2 * (q8 >> 1) + sub, cl = (lane & 3) + 4 * ((q8 & 1) ^ sub);
+        else rl = lane >> 2, cl = lane & 3;
+        constexpr int RP = 32 / CHR;  // rows per pass
         for (;;) {
-            const int t0 = p.t0, t1 = p.t1;
-            const int i0 = p.qt * a.tq, ntok = min(a.tq, p.s.m - i0), rows = ntok * a.G;
-            const int kend = min(t1 * BN, p.s.L - p.s.m + i0 + ntok);
-            // ---- queries
-            const int qrows = C::QTM ? 0 : (rows > 128 ? 256 : 128);
-            if (!C::QTM) {
+            if constexpr (!C::QTM) {
+                const int i0 = p.qt * a.tq, rows = min(a.tq, p.s.m - i0) * a.G;
                 ok = warp_wait(TB_QE, (unit & 1) ^ 1);
                 if (!ok) break;
-            }
-            if constexpr (C::QTM) {
-                (void)qrows;
-            } else if constexpr (!F8) {
-                for (int idx = tl; idx < qrows * (D / 8); idx += 128) {
-                    const int r = idx / (D / 8), c = idx % (D / 8);
-                    const bool on = r < rows;
-                    const int tok = on ? r / a.G : 0;
-                    const uint16_t* src = a.q + (p.s.q0 + i0 + tok) * a.q_stride +
-                                          static_cast<long long>(p.h * a.G + (on ? r - tok * a.G : 0)) * D + c * 8;
-                    cp_async16(sb + (r >> 7) * C::QTILE + tc::sw_chunk(r & 127, c, 128), src, on);
-                }
-                push(TB_QF);
-            } else {
-                for (int r = tl; r < qrows; r += 128) {
+                for (int r = tl; r < (rows > 128 ? 256 : 128); r += 128) {
                     const bool on = r < rows;
                     const int tok = on ? r / a.G : 0;
                     const uint4* src = reinterpret_cast<const uint4*>(
@@ -356,12 +271,92 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                 tc::fence_proxy_async();
                 warp_arrive(TB_QF);
             }
+            const int items = (p.t1 - p.t0) * (C::DUAL ? 1 : 2);
+            for (int i = 0; i < items && ok; ++i) {
+                const uint32_t ring = lg * C::NRAW + slot;
+                ok = warp_wait(RAW_FULL + ring, rpar) && warp_wait(KV_EMPTY + stage, par);
+                if (!ok) break;
+                const uint32_t raw = sb + C::OFF_RAW + ring * C::RAW + (r0 + rl) * D + cl * 16;
+                const uint32_t dst = sb + C::OFF_KV + stage * C::TILE;
+                uint4 held[PER];
+#pragma unroll
+                for (int k = 0; k < PER; ++k) held[k] = lds128(raw + k * (RP * D));
+#pragma unroll
+                for (int k = 0; k < PER; ++k) {
+                    const int r = r0 + k * RP + rl;
+                    const uint4 w = held[k];
+                    sts128(dst + tc::sw_chunk(r, 2 * cl, BN), make_uint4(e4m3_lo(w.x), e4m3_hi(w.x), e4m3_lo(w.y), e4m3_hi(w.y)));
+                    sts128(dst + tc::sw_chunk(r, 2 * cl + 1, BN), make_uint4(e4m3_lo(w.z), e4m3_hi(w.z), e4m3_lo(w.w), e4m3_hi(w.w)));
+                }
+                tc::fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {
+                    tc::mbar_arrive(&bars[KV_FULL + stage]);
+                    tc::mbar_arrive(&bars[RAW_EMPTY + ring]);
+                }
+                stage += STEP;
+                if (stage >= NST) stage -= NST, par ^= 1;
+                if (++slot == C::NRAW) slot = 0, rpar ^= 1;
+            }
+            if (!ok) break;
+            ++unit;
+            if (tid == 256) leave_join(a, p, per);  // the last unit's stands
+            if (!advance<T>(a, p)) break;
+        }
+    } else if (!F8 && wg == 2) {
+        // ------------------------------------------------------------ 16 bits: loader
+        // warp w moves rows w RW .. w RW + RW - 1 of every tile; lane l holds the cache offset of one of them
+        regs_down<kRegsOther>();
+        const int tl = tid & 127, r0 = (warp & 3) * RW, mine = r0 + lane % RW;
+        // rows that lie within the keys come by TMA, in boxes of a.box rows that never straddle a page; a
+        // warp with a row past the keys (or a page size without a factor of 8) uses cp.async and zero-fills
+        const int box = a.box, boxes = box ? RW / box : 0;
+        uint32_t open = 0, stage = 0, par = 1, pend = 0, unit = 0;
+        bool ok = true;
+        if (tid == 256) leave_no_join(a);  // stands if this CTA gives up
+        auto finish = [&](uint32_t what) {  // the oldest copy group has landed
+            tc::fence_proxy_async();
+            warp_arrive(what);
+        };
+        auto push = [&](uint32_t what) {  // closes a copy group, which fills what barrier `what` stands for
+            cp_async_commit();
+            pend = pend << 8 | what;
+            if (open == LAG) {
+                cp_async_wait<LAG>();
+                finish(pend >> (8 * LAG) & 0xff);
+            } else {
+                ++open;
+            }
+        };
+        auto flush = [&]() {
+            cp_async_wait<0>();
+            for (; open > 0; --open) finish(pend >> (8 * (open - 1)) & 0xff);
+        };
+        for (;;) {
+            const int t0 = p.t0, t1 = p.t1;
+            const int i0 = p.qt * a.tq, ntok = min(a.tq, p.s.m - i0), rows = ntok * a.G;
+            const int kend = min(t1 * BN, p.s.L - p.s.m + i0 + ntok);
+            // ---- queries
+            if constexpr (!C::QTM) {
+                const int qrows = rows > 128 ? 256 : 128;
+                ok = warp_wait(TB_QE, (unit & 1) ^ 1);
+                if (!ok) break;
+                for (int idx = tl; idx < qrows * (D / 8); idx += 128) {
+                    const int r = idx / (D / 8), c = idx % (D / 8);
+                    const bool on = r < rows;
+                    const int tok = on ? r / a.G : 0;
+                    const uint16_t* src = a.q + (p.s.q0 + i0 + tok) * a.q_stride +
+                                          static_cast<long long>(p.h * a.G + (on ? r - tok * a.G : 0)) * D + c * 8;
+                    cp_async16(sb + (r >> 7) * C::QTILE + tc::sw_chunk(r & 127, c, 128), src, on);
+                }
+                push(TB_QF);
+            }
             // ---- keys and values, tile by tile
-            auto entry = [&](int t) -> long long {
+            auto entry = [&](int t) -> long long {  // a tile ahead: the page table is some hundred cycles away
                 const int pos = t * BN + mine;
                 return t < t1 && pos < kend ? page_entry(a, p.n, pos) : 0;
             };
-            long long next = entry(t0);  // a tile ahead: the page table is some hundred cycles away
+            long long next = entry(t0);
             for (int t = t0; t < t1 && ok; ++t) {
                 const int pos = t * BN + mine;
                 const long long off = pos < kend ? row_of(a, next, p.h, pos) : -1;
@@ -369,34 +364,19 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                 const bool tma = box && __all_sync(kFullMask, off >= 0);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    if (C::DUAL && kv != static_cast<int>(lg)) continue;
-                    const uint32_t stage = item % NST, ring = F8 ? item / STEP % C::NRAW : 0;
-                    uint32_t dst;  // of this warp's rows
-                    if constexpr (F8) {
-                        dst = sb + C::OFF_RAW + (lg * C::NRAW + ring) * C::RAW + (warp & 3) * (PER * 512);
-                        if (kv == 0 && lane < RW) {
-                            const uint32_t rsc = sb + C::OFF_RSC + ring * 1024 + mine * 4;
-                            cp_async4(rsc, a.ks + (off < 0 ? 0 : off), off >= 0);
-                            cp_async4(rsc + 512, a.vs + (off < 0 ? 0 : off), off >= 0);
-                        }
-                    } else {
-                        if (!warp_wait(KV_EMPTY + stage, (item / NST & 1) ^ 1)) {
-                            ok = false;
-                            break;
-                        }
-                        dst = sb + C::OFF_KV + stage * C::TILE + r0 * 128;
-                    }
+                    ok = warp_wait(KV_EMPTY + stage, par);
+                    if (!ok) break;
+                    const uint32_t dst = sb + C::OFF_KV + stage * C::TILE;
                     if (tma) {
-                        constexpr int COLS = F8 ? 1 : D / 64;  // boxes side by side
-                        uint64_t* bar = &bars[F8 ? RAW_FULL + 4 * (lg * C::NRAW + ring) + (warp & 3) : KV_FULL + stage];
+                        constexpr int COLS = D / 64;  // boxes side by side
+                        uint64_t* bar = &bars[KV_FULL + stage];
                         if (lane == 0) tc::mbar_expect_tx(bar, RW * CHR * 16);
                         __syncwarp();
                         for (int i = lane; i < (boxes * COLS + 31) / 32 * 32; i += 32) {
                             const int rb = i / COLS * box, x = i % COLS;
                             const long long ro = __shfl_sync(kFullMask, off, rb % RW);
                             if (i < boxes * COLS)
-                                tma_load_2d(F8 ? dst + rb * CHR * 16 : dst + x * (BN * 128) + rb * 128, kv ? &maps.v : &maps.k,
-                                            x * 64, static_cast<int>(ro), bar);
+                                tma_load_2d(dst + x * (BN * 128) + (r0 + rb) * 128, kv ? &maps.v : &maps.k, x * 64, static_cast<int>(ro), bar);
                         }
                     } else {
                         const uint8_t* base = static_cast<const uint8_t*>(kv ? a.vc : a.kc);
@@ -405,24 +385,17 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                             const int idx = i * 32 + lane, rl = idx / CHR, c = idx % CHR;
                             const long long ro = __shfl_sync(kFullMask, off, rl);
                             const uint8_t* src = base + (ro < 0 ? 0 : ro * (CHR * 16)) + c * 16;
-                            cp_async16(F8 ? dst + idx * 16 : dst - r0 * 128 + tc::sw_chunk(r0 + rl, c, BN), src, ro >= 0);
+                            cp_async16(dst + tc::sw_chunk(r0 + rl, c, BN), src, ro >= 0);
                         }
-                    }
-                    if constexpr (F8) {
-                        raw_tma = (raw_tma & ~(1u << ring)) | (tma ? 1u << ring : 0u);
-                        push(0);
-                    } else if (!tma) {
                         push(KV_FULL + stage);
                     }
-                    item += STEP;
-                    if (!ok) break;
+                    if (++stage == NST) stage = 0, par ^= 1;
                 }
                 // the queries, copied meanwhile, are handed over behind two tiles' copies
-                if (!F8 && !C::QTM && box && t == t0 + 1 && ok) flush();
+                if (!C::QTM && box && t == t0 + 1 && ok) flush();
             }
-            // the MMAs of this unit, which free the query tiles, need all of its keys
-            if (ok) flush();
             if (!ok) break;
+            flush();  // the MMAs of this unit, which free the query tiles, need all of its keys
             ++unit;
             if (tid == 256) leave_join(a, p, per);  // the last unit's stands
             if (!advance<T>(a, p)) break;
@@ -432,12 +405,114 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             for (int i = 0; i < 100; ++i) __nanosleep(10000);
         }
     } else if (wg == 3) {
-        // ------------------------------------------------------------ MMA issue
-        // The whole warp runs the loop, and one elected lane issues: descriptors stay warp-uniform (an MMA
-        // takes them from uniform registers; issued from a branch on the lane index, each one's operands are
-        // moved there first, which made the issue twice as long as the products).
-        regs_down<kRegsOther>();
-        if (warp == 12 && elect()) {
+        regs_down<kRegsOther>();  // by the whole warpgroup, then its warps part
+        if (F8 && (warp == 13 || (C::DUAL && warp == 14))) {
+            // ------------------------------------------------------------ 8 bits: copies into the staging ring
+            const uint32_t lg = C::DUAL && warp == 14 ? 1 : 0;
+            const int box = a.box, boxes = box ? BN / box : 0, mine = lane * box;  // lane i copies box i
+            uint32_t slot = 0, par = 1;
+            bool ok = true;
+            for (;;) {
+                const int t0 = p.t0, t1 = p.t1, i0 = p.qt * a.tq, ntok = min(a.tq, p.s.m - i0);
+                const int kend = min(t1 * BN, p.s.L - p.s.m + i0 + ntok);
+                auto entry = [&](int t) -> long long {  // a tile ahead: the page table is some hundred cycles away
+                    const int pos = t * BN + mine;
+                    return t < t1 && lane < boxes && pos < kend ? page_entry(a, p.n, pos) : 0;
+                };
+                long long next = entry(t0);
+                for (int t = t0; t < t1 && ok; ++t) {
+                    const int pos = t * BN + mine;
+                    // boxes whose rows are all keys; the ragged end's rows go one by one
+                    const long long off = lane < boxes && pos + box <= kend ? row_of(a, next, p.h, pos) : -1;
+                    next = entry(t + 1);
+                    const unsigned on = __ballot_sync(kFullMask, off >= 0);
+    #pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        if (C::DUAL && kv != static_cast<int>(lg)) continue;
+                        const uint32_t ring = lg * C::NRAW + slot, dst = sb + C::OFF_RAW + ring * C::RAW;
+                        ok = warp_wait(RAW_EMPTY + ring, par);
+                        if (!ok) break;
+                        uint64_t* bar = &bars[RAW_FULL + ring];
+                        if (off >= 0) tma_load_2d(dst + mine * D, kv ? &maps.v : &maps.k, 0, static_cast<int>(off), bar);
+                        if (__popc(on) * box < BN) {
+                            const uint8_t* base = static_cast<const uint8_t*>(kv ? a.vc : a.kc);
+                            for (int idx = lane; idx < BN * CHR; idx += 32) {
+                                const int r = idx / CHR, c = idx % CHR;
+                                if (box && (on >> (r / box) & 1)) continue;
+                                const int at = t * BN + r;
+                                const long long ro = at < kend ? row_of(a, page_entry(a, p.n, at), p.h, at) : -1;
+                                cp_async16(dst + idx * 16, base + (ro < 0 ? 0 : ro * D) + c * 16, ro >= 0);
+                            }
+                            cp_async_commit();
+                            cp_async_wait<0>();
+                        }
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_expect_tx(bar, __popc(on) * box * D);  // the slot's one arrival
+                        if (++slot == C::NRAW) slot = 0, par ^= 1;
+                    }
+                }
+                if (!ok || !advance<T>(a, p)) break;
+            }
+            if (!ok) {  // gave up: leave what TMA copies are in flight (microseconds) a millisecond
+                for (int i = 0; i < 100; ++i) __nanosleep(10000);
+            }
+        } else if (F8 && warp == 15) {
+            // ------------------------------------------------------------ 8 bits: the keys' scales, for the softmax
+            constexpr int NK = BN / 32;  // keys per lane
+            uint32_t tile = 0;
+            bool ok = true;
+            for (;;) {
+                const int t0 = p.t0, t1 = p.t1, i0 = p.qt * a.tq, ntok = min(a.tq, p.s.m - i0);
+                const int kend = min(t1 * BN, p.s.L - p.s.m + i0 + ntok);
+                long long next[NK];
+                auto entries = [&](int t) {
+    #pragma unroll
+                    for (int i = 0; i < NK; ++i) {
+                        const int pos = t * BN + i * 32 + lane;
+                        next[i] = t < t1 && pos < kend ? page_entry(a, p.n, pos) : 0;
+                    }
+                };
+                float ks[NK], vs[NK];  // 1 past the keys, where no weight is
+                auto load = [&](int t) {
+    #pragma unroll
+                    for (int i = 0; i < NK; ++i) {
+                        const int pos = t * BN + i * 32 + lane;
+                        const long long off = t < t1 && pos < kend ? row_of(a, next[i], p.h, pos) : -1;
+                        ks[i] = off < 0 ? 1.f : a.ks[off];
+                        vs[i] = off < 0 ? 1.f : a.vs[off];
+                    }
+                };
+                entries(t0);
+                load(t0);
+                entries(t0 + 1);
+                for (int t = t0; t < t1 && ok; ++t, ++tile) {
+                    float k[NK], lv[NK], iv[NK];
+    #pragma unroll
+                    for (int i = 0; i < NK; ++i) {
+                        k[i] = ks[i];
+                        lv[i] = fast_log2(vs[i]);
+                        iv[i] = fast_rcp(vs[i]);
+                    }
+                    load(t + 1);
+                    entries(t + 2);
+                    ok = warp_wait(SC_EMPTY + tile % C::SCN, (tile / C::SCN & 1) ^ 1);
+                    if (!ok) break;
+                    float* sc = reinterpret_cast<float*>(sm + C::OFF_SC) + tile % C::SCN * (3 * BN);
+    #pragma unroll
+                    for (int i = 0; i < NK; ++i) {
+                        sc[i * 32 + lane] = k[i];
+                        sc[BN + i * 32 + lane] = lv[i];
+                        sc[2 * BN + i * 32 + lane] = iv[i];
+                    }
+                    warp_arrive(SC_FULL + tile % C::SCN);
+                }
+                if (!ok || !advance<T>(a, p)) break;
+            }
+        } else if (warp == 12 && elect()) {
+            // ------------------------------------------------------------ MMA issue
+            // The whole warp runs the loop, and one elected lane issues: descriptors stay warp-uniform (an MMA
+            // takes them from uniform registers; issued from a branch on the lane index, each one's operands are
+            // moved there first, which made the issue twice as long as the products).
             constexpr uint32_t FMT = MF16 ? 0u : (1u << 7) | (1u << 10);
             constexpr uint32_t ID_S = (tc::idesc_bf16(128, BN, 0, 0, 0) & ~((1u << 7) | (1u << 10))) | FMT;
             constexpr uint32_t ID_O = (tc::idesc_bf16(128, D, 0, 1, 0) & ~((1u << 7) | (1u << 10))) | FMT;
@@ -587,7 +662,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                 const float* sc = nullptr;
                 if constexpr (F8) {
                     const uint32_t ti = tiles + tile;
-                    ok = warp_wait(TB_SC0 + ti % C::SCN, ti / C::SCN & 1);
+                    ok = warp_wait(SC_FULL + ti % C::SCN, ti / C::SCN & 1);
                     if (!ok) break;
                     sc = reinterpret_cast<const float*>(sm + C::OFF_SC) + ti % C::SCN * (3 * BN);
                 }
@@ -686,6 +761,13 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                 }
                 tc::fence_before();
                 warp_arrive(TB_P0 + b);
+                if constexpr (F8) {  // eight arrivals free a tile's scales: two of each warp where one warpgroup reads them
+                    if (lane == 0) {
+                        uint64_t* bar = &bars[SC_EMPTY + (tiles + tile) % C::SCN];
+                        tc::mbar_arrive(bar);
+                        if (!full) tc::mbar_arrive(bar);
+                    }
+                }
             }
             if (!ok) break;
             // operations of the two accumulators up to the unit's end
