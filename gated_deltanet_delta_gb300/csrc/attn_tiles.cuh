@@ -14,7 +14,8 @@
 // warpgroup, and a warp whose lane 0 issues every MMA:  S(0) S(1) | P(0)? PV(0) S(2) | P(1)? PV(1) S(3) ..
 // Operations of one issuing thread run in order, so S(s + 2) overwrites a buffer only after PV(s) has
 // read P from it.  P is handed over in two halves, so that its products begin while the second half is
-// exponentiated: the chain S, softmax, PV of a slot is what bounds long chunks.
+// exponentiated: the chain S, softmax, PV of a slot is what bounds long chunks.  D = 64 has TMEM left for
+// P besides S, so there S(s + 2) is issued as soon as S(s) has been read, and the softmax never waits for it.
 // The loader gathers rows by page: whole boxes of rows by TMA, the ragged end of the keys by cp.async with
 // zero fill (nothing stale may meet a weight of zero).  8-bit caches go through a staging ring, a part per
 // loader warp, and are widened into the tile; attn_rows.cuh says how their scales are applied.
@@ -40,13 +41,14 @@ struct TilesCfg {
     static constexpr int R = 128 * SLOTS;                  // rows per unit
     static constexpr int HALVES = D / 64;                  // 64-feature halves of an operand tile
     static constexpr bool QTM = D == 256;                  // queries in TMEM, not in shared memory
+    static constexpr bool PSEP = D == 64;                  // P in columns of its own, not over S
     static constexpr bool DUAL = F8 && D == 256;           // warpgroup 1, idle else, widens the values
     static constexpr uint32_t QTILE = 128u * D * 2, TILE = static_cast<uint32_t>(BN) * D * 2;
     static constexpr uint32_t RAW = F8 ? TILE / 2 : 0;
     // K and V tiles in shared memory.  Two widening warpgroups: 4, so that each has places of its own.
-    static constexpr int NST = F8 ? (DUAL ? 4 : 3) : (D == 64 ? 8 : (D == 128 ? 5 : 6));
-    // copy groups in flight behind the newest: at most NST - 2, as S(s + 2) needs its K tile before the V tile
-    // before it is released
+    static constexpr int NST = F8 ? (DUAL ? 4 : (PSEP ? 5 : 3)) : (D == 64 ? 8 : (D == 128 ? 5 : 6));
+    // copy groups in flight behind the newest: at most NST - 2 (PSEP: NST - 5), as S(s + 2) needs its K tile
+    // before the V tile (the two V tiles and a K tile) before it is released
     static constexpr int LAG = 3;
     // 8 bits: staging slots, one ring for all tiles or (DUAL) one for the keys' and one for the values'
     static constexpr int NRAW = F8 ? (D == 64 ? 6 : (DUAL ? 2 : 3)) : 0, RINGS = (DUAL ? 2 : 1) * NRAW;
@@ -59,13 +61,14 @@ struct TilesCfg {
     static constexpr uint32_t USED = OFF_RS + (F8 && !QTM ? 2 * R * 4 : 0);
     static constexpr uint32_t SMEM = USED + 1024;          // 1024-byte alignment
     static constexpr uint32_t TM_S = 0, TM_Q = 128, TM_O = 256, TM_SB = BN;  // TMEM columns
+    static constexpr uint32_t TM_P = PSEP ? 384 : TM_S, TM_PB = PSEP ? 64 : TM_SB;
 };
 
 // Barriers: queries full / empty, S, P (halves first), products with V done, accumulators read, (ref, l)
 // handed over / read, end; then KV_FULL and KV_EMPTY of every place and, for 8 bits, staging slots and scales
 // full / empty.
 enum : int {
-    TB_QF = 0, TB_QE, TB_S0, TB_S1, TB_P0, TB_P1, TB_H0, TB_H1, TB_OD0, TB_OD1, TB_OF0, TB_OF1, TB_MF, TB_ME, TB_DRAIN, TB_KV
+    TB_QF = 0, TB_QE, TB_S0, TB_S1, TB_P0, TB_P1, TB_H0, TB_H1, TB_R0, TB_R1, TB_OD0, TB_OD1, TB_OF0, TB_OF1, TB_MF, TB_ME, TB_DRAIN, TB_KV
 };
 
 __device__ __forceinline__ void tm_ld32(uint32_t taddr, float* v) {
@@ -180,7 +183,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
     if (warp == 12) tc::tmem_alloc(&tmem_slot, 512);
     if (tid == 0) {
         for (int i = 0; i < NBAR; ++i) {
-            const bool by_warps = i == TB_QF || (i >= TB_P0 && i <= TB_H1) || i == TB_OF0 || i == TB_OF1 || i == TB_MF ||
+            const bool by_warps = i == TB_QF || (i >= TB_P0 && i <= TB_R1) || i == TB_OF0 || i == TB_OF1 || i == TB_MF ||
                                   i == TB_ME || (i >= KV_FULL && i < KV_EMPTY) || (i >= RAW_EMPTY && i < SC_FULL);
             tc::mbar_init(&bars[i], i >= SC_EMPTY ? 8 : (by_warps ? 4 : 1));
         }
@@ -519,7 +522,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             const uint32_t tmu = tm;
             const uint64_t dq = (tc::sdesc(sb, 16, 1024)), dk = (tc::sdesc(sb + C::OFF_KV, 16, 1024));
             const uint64_t dv = (tc::sdesc(sb + C::OFF_KV, BN * 128, 1024));
-            uint32_t unit = 0, np[2] = {0, 0};
+            uint32_t unit = 0, np[2] = {0, 0}, nr[2] = {0, 0};
             uint32_t ks = 0, kp = 0, vs = 1, vp = 0;  // stage and parity of the next K tile, of the next V tile
             auto step = [](uint32_t& stage, uint32_t& parity) {
                 stage += 2;
@@ -556,6 +559,11 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                 ok = ok && issue_s(0) && (nops < 2 || issue_s(1));
                 for (int s = 0; s < nops && ok; ++s) {
                     const int b = s & 1, o = SLOTS == 2 ? b : 0;
+                    if (C::PSEP && s + 2 < nops) {  // S(s) has been read
+                        ok = one_wait(TB_R0 + b, nr[b] & 1) && issue_s(s + 2);
+                        if (!ok) break;
+                    }
+                    ++nr[b];
                     const bool fresh = SLOTS == 2 ? s < 2 : s == 0, last = !full || b;
                     ok = ((full && b) || one_wait(KV_FULL + vs, vp)) && (!fresh || one_wait(TB_OF0 + o, (unit & 1) ^ 1)) &&
                          one_wait((SLOTS == 2 ? TB_H0 : TB_P0) + b, np[b] & 1);
@@ -567,7 +575,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                         for (int k = 0; k < BN / 16; ++k) {
                             // the first half of P came first; now the rest
                             if (SLOTS == 2 && k == BN / 32 && !(ok = one_wait(TB_P0 + b, np[b] - 1 & 1))) break;
-                            tc::mma_bf16_ts(tmu + C::TM_O + o * D, tmu + C::TM_S + b * C::TM_SB + 8 * k, va + k * (2048 / 16), ID_O,
+                            tc::mma_bf16_ts(tmu + C::TM_O + o * D, tmu + C::TM_P + b * C::TM_PB + 8 * k, va + k * (2048 / 16), ID_O,
                                             !fresh || k > 0);
                         }
                         if (!ok) break;
@@ -575,7 +583,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                         if (last) tc::commit(&bars[KV_EMPTY + vs]);
                     }
                     if (last) step(vs, vp);
-                    if (s + 2 < nops) ok = issue_s(s + 2);
+                    if (!C::PSEP && s + 2 < nops) ok = issue_s(s + 2);
                 }
                 if (!ok) break;
                 ++unit;
@@ -676,6 +684,10 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
 #pragma unroll
                     for (int ch = 0; ch < BN / 32; ++ch) tm_ld32(ts + ch * 32, y + ch * 32);
                     tc::wait_ld();
+                    if constexpr (C::PSEP) {
+                        tc::fence_before();
+                        warp_arrive(TB_R0 + b);
+                    }
                     // y_j = raw_j times `times`, which is not negative
                     float times = fabsf(c);
                     if constexpr (F8) {
@@ -707,13 +719,17 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                         for (int j = 0; j < 4; ++j) m4[j] = i + 4 + j < BN ? fmaxf(fmaxf(m4[j], y[i + j]), y[i + 4 + j]) : fmaxf(m4[j], y[i + j]);
                     }
                     const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * times;
+                    if (C::PSEP && done > 0) {  // P's columns are free
+                        ok = warp_wait(TB_OD0 + o, (od[o] + done - 1) & 1);
+                        if (!ok) break;
+                    }
                     if (__any_sync(kFullMask, mx > ref + kRefSlack)) {
                         const float to = fmaxf(ref, mx);
                         const float f = to == -INFINITY ? 1.f : fast_exp2(ref - to);
                         ref = to;
                         l *= f;
                         if (done > 0) {  // what has been accumulated so far
-                            ok = warp_wait(TB_OD0 + o, (od[o] + done - 1) & 1);
+                            ok = C::PSEP || warp_wait(TB_OD0 + o, (od[o] + done - 1) & 1);
                             if (!ok) break;
 #pragma unroll 1
                             for (int ch = 0; ch < D / 16; ++ch) {
@@ -747,7 +763,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                             w[i / 2] = pack2<MF16>(x[0], x[1]);
                             w[i / 2 + 1] = pack2<MF16>(x[2], x[3]);
                         }
-                        tm_st16(ts + ch * 16, w);
+                        tm_st16(trow + C::TM_P + b * C::TM_PB + ch * 16, w);
                         if (SLOTS == 2 && ch == BN / 64 - 1) {  // half of P: its products can start
                             tc::wait_st();
                             tc::fence_before();
@@ -757,6 +773,12 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                     l += (l2[0] + l2[1]) + (l2[2] + l2[3]);
                     tc::wait_st();
                 } else if (SLOTS == 2) {
+                    if (C::PSEP) {
+                        warp_arrive(TB_R0 + b);
+                        // the barrier's phases are waited for one by one
+                        ok = done == 0 || warp_wait(TB_OD0 + o, (od[o] + done - 1) & 1);
+                        if (!ok) break;
+                    }
                     warp_arrive(TB_H0 + b);
                 }
                 tc::fence_before();
