@@ -169,10 +169,14 @@ cudaError_t launch_tiles(AttnArgs a, cudaStream_t stream) {
 
 template <int D, bool F16, bool F8>
 cudaError_t launch_any(const AttnArgs& a, int max_q, cudaStream_t stream) {
-    // One 16-row tile holds the rows that share a key head: the row kernel.  Beyond that it would read
-    // every key once per 16 rows.
-    return static_cast<long long>(std::max(max_q, 1)) * a.G <= attn::kRowsTile ? launch_rows<D, F16, F8>(a, stream)
-                                                                  : launch_tiles<D, F16, F8>(a, stream);
+    // The row kernel reads a key once per 16 rows that share it, the tile kernel once.  Measured with 32
+    // sequences of up to 8192 keys, heads of 128, row kernel and tile kernel: 16 bits, 16 rows 106 and 118 us,
+    // 24 rows 172 and 119 us; 8 bits, where the tile kernel has to widen every key tile first, 32 rows 124 and 215
+    // us, 64 rows 171 and 235 us; 8 bits and heads of 256, 16 rows 84 and 120 us, 24 rows 148 and 123 us.
+    const int most = F8 && D <= 128 ? 4 * attn::kRowsTile : attn::kRowsTile;
+    return static_cast<long long>(std::max(max_q, 1)) * a.G <= most && a.G <= attn::kRowsTile
+               ? launch_rows<D, F16, F8>(a, stream)
+               : launch_tiles<D, F16, F8>(a, stream);
 }
 
 template <int D>

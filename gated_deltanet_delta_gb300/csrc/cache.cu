@@ -6,7 +6,9 @@ namespace gdn {
 namespace {
 
 // 64 tokens per CTA keep four rows of 128 in flight per group; with few tokens there are not enough
-// CTAs that way, and 16 tokens each take more of them.
+// CTAs that way, and 16 tokens each take more of them.  Measured with 8 heads of 128, 8 bits, 64 and 16 tokens per
+// CTA: write, 1024 tokens 3.5 and 3.0 us, 4096 tokens 6.9 and 7.4 us, 16384 tokens 21.3 and 25.8 us; read, 1024
+// tokens 3.2 and 3.1 us, 4096 tokens 4.8 and 6.3 us, 16384 tokens 13.6 and 21.7 us.
 template <int D, bool F16, bool F8>
 void write(const CacheMoveArgs& a, cudaStream_t stream) {
     if (a.T >= 2048) {
