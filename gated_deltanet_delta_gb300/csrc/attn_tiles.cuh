@@ -10,15 +10,19 @@
 // D = 256: one row tile and one accumulator (256 columns), key tiles of 64 in two S buffers.
 // So operation s (s = 0, 1, ..) works in buffer s & 1 on key tile s / 2 (two row tiles) or s.
 //
-// Roles, 512 threads: two softmax warpgroups (one per buffer; thread i owns TMEM lane i, a row), a loader
-// warpgroup, and a warp whose lane 0 issues every MMA:  S(0) S(1) | P(0)? PV(0) S(2) | P(1)? PV(1) S(3) ..
+// Roles, 512 threads: warpgroups 0 and 1 are the softmax, one per buffer (D = 256: warpgroup 0 has both; thread i
+// owns TMEM lane i, a row); warpgroup 2 loads; one lane of warp 12 issues every MMA:
+//   S(0) S(1) | P(0)? PV(0) S(2) | P(1)? PV(1) S(3) ..
 // Operations of one issuing thread run in order, so S(s + 2) overwrites a buffer only after PV(s) has
 // read P from it.  P is handed over in two halves, so that its products begin while the second half is
 // exponentiated: the chain S, softmax, PV of a slot is what bounds long chunks.  D = 64 has TMEM left for
 // P besides S, so there S(s + 2) is issued as soon as S(s) has been read, and the softmax never waits for it.
 // The loader gathers rows by page: whole boxes of rows by TMA, the ragged end of the keys by cp.async with
-// zero fill (nothing stale may meet a weight of zero).  8-bit caches go through a staging ring, a part per
-// loader warp, and are widened into the tile; attn_rows.cuh says how their scales are applied.
+// zero fill (nothing stale may meet a weight of zero).
+// 8-bit caches: warp 13 (D = 256: 13 the keys, 14 the values) copies into a staging ring, warp 15 fetches the
+// scales, and warpgroup 2 (D = 256: 2 the keys, 1 the values) does nothing but widen into the tiles, 128 threads
+// on 2-clock conversions; one warpgroup that did all three took 136 us where this takes 111 (32 sequences of up to
+// 8192 keys, 64 rows, 4 x 256).  attn_rows.cuh says how the scales are applied.
 //
 // Every wait is bounded: one that runs out sets GDN_STATUS_TIMEOUT and the CTA's abort flag, on which
 // all roles leave; copies and MMAs in flight are waited for (bounded) before the CTA ends.
@@ -39,7 +43,6 @@ struct TilesCfg {
     static constexpr int BN = D == 256 ? 64 : 128;         // keys per tile
     static constexpr int SLOTS = D == 256 ? 1 : 2;         // row tiles per unit
     static constexpr int R = 128 * SLOTS;                  // rows per unit
-    static constexpr int HALVES = D / 64;                  // 64-feature halves of an operand tile
     static constexpr bool QTM = D == 256;                  // queries in TMEM, not in shared memory
     static constexpr bool PSEP = D == 64;                  // P in columns of its own, not over S
     static constexpr bool DUAL = F8 && D == 256;           // warpgroup 1, idle else, widens the values
@@ -513,9 +516,9 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             }
         } else if (warp == 12 && elect()) {
             // ------------------------------------------------------------ MMA issue
-            // The whole warp runs the loop, and one elected lane issues: descriptors stay warp-uniform (an MMA
-            // takes them from uniform registers; issued from a branch on the lane index, each one's operands are
-            // moved there first, which made the issue twice as long as the products).
+            // One elected lane (elect.sync, which the compiler knows to leave one: an MMA takes its descriptors from uniform
+            // registers, and behind a branch on the lane index each one's operands are moved there first, which made
+            // the issue twice as long as the products).
             constexpr uint32_t FMT = MF16 ? 0u : (1u << 7) | (1u << 10);
             constexpr uint32_t ID_S = (tc::idesc_bf16(128, BN, 0, 0, 0) & ~((1u << 7) | (1u << 10))) | FMT;
             constexpr uint32_t ID_O = (tc::idesc_bf16(128, D, 0, 1, 0) & ~((1u << 7) | (1u << 10))) | FMT;
@@ -579,7 +582,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                                             !fresh || k > 0);
                         }
                         if (!ok) break;
-                        tc::commit(&bars[TB_OD0 + o]);
+                        tc::commit(&bars[TB_OD0 + b]);
                         if (last) tc::commit(&bars[KV_EMPTY + vs]);
                     }
                     if (last) step(vs, vp);
@@ -664,6 +667,10 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             float ref = -INFINITY, l = 0.f;
             bool ok = true;
             int done = 0;  // this slot's operations of the unit
+            // Operation s's product with V is done.  Each buffer has a barrier, of which one phase at most is pending: S(s)
+            // was read, and the product before on this buffer came before it.  (A barrier for both could be two phases
+            // on, or none, which a wait for a parity takes for the same.)
+            auto product = [&](int s) { return warp_wait(TB_OD0 + (s & 1), ((s & 1 ? od[1] : od[0]) + (s >> 1)) & 1); };
             for (int s = SLOTS == 2 ? wg : 0; s < nops; s += SLOTS, ++done) {
                 const int b = s & 1, tile = full ? s >> 1 : s, o = SLOTS == 2 ? b : 0;
                 const uint32_t ts = trow + C::TM_S + b * C::TM_SB;
@@ -720,7 +727,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                     }
                     const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * times;
                     if (C::PSEP && done > 0) {  // P's columns are free
-                        ok = warp_wait(TB_OD0 + o, (od[o] + done - 1) & 1);
+                        ok = product(s - SLOTS);
                         if (!ok) break;
                     }
                     if (__any_sync(kFullMask, mx > ref + kRefSlack)) {
@@ -729,7 +736,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                         ref = to;
                         l *= f;
                         if (done > 0) {  // what has been accumulated so far
-                            ok = C::PSEP || warp_wait(TB_OD0 + o, (od[o] + done - 1) & 1);
+                            ok = C::PSEP || product(s - SLOTS);
                             if (!ok) break;
 #pragma unroll 1
                             for (int ch = 0; ch < D / 16; ++ch) {
@@ -776,7 +783,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                     if (C::PSEP) {
                         warp_arrive(TB_R0 + b);
                         // the barrier's phases are waited for one by one
-                        ok = done == 0 || warp_wait(TB_OD0 + o, (od[o] + done - 1) & 1);
+                        ok = done == 0 || product(s - SLOTS);
                         if (!ok) break;
                     }
                     warp_arrive(TB_H0 + b);
@@ -792,9 +799,6 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                 }
             }
             if (!ok) break;
-            // operations of the two accumulators up to the unit's end
-            od[0] += SLOTS == 2 ? (nops + 1) / 2 : nops;
-            od[1] += SLOTS == 2 ? nops / 2 : 0;
             tiles += t1 - t0;
 
             // ---- the unit's rows
@@ -821,9 +825,9 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                     ref = top;
                 }
                 const int o = SLOTS == 2 ? wg : 0;
-                // One accumulator for both buffers: the last two products may both be pending, and a barrier is
-                // waited for one phase at a time (what was read of S says that those before them are done)
-                ok = (SLOTS == 2 || warp_wait(TB_OD0, od[0] & 1)) && warp_wait(TB_OD0 + o, (od[o] - 1) & 1) && (!both || nops < 2 || warp_wait(TB_OD0 + 1, (od[1] - 1) & 1));
+                // this accumulator's last product (one accumulator: the unit's last), and the other slot's
+                auto newest = [&](int b) { return nops - 1 - ((nops - 1 ^ b) & 1); };  // the last operation in buffer b
+                ok = product(SLOTS == 2 ? newest(wg) : nops - 1) && (!both || nops < 2 || product(newest(1)));
                 if (!ok) break;
                 if (some) {
                     const bool whole = t0 == 0 && t1 == p.nk;
@@ -870,6 +874,8 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                 if (both) warp_arrive(TB_OF0 + 1);
             }
             if (both) ++nml;
+            od[0] += (nops + 1) / 2;  // operations of the buffers up to the unit's end
+            od[1] += nops / 2;
             ++unit;
             if (!advance<T>(a, p)) break;
         }
