@@ -3,8 +3,8 @@
 // Bound: the cache is read once from HBM and each key row meets at most 16 query rows, about 16
 // operations per byte, so the time is the bytes' time.  What the kernel has to do is keep enough of
 // them in flight and stay out of their way.  Hence: four independent warps per CTA, each with its own
-// ring of stages of 16 or 32 keys (no block barrier inside a unit); warp w takes keys 16 w .. 16 w + 15
-// of each 64-key tile and keeps its own reference, sum and accumulator, joined once per unit through
+// ring of stages of TK = 16 or 32 keys (no block barrier inside a unit); warp w takes keys TK w .. TK w + TK - 1
+// of each tile of 4 TK keys and keeps its own reference, sum and accumulator, joined once per unit through
 // shared memory.  The products run on mma.sync m16n8k16: its 16 rows are the whole tile, whereas a
 // tcgen05.mma would compute 128 rows for them and add a TMEM round trip per tile.
 //
@@ -14,6 +14,9 @@
 // softmax scale multiply the fp32 product.  The value's scale moves into the exponent,
 //     p'_j = 2^{y_j + log2(vs_j) - ref},   l = sum p'_j / vs_j,   acc = sum p'_j v_j,
 // so that p' fits binary16 whatever the scales' sizes are.
+//
+// Measured, one token each of 64 sequences: 16 bits, up to 8192 keys of 8 x 128, 187 us, 97 % of a copy's rate; 8
+// bits, up to 16384 keys of 4 x 128, 114 us, 81 %: there the widening's and the products' instructions take as long.
 #pragma once
 
 #include "attn.cuh"

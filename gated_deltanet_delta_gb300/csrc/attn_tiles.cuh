@@ -21,8 +21,12 @@
 // zero fill (nothing stale may meet a weight of zero).
 // 8-bit caches: warp 13 (D = 256: 13 the keys, 14 the values) copies into a staging ring, warp 15 fetches the
 // scales, and warpgroup 2 (D = 256: 2 the keys, 1 the values) does nothing but widen into the tiles, 128 threads
-// on 2-clock conversions; one warpgroup that did all three took 136 us where this takes 111 (32 sequences of up to
-// 8192 keys, 64 rows, 4 x 256).  attn_rows.cuh says how the scales are applied.
+// on 2-clock conversions; one warpgroup that did all three took 136 us where this took 111 (the windows below).
+// attn_rows.cuh says how the scales are applied.
+//
+// Measured: chunks of 4096 tokens over up to 15360 keys, two sequences, 32 / 8 heads of 128: 915 us, 1.41 PFLOP/s,
+// bound by the chain above; whole prompts of up to 4096 tokens, nine, 16 / 4 heads of 64: 267 us, bound by the
+// exponentials; windows of 8 tokens over up to 15360 8-bit keys, 32, 16 / 2 heads of 256: 117 us, bound by the softmax.
 //
 // Every wait is bounded: one that runs out sets GDN_STATUS_TIMEOUT and the CTA's abort flag, on which
 // all roles leave; copies and MMAs in flight are waited for (bounded) before the CTA ends.
@@ -603,7 +607,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
         regs_up<kRegsSoftmax>();
         const int row = tid & 127;
         const uint32_t trow = tm + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        uint32_t unit = 0, ns[2] = {0, 0}, od[2] = {0, 0}, nml = 0, tiles = 0;
+        uint32_t unit = 0, ns[2] = {0, 0}, odp = 0, nml = 0, tiles = 0;
         (void)tiles;
         for (;;) {
             const int t0 = p.t0, t1 = p.t1;
@@ -670,7 +674,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             // Operation s's product with V is done.  Each buffer has a barrier, of which one phase at most is pending: S(s)
             // was read, and the product before on this buffer came before it.  (A barrier for both could be two phases
             // on, or none, which a wait for a parity takes for the same.)
-            auto product = [&](int s) { return warp_wait(TB_OD0 + (s & 1), ((s & 1 ? od[1] : od[0]) + (s >> 1)) & 1); };
+            auto product = [&](int s) { return warp_wait(TB_OD0 + (s & 1), (odp >> (s & 1) ^ s >> 1) & 1); };
             for (int s = SLOTS == 2 ? wg : 0; s < nops; s += SLOTS, ++done) {
                 const int b = s & 1, tile = full ? s >> 1 : s, o = SLOTS == 2 ? b : 0;
                 const uint32_t ts = trow + C::TM_S + b * C::TM_SB;
@@ -874,8 +878,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                 if (both) warp_arrive(TB_OF0 + 1);
             }
             if (both) ++nml;
-            od[0] += (nops + 1) / 2;  // operations of the buffers up to the unit's end
-            od[1] += nops / 2;
+            odp ^= ((nops + 1) / 2 & 1) | (nops / 2 & 1) << 1;  // parities of the buffers' operations so far
             ++unit;
             if (!advance<T>(a, p)) break;
         }
