@@ -26,7 +26,7 @@
 //
 // Measured: chunks of 4096 tokens over up to 15360 keys, two sequences, 32 / 8 heads of 128: 915 us, 1.41 PFLOP/s,
 // bound by the chain above; whole prompts of up to 4096 tokens, nine, 16 / 4 heads of 64: 267 us, bound by the
-// exponentials; windows of 8 tokens over up to 15360 8-bit keys, 32, 16 / 2 heads of 256: 117 us, bound by the softmax.
+// exponentials; windows of 8 tokens over up to 15360 8-bit keys, 32, 16 / 2 heads of 256: 115 us, bound by the softmax.
 //
 // Every wait is bounded: one that runs out sets GDN_STATUS_TIMEOUT and the CTA's abort flag, on which
 // all roles leave; copies and MMAs in flight are waited for (bounded) before the CTA ends.
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
         for (int i = 0; i < NBAR; ++i) {
             const bool by_warps = i == TB_QF || (i >= TB_P0 && i <= TB_R1) || i == TB_OF0 || i == TB_OF1 || i == TB_MF ||
                                   i == TB_ME || (i >= KV_FULL && i < KV_EMPTY) || (i >= RAW_EMPTY && i < SC_FULL);
-            tc::mbar_init(&bars[i], i >= SC_EMPTY ? 8 : (by_warps ? 4 : 1));
+            tc::mbar_init(&bars[i], by_warps ? 4 : 1);
         }
         abort_flag = 0;
     }
@@ -531,6 +531,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             const uint64_t dv = (tc::sdesc(sb + C::OFF_KV, BN * 128, 1024));
             uint32_t unit = 0, np[2] = {0, 0}, nr[2] = {0, 0};
             uint32_t ks = 0, kp = 0, vs = 1, vp = 0;  // stage and parity of the next K tile, of the next V tile
+            uint32_t sc_in = 0, sc_out = 0;           // 8 bits: tiles whose scales have come, have been used
             auto step = [](uint32_t& stage, uint32_t& parity) {
                 stage += 2;
                 if (stage >= NST) {
@@ -555,6 +556,12 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                             if constexpr (C::QTM) tc::mma_bf16_ts(tmu + C::TM_S + b * C::TM_SB, tmu + C::TM_Q + 8 * k, ka + ((k >> 2) * (BN * 128) + (k & 3) * 32) / 16, ID_S, k > 0);
                             else tc::mma_bf16(tmu + C::TM_S + b * C::TM_SB, qa + ((k >> 2) * 16384 + (k & 3) * 32) / 16,
                                          ka + ((k >> 2) * (BN * 128) + (k & 3) * 32) / 16, ID_S, k > 0);
+                        // S stands for the tile's scales too, and P for their having been read: even a wait that is over
+                        // takes some 200 clocks, which this lane has and the softmax has not (windows: 117 -> 115 us)
+                        if (F8 && (!full || !b)) {
+                            if (!one_wait(SC_FULL + sc_in % C::SCN, sc_in / C::SCN & 1)) return false;
+                            ++sc_in;
+                        }
                         tc::commit(&bars[TB_S0 + b]);
                         if (last) tc::commit(&bars[KV_EMPTY + ks]);
                         if (!C::QTM && s == nops - 1) tc::commit(&bars[TB_QE]);
@@ -586,6 +593,10 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                                             !fresh || k > 0);
                         }
                         if (!ok) break;
+                        if (F8 && last) {
+                            tc::mbar_arrive(&bars[SC_EMPTY + sc_out % C::SCN]);
+                            ++sc_out;
+                        }
                         tc::commit(&bars[TB_OD0 + b]);
                         if (last) tc::commit(&bars[KV_EMPTY + vs]);
                     }
@@ -680,10 +691,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                 const uint32_t ts = trow + C::TM_S + b * C::TM_SB;
                 const float* sc = nullptr;
                 if constexpr (F8) {
-                    const uint32_t ti = tiles + tile;
-                    ok = warp_wait(SC_FULL + ti % C::SCN, ti / C::SCN & 1);
-                    if (!ok) break;
-                    sc = reinterpret_cast<const float*>(sm + C::OFF_SC) + ti % C::SCN * (3 * BN);
+                    sc = reinterpret_cast<const float*>(sm + C::OFF_SC) + (tiles + tile) % C::SCN * (3 * BN);
                 }
                 ok = warp_wait(TB_S0 + b, ns[b] & 1);
                 if (!ok) break;
@@ -794,13 +802,6 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                 }
                 tc::fence_before();
                 warp_arrive(TB_P0 + b);
-                if constexpr (F8) {  // eight arrivals free a tile's scales: two of each warp where one warpgroup reads them
-                    if (lane == 0) {
-                        uint64_t* bar = &bars[SC_EMPTY + (tiles + tile) % C::SCN];
-                        tc::mbar_arrive(bar);
-                        if (!full) tc::mbar_arrive(bar);
-                    }
-                }
             }
             if (!ok) break;
             tiles += t1 - t0;
