@@ -210,6 +210,21 @@ def test_same_bits_with_cold_and_warm_caches(gdn, max_q, dim, f8):
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1]), i
 
 
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_no_wait_runs_out_at_the_ends_of_units(gdn, dim, f8):
+    # many units of one to five key tiles, so that every wait at a unit's end meets early and late arrivals
+    kv = [40 + 7 * n for n in range(40)]
+    x = make(16, [min(k, 40) for k in kv], kv, 16, 4, dim, 64, torch.bfloat16, f8)
+    first = call(gdn, x, 0.06, max_q=64)
+    assert first[2] == 0
+    check(x, first[0], first[1], 0.06)
+    for i in range(100):
+        again = call(gdn, x, 0.06, max_q=64)
+        assert again[2] == 0, i
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1]), i
+
+
 @pytest.mark.parametrize("max_q", [1, 64])
 def test_many_sequences(gdn, max_q):
     # more sequences than a block has threads, most of them tiny
