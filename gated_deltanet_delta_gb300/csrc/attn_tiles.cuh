@@ -14,9 +14,10 @@
 // owns TMEM lane i, a row); warpgroup 2 loads; one lane of warp 12 issues every MMA:
 //   S(0) S(1) | P(0)? PV(0) S(2) | P(1)? PV(1) S(3) ..
 // Operations of one issuing thread run in order, so S(s + 2) overwrites a buffer only after PV(s) has
-// read P from it.  P is handed over in two halves, so that its products begin while the second half is
-// exponentiated: the chain S, softmax, PV of a slot is what bounds long chunks.  D = 64 has TMEM left for
-// P besides S, so there S(s + 2) is issued as soon as S(s) has been read, and the softmax never waits for it.
+// read P from it.  D = 128: P is handed over in two halves, so that its products begin while the second half is
+// exponentiated: the chain S, softmax, PV of a slot is what bounds long chunks.  D = 64 has TMEM left for P
+// besides S, so there S(s + 2) is issued as soon as S(s) has been read, the softmax never waits for it, and a
+// hand-over in halves only costs (prompts 264 us, without it 261).
 // The loader gathers rows by page: whole boxes of rows by TMA, the ragged end of the keys by cp.async with
 // zero fill (nothing stale may meet a weight of zero).
 // 8-bit caches: warp 13 (D = 256: 13 the keys, 14 the values) copies into a staging ring, warp 15 fetches the
@@ -25,7 +26,7 @@
 // attn_rows.cuh says how the scales are applied.
 //
 // Measured: chunks of 4096 tokens over up to 15360 keys, two sequences, 32 / 8 heads of 128: 915 us, 1.41 PFLOP/s,
-// bound by the chain above; whole prompts of up to 4096 tokens, nine, 16 / 4 heads of 64: 267 us, bound by the
+// bound by the chain above; whole prompts of up to 4096 tokens, nine, 16 / 4 heads of 64: 261 us, bound by the
 // exponentials; windows of 8 tokens over up to 15360 8-bit keys, 32, 16 / 2 heads of 256: 115 us, bound by the softmax.
 //
 // Every wait is bounded: one that runs out sets GDN_STATUS_TIMEOUT and the CTA's abort flag, on which
@@ -49,6 +50,7 @@ struct TilesCfg {
     static constexpr int R = 128 * SLOTS;                  // rows per unit
     static constexpr bool QTM = D == 256;                  // queries in TMEM, not in shared memory
     static constexpr bool PSEP = D == 64;                  // P in columns of its own, not over S
+    static constexpr bool HALF = SLOTS == 2 && !PSEP;      // P handed over in halves
     static constexpr bool DUAL = F8 && D == 256;           // warpgroup 1, idle else, widens the values
     static constexpr uint32_t QTILE = 128u * D * 2, TILE = static_cast<uint32_t>(BN) * D * 2;
     static constexpr uint32_t RAW = F8 ? TILE / 2 : 0;
@@ -580,7 +582,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                     ++nr[b];
                     const bool fresh = SLOTS == 2 ? s < 2 : s == 0, last = !full || b;
                     ok = ((full && b) || one_wait(KV_FULL + vs, vp)) && (!fresh || one_wait(TB_OF0 + o, (unit & 1) ^ 1)) &&
-                         one_wait((SLOTS == 2 ? TB_H0 : TB_P0) + b, np[b] & 1);
+                         one_wait((C::HALF ? TB_H0 : TB_P0) + b, np[b] & 1);
                     if (!ok) break;
                     ++np[b];
                     const uint64_t va = dv + vs * (C::TILE >> 4);
@@ -588,7 +590,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
 #pragma unroll
                         for (int k = 0; k < BN / 16; ++k) {
                             // the first half of P came first; now the rest
-                            if (SLOTS == 2 && k == BN / 32 && !(ok = one_wait(TB_P0 + b, np[b] - 1 & 1))) break;
+                            if (C::HALF && k == BN / 32 && !(ok = one_wait(TB_P0 + b, np[b] - 1 & 1))) break;
                             tc::mma_bf16_ts(tmu + C::TM_O + o * D, tmu + C::TM_P + b * C::TM_PB + 8 * k, va + k * (2048 / 16), ID_O,
                                             !fresh || k > 0);
                         }
@@ -783,7 +785,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                             w[i / 2 + 1] = pack2<MF16>(x[2], x[3]);
                         }
                         tm_st16(trow + C::TM_P + b * C::TM_PB + ch * 16, w);
-                        if (SLOTS == 2 && ch == BN / 64 - 1) {  // half of P: its products can start
+                        if (C::HALF && ch == BN / 64 - 1) {  // half of P: its products can start
                             tc::wait_st();
                             tc::fence_before();
                             warp_arrive(TB_H0 + b);
@@ -798,7 +800,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                         ok = done == 0 || product(s - SLOTS);
                         if (!ok) break;
                     }
-                    warp_arrive(TB_H0 + b);
+                    if (C::HALF) warp_arrive(TB_H0 + b);
                 }
                 tc::fence_before();
                 warp_arrive(TB_P0 + b);
