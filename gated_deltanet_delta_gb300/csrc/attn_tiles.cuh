@@ -403,8 +403,10 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                     }
                     if (++stage == NST) stage = 0, par ^= 1;
                 }
-                // the queries, copied meanwhile, are handed over behind two tiles' copies
-                if (!C::QTM && box && t == t0 + 1 && ok) flush();
+                // The queries, copied meanwhile, are handed over behind two tiles' copies.  A tile that went by
+                // cp.async is handed over at once: the next ones may go by TMA, push nothing, and wait for places that only
+                // this tile's products free (a page outside the cache, amid good ones).
+                if (box && ok && (!tma || (!C::QTM && t == t0 + 1))) flush();
             }
             if (!ok) break;
             flush();  // the MMAs of this unit, which free the query tiles, need all of its keys
