@@ -194,7 +194,8 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
         for (int i = 0; i < NBAR; ++i) {
             const bool by_warps = i == TB_QF || (i >= TB_P0 && i <= TB_R1) || i == TB_OF0 || i == TB_OF1 || i == TB_MF ||
                                   i == TB_ME || (i >= KV_FULL && i < KV_EMPTY) || (i >= RAW_EMPTY && i < SC_FULL);
-            tc::mbar_init(&bars[i], by_warps ? 4 : 1);
+            // TB_QE, 8 bits: the last product with the queries, and each softmax warp that has read its rows' scales
+            tc::mbar_init(&bars[i], i == TB_QE && F8 && !C::QTM ? 1 + 4 * SLOTS : (by_warps ? 4 : 1));
         }
         abort_flag = 0;
     }
@@ -682,6 +683,10 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             } else if constexpr (F8) {
                 if (!warp_wait(TB_QF, unit & 1)) break;
                 c = reinterpret_cast<const float*>(sm + C::OFF_RS)[(unit & 1) * C::R + r];
+                // The next queries wait for this: a unit of one or two operations has all its products with Q done without
+                // the softmax, which could still be in the unit before, and its wait above meet the phase after the one it
+                // means (the same parity as the phase before).
+                warp_arrive(TB_QE);
             }
             float ref = -INFINITY, l = 0.f;
             bool ok = true;

@@ -120,3 +120,19 @@ def test_a_bad_page_amid_a_sequence(gdn, dim, f8):
         out, lse, status = call(gdn, dict(x, table=t), 0.07)
         assert status == gdn.STATUS_BAD_CACHE_INDEX, (seed, status)
         assert torch.equal(out[others], good[others]) and torch.equal(lse[others], glse[others]), seed
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_many_short_prompts(gdn, dim, f8):
+    # some forty units per CTA, of one to four key tiles and of few or many rows, so that a unit's roles are in
+    # step with those of the units before and behind it, or out of step as far as the barriers let them
+    kv = [20 + (53 * n) % 231 for n in range(1500)]
+    x = make(22, kv, kv, 8, 2, dim, 32, torch.bfloat16, f8)
+    first = call(gdn, x, 0.08)
+    assert first[2] == 0
+    check(x, first[0], first[1], 0.08, range(0, 1500, 31))
+    for i in range(40):
+        again = call(gdn, x, 0.08)
+        assert again[2] == 0, i
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1]), i
