@@ -129,3 +129,25 @@ def test_refusals(gdn):
         big = torch.zeros((1, 1, (1 << 20) + 1), device="cuda")
         gdn.draft_verify(big, torch.empty((1, 0, (1 << 20) + 1), device="cuda"), torch.empty((1, 0), dtype=torch.int64, device="cuda"),
                          torch.empty((1, 0), device="cuda"), us[:1].contiguous())
+
+
+@pytest.mark.parametrize("N,V", [(76, 16384), (600, 8192), (3000, 4096), (4001, 900)])
+def test_short_rows_of_many_clusters(gdn, N, V):
+    # clusters of 8, 4, 2 CTAs and single ones with the least work per CTA, in many waves: a CTA's sum reaches
+    # another soon after, or before, that one has begun
+    g = torch.Generator(device="cuda").manual_seed(N)
+    p = torch.softmax(2 * torch.randn((N, 2, V), generator=g, device="cuda"), -1)
+    q = torch.softmax(2 * torch.randn((N, 1, V), generator=g, device="cuda"), -1)
+    x = torch.randint(V, (N, 1), generator=g, device="cuda")
+    u, us = torch.rand((N, 1), generator=g, device="cuda"), torch.rand(N, generator=g, device="cuda")
+    stands = u[:, 0] * q[:, 0].gather(1, x)[:, 0] < p[:, 0].gather(1, x)[:, 0]
+    row = torch.where(stands[:, None], p[:, 1], p[:, 0])
+    whole = (row.double() * 2.0 ** 36).long()
+    units = torch.where(stands[:, None], whole, (whole - (q[:, 0].double() * 2.0 ** 36).long()).clamp(min=0))
+    mark = units.sum(1) * (us.double() * 2 ** 24).long() >> 24
+    token = (units.cumsum(1) <= mark[:, None]).sum(1)
+    for i in range(20):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        accepted, tokens = gdn.draft_verify(p, q, x, u, us, dev_status=status)
+        assert status.item() == 0 and torch.equal(accepted, stands.long()), i
+        assert torch.equal(tokens.gather(1, stands.long()[:, None])[:, 0], token), i
