@@ -30,7 +30,7 @@ ABI_SYMBOLS = ("gdn_decode_step", "gdn_decode_multi", "gdn_decode_step_pooled", 
                "gdn_prefill_workspace_size",
                "gdn_prefill_chunked", "gdn_prefill_chunked_f16", "gdn_prefill_chunked_noalloc",
                "comba_prefill_chunked", "gdn_window_fused", "gdn_prefill_set_wait_limit",
-               "attn_cache_write", "attn_cache_read", "attn_paged_workspace_size", "attn_paged", "draft_verify",
+               "attn_cache_write", "attn_cache_read", "attn_paged_workspace_size", "attn_paged", "attn_set_wait_limit", "draft_verify",
                "gdn_status_string", "gdn_last_error")
 
 
@@ -96,6 +96,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.attn_paged.argtypes = [P, I64, I, P, P, P, P, I, I64, I, P, I, P, P, I, I64, I64, I, I, I, F, P, P, P, SZ,
                                    P, P]
         lib.attn_paged.restype = I
+        lib.attn_set_wait_limit.argtypes = [ctypes.c_uint32]
+        lib.attn_set_wait_limit.restype = None
         lib.draft_verify.argtypes = [P, P, P, P, P, P, I, I, I, P, P, P, P]
         lib.draft_verify.restype = I
         lib.gdn_status_string.argtypes = [I]
@@ -110,6 +112,12 @@ def set_prefill_wait_limit(polls: int) -> None:
     """Bound every device-side wait of the prefill kernels to `polls` mbarrier polls (0: the
     built-in limits).  A wait that runs out sets STATUS_TIMEOUT in the call's dev_status."""
     load().gdn_prefill_set_wait_limit(int(polls))
+
+
+def set_attn_wait_limit(polls: int) -> None:
+    """Bound every device-side wait of attn_paged's kernels to `polls` barrier polls (0: the built-in
+    limit).  A wait that runs out sets STATUS_TIMEOUT in the call's dev_status."""
+    load().attn_set_wait_limit(int(polls))
 
 
 def last_error() -> str:

@@ -585,6 +585,12 @@ extern "C" gdn_status gdn_prefill_chunked_noalloc(const void* q, const void* k, 
 
 // ------------------------------------------------------------------------------------------------
 // the paged attention cache, attention over it, and draft verification
+namespace {
+std::atomic<uint32_t> g_attn_wait_polls{0};  // attn_set_wait_limit
+}  // namespace
+
+extern "C" void attn_set_wait_limit(uint32_t polls) { g_attn_wait_polls.store(polls, std::memory_order_relaxed); }
+
 static bool attn_dim_ok(int D) { return D == 64 || D == 128 || D == 256; }
 
 // What attn_cache_write, attn_cache_read and attn_paged ask of their cache.
@@ -765,6 +771,7 @@ extern "C" gdn_status attn_paged(const void* q, int64_t q_stride, gdn_dtype dtyp
     while ((1LL << sh) < page_size) ++sh;
     a.page_mul = static_cast<uint32_t>(((1ULL << (31 + sh)) + page_size - 1) / page_size);
     a.page_shift = 31 + sh;
+    a.polls = g_attn_wait_polls.load(std::memory_order_relaxed);
     const cudaError_t e =
         gdn::launch_attn(a, workspace, D, cache_dtype == GDN_E4M3, static_cast<int>(max_q < T ? max_q : T), static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));

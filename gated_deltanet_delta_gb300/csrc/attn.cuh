@@ -31,6 +31,7 @@ namespace gdn {
 namespace attn {
 
 constexpr float kRefSlack = 8.f;
+constexpr uint32_t kWaitPolls = 1u << 22;  // the built-in limit of a wait (seconds), and that of the waits after one gave up
 constexpr float kLn2 = 0.69314718055994530942f;
 
 struct Seq {

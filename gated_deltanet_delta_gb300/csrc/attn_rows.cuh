@@ -28,7 +28,6 @@ namespace attn {
 
 constexpr int kRowsTile = 16;   // rows per query tile
 constexpr int kRowsNT = 128;
-constexpr uint32_t kRowsWait = 1u << 22;  // polls before a wait gives up (seconds)
 
 template <int D, bool F8>
 struct RowsCfg {
@@ -224,7 +223,7 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
             const int st = s % NS, base = first + s * BN;
             const uint32_t kst = ring_a + st * C::STAGE, vst = kst + TK * C::ROWB, sst = scale_a + st * C::SCALE;
             if (tma) {
-                if (!tc::mbar_wait(&full[warp][st], phase >> st & 1, kRowsWait)) {
+                if (!tc::mbar_wait(&full[warp][st], phase >> st & 1, a.polls)) {
                     atomicOr(a.status, kStatusTimeout);
                     gave_up = true;
                 }
@@ -240,6 +239,9 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
             }
             if (__any_sync(kFullMask, gave_up)) {
                 gave_up = true;
+                // this step's copies and the next ones' are in flight: they land before the warp goes on
+                for (int k = s; k < min(s + NS - 1, steps); ++k)
+                    tc::mbar_wait(&full[warp][k % NS], (phase >> k % NS & 1) ^ (k == s), kWaitPolls);
                 break;
             }
             __syncwarp();  // all lanes' copies and zeros are in place, and the previous step has read its stage
@@ -443,9 +445,6 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
         if (!advance<RowsTiling>(a, p)) break;
         tc::fence_proxy_async();
         __syncthreads();  // the rings are written again
-    }
-    if (gave_up) {  // leave the copies in flight (microseconds) a millisecond
-        for (int i = 0; i < 100; ++i) __nanosleep(10000);
     }
 }
 

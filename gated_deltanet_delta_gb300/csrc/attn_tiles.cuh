@@ -41,7 +41,6 @@ namespace gdn {
 namespace attn {
 
 constexpr int kTilesNT = 512;
-constexpr uint32_t kTilesWait = 1u << 22;  // polls before a wait gives up (seconds)
 
 template <int D, bool F8>
 struct TilesCfg {
@@ -205,7 +204,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
     const uint32_t tm = tmem_slot;
 
     auto wait = [&](int i, uint32_t parity) -> bool {
-        if (tc::mbar_wait_or_abort(&bars[i], parity, kTilesWait, &abort_flag)) return true;
+        if (tc::mbar_wait_or_abort(&bars[i], parity, a.polls, &abort_flag)) return true;
         abort_flag = 1;
         return false;
     };
@@ -615,7 +614,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             // nothing of this CTA's may be in flight when it ends, its barriers' arrivals included
             {
                 tc::commit(&bars[TB_DRAIN]);
-                tc::mbar_wait(&bars[TB_DRAIN], 0, kTilesWait);
+                tc::mbar_wait(&bars[TB_DRAIN], 0, kWaitPolls);
             }
         }
     } else if (wg < SLOTS) {

@@ -204,6 +204,7 @@ struct AttnArgs {
     uint32_t page_mul;   // division by page_size
     int page_shift;
     int box;             // rows per TMA box, a divisor of page_size; 0: no TMA
+    uint32_t polls;      // of a barrier, before a wait gives up
 };
 
 // The caches as rows of D elements.

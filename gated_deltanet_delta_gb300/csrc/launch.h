@@ -43,6 +43,7 @@ cudaError_t launch_prefill(const PrefillArgs& a, void* workspace, size_t workspa
 // Attention over a paged cache.  D in {64, 128, 256}; f8: the caches hold e4m3 values with scales.
 // max_q (the longest chunk) only chooses the kernel.
 size_t attn_workspace_bytes(int D);
+// a.polls: 0 for the built-in limit.
 cudaError_t launch_attn(const AttnArgs& a, void* workspace, int D, bool f8, int max_q, cudaStream_t stream);
 // Rows into and out of a paged cache.  f16: the dense side is binary16 (else bf16).
 void launch_cache_write(const CacheMoveArgs& a, int D, bool f16, bool f8, cudaStream_t stream);

@@ -456,6 +456,15 @@ gdn_status attn_paged(const void* q, int64_t q_stride, gdn_dtype dtype, const vo
                       int32_t* dev_status, gdn_stream_t stream);
 
 /*
+ * attn_set_wait_limit -- bound every device-side wait of attn_paged's kernels to `polls` polls of its
+ * barrier instead of the built-in limit (seconds), as gdn_prefill_set_wait_limit does for the prefill: a
+ * wait that runs out sets GDN_STATUS_TIMEOUT, its CTA lets the copies and products it has in flight end
+ * (bounded) and stops, and the call's rows hold no meaningful value.  0 restores the built-in limit.
+ * Process-wide; it applies to calls launched after it returns.
+ */
+void attn_set_wait_limit(uint32_t polls);
+
+/*
  * draft_verify -- verification of drafted tokens by rejection sampling, from given random numbers.
  * Drafted token t of sequence n is accepted while u_accept * draft_p[x] < target_p[x] (x the token, rows
  * t).  At the first rejection r the next token is drawn from max(target_p[r] - draft_p[r], 0); with all T

@@ -123,3 +123,9 @@ def test_draft_verify_refuses(lib, kw, want, word):
 
 def test_draft_verify_without_work(lib):
     assert verify(lib, N=0, p=N) == OK
+
+
+def test_attn_wait_limit_is_a_host_setting(lib):
+    gdn.set_attn_wait_limit(1)
+    lib.attn_set_wait_limit(ctypes.c_uint32(0xFFFFFFFF))
+    gdn.set_attn_wait_limit(0)
