@@ -44,7 +44,7 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int n, bool* bad) {
     const long long b = a.cu[n], e = a.cu[n + 1], L = a.kv_lens[n];
     Seq s;
     s.q0 = b;
-    *bad = b < 0 || e < b || e > a.T || L < 0 || L > static_cast<long long>(a.max_pages) * a.page_size;
+    *bad = b < 0 || e < b || e > a.T || L < 0 || L > a.max_keys;
     s.m = *bad ? 0 : static_cast<int>(e - b);
     s.L = *bad ? 0 : static_cast<int>(L);
     return s;

@@ -172,6 +172,9 @@ constexpr int kWinMaxTok = 8;
 constexpr int kStatusBadCacheIndex = 1, kStatusBadSeqlens = 2, kStatusTimeout = 4, kStatusBadProbs = 8,
               kStatusBadToken = 16;
 
+// Keys of a sequence, and a few tiles more (positions are looked at up to three tiles ahead), count in 32 bits.
+constexpr int kAttnMaxKeys = 0x7fffffff - 1023;
+
 struct AttnJoin {  // see attn.cuh
     int parts, rows, h, pad;
     long long token;
@@ -196,6 +199,7 @@ struct AttnArgs {
     int32_t* status;
     long long T, num_pages;
     int page_size, max_pages, num_seqs;
+    int max_keys;        // the most that a sequence may have: what its page table holds, at most kAttnMaxKeys
     int Hq, Hkv, G;      // G = Hq / Hkv
     int tq;              // tokens per query tile
     int ov, min_per;     // a unit's fixed cost; the least cost per CTA (attn.cuh)

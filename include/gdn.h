@@ -446,7 +446,7 @@ size_t attn_paged_workspace_size(int D);
  * queries fit exactly), weights are rounded to that type for the second product; scores, sums and
  * outputs accumulate in f32.  Results do not depend on timing.
  * Supported: D in {64, 128, 256}, Hq % Hkv == 0, Hq / Hkv <= 128, cache_dtype dtype or GDN_E4M3,
- * max_pages * page_size < 2^31, T < 2^30.
+ * max_pages * page_size < 2^31, T < 2^30; a length of more than 2^31 - 1024 is malformed.
  */
 gdn_status attn_paged(const void* q, int64_t q_stride, gdn_dtype dtype, const void* k_cache, const void* v_cache,
                       const float* k_scale, const float* v_scale, gdn_dtype cache_dtype, int64_t num_pages,
