@@ -10,9 +10,11 @@
 // Quantisation (cache type e4m3): per row, scale = the least power of two s with max |x| <= 448 s, and
 // the value e4m3(x / s), to nearest, ties to even.  A power of two, because a floating-point type loses
 // nothing by it (its relative step is the same at every scale), x / s and value * s are exact, and the
-// dequantised value is itself a bf16 (or binary16) number: reading back rounds nothing.  s is at least
-// 2^-100.  A row of zeros gets scale 1.  Elements that are not finite become e4m3's NaN and do not
-// count for the scale.
+// dequantised value is itself a bf16 (or binary16) number: reading back rounds nothing.  At the source type's
+// largest scale (kTop) rounding up to the value 256 would leave the type (256 kTop is its first power of two past the
+// largest number), so there such elements take 240, the value below: within a sixteenth, e4m3's relative error
+// elsewhere too.  s is at least 2^-100.  A row of zeros gets scale 1.  Elements that are not finite become e4m3's
+// NaN and do not count for the scale.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -103,6 +105,12 @@ __global__ void __launch_bounds__(kThreads) attn_cache_write_kernel(const __grid
             const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] *= inv;
+            constexpr int kTop = F16 ? 8 : 120;  // 2^kTop: the scale of a row that reaches past 7/8 of the type's range
+            if (e == kTop) {                     // its elements are below 256
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (fabsf(f[j]) > 240.f && fabsf(f[j]) < INFINITY) f[j] = copysignf(240.f, f[j]);
+            }
             q.x = to_e4m3x2(f[0], f[1]) | to_e4m3x2(f[2], f[3]) << 16;
             q.y = to_e4m3x2(f[4], f[5]) | to_e4m3x2(f[6], f[7]) << 16;
         }

@@ -389,8 +389,10 @@ void gdn_prefill_set_wait_limit(uint32_t polls);
  *              out; distinct (of two tokens with one slot either may stay)
  *   cache_dtype  dtype (rows are copied), or GDN_E4M3: per (token, head) row the scale is the least power
  *              of two s >= 2^-100 with max |x| <= 448 s (1 for a row of zeros) and the stored value
- *              e4m3(x / s), to nearest even.  x / s is exact, and so is value * s in bf16.  Elements that
- *              are not finite are stored as NaN and do not count for the scale.
+ *              e4m3(x / s), to nearest even; but in rows at the top of dtype's range (s = 2^8 for binary16, 2^120
+ *              for bf16) a value that would round to 256, and 256 s past the range, is 240.  x / s is exact, and
+ *              value * s is a finite number of dtype.  Elements that are not finite are stored as NaN and do not
+ *              count for the scale.
  * The sources must not overlap the cache.  Supported: D in {64, 128, 256}, Hkv <= 65535.
  */
 gdn_status attn_cache_write(const void* k, const void* v, int64_t k_stride, int64_t v_stride, gdn_dtype dtype,

@@ -156,3 +156,41 @@ def test_no_tokens_and_refusals(gdn):
         gdn.attn_cache_write(torch.ones((3, 2, 96), dtype=torch.bfloat16, device="cuda"),
                              torch.ones((3, 2, 96), dtype=torch.bfloat16, device="cuda"), s,
                              *(torch.zeros((4, 2, 8, 96), dtype=torch.bfloat16, device="cuda") for _ in range(2)))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_rows_at_the_top_of_the_range(gdn, dtype):
+    # 256 times the largest scale is past the type's range: what would round to it becomes 240 times it, and what
+    # comes back, and what is computed with it, is finite
+    big = torch.finfo(dtype).max
+    s = 2.0 ** (8 if dtype == torch.float16 else 120)
+    f = torch.tensor([255.0, 248.0, 247.0, 240.0, 232.0, 225.0, 224.5, 224.0]) * s
+    x = torch.randn((16, 2, 64), generator=torch.Generator().manual_seed(9)) * 8 * s
+    x = x.clamp(-0.5 * big, 0.5 * big)
+    for i in range(8):
+        x[i, 0, 3], x[8 + i, 1, 5] = f[i], -f[i]
+    x[0, 1, 7], x[1, 1, 7], x[2, 1, 7], x[3, 1, 7] = big, -big, float("inf"), float("nan")
+    x[2, 1, 8] = big
+    x = x.to(dtype)
+    kc, vc = (torch.zeros((2, 2, 8, 64), device="cuda").to(F8) for _ in range(2))
+    ks, vs = (torch.ones((2, 2, 8), device="cuda") for _ in range(2))
+    gdn.attn_cache_write(x.cuda(), x.cuda(), torch.arange(16).cuda(), kc, vc, ks, vs)
+    val, sc = ar.quantise(x.double().numpy())       # to nearest, and at the top scale 240 in the place of 256
+    val = np.where((sc[..., None] == s) & (np.abs(val) == 256), np.sign(val) * 240, val)
+    want = torch.from_numpy(val * sc[..., None]).float()
+    assert int((torch.from_numpy(sc) == s).sum()) >= 10
+    table, cu = torch.tensor([[0, 1]]).cuda(), torch.tensor([0, 16]).cuda()
+    k, v = gdn.attn_cache_read(kc, vc, table, cu, 16, dtype=dtype, k_scale=ks, v_scale=vs)
+    assert same(k.float().cpu(), want) and same(v.float().cpu(), want)
+    assert bool(torch.isfinite(k)[x.cuda().isfinite()].all())
+    assert float(((k.double().cpu() - x.double()).abs() / x.double().abs().clamp(min=s))[x.isfinite()].max()) <= 2.0 ** -4
+    # a token whose one key is such a row: the output is that row
+    for t in (0, 1, 5):
+        one = torch.tensor([[0]]).cuda()
+        kc1, vc1 = (c.view(torch.uint8)[:, :, t:t + 1].contiguous().view(F8) for c in (kc, vc))
+        ks1, vs1 = (c[:, :, t:t + 1].contiguous() for c in (ks, vs))
+        q = torch.zeros((40, 2, 64), dtype=dtype, device="cuda")
+        for T in (1, 40):
+            lens, n = torch.ones(T, dtype=torch.int64).cuda(), torch.arange(T + 1).cuda()
+            out = gdn.attn_paged(q[:T], kc1, vc1, one.expand(T, 1).contiguous(), lens, n, 1, k_scale=ks1, v_scale=vs1)
+            assert torch.equal(out.float().cpu(), want[t].expand(T, 2, 64)), (t, T)
