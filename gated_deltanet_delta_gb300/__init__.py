@@ -173,6 +173,14 @@ def _want(t, name: str, dtype, shape=None):
     return t
 
 
+def _want_workspace(t, size: int, device):
+    """The caller's workspace (the library checks its size), or a new one of `size` bytes."""
+    torch = _torch_module or _torch()
+    if t is None:
+        return torch.empty(size, dtype=torch.uint8, device=device)
+    return _want(t, "workspace", t.dtype if isinstance(t, torch.Tensor) else None)
+
+
 def _out_code(dtype) -> int:
     torch = _torch()
     if dtype == torch.bfloat16:
@@ -351,13 +359,12 @@ def gdn_prefill_chunked(q, k, v, a, b, A_log, dt_bias, state_pool, cache_indices
         out = torch.empty((T, Hv, V), dtype=dt, device=q.device)
     _want(out, "out", dt, (T, Hv, V))
     ws_bytes = gdn_prefill_workspace_size(N, T, Hk, Hv, K, V, chunk_size)
-    if workspace is None and ws_bytes > 0:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+    workspace = _want_workspace(workspace, ws_bytes, q.device)
     if dev_status is None:
         dev_status = torch.zeros(1, dtype=torch.int32, device=q.device)
     _want(dev_status, "dev_status", torch.int32, (1,))
     scale = K ** -0.5 if scale is None else float(scale)
-    wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    wsz = workspace.numel() * workspace.element_size()
     name = "gdn_prefill_chunked_f16" if dt == torch.float16 else "gdn_prefill_chunked"
     _check(getattr(load(), name)(_ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(b), _ptr(A_log),
                                  _ptr(dt_bias), _ptr(state_pool), state_pool.shape[0],
@@ -393,13 +400,12 @@ def comba_prefill_chunked(q, k, v, p, beta, g, state_pool, cache_indices, cu_seq
         out = torch.empty((T, H, V), dtype=bf, device=q.device)
     _want(out, "out", bf, (T, H, V))
     ws_bytes = gdn_prefill_workspace_size(N, T, H, H, K, V, chunk_size)
-    if workspace is None and ws_bytes > 0:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+    workspace = _want_workspace(workspace, ws_bytes, q.device)
     if dev_status is None:
         dev_status = torch.zeros(1, dtype=torch.int32, device=q.device)
     _want(dev_status, "dev_status", torch.int32, (1,))
     scale = K ** -0.5 if scale is None else float(scale)
-    wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    wsz = workspace.numel() * workspace.element_size()
     _check(load().comba_prefill_chunked(_ptr(q), _ptr(k), _ptr(v), _ptr(p), _ptr(beta), _ptr(g), _ptr(state_pool),
                                         state_pool.shape[0], _ptr(cache_indices), _ptr(cu_seqlens), N, T, H, K, V,
                                         int(chunk_size), scale, _ptr(out), _ptr(workspace), wsz, _ptr(dev_status),
@@ -624,8 +630,7 @@ def attn_paged(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens, max_q: int,
         _want(out, "out", dtype, rows)
     if lse is not None:
         _want(lse, "lse", torch.float32, (T, Hq))
-    if workspace is None:
-        workspace = torch.empty(attn_paged_workspace_size(D), dtype=torch.uint8, device=device)
+    workspace = _want_workspace(workspace, attn_paged_workspace_size(D) if workspace is None else 0, device)
     dev_status = _want_status(dev_status, device)
     _check(load().attn_paged(q.data_ptr(), q_stride, code, k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
                              _ptr(v_scale), cache, pages, page_size, page_table.data_ptr(), table[1],

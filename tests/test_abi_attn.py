@@ -129,3 +129,13 @@ def test_attn_wait_limit_is_a_host_setting(lib):
     gdn.set_attn_wait_limit(1)
     lib.attn_set_wait_limit(ctypes.c_uint32(0xFFFFFFFF))
     gdn.set_attn_wait_limit(0)
+
+
+def test_a_workspace_off_the_device_is_refused():
+    # its address would be written to by the kernels
+    torch = pytest.importorskip("torch")
+    with pytest.raises(ValueError, match="workspace must be a CUDA tensor"):
+        gdn._want_workspace(torch.empty(64, dtype=torch.uint8), 64, "cpu")
+    with pytest.raises(TypeError, match="workspace"):
+        gdn._want_workspace(bytes(64), 64, "cpu")
+    assert gdn._want_workspace(None, 64, "cpu").nbytes == 64 and gdn._want_workspace(None, 0, "cpu").nbytes == 0

@@ -298,3 +298,17 @@ def test_refusals(gdn):
         gdn.attn_paged(c["q"][:, :3].contiguous(), c["k"], c["v"], c["table"], kv, cu, 1, **sc)
     with pytest.raises(gdn.GdnError):  # workspace too small
         gdn.attn_paged(c["q"], c["k"], c["v"], c["table"], kv, cu, 1, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"), **sc)
+
+
+def test_workspace_refusals(gdn):
+    x = make(17, [1], [8], 4, 2, 64, 16, torch.bfloat16, False)
+    size = gdn.attn_paged_workspace_size(64)
+    for ws, err in ((torch.empty(size, dtype=torch.uint8), ValueError), (torch.empty(2 * size, dtype=torch.uint8, device="cuda")[::2], ValueError),
+                    (0, TypeError)):
+        with pytest.raises(err, match="workspace"):
+            call(gdn, x, 1.0, workspace=ws)
+    # any element type will do; without a workspace, an unsupported head width is still the library's to refuse
+    a, b = call(gdn, x, 1.0), call(gdn, x, 1.0, workspace=torch.empty(size // 4, device="cuda"))
+    assert torch.equal(a[0], b[0])
+    with pytest.raises(gdn.GdnError, match="64, 128 or 256"):
+        call(gdn, make(18, [1], [8], 4, 2, 96, 16, torch.bfloat16, False), 1.0)
