@@ -6,9 +6,13 @@
 // head hq reads key head hq / G, G = Hq / Hkv:
 //     s_j = scale q.k_j,   o = sum_j e^{s_j} v_j / sum_j e^{s_j},   lse = ln sum_j e^{s_j}.
 // All kernels make one pass over the keys with a running maximum, in base 2: y_j = s_j log2(e),
-// p_j = 2^{y_j - ref}, l = sum p_j and acc = sum p_j v_j in fp32.  ref follows the running maximum only
-// when that is more than kRefSlack above it, so p_j <= 2^kRefSlack and the accumulators are rescaled
-// a few times per row instead of at every tile; any ref gives the same quotient.
+// p_j = 2^{y_j - ref + kLift}, l = 2^-kLift sum p_j and acc = sum p_j v_j in fp32.  ref follows the running
+// maximum only when that is more than kRefSlack above it, so p_j <= 2^(kRefSlack + kLift) and the accumulators are
+// rescaled a few times per row instead of at every tile; any ref gives the same quotient.  p_j is rounded to the
+// operands' type for the product with v_j.  In binary16 what is below 2^-25 becomes 0, and would count in l but not in
+// acc: without the lift 2^17 keys of 2^-26 of the largest weight were missing from the output.  kLift puts p_j at the
+// top of binary16's range (at most 2^15), so that only weights below 2^-32 of the largest are lost; n of them are n 2^-32 of
+// the output at most, less than binary16's own rounding up to 2^20 keys.
 //
 // Division of the work.  The G heads that share a key head are rows of one tile: row r of a query tile
 // is token i0 + r / G and head h G + r % G, so a key row is read once for all of them.  A unit is
@@ -30,7 +34,7 @@
 namespace gdn {
 namespace attn {
 
-constexpr float kRefSlack = 8.f;
+constexpr float kRefSlack = 8.f, kLift = 7.f, kUnlift = 1.f / 128;  // kUnlift = 2^-kLift
 constexpr uint32_t kWaitPolls = 1u << 22;  // the built-in limit of a wait (seconds), and that of the waits after one gave up
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -337,7 +341,7 @@ __global__ void __launch_bounds__(kCombineThreads, 5) attn_combine_kernel(const 
         }
     };
     auto finish = [&](int r, float ref, float l, const float4& acc) {
-        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+        const float inv = l > 0.f || l != l ? kUnlift / l : 0.f;
         const long long row = (j.token + r / a.G) * a.Hq + j.h * a.G + r % a.G;
         uint2 w;
         w.x = a.f16 ? pack2<true>(acc.x * inv, acc.y * inv) : pack2<false>(acc.x * inv, acc.y * inv);

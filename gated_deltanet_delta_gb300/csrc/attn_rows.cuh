@@ -12,7 +12,7 @@
 // A query row is first multiplied by a power of two that brings its largest element to 2^13 .. 2^14
 // (bf16 elements down to 2^-27 of the row's largest stay exact); the power, the key's scale and the
 // softmax scale multiply the fp32 product.  The value's scale moves into the exponent,
-//     p'_j = 2^{y_j + log2(vs_j) - ref},   l = sum p'_j / vs_j,   acc = sum p'_j v_j,
+//     p'_j = 2^{y_j + log2(vs_j) - ref + kLift},   l = 2^-kLift sum p'_j / vs_j,   acc = sum p'_j v_j,
 // so that p' fits binary16 whatever the scales' sizes are.
 //
 // Measured, one token each of 64 sequences: 16 bits, up to 8192 keys of 8 x 128, 187 us, 97 % of a copy's rate; 8
@@ -278,8 +278,8 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
                 for (int nt = 0; nt < NT; ++nt) {
                     const float2 ks = lds64(sst + (nt * 8 + 2 * t) * 4), vs = lds64(sst + TK * 4 + (nt * 8 + 2 * t) * 4);
                     const float lv[2] = {fast_log2(vs.x), fast_log2(vs.y)};
-                    iv[nt][0] = fast_rcp(vs.x);
-                    iv[nt][1] = fast_rcp(vs.y);
+                    iv[nt][0] = fast_rcp(vs.x) * kUnlift;
+                    iv[nt][1] = fast_rcp(vs.y) * kUnlift;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         sc[nt][2 * half] = fmaf(sc[nt][2 * half] * rscale[half], ks.x, lv[0]);
@@ -330,8 +330,8 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
                     o[i][3] *= f[1];
                 }
             }
-            use[0] = ref[0] == -INFINITY ? 0.f : ref[0];
-            use[1] = ref[1] == -INFINITY ? 0.f : ref[1];
+            use[0] = ref[0] == -INFINITY ? 0.f : ref[0] - kLift;
+            use[1] = ref[1] == -INFINITY ? 0.f : ref[1] - kLift;
             uint32_t pf[NT / 2][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -378,6 +378,7 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
         for (int half = 0; half < 2; ++half) {
             lsum[half] += __shfl_xor_sync(kFullMask, lsum[half], 1);
             lsum[half] += __shfl_xor_sync(kFullMask, lsum[half], 2);
+            if constexpr (!F8) lsum[half] *= kUnlift;
         }
 
         // ---- join the four warps: accumulators through shared memory (the rings are drained) ----
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
                 acc.w = fmaf(f, v.w, acc.w);
             }
             if (whole) {
-                const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+                const float inv = l > 0.f || l != l ? kUnlift / l : 0.f;
                 const long long row = (p.s.q0 + i0 + r / a.G) * a.Hq + p.h * a.G + r % a.G;
                 uint2 w;
                 w.x = pack2<F16>(acc.x * inv, acc.y * inv);

@@ -1,7 +1,7 @@
 // attn_tiles.cuh -- attn_paged for many query rows per key head (drafted windows, chunks, prompts): tiles
 // of 128 rows on the tensor cores (tcgen05, accumulators in TMEM).
 //
-// Per key tile of BN keys and 128 rows:  S = Q K^T (128 x BN x D),  P = 2^{y - ref},  O += P V
+// Per key tile of BN keys and 128 rows:  S = Q K^T (128 x BN x D),  P = 2^{y - ref + kLift},  O += P V
 // (128 x D x BN).  S, P (over S's columns) and O live in TMEM; Q, K and V tiles in shared memory in the
 // 128-byte-swizzled operand layouts; a row's reference and sum in its thread's registers.
 // Two S buffers keep the tensor core busy while one of them is exponentiated.  D <= 128: a unit has up to
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                     for (int i = 0; i < NK; ++i) {
                         k[i] = ks[i];
                         lv[i] = fast_log2(vs[i]);
-                        iv[i] = fast_rcp(vs[i]);
+                        iv[i] = fast_rcp(vs[i]) * kUnlift;
                     }
                     load(t + 1);
                     entries(t + 2);
@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                             }
                         }
                     }
-                    const float use = ref == -INFINITY ? 0.f : ref;
+                    const float use = ref == -INFINITY ? 0.f : ref - kLift;
                     float l2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int ch = 0; ch < BN / 32; ++ch) {
@@ -797,7 +797,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                             warp_arrive(TB_H0 + b);
                         }
                     }
-                    l += (l2[0] + l2[1]) + (l2[2] + l2[3]);
+                    l = fmaf((l2[0] + l2[1]) + (l2[2] + l2[3]), F8 ? 1.f : kUnlift, l);
                     tc::wait_st();
                 } else if (SLOTS == 2) {
                     if (C::PSEP) {
@@ -844,7 +844,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                 if (!ok) break;
                 if (some) {
                     const bool whole = t0 == 0 && t1 == p.nk;
-                    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+                    const float inv = l > 0.f || l != l ? kUnlift / l : 0.f;
                     const long long orow = (p.s.q0 + i0 + r / a.G) * a.Hq + p.h * a.G + r % a.G;
                     float* part = a.part + (static_cast<long long>(blockIdx.x) * 2 + (t0 > 0 ? 0 : 1)) *
                                                (static_cast<long long>(C::R) * (D + 2));

@@ -446,7 +446,8 @@ size_t attn_paged_workspace_size(int D);
  * GDN_STATUS_BAD_CACHE_INDEX and its rows hold no meaningful value.
  * Products take 16-bit operands (dtype; binary16 for an 8-bit cache, which its values and the scaled
  * queries fit exactly), weights are rounded to that type for the second product; scores, sums and
- * outputs accumulate in f32.  Results do not depend on timing.
+ * outputs accumulate in f32.  binary16 weights (dtype GDN_F16, or an 8-bit cache, where they include the value's
+ * scale) below 2^-32 of the row's largest add nothing to out; they count in lse.  Results do not depend on timing.
  * Supported: D in {64, 128, 256}, Hq % Hkv == 0, Hq / Hkv <= 128, cache_dtype dtype or GDN_E4M3,
  * max_pages * page_size < 2^31, T < 2^30; a length of more than 2^31 - 1024 is malformed.
  */
