@@ -195,7 +195,7 @@ size_t attn_workspace_bytes(int D) {
 
 cudaError_t launch_attn(const AttnArgs& args, void* workspace, int D, bool f8, int max_q, cudaStream_t stream) {
     AttnArgs a = args;
-    if (a.polls == 0) a.polls = attn::kWaitPolls;
+    if (a.polls == 0 || a.polls > attn::kWaitPolls) a.polls = attn::kWaitPolls;
     a.joins = static_cast<AttnJoin*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kJoinBytes);
     if (D == 64) return launch_d<64>(a, f8, max_q, stream);

@@ -102,6 +102,24 @@ __device__ __forceinline__ bool mbar_wait_or_abort(uint64_t* mbar, uint32_t pari
     return false;
 }
 
+// Poll as mbar_wait does, at most kMost times, and give up early once the polls so far are *most or more
+// (looked at every 16 polls).
+template <uint32_t kMost>
+__device__ __forceinline__ bool mbar_wait_most(uint64_t* mbar, uint32_t parity, const volatile uint32_t* most) {
+    const uint32_t a = smem_u32(mbar);
+    for (uint32_t i = 0; i < kMost; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{.reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p;}"
+            : "=r"(done)
+            : "r"(a), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if ((i & 15u) == 15u && i >= *most) return false;
+    }
+    return false;
+}
+
 // Poll with a suspend-time hint: each try_wait may park the thread for up to `hint_ns` until the
 // phase completes, so waiting warps leave the issue slots to the working ones.  At most `limit`
 // polls (with a 1 us hint, 2^22 polls bound the wait to a few seconds); gives up early once *abort

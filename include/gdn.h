@@ -460,7 +460,8 @@ gdn_status attn_paged(const void* q, int64_t q_stride, gdn_dtype dtype, const vo
 
 /*
  * attn_set_wait_limit -- bound every device-side wait of attn_paged's kernels to `polls` polls of its
- * barrier instead of the built-in limit (seconds), as gdn_prefill_set_wait_limit does for the prefill: a
+ * barrier (to the next multiple of 16 in the kernel for many rows; at most the built-in limit) instead of
+ * the built-in limit (seconds), as gdn_prefill_set_wait_limit does for the prefill: a
  * wait that runs out sets GDN_STATUS_TIMEOUT, its CTA lets the copies and products it has in flight end
  * (bounded) and stops, and the call's rows hold no meaningful value.  0 restores the built-in limit.
  * Process-wide; it applies to calls launched after it returns.
