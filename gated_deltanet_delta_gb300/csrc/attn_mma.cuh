@@ -104,12 +104,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     }
 }
 
-// The power of two that brings `mx` into [2^13, 2^14) (1 for zero, and for what is not finite).
-// Limited to 2^-100 .. 2^100, so that its reciprocal times a scale stays an ordinary number.
+// The power of two that brings `mx` into [2^13, 2^14) (1 for zero, and for what is not finite), at most 2^126, whose
+// reciprocal is still a normal number: an mx below 2^-113 ends lower, where binary16 still holds bf16's eight bits.
 __device__ __forceinline__ float row_up(float mx) {
     const int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
     if (!(mx > 0.f) || e > 127) return 1.f;
-    return __uint_as_float(static_cast<uint32_t>(min(max(13 - e, -100), 100) + 127) << 23);
+    return __uint_as_float(static_cast<uint32_t>(min(13 - e, 126) + 127) << 23);
 }
 
 // log2 and the reciprocal for the scales of 8-bit values (exact for powers of two; to about 2^-22 else).

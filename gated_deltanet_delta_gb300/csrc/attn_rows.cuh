@@ -282,8 +282,9 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
                     iv[nt][1] = fast_rcp(vs.y) * kUnlift;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        sc[nt][2 * half] = fmaf(sc[nt][2 * half] * rscale[half], ks.x, lv[0]);
-                        sc[nt][2 * half + 1] = fmaf(sc[nt][2 * half + 1] * rscale[half], ks.y, lv[1]);
+                        // the scales first: either may be as large or as small as numbers get
+                        sc[nt][2 * half] = fmaf(sc[nt][2 * half], rscale[half] * ks.x, lv[0]);
+                        sc[nt][2 * half + 1] = fmaf(sc[nt][2 * half + 1], rscale[half] * ks.y, lv[1]);
                     }
                 }
             } else {

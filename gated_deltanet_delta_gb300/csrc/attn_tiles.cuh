@@ -131,9 +131,10 @@ __device__ __forceinline__ void pair_exp2(float* x, float times, float plus) {
     x[0] = fast_exp2(x[0]);
     x[1] = fast_exp2(x[1]);
 }
-// y <- x c k + v
+// y <- x (c k) + v.  In this order, because c (the softmax scale over the query row's power of two) and k (the key's
+// scale) may be as large and as small as numbers get, and only their product is sure not to be.
 __device__ __forceinline__ void pair_fma(float* y, const float* x, float c, float k0, float k1, float v0, float v1) {
-    unpair(fma2(mul2(pair(x[0], x[1]), pair(c, c)), pair(k0, k1), pair(v0, v1)), y);
+    unpair(fma2(pair(x[0], x[1]), mul2(pair(c, c), pair(k0, k1)), pair(v0, v1)), y);
 }
 __device__ __forceinline__ void pair_add(float* s, const float* x) { unpair(add2(pair(s[0], s[1]), pair(x[0], x[1])), s); }
 __device__ __forceinline__ void pair_mac(float* s, const float* x, float k0, float k1) {

@@ -312,3 +312,16 @@ def test_workspace_refusals(gdn):
     assert torch.equal(a[0], b[0])
     with pytest.raises(gdn.GdnError, match="64, 128 or 256"):
         call(gdn, make(18, [1], [8], 4, 2, 96, 16, torch.bfloat16, False), 1.0)
+
+
+@pytest.mark.parametrize("new", [[1, 3], [20, 30]])  # the row kernel, the tile kernel
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("power", [120, 100, -100, -125])
+def test_queries_of_any_finite_size(gdn, power, dim, new):
+    # an 8-bit cache: queries close to the largest and the smallest numbers, keys that bring the scores back
+    x = make(19, new, [130, 70], 8, 2, dim, 16, torch.bfloat16, True)
+    x["q"] = (x["q"].float() * 2.0 ** power).bfloat16()
+    x["k_scale"] = (x["k_scale"].double() * 2.0 ** -power).float()
+    out, lse, status = call(gdn, x, dim ** -0.5)
+    assert status == 0
+    check(x, out, lse, dim ** -0.5)
