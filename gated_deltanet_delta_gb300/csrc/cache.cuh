@@ -134,6 +134,13 @@ __global__ void __launch_bounds__(kThreads) attn_cache_read_kernel(const __grid_
     __shared__ long long rows_s[TOKENS];
     const int h = blockIdx.y, kv = blockIdx.z, lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
     const long long t0 = static_cast<long long>(blockIdx.x) * TOKENS;
+    const long long most = static_cast<long long>(a.max_pages) * a.page_size;  // tokens that a page table holds
+    if (blockIdx.x == 0 && h == 0 && kv == 0) {  // malformed bounds are reported whether or not a row falls to them
+        for (int n = threadIdx.x; n < a.num_seqs; n += kThreads) {
+            const long long b = a.cu[n], e = a.cu[n + 1];
+            if (b < 0 || e < b || e > a.T || e - b > most) atomicOr(a.status, kStatusBadSeqlens);
+        }
+    }
     if (threadIdx.x < TOKENS) {  // the cached row of each token (-1: none)
         const long long t = t0 + threadIdx.x;
         long long row = -1;
@@ -146,9 +153,7 @@ __global__ void __launch_bounds__(kThreads) attn_cache_read_kernel(const __grid_
                 else hi = mid;
             }
             const long long b = a.cu[lo], e = a.cu[lo + 1], pos = t - b;
-            const bool fits = e - b <= static_cast<long long>(a.max_pages) * a.page_size;
-            if (b < 0 || e > a.T || !fits) atomicOr(a.status, kStatusBadSeqlens);
-            if (b >= 0 && t < e && e <= a.T && pos >= 0 && fits) {
+            if (b >= 0 && t < e && e <= a.T && pos >= 0 && e - b <= most) {
                 const long long pg = pos / a.page_size;
                 const long long page = a.table[static_cast<long long>(lo) * a.max_pages + pg];
                 if (page >= 0 && page < a.num_pages) row = (page * a.H + h) * a.page_size + (pos - pg * a.page_size);

@@ -194,3 +194,14 @@ def test_rows_at_the_top_of_the_range(gdn, dtype):
             lens, n = torch.ones(T, dtype=torch.int64).cuda(), torch.arange(T + 1).cuda()
             out = gdn.attn_paged(q[:T], kc1, vc1, one.expand(T, 1).contiguous(), lens, n, 1, k_scale=ks1, v_scale=vs1)
             assert torch.equal(out.float().cpu(), want[t].expand(T, 2, 64)), (t, T)
+
+
+@pytest.mark.parametrize("cu", [[0, 10, 5, 12], [0, 12, 11, 12], [0, 5, 40, 12], [-3, 4, 8, 12], [0, 4, 8, 13], [20, 20, 12, 12]])
+def test_malformed_bounds_are_reported(gdn, cu):
+    # a sequence that ends before it begins, begins below 0 or ends past T, whether or not a row falls to it
+    kc = torch.ones((4, 2, 8, 64), dtype=torch.bfloat16, device="cuda")
+    table = torch.tensor([[0, 1], [2, 3], [1, 2]]).cuda()
+    for bounds, bad in ((cu, True), ([0, 4, 4, 12], False)):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        gdn.attn_cache_read(kc, kc.clone(), table, torch.tensor(bounds).cuda(), 12, dev_status=status)
+        assert status.item() == (gdn.STATUS_BAD_SEQLENS if bad else 0)
