@@ -6,9 +6,10 @@ namespace gdn {
 namespace {
 
 // 64 tokens per CTA keep four rows of 128 in flight per group; with few tokens there are not enough
-// CTAs that way, and 16 tokens each take more of them.  Measured with 8 heads of 128, 8 bits, 64 and 16 tokens per
-// CTA: write, 1024 tokens 3.5 and 3.0 us, 4096 tokens 6.9 and 7.4 us, 16384 tokens 21.3 and 25.8 us; read, 1024
-// tokens 3.2 and 3.1 us, 4096 tokens 4.8 and 6.3 us, 16384 tokens 13.6 and 21.7 us.
+// CTAs that way, and 16 tokens each take more of them.  Measured with 8 heads of 128, 8 bits, memory that L2 does not
+// hold, 64 and 16 tokens per CTA: write, 1024 tokens 3.8 and 3.1 us, 2048 tokens 5.4 and 5.4 us, 4096 tokens 7.8 and
+// 8.6 us, 16384 tokens 20.4 and 26.1 us; read, 256 tokens 2.6 and 2.4 us, 1024 tokens 3.5 and 3.7 us, 4096 tokens
+// 6.5 and 8.1 us, 16384 tokens 18.6 and 26.0 us.
 template <int D, bool F16, bool F8>
 void write(const CacheMoveArgs& a, cudaStream_t stream) {
     if (a.T >= 2048) {
