@@ -1,38 +1,20 @@
 // attn.cu -- launch of attention over a paged cache: choice of the kernel and of its grid.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <atomic>
 #include <cstring>
-#include <mutex>
 
 #include "attn_rows.cuh"
 #include "attn_tiles.cuh"
+#include "host.h"
 #include "launch.h"
 
 namespace gdn {
 namespace {
 
-constexpr int kMaxDevices = 64;
 constexpr int kMaxCtas = 608;      // of the row kernel; the workspace has two partial slots for each
 constexpr int kMaxTileCtas = 160;  // of the tile kernel, likewise
 constexpr size_t kJoinBytes = kMaxCtas * sizeof(AttnJoin);  // at the workspace's start
 static_assert(kJoinBytes % 16 == 0, "the partials are read by 16 bytes");
-std::atomic<int> g_sms[kMaxDevices];
-
-cudaError_t sm_count(int* n) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    *n = g_sms[dev].load(std::memory_order_acquire);
-    if (*n == 0) {
-        e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess) return e;
-        g_sms[dev].store(*n, std::memory_order_release);
-    }
-    return cudaSuccess;
-}
 
 // Raises a kernel's shared-memory limit once per device.
 template <typename K>
@@ -45,20 +27,6 @@ cudaError_t raise_smem(K kernel, int bytes, std::atomic<unsigned long long>& don
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess) done.fetch_or(1ull << dev, std::memory_order_release);
     return e;
-}
-
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no link against libcuda).
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static std::once_flag once;
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
 }
 
 // A cache as rows of D elements, in boxes of `box` rows and `line` bytes (a row, or 128 bytes of it), with the

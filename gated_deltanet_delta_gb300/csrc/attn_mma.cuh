@@ -56,11 +56,6 @@ __device__ __forceinline__ float2 lds64(uint32_t addr) {
     asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
     return v;
 }
-__device__ __forceinline__ float lds32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
 
 // c += a b with a 16 x 16 (row), b 16 x 8 (column), binary16 (F16) or bf16 operands.
 template <bool F16>

@@ -19,6 +19,7 @@
 
 #include <cuda_fp8.h>
 
+#include "attn_mma.cuh"
 #include "common.cuh"
 #include "kernel_args.h"
 
@@ -26,21 +27,6 @@ namespace gdn {
 namespace cache {
 
 constexpr int kThreads = 256;
-
-template <bool F16>
-__device__ __forceinline__ float2 widen2(uint32_t w) {
-    if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
-    else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-template <bool F16>
-__device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
-    if constexpr (F16) {
-        const __half2 h = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-        return pack_bf16x2(lo, hi);
-    }
-}
 
 // The largest of the values that the LANES lanes of a row hold.
 template <int LANES>
@@ -93,7 +79,7 @@ __global__ void __launch_bounds__(kThreads) attn_cache_write_kernel(const __grid
             float mx = 0.f;                                  // fmaxf passes over NaN
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 p = widen2<F16>(w[j]);
+                const float2 p = attn::unpack2<F16>(w[j]);
                 f[2 * j] = p.x;
                 f[2 * j + 1] = p.y;
                 mx = fmaxf(mx, fmaxf(fabsf(p.x), fabsf(p.y)));
@@ -198,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) attn_cache_read_kernel(const __grid_
                 const uint32_t two = (j < 2 ? x[i].x : x[i].y) >> (16 * (j & 1)) & 0xffffu;
                 const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
                 const float2 f = __half22float2(__half2(hr));
-                w[j] = narrow2<F16>(f.x * s[i], f.y * s[i]);
+                w[j] = attn::pack2<F16>(f.x * s[i], f.y * s[i]);
             }
             x[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }

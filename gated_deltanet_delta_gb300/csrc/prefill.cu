@@ -1,34 +1,16 @@
 // prefill.cu -- launch of the chunkwise-WY prefill (kernels in prefill.cuh): the workspace layout, the
 // TMA descriptors of q, k, v and the per-device shared-memory limits.
-#include <cudaTypedefs.h>
-
 #include <atomic>
 #include <cstring>
-#include <mutex>
 
+#include "host.h"
 #include "launch.h"
 #include "prefill.cuh"
 
 namespace gdn {
 
 namespace {
-constexpr int kMaxDevices = 64;
 std::atomic<int> g_smem_set[kMaxDevices];  // per device: dynamic shared memory limits raised
-
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no link against libcuda).
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static std::once_flag once;
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
 
 // [T, H, 128] bf16 or fp16, boxes of 64 features x 1 head x 64 tokens, 128-byte swizzle, zero fill
 // past T.
