@@ -1,4 +1,5 @@
 // verify.cu -- launch of the draft verification (verify.cuh).
+#include "host.h"
 #include "launch.h"
 #include "verify.cuh"
 
@@ -8,7 +9,10 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream) {
     const int chunks = (a.V + verify::kChunk - 1) / verify::kChunk;
     // Four CTAs fit an SM.  Eight per sequence while they all run at once (64 sequences of 131072: 18.7 us,
     // with four 19.3); beyond that four (255 sequences of 100003: 47.0 us, with eight 51.1, with two 47.7).
-    int C = a.N <= 76 ? 8 : 4;
+    int sms = 0;
+    const cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    int C = static_cast<long long>(a.N) * 8 <= static_cast<long long>(sms) * 4 ? 8 : 4;
     // a CTA has 8 warps: no more CTAs than the row has chunks for
     while (C > 1 && chunks < C * 8) C /= 2;
     const int per = (chunks + C - 1) / C + 1;
