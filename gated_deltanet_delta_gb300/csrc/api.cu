@@ -1,6 +1,5 @@
 // api.cu -- the C ABI of libgdn (declared in include/gdn.h): host-side validation, choice of kernel
 // configuration, launch, and error reporting.  No device memory is allocated here.
-#include <algorithm>
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
@@ -762,7 +761,6 @@ extern "C" gdn_status attn_paged(const void* q, int64_t q_stride, gdn_dtype dtyp
     a.num_pages = num_pages;
     a.page_size = page_size;
     a.max_pages = max_pages;
-    a.max_keys = static_cast<int>(std::min<long long>(static_cast<long long>(max_pages) * page_size, gdn::kAttnMaxKeys));
     a.num_seqs = num_seqs;
     a.Hq = Hq;
     a.Hkv = Hkv;

@@ -12,7 +12,7 @@
 // A query row is first multiplied by a power of two that brings its largest element to 2^13 .. 2^14
 // (bf16 elements down to 2^-27 of the row's largest stay exact); the power, the key's scale and the
 // softmax scale multiply the fp32 product.  The value's scale moves into the exponent,
-//     p'_j = 2^{y_j + log2(vs_j) - ref + kLift},   l = 2^-kLift sum p'_j / vs_j,   acc = sum p'_j v_j,
+//     p'_j = 2^{y_j + log2(vs_j) - ref},   2^-kLift l = sum p'_j / (2^kLift vs_j),   acc = sum p'_j v_j,
 // so that p' fits binary16 whatever the scales' sizes are.
 //
 // Measured, one token each of 64 sequences: 16 bits, up to 8192 keys of 8 x 128, 187 us, 97 % of a copy's rate; 8
@@ -312,13 +312,13 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
                 x = fmaxf(x, __shfl_xor_sync(kFullMask, x, 1));
                 mx[half] = fmaxf(x, __shfl_xor_sync(kFullMask, x, 2));
             }
-            // rows move their reference when a score is kRefSlack above it (the first time: above -inf)
-            const bool up = mx[0] > ref[0] + kRefSlack || mx[1] > ref[1] + kRefSlack;
+            // rows move their reference when a score is kRefMove above it (the first time: above -inf)
+            const bool up = mx[0] > ref[0] + kRefMove || mx[1] > ref[1] + kRefMove;
             if (__any_sync(kFullMask, up)) {
                 float f[2];
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    const float to = fmaxf(ref[half], mx[half]);
+                    const float to = fmaxf(ref[half], mx[half] - kLift);
                     f[half] = to == -INFINITY ? 1.f : fast_exp2(ref[half] - to);
                     ref[half] = to;
                     lsum[half] *= f[half];
@@ -331,8 +331,8 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
                     o[i][3] *= f[1];
                 }
             }
-            use[0] = ref[0] == -INFINITY ? 0.f : ref[0] - kLift;
-            use[1] = ref[1] == -INFINITY ? 0.f : ref[1] - kLift;
+            use[0] = ref[0] == -INFINITY ? 0.f : ref[0];
+            use[1] = ref[1] == -INFINITY ? 0.f : ref[1];
             uint32_t pf[NT / 2][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -380,6 +380,7 @@ __global__ void __launch_bounds__(kRowsNT, RowsCfg<D, F8>::OCC) attn_rows_kernel
             lsum[half] += __shfl_xor_sync(kFullMask, lsum[half], 1);
             lsum[half] += __shfl_xor_sync(kFullMask, lsum[half], 2);
             if constexpr (!F8) lsum[half] *= kUnlift;
+            ref[half] += kLift;
         }
 
         // ---- join the four warps: accumulators through shared memory (the rings are drained) ----

@@ -1,7 +1,7 @@
 // attn_tiles.cuh -- attn_paged for many query rows per key head (drafted windows, chunks, prompts): tiles
 // of 128 rows on the tensor cores (tcgen05, accumulators in TMEM).
 //
-// Per key tile of BN keys and 128 rows:  S = Q K^T (128 x BN x D),  P = 2^{y - ref + kLift},  O += P V
+// Per key tile of BN keys and 128 rows:  S = Q K^T (128 x BN x D),  P = 2^{y - ref},  O += P V
 // (128 x D x BN).  S, P (over S's columns) and O live in TMEM; Q, K and V tiles in shared memory in the
 // 128-byte-swizzled operand layouts; a row's reference and sum in its thread's registers.
 // Two S buffers keep the tensor core busy while one of them is exponentiated.  D <= 128: a unit has up to
@@ -753,8 +753,8 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                         ok = product(s - SLOTS);
                         if (!ok) break;
                     }
-                    if (__any_sync(kFullMask, mx > ref + kRefSlack)) {
-                        const float to = fmaxf(ref, mx);
+                    if (__any_sync(kFullMask, mx > ref + kRefMove)) {
+                        const float to = fmaxf(ref, mx - kLift);
                         const float f = to == -INFINITY ? 1.f : fast_exp2(ref - to);
                         ref = to;
                         l *= f;
@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                             }
                         }
                     }
-                    const float use = ref == -INFINITY ? 0.f : ref - kLift;
+                    const float use = ref == -INFINITY ? 0.f : ref;
                     float l2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int ch = 0; ch < BN / 32; ++ch) {
@@ -800,7 +800,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                             warp_arrive(TB_H0 + b);
                         }
                     }
-                    l = fmaf((l2[0] + l2[1]) + (l2[2] + l2[3]), F8 ? 1.f : kUnlift, l);
+                    l += (l2[0] + l2[1]) + (l2[2] + l2[3]);
                     tc::wait_st();
                 } else if (SLOTS == 2) {
                     if (C::PSEP) {
@@ -818,6 +818,8 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             tiles += t1 - t0;
 
             // ---- the unit's rows
+            ref += kLift;
+            if constexpr (!F8) l *= kUnlift;
             const bool both = SLOTS == 2 && !full;  // the slots hold two parts of the same rows
             float f0 = 1.f, f1 = 0.f;
             if (both && wg == 1) {

@@ -199,7 +199,6 @@ struct AttnArgs {
     int32_t* status;
     long long T, num_pages;
     int page_size, max_pages, num_seqs;
-    int max_keys;        // the most that a sequence may have: what its page table holds, at most kAttnMaxKeys
     int Hq, Hkv, G;      // G = Hq / Hkv
     int tq;              // tokens per query tile
     int ov, min_per;     // a unit's fixed cost; the least cost per CTA (attn.cuh)
