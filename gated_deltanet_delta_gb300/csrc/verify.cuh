@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const __grid_
     const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
     const int n = blockIdx.x / C;
     // A CTA may write into another's shared memory only when that one has begun; waited for below, behind the row
-    cluster.barrier_arrive();
+    asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
 
     if (warp == 0) {  // every CTA of the cluster counts for itself
         const long long given = a.num_drafts ? a.num_drafts[n] : a.T;
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const __grid_
         mine = 0;
 #pragma unroll
         for (int i = 0; i < kThreads / 32; ++i) mine += warp_s[i];
-        if (pass == 0) cluster.barrier_wait();
+        if (pass == 0) asm volatile("barrier.cluster.wait;" ::: "memory");
         if (tid < C) *cluster.map_shared_rank(&total_s[pass][rank], tid) = mine;
         cluster.sync();
         all = before = 0;
