@@ -6,10 +6,9 @@
 // head hq reads key head hq / G, G = Hq / Hkv:
 //     s_j = scale q.k_j,   o = sum_j e^{s_j} v_j / sum_j e^{s_j},   lse = ln sum_j e^{s_j}.
 // All kernels make one pass over the keys with a running maximum, in base 2: y_j = s_j log2(e),
-// p_j = 2^{y_j - ref}, l = sum p_j and acc = sum p_j v_j in fp32.  ref is kLift below the running maximum, and
-// follows it only when that is more than kRefSlack above where it was, so p_j <= 2^(kRefSlack + kLift) and the
-// accumulators are rescaled a few times per row instead of at every tile; any ref gives the same quotient.  (What
-// leaves a kernel, through memory or to lse, is ref + kLift and 2^-kLift l.)  p_j is rounded to the
+// p_j = 2^{y_j - ref + kLift}, l = 2^-kLift sum p_j and acc = sum p_j v_j in fp32.  ref follows the running
+// maximum only when that is more than kRefSlack above it, so p_j <= 2^(kRefSlack + kLift) and the accumulators are
+// rescaled a few times per row instead of at every tile; any ref gives the same quotient.  p_j is rounded to the
 // operands' type for the product with v_j.  In binary16 what is below 2^-25 becomes 0, and would count in l but not in
 // acc: without the lift 2^17 keys of 2^-26 of the largest weight were missing from the output.  kLift puts p_j at the
 // top of binary16's range (at most 2^15), so that only weights below 2^-32 of the largest are lost; n of them are n 2^-32 of
@@ -36,7 +35,6 @@ namespace gdn {
 namespace attn {
 
 constexpr float kRefSlack = 8.f, kLift = 7.f, kUnlift = 1.f / 128;  // kUnlift = 2^-kLift
-constexpr float kRefMove = kLift + kRefSlack;  // a maximum that far above ref moves it
 constexpr uint32_t kWaitPolls = 1u << 22;  // the built-in limit of a wait (seconds), and that of the waits after one gave up
 constexpr float kLn2 = 0.69314718055994530942f;
 

@@ -1,7 +1,7 @@
 // attn_tiles.cuh -- attn_paged for many query rows per key head (drafted windows, chunks, prompts): tiles
 // of 128 rows on the tensor cores (tcgen05, accumulators in TMEM).
 //
-// Per key tile of BN keys and 128 rows:  S = Q K^T (128 x BN x D),  P = 2^{y - ref},  O += P V
+// Per key tile of BN keys and 128 rows:  S = Q K^T (128 x BN x D),  P = 2^{y - ref + kLift},  O += P V
 // (128 x D x BN).  S, P (over S's columns) and O live in TMEM; Q, K and V tiles in shared memory in the
 // 128-byte-swizzled operand layouts; a row's reference and sum in its thread's registers.
 // Two S buffers keep the tensor core busy while one of them is exponentiated.  D <= 128: a unit has up to
@@ -403,13 +403,15 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                             cp_async16(dst + tc::sw_chunk(r0 + rl, c, BN), src, ro >= 0);
                         }
                         push(KV_FULL + stage);
+                        // A tile that went this way is handed over at once where the next ones may go by TMA (a page outside
+                        // the cache, amid good ones): those push nothing, and wait for places that only this tile's
+                        // products free.
+                        if (box && kv == 1) flush();
                     }
                     if (++stage == NST) stage = 0, par ^= 1;
                 }
-                // The queries, copied meanwhile, are handed over behind two tiles' copies.  A tile that went by
-                // cp.async is handed over at once: the next ones may go by TMA, push nothing, and wait for places that only
-                // this tile's products free (a page outside the cache, amid good ones).
-                if (box && ok && (!tma || (!C::QTM && t == t0 + 1))) flush();
+                // the queries, copied meanwhile, are handed over behind two tiles' copies
+                if (!C::QTM && box && t == t0 + 1 && ok) flush();
             }
             if (!ok) break;
             flush();  // the MMAs of this unit, which free the query tiles, need all of its keys
@@ -753,8 +755,8 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                         ok = product(s - SLOTS);
                         if (!ok) break;
                     }
-                    if (__any_sync(kFullMask, mx > ref + kRefMove)) {
-                        const float to = fmaxf(ref, mx - kLift);
+                    if (__any_sync(kFullMask, mx > ref + kRefSlack)) {
+                        const float to = fmaxf(ref, mx);
                         const float f = to == -INFINITY ? 1.f : fast_exp2(ref - to);
                         ref = to;
                         l *= f;
@@ -772,7 +774,7 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                             }
                         }
                     }
-                    const float use = ref == -INFINITY ? 0.f : ref;
+                    const float use = ref == -INFINITY ? 0.f : ref - kLift;
                     float l2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int ch = 0; ch < BN / 32; ++ch) {
@@ -818,7 +820,6 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             tiles += t1 - t0;
 
             // ---- the unit's rows
-            ref += kLift;
             if constexpr (!F8) l *= kUnlift;
             const bool both = SLOTS == 2 && !full;  // the slots hold two parts of the same rows
             float f0 = 1.f, f1 = 0.f;
