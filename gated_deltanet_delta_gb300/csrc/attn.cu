@@ -137,11 +137,12 @@ cudaError_t launch_tiles(AttnArgs a, cudaStream_t stream) {
 
 template <int D, bool F16, bool F8>
 cudaError_t launch_any(const AttnArgs& a, int max_q, cudaStream_t stream) {
-    // The row kernel reads a key once per 16 rows that share it, the tile kernel once.  Measured with 32
-    // sequences of up to 8192 keys, heads of 128, row kernel and tile kernel: 16 bits, 16 rows 106 and 118 us,
-    // 24 rows 172 and 119 us; 8 bits, where the tile kernel has to widen every key tile first, 32 rows 124 and 220
-    // us, 64 rows 171 and 239 us, 128 rows 307 and 243 us (heads of 64: 64 rows 112 and 197 us, 128 rows 199 and 197
-    // us); 8 bits and heads of 256, 16 rows 85 and 117 us, 32 rows 152 and 117 us.
+    // The row kernel reads a key once per 16 rows that share it, the tile kernel once.  Measured with 32 sequences of up
+    // to 8192 keys, 1024 values each, and 8 heads per key head, row kernel and tile kernel.  16 bits: heads of 128, 16 rows
+    // 106 and 117 us, 24 rows 172 and 117 us; heads of 256, 16 rows 116 and 109 us, 32 rows 217 and 113 us (2 rows,
+    // 64 sequences, 199 and 189 us: the rule leaves aside that this width is always the tile kernel's).  8 bits, where the tile kernel has to widen every key
+    // tile first: heads of 128, 32 rows 119 and 215 us, 64 rows 221 and 225 us, 128 rows 292 and 239 us; heads of
+    // 64, 64 rows 287 and 333 us, 128 rows 379 and 383 us; heads of 256, 16 rows 84 and 115 us, 32 rows 151 and 116 us.
     const int most = F8 && D <= 128 ? 4 * attn::kRowsTile : attn::kRowsTile;
     return static_cast<long long>(std::max(max_q, 1)) * a.G <= most && a.G <= attn::kRowsTile
                ? launch_rows<D, F16, F8>(a, stream)

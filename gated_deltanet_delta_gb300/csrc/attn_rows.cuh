@@ -16,7 +16,7 @@
 // so that p' fits binary16 whatever the scales' sizes are.
 //
 // Measured, one token each of 64 sequences: 16 bits, up to 8192 keys of 8 x 128, 187 us, 97 % of a copy's rate; 8
-// bits, up to 16384 keys of 4 x 128, 114 us, 81 %: there the widening's and the products' instructions take as long.
+// bits, up to 16384 keys of 4 x 128, 112 us, 84 %: there the widening's and the products' instructions take as long.
 #pragma once
 
 #include "attn.cuh"

@@ -25,9 +25,11 @@
 // on 2-clock conversions; one warpgroup that did all three took 136 us where this took 111 (the windows below).
 // attn_rows.cuh says how the scales are applied.
 //
-// Measured: chunks of 4096 tokens over up to 15360 keys, two sequences, 32 / 8 heads of 128: 915 us, 1.41 PFLOP/s,
-// bound by the chain above; whole prompts of up to 4096 tokens, nine, 16 / 4 heads of 64: 261 us, bound by the
-// exponentials; windows of 8 tokens over up to 15360 8-bit keys, 32, 16 / 2 heads of 256: 115 us, bound by the softmax.
+// Measured: chunks of 4096 tokens over up to 15360 keys, two sequences, 32 / 8 heads of 128: 910 to 925 us, 1.4
+// PFLOP/s, bound by the chain above; whole prompts of up to 4096 tokens, nine, 16 / 4 heads of 64: 262 to 271 us, where no
+// unit is the limit (exponentials and tensor core 25 % each, issue 40 %) but the latency of two softmax warps per
+// scheduler, and the SMs' uneven ends; windows of 8 tokens over up to 15360 8-bit keys, 32, 16 / 2 heads of 256: 113
+// us, bound by the softmax of one warpgroup, and by uneven ends.
 //
 // Every wait is bounded: one that runs out sets GDN_STATUS_TIMEOUT and the CTA's limit of polls to 0, on which
 // all roles leave; copies and MMAs in flight are waited for (bounded) before the CTA ends.

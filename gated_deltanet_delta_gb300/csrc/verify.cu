@@ -7,8 +7,8 @@ namespace gdn {
 
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream) {
     const int chunks = (a.V + verify::kChunk - 1) / verify::kChunk;
-    // Four CTAs fit an SM.  Eight per sequence while they all run at once (64 sequences of 131072: 18.7 us,
-    // with four 19.3); beyond that four (255 sequences of 100003: 47.0 us, with eight 51.1, with two 47.7).
+    // Four CTAs fit an SM.  Eight per sequence while they all run at once (64 sequences of 131072: 16.8 us,
+    // with four 17.3); beyond that four (255 sequences of 100003: 44.4 us, with eight 48.9, with two 44.5).
     int sms = 0;
     const cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;

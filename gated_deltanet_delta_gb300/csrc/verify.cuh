@@ -9,11 +9,12 @@
 // Integer sums do not depend on their order, so the token is a function of the inputs alone, whatever
 // the division among threads; what the floor takes off is at most V 2^-36 of the mass.
 //
-// Bound: one row of p, and of q after a rejection, is read once: HBM for a batch, latency for one
-// sequence.  A cluster of CTAs takes a sequence: each sums its part of the row by chunks of 256
+// Bound: one row of p, and of q after a rejection, is read once.  HBM in the limit; one sequence is a chain of
+// dependent loads, and a batch has such a chain at each wave's beginning and a last wave that is not full (255 sequences
+// in clusters of four are 1.7 waves).  A cluster of CTAs takes a sequence: each sums its part of the row by chunks of 256
 // entries and writes its sum into every CTA's shared memory, and the one CTA whose part holds the mark
 // finds the chunk and reads its 256 entries again (from L2) while the others are already gone.  One launch, no workspace, no atomics.
-// Measured: 3 drafts, 255 sequences, 100003 entries, 204 MB: 44 us, 4.6 TB/s; 4 drafts, one sequence: 7 us.
+// Measured: 3 drafts, 255 sequences, 100003 entries, 204 MB: 44 us, 4.6 TB/s; 4 drafts, one sequence: 6.9 us.
 #pragma once
 
 #include <cooperative_groups.h>

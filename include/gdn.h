@@ -441,7 +441,7 @@ size_t attn_paged_workspace_size(int D);
  * A query that sees no key (L < m - i) gets out = 0, lse = -infinity.  Memory of the cache past a
  * sequence's length is never used, whatever it holds.  Keys and values that some query of a sequence's
  * chunk sees must be finite: the products with them also run, with weight zero, for the chunk's earlier
- * queries.  Scales must be positive and finite.  A sequence with malformed bounds sets
+ * queries.  Scales must be positive and finite, those of values at least 2^-100.  A sequence with malformed bounds sets
  * GDN_STATUS_BAD_SEQLENS and is skipped (its rows are not written); one with a page outside the cache sets
  * GDN_STATUS_BAD_CACHE_INDEX and its rows hold no meaningful value.
  * Products take 16-bit operands (dtype; binary16 for an 8-bit cache, which its values and the scaled
