@@ -641,6 +641,8 @@ extern "C" gdn_status attn_cache_write(const void* k, const void* v, int64_t k_s
     REQUIRE(!any_overlap(k_cache, cb, v_cache, cb) && !any_overlap(k, kb, k_cache, cb) && !any_overlap(k, kb, v_cache, cb) &&
                 !any_overlap(v, vb, k_cache, cb) && !any_overlap(v, vb, v_cache, cb),
             GDN_ERR_INVALID_ARG, "%s: the caches overlap each other or the sources", fn);
+    const size_t sb = k_scale ? static_cast<size_t>(num_pages) * Hkv * page_size * 4 : 0;
+    REQUIRE(!any_overlap(k_scale, sb, v_scale, sb), GDN_ERR_INVALID_ARG, "%s: k_scale and v_scale overlap", fn);
     gdn::CacheMoveArgs a;
     std::memset(&a, 0, sizeof(a));
     a.k_in = static_cast<const uint16_t*>(k);

@@ -386,7 +386,7 @@ void gdn_prefill_set_wait_limit(uint32_t polls);
  *              after token t - 1 (a slice of a fused projection needs no copy); 16-byte aligned, strides
  *              multiples of 8
  *   slots      int64 [T]   where token t goes: page * page_size + offset; a negative slot leaves the token
- *              out; distinct (of two tokens with one slot either may stay)
+ *              out; distinct (of two tokens with one slot parts of either may stay)
  *   cache_dtype  dtype (rows are copied), or GDN_E4M3: per (token, head) row the scale is the least power
  *              of two s >= 2^-100 with max |x| <= 448 s (1 for a row of zeros) and the stored value
  *              e4m3(x / s), to nearest even; but in rows at the top of dtype's range (s = 2^8 for binary16, 2^120

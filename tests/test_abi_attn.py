@@ -139,3 +139,9 @@ def test_a_workspace_off_the_device_is_refused():
     with pytest.raises(TypeError, match="workspace"):
         gdn._want_workspace(bytes(64), 64, "cpu")
     assert gdn._want_workspace(None, 64, "cpu").nbytes == 64 and gdn._want_workspace(None, 0, "cpu").nbytes == 0
+
+
+def test_cache_write_refuses_shared_scales(lib):
+    # keys and values would write their scales to the same places
+    assert write(lib, vsc=at(5)) == INVALID and "k_scale and v_scale overlap" in gdn.last_error()
+    assert write(lib, vsc=ctypes.c_void_p((6 << 44) + 4 * 16 * 2 * 4 - 4)) == INVALID
