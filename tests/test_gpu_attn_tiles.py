@@ -269,6 +269,8 @@ def test_offsets_beyond_32_bits(gdn, f8):
 
 def test_rows_past_the_coordinates_of_a_box(gdn):
     # over 2^31 rows of 64 bytes: too many for a box's coordinates, so the copies go without
+    if torch.cuda.mem_get_info()[0] < 160 << 30:
+        pytest.skip("needs 150 GB")
     pages, hkv, page, dim = 16500, 8, 16384, 64
     x = {"kv": [20000], "cu": [0, 20], "table": torch.tensor([[pages - 1, 1]]).cuda()}
     g = torch.Generator(device="cuda").manual_seed(4)
@@ -285,6 +287,8 @@ def test_rows_past_the_coordinates_of_a_box(gdn):
                        k_scale=scale, v_scale=scale, out=out, lse=lse, dev_status=status)
         assert status.item() == 0
         check(dict(x, k=one, v=one, k_scale=scale, v_scale=scale), out, lse, 0.125)
+    del one, scale
+    torch.cuda.empty_cache()
 
 
 def test_other_stream_strided_queries_given_buffers(gdn):
