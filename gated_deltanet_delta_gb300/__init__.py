@@ -24,6 +24,7 @@ STATUS_BAD_SEQLENS = 2
 STATUS_TIMEOUT = 4
 STATUS_BAD_PROBS = 8
 STATUS_BAD_TOKEN = 16
+STATUS_BAD_POSITION = 32
 
 # Every symbol that include/gdn.h declares.
 ABI_SYMBOLS = ("gdn_decode_step", "gdn_decode_multi", "gdn_decode_step_pooled", "comba_decode_step", "comba_forward",
@@ -31,6 +32,7 @@ ABI_SYMBOLS = ("gdn_decode_step", "gdn_decode_multi", "gdn_decode_step_pooled", 
                "gdn_prefill_chunked", "gdn_prefill_chunked_f16", "gdn_prefill_chunked_noalloc",
                "comba_prefill_chunked", "gdn_window_fused", "gdn_prefill_set_wait_limit",
                "attn_cache_write", "attn_cache_read", "attn_paged_workspace_size", "attn_paged", "attn_set_wait_limit", "draft_verify",
+               "attn_cache_append", "short_conv", "ssm_decode_step", "ssm_prefill_workspace_size", "ssm_prefill_chunked", "add_rms_norm",
                "gdn_status_string", "gdn_last_error")
 
 
@@ -100,6 +102,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.attn_set_wait_limit.restype = None
         lib.draft_verify.argtypes = [P, P, P, P, P, P, I, I, I, P, P, P, P]
         lib.draft_verify.restype = I
+        lib.attn_cache_append.argtypes = [P, P, P, I64, I64, I64, I, P, I64, I, I, P, P, I64, P, I64, P, P, P, P, I, I64, I, I, I,
+                                          I, P, P]
+        lib.attn_cache_append.restype = I
+        lib.short_conv.argtypes = [P, I64, I, P, P, P, I, P, P, I, I64, I, I, I, P, I, P, I, P, I, P, P]
+        lib.short_conv.restype = I
+        lib.ssm_decode_step.argtypes = [P, P, P, P, P, P, P, P, P, P, I, P, I, I, I, I, I, P, P, P]
+        lib.ssm_decode_step.restype = I
+        lib.ssm_prefill_workspace_size.argtypes = [I, I64, I, I, I]
+        lib.ssm_prefill_workspace_size.restype = SZ
+        lib.ssm_prefill_chunked.argtypes = [P, P, P, P, P, P, P, P, P, P, I, P, P, I, I64, I64, I, I, I, I, P, P, SZ, P, P]
+        lib.ssm_prefill_chunked.restype = I
+        lib.add_rms_norm.argtypes = [P, I64, P, I, P, F, I64, I, P, I, P, I, P]
+        lib.add_rms_norm.restype = I
         lib.gdn_status_string.argtypes = [I]
         lib.gdn_status_string.restype = ctypes.c_char_p
         lib.gdn_last_error.argtypes = []
@@ -671,3 +686,202 @@ def draft_verify(target_p, draft_p, drafts, u_accept, u_sample, num_drafts=None,
                                u_accept.data_ptr(), u_sample.data_ptr(), N, T, V, accepted.data_ptr(),
                                tokens.data_ptr(), dev_status.data_ptr(), _stream(device)), "draft_verify")
     return accepted, tokens
+
+
+# ------------------------------------------------------------------------------------------------
+# Between the matrix products: rotation with the append, short convolution, state space scan, norm
+# ------------------------------------------------------------------------------------------------
+def attn_cache_append(q, k, v, rotation, positions, slots, k_cache, v_cache, k_scale=None, v_scale=None, q_out=None,
+                      neighbours: bool = False, dev_status=None):
+    """attn_cache_write with the rotation of queries and keys by their positions on the way.  q [T,Hq,D] (or None), k, v
+    [T,Hkv,D] bf16 or float16 (tokens may stand apart); rotation f32 [positions,R]: cos of the R / 2 angles, then sin;
+    positions, slots int64 [T]; caches and scales as attn_cache_write's.  Features i and i + R / 2 are a pair, or, with
+    neighbours, 2 i and 2 i + 1; those from R on are not turned.  Returns the rotated queries (q_out, which may be q)."""
+    torch = _torch_module or _torch()
+    dtype, device, T = k.dtype, k.device, k.shape[0]
+    code = _row_code(dtype, "k")
+    cache, (pages, H, page_size, D) = _want_cache(k_cache, v_cache, k_scale, v_scale, dtype)
+    rows = (T, H, D)
+    ks = _want_rows(k, "k", dtype, rows)
+    vs = _want_rows(v, "v", dtype, rows)
+    _want(rotation, "rotation", torch.float32)
+    if rotation.dim() != 2:
+        raise ValueError(f"rotation must be [positions,R], got {tuple(rotation.shape)}")
+    _want(positions, "positions", torch.int64, (T,))
+    _want(slots, "slots", torch.int64, (T,))
+    Hq = qs = os_ = 0
+    if q is not None:
+        Hq = q.shape[1]
+        qs = _want_rows(q, "q", dtype, (T, Hq, D))
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=dtype, device=device)
+        os_ = _want_rows(q_out, "q_out", dtype, (T, Hq, D))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    dev_status = _want_status(dev_status, device)
+    _check(load().attn_cache_append(_ptr(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, code, rotation.data_ptr(), rotation.shape[0],
+                                    rotation.shape[1], int(neighbours), positions.data_ptr(), slots.data_ptr(), T, _ptr(q_out), os_,
+                                    k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale), cache, pages, page_size,
+                                    Hq, H, D, dev_status.data_ptr(), _stream(device)), "attn_cache_append")
+    return q_out
+
+
+def _row_stride(t, name: str, dtype, shape):
+    """A [T, C] tensor whose rows may stand apart; returns the distance between them."""
+    torch = _torch_module or _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    T, C = shape
+    if T == 0:
+        return C
+    s0, s1 = t.stride()
+    if s1 != 1 and C > 1:
+        raise ValueError(f"{name}: a row must be contiguous (strides {t.stride()})")
+    return s0 if T > 1 else max(C, s0)
+
+
+def short_conv(x, weight, hist_pool, cache_indices, cu_seqlens=None, bias=None, splits=None, silu: bool = True, outs=None,
+               dev_status=None):
+    """Short causal convolution (and SiLU) of packed sequences.  x [T,C] bf16 or float16 (rows may stand apart); weight f32
+    [C,taps], taps 2 to 4; hist_pool f32 [pool,C,taps-1], oldest first, updated in place; cache_indices int64 [N];
+    cu_seqlens int64 [N+1], or None: one token per sequence.  splits: the widths of up to three outputs, [C] by
+    default.  Returns the tuple of outputs [T,width]."""
+    torch = _torch_module or _torch()
+    dtype, device = x.dtype, x.device
+    code = _row_code(dtype, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [T,C], got {tuple(x.shape)}")
+    T, C = x.shape
+    stride = _row_stride(x, "x", dtype, x.shape)
+    f32 = torch.float32
+    _want(weight, "weight", f32)
+    if weight.dim() != 2 or weight.shape[0] != C:
+        raise ValueError(f"weight must be [{C},taps], got {tuple(weight.shape)}")
+    taps = weight.shape[1]
+    _want(hist_pool, "hist_pool", f32)
+    if hist_pool.dim() != 3 or tuple(hist_pool.shape[1:]) != (C, taps - 1):
+        raise ValueError(f"hist_pool must be [pool,{C},{taps - 1}], got {tuple(hist_pool.shape)}")
+    if bias is not None:
+        _want(bias, "bias", f32, (C,))
+    N = cache_indices.shape[0]
+    _want(cache_indices, "cache_indices", torch.int64, (N,))
+    if cu_seqlens is not None:
+        _want(cu_seqlens, "cu_seqlens", torch.int64, (N + 1,))
+    widths = [C] if splits is None else list(splits)
+    if not 1 <= len(widths) <= 3 or sum(widths) != C or min(widths) < 1:
+        raise ValueError(f"splits must be one to three widths that add up to {C}, got {widths}")
+    if outs is None:
+        outs = tuple([torch.empty((T, w), dtype=dtype, device=device) for w in widths])
+    elif len(outs) != len(widths):
+        raise ValueError(f"{len(widths)} outs wanted, got {len(outs)}")
+    else:
+        for i, w in enumerate(widths):
+            _want(outs[i], f"outs[{i}]", dtype, (T, w))
+    dev_status = _want_status(dev_status, device)
+    parts = []
+    for i in range(3):
+        parts += [outs[i].data_ptr(), widths[i]] if i < len(widths) else [None, 0]
+    _check(load().short_conv(x.data_ptr(), stride, code, weight.data_ptr(), _ptr(bias), hist_pool.data_ptr(), hist_pool.shape[0],
+                             cache_indices.data_ptr(), _ptr(cu_seqlens), N, T, C, taps, int(silu), *parts, dev_status.data_ptr(),
+                             _stream(device)), "short_conv")
+    return tuple(outs)
+
+
+_Strides = ctypes.c_int64 * 5
+
+
+def _ssm_args(x, dt, B, C, A_log, dt_bias, state_pool, cache_indices, D, z, out, dev_status):
+    """The checks that both forms of the scan share; returns the arguments in the C order, and what is returned."""
+    torch = _torch_module or _torch()
+    bf, f32, device = torch.bfloat16, torch.float32, x.device
+    T, H, P = x.shape
+    G, N = B.shape[1:]
+    rows, bc = (T, H, P), (T, G, N)
+    strides = _Strides(_want_rows(x, "x", bf, rows), _row_stride(dt, "dt", bf, (T, H)), _want_rows(B, "B", bf, bc),
+                       _want_rows(C, "C", bf, bc), H * P if z is None else _want_rows(z, "z", bf, rows))
+    _want(A_log, "A_log", f32, (H,))
+    _want(dt_bias, "dt_bias", f32, (H,))
+    if D is not None:
+        _want(D, "D", f32, (H,))
+    _want(state_pool, "state_pool", f32)
+    if state_pool.dim() != 4 or tuple(state_pool.shape[1:]) != (H, P, N):
+        raise ValueError(f"state_pool must be [pool,{H},{P},{N}], got {tuple(state_pool.shape)}")
+    _want(cache_indices, "cache_indices", torch.int64, (cache_indices.shape[0],))
+    if out is None:
+        out = torch.empty(rows, dtype=bf, device=device)
+    else:
+        _want(out, "out", bf, rows)
+    dev_status = _want_status(dev_status, device)
+    return (x.data_ptr(), dt.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(z), strides, A_log.data_ptr(), _ptr(D), dt_bias.data_ptr(),
+            state_pool.data_ptr(), state_pool.shape[0], cache_indices.data_ptr()), (H, P, G, N), out, dev_status
+
+
+def ssm_decode_step(x, dt, B, C, A_log, dt_bias, state_pool, cache_indices, D=None, z=None, out=None, dev_status=None):
+    """One token per sequence of the selective state space scan.  x, z bf16 [N,H,P]; dt bf16 [N,H]; B, C bf16 [N,G,S] (the
+    rows of all five may stand apart); A_log, dt_bias, D f32 [H]; state_pool f32 [pool,H,P,S], updated in place;
+    cache_indices int64 [N].  Returns out bf16 [N,H,P]."""
+    args, sizes, out, dev_status = _ssm_args(x, dt, B, C, A_log, dt_bias, state_pool, cache_indices, D, z, out, dev_status)
+    N = cache_indices.shape[0]
+    if x.shape[0] != N:
+        raise ValueError(f"one token per sequence: x has {x.shape[0]} tokens, cache_indices {N}")
+    _check(load().ssm_decode_step(*args, N, *sizes, out.data_ptr(), dev_status.data_ptr(), _stream(x.device)), "ssm_decode_step")
+    return out
+
+
+def ssm_prefill_workspace_size(N: int, T: int, H: int, P: int, S: int) -> int:
+    return int(load().ssm_prefill_workspace_size(N, T, H, P, S))
+
+
+def ssm_prefill_chunked(x, dt, B, C, A_log, dt_bias, state_pool, cache_indices, cu_seqlens, max_len: int, D=None, z=None, out=None,
+                        workspace=None, dev_status=None):
+    """The scan of ssm_decode_step over packed sequences: x, z bf16 [T,H,P]; dt bf16 [T,H]; B, C bf16 [T,G,S]; cu_seqlens
+    int64 [N+1]; max_len: the longest sequence (it only chooses the kernel).  Returns out bf16 [T,H,P]."""
+    torch = _torch_module or _torch()
+    args, sizes, out, dev_status = _ssm_args(x, dt, B, C, A_log, dt_bias, state_pool, cache_indices, D, z, out, dev_status)
+    T, N = x.shape[0], cache_indices.shape[0]
+    H, P, _, S = sizes
+    _want(cu_seqlens, "cu_seqlens", torch.int64, (N + 1,))
+    workspace = _want_workspace(workspace, ssm_prefill_workspace_size(N, T, H, P, S) if workspace is None else 0, x.device)
+    _check(load().ssm_prefill_chunked(*args, cu_seqlens.data_ptr(), N, T, max_len, *sizes, out.data_ptr(), workspace.data_ptr(),
+                                      workspace.nbytes, dev_status.data_ptr(), _stream(x.device)), "ssm_prefill_chunked")
+    return out
+
+
+def add_rms_norm(x, weight, residual=None, eps: float = 1e-6, e4m3: bool = False, group: int = 0, out=None, scale=None):
+    """Residual addition and root-mean-square norm.  x [T,C] bf16 or float16 (rows may stand apart); weight f32 [C]; residual
+    [T,C] of x's type, updated in place to x + residual, or None.  Returns out [T,C] of x's type; or, with e4m3, (out
+    float8_e4m3fn, scale f32 [T, C / group]; [T,1] for group 0): the norm is out * scale."""
+    torch = _torch_module or _torch()
+    dtype, device = x.dtype, x.device
+    code = _row_code(dtype, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [T,C], got {tuple(x.shape)}")
+    shape = T, C = x.shape
+    stride = _row_stride(x, "x", dtype, x.shape)
+    _want(weight, "weight", torch.float32, (C,))
+    if residual is not None:
+        _want(residual, "residual", dtype, shape)
+    kind = torch.float8_e4m3fn if e4m3 else dtype
+    if out is None:
+        out = torch.empty(shape, dtype=kind, device=device)
+    else:
+        _want(out, "out", kind, shape)
+    if e4m3:
+        if group < 0 or (group and C % group):
+            raise ValueError(f"group must be 0 or a divisor of {C}, got {group}")
+        groups = (T, C // group if group else 1)
+        if scale is None:
+            scale = torch.empty(groups, dtype=torch.float32, device=device)
+        else:
+            _want(scale, "scale", torch.float32, groups)
+    elif scale is not None or group:
+        raise ValueError("scale and group are for an e4m3 output")
+    _check(load().add_rms_norm(x.data_ptr(), stride, _ptr(residual), code, weight.data_ptr(), eps, T, C, out.data_ptr(),
+                               GDN_E4M3 if e4m3 else code, _ptr(scale), group, _stream(device)), "add_rms_norm")
+    return (out, scale) if e4m3 else out

@@ -816,3 +816,292 @@ extern "C" gdn_status draft_verify(const float* target_p, const float* draft_p, 
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
     return launched(fn);
 }
+
+// ------------------------------------------------------------------------------------------------
+// what stands between the matrix products: rotation with the append, short convolution, state space scan, norm
+extern "C" gdn_status attn_cache_append(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                                        int64_t v_stride, gdn_dtype dtype, const float* rotation, int64_t max_positions,
+                                        int rotary_dim, int neighbours, const int64_t* positions, const int64_t* slots,
+                                        int64_t T, void* q_out, int64_t q_out_stride, void* k_cache, void* v_cache,
+                                        float* k_scale, float* v_scale, gdn_dtype cache_dtype, int64_t num_pages,
+                                        int page_size, int Hq, int Hkv, int D, int32_t* dev_status, gdn_stream_t stream) {
+    const char* fn = "attn_cache_append";
+    REQUIRE(T >= 0 && num_pages >= 0 && max_positions >= 0 && Hq >= 0 && page_size >= 1 && Hkv >= 1, GDN_ERR_INVALID_ARG,
+            "%s: sizes must be T, num_pages, max_positions, Hq >= 0 and page_size, Hkv >= 1", fn);
+    if (T == 0) return GDN_OK;
+    size_t cb = 0;
+    const gdn_status s = cache_check(fn, k_cache, v_cache, k_scale, v_scale, cache_dtype, dtype, num_pages, page_size,
+                                     Hkv, D, dev_status, &cb);
+    if (s != GDN_OK) return s;
+    REQUIRE(Hq <= 65535, GDN_ERR_UNSUPPORTED, "%s: at most 65535 heads (got %d)", fn, Hq);
+    REQUIRE(rotary_dim >= 16 && rotary_dim <= D && rotary_dim % 16 == 0, GDN_ERR_UNSUPPORTED,
+            "%s: rotary_dim must be a multiple of 16 between 16 and D (got %d)", fn, rotary_dim);
+    REQUIRE(k && v && slots && positions && rotation && (Hq == 0 || (q && q_out)), GDN_ERR_INVALID_ARG, "%s: null pointer", fn);
+    const long long row = static_cast<long long>(Hkv) * D, qrow = static_cast<long long>(Hq) * D;
+    REQUIRE(k_stride >= row && v_stride >= row && k_stride % 8 == 0 && v_stride % 8 == 0 &&
+                (Hq == 0 || (q_stride >= qrow && q_out_stride >= qrow && q_stride % 8 == 0 && q_out_stride % 8 == 0)),
+            GDN_ERR_INVALID_ARG, "%s: token strides must be multiples of 8 and at least the heads' width", fn);
+    REQUIRE(aligned(q, 16) && aligned(k, 16) && aligned(v, 16) && aligned(q_out, 16) && aligned(rotation, 16) &&
+                aligned(slots, 8) && aligned(positions, 8),
+            GDN_ERR_INVALID_ARG, "%s: q, k, v, q_out and rotation must be 16-byte aligned", fn);
+    REQUIRE(T < (1LL << 31) && k_stride < (1LL << 31) && v_stride < (1LL << 31) &&
+                (Hq == 0 || (q_stride < (1LL << 31) && q_out_stride < (1LL << 31))),
+            GDN_ERR_UNSUPPORTED, "%s: T and the strides must be below 2^31", fn);
+    REQUIRE(max_positions <= (1LL << 52) / rotary_dim, GDN_ERR_UNSUPPORTED, "%s: max_positions too large", fn);
+    const size_t kb = (static_cast<size_t>(T - 1) * k_stride + row) * 2, vb = (static_cast<size_t>(T - 1) * v_stride + row) * 2;
+    const size_t qb = Hq ? (static_cast<size_t>(T - 1) * q_stride + qrow) * 2 : 0;
+    const size_t ob = Hq ? (static_cast<size_t>(T - 1) * q_out_stride + qrow) * 2 : 0;
+    REQUIRE(!any_overlap(k_cache, cb, v_cache, cb) && !any_overlap(k, kb, k_cache, cb) && !any_overlap(k, kb, v_cache, cb) &&
+                !any_overlap(v, vb, k_cache, cb) && !any_overlap(v, vb, v_cache, cb) && !any_overlap(q, qb, k_cache, cb) &&
+                !any_overlap(q, qb, v_cache, cb) && !any_overlap(q_out, ob, k_cache, cb) && !any_overlap(q_out, ob, v_cache, cb),
+            GDN_ERR_INVALID_ARG, "%s: the caches overlap each other, the sources or q_out", fn);
+    const size_t rb = static_cast<size_t>(max_positions) * rotary_dim * 4;
+    // q_out may be q itself; then its rows may stand among the rows of k and v, as those of a fused projection do
+    const bool in_place = Hq > 0 && q_out == q && q_out_stride == q_stride;
+    REQUIRE(in_place || (!any_overlap(q_out, ob, q, qb) && !any_overlap(q_out, ob, k, kb) && !any_overlap(q_out, ob, v, vb)),
+            GDN_ERR_INVALID_ARG, "%s: q_out overlaps a source (it may be q itself, with the same stride)", fn);
+    REQUIRE(!any_overlap(q_out, ob, rotation, rb) && !any_overlap(k_cache, cb, rotation, rb) && !any_overlap(v_cache, cb, rotation, rb),
+            GDN_ERR_INVALID_ARG, "%s: rotation overlaps an output", fn);
+    const size_t sb = k_scale ? static_cast<size_t>(num_pages) * Hkv * page_size * 4 : 0;
+    REQUIRE(!any_overlap(k_scale, sb, v_scale, sb), GDN_ERR_INVALID_ARG, "%s: k_scale and v_scale overlap", fn);
+    gdn::AppendArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.q = static_cast<const uint16_t*>(q);
+    a.k = static_cast<const uint16_t*>(k);
+    a.v = static_cast<const uint16_t*>(v);
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_out = static_cast<uint16_t*>(q_out);
+    a.q_out_stride = q_out_stride;
+    a.rotation = rotation;
+    a.positions = positions;
+    a.slots = slots;
+    a.kc = k_cache;
+    a.vc = v_cache;
+    a.ks = k_scale;
+    a.vs = v_scale;
+    a.status = dev_status;
+    a.T = T;
+    a.num_pages = num_pages;
+    a.max_pos = max_positions;
+    a.page_size = page_size;
+    a.Hq = Hq;
+    a.H = Hkv;
+    a.turned = rotary_dim;
+    gdn::launch_cache_append(a, D, dtype == GDN_F16, cache_dtype == GDN_E4M3, neighbours != 0, static_cast<cudaStream_t>(stream));
+    return launched(fn);
+}
+
+extern "C" gdn_status short_conv(const void* x, int64_t x_stride, gdn_dtype dtype, const float* weight, const float* bias,
+                                 float* hist_pool, int pool_size, const int64_t* cache_indices, const int64_t* cu_seqlens,
+                                 int num_seqs, int64_t T, int C, int taps, int silu, void* out0, int c0, void* out1, int c1,
+                                 void* out2, int c2, int32_t* dev_status, gdn_stream_t stream) {
+    const char* fn = "short_conv";
+    REQUIRE(T >= 0 && num_seqs >= 0 && pool_size >= 0 && C >= 1, GDN_ERR_INVALID_ARG,
+            "%s: sizes must be T, num_seqs, pool_size >= 0 and C >= 1", fn);
+    REQUIRE(dtype == GDN_BF16 || dtype == GDN_F16, GDN_ERR_INVALID_ARG, "%s: dtype must be GDN_BF16 or GDN_F16", fn);
+    REQUIRE(taps >= 2 && taps <= 4, GDN_ERR_UNSUPPORTED, "%s: taps must be 2, 3 or 4 (got %d)", fn, taps);
+    REQUIRE(c0 >= 1 && c1 >= 0 && c2 >= 0 && (c1 > 0 || c2 == 0) && static_cast<long long>(c0) + c1 + c2 == C, GDN_ERR_INVALID_ARG,
+            "%s: the outputs' widths must be positive and add up to C", fn);
+    REQUIRE(c0 % 8 == 0 && c1 % 8 == 0 && c2 % 8 == 0, GDN_ERR_UNSUPPORTED, "%s: the outputs' widths must be multiples of 8", fn);
+    REQUIRE(C <= (1 << 24) && T < (1LL << 31), GDN_ERR_UNSUPPORTED, "%s: C must be at most 2^24 and T below 2^31", fn);
+    if (T == 0 || num_seqs == 0) return GDN_OK;
+    REQUIRE(cu_seqlens || T == num_seqs, GDN_ERR_INVALID_ARG, "%s: without cu_seqlens T must be num_seqs", fn);
+    REQUIRE(x && weight && hist_pool && cache_indices && dev_status && out0 && (c1 == 0 || out1) && (c2 == 0 || out2),
+            GDN_ERR_INVALID_ARG, "%s: null pointer", fn);
+    REQUIRE(x_stride >= C && x_stride % 8 == 0 && x_stride < (1LL << 31), GDN_ERR_INVALID_ARG,
+            "%s: x_stride must be a multiple of 8, at least C and below 2^31", fn);
+    REQUIRE(aligned(x, 16) && aligned(weight, 16) && aligned(bias, 4) && aligned(hist_pool, 16) && aligned(out0, 16) &&
+                aligned(out1, 16) && aligned(out2, 16) && aligned(cache_indices, 8) && aligned(cu_seqlens, 8) && aligned(dev_status, 4),
+            GDN_ERR_INVALID_ARG, "%s: x, weight, hist_pool and the outputs must be 16-byte aligned", fn);
+    const size_t xb = (static_cast<size_t>(T - 1) * x_stride + C) * 2, hb = static_cast<size_t>(pool_size) * C * (taps - 1) * 4;
+    const size_t wb = static_cast<size_t>(C) * taps * 4, bb = bias ? static_cast<size_t>(C) * 4 : 0;
+    void* const outs[3] = {out0, out1, out2};
+    const int widths[3] = {c0, c1, c2};
+    REQUIRE(!any_overlap(hist_pool, hb, x, xb) && !any_overlap(hist_pool, hb, weight, wb) && !any_overlap(hist_pool, hb, bias, bb),
+            GDN_ERR_INVALID_ARG, "%s: hist_pool overlaps an input", fn);
+    for (int i = 0; i < 3; ++i) {
+        const size_t ob = static_cast<size_t>(T) * widths[i] * 2;
+        REQUIRE(!any_overlap(outs[i], ob, x, xb) && !any_overlap(outs[i], ob, hist_pool, hb) && !any_overlap(outs[i], ob, weight, wb) &&
+                    !any_overlap(outs[i], ob, bias, bb),
+                GDN_ERR_INVALID_ARG, "%s: an output overlaps an input", fn);
+        for (int j = 0; j < i; ++j)
+            REQUIRE(!any_overlap(outs[i], ob, outs[j], static_cast<size_t>(T) * widths[j] * 2), GDN_ERR_INVALID_ARG,
+                    "%s: the outputs overlap", fn);
+    }
+    gdn::ConvArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = static_cast<const uint16_t*>(x);
+    a.x_stride = x_stride;
+    a.w = weight;
+    a.bias = bias;
+    a.hist = hist_pool;
+    a.slots = cache_indices;
+    a.cu = cu_seqlens;
+    for (int i = 0; i < 3; ++i) {
+        a.out[i] = static_cast<uint16_t*>(outs[i]);
+        a.width[i] = widths[i];
+    }
+    a.status = dev_status;
+    a.T = T;
+    a.C = C;
+    a.num_seqs = num_seqs;
+    a.pool_size = pool_size;
+    a.silu = silu != 0;
+    gdn::launch_conv(a, taps, dtype == GDN_F16, static_cast<cudaStream_t>(stream));
+    return launched(fn);
+}
+
+// What the two forms of the scan ask of their arguments; fills `a`.
+static gdn_status ssm_check(const char* fn, gdn::SsmArgs* a, const void* x, const void* dt, const void* B, const void* C, const void* z,
+                            const int64_t* strides, const float* A_log, const float* D, const float* dt_bias, float* state_pool,
+                            int pool_size, const int64_t* cache_indices, int num_seqs, int64_t T, int H, int P, int G, int N, void* out,
+                            int32_t* dev_status) {
+    REQUIRE(x && dt && B && C && A_log && dt_bias && state_pool && cache_indices && out && dev_status && strides, GDN_ERR_INVALID_ARG,
+            "%s: null pointer", fn);
+    const long long inner = static_cast<long long>(H) * P, gn = static_cast<long long>(G) * N;
+    const long long least[5] = {inner, H, gn, gn, z ? inner : 0};
+    for (int i = 0; i < 5; ++i)
+        REQUIRE((i == 4 && !z) || (strides[i] >= least[i] && strides[i] < (1LL << 31) && (i == 1 || strides[i] % 8 == 0)), GDN_ERR_INVALID_ARG,
+                "%s: token strides must cover a token, be below 2^31 and (but for dt's) be multiples of 8", fn);
+    REQUIRE(aligned(x, 16) && aligned(B, 16) && aligned(C, 16) && aligned(z, 16) && aligned(out, 16) && aligned(state_pool, 16) &&
+                aligned(dt, 2) && aligned(A_log, 4) && aligned(D, 4) && aligned(dt_bias, 4) && aligned(cache_indices, 8) && aligned(dev_status, 4),
+            GDN_ERR_INVALID_ARG, "%s: x, B, C, z, out and state_pool must be 16-byte aligned", fn);
+    REQUIRE(T < (1LL << 31) && static_cast<long long>(num_seqs) * H * (P / 64) < (1LL << 31) && inner < (1LL << 31) && gn < (1LL << 31),
+            GDN_ERR_UNSUPPORTED, "%s: T and num_seqs * H must be below 2^31", fn);
+    const size_t ob = static_cast<size_t>(T) * inner * 2, sb = static_cast<size_t>(pool_size) * inner * N * 4;
+    auto span = [&](int i) { return (static_cast<size_t>(T - 1) * strides[i] + least[i]) * 2; };
+    const void* const in[5] = {x, dt, B, C, z};
+    for (int i = 0; i < 5; ++i) {
+        const size_t b = in[i] ? span(i) : 0;
+        REQUIRE(!any_overlap(out, ob, in[i], b) && !any_overlap(state_pool, sb, in[i], b), GDN_ERR_INVALID_ARG,
+                "%s: out or state_pool overlaps an input", fn);
+    }
+    const size_t hb = static_cast<size_t>(H) * 4;
+    REQUIRE(!any_overlap(out, ob, state_pool, sb) && !any_overlap(out, ob, A_log, hb) && !any_overlap(out, ob, dt_bias, hb) &&
+                !any_overlap(out, ob, D, D ? hb : 0),
+            GDN_ERR_INVALID_ARG, "%s: out overlaps another buffer", fn);
+    std::memset(a, 0, sizeof(*a));
+    a->x = static_cast<const uint16_t*>(x);
+    a->dt = static_cast<const uint16_t*>(dt);
+    a->B = static_cast<const uint16_t*>(B);
+    a->C = static_cast<const uint16_t*>(C);
+    a->z = static_cast<const uint16_t*>(z);
+    a->x_stride = strides[0];
+    a->dt_stride = strides[1];
+    a->b_stride = strides[2];
+    a->c_stride = strides[3];
+    a->z_stride = strides[4];
+    a->A_log = A_log;
+    a->D = D;
+    a->dt_bias = dt_bias;
+    a->state = state_pool;
+    a->slots = cache_indices;
+    a->out = static_cast<uint16_t*>(out);
+    a->status = dev_status;
+    a->T = T;
+    a->num_seqs = num_seqs;
+    a->pool_size = pool_size;
+    a->H = H;
+    a->P = P;
+    a->G = G;
+    return GDN_OK;
+}
+
+static gdn_status ssm_sizes(const char* fn, int num_seqs, int64_t T, int pool_size, int H, int P, int G, int N) {
+    REQUIRE(num_seqs >= 0 && T >= 0 && pool_size >= 0 && H >= 1 && G >= 1, GDN_ERR_INVALID_ARG,
+            "%s: sizes must be num_seqs, T, pool_size >= 0 and H, G >= 1", fn);
+    REQUIRE(H % G == 0, GDN_ERR_INVALID_ARG, "%s: H (%d) must be a multiple of G (%d)", fn, H, G);
+    REQUIRE((P == 64 || P == 128) && (N == 64 || N == 128), GDN_ERR_UNSUPPORTED, "%s: P and N must be 64 or 128 (got %d and %d)", fn, P, N);
+    return GDN_OK;
+}
+
+extern "C" gdn_status ssm_decode_step(const void* x, const void* dt, const void* B, const void* C, const void* z,
+                                      const int64_t* token_strides, const float* A_log, const float* D, const float* dt_bias,
+                                      float* state_pool, int pool_size, const int64_t* cache_indices, int num_seqs, int H, int P,
+                                      int G, int N, void* out, int32_t* dev_status, gdn_stream_t stream) {
+    const char* fn = "ssm_decode_step";
+    gdn_status s = ssm_sizes(fn, num_seqs, num_seqs, pool_size, H, P, G, N);
+    if (s != GDN_OK || num_seqs == 0) return s;
+    gdn::SsmArgs a;
+    s = ssm_check(fn, &a, x, dt, B, C, z, token_strides, A_log, D, dt_bias, state_pool, pool_size, cache_indices, num_seqs, num_seqs, H, P,
+                  G, N, out, dev_status);
+    if (s != GDN_OK) return s;
+    gdn::launch_ssm_steps(a, N, static_cast<cudaStream_t>(stream));
+    return launched(fn);
+}
+
+extern "C" size_t ssm_prefill_workspace_size(int num_seqs, int64_t T, int H, int P, int N) {
+    if (num_seqs < 0 || T < 0 || H < 1 || (P != 64 && P != 128) || (N != 64 && N != 128)) return 0;
+    return gdn::ssm_workspace_bytes(num_seqs, T, H, P, N);
+}
+
+extern "C" gdn_status ssm_prefill_chunked(const void* x, const void* dt, const void* B, const void* C, const void* z,
+                                          const int64_t* token_strides, const float* A_log, const float* D, const float* dt_bias,
+                                          float* state_pool, int pool_size, const int64_t* cache_indices, const int64_t* cu_seqlens,
+                                          int num_seqs, int64_t T, int64_t max_len, int H, int P, int G, int N, void* out,
+                                          void* workspace, size_t workspace_bytes, int32_t* dev_status, gdn_stream_t stream) {
+    const char* fn = "ssm_prefill_chunked";
+    gdn_status s = ssm_sizes(fn, num_seqs, T, pool_size, H, P, G, N);
+    if (s != GDN_OK || num_seqs == 0 || T == 0) return s;
+    REQUIRE(max_len >= 0, GDN_ERR_INVALID_ARG, "%s: max_len must not be negative", fn);
+    gdn::SsmArgs a;
+    s = ssm_check(fn, &a, x, dt, B, C, z, token_strides, A_log, D, dt_bias, state_pool, pool_size, cache_indices, num_seqs, T, H, P, G, N,
+                  out, dev_status);
+    if (s != GDN_OK) return s;
+    REQUIRE(cu_seqlens && aligned(cu_seqlens, 8), GDN_ERR_INVALID_ARG, "%s: null or misaligned cu_seqlens", fn);
+    const size_t need = gdn::ssm_workspace_bytes(num_seqs, T, H, P, N);
+    REQUIRE(need == 0 || (workspace && workspace_bytes >= need), GDN_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed (got %zu)", fn, need,
+            workspace ? workspace_bytes : size_t(0));
+    REQUIRE(aligned(workspace, 16), GDN_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
+    const size_t inner = static_cast<size_t>(H) * P, sb = static_cast<size_t>(pool_size) * inner * N * 4;
+    REQUIRE(!any_overlap(workspace, need, out, static_cast<size_t>(T) * inner * 2) && !any_overlap(workspace, need, state_pool, sb),
+            GDN_ERR_INVALID_ARG, "%s: workspace overlaps another buffer", fn);
+    a.cu = cu_seqlens;
+    const cudaError_t e = gdn::launch_ssm_prefill(a, N, max_len, workspace, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+    return launched(fn);
+}
+
+extern "C" gdn_status add_rms_norm(const void* x, int64_t x_stride, void* residual, gdn_dtype dtype, const float* weight, float eps,
+                                   int64_t T, int C, void* out, gdn_dtype out_dtype, float* scale, int group, gdn_stream_t stream) {
+    const char* fn = "add_rms_norm";
+    REQUIRE(T >= 0 && C >= 1, GDN_ERR_INVALID_ARG, "%s: sizes must be T >= 0 and C >= 1", fn);
+    REQUIRE(dtype == GDN_BF16 || dtype == GDN_F16, GDN_ERR_INVALID_ARG, "%s: dtype must be GDN_BF16 or GDN_F16", fn);
+    REQUIRE(out_dtype == dtype || out_dtype == GDN_E4M3, GDN_ERR_INVALID_ARG, "%s: out_dtype must be dtype or GDN_E4M3", fn);
+    REQUIRE(C % 8 == 0 && C <= 32768, GDN_ERR_UNSUPPORTED, "%s: C must be a multiple of 8, at most 32768 (got %d)", fn, C);
+    const bool f8 = out_dtype == GDN_E4M3;
+    REQUIRE(f8 == (scale != nullptr) || T == 0, GDN_ERR_INVALID_ARG, "%s: scale is for an 8-bit output, which needs it", fn);
+    REQUIRE(group == 0 || (f8 && (group == 32 || group == 64 || group == 128 || group == 256) && C % group == 0), GDN_ERR_UNSUPPORTED,
+            "%s: group must be 0, or (8 bits) 32, 64, 128 or 256 and a divisor of C (got %d)", fn, group);
+    REQUIRE(T < (1LL << 31), GDN_ERR_UNSUPPORTED, "%s: T must be below 2^31", fn);
+    if (T == 0) return GDN_OK;
+    REQUIRE(x && weight && out, GDN_ERR_INVALID_ARG, "%s: null pointer", fn);
+    REQUIRE(x_stride >= C && x_stride % 8 == 0 && x_stride < (1LL << 31), GDN_ERR_INVALID_ARG,
+            "%s: x_stride must be a multiple of 8, at least C and below 2^31", fn);
+    REQUIRE(aligned(x, 16) && aligned(residual, 16) && aligned(weight, 16) && aligned(out, 16) && aligned(scale, 4), GDN_ERR_INVALID_ARG,
+            "%s: x, residual, weight and out must be 16-byte aligned", fn);
+    const size_t xb = (static_cast<size_t>(T - 1) * x_stride + C) * 2, rb = residual ? static_cast<size_t>(T) * C * 2 : 0;
+    const size_t ob = static_cast<size_t>(T) * C * (f8 ? 1 : 2), sb = f8 ? static_cast<size_t>(T) * (group ? C / group : 1) * 4 : 0;
+    const size_t wb = static_cast<size_t>(C) * 4;
+    REQUIRE((out == x && !f8 && x_stride == C) || !any_overlap(out, ob, x, xb), GDN_ERR_INVALID_ARG,
+            "%s: out overlaps x (it may be x itself, in 16 bits and dense)", fn);
+    REQUIRE(!any_overlap(residual, rb, x, xb) && !any_overlap(out, ob, residual, rb) && !any_overlap(out, ob, weight, wb) &&
+                !any_overlap(residual, rb, weight, wb) && !any_overlap(scale, sb, x, xb) && !any_overlap(scale, sb, residual, rb) &&
+                !any_overlap(scale, sb, out, ob) && !any_overlap(scale, sb, weight, wb),
+            GDN_ERR_INVALID_ARG, "%s: residual, out or scale overlaps another buffer", fn);
+    gdn::NormArgs a;
+    a.x = static_cast<const uint16_t*>(x);
+    a.x_stride = x_stride;
+    a.residual = static_cast<uint16_t*>(residual);
+    a.w = weight;
+    a.out = out;
+    a.scale = scale;
+    a.T = T;
+    a.C = C;
+    a.lanes = group / 8;
+    a.eps = eps;
+    gdn::launch_norm(a, dtype == GDN_F16, f8, static_cast<cudaStream_t>(stream));
+    return launched(fn);
+}

@@ -1,4 +1,4 @@
-// cache.cu -- launch of the cache write and read kernels (cache.cuh).
+// cache.cu -- launch of the cache write, read and append kernels (cache.cuh).
 #include "cache.cuh"
 #include "launch.h"
 
@@ -43,8 +43,24 @@ void read_d(const CacheMoveArgs& a, bool f16, bool f8, cudaStream_t stream) {
     else if (f16) read<D, true, true>(a, stream);
     else read<D, false, true>(a, stream);
 }
+template <int D, bool F16, bool F8, bool HALVES>
+void append(const AppendArgs& a, cudaStream_t stream) {
+    constexpr int groups = cache::kThreads / (D / 8), heads = 4;
+    const dim3 grid(static_cast<unsigned>((a.T + groups - 1) / groups), (a.Hq + 2 * a.H + heads - 1) / heads);
+    cache::attn_cache_append_kernel<D, F16, F8, HALVES, heads><<<grid, cache::kThreads, 0, stream>>>(a);
+}
+template <int D, bool HALVES>
+void append_d(const AppendArgs& a, bool f16, bool f8, cudaStream_t stream) {
+    if (f8) f16 ? append<D, true, true, HALVES>(a, stream) : append<D, false, true, HALVES>(a, stream);
+    else f16 ? append<D, true, false, HALVES>(a, stream) : append<D, false, false, HALVES>(a, stream);
+}
 }  // namespace
 
+void launch_cache_append(const AppendArgs& a, int D, bool f16, bool f8, bool neighbours, cudaStream_t stream) {
+    if (D == 64) neighbours ? append_d<64, false>(a, f16, f8, stream) : append_d<64, true>(a, f16, f8, stream);
+    else if (D == 128) neighbours ? append_d<128, false>(a, f16, f8, stream) : append_d<128, true>(a, f16, f8, stream);
+    else neighbours ? append_d<256, false>(a, f16, f8, stream) : append_d<256, true>(a, f16, f8, stream);
+}
 void launch_cache_write(const CacheMoveArgs& a, int D, bool f16, bool f8, cudaStream_t stream) {
     if (D == 64) write_d<64>(a, f16, f8, stream);
     else if (D == 128) write_d<128>(a, f16, f8, stream);

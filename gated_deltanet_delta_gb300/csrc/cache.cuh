@@ -41,6 +41,42 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
     return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
+// The eight values of a lane, of a row that LANES lanes hold, to e4m3; the row's scale.
+template <int LANES, bool F16>
+__device__ __forceinline__ uint2 quantise8(const uint32_t (&w)[4], float& scale) {
+    constexpr float kTop = F16 ? 0x1p8f : 0x1p120f;  // the largest scale that the type's finite rows have
+    float f[8], mx = 0.f;                            // fmaxf passes over NaN
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 p = attn::unpack2<F16>(w[j]);
+        f[2 * j] = p.x;
+        f[2 * j + 1] = p.y;
+        mx = fmaxf(mx, fmaxf(fabsf(p.x), fabsf(p.y)));
+    }
+    mx = row_max<LANES>(mx, kFullMask);
+    // Rows of scale kTop, and rows with infinities, which are not to count.  In a branch: as selects in every row
+    // both together took 14 % more time.
+    if (mx > 224.f * kTop) {
+        mx = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (fabsf(f[j]) < INFINITY) mx = fmaxf(mx, fabsf(f[j] = fminf(fmaxf(f[j], -240.f * kTop), 240.f * kTop)));
+            else f[j] = __int_as_float(0x7fffffff);
+        }
+        mx = row_max<LANES>(mx, LANES == 32 ? kFullMask : ((1u << LANES % 32) - 1) << (threadIdx.x & (32 - LANES)));
+    }
+    // 448 = 1.75 2^8: the exponent is mx's less 8, less 7 where mx's significand is over 1.75
+    const uint32_t u = __float_as_uint(mx);
+    int e = static_cast<int>(u >> 23) - 127 - ((u & 0x7fffffu) > 0x600000u ? 7 : 8);
+    e = max(e, -100);
+    if (mx == 0.f) e = 0;
+    scale = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] *= inv;
+    return make_uint2(to_e4m3x2(f[0], f[1]) | to_e4m3x2(f[2], f[3]) << 16, to_e4m3x2(f[4], f[5]) | to_e4m3x2(f[6], f[7]) << 16);
+}
+
 // kv: 0 moves keys, 1 values (blockIdx.z).
 template <int D, bool F16, bool F8, int TOKENS>
 __global__ void __launch_bounds__(kThreads) attn_cache_write_kernel(const __grid_constant__ CacheMoveArgs a) {
@@ -72,42 +108,9 @@ __global__ void __launch_bounds__(kThreads) attn_cache_write_kernel(const __grid
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        float f[8], scale = 1.f;
+        float scale = 1.f;
         uint2 q = make_uint2(0, 0);
-        if constexpr (F8) {
-            constexpr float kTop = F16 ? 0x1p8f : 0x1p120f;  // the largest scale that the type's finite rows have
-            float mx = 0.f;                                  // fmaxf passes over NaN
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 p = attn::unpack2<F16>(w[j]);
-                f[2 * j] = p.x;
-                f[2 * j + 1] = p.y;
-                mx = fmaxf(mx, fmaxf(fabsf(p.x), fabsf(p.y)));
-            }
-            mx = row_max<LANES>(mx, kFullMask);
-            // Rows of scale kTop, and rows with infinities, which are not to count.  In a branch: as selects in every row
-            // both together took 14 % more time.
-            if (mx > 224.f * kTop) {
-                mx = 0.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (fabsf(f[j]) < INFINITY) mx = fmaxf(mx, fabsf(f[j] = fminf(fmaxf(f[j], -240.f * kTop), 240.f * kTop)));
-                    else f[j] = __int_as_float(0x7fffffff);
-                }
-                mx = row_max<LANES>(mx, LANES == 32 ? kFullMask : ((1u << LANES % 32) - 1) << (threadIdx.x & (32 - LANES)));
-            }
-            // 448 = 1.75 2^8: the exponent is mx's less 8, less 7 where mx's significand is over 1.75
-            const uint32_t u = __float_as_uint(mx);
-            int e = static_cast<int>(u >> 23) - 127 - ((u & 0x7fffffu) > 0x600000u ? 7 : 8);
-            e = max(e, -100);
-            if (mx == 0.f) e = 0;
-            scale = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-            const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] *= inv;
-            q.x = to_e4m3x2(f[0], f[1]) | to_e4m3x2(f[2], f[3]) << 16;
-            q.y = to_e4m3x2(f[4], f[5]) | to_e4m3x2(f[6], f[7]) << 16;
-        }
+        if constexpr (F8) q = quantise8<LANES, F16>(w, scale);
         const int k = group + i * GROUPS;
         const long long row = k < TOKENS ? rows_s[k] : -1;
         if (row < 0) continue;
@@ -190,6 +193,108 @@ __global__ void __launch_bounds__(kThreads) attn_cache_read_kernel(const __grid_
         }
         uint16_t* dst = kv ? a.v_out : a.k_out;
         __stcs(reinterpret_cast<uint4*>(dst + ((t0 + group + i * GROUPS) * a.H + h) * D + lane * 8), x[i]);
+    }
+}
+
+// Rotation by position on the way: query rows to q_out, key rows to the cache, and value rows, which are not turned.  The
+// pairs (a, b) of features become (a cos - b sin, b cos + a sin), each product and sum rounded to fp32 by itself, so
+// that the result does not depend on how a compiler contracts them; the turned row is rounded to its type before it is quantised,
+// so that an 8-bit cache holds what attn_cache_write would make of the 16-bit rows.
+//
+// A copy too: each row is read once and written once.  A group of D / 8 lanes takes HEADS heads of one token, so that the token's
+// row of the table is read once for HEADS rows; the heads' loads are in flight together.  HALVES: feature i's partner
+// is i + turned / 2, in another lane of the group: it comes by a shuffle of the packed row.  Else 2 i and 2 i + 1 are partners.
+template <int D, bool F16, bool F8, bool HALVES, int HEADS>
+__global__ void __launch_bounds__(kThreads) attn_cache_append_kernel(const __grid_constant__ AppendArgs a) {
+    constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
+    const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+    const long long t = static_cast<long long>(blockIdx.x) * GROUPS + group;
+    const int h0 = blockIdx.y * HEADS, total = a.Hq + 2 * a.H;
+    const bool here = t < a.T;
+    uint4 x[HEADS];
+#pragma unroll
+    for (int i = 0; i < HEADS; ++i) {
+        const int h = h0 + i;
+        const uint16_t* src = h < a.Hq          ? a.q + t * a.q_stride + static_cast<long long>(h) * D
+                              : h < a.Hq + a.H  ? a.k + t * a.k_stride + static_cast<long long>(h - a.Hq) * D
+                                                : a.v + t * a.v_stride + static_cast<long long>(h - a.Hq - a.H) * D;
+        x[i] = here && h < total ? __ldcs(reinterpret_cast<const uint4*>(src + lane * 8)) : make_uint4(0, 0, 0, 0);
+    }
+    const long long pos = here ? a.positions[t] : -1;
+    const bool known = pos >= 0 && pos < a.max_pos;
+    if (here && !known && lane == 0 && blockIdx.y == 0) atomicOr(a.status, kStatusBadPosition);
+    // the cached row of the token's first head (-1: none); a negative slot: the token's key and value are not kept
+    long long row0 = -1;
+    if (known && h0 + HEADS > a.Hq) {
+        const long long slot = a.slots[t];
+        if (slot >= 0) {
+            const long long page = (slot | a.page_size) >> 32 ? slot / a.page_size : static_cast<unsigned>(slot) / static_cast<unsigned>(a.page_size);
+            if (page < a.num_pages) row0 = page * a.H * a.page_size + (slot - page * a.page_size);
+            else if (lane == 0) atomicOr(a.status, kStatusBadCacheIndex);
+        }
+    }
+    // cos and sin of this lane's features: HALVES: of feature i mod turned / 2; else of pair i / 2
+    const int half = a.turned / 2;
+    const bool turns = lane * 8 < a.turned;
+    constexpr int NC = HALVES ? 8 : 4;
+    float c[NC], s[NC];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) c[j] = 1.f, s[j] = 0.f;
+    if (known && turns && h0 < a.Hq + a.H) {
+        const float* tab = a.rotation + pos * a.turned + (HALVES ? (lane * 8 < half ? lane * 8 : lane * 8 - half) : lane * 4);
+#pragma unroll
+        for (int j = 0; j < NC; j += 4) {
+            const float4 u = __ldg(reinterpret_cast<const float4*>(tab + j)), w = __ldg(reinterpret_cast<const float4*>(tab + half + j));
+            c[j] = u.x, c[j + 1] = u.y, c[j + 2] = u.z, c[j + 3] = u.w;
+            s[j] = w.x, s[j + 1] = w.y, s[j + 2] = w.z, s[j + 3] = w.w;
+        }
+    }
+    const bool first = lane * 8 < half;
+    const int base = threadIdx.x & 31 & ~(LANES - 1);
+    const int partner = base + (turns ? (first ? lane + half / 8 : lane - half / 8) : lane);
+#pragma unroll
+    for (int i = 0; i < HEADS; ++i) {
+        const int h = h0 + i;
+        if (h >= total) break;  // the same for the whole CTA
+        uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        if (h < a.Hq + a.H) {
+            if constexpr (HALVES) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 p = attn::unpack2<F16>(w[j]), o = attn::unpack2<F16>(__shfl_sync(kFullMask, w[j], partner));
+                    // the first of a pair: a cos - b sin; the second: b cos + a sin
+                    const float m0 = __fmul_rn(o.x, s[2 * j]), m1 = __fmul_rn(o.y, s[2 * j + 1]);
+                    const float r0 = __fadd_rn(__fmul_rn(p.x, c[2 * j]), first ? -m0 : m0);
+                    const float r1 = __fadd_rn(__fmul_rn(p.y, c[2 * j + 1]), first ? -m1 : m1);
+                    const uint32_t r = attn::pack2<F16>(r0, r1);
+                    if (turns) w[j] = r;  // what is not turned keeps its bits
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 p = attn::unpack2<F16>(w[j]);
+                    const float r0 = __fsub_rn(__fmul_rn(p.x, c[j]), __fmul_rn(p.y, s[j]));
+                    const float r1 = __fadd_rn(__fmul_rn(p.y, c[j]), __fmul_rn(p.x, s[j]));
+                    if (turns) w[j] = attn::pack2<F16>(r0, r1);
+                }
+            }
+        }
+        if (h < a.Hq) {
+            if (known) __stcs(reinterpret_cast<uint4*>(a.q_out + t * a.q_out_stride + static_cast<long long>(h) * D + lane * 8), make_uint4(w[0], w[1], w[2], w[3]));
+            continue;
+        }
+        const bool val = h >= a.Hq + a.H;
+        const long long row = row0 + static_cast<long long>(h - a.Hq - (val ? a.H : 0)) * a.page_size;
+        if constexpr (F8) {
+            float scale;
+            const uint2 q = quantise8<LANES, F16>(w, scale);
+            if (row0 < 0) continue;
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(val ? a.vc : a.kc) + row * D + lane * 8) = q;
+            if (lane == 0) (val ? a.vs : a.ks)[row] = scale;
+        } else {
+            if (row0 < 0) continue;
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(val ? a.vc : a.kc) + row * D + lane * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
     }
 }
 

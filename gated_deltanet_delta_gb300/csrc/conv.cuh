@@ -1,0 +1,234 @@
+// conv.cuh -- the short causal convolution of packed sequences, channel by channel:
+//     y[t, c] = act(bias_c + sum_j w[c, j] x[t - (TAPS - 1) + j, c]),   act(y) = y / (1 + e^-y) or y,
+// where the tokens ahead of a sequence's first are its history, TAPS - 1 values per channel that the pool keeps from call
+// to call (oldest first, the layout that the decode window's history has).
+//
+// Each value is read once and written once: the bound is HBM.  A thread has eight channels (16-byte accesses) of
+// kTokens consecutive tokens, with the weights in registers; the TAPS - 1 tokens ahead of its tile come from L2, where the
+// tile before read them.  The new history is written by a kernel of its own behind the first: in the same one, the CTA that
+// reaches a sequence's end would overwrite what the CTA at its start has yet to read.  A step of one token per
+// sequence has no such order to keep, and is one launch.
+#pragma once
+
+#include "attn_mma.cuh"
+#include "common.cuh"
+#include "kernel_args.h"
+
+namespace gdn {
+namespace conv {
+
+constexpr int kThreads = 128;
+constexpr int kTokens = 16;
+
+// A token's sequence: which, where it begins and ends; n = -1 for a token of no (well-formed) sequence.
+struct Place {
+    long long begin, end;
+    int n;
+};
+__device__ __forceinline__ Place place_of(const int64_t* cu, int num_seqs, long long T, long long t) {
+    int lo = 0, hi = num_seqs;  // the last sequence that begins at or before t
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (cu[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    Place p{cu[lo], cu[lo + 1], lo};
+    if (p.begin < 0 || p.begin > t || t >= p.end || p.end > T) p.n = -1;
+    return p;
+}
+
+template <int TAPS>
+struct Weights {
+    float w[TAPS][8], b[8];
+    __device__ __forceinline__ void load(const ConvArgs& a, int c) {
+        float f[8 * TAPS];
+        const float4* src = reinterpret_cast<const float4*>(a.w + static_cast<long long>(c) * TAPS);
+#pragma unroll
+        for (int i = 0; i < 2 * TAPS; ++i) reinterpret_cast<float4*>(f)[i] = __ldg(src + i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+#pragma unroll
+            for (int j = 0; j < TAPS; ++j) w[j][i] = f[i * TAPS + j];
+            b[i] = a.bias ? __ldg(a.bias + c + i) : 0.f;
+        }
+    }
+};
+
+// TAPS - 1 values of each of eight channels, oldest first.
+template <int TAPS>
+struct Past {
+    float v[TAPS - 1][8];
+    __device__ __forceinline__ void load(const float* hist) {
+        float f[8 * (TAPS - 1)];
+#pragma unroll
+        for (int i = 0; i < 2 * (TAPS - 1); ++i) reinterpret_cast<float4*>(f)[i] = reinterpret_cast<const float4*>(hist)[i];
+#pragma unroll
+        for (int j = 0; j < TAPS - 1; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[j][i] = f[i * (TAPS - 1) + j];
+    }
+    __device__ __forceinline__ void store(float* hist) const {
+        float f[8 * (TAPS - 1)];
+#pragma unroll
+        for (int j = 0; j < TAPS - 1; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i * (TAPS - 1) + j] = v[j][i];
+#pragma unroll
+        for (int i = 0; i < 2 * (TAPS - 1); ++i) reinterpret_cast<float4*>(hist)[i] = reinterpret_cast<const float4*>(f)[i];
+    }
+    __device__ __forceinline__ void push(const float (&x)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+#pragma unroll
+            for (int j = 0; j + 1 < TAPS - 1; ++j) v[j][i] = v[j + 1][i];
+            v[TAPS - 2][i] = x[i];
+        }
+    }
+};
+
+template <bool F16>
+__device__ __forceinline__ void widen8(const uint4& p, float (&f)[8]) {
+    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 u = attn::unpack2<F16>(w[j]);
+        f[2 * j] = u.x;
+        f[2 * j + 1] = u.y;
+    }
+}
+
+// One token's eight outputs.
+template <int TAPS, bool F16>
+__device__ __forceinline__ uint4 token(const Weights<TAPS>& w, const Past<TAPS>& p, const float (&x)[8], bool silu) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        y[i] = w.b[i];
+#pragma unroll
+        for (int j = 0; j < TAPS - 1; ++j) y[i] = fmaf(w.w[j][i], p.v[j][i], y[i]);
+        y[i] = fmaf(w.w[TAPS - 1][i], x[i], y[i]);
+        // e^-y beyond the type's range gives y / infinity = -0, the limit
+        if (silu) y[i] = __fdividef(y[i], 1.f + __expf(fminf(-y[i], 80.f)));
+    }
+    return make_uint4(attn::pack2<F16>(y[0], y[1]), attn::pack2<F16>(y[2], y[3]), attn::pack2<F16>(y[4], y[5]), attn::pack2<F16>(y[6], y[7]));
+}
+
+// Where channel c of token 0 goes, and the distance between tokens.
+__device__ __forceinline__ uint16_t* out_of(const ConvArgs& a, int c, int& width) {
+    const int i = c < a.width[0] ? 0 : c < a.width[0] + a.width[1] ? 1 : 2;
+    width = a.width[i];
+    return a.out[i] + (c - (i > 0 ? a.width[0] : 0) - (i > 1 ? a.width[1] : 0));
+}
+
+// One token per sequence: outputs, and the history in place.
+template <int TAPS, bool F16>
+__global__ void __launch_bounds__(kThreads) short_conv_step_kernel(const __grid_constant__ ConvArgs a) {
+    const int n = blockIdx.x, c = (blockIdx.y * kThreads + threadIdx.x) * 8;
+    const long long slot = a.slots[n];
+    if (slot < 0 || slot >= a.pool_size) {
+        if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(a.status, kStatusBadCacheIndex);
+        return;
+    }
+    if (c >= a.C) return;
+    float x[8];
+    widen8<F16>(__ldcs(reinterpret_cast<const uint4*>(a.x + n * a.x_stride + c)), x);
+    float* hist = a.hist + (slot * a.C + c) * (TAPS - 1);
+    Past<TAPS> p;
+    p.load(hist);
+    Weights<TAPS> w;
+    w.load(a, c);
+    int width;
+    uint16_t* out = out_of(a, c, width);
+    *reinterpret_cast<uint4*>(out + static_cast<long long>(n) * width) = token<TAPS, F16>(w, p, x, a.silu);
+    p.push(x);
+    p.store(hist);
+}
+
+template <int TAPS, bool F16>
+__global__ void __launch_bounds__(kThreads) short_conv_kernel(const __grid_constant__ ConvArgs a) {
+    __shared__ long long slot_s[kTokens];  // of each token; -1: the token belongs to no sequence, -2: as the token before
+    __shared__ int ahead_s[kTokens];       // tokens of its sequence ahead of it, at most TAPS - 1
+    const int c = (blockIdx.y * kThreads + threadIdx.x) * 8;
+    const long long t0 = static_cast<long long>(blockIdx.x) * kTokens;
+    const int count = static_cast<int>(a.T - t0 < kTokens ? a.T - t0 : kTokens);
+    if (threadIdx.x < kTokens) {
+        const int i = threadIdx.x;
+        long long slot = -1;
+        int ahead = 0;
+        if (i < count) {
+            const Place p = place_of(a.cu, a.num_seqs, a.T, t0 + i);
+            if (p.n >= 0) {
+                slot = a.slots[p.n];
+                if (slot < 0 || slot >= a.pool_size) slot = -1;  // reported by the history's kernel
+                ahead = static_cast<int>(t0 + i - p.begin < TAPS - 1 ? t0 + i - p.begin : TAPS - 1);
+            }
+        }
+        slot_s[i] = slot;
+        ahead_s[i] = ahead;
+    }
+    const uint16_t* src = a.x + t0 * a.x_stride + c;
+    const bool on = c < a.C;
+    uint4 x[kTokens];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) x[i] = on && i < count ? *reinterpret_cast<const uint4*>(src + i * a.x_stride) : make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    if (!on) return;
+    Weights<TAPS> w;
+    w.load(a, c);
+    int width;
+    uint16_t* out = out_of(a, c, width) + t0 * width;
+    Past<TAPS> p;
+    {  // ahead of the tile: its first token's sequence's tokens, and before those the history
+        const int ahead = ahead_s[0];
+        const long long slot = slot_s[0];
+        if (slot >= 0 && ahead < TAPS - 1) {
+            p.load(a.hist + (slot * a.C + c) * (TAPS - 1));
+        } else {
+#pragma unroll
+            for (int j = 0; j < TAPS - 1; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) p.v[j][i] = 0.f;
+        }
+        for (int j = slot >= 0 ? ahead : 0; j > 0; --j) {
+            float f[8];
+            widen8<F16>(*reinterpret_cast<const uint4*>(src - j * a.x_stride), f);
+            p.push(f);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        if (i >= count) break;
+        const long long slot = slot_s[i];
+        if (i > 0 && ahead_s[i] == 0 && slot >= 0) p.load(a.hist + (slot * a.C + c) * (TAPS - 1));
+        float f[8];
+        widen8<F16>(x[i], f);
+        if (slot >= 0) __stcs(reinterpret_cast<uint4*>(out + static_cast<long long>(i) * width), token<TAPS, F16>(w, p, f, a.silu));
+        p.push(f);
+    }
+}
+
+// The history behind each sequence's last token, and the report of malformed bounds and slots.
+template <int TAPS, bool F16>
+__global__ void __launch_bounds__(kThreads) short_conv_history_kernel(const __grid_constant__ ConvArgs a) {
+    const int n = blockIdx.x, c = (blockIdx.y * kThreads + threadIdx.x) * 8;
+    const long long begin = a.cu[n], end = a.cu[n + 1], slot = a.slots[n];
+    const bool bad = begin < 0 || end < begin || end > a.T, off = slot < 0 || slot >= a.pool_size;
+    if (bad || off) {
+        if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(a.status, (bad ? kStatusBadSeqlens : 0) | (off ? kStatusBadCacheIndex : 0));
+        return;
+    }
+    if (c >= a.C || end == begin) return;
+    float* hist = a.hist + (slot * a.C + c) * (TAPS - 1);
+    Past<TAPS> p;
+    if (end - begin < TAPS - 1) p.load(hist);
+    const int fresh = static_cast<int>(end - begin < TAPS - 1 ? end - begin : TAPS - 1);
+    for (int j = fresh; j > 0; --j) {
+        float f[8];
+        widen8<F16>(*reinterpret_cast<const uint4*>(a.x + (end - j) * a.x_stride + c), f);
+        p.push(f);
+    }
+    p.store(hist);
+}
+
+}  // namespace conv
+}  // namespace gdn

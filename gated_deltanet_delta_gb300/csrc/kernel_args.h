@@ -170,7 +170,7 @@ constexpr int kWinMaxTok = 8;
 
 // Bits of the device status word (GDN_STATUS_* of gdn.h).
 constexpr int kStatusBadCacheIndex = 1, kStatusBadSeqlens = 2, kStatusTimeout = 4, kStatusBadProbs = 8,
-              kStatusBadToken = 16;
+              kStatusBadToken = 16, kStatusBadPosition = 32;
 
 // Keys of a sequence, and a few tiles more (positions are looked at up to three tiles ahead), count in 32 bits.
 constexpr int kAttnMaxKeys = 0x7fffffff - 1023;
@@ -245,6 +245,74 @@ struct VerifyArgs {
     int64_t* tokens;       // [N, T + 1]
     int32_t* status;
     int N, T, V;
+};
+
+// Rotation by position on the way to the cache: q to dense rows, k and v to the cache.
+struct AppendArgs {
+    const uint16_t* q;       // [T, Hq, D]; null: no queries
+    const uint16_t* k;       // [T, H, D]
+    const uint16_t* v;
+    long long q_stride, k_stride, v_stride, q_out_stride;
+    uint16_t* q_out;
+    const float* rotation;   // [positions, turned]: cos, then sin
+    const int64_t* positions;
+    const int64_t* slots;
+    void* kc;
+    void* vc;
+    float* ks;
+    float* vs;
+    int32_t* status;
+    long long T, num_pages, max_pos;
+    int page_size, Hq, H, turned;
+};
+
+// The short convolution: channel c of token t goes to out[i] + t * width[i] + c - first[i].
+struct ConvArgs {
+    const uint16_t* x;      // [T, C], tokens x_stride elements apart
+    long long x_stride;
+    const float* w;         // [C, taps]
+    const float* bias;      // [C] or null
+    float* hist;            // [pool, C, taps - 1], oldest first
+    const int64_t* slots;   // [num_seqs]
+    const int64_t* cu;      // [num_seqs + 1] or null: one token per sequence
+    uint16_t* out[3];
+    int width[3];
+    int32_t* status;
+    long long T;
+    int C, num_seqs, pool_size, silu;
+};
+
+// The selective state space scan.
+struct SsmArgs {
+    const uint16_t* x;      // [T, H, P]
+    const uint16_t* dt;     // [T, H]
+    const uint16_t* B;      // [T, G, S]
+    const uint16_t* C;
+    const uint16_t* z;      // [T, H, P] or null
+    long long x_stride, dt_stride, b_stride, c_stride, z_stride;
+    const float* A_log;     // [H]
+    const float* D;         // [H] or null
+    const float* dt_bias;   // [H]
+    float* state;           // [pool, H, P, S]
+    const int64_t* slots;   // [num_seqs]
+    const int64_t* cu;      // [num_seqs + 1] or null: one token per sequence
+    uint16_t* out;          // [T, H, P]
+    int32_t* status;
+    long long T;
+    int num_seqs, pool_size, H, P, G;
+    int tiles;              // row tiles per head
+};
+
+struct NormArgs {
+    const uint16_t* x;      // [T, C], rows x_stride elements apart
+    long long x_stride;
+    uint16_t* residual;     // [T, C], updated in place, or null
+    const float* w;         // [C]
+    void* out;              // [T, C]
+    float* scale;           // [T, C / group] (e4m3)
+    long long T;
+    int C, lanes;           // lanes per group (group / 8); 0: one scale per row
+    float eps;
 };
 
 }  // namespace gdn

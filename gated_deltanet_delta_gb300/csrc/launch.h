@@ -48,6 +48,16 @@ cudaError_t launch_attn(const AttnArgs& a, void* workspace, int D, bool f8, int 
 // Rows into and out of a paged cache.  f16: the dense side is binary16 (else bf16).
 void launch_cache_write(const CacheMoveArgs& a, int D, bool f16, bool f8, cudaStream_t stream);
 void launch_cache_read(const CacheMoveArgs& a, int D, bool f16, bool f8, cudaStream_t stream);
+void launch_cache_append(const AppendArgs& a, int D, bool f16, bool f8, bool neighbours, cudaStream_t stream);
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream);
+
+// taps in 2 .. 4.
+void launch_conv(const ConvArgs& a, int taps, bool f16, cudaStream_t stream);
+// One token per sequence, or sequences of few tokens each: the recurrence as it stands.  S in {64, 128}.
+void launch_ssm_steps(SsmArgs a, int S, cudaStream_t stream);
+// Sequences of any length; max_len (the longest) only chooses the kernel.
+size_t ssm_workspace_bytes(int num_seqs, long long T, int H, int P, int S);
+cudaError_t launch_ssm_prefill(const SsmArgs& a, int S, long long max_len, void* workspace, cudaStream_t stream);
+void launch_norm(const NormArgs& a, bool f16, bool f8, cudaStream_t stream);
 
 }  // namespace gdn

@@ -1,0 +1,144 @@
+// norm.cuh -- root-mean-square norm with the residual's addition:
+//     r = x + residual (rounded to the rows' type, and stored: the residual stream);   y = r / sqrt(mean(r^2) + eps) * w,
+// in the rows' type, or in e4m3 with scale = max |y| / 448 for each group of features (1 where all are zero, at least
+// 2^-126): for the operand of a product in 8 bits the whole range is used; a power of two would leave up to half of it.
+//
+// Each value is read once and written once: the bound is HBM.  blockDim.x threads hold a row in registers, R
+// pieces of eight features each, blockDim.y rows per CTA; the sum of squares is taken over the rounded r, in fp32.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "attn_mma.cuh"
+#include "common.cuh"
+#include "kernel_args.h"
+
+namespace gdn {
+namespace norm {
+
+constexpr int kMaxThreads = 1024;
+
+// Sum (or largest) over the row's threads; every thread gets it.  buf: 32 floats per row.
+template <bool MAX>
+__device__ __forceinline__ float row_join(float v, float* buf) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float u = __shfl_xor_sync(kFullMask, v, o);
+        v = MAX ? fmaxf(v, u) : v + u;
+    }
+    if (blockDim.x == 32) return v;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
+    if (lane == 0) buf[warp] = v;
+    __syncthreads();
+    v = lane < warps ? buf[lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float u = __shfl_xor_sync(kFullMask, v, o);
+        v = MAX ? fmaxf(v, u) : v + u;
+    }
+    return v;
+}
+
+template <bool F16, bool F8, int R>
+__global__ void __launch_bounds__(R == 1 ? 256 : kMaxThreads) add_rms_norm_kernel(const __grid_constant__ NormArgs a) {
+    __shared__ float buf[2][8][32];
+    const long long t = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const bool here = t < a.T;
+    const int pieces = a.C / 8;
+    uint4 x[R], r[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int p = threadIdx.x + i * blockDim.x;
+        const bool on = here && p < pieces;
+        x[i] = on ? *reinterpret_cast<const uint4*>(a.x + t * a.x_stride + p * 8) : make_uint4(0, 0, 0, 0);
+        r[i] = on && a.residual ? *reinterpret_cast<const uint4*>(a.residual + t * a.C + p * 8) : make_uint4(0, 0, 0, 0);
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int p = threadIdx.x + i * blockDim.x;
+        uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        const uint32_t v[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (a.residual) {
+                const float2 b = attn::unpack2<F16>(v[j]), c = attn::unpack2<F16>(u[j]);
+                u[j] = attn::pack2<F16>(b.x + c.x, b.y + c.y);
+            }
+            const float2 f = attn::unpack2<F16>(u[j]);
+            sum = fmaf(f.x, f.x, fmaf(f.y, f.y, sum));
+        }
+        x[i] = make_uint4(u[0], u[1], u[2], u[3]);
+        if (a.residual && here && p < pieces) *reinterpret_cast<uint4*>(a.residual + t * a.C + p * 8) = x[i];
+    }
+    const float inv = rsqrtf(row_join<false>(sum, buf[0][threadIdx.y]) / static_cast<float>(a.C) + a.eps);
+    float amax = 0.f;  // of the row (one scale per row)
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int p = threadIdx.x + i * blockDim.x;
+        const bool on = here && p < pieces;
+        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        float f[8];
+        float4 w0 = make_float4(0.f, 0.f, 0.f, 0.f), w1 = w0;
+        if (p < pieces) {
+            w0 = __ldg(reinterpret_cast<const float4*>(a.w + p * 8));
+            w1 = __ldg(reinterpret_cast<const float4*>(a.w + p * 8 + 4));
+        }
+        const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 b = attn::unpack2<F16>(u[j]);
+            f[2 * j] = b.x * inv * w[2 * j];
+            f[2 * j + 1] = b.y * inv * w[2 * j + 1];
+        }
+        if constexpr (!F8) {
+            if (on)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + t * a.C + p * 8) =
+                    make_uint4(attn::pack2<F16>(f[0], f[1]), attn::pack2<F16>(f[2], f[3]), attn::pack2<F16>(f[4], f[5]), attn::pack2<F16>(f[6], f[7]));
+        } else {
+            float m = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
+            if (a.lanes == 0) {
+                amax = fmaxf(amax, m);
+            } else {
+                for (int o = a.lanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
+                const float scale = m > 0.f ? fmaxf(m / 448.f, 1.17549435e-38f) : 1.f, up = 1.f / scale;
+                if (on) {
+                    uint2 q;
+                    q.x = __nv_cvt_float2_to_fp8x2(make_float2(f[0] * up, f[1] * up), __NV_SATFINITE, __NV_E4M3) |
+                          __nv_cvt_float2_to_fp8x2(make_float2(f[2] * up, f[3] * up), __NV_SATFINITE, __NV_E4M3) << 16;
+                    q.y = __nv_cvt_float2_to_fp8x2(make_float2(f[4] * up, f[5] * up), __NV_SATFINITE, __NV_E4M3) |
+                          __nv_cvt_float2_to_fp8x2(make_float2(f[6] * up, f[7] * up), __NV_SATFINITE, __NV_E4M3) << 16;
+                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + t * a.C + p * 8) = q;
+                    if (p % a.lanes == 0) a.scale[t * (pieces / a.lanes) + p / a.lanes] = scale;
+                }
+            }
+        }
+    }
+    if constexpr (F8) {
+        if (a.lanes == 0) {
+            amax = row_join<true>(amax, buf[1][threadIdx.y]);
+            const float scale = amax > 0.f ? fmaxf(amax / 448.f, 1.17549435e-38f) : 1.f, up = 1.f / scale;
+            if (here && threadIdx.x == 0) a.scale[t] = scale;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int p = threadIdx.x + i * blockDim.x;
+                if (!here || p >= pieces) continue;
+                const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                const float4 w0 = __ldg(reinterpret_cast<const float4*>(a.w + p * 8)), w1 = __ldg(reinterpret_cast<const float4*>(a.w + p * 8 + 4));
+                const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                uint32_t q[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 b = attn::unpack2<F16>(u[j]);
+                    q[j] = __nv_cvt_float2_to_fp8x2(make_float2(b.x * inv * w[2 * j] * up, b.y * inv * w[2 * j + 1] * up), __NV_SATFINITE, __NV_E4M3);
+                }
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + t * a.C + p * 8) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+            }
+        }
+    }
+}
+
+}  // namespace norm
+}  // namespace gdn

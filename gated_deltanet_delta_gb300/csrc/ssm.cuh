@@ -1,0 +1,100 @@
+// ssm.cuh -- the selective state space recurrence as it stands, token by token, for single tokens and short sequences:
+//     dt_t = softplus(raw_t + bias);  S_t = e^(A dt_t) S_(t-1) + dt_t x_t (x) B_t,  A = -e^A_log;
+//     y_t = S_t C_t + D x_t, times silu(z_t) where there is a gate.
+// Head h has P features and reads B and C of group h / (H / G); its state is [P, N], in fp32.
+//
+// A stream of the state, 8 bytes per element and call against 4 operations per token: HBM is the bound up to some ten
+// tokens.  A state row of N floats is split over TPR lanes, a thread has two rows and asks for all of its 16-byte pieces
+// before any arithmetic (as gdn_decode_kernel does); the tokens' inputs are staged in shared memory, kSteps at a time.
+#pragma once
+
+#include "common.cuh"
+#include "kernel_args.h"
+
+namespace gdn {
+namespace ssm {
+
+constexpr int kSteps = 8;    // tokens staged at a time
+constexpr int kRows = 64;    // state rows per CTA
+
+__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+// z / (1 + e^-z)
+__device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.f + __expf(fminf(-z, 80.f))); }
+
+// The bounds and the slot of sequence n; false (and the status) if they are malformed.
+__device__ __forceinline__ bool sequence(const SsmArgs& a, int n, long long& begin, long long& end, long long& slot, bool report) {
+    begin = a.cu ? a.cu[n] : n;
+    end = a.cu ? a.cu[n + 1] : n + 1;
+    slot = a.slots[n];
+    const bool bad = begin < 0 || end < begin || end > a.T, off = slot < 0 || slot >= a.pool_size;
+    if ((bad || off) && report) atomicOr(a.status, (bad ? kStatusBadSeqlens : 0) | (off ? kStatusBadCacheIndex : 0));
+    return !bad && !off;
+}
+
+template <int S, int TPR>
+__global__ void __launch_bounds__(kRows / 2 * TPR) ssm_steps_kernel(const __grid_constant__ SsmArgs a) {
+    constexpr int NT = kRows / 2 * TPR, NV = S / (4 * TPR), RPP = NT / TPR;
+    __shared__ float4 Bs[kSteps][S / 4], Cs[kSteps][S / 4];
+    __shared__ float xs[kSteps][kRows], keep_s[kSteps], dt_s[kSteps];
+    const int tile = blockIdx.x % a.tiles, h = blockIdx.x / a.tiles % a.H, n = blockIdx.x / a.tiles / a.H;
+    const int g = h / (a.H / a.G), p0 = tile * kRows;
+    const int lr = threadIdx.x % TPR, rw = threadIdx.x / TPR;
+    long long begin, end, slot;
+    if (!sequence(a, n, begin, end, slot, threadIdx.x == 0 && tile == 0 && h == 0) || begin == end) return;
+    float4* st = reinterpret_cast<float4*>(a.state) + ((slot * a.H + h) * a.P + p0) * (S / 4);
+    float4 s[2][NV];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int m = 0; m < NV; ++m) s[r][m] = ld_stream(st + (r * RPP + rw) * (S / 4) + lr + TPR * m);
+    const float A = -expf(a.A_log[h]), bias = a.dt_bias[h], D = a.D ? a.D[h] : 0.f;
+    for (long long t0 = begin; t0 < end; t0 += kSteps) {
+        const int count = static_cast<int>(end - t0 < kSteps ? end - t0 : kSteps);
+        if (t0 > begin) __syncthreads();  // the block before is no longer read
+        for (int i = threadIdx.x; i < count * (S / 4); i += NT) {
+            const int k = i / (S / 4), j = i % (S / 4);
+            Bs[k][j] = bf16x4_to_f32x4(*reinterpret_cast<const uint2*>(a.B + (t0 + k) * a.b_stride + g * S + 4 * j));
+            Cs[k][j] = bf16x4_to_f32x4(*reinterpret_cast<const uint2*>(a.C + (t0 + k) * a.c_stride + g * S + 4 * j));
+        }
+        for (int i = threadIdx.x; i < count * kRows; i += NT)
+            xs[i / kRows][i % kRows] = bf16_to_f32(a.x[(t0 + i / kRows) * a.x_stride + h * a.P + p0 + i % kRows]);
+        if (threadIdx.x < count) {
+            const float dt = softplus(bf16_to_f32(a.dt[(t0 + threadIdx.x) * a.dt_stride + h]) + bias);
+            dt_s[threadIdx.x] = dt;
+            keep_s[threadIdx.x] = expf(A * dt);
+        }
+        __syncthreads();
+        for (int k = 0; k < count; ++k) {
+            const float keep = keep_s[k], dt = dt_s[k];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = r * RPP + rw;
+                const float x = xs[k][row], add = dt * x;
+                float y = 0.f;
+#pragma unroll
+                for (int m = 0; m < NV; ++m) {
+                    const float4 b = Bs[k][lr + TPR * m];
+                    float4& v = s[r][m];
+                    v.x = fmaf(keep, v.x, add * b.x);
+                    v.y = fmaf(keep, v.y, add * b.y);
+                    v.z = fmaf(keep, v.z, add * b.z);
+                    v.w = fmaf(keep, v.w, add * b.w);
+                    y += dot4(v, Cs[k][lr + TPR * m]);
+                }
+                y = fmaf(D, x, group_sum<TPR>(y));
+                if (lr == 0) {
+                    const long long at = h * a.P + p0 + row;
+                    if (a.z) y *= silu(bf16_to_f32(a.z[(t0 + k) * a.z_stride + at]));
+                    a.out[(t0 + k) * a.H * a.P + at] = f32_to_bf16_rne(y);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int m = 0; m < NV; ++m) st_stream(st + (r * RPP + rw) * (S / 4) + lr + TPR * m, s[r][m]);
+}
+
+}  // namespace ssm
+}  // namespace gdn

@@ -18,7 +18,13 @@
  *   attn_paged           causal attention of each sequence's new tokens over its paged cache
  *   attn_cache_write     keys and values into the paged cache, quantised to 8 bits or as they are
  *   attn_cache_read      cached keys and values back to dense rows
+ *   attn_cache_append    queries and keys rotated by their positions, keys and values into that cache
  *   draft_verify         which drafted tokens the target accepts, and the token that follows them
+ * and what stands ahead of a layer and beside the delta rule:
+ *   short_conv           the short causal convolution of packed sequences (or single tokens), with its history
+ *   ssm_decode_step      one token of the selective state space scan on a pooled state
+ *   ssm_prefill_chunked  the same scan over packed sequences
+ *   add_rms_norm         residual addition and root-mean-square norm, in 16 bits or e4m3 with scales
  *
  * Conventions shared by every entry point
  *   - Every tensor argument is a DEVICE pointer to dense, contiguous, row-major memory in the layout
@@ -78,6 +84,7 @@ typedef void* gdn_stream_t;
 #define GDN_STATUS_TIMEOUT 4         /* a bounded wait for the tensor core or a copy gave up */
 #define GDN_STATUS_BAD_PROBS 8       /* draft_verify: a distribution to draw from has no mass */
 #define GDN_STATUS_BAD_TOKEN 16      /* draft_verify: a drafted token outside [0, V) */
+#define GDN_STATUS_BAD_POSITION 32   /* attn_cache_append: a position outside the table */
 
 /*
  * gdn_decode_step -- one GDN decode step for B sequences.  [gated_delta.rs] "Recurrence per step":
@@ -493,6 +500,109 @@ void attn_set_wait_limit(uint32_t polls);
 gdn_status draft_verify(const float* target_p, const float* draft_p, const int64_t* drafts,
                         const int64_t* num_drafts, const float* u_accept, const float* u_sample, int N, int T,
                         int V, int64_t* accepted, int64_t* tokens, int32_t* dev_status, gdn_stream_t stream);
+
+/*
+ * attn_cache_append -- attn_cache_write with the rotation by position on the way, for queries and keys.  With
+ * (cos_i, sin_i) the table's row of the token's position, the pairs (a, b) of a head's first rotary_dim features become
+ * (a cos_i - b sin_i, b cos_i + a sin_i), in fp32 (every product and sum rounded), rounded to dtype; the others stay.  A cache
+ * then holds what attn_cache_write would make of the rotated rows, bit for bit.
+ *
+ *   q, k, v    [T, Hq or Hkv, D] of dtype (GDN_BF16 or GDN_F16), token t q_stride (k_stride, v_stride) elements after token
+ *              t - 1; 16-byte aligned, strides multiples of 8.  Hq may be 0 (q, q_out NULL): keys and values alone
+ *   rotation   f32 [max_positions, rotary_dim]: rotary_dim / 2 cosines, then as many sines; 16-byte aligned
+ *   neighbours 0: features i and i + rotary_dim / 2 are a pair; else 2 i and 2 i + 1
+ *   positions  int64 [T]; one outside the table sets GDN_STATUS_BAD_POSITION, and nothing of its token is written
+ *   slots      int64 [T], as attn_cache_write's: a negative slot leaves the token out of the cache (its query is rotated);
+ *              one outside it sets GDN_STATUS_BAD_CACHE_INDEX, likewise
+ *   q_out      [T, Hq, D] of dtype, token t q_out_stride elements after token t - 1; may be q itself (with the same stride)
+ * Supported: D in {64, 128, 256}, rotary_dim a multiple of 16, 16 .. D, Hq, Hkv <= 65535.
+ */
+gdn_status attn_cache_append(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                             int64_t v_stride, gdn_dtype dtype, const float* rotation, int64_t max_positions,
+                             int rotary_dim, int neighbours, const int64_t* positions, const int64_t* slots, int64_t T,
+                             void* q_out, int64_t q_out_stride, void* k_cache, void* v_cache, float* k_scale,
+                             float* v_scale, gdn_dtype cache_dtype, int64_t num_pages, int page_size, int Hq, int Hkv,
+                             int D, int32_t* dev_status, gdn_stream_t stream);
+
+/*
+ * short_conv -- the short causal convolution of packed sequences:
+ *     y[t, c] = act(bias[c] + sum_j weight[c, j] x[t - (taps - 1) + j, c]),   act(y) = y / (1 + e^-y) if silu, else y,
+ * where the taps - 1 tokens ahead of a sequence's first are its history.  The history then holds the sequence's last
+ * taps - 1 inputs: a prompt may come in pieces, single tokens go on from it, and so does gdn_window_fused (taps 4).
+ *
+ *   x          [T, C] of dtype (GDN_BF16 or GDN_F16), token t x_stride elements after token t - 1; 16-byte aligned, x_stride a
+ *              multiple of 8
+ *   weight     f32 [C, taps];  bias f32 [C] or NULL
+ *   hist_pool  f32 [pool_size, C, taps - 1], oldest first, 16-byte aligned; updated in place
+ *   cache_indices  int64 [num_seqs], distinct: the sequences' rows of hist_pool
+ *   cu_seqlens int64 [num_seqs + 1], or NULL: one token per sequence (T = num_seqs)
+ *   out0..2    [T, c0], [T, c1], [T, c2] of dtype, 16-byte aligned: channels 0 .. c0 - 1, the next c1, the next c2 (queries, keys
+ *              and values for gdn_prefill_chunked; x, B and C for the scan).  c0 + c1 + c2 = C; c1, c2 may be 0
+ * A sequence with malformed bounds (GDN_STATUS_BAD_SEQLENS) or a bad slot (GDN_STATUS_BAD_CACHE_INDEX) is skipped: its history stays
+ * and, where the bounds tell which they are, its rows are not written.  Rows of no sequence are not written.
+ * Supported: taps 2, 3 or 4; c0, c1, c2 multiples of 8, C <= 2^24.
+ */
+gdn_status short_conv(const void* x, int64_t x_stride, gdn_dtype dtype, const float* weight, const float* bias,
+                      float* hist_pool, int pool_size, const int64_t* cache_indices, const int64_t* cu_seqlens,
+                      int num_seqs, int64_t T, int C, int taps, int silu, void* out0, int c0, void* out1, int c1,
+                      void* out2, int c2, int32_t* dev_status, gdn_stream_t stream);
+
+/*
+ * ssm_decode_step -- one token per sequence of the selective state space scan.  Per head h (group g = h / (H / G)):
+ *     dt = softplus(dt_raw + dt_bias[h]);   S <- e^(-e^A_log[h] dt) S + dt x (x) B[g];   y = S C[g] + D[h] x,
+ * and y z / (1 + e^-z) in y's place where there is a gate z.  S is [P, N].
+ *
+ *   x, z       bf16 [num_seqs, H, P] (z may be NULL);  dt bf16 [num_seqs, H];  B, C bf16 [num_seqs, G, N]
+ *   token_strides  host int64 [5]: elements between tokens of x, dt, B, C, z (slices of wider rows need no copy); but for dt's
+ *              multiples of 8, and those arrays 16-byte aligned
+ *   A_log, dt_bias  f32 [H];  D f32 [H] or NULL
+ *   state_pool f32 [pool_size, H, P, N], updated in place;  cache_indices int64 [num_seqs], distinct
+ *   out        bf16 [num_seqs, H, P], 16-byte aligned
+ * All arithmetic is f32.  A bad slot sets GDN_STATUS_BAD_CACHE_INDEX and its sequence is skipped.
+ * Supported: P and N 64 or 128, H % G == 0.
+ */
+gdn_status ssm_decode_step(const void* x, const void* dt, const void* B, const void* C, const void* z,
+                           const int64_t* token_strides, const float* A_log, const float* D, const float* dt_bias,
+                           float* state_pool, int pool_size, const int64_t* cache_indices, int num_seqs, int H, int P,
+                           int G, int N, void* out, int32_t* dev_status, gdn_stream_t stream);
+
+/*
+ * ssm_prefill_workspace_size -- bytes of device workspace that ssm_prefill_chunked needs (possibly 0); 0 for sizes that it
+ * does not support.  Pure host function.
+ */
+size_t ssm_prefill_workspace_size(int num_seqs, int64_t T, int H, int P, int N);
+
+/*
+ * ssm_prefill_chunked -- the scan of ssm_decode_step over packed sequences: tokens cu_seqlens[n] .. cu_seqlens[n + 1] - 1 are
+ * sequence n's, its state goes from slot to slot in place, so that a prompt may come in pieces.
+ *   x, z, dt, B, C, out   as above with T tokens
+ *   cu_seqlens int64 [num_seqs + 1]
+ *   max_len    the longest sequence, as far as the caller knows it: it chooses the kernel and changes no result beyond rounding
+ *   workspace  ssm_prefill_workspace_size bytes, 16-byte aligned, contents need not be initialised; calls that share it must
+ *              not overlap on the GPU
+ * A sequence with malformed bounds sets GDN_STATUS_BAD_SEQLENS, one with a bad slot GDN_STATUS_BAD_CACHE_INDEX; it is skipped.  Rows of
+ * no sequence are not written.
+ */
+gdn_status ssm_prefill_chunked(const void* x, const void* dt, const void* B, const void* C, const void* z,
+                               const int64_t* token_strides, const float* A_log, const float* D, const float* dt_bias,
+                               float* state_pool, int pool_size, const int64_t* cache_indices, const int64_t* cu_seqlens,
+                               int num_seqs, int64_t T, int64_t max_len, int H, int P, int G, int N, void* out,
+                               void* workspace, size_t workspace_bytes, int32_t* dev_status, gdn_stream_t stream);
+
+/*
+ * add_rms_norm -- r = x + residual, rounded to dtype and stored in residual;  y = r / sqrt(mean(r^2) + eps) weight.
+ *   x          [T, C] of dtype (GDN_BF16 or GDN_F16), row t x_stride elements after row t - 1; 16-byte aligned, x_stride a
+ *              multiple of 8
+ *   residual   [T, C] of dtype, updated in place; or NULL: r = x
+ *   weight     f32 [C], 16-byte aligned
+ *   out        [T, C] of out_dtype: dtype (then it may be x itself, where x is dense), or GDN_E4M3: y / s to nearest even, with
+ *              s = max |y| / 448 over each group of features (1 where all are zero; at least 2^-126)
+ *   scale      f32 [T, C / group], or [T] for group 0 (one scale per row); NULL for a 16-bit out
+ * Sums and y are f32.  A row with an element that is not finite has no meaningful y.
+ * Supported: C a multiple of 8, at most 32768; group 0, 32, 64, 128 or 256, a divisor of C.
+ */
+gdn_status add_rms_norm(const void* x, int64_t x_stride, void* residual, gdn_dtype dtype, const float* weight, float eps,
+                        int64_t T, int C, void* out, gdn_dtype out_dtype, float* scale, int group, gdn_stream_t stream);
 
 /* Static description of a status code. */
 const char* gdn_status_string(gdn_status status);
