@@ -1059,6 +1059,7 @@ extern "C" gdn_status ssm_prefill_chunked(const void* x, const void* dt, const v
     REQUIRE(!any_overlap(workspace, need, out, static_cast<size_t>(T) * inner * 2) && !any_overlap(workspace, need, state_pool, sb),
             GDN_ERR_INVALID_ARG, "%s: workspace overlaps another buffer", fn);
     a.cu = cu_seqlens;
+    a.polls = g_prefill_wait_polls.load(std::memory_order_relaxed);
     const cudaError_t e = gdn::launch_ssm_prefill(a, N, max_len, workspace, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
     return launched(fn);

@@ -300,7 +300,17 @@ struct SsmArgs {
     int32_t* status;
     long long T;
     int num_seqs, pool_size, H, P, G;
-    int tiles;              // row tiles per head
+    int tiles;              // row tiles per head (token by token)
+    // chunks of 128 tokens (ssm_chunk.cuh)
+    int seg, sub;           // chunks per segment and per piece of one
+    float* ws;              // states [.., H, P, S] of the pieces, and the logarithms (base 2) of their decays [.., H]
+    float* ws_decay;
+    uint32_t polls;         // of a barrier, before a wait gives up
+};
+
+// x, B and C as rows of a token each.
+struct SsmMaps {
+    CUtensorMap x, B, C;
 };
 
 struct NormArgs {

@@ -1,8 +1,88 @@
-// ssm.cu -- launch of the state space scan (ssm.cuh).
+// ssm.cu -- launch of the state space scan (ssm.cuh, ssm_chunk.cuh).
+#include <algorithm>
+#include <atomic>
+#include <cstring>
+
+#include "host.h"
 #include "launch.h"
-#include "ssm.cuh"
+#include "ssm_chunk.cuh"
 
 namespace gdn {
+namespace {
+
+constexpr int kSub = 8;  // chunks per piece of the launch ahead; segments are multiples of it
+
+// Tokens as rows of `width` elements: boxes of 64 columns and 128 rows, 128-byte swizzle, zero fill outside.
+bool encode_tokens(CUtensorMap* map, const void* base, long long T, long long width, long long stride) {
+    const auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(T)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
+    const cuuint32_t box[2] = {64, 128}, step[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int P, int S, bool STATE>
+cudaError_t run(const SsmArgs& a, const SsmMaps& maps, unsigned grid, cudaStream_t stream) {
+    using C = ssm::ChunkCfg<S>;
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!(done.load(std::memory_order_acquire) >> dev & 1)) {
+        e = cudaFuncSetAttribute(ssm::ssm_chunk_kernel<P, S, STATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess) return e;
+        // the split of registers among roles waits forever where the launch has fewer than it adds up to
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, ssm::ssm_chunk_kernel<P, S, STATE>);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs < ssm::kRegsLaunch) return cudaErrorInvalidConfiguration;
+        done.fetch_or(1ull << dev, std::memory_order_release);
+    }
+    ssm::ssm_chunk_kernel<P, S, STATE><<<grid, ssm::kChunkNT, C::SMEM, stream>>>(a, maps);
+    return cudaGetLastError();
+}
+
+template <int P, int S>
+cudaError_t chunks(SsmArgs a, long long max_len, void* workspace, cudaStream_t stream) {
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    SsmMaps maps;
+    const long long inner = static_cast<long long>(a.H) * P, gs = static_cast<long long>(a.G) * S;
+    if (!encode_tokens(&maps.x, a.x, a.T, inner, a.x_stride) || !encode_tokens(&maps.B, a.B, a.T, gs, a.b_stride) ||
+        !encode_tokens(&maps.C, a.C, a.T, gs, a.c_stride))
+        return cudaErrorInvalidValue;
+    // Segments.  In chunk times of one SM: `share` is the work over the SMs, a chain takes as long as it is, units that are
+    // more than the SMs end unevenly by about half a unit, and the launch ahead costs two fifths of what it covers and a start.
+    const long long per_seg = static_cast<long long>(a.G) * ((a.H / a.G * P + 127) / 128);
+    const double total = static_cast<double>((a.T + 127) / 128), share = total * per_seg / sms;
+    const double longest = static_cast<double>((std::min(std::max(max_len, 1LL), a.T) + 127) / 128);
+    auto cost = [&](double seg) {
+        const double units = total / longest * std::max(1.0, static_cast<double>(static_cast<long long>((longest + seg - 1) / seg))) * per_seg;
+        const double ahead = seg < longest ? 0.4 * share * (longest - seg) / longest + 3.0 : 0.0;
+        return (units <= sms ? seg : std::max(seg, share + seg / 2)) + ahead;
+    };
+    a.seg = a.sub = 1 << 24;  // one segment per sequence
+    double best = 0.85 * cost(longest);
+    for (int seg = kSub; seg < longest; seg += kSub)
+        if (cost(seg) < best) best = cost(seg), a.seg = seg, a.sub = kSub;
+    const long long state = static_cast<long long>(a.H) * P * S, states = 2 * (a.T / (128 * kSub));
+    a.ws = static_cast<float*>(workspace);
+    a.ws_decay = a.ws + states * state;
+    if (a.seg < 1 << 24) {
+        const long long grid = a.T / (128 * kSub) * per_seg;
+        e = run<P, S, true>(a, maps, static_cast<unsigned>(grid), stream);
+        if (e != cudaSuccess) return e;
+    }
+    const long long grid = (a.T / 128 / a.seg + a.num_seqs) * per_seg;
+    if (grid >= 1LL << 31) return cudaErrorInvalidConfiguration;
+    return run<P, S, false>(a, maps, static_cast<unsigned>(grid), stream);
+}
+
+}  // namespace
 
 void launch_ssm_steps(SsmArgs a, int S, cudaStream_t stream) {
     a.tiles = a.P / ssm::kRows;
@@ -11,11 +91,20 @@ void launch_ssm_steps(SsmArgs a, int S, cudaStream_t stream) {
     else ssm::ssm_steps_kernel<128, 8><<<grid, ssm::kRows / 2 * 8, 0, stream>>>(a);
 }
 
-size_t ssm_workspace_bytes(int, long long, int, int, int) { return 0; }
+// Two states for every piece that a call of T tokens can have, and their decays.
+size_t ssm_workspace_bytes(int, long long T, int H, int P, int S) {
+    return static_cast<size_t>(2 * (T / (128 * kSub))) * H * (static_cast<size_t>(P) * S + 1) * sizeof(float);
+}
 
-cudaError_t launch_ssm_prefill(const SsmArgs& a, int S, long long, void*, cudaStream_t stream) {
-    launch_ssm_steps(a, S, stream);
-    return cudaGetLastError();
+cudaError_t launch_ssm_prefill(const SsmArgs& args, int S, long long max_len, void* workspace, cudaStream_t stream) {
+    if (max_len <= 16) {
+        launch_ssm_steps(args, S, stream);
+        return cudaGetLastError();
+    }
+    SsmArgs a = args;
+    if (a.polls == 0 || a.polls > ssm::kPolls) a.polls = ssm::kPolls;
+    if (a.P == 64) return S == 64 ? chunks<64, 64>(a, max_len, workspace, stream) : chunks<64, 128>(a, max_len, workspace, stream);
+    return S == 64 ? chunks<128, 64>(a, max_len, workspace, stream) : chunks<128, 128>(a, max_len, workspace, stream);
 }
 
 }  // namespace gdn

@@ -1,0 +1,682 @@
+// ssm_chunk.cuh -- the state space scan over prompts, in chunks of 128 tokens on the tensor cores (tcgen05, accumulators in TMEM).
+//
+// With a_t = A dt_t and s <= t in a chunk whose first state is S:
+//     y_t = sum_s (C_t . B_s) e^(a_(s+1) + .. + a_t) dt_s x_s + e^(a_1 + .. + a_t) C_t S^T + D x_t,
+//     S' = e^(a_1 + .. + a_Q) S + sum_s e^(a_(s+1) + .. + a_Q) dt_s x_s (x) B_s.
+// A CTA has 128 features of one segment of a sequence (two heads of 64 that share B and C, or one of 128) and walks its chunks:
+//     G = C B^T (128 x 128 x N),  Y = C S^T (128 x 128 x N),  Y = e^(..) Y + M X (128 x 64 x 128 per head of 64),
+//     S = e^(..) S + X'^T B (128 x N x 128, twice),
+// M = G with the weights of its pairs and X' = the rows of x with theirs, made by threads.  S, G, M and Y fill TMEM (512 columns for
+// N = 128); tiles of x, B and C come by TMA.
+//
+// No decay is the exponential of a difference of running sums, which would lose as many bits as the sum has: the sums run
+// over blocks of 32 tokens, and a pair of tokens in two blocks has the product of two factors, the one of the row and
+// its block, the other of the column, which also saves the exponentials: one per pair only inside the blocks.
+//
+// The state is an fp32 result and is carried for thousands of chunks, so X' is held in two bf16 parts (2^-16 relative); M and
+// the copy of S that Y is made from are rounded to bf16 (2^-8 of each product, like the output's own rounding).
+//
+// Roles, 640 threads.  Sixteen workers' warps: a thread is a token (a TMEM lane) of M, of Y and of X', and a feature of the state.
+// Warpgroups 0 and 1 (A) have M's diagonal blocks and the next ones, 2 and 3 (B) the blocks further off, dt, the decays' sums, X' and
+// the state between two chunks; the output (D, the gate) is shared, 32 features each.  Warp 16 loads, a lane each of warps 17
+// and 18 issues the MMAs.  Per chunk c
+//     A: M, Y scaled | output        B: M, X' low, Y scaled | dt, sums, X' high, state of c + 1 | output.
+// Measured: prompts of up to 8192 tokens, four, 64 heads of 64, N = 128, gated: 382 us, 6.0 us per chunk of the longest chain (with A
+// alone for M and the outputs, B alone for the state, 6.9 us).  What bounds it is the chain of hand-overs within a chunk and the
+// latency of the workers' instructions, four warps per scheduler; HBM would take 104 us for the whole, the tensor core 1.6 us a chunk.
+//
+// Segments.  A sequence is a chain, and a call with few sequences and heads has fewer chains than the GPU has SMs.  Long sequences are
+// cut into segments that run side by side: a launch ahead (STATE) forms, over pieces of them, the states that
+// zero states (for the first piece the pool's) end in, without the outputs; a segment then starts from the sum of the
+// pieces ahead of it with their decays.  Its cost is the state's part (about two fifths) of all but the last segments.
+//
+// Every wait is bounded (attn_tiles.cuh): one that runs out sets GDN_STATUS_TIMEOUT and the CTA's limit of polls to 0.
+#pragma once
+
+#include "attn_mma.cuh"
+#include "ssm.cuh"
+#include "tcgen05.cuh"
+#include "tile_util.cuh"
+
+namespace gdn {
+namespace ssm {
+
+constexpr int kChunk = 128;
+constexpr int kChunkNT = 640;
+// registers per thread: the launch's 96 x 5 warpgroups, parted as 104 x 4 for the workers and 64 for those that load and issue
+constexpr int kRegsLaunch = 96, kRegsWork = 104, kRegsIssue = 64;
+constexpr uint32_t kPolls = 1u << 22;  // the built-in limit of a wait (seconds)
+
+template <int S>
+struct ChunkCfg {
+    static constexpr uint32_t X = 32768, CB = kChunk * S * 2;  // bytes of a tile of x, of B or C
+    static constexpr int NCB = S == 64 ? 2 : 1;                // buffers of B and of C each; x has two
+    static constexpr uint32_t OFF_XH = 0;                      // X', high parts
+    static constexpr uint32_t OFF_SX = X;                      // the state's copy, then X', low parts
+    static constexpr uint32_t OFF_C = 2 * X, OFF_B = OFF_C + NCB * CB, OFF_X = OFF_B + NCB * CB, OFF_V = OFF_X + 2 * X;
+    // per chunk (two in turn) and head: the decays' sums within blocks of 32 tokens, the columns' factors, dt (in the
+    // exponent it would be lost beside a large sum), the blocks' sums
+    static constexpr int VEC = 3 * kChunk + 16;
+    static constexpr uint32_t USED = OFF_V + 2 * 2 * VEC * 4;
+    static constexpr uint32_t SMEM = USED + 1024;
+    static constexpr uint32_t TM_S = 0, TM_G = 128, TM_M = 256, TM_Y = 384;
+};
+
+// Barriers, two of each for the chunks in turn.
+enum : int {
+    CK_X = 0, CK_BC, CK_XE, CK_G, CK_CS, CK_UPH, CK_UPD, CK_MX0, CK_MX1, CK_V, CK_S, CK_XL, CK_Y0, CK_Y1, CK_YF, CK_DRAIN, CK_N
+};
+
+struct Unit {
+    long long begin;   // first token
+    long long slot;    // of the state pool
+    long long ws;      // first state of the sequence in the workspace
+    int len, chunks;   // tokens, chunks
+    int k;             // segment (piece) of its sequence
+    int parts;         // segments of its sequence
+    int found;
+};
+
+// 32 bytes at an address that is a multiple of 32.
+__device__ __forceinline__ void ld32bytes(const void* p, uint4& x, uint4& y) {
+    asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w), "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+                 : "l"(p));
+}
+__device__ __forceinline__ void st32bytes(void* p, const uint4& x, const uint4& y) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
+}
+// 8 consecutive 32-bit TMEM columns of this thread's lane.
+__device__ __forceinline__ void st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+                 "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// x, which the compiler does not know to be the same from chunk to chunk: what depends on it is computed where it is used, and does
+// not take registers in between (they were spilled, and each reload from memory took some 300 clocks).
+__device__ __forceinline__ int anew(int x) {
+    asm volatile("" : "+r"(x));
+    return x;
+}
+__device__ __forceinline__ float ex2(float x) { return attn::fast_exp2(x); }
+// Two packed bf16 as a pair of fp32.
+__device__ __forceinline__ attn::f32x2 widen2(uint32_t w) { return attn::pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+// z / (1 + e^-z) of both: one reciprocal, of the denominators' product.  e^-z is held at e^40, whose square is still a number: what
+// that leaves for a z below -40 is less than 2^-50 in the place of less than e^-40 |z|.
+__device__ __forceinline__ attn::f32x2 silu2(attn::f32x2 z) {
+    float e[2];
+    attn::unpair(attn::mul2(z, attn::pair(-1.44269504f, -1.44269504f)), e);
+    const attn::f32x2 d = attn::add2(attn::pair(ex2(fminf(e[0], 57.7f)), ex2(fminf(e[1], 57.7f))), attn::pair(1.f, 1.f));
+    attn::unpair(d, e);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e[0] * e[1]));
+    return attn::mul2(z, attn::mul2(attn::pair(e[1], e[0]), attn::pair(r, r)));
+}
+
+// The unit with number `rank`: one warp walks the sequences.  A sequence of more than a.seg chunks has the states of its
+// pieces in the workspace: the first the pool's, then one behind each piece.
+template <bool STATE>
+__device__ __forceinline__ void find_unit(const SsmArgs& a, int rank, Unit& u) {
+    const int lane = threadIdx.x & 31;
+    const int per = a.seg / a.sub;  // pieces per segment
+    int base = 0;
+    long long ws = 0;
+    if (lane == 0) u.found = 0;
+    for (int n0 = 0; n0 < a.num_seqs; n0 += 32) {
+        const int n = n0 + lane;
+        long long b = 0, e = 0, slot = 0;
+        if (n >= a.num_seqs || !sequence(a, n, b, e, slot, false)) b = e = 0;
+        const int chunks = static_cast<int>((e - b + kChunk - 1) / kChunk), segs = (chunks + a.seg - 1) / a.seg;
+        const int pieces = segs > 1 ? (segs - 1) * per : 0, mine = STATE ? pieces : segs, states = pieces ? pieces + 1 : 0;
+        int upto = mine, held = states;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int x = __shfl_up_sync(kFullMask, upto, o), y = __shfl_up_sync(kFullMask, held, o);
+            if (lane >= o) upto += x, held += y;
+        }
+        const unsigned hit = __ballot_sync(kFullMask, rank < base + upto);
+        if (hit) {
+            if (lane == __ffs(hit) - 1) {
+                const int k = rank - (base + upto - mine), c0 = k * (STATE ? a.sub : a.seg);
+                u.begin = b + static_cast<long long>(c0) * kChunk;
+                u.slot = slot;
+                u.ws = ws + held - states;
+                u.chunks = min(STATE ? a.sub : a.seg, chunks - c0);
+                u.len = static_cast<int>(min(e - u.begin, static_cast<long long>(u.chunks) * kChunk));
+                u.k = k;
+                u.parts = segs;
+                u.found = 1;
+            }
+            return;
+        }
+        base += __shfl_sync(kFullMask, upto, 31);
+        ws += __shfl_sync(kFullMask, held, 31);
+    }
+}
+
+template <int P, int S, bool STATE>
+__global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ SsmMaps maps) {
+    using K = ChunkCfg<S>;
+    constexpr int NCB = K::NCB;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bars[2 * CK_N];
+    __shared__ Unit us;
+    __shared__ volatile float head_s[2][3];  // of the unit's heads: A (base 2), dt's bias, D
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile uint32_t most_polls;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    // units: per segment the groups, and in each the pairs of heads (heads of 128: the heads)
+    const int in_group = a.H / a.G, per_group = (in_group * P + 127) / 128, per_seg = a.G * per_group;
+    const int rank = blockIdx.x / per_seg, which = blockIdx.x % per_seg, g = which / per_group;
+    const int h0 = g * in_group + which % per_group * (128 / P), heads = min(128 / P, (g + 1) * in_group - h0);
+    if (!STATE && blockIdx.x == 0)
+        for (int n = tid; n < a.num_seqs; n += kChunkNT) {
+            long long b, e, slot;
+            sequence(a, n, b, e, slot, true);
+        }
+    if (warp == 0) find_unit<STATE>(a, rank, us);
+    if (tid == 32) {
+        for (int i = 0; i < 2 * CK_N; ++i) {
+            const int id = i / 2;
+            // B and C arrive one after the other; at the others but for the copies' and products' arrive warps
+            const int count = id == CK_BC ? (STATE ? 1 : 2) : id == CK_YF || (!STATE && id == CK_XE) || (P == 128 && id == CK_Y0) ? 16
+                              : id == CK_XE || id == CK_V || id == CK_S || id == CK_XL || id == CK_Y0 || id == CK_Y1 ? 8 : 1;
+            tc::mbar_init(&bars[i], count);
+        }
+        most_polls = a.polls;
+    }
+    __syncthreads();
+    if (!us.found) return;
+    if (warp == 17) tc::tmem_alloc(&tmem_slot, 512);
+    if (tid < 2) {
+        const int h = h0 + (tid < heads ? tid : 0);
+        head_s[tid][0] = -expf(a.A_log[h]) * 1.44269504f;
+        head_s[tid][1] = a.dt_bias[h];
+        head_s[tid][2] = a.D ? a.D[h] : 0.f;
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tm = tmem_slot;
+    const Unit& u = us;
+    uint8_t* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sb = tc::smem_u32(sm);
+
+    auto wait = [&](int id, int c) -> bool {
+        if (tc::mbar_wait_most<kPolls>(&bars[2 * id + (c & 1)], c >> 1 & 1, &most_polls)) return true;
+        most_polls = 0;
+        return false;
+    };
+    auto warp_wait = [&](int id, int c) -> bool {
+        const bool ok = __all_sync(kFullMask, wait(id, c));
+        tc::fence_after();
+        return ok;
+    };
+    auto one_wait = [&](int id, int c) -> bool {
+        const bool ok = wait(id, c);
+        tc::fence_after();
+        return ok;
+    };
+    auto warp_arrive = [&](int id, int c) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars[2 * id + (c & 1)]);
+    };
+    auto vec = [&](int c, int hh) { return reinterpret_cast<float*>(sm + K::OFF_V) + ((c & 1) * 2 + hh) * K::VEC; };
+    const uint32_t trow = tm + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+
+    if (warp >= 16) {
+        attn::regs_down<kRegsIssue>();  // by the whole warpgroup, then its warps part
+        if (warp == 16 && attn::elect()) {
+            // -------------------------------------------------------- loader
+            bool ok = true;
+            for (int c = 0; c < u.chunks && ok; ++c) {
+                const int row = static_cast<int>(u.begin) + c * kChunk;
+                if (c >= 2) ok = wait(CK_XE, c - 2);
+                if (!ok) break;
+                uint64_t* bar = &bars[2 * CK_X + (c & 1)];
+                const int halves = heads * P / 64;
+                tc::mbar_expect_tx(bar, halves * 16384);
+                for (int i = 0; i < halves; ++i) attn::tma_load_2d(sb + K::OFF_X + (c & 1) * K::X + i * 16384, &maps.x, h0 * P + 64 * i, row, bar);
+                if constexpr (!STATE) {
+                    if (c >= NCB) ok = wait(CK_CS, c - NCB);
+                    if (!ok) break;
+                    bar = &bars[2 * CK_BC + (c & 1)];
+                    tc::mbar_expect_tx(bar, K::CB);
+#pragma unroll
+                    for (int i = 0; i < S / 64; ++i) attn::tma_load_2d(sb + K::OFF_C + c % NCB * K::CB + i * 16384, &maps.C, g * S + 64 * i, row, bar);
+                }
+                if (c >= NCB) ok = wait(CK_UPD, c - NCB);
+                if (!ok) break;
+                bar = &bars[2 * CK_BC + (c & 1)];
+                tc::mbar_expect_tx(bar, K::CB);
+#pragma unroll
+                for (int i = 0; i < S / 64; ++i) attn::tma_load_2d(sb + K::OFF_B + c % NCB * K::CB + i * 16384, &maps.B, g * S + 64 * i, row, bar);
+            }
+            if (!ok)  // gave up: leave what copies are in flight (microseconds) a millisecond
+                for (int i = 0; i < 100; ++i) __nanosleep(10000);
+        }
+        // The products' loops are unrolled by four only: unrolled in full, their descriptors, which are the same from chunk to chunk,
+        // were kept in more registers than there are.  Two lanes issue: one what the outputs are made of, the other the state's update, so that neither chain waits for the
+        // other's barriers.  What must be in order between the two is so by those: a chunk's update ends behind its Y = C S^T, whose
+        // copy's place the low parts take, and that behind its G.
+        if (!STATE && warp == 17 && attn::elect()) {
+            // -------------------------------------------------------- G, Y
+            constexpr uint32_t ID_G = tc::idesc_bf16(128, 128, 0, 0, 0), ID_MX = tc::idesc_bf16(128, P, 0, 1, 0);
+            const uint64_t dC = tc::sdesc(sb + K::OFF_C, 16, 1024), dB = tc::sdesc(sb + K::OFF_B, 16, 1024), dS = tc::sdesc(sb + K::OFF_SX, 16, 1024);
+            const uint64_t dX = tc::sdesc(sb + K::OFF_X, 16384, 1024);
+            auto pairs = [&](int c) -> bool {  // G of chunk c
+                if (!one_wait(CK_BC, c)) return false;
+                const uint64_t off = c % NCB * (K::CB >> 4);
+#pragma unroll 1
+                for (uint32_t q = 0; q < S / 64; ++q)
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; ++k) tc::mma_bf16(tm + K::TM_G, dC + off + q * 1024 + 2 * k, dB + off + q * 1024 + 2 * k, ID_G, q + k > 0);
+                tc::commit(&bars[2 * CK_G + (c & 1)]);
+                return true;
+            };
+            bool ok = pairs(0);
+            for (int c = 0; c < u.chunks && ok; ++c) {
+                const uint64_t off = c % NCB * (K::CB >> 4), xoff = (c & 1) * (K::X >> 4);
+                ok = (c == 0 || one_wait(CK_YF, c - 1)) && one_wait(CK_S, c);
+                if (!ok) break;
+#pragma unroll 1
+                for (uint32_t q = 0; q < S / 64; ++q)
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; ++k) tc::mma_bf16(tm + K::TM_Y, dC + off + q * 1024 + 2 * k, dS + q * 1024 + 2 * k, ID_G, q + k > 0);
+                tc::commit(&bars[2 * CK_CS + (c & 1)]);
+                if constexpr (P == 64) {
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        ok = ok && one_wait(CK_Y0 + h, c);
+                        if (!ok) break;
+                        if (h < heads) {
+#pragma unroll 1
+                            for (uint32_t q = 0; q < 2; ++q)
+#pragma unroll
+                                for (uint32_t k = 4 * q, i = 0; i < 4; ++k, ++i)
+                                    tc::mma_bf16_ts(tm + K::TM_Y + 64 * h, tm + K::TM_M + 64 * h + 8 * k, dX + xoff + h * 1024 + k * 128, ID_MX, 1);
+                        }
+                        tc::commit(&bars[2 * (CK_MX0 + h) + (c & 1)]);
+                    }
+                } else {
+                    ok = one_wait(CK_Y0, c);
+                    if (!ok) break;
+#pragma unroll 1
+                    for (uint32_t q = 0; q < 2; ++q)
+#pragma unroll
+                        for (uint32_t k = 4 * q, i = 0; i < 4; ++k, ++i) tc::mma_bf16_ts(tm + K::TM_Y, tm + K::TM_M + 8 * k, dX + xoff + k * 128, ID_MX, 1);
+                    tc::commit(&bars[2 * CK_MX0 + (c & 1)]);
+                }
+                if (!ok) break;
+                if (c + 1 < u.chunks) ok = pairs(c + 1);
+            }
+            // nothing of this CTA's may be in flight when it ends, its barriers' arrivals included
+            tc::commit(&bars[2 * CK_DRAIN]);
+            tc::mbar_wait(&bars[2 * CK_DRAIN], 0, kPolls);
+        }
+        if (warp == 18 && attn::elect()) {
+            // -------------------------------------------------------- the state
+            constexpr uint32_t ID_UPD = tc::idesc_bf16(128, S, 1, 1, 0);
+            const uint64_t dBm = tc::sdesc(sb + K::OFF_B, 16384, 1024), dXH = tc::sdesc(sb + K::OFF_XH, 16384, 1024), dXL = tc::sdesc(sb + K::OFF_SX, 16384, 1024);
+            bool ok = true;
+            for (int c = 0; c < u.chunks && ok; ++c) {
+                const uint64_t off = c % NCB * (K::CB >> 4);
+                ok = one_wait(CK_BC, c) && one_wait(CK_S, c);
+                if (!ok) break;
+#pragma unroll 1
+                for (uint32_t q = 0; q < 2; ++q)
+#pragma unroll
+                    for (uint32_t k = 4 * q, i = 0; i < 4; ++k, ++i) tc::mma_bf16(tm + K::TM_S, dXH + k * 128, dBm + off + k * 128, ID_UPD, 1);
+                tc::commit(&bars[2 * CK_UPH + (c & 1)]);
+                ok = one_wait(CK_XL, c);
+                if (!ok) break;
+#pragma unroll 1
+                for (uint32_t q = 0; q < 2; ++q)
+#pragma unroll
+                    for (uint32_t k = 4 * q, i = 0; i < 4; ++k, ++i) tc::mma_bf16(tm + K::TM_S, dXL + k * 128, dBm + off + k * 128, ID_UPD, 1);
+                tc::commit(&bars[2 * CK_UPD + (c & 1)]);
+            }
+            tc::commit(&bars[2 * CK_DRAIN + 1]);
+            tc::mbar_wait(&bars[2 * CK_DRAIN + 1], 0, kPolls);
+        }
+    } else {
+        // ------------------------------------------------------------ workers: warpgroups 0, 1 (A) and 2, 3 (B)
+        attn::regs_up<kRegsWork>();
+        const int wg = warp >> 2, w = warp & 3, t = tid & 127, side = wg & 1;
+        const bool isb = wg >= 2;
+        const int hh = P == 64 ? side : 0;
+        const bool valid = hh < heads;
+        const int h = h0 + (valid ? hh : 0);
+
+        // ---- what all do: the weights of pairs in M, the scaling of Y, the output
+        // blocks of 32 columns of M: an A warp has the diagonal one (and the one ahead of it), a B warp those further ahead
+        auto mine = [&](int j) {
+            if (P == 64) return isb ? j <= w - 2 : j >= w - 1;
+            return j == w - wg;
+        };
+        const uint32_t tM = trow + K::TM_M + (P == 64 ? side * 64 : 0), tY = trow + K::TM_Y + side * 64 + (wg >> 1) * 32;
+        auto weights = [&](int c) -> bool {
+            const float* V = vec(c, hh);
+            const float pre = V[t];
+            if (w - wg < 0 && P == 128) return true;
+            if (P == 64 && isb && w < 2) return true;
+            if (!warp_wait(CK_G, c)) return false;
+            float ahead = pre;  // the decay from the end of block j to the row
+#pragma unroll 1
+            for (int j = w; j >= 0; --j) {  // one body for all blocks: unrolled, the code did not stay in the instruction cache
+                if (j < w - 1) ahead += V[3 * kChunk + j + 1];
+                if (!mine(j)) continue;
+                const float r = ex2(ahead);
+                const attn::f32x2 pp = attn::pair(pre, pre), minus = attn::pair(-1.f, -1.f), rr = attn::pair(r, r);
+#pragma unroll
+                for (int i0 = 0; i0 < 32; i0 += 16) {
+                    float x[16];
+                    uint32_t m[8];
+                    tc::ld16(trow + K::TM_G + 32 * j + i0, x);
+                    tc::wait_ld();
+                    const float* Vc = V + 32 * j + i0;
+                    if (j == w) {
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            const float4 p = *reinterpret_cast<const float4*>(Vc + i), d = *reinterpret_cast<const float4*>(Vc + 2 * kChunk + i);
+                            float f[4], e[4];
+                            attn::unpair(attn::fma2(attn::pair(p.x, p.y), minus, pp), f);
+                            attn::unpair(attn::fma2(attn::pair(p.z, p.w), minus, pp), f + 2);
+                            attn::unpair(attn::mul2(attn::pair(x[i], x[i + 1]), attn::pair(d.x, d.y)), e);
+                            attn::unpair(attn::mul2(attn::pair(x[i + 2], x[i + 3]), attn::pair(d.z, d.w)), e + 2);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) x[i + q] = i0 + i + q <= lane ? e[q] * ex2(f[q]) : 0.f;
+                            m[i / 2] = pack_bf16x2(x[i], x[i + 1]);
+                            m[i / 2 + 1] = pack_bf16x2(x[i + 2], x[i + 3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(Vc + kChunk + i);
+                            float y[4];
+                            attn::unpair(attn::mul2(attn::mul2(attn::pair(f.x, f.y), rr), attn::pair(x[i], x[i + 1])), y);
+                            attn::unpair(attn::mul2(attn::mul2(attn::pair(f.z, f.w), rr), attn::pair(x[i + 2], x[i + 3])), y + 2);
+                            m[i / 2] = pack_bf16x2(y[0], y[1]);
+                            m[i / 2 + 1] = pack_bf16x2(y[2], y[3]);
+                        }
+                    }
+                    st8(tM + 16 * j + i0 / 2, m);
+                }
+            }
+            return true;
+        };
+        auto scale_y = [&](int c) {
+            const float* V = vec(c, hh);
+            float sum = V[t];  // the decay from the chunk's start
+            for (int j = 0; j < w; ++j) sum += V[3 * kChunk + j];
+            const float from = ex2(sum);
+            const attn::f32x2 ff = attn::pair(from, from);
+            float y0[16], y1[16];
+            tc::ld16(tY, y0);
+            tc::ld16(tY + 16, y1);
+            tc::wait_ld();
+#pragma unroll
+            for (int q = 0; q < 16; q += 2) {
+                attn::unpair(attn::mul2(attn::pair(y0[q], y0[q + 1]), ff), y0 + q);
+                attn::unpair(attn::mul2(attn::pair(y1[q], y1[q + 1]), ff), y1 + q);
+            }
+            tc::st16(tY, y0);
+            tc::st16(tY + 16, y1);
+            tc::wait_st();
+            tc::fence_before();
+            warp_arrive(P == 64 ? CK_Y0 + side : CK_Y0, c);
+        };
+        const long long col = static_cast<long long>(h0) * P + side * 64;  // the first feature of this half of the tile
+        const uint32_t line = static_cast<uint32_t>(side * 16384 + t * 128);  // this row of that half
+        // A thread's 32 features are two sectors of global memory, taken whole where their address allows it.
+        const bool z32 = reinterpret_cast<uintptr_t>(a.z) % 32 == 0 && a.z_stride % 16 == 0, y32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
+        auto output = [&](int c) -> bool {
+            const bool live = t < u.len - c * kChunk && valid;
+            const long long tok = u.begin + c * kChunk + t;
+            uint4 z[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[i] = make_uint4(0, 0, 0, 0);
+            if (a.z && live) {
+                const uint16_t* src = a.z + tok * a.z_stride + col + (wg >> 1) * 32;
+                if (z32) ld32bytes(src, z[0], z[1]), ld32bytes(src + 16, z[2], z[3]);
+                else
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) z[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+            }
+            __syncwarp();
+            if (!warp_wait(P == 64 ? CK_MX0 + side : CK_MX0, c) || !warp_wait(CK_X, c)) return false;
+            const uint32_t at = sb + K::OFF_X + (c & 1) * K::X + line;
+            const int t7 = anew(t) & 7;
+            const float D = head_s[hh][2];
+            const attn::f32x2 dd = attn::pair(D, D);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float y[16];
+                tc::ld16(tY + 16 * i, y);
+                tc::wait_ld();
+                if (i == 1) {
+                    tc::fence_before();
+                    warp_arrive(CK_YF, c);
+                }
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const uint4 x = attn::lds128(at + ((((wg >> 1) * 4 + 2 * i + q) ^ t7) << 4));
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, zs[4] = {z[2 * i + q].x, z[2 * i + q].y, z[2 * i + q].z, z[2 * i + q].w};
+                    uint32_t r[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        attn::f32x2 o = attn::fma2(widen2(xs[k]), dd, attn::pair(y[8 * q + 2 * k], y[8 * q + 2 * k + 1]));
+                        if (a.z) o = attn::mul2(o, silu2(widen2(zs[k])));
+                        float f[2];
+                        attn::unpair(o, f);
+                        r[k] = pack_bf16x2(f[0], f[1]);
+                    }
+                    z[2 * i + q] = make_uint4(r[0], r[1], r[2], r[3]);
+                }
+            }
+            warp_arrive(CK_XE, c);
+            if (live) {
+                uint16_t* dst = a.out + tok * a.H * P + col + (wg >> 1) * 32;
+                if (y32) st32bytes(dst, z[0], z[1]), st32bytes(dst + 16, z[2], z[3]);
+                else
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(dst)[i] = z[i];
+            }
+            __syncwarp();
+            return true;
+        };
+
+        // ---- what B does besides: dt and the decays' sums, X', the state between two chunks (thread = feature)
+        const int ph = P == 64 ? t >> 6 : 0;  // this feature's head
+        const bool there = ph < heads;
+        auto srow = [&] { return (static_cast<long long>(h0 + (there ? ph : 0)) * P + (P == 64 ? t & 63 : t)) * S + side * (S / 2); };
+        auto state = [&] { return static_cast<long long>(a.H) * P * S; };
+        auto raw_at = [&](int c) {
+            const int i = c * kChunk + t;
+            return valid && i < u.len ? a.dt[(u.begin + i) * a.dt_stride + h] : static_cast<uint16_t>(0);
+        };
+        float gone = 0.f;  // the decay of the chunks so far
+        if (isb) {  // the unit's first state
+            const bool from_pool = STATE ? u.k == 0 : u.parts == 1;
+            const int pieces = STATE ? 0 : u.k * (a.seg / a.sub);
+            const float* src = (from_pool ? a.state + u.slot * state() : a.ws + u.ws * state()) + srow();
+#pragma unroll 1
+            for (int i = 0; i < S / 32; ++i) {
+                float s[16];
+#pragma unroll
+                for (int q = 0; q < 16; q += 4) {
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (there && (!STATE || u.k == 0) && pieces == 0) v = *reinterpret_cast<const float4*>(src + 16 * i + q);
+                    s[q] = v.x, s[q + 1] = v.y, s[q + 2] = v.z, s[q + 3] = v.w;
+                }
+                if (STATE && u.k == 0 && there) {  // the pool's state for the first segment: the last one may have replaced it by then
+                    float* to = a.ws + u.ws * state() + srow() + 16 * i;
+#pragma unroll
+                    for (int q = 0; q < 16; q += 4) *reinterpret_cast<float4*>(to + q) = make_float4(s[q], s[q + 1], s[q + 2], s[q + 3]);
+                }
+                for (int j = 0; j < pieces && there; ++j) {
+                    const long long at = u.ws + 1 + j;
+                    const float f = ex2(a.ws_decay[at * a.H + h0 + ph]);
+                    const float* from = a.ws + at * state() + srow() + 16 * i;
+#pragma unroll
+                    for (int q = 0; q < 16; q += 4) {
+                        const float4 v = *reinterpret_cast<const float4*>(from + q);
+                        s[q] = fmaf(f, s[q], v.x), s[q + 1] = fmaf(f, s[q + 1], v.y), s[q + 2] = fmaf(f, s[q + 2], v.z), s[q + 3] = fmaf(f, s[q + 3], v.w);
+                    }
+                }
+                __syncwarp();
+                tc::st16(trow + K::TM_S + side * (S / 2) + 16 * i, s);
+            }
+            tc::wait_st();
+        }
+        uint16_t raw = isb ? raw_at(0) : static_cast<uint16_t>(0);
+        float dt = 0.f, behind = 0.f, weight = 0.f;
+        auto decays = [&](int c) {
+            dt = valid && t < u.len - c * kChunk ? softplus(bf16_to_f32(raw) + head_s[hh][1]) : 0.f;
+            raw = raw_at(c + 1);
+            const float step = head_s[hh][0] * dt;
+            float upto = step;
+            behind = __shfl_down_sync(kFullMask, step, 1);
+            if (lane == 31) behind = 0.f;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const float x = __shfl_up_sync(kFullMask, upto, o), y = __shfl_down_sync(kFullMask, behind, o);
+                if (lane >= o) upto += x;
+                if (lane + o < 32) behind += y;
+            }
+            float* V = vec(c, hh);
+            if (P == 64 || side == 0) {
+                V[t] = upto;
+                V[kChunk + t] = dt * ex2(behind);
+                V[2 * kChunk + t] = dt;
+                if (lane == 31) V[3 * kChunk + w] = upto;
+            }
+            warp_arrive(CK_V, c);
+        };
+        // The row times its weight to X': in bf16 arithmetic, with the weight as w0 + w1.  h = x w0, rounded; x w0 - h is
+        // exact (16 bits less the first 8); with x w1 added it is the low part.
+        auto weigh = [&](int c, bool high, uint32_t to) {
+            const __nv_bfloat16 wh = __float2bfloat16(weight);
+            const int t7 = anew(t) & 7;
+            const __nv_bfloat162 w0 = __bfloat162bfloat162(wh), w1 = __bfloat162bfloat162(__float2bfloat16(weight - __bfloat162float(wh)));
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const uint32_t at = line + ((q ^ t7) << 4);
+                const uint4 p = attn::lds128(sb + K::OFF_X + (c & 1) * K::X + at);
+                uint32_t v[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const __nv_bfloat162 x2 = *reinterpret_cast<const __nv_bfloat162*>(&v[k]);
+                    __nv_bfloat162 r = __hmul2_rn(x2, w0);
+                    if (!high) r = __hfma2(x2, w1, __hfma2(x2, w0, __hneg2(r)));
+                    v[k] = *reinterpret_cast<const uint32_t*>(&r);
+                }
+                attn::sts128(sb + to + at, make_uint4(v[0], v[1], v[2], v[3]));
+            }
+        };
+        // X', high parts, and the state that chunk c begins with: a copy in bf16 for Y, and the decayed state
+        auto begin = [&](int c) -> bool {
+            const int rows = min(kChunk, u.len - c * kChunk);
+            if (!warp_wait(CK_X, c) || !warp_wait(CK_V, c)) return false;
+            {
+                const float* W = vec(c, hh) + 3 * kChunk;
+                for (int j = w + 1; j < 4; ++j) behind += W[j];
+                weight = dt * ex2(behind);
+            }
+            const float* W = vec(c, ph) + 3 * kChunk;  // of this feature's head
+            const float all = (W[0] + W[1]) + (W[2] + W[3]), keep = ex2(all);
+            gone += all;
+            if (rows < kChunk || !valid) {  // what a weight of zero meets must be finite: rows behind the sequence may hold anything
+                if (!warp_wait(CK_BC, c)) return false;
+                const uint4 none = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    if (t >= rows || !valid) attn::sts128(sb + K::OFF_X + (c & 1) * K::X + line + (q << 4), none);
+                    if (t >= rows && (S == 128 || side == 0)) attn::sts128(sb + K::OFF_B + c % NCB * K::CB + line + (q << 4), none);
+                }
+            }
+            if (c > 0 && !warp_wait(CK_UPH, c - 1)) return false;
+            weigh(c, true, K::OFF_XH);
+            if (c > 0 && !warp_wait(CK_UPD, c - 1)) return false;
+            const attn::f32x2 kk = attn::pair(keep, keep);
+            const int ts = anew(t);
+#pragma unroll
+            for (int i = 0; i < S / 32; ++i) {
+                float s[16];
+                const int n0 = side * (S / 2) + 16 * i;
+                tc::ld16(trow + K::TM_S + n0, s);
+                tc::wait_ld();
+                if constexpr (!STATE) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        attn::sts128(sb + K::OFF_SX + tc::sw_chunk(ts, n0 / 8 + q, 128),
+                                     make_uint4(pack_bf16x2(s[8 * q], s[8 * q + 1]), pack_bf16x2(s[8 * q + 2], s[8 * q + 3]), pack_bf16x2(s[8 * q + 4], s[8 * q + 5]),
+                                                pack_bf16x2(s[8 * q + 6], s[8 * q + 7])));
+                }
+#pragma unroll
+                for (int q = 0; q < 16; q += 2) attn::unpair(attn::mul2(attn::pair(s[q], s[q + 1]), kk), s + q);
+                tc::st16(trow + K::TM_S + n0, s);
+            }
+            tc::wait_st();
+            tc::fence_before();
+            tc::fence_proxy_async();
+            warp_arrive(CK_S, c);
+            return true;
+        };
+        bool ok = true;
+        if (!STATE && !isb) {
+            for (int j = w + 1; j < 4; ++j) {  // tokens behind the row's: zero, once for all
+                const uint32_t zero[16] = {};
+                if (P == 64 || wg == 0) attn::tm_st16(tM + 16 * j, zero);
+            }
+        }
+#pragma unroll 1
+        for (int c = -1; c < u.chunks && (isb || !STATE); ++c) {
+            if (c >= 0) {
+                if constexpr (!STATE) {
+                    ok = (isb || warp_wait(CK_V, c)) && weights(c);
+                    if (!ok) break;
+                    ok = warp_wait(CK_CS, c);
+                    if (!ok) break;
+                }
+                if (isb) {  // the state's copy has been read: its place is X's low parts' now
+                    weigh(c, false, K::OFF_SX);
+                    tc::fence_proxy_async();
+                    warp_arrive(CK_XL, c);
+                    if (STATE) warp_arrive(CK_XE, c);
+                }
+                if constexpr (!STATE) scale_y(c);
+            }
+            if (isb && c + 1 < u.chunks) {
+                decays(c + 1);
+                ok = begin(c + 1);
+            }
+            if (!STATE && c >= 0) ok = ok && output(c);
+            if (!ok) break;
+        }
+        ok = ok && isb && warp_wait(CK_UPD, u.chunks - 1);
+        if (ok && (STATE || u.k == u.parts - 1)) {
+            float* dst = (STATE ? a.ws + (u.ws + 1 + u.k) * state() : a.state + u.slot * state()) + srow();
+            if (STATE && side == 0 && there && (P == 64 ? t & 63 : t) == 0) a.ws_decay[(u.ws + 1 + u.k) * a.H + h0 + ph] = gone;
+#pragma unroll 1
+            for (int i = 0; i < S / 32; ++i) {
+                float v[16];
+                tc::ld16(trow + K::TM_S + side * (S / 2) + 16 * i, v);
+                tc::wait_ld();
+                if (there)
+#pragma unroll
+                    for (int q = 0; q < 16; q += 4) *reinterpret_cast<float4*>(dst + 16 * i + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+                __syncwarp();
+            }
+        }
+    }
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 17) tc::tmem_dealloc(tm, 512);
+    if (tid == 0 && most_polls == 0) atomicOr(a.status, kStatusTimeout);
+}
+
+}  // namespace ssm
+}  // namespace gdn

@@ -101,3 +101,131 @@ def test_without_d(gdn):
     s["D"] = None
     y, state, _ = prefill(gdn, s)
     check(s, y, state, reference(s), True)
+
+
+@pytest.mark.parametrize("lens,H,P,G,S", [([2500, 5, 1400], 1, 64, 1, 128), ([1025], 3, 128, 1, 64), ([0, 4097, 1024, 1300], 2, 64, 2, 64),
+                                          ([3000], 2, 128, 2, 128)])
+def test_segments(gdn, lens, H, P, G, S):
+    """Sequences long enough to be cut: the states of pieces are formed ahead, the pool's state is replaced meanwhile."""
+    s = make(sum(lens), lens, H, P, G, S, pad=3, dt=(0.0003, 0.01))
+    assert gdn.ssm_prefill_workspace_size(len(lens), sum(lens), H, P, S) > 0
+    ref = reference(s)
+    for max_len in (max(lens), 100):  # cut, and not
+        y, state, status = prefill(gdn, s, max_len=max_len)
+        assert status == 0
+        check(s, y, state, ref, True)
+        assert bool((y[sum(lens):] == 9.0).all())
+
+
+def test_strong_decays_keep_their_digits(gdn):
+    """Steps of up to 60 units of decay: sums of hundreds within a chunk, of which a pair of near tokens sees the difference."""
+    s = make(11, [400, 130], 4, 64, 1, 128, dt=(0.5, 4.0))
+    y, state, status = prefill(gdn, s, max_len=400)
+    assert status == 0
+    check(s, y, state, reference(s), True)
+    s["A_log"].fill_(30.0)  # nothing is left of what came before
+    y, state, status = prefill(gdn, s, max_len=400)
+    check(s, y, state, reference(s), True)
+
+
+def test_tokens_behind_a_sequence_may_hold_anything(gdn):
+    """A chunk's tile reaches into the next sequence's rows, and behind the last sequence into what memory holds."""
+    lens = [100, 40, 129, 3]
+    s = make(12, lens, 3, 64, 1, 128, pad=200)
+    clean = prefill(gdn, s, max_len=129)
+    for n in (0, 2):  # sequences 1 and 3 hold no numbers, and the rows behind the last neither
+        cut = dict(s, lens=lens[:n + 1])
+        for name in ("x", "B", "C", "z", "dt"):
+            cut[name] = s[name].clone()
+            cut[name][sum(lens[:n + 1]):] = float("nan")
+        y, state, status = prefill(gdn, cut, cu=s["cu"][:n + 2].contiguous(), slots=s["slots"][:n + 1].contiguous(), max_len=129)
+        assert status == 0
+        T = sum(lens[:n + 1])
+        assert torch.equal(y[:T], clean[0][:T]) and bool((y[T:] == 9.0).all())
+        assert torch.equal(state[s["slots"][:n + 1]], clean[1][s["slots"][:n + 1]])
+
+
+def test_malformed_sequences_are_skipped(gdn):
+    lens = [60, 200, 30]
+    s = make(13, lens, 2, 64, 1, 64, pad=10)
+    for max_len in (8, 200):
+        good, gstate, _ = prefill(gdn, s, max_len=max_len)
+        slots = s["slots"].clone()
+        slots[1] = 5
+        y, state, status = prefill(gdn, s, slots=slots, max_len=max_len)
+        assert status == gdn.STATUS_BAD_CACHE_INDEX
+        assert bool((y[60:260] == 9.0).all()) and torch.equal(y[:60], good[:60]) and torch.equal(y[260:290], good[260:290])
+        assert torch.equal(state[s["slots"][1]], s["state"][s["slots"][1]]) and torch.equal(state[s["slots"][2]], gstate[s["slots"][2]])
+        y, state, status = prefill(gdn, s, cu=torch.tensor([0, 60, 260, 301], device="cuda"), max_len=max_len)
+        assert status == gdn.STATUS_BAD_SEQLENS
+        assert bool((y[260:] == 9.0).all()) and torch.equal(y[:260], good[:260]) and torch.equal(state[s["slots"][2]], s["state"][s["slots"][2]])
+
+
+def test_a_prompt_in_pieces_and_single_tokens(gdn):
+    """A prompt at once, in two pieces, and its last tokens one by one."""
+    s = make(14, [300], 4, 64, 2, 128)
+    ref = reference(s)
+    state = s["state"].clone()
+    outs = []
+    for a, b in ((0, 150), (150, 297), (297, 298), (298, 299), (299, 300)):
+        part = [s[k][a:b] for k in ("x", "dt", "B", "C")]
+        kw = dict(D=s["D"], z=s["z"][a:b])
+        if b - a > 1:
+            outs.append(gdn.ssm_prefill_chunked(*part, s["A_log"], s["dt_bias"], state, s["slots"], torch.tensor([0, b - a], device="cuda"), b - a, **kw))
+        else:
+            outs.append(gdn.ssm_decode_step(*part, s["A_log"], s["dt_bias"], state, s["slots"], **kw))
+    check(s, torch.cat(outs), state, ref, True)
+
+
+def test_captured_with_two_workspaces(gdn):
+    """Two captured calls, replayed on streams of their own at once: each has its own workspace and answers as alone."""
+    calls = []
+    for seed in (15, 16):
+        s = make(seed, [1500, 700], 2, 64, 1, 128)
+        state, out, status = s["state"].clone(), torch.empty_like(s["x"].contiguous()), torch.zeros(1, dtype=torch.int32, device="cuda")
+        ws = torch.empty(gdn.ssm_prefill_workspace_size(2, 2200, 2, 64, 128), dtype=torch.uint8, device="cuda")
+        go = lambda s=s, state=state, out=out, ws=ws, status=status: gdn.ssm_prefill_chunked(  # noqa: E731
+            s["x"], s["dt"], s["B"], s["C"], s["A_log"], s["dt_bias"], state, s["slots"], s["cu"], 1500, D=s["D"], z=s["z"], out=out, workspace=ws, dev_status=status)
+        go()
+        torch.cuda.synchronize()
+        want = out.clone(), state.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            state.copy_(s["state"])
+            go()
+        calls.append((graph, out, state, want, status, go))  # go keeps what the graph reads
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(3):
+        for st, (graph, *_r) in zip(streams, calls):
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, out, state, want, status, _ in calls:
+        assert status.item() == 0 and torch.equal(out, want[0]) and torch.equal(state, want[1])
+
+
+def test_a_wait_that_runs_out_reports_and_the_next_call_is_right(gdn):
+    s = make(17, [1400], 2, 64, 1, 128)
+    try:
+        gdn.set_prefill_wait_limit(1)
+        _, _, status = prefill(gdn, s)
+    finally:
+        gdn.set_prefill_wait_limit(0)
+    assert status & gdn.STATUS_TIMEOUT
+    y, state, status = prefill(gdn, s)
+    assert status == 0
+    check(s, y, state, reference(s), True)
+
+
+def test_refuses_from_python(gdn):
+    s = make(18, [2, 2], 2, 64, 1, 64, strided=False)
+    args = [s["x"], s["dt"], s["B"], s["C"], s["A_log"], s["dt_bias"], s["state"], s["slots"], s["cu"], 2]
+    for i, bad, err in ((0, s["x"].half(), TypeError), (1, s["dt"].T, ValueError), (2, s["B"][:3], ValueError), (3, s["C"][..., ::2], ValueError),
+                        (4, s["A_log"][:1], ValueError), (6, s["state"][..., :32], ValueError), (6, s["state"].double(), TypeError), (7, s["slots"].int(), TypeError),
+                        (8, s["cu"][:2], ValueError), (9, -1, gdn.GdnError)):
+        with pytest.raises(err):
+            gdn.ssm_prefill_chunked(*[bad if j == i else a for j, a in enumerate(args)])
+    with pytest.raises(ValueError):  # four tokens, two sequences
+        gdn.ssm_decode_step(*args[:8])
+    with pytest.raises(gdn.GdnError):
+        gdn.ssm_prefill_chunked(*args, out=s["x"])
