@@ -16,19 +16,6 @@ constexpr int kMaxTileCtas = 160;  // of the tile kernel, likewise
 constexpr size_t kJoinBytes = kMaxCtas * sizeof(AttnJoin);  // at the workspace's start
 static_assert(kJoinBytes % 16 == 0, "the partials are read by 16 bytes");
 
-// Raises a kernel's shared-memory limit once per device.
-template <typename K>
-cudaError_t raise_smem(K kernel, int bytes, std::atomic<unsigned long long>& done) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    if (done.load(std::memory_order_acquire) >> dev & 1) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) done.fetch_or(1ull << dev, std::memory_order_release);
-    return e;
-}
-
 // A cache as rows of D elements, in boxes of `box` rows and `line` bytes (a row, or 128 bytes of it), with the
 // swizzle of that width, or none.
 bool encode_cache(CUtensorMap* map, const void* base, long long rows, int D, int box, int line, bool swizzle, bool f8, bool f16) {

@@ -46,8 +46,8 @@ void read_d(const CacheMoveArgs& a, bool f16, bool f8, cudaStream_t stream) {
 template <int D, bool F16, bool F8, bool HALVES>
 void append(const AppendArgs& a, cudaStream_t stream) {
     constexpr int groups = cache::kThreads / (D / 8), heads = 4;
-    const dim3 grid(static_cast<unsigned>((a.T + groups - 1) / groups), (a.Hq + 2 * a.H + heads - 1) / heads);
-    cache::attn_cache_append_kernel<D, F16, F8, HALVES, heads><<<grid, cache::kThreads, 0, stream>>>(a);
+    const long long grid = (a.T + groups - 1) / groups * ((a.Hq + 2 * a.H + heads - 1) / heads);
+    cache::attn_cache_append_kernel<D, F16, F8, HALVES, heads><<<static_cast<unsigned>(grid), cache::kThreads, 0, stream>>>(a);
 }
 template <int D, bool HALVES>
 void append_d(const AppendArgs& a, bool f16, bool f8, cudaStream_t stream) {

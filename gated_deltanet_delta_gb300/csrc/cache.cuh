@@ -208,8 +208,10 @@ template <int D, bool F16, bool F8, bool HALVES, int HEADS>
 __global__ void __launch_bounds__(kThreads) attn_cache_append_kernel(const __grid_constant__ AppendArgs a) {
     constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
-    const long long t = static_cast<long long>(blockIdx.x) * GROUPS + group;
-    const int h0 = blockIdx.y * HEADS, total = a.Hq + 2 * a.H;
+    // a token's heads in consecutive CTAs: those that quantise among those that copy, and the table's rows in L2
+    const int total = a.Hq + 2 * a.H, parts = (total + HEADS - 1) / HEADS, part = blockIdx.x % parts;
+    const long long t = static_cast<long long>(blockIdx.x / parts) * GROUPS + group;
+    const int h0 = part * HEADS;
     const bool here = t < a.T;
     uint4 x[HEADS];
 #pragma unroll
@@ -222,7 +224,7 @@ __global__ void __launch_bounds__(kThreads) attn_cache_append_kernel(const __gri
     }
     const long long pos = here ? a.positions[t] : -1;
     const bool known = pos >= 0 && pos < a.max_pos;
-    if (here && !known && lane == 0 && blockIdx.y == 0) atomicOr(a.status, kStatusBadPosition);
+    if (here && !known && lane == 0 && part == 0) atomicOr(a.status, kStatusBadPosition);
     // the cached row of the token's first head (-1: none); a negative slot: the token's key and value are not kept
     long long row0 = -1;
     if (known && h0 + HEADS > a.Hq) {

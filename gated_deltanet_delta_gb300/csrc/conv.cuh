@@ -13,12 +13,14 @@
 #include "attn_mma.cuh"
 #include "common.cuh"
 #include "kernel_args.h"
+#include "tile_util.cuh"
 
 namespace gdn {
 namespace conv {
 
 constexpr int kThreads = 128;
-constexpr int kTokens = 16;
+constexpr int kTokens = 32;
+constexpr int kStep = 8;  // tokens in registers, and as many on their way
 
 // A token's sequence: which, where it begins and ends; n = -1 for a token of no (well-formed) sequence.
 struct Place {
@@ -37,19 +39,22 @@ __device__ __forceinline__ Place place_of(const int64_t* cu, int num_seqs, long 
     return p;
 }
 
+using attn::f32x2;
+
+// Eight channels as pairs.
 template <int TAPS>
 struct Weights {
-    float w[TAPS][8], b[8];
+    f32x2 w[TAPS][4], b[4];
     __device__ __forceinline__ void load(const ConvArgs& a, int c) {
         float f[8 * TAPS];
         const float4* src = reinterpret_cast<const float4*>(a.w + static_cast<long long>(c) * TAPS);
 #pragma unroll
         for (int i = 0; i < 2 * TAPS; ++i) reinterpret_cast<float4*>(f)[i] = __ldg(src + i);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
 #pragma unroll
-            for (int j = 0; j < TAPS; ++j) w[j][i] = f[i * TAPS + j];
-            b[i] = a.bias ? __ldg(a.bias + c + i) : 0.f;
+            for (int j = 0; j < TAPS; ++j) w[j][i] = attn::pair(f[2 * i * TAPS + j], f[(2 * i + 1) * TAPS + j]);
+            b[i] = a.bias ? attn::pair(__ldg(a.bias + c + 2 * i), __ldg(a.bias + c + 2 * i + 1)) : attn::pair(0.f, 0.f);
         }
     }
 };
@@ -57,7 +62,7 @@ struct Weights {
 // TAPS - 1 values of each of eight channels, oldest first.
 template <int TAPS>
 struct Past {
-    float v[TAPS - 1][8];
+    f32x2 v[TAPS - 1][4];
     __device__ __forceinline__ void load(const float* hist) {
         float f[8 * (TAPS - 1)];
 #pragma unroll
@@ -65,20 +70,24 @@ struct Past {
 #pragma unroll
         for (int j = 0; j < TAPS - 1; ++j)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[j][i] = f[i * (TAPS - 1) + j];
+            for (int i = 0; i < 4; ++i) v[j][i] = attn::pair(f[2 * i * (TAPS - 1) + j], f[(2 * i + 1) * (TAPS - 1) + j]);
     }
     __device__ __forceinline__ void store(float* hist) const {
-        float f[8 * (TAPS - 1)];
+        float f[8 * (TAPS - 1)], u[2];
 #pragma unroll
         for (int j = 0; j < TAPS - 1; ++j)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i * (TAPS - 1) + j] = v[j][i];
+            for (int i = 0; i < 4; ++i) {
+                attn::unpair(v[j][i], u);
+                f[2 * i * (TAPS - 1) + j] = u[0];
+                f[(2 * i + 1) * (TAPS - 1) + j] = u[1];
+            }
 #pragma unroll
         for (int i = 0; i < 2 * (TAPS - 1); ++i) reinterpret_cast<float4*>(hist)[i] = reinterpret_cast<const float4*>(f)[i];
     }
-    __device__ __forceinline__ void push(const float (&x)[8]) {
+    __device__ __forceinline__ void push(const f32x2 (&x)[4]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
 #pragma unroll
             for (int j = 0; j + 1 < TAPS - 1; ++j) v[j][i] = v[j + 1][i];
             v[TAPS - 2][i] = x[i];
@@ -87,30 +96,31 @@ struct Past {
 };
 
 template <bool F16>
-__device__ __forceinline__ void widen8(const uint4& p, float (&f)[8]) {
+__device__ __forceinline__ void widen8(const uint4& p, f32x2 (&f)[4]) {
     const uint32_t w[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float2 u = attn::unpack2<F16>(w[j]);
-        f[2 * j] = u.x;
-        f[2 * j + 1] = u.y;
+        f[j] = attn::pair(u.x, u.y);
     }
 }
 
 // One token's eight outputs.
 template <int TAPS, bool F16>
-__device__ __forceinline__ uint4 token(const Weights<TAPS>& w, const Past<TAPS>& p, const float (&x)[8], bool silu) {
-    float y[8];
+__device__ __forceinline__ uint4 token(const Weights<TAPS>& w, const Past<TAPS>& p, const f32x2 (&x)[4], bool silu) {
+    uint32_t r[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        y[i] = w.b[i];
+    for (int i = 0; i < 4; ++i) {
+        f32x2 y = w.b[i];
 #pragma unroll
-        for (int j = 0; j < TAPS - 1; ++j) y[i] = fmaf(w.w[j][i], p.v[j][i], y[i]);
-        y[i] = fmaf(w.w[TAPS - 1][i], x[i], y[i]);
-        // e^-y beyond the type's range gives y / infinity = -0, the limit
-        if (silu) y[i] = __fdividef(y[i], 1.f + __expf(fminf(-y[i], 80.f)));
+        for (int j = 0; j < TAPS - 1; ++j) y = attn::fma2(w.w[j][i], p.v[j][i], y);
+        y = attn::fma2(w.w[TAPS - 1][i], x[i], y);
+        if (silu) y = attn::silu2(y);
+        float f[2];
+        attn::unpair(y, f);
+        r[i] = attn::pack2<F16>(f[0], f[1]);
     }
-    return make_uint4(attn::pack2<F16>(y[0], y[1]), attn::pack2<F16>(y[2], y[3]), attn::pack2<F16>(y[4], y[5]), attn::pack2<F16>(y[6], y[7]));
+    return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // Where channel c of token 0 goes, and the distance between tokens.
@@ -130,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) short_conv_step_kernel(const __grid_
         return;
     }
     if (c >= a.C) return;
-    float x[8];
+    f32x2 x[4];
     widen8<F16>(__ldcs(reinterpret_cast<const uint4*>(a.x + n * a.x_stride + c)), x);
     float* hist = a.hist + (slot * a.C + c) * (TAPS - 1);
     Past<TAPS> p;
@@ -146,11 +156,21 @@ __global__ void __launch_bounds__(kThreads) short_conv_step_kernel(const __grid_
 
 template <int TAPS, bool F16>
 __global__ void __launch_bounds__(kThreads) short_conv_kernel(const __grid_constant__ ConvArgs a) {
-    __shared__ long long slot_s[kTokens];  // of each token; -1: the token belongs to no sequence, -2: as the token before
+    __shared__ long long slot_s[kTokens];  // of each token; -1: of no (well-formed) sequence
     __shared__ int ahead_s[kTokens];       // tokens of its sequence ahead of it, at most TAPS - 1
     const int c = (blockIdx.y * kThreads + threadIdx.x) * 8;
     const long long t0 = static_cast<long long>(blockIdx.x) * kTokens;
     const int count = static_cast<int>(a.T - t0 < kTokens ? a.T - t0 : kTokens);
+    const bool on = c < a.C;
+    const uint16_t* src = a.x + t0 * a.x_stride + c;
+    auto fetch = [&](uint4 (&x)[kStep], int i0) {
+#pragma unroll
+        for (int i = 0; i < kStep; ++i)
+            x[i] = on && i0 + i < count ? *reinterpret_cast<const uint4*>(src + (i0 + i) * a.x_stride) : make_uint4(0, 0, 0, 0);
+    };
+    uint4 x[kStep], next[kStep];
+    fetch(x, 0);
+    int odd = 0;  // whether the token begins a sequence, or belongs to none
     if (threadIdx.x < kTokens) {
         const int i = threadIdx.x;
         long long slot = -1;
@@ -165,13 +185,9 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(const __grid_const
         }
         slot_s[i] = slot;
         ahead_s[i] = ahead;
+        odd = slot < 0 || (i > 0 && ahead == 0);
     }
-    const uint16_t* src = a.x + t0 * a.x_stride + c;
-    const bool on = c < a.C;
-    uint4 x[kTokens];
-#pragma unroll
-    for (int i = 0; i < kTokens; ++i) x[i] = on && i < count ? *reinterpret_cast<const uint4*>(src + i * a.x_stride) : make_uint4(0, 0, 0, 0);
-    __syncthreads();
+    const bool plain = !__syncthreads_or(odd);  // one sequence throughout
     if (!on) return;
     Weights<TAPS> w;
     w.load(a, c);
@@ -187,21 +203,35 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(const __grid_const
 #pragma unroll
             for (int j = 0; j < TAPS - 1; ++j)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) p.v[j][i] = 0.f;
+                for (int i = 0; i < 4; ++i) p.v[j][i] = attn::pair(0.f, 0.f);
         }
         for (int j = slot >= 0 ? ahead : 0; j > 0; --j) {
-            float f[8];
+            f32x2 f[4];
             widen8<F16>(*reinterpret_cast<const uint4*>(src - j * a.x_stride), f);
             p.push(f);
         }
     }
+    if (plain) {
+#pragma unroll 1
+        for (int i0 = 0; i0 < kTokens; i0 += kStep) {
+            fetch(next, i0 + kStep);
 #pragma unroll
-    for (int i = 0; i < kTokens; ++i) {
-        if (i >= count) break;
+            for (int i = 0; i < kStep; ++i) {
+                f32x2 f[4];
+                widen8<F16>(x[i], f);
+                __stcs(reinterpret_cast<uint4*>(out + static_cast<long long>(i0 + i) * width), token<TAPS, F16>(w, p, f, a.silu));
+                p.push(f);
+                x[i] = next[i];
+            }
+        }
+        return;
+    }
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
         const long long slot = slot_s[i];
         if (i > 0 && ahead_s[i] == 0 && slot >= 0) p.load(a.hist + (slot * a.C + c) * (TAPS - 1));
-        float f[8];
-        widen8<F16>(x[i], f);
+        f32x2 f[4];
+        widen8<F16>(*reinterpret_cast<const uint4*>(src + i * a.x_stride), f);
         if (slot >= 0) __stcs(reinterpret_cast<uint4*>(out + static_cast<long long>(i) * width), token<TAPS, F16>(w, p, f, a.silu));
         p.push(f);
     }
@@ -223,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) short_conv_history_kernel(const __gr
     if (end - begin < TAPS - 1) p.load(hist);
     const int fresh = static_cast<int>(end - begin < TAPS - 1 ? end - begin : TAPS - 1);
     for (int j = fresh; j > 0; --j) {
-        float f[8];
+        f32x2 f[4];
         widen8<F16>(*reinterpret_cast<const uint4*>(a.x + (end - j) * a.x_stride + c), f);
         p.push(f);
     }

@@ -27,6 +27,19 @@ inline cudaError_t sm_count(int* n) {
     return cudaSuccess;
 }
 
+// Raises a kernel's shared-memory limit once per device.
+template <typename K>
+inline cudaError_t raise_smem(K kernel, int bytes, std::atomic<unsigned long long>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (done.load(std::memory_order_acquire) >> dev & 1) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(1ull << dev, std::memory_order_release);
+    return e;
+}
+
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no link against libcuda).
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static std::once_flag once;

@@ -4,7 +4,7 @@
 // 2^-126): for the operand of a product in 8 bits the whole range is used; a power of two would leave up to half of it.
 //
 // Each value is read once and written once: the bound is HBM.  blockDim.x threads hold a row in registers, R
-// pieces of eight features each, blockDim.y rows per CTA; the sum of squares is taken over the rounded r, in fp32.
+// pieces of eight features each, blockDim.y short rows per CTA.  The sum of squares is taken over the rounded r, in fp32.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -16,7 +16,7 @@
 namespace gdn {
 namespace norm {
 
-constexpr int kMaxThreads = 1024;
+constexpr int kMaxThreads = 512;
 
 // Sum (or largest) over the row's threads; every thread gets it.  buf: 32 floats per row.
 template <bool MAX>
@@ -39,24 +39,24 @@ __device__ __forceinline__ float row_join(float v, float* buf) {
     return v;
 }
 
-template <bool F16, bool F8, int R>
-__global__ void __launch_bounds__(R == 1 ? 256 : kMaxThreads) add_rms_norm_kernel(const __grid_constant__ NormArgs a) {
-    __shared__ float buf[2][8][32];
-    const long long t = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
-    const bool here = t < a.T;
-    const int pieces = a.C / 8;
-    uint4 x[R], r[R];
+__device__ __forceinline__ float scale_of(float amax) { return amax > 0.f ? fmaxf(amax * (1.f / 448.f), 1.17549435e-38f) : 1.f; }
+// Eight values to e4m3.
+__device__ __forceinline__ uint2 to_e4m3(const float (&f)[8], float up) {
+    uint32_t q[4];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int p = threadIdx.x + i * blockDim.x;
-        const bool on = here && p < pieces;
-        x[i] = on ? *reinterpret_cast<const uint4*>(a.x + t * a.x_stride + p * 8) : make_uint4(0, 0, 0, 0);
-        r[i] = on && a.residual ? *reinterpret_cast<const uint4*>(a.residual + t * a.C + p * 8) : make_uint4(0, 0, 0, 0);
-    }
+    for (int j = 0; j < 4; ++j) q[j] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * j] * up, f[2 * j + 1] * up), __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+}
+
+// What a thread does with its pieces of row t: x, r in; the residual, y and the scales out.  The joins take part in the
+// CTA's barriers, so every thread comes here (`here`: whether it has a row).
+template <bool F16, bool F8, int R>
+__device__ __forceinline__ void row(const NormArgs& a, long long t, bool here, uint4 (&x)[R], const uint4 (&r)[R], float* sums, float* tops) {
+    const int pieces = a.C / 8;
+    auto piece = [&](int i) { return static_cast<int>(threadIdx.x + i * blockDim.x); };
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const int p = threadIdx.x + i * blockDim.x;
         uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
         const uint32_t v[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
 #pragma unroll
@@ -69,32 +69,35 @@ __global__ void __launch_bounds__(R == 1 ? 256 : kMaxThreads) add_rms_norm_kerne
             sum = fmaf(f.x, f.x, fmaf(f.y, f.y, sum));
         }
         x[i] = make_uint4(u[0], u[1], u[2], u[3]);
-        if (a.residual && here && p < pieces) *reinterpret_cast<uint4*>(a.residual + t * a.C + p * 8) = x[i];
+        if (a.residual && here && piece(i) < pieces) *reinterpret_cast<uint4*>(a.residual + t * a.C + piece(i) * 8) = x[i];
     }
-    const float inv = rsqrtf(row_join<false>(sum, buf[0][threadIdx.y]) / static_cast<float>(a.C) + a.eps);
-    float amax = 0.f;  // of the row (one scale per row)
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int p = threadIdx.x + i * blockDim.x;
-        const bool on = here && p < pieces;
+    const float inv = rsqrtf(row_join<false>(sum, sums) / static_cast<float>(a.C) + a.eps);
+    auto normed = [&](int i, float (&f)[8]) {
         const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        float f[8];
-        float4 w0 = make_float4(0.f, 0.f, 0.f, 0.f), w1 = w0;
-        if (p < pieces) {
-            w0 = __ldg(reinterpret_cast<const float4*>(a.w + p * 8));
-            w1 = __ldg(reinterpret_cast<const float4*>(a.w + p * 8 + 4));
+        float4 p = make_float4(0.f, 0.f, 0.f, 0.f), q = p;
+        if (piece(i) < pieces) {
+            p = __ldg(reinterpret_cast<const float4*>(a.w + piece(i) * 8));
+            q = __ldg(reinterpret_cast<const float4*>(a.w + piece(i) * 8 + 4));
         }
-        const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        const float w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float2 b = attn::unpack2<F16>(u[j]);
             f[2 * j] = b.x * inv * w[2 * j];
             f[2 * j + 1] = b.y * inv * w[2 * j + 1];
         }
+    };
+    float amax = 0.f;  // of the row (one scale per row)
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int p = piece(i);
+        const bool on = here && p < pieces;
+        float f[8];
+        normed(i, f);
         if constexpr (!F8) {
             if (on)
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + t * a.C + p * 8) =
-                    make_uint4(attn::pack2<F16>(f[0], f[1]), attn::pack2<F16>(f[2], f[3]), attn::pack2<F16>(f[4], f[5]), attn::pack2<F16>(f[6], f[7]));
+                __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + t * a.C + p * 8),
+                       make_uint4(attn::pack2<F16>(f[0], f[1]), attn::pack2<F16>(f[2], f[3]), attn::pack2<F16>(f[4], f[5]), attn::pack2<F16>(f[6], f[7])));
         } else {
             float m = 0.f;
 #pragma unroll
@@ -103,14 +106,9 @@ __global__ void __launch_bounds__(R == 1 ? 256 : kMaxThreads) add_rms_norm_kerne
                 amax = fmaxf(amax, m);
             } else {
                 for (int o = a.lanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
-                const float scale = m > 0.f ? fmaxf(m / 448.f, 1.17549435e-38f) : 1.f, up = 1.f / scale;
+                const float scale = scale_of(m);
                 if (on) {
-                    uint2 q;
-                    q.x = __nv_cvt_float2_to_fp8x2(make_float2(f[0] * up, f[1] * up), __NV_SATFINITE, __NV_E4M3) |
-                          __nv_cvt_float2_to_fp8x2(make_float2(f[2] * up, f[3] * up), __NV_SATFINITE, __NV_E4M3) << 16;
-                    q.y = __nv_cvt_float2_to_fp8x2(make_float2(f[4] * up, f[5] * up), __NV_SATFINITE, __NV_E4M3) |
-                          __nv_cvt_float2_to_fp8x2(make_float2(f[6] * up, f[7] * up), __NV_SATFINITE, __NV_E4M3) << 16;
-                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + t * a.C + p * 8) = q;
+                    __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + t * a.C + p * 8), to_e4m3(f, attn::fast_rcp(scale)));
                     if (p % a.lanes == 0) a.scale[t * (pieces / a.lanes) + p / a.lanes] = scale;
                 }
             }
@@ -118,26 +116,34 @@ __global__ void __launch_bounds__(R == 1 ? 256 : kMaxThreads) add_rms_norm_kerne
     }
     if constexpr (F8) {
         if (a.lanes == 0) {
-            amax = row_join<true>(amax, buf[1][threadIdx.y]);
-            const float scale = amax > 0.f ? fmaxf(amax / 448.f, 1.17549435e-38f) : 1.f, up = 1.f / scale;
+            amax = row_join<true>(amax, tops);
+            const float scale = scale_of(amax), up = attn::fast_rcp(scale);
             if (here && threadIdx.x == 0) a.scale[t] = scale;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const int p = threadIdx.x + i * blockDim.x;
-                if (!here || p >= pieces) continue;
-                const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                const float4 w0 = __ldg(reinterpret_cast<const float4*>(a.w + p * 8)), w1 = __ldg(reinterpret_cast<const float4*>(a.w + p * 8 + 4));
-                const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-                uint32_t q[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 b = attn::unpack2<F16>(u[j]);
-                    q[j] = __nv_cvt_float2_to_fp8x2(make_float2(b.x * inv * w[2 * j] * up, b.y * inv * w[2 * j + 1] * up), __NV_SATFINITE, __NV_E4M3);
-                }
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + t * a.C + p * 8) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+                if (!here || piece(i) >= pieces) continue;
+                float f[8];
+                normed(i, f);
+                __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + t * a.C + piece(i) * 8), to_e4m3(f, up));
             }
         }
     }
+}
+
+template <bool F16, bool F8, int R>
+__global__ void __launch_bounds__(R == 1 ? 256 : kMaxThreads, R == 1 ? 6 : R == 2 ? 3 : 1) add_rms_norm_kernel(const __grid_constant__ NormArgs a) {
+    __shared__ float buf[2][8][32];
+    const long long t = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const bool here = t < a.T;
+    uint4 x[R], r[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int p = threadIdx.x + i * blockDim.x;
+        const bool on = here && p < a.C / 8;
+        x[i] = on ? *reinterpret_cast<const uint4*>(a.x + t * a.x_stride + p * 8) : make_uint4(0, 0, 0, 0);
+        r[i] = on && a.residual ? *reinterpret_cast<const uint4*>(a.residual + t * a.C + p * 8) : make_uint4(0, 0, 0, 0);
+    }
+    row<F16, F8, R>(a, t, here, x, r, buf[0][threadIdx.y], buf[1][threadIdx.y]);
 }
 
 }  // namespace norm

@@ -27,20 +27,17 @@ template <int P, int S, bool STATE>
 cudaError_t run(const SsmArgs& a, const SsmMaps& maps, unsigned grid, cudaStream_t stream) {
     using C = ssm::ChunkCfg<S>;
     static std::atomic<unsigned long long> done{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    cudaError_t e = raise_smem(ssm::ssm_chunk_kernel<P, S, STATE>, C::SMEM, done);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    if (!(done.load(std::memory_order_acquire) >> dev & 1)) {
-        e = cudaFuncSetAttribute(ssm::ssm_chunk_kernel<P, S, STATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-        if (e != cudaSuccess) return e;
-        // the split of registers among roles waits forever where the launch has fewer than it adds up to
+    // the split of registers among roles waits forever where the launch has fewer than it adds up to
+    static std::atomic<int> regs{0};
+    if (regs.load(std::memory_order_relaxed) == 0) {
         cudaFuncAttributes fa;
         e = cudaFuncGetAttributes(&fa, ssm::ssm_chunk_kernel<P, S, STATE>);
         if (e != cudaSuccess) return e;
-        if (fa.numRegs < ssm::kRegsLaunch) return cudaErrorInvalidConfiguration;
-        done.fetch_or(1ull << dev, std::memory_order_release);
+        regs.store(fa.numRegs, std::memory_order_relaxed);
     }
+    if (regs.load(std::memory_order_relaxed) < ssm::kRegsLaunch) return cudaErrorInvalidConfiguration;
     ssm::ssm_chunk_kernel<P, S, STATE><<<grid, ssm::kChunkNT, C::SMEM, stream>>>(a, maps);
     return cudaGetLastError();
 }
@@ -87,8 +84,13 @@ cudaError_t chunks(SsmArgs a, long long max_len, void* workspace, cudaStream_t s
 void launch_ssm_steps(SsmArgs a, int S, cudaStream_t stream) {
     a.tiles = a.P / ssm::kRows;
     const unsigned grid = static_cast<unsigned>(a.num_seqs) * a.H * a.tiles;
-    if (S == 64) ssm::ssm_steps_kernel<64, 4><<<grid, ssm::kRows / 2 * 4, 0, stream>>>(a);
-    else ssm::ssm_steps_kernel<128, 8><<<grid, ssm::kRows / 2 * 8, 0, stream>>>(a);
+    if (S == 64) {
+        if (!a.cu) ssm::ssm_steps_kernel<64, 4, true><<<grid, ssm::kRows / 2 * 4, 0, stream>>>(a);
+        else ssm::ssm_steps_kernel<64, 4, false><<<grid, ssm::kRows / 2 * 4, 0, stream>>>(a);
+    } else {
+        if (!a.cu) ssm::ssm_steps_kernel<128, 8, true><<<grid, ssm::kRows / 2 * 8, 0, stream>>>(a);
+        else ssm::ssm_steps_kernel<128, 8, false><<<grid, ssm::kRows / 2 * 8, 0, stream>>>(a);
+    }
 }
 
 // Two states for every piece that a call of T tokens can have, and their decays.

@@ -31,11 +31,12 @@ __device__ __forceinline__ bool sequence(const SsmArgs& a, int n, long long& beg
     return !bad && !off;
 }
 
-template <int S, int TPR>
-__global__ void __launch_bounds__(kRows / 2 * TPR) ssm_steps_kernel(const __grid_constant__ SsmArgs a) {
-    constexpr int NT = kRows / 2 * TPR, NV = S / (4 * TPR), RPP = NT / TPR;
-    __shared__ float4 Bs[kSteps][S / 4], Cs[kSteps][S / 4];
-    __shared__ float xs[kSteps][kRows], keep_s[kSteps], dt_s[kSteps];
+// ONE: one token per sequence.  Without the loop over tokens it takes fewer registers, and three CTAs fit an SM.
+template <int S, int TPR, bool ONE>
+__global__ void __launch_bounds__(kRows / 2 * TPR, 768 / (kRows / 2 * TPR)) ssm_steps_kernel(const __grid_constant__ SsmArgs a) {
+    constexpr int NT = kRows / 2 * TPR, NV = S / (4 * TPR), RPP = NT / TPR, STEPS = ONE ? 1 : kSteps;
+    __shared__ float4 Bs[STEPS][S / 4], Cs[STEPS][S / 4];
+    __shared__ float xs[STEPS][kRows], keep_s[STEPS], dt_s[STEPS];
     const int tile = blockIdx.x % a.tiles, h = blockIdx.x / a.tiles % a.H, n = blockIdx.x / a.tiles / a.H;
     const int g = h / (a.H / a.G), p0 = tile * kRows;
     const int lr = threadIdx.x % TPR, rw = threadIdx.x / TPR;
@@ -48,9 +49,9 @@ __global__ void __launch_bounds__(kRows / 2 * TPR) ssm_steps_kernel(const __grid
 #pragma unroll
         for (int m = 0; m < NV; ++m) s[r][m] = ld_stream(st + (r * RPP + rw) * (S / 4) + lr + TPR * m);
     const float A = -expf(a.A_log[h]), bias = a.dt_bias[h], D = a.D ? a.D[h] : 0.f;
-    for (long long t0 = begin; t0 < end; t0 += kSteps) {
-        const int count = static_cast<int>(end - t0 < kSteps ? end - t0 : kSteps);
-        if (t0 > begin) __syncthreads();  // the block before is no longer read
+    for (long long t0 = begin; t0 < end; t0 += STEPS) {
+        const int count = ONE ? 1 : static_cast<int>(end - t0 < STEPS ? end - t0 : STEPS);
+        if (!ONE && t0 > begin) __syncthreads();  // the block before is no longer read
         for (int i = threadIdx.x; i < count * (S / 4); i += NT) {
             const int k = i / (S / 4), j = i % (S / 4);
             Bs[k][j] = bf16x4_to_f32x4(*reinterpret_cast<const uint2*>(a.B + (t0 + k) * a.b_stride + g * S + 4 * j));
@@ -89,6 +90,7 @@ __global__ void __launch_bounds__(kRows / 2 * TPR) ssm_steps_kernel(const __grid
                 }
             }
         }
+        if (ONE) break;
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r)

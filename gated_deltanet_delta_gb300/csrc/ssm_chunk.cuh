@@ -99,19 +99,6 @@ __device__ __forceinline__ int anew(int x) {
     return x;
 }
 __device__ __forceinline__ float ex2(float x) { return attn::fast_exp2(x); }
-// Two packed bf16 as a pair of fp32.
-__device__ __forceinline__ attn::f32x2 widen2(uint32_t w) { return attn::pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
-// z / (1 + e^-z) of both: one reciprocal, of the denominators' product.  e^-z is held at e^40, whose square is still a number: what
-// that leaves for a z below -40 is less than 2^-50 in the place of less than e^-40 |z|.
-__device__ __forceinline__ attn::f32x2 silu2(attn::f32x2 z) {
-    float e[2];
-    attn::unpair(attn::mul2(z, attn::pair(-1.44269504f, -1.44269504f)), e);
-    const attn::f32x2 d = attn::add2(attn::pair(ex2(fminf(e[0], 57.7f)), ex2(fminf(e[1], 57.7f))), attn::pair(1.f, 1.f));
-    attn::unpair(d, e);
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e[0] * e[1]));
-    return attn::mul2(z, attn::mul2(attn::pair(e[1], e[0]), attn::pair(r, r)));
-}
 
 // The unit with number `rank`: one warp walks the sequences.  A sequence of more than a.seg chunks has the states of its
 // pieces in the workspace: the first the pool's, then one behind each piece.
@@ -466,8 +453,8 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                     uint32_t r[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        attn::f32x2 o = attn::fma2(widen2(xs[k]), dd, attn::pair(y[8 * q + 2 * k], y[8 * q + 2 * k + 1]));
-                        if (a.z) o = attn::mul2(o, silu2(widen2(zs[k])));
+                        attn::f32x2 o = attn::fma2(attn::widen2(xs[k]), dd, attn::pair(y[8 * q + 2 * k], y[8 * q + 2 * k + 1]));
+                        if (a.z) o = attn::mul2(o, attn::silu2(attn::widen2(zs[k])));
                         float f[2];
                         attn::unpair(o, f);
                         r[k] = pack_bf16x2(f[0], f[1]);

@@ -3,6 +3,7 @@
 // moved between warpgroups.
 #pragma once
 
+#include "attn_mma.cuh"
 #include "common.cuh"
 
 namespace gdn {
@@ -54,6 +55,19 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+// Two packed bf16 as a pair of fp32.
+__device__ __forceinline__ f32x2 widen2(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+// z / (1 + e^-z) of both, as z e^z / (1 + e^z), which loses nothing for a z far below zero; one reciprocal, of the
+// denominators' product.  e^z is held at e^40, whose square is still a number: from there on the quotient rounds to 1.
+__device__ __forceinline__ f32x2 silu2(f32x2 z) {
+    float e[2], r;
+    unpair(mul2(z, pair(1.44269504f, 1.44269504f)), e);
+    const f32x2 t = pair(fast_exp2(fminf(e[0], 57.7f)), fast_exp2(fminf(e[1], 57.7f)));
+    unpair(add2(t, pair(1.f, 1.f)), e);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e[0] * e[1]));
+    return mul2(mul2(z, t), mul2(pair(e[1], e[0]), pair(r, r)));
+}
+
 // True in one lane of the (converged) warp.
 __device__ __forceinline__ bool elect() {
     uint32_t one;
