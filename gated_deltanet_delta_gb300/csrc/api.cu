@@ -848,7 +848,7 @@ extern "C" gdn_status attn_cache_append(const void* q, const void* k, const void
                 (Hq == 0 || (q_stride < (1LL << 31) && q_out_stride < (1LL << 31))),
             GDN_ERR_UNSUPPORTED, "%s: T and the strides must be below 2^31", fn);
     REQUIRE(max_positions <= (1LL << 52) / rotary_dim, GDN_ERR_UNSUPPORTED, "%s: max_positions too large", fn);
-    REQUIRE((T / 8 + 1) * ((Hq + 2LL * Hkv) / 4 + 1) < (1LL << 31), GDN_ERR_UNSUPPORTED, "%s: too many tokens and heads for one call", fn);
+    REQUIRE((T / 8 + 1) * ((Hq + 2LL * Hkv) / 4 + 3) < (1LL << 31), GDN_ERR_UNSUPPORTED, "%s: too many tokens and heads for one call", fn);
     const size_t kb = (static_cast<size_t>(T - 1) * k_stride + row) * 2, vb = (static_cast<size_t>(T - 1) * v_stride + row) * 2;
     const size_t qb = Hq ? (static_cast<size_t>(T - 1) * q_stride + qrow) * 2 : 0;
     const size_t ob = Hq ? (static_cast<size_t>(T - 1) * q_out_stride + qrow) * 2 : 0;
@@ -950,7 +950,8 @@ extern "C" gdn_status short_conv(const void* x, int64_t x_stride, gdn_dtype dtyp
     a.num_seqs = num_seqs;
     a.pool_size = pool_size;
     a.silu = silu != 0;
-    gdn::launch_conv(a, taps, dtype == GDN_F16, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = gdn::launch_conv(a, taps, dtype == GDN_F16, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
     return launched(fn);
 }
 

@@ -43,11 +43,18 @@ void read_d(const CacheMoveArgs& a, bool f16, bool f8, cudaStream_t stream) {
     else if (f16) read<D, true, true>(a, stream);
     else read<D, false, true>(a, stream);
 }
+template <int D, bool F16, bool F8, bool HALVES, int HEADS>
+void append_heads(const AppendArgs& a, cudaStream_t stream) {
+    constexpr int groups = cache::kThreads / (D / 8);
+    const long long grid = (a.T + groups - 1) / groups * ((a.Hq + HEADS - 1) / HEADS + 2 * ((a.H + HEADS - 1) / HEADS));
+    cache::attn_cache_append_kernel<D, F16, F8, HALVES, HEADS><<<static_cast<unsigned>(grid), cache::kThreads, 0, stream>>>(a);
+}
+// Eight heads of a token per group share more, four give more CTAs.  Measured with 32 / 8 heads of 128, 8 bits, eight and four: 23k
+// tokens 89.3 and 92.7 us, 64 tokens (calls from Python) 20.2 and 18.3 us.
 template <int D, bool F16, bool F8, bool HALVES>
 void append(const AppendArgs& a, cudaStream_t stream) {
-    constexpr int groups = cache::kThreads / (D / 8), heads = 4;
-    const long long grid = (a.T + groups - 1) / groups * ((a.Hq + 2 * a.H + heads - 1) / heads);
-    cache::attn_cache_append_kernel<D, F16, F8, HALVES, heads><<<static_cast<unsigned>(grid), cache::kThreads, 0, stream>>>(a);
+    if (a.T >= 2048) append_heads<D, F16, F8, HALVES, 8>(a, stream);
+    else append_heads<D, F16, F8, HALVES, 4>(a, stream);
 }
 template <int D, bool HALVES>
 void append_d(const AppendArgs& a, bool f16, bool f8, cudaStream_t stream) {

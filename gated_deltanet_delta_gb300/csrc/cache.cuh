@@ -201,101 +201,103 @@ __global__ void __launch_bounds__(kThreads) attn_cache_read_kernel(const __grid_
 // that the result does not depend on how a compiler contracts them; the turned row is rounded to its type before it is quantised,
 // so that an 8-bit cache holds what attn_cache_write would make of the 16-bit rows.
 //
-// A copy too: each row is read once and written once.  A group of D / 8 lanes takes HEADS heads of one token, so that the token's
-// row of the table is read once for HEADS rows; the heads' loads are in flight together.  HALVES: feature i's partner
-// is i + turned / 2, in another lane of the group: it comes by a shuffle of the packed row.  Else 2 i and 2 i + 1 are partners.
+// A copy too: each row is read once and written once.  A group of D / 8 lanes takes up to HEADS heads of one token, all queries, keys or
+// values, so that the token's row of the table, its slot and its addresses are there once for HEADS rows; the rows' loads are in
+// flight together.  HALVES: feature i's partner is i + turned / 2, in another lane of the group: it comes by a shuffle of the
+// packed row.  Else 2 i and 2 i + 1 are partners.
 template <int D, bool F16, bool F8, bool HALVES, int HEADS>
 __global__ void __launch_bounds__(kThreads) attn_cache_append_kernel(const __grid_constant__ AppendArgs a) {
     constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
     // a token's heads in consecutive CTAs: those that quantise among those that copy, and the table's rows in L2
-    const int total = a.Hq + 2 * a.H, parts = (total + HEADS - 1) / HEADS, part = blockIdx.x % parts;
+    const int qparts = (a.Hq + HEADS - 1) / HEADS, kparts = (a.H + HEADS - 1) / HEADS, parts = qparts + 2 * kparts;
+    const int part = blockIdx.x % parts, kind = part < qparts ? 0 : part < qparts + kparts ? 1 : 2;  // queries, keys, values
     const long long t = static_cast<long long>(blockIdx.x / parts) * GROUPS + group;
-    const int h0 = part * HEADS;
+    const int h0 = (part - (kind > 0 ? qparts : 0) - (kind > 1 ? kparts : 0)) * HEADS, heads = min(HEADS, (kind ? a.H : a.Hq) - h0);
     const bool here = t < a.T;
+    const uint16_t* src = (kind == 0 ? a.q + t * a.q_stride : kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride) + h0 * D + lane * 8;
     uint4 x[HEADS];
 #pragma unroll
-    for (int i = 0; i < HEADS; ++i) {
-        const int h = h0 + i;
-        const uint16_t* src = h < a.Hq          ? a.q + t * a.q_stride + static_cast<long long>(h) * D
-                              : h < a.Hq + a.H  ? a.k + t * a.k_stride + static_cast<long long>(h - a.Hq) * D
-                                                : a.v + t * a.v_stride + static_cast<long long>(h - a.Hq - a.H) * D;
-        x[i] = here && h < total ? __ldcs(reinterpret_cast<const uint4*>(src + lane * 8)) : make_uint4(0, 0, 0, 0);
-    }
+    for (int i = 0; i < HEADS; ++i) x[i] = here && i < heads ? __ldcs(reinterpret_cast<const uint4*>(src + i * D)) : make_uint4(0, 0, 0, 0);
     const long long pos = here ? a.positions[t] : -1;
     const bool known = pos >= 0 && pos < a.max_pos;
     if (here && !known && lane == 0 && part == 0) atomicOr(a.status, kStatusBadPosition);
-    // the cached row of the token's first head (-1: none); a negative slot: the token's key and value are not kept
-    long long row0 = -1;
-    if (known && h0 + HEADS > a.Hq) {
+    long long row0 = -1;  // the cached row of the first of these heads (-1: none); a negative slot: the token is not kept
+    if (known && kind) {
         const long long slot = a.slots[t];
         if (slot >= 0) {
             const long long page = (slot | a.page_size) >> 32 ? slot / a.page_size : static_cast<unsigned>(slot) / static_cast<unsigned>(a.page_size);
-            if (page < a.num_pages) row0 = page * a.H * a.page_size + (slot - page * a.page_size);
+            if (page < a.num_pages) row0 = (page * a.H + h0) * a.page_size + (slot - page * a.page_size);
             else if (lane == 0) atomicOr(a.status, kStatusBadCacheIndex);
         }
     }
-    // cos and sin of this lane's features: HALVES: of feature i mod turned / 2; else of pair i / 2
-    const int half = a.turned / 2;
-    const bool turns = lane * 8 < a.turned;
-    constexpr int NC = HALVES ? 8 : 4;
-    float c[NC], s[NC];
+    if (kind < 2) {
+        // cos and sin of this lane's features: HALVES: of feature i mod turned / 2; else of pair i / 2
+        const int half = a.turned / 2;
+        const bool turns = lane * 8 < a.turned, first = lane * 8 < half;
+        constexpr int NC = HALVES ? 8 : 4;
+        float c[NC], s[NC];
 #pragma unroll
-    for (int j = 0; j < NC; ++j) c[j] = 1.f, s[j] = 0.f;
-    if (known && turns && h0 < a.Hq + a.H) {
-        const float* tab = a.rotation + pos * a.turned + (HALVES ? (lane * 8 < half ? lane * 8 : lane * 8 - half) : lane * 4);
+        for (int j = 0; j < NC; ++j) c[j] = 1.f, s[j] = 0.f;
+        if (known && turns) {
+            const float* tab = a.rotation + pos * a.turned + (HALVES ? (first ? lane * 8 : lane * 8 - half) : lane * 4);
 #pragma unroll
-        for (int j = 0; j < NC; j += 4) {
-            const float4 u = __ldg(reinterpret_cast<const float4*>(tab + j)), w = __ldg(reinterpret_cast<const float4*>(tab + half + j));
-            c[j] = u.x, c[j + 1] = u.y, c[j + 2] = u.z, c[j + 3] = u.w;
-            s[j] = w.x, s[j + 1] = w.y, s[j + 2] = w.z, s[j + 3] = w.w;
-        }
-    }
-    const bool first = lane * 8 < half;
-    const int base = threadIdx.x & 31 & ~(LANES - 1);
-    const int partner = base + (turns ? (first ? lane + half / 8 : lane - half / 8) : lane);
-#pragma unroll
-    for (int i = 0; i < HEADS; ++i) {
-        const int h = h0 + i;
-        if (h >= total) break;  // the same for the whole CTA
-        uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        if (h < a.Hq + a.H) {
-            if constexpr (HALVES) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 p = attn::unpack2<F16>(w[j]), o = attn::unpack2<F16>(__shfl_sync(kFullMask, w[j], partner));
-                    // the first of a pair: a cos - b sin; the second: b cos + a sin
-                    const float m0 = __fmul_rn(o.x, s[2 * j]), m1 = __fmul_rn(o.y, s[2 * j + 1]);
-                    const float r0 = __fadd_rn(__fmul_rn(p.x, c[2 * j]), first ? -m0 : m0);
-                    const float r1 = __fadd_rn(__fmul_rn(p.y, c[2 * j + 1]), first ? -m1 : m1);
-                    const uint32_t r = attn::pack2<F16>(r0, r1);
-                    if (turns) w[j] = r;  // what is not turned keeps its bits
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 p = attn::unpack2<F16>(w[j]);
-                    const float r0 = __fsub_rn(__fmul_rn(p.x, c[j]), __fmul_rn(p.y, s[j]));
-                    const float r1 = __fadd_rn(__fmul_rn(p.y, c[j]), __fmul_rn(p.x, s[j]));
-                    if (turns) w[j] = attn::pack2<F16>(r0, r1);
-                }
+            for (int j = 0; j < NC; j += 4) {
+                const float4 u = __ldg(reinterpret_cast<const float4*>(tab + j)), w = __ldg(reinterpret_cast<const float4*>(tab + half + j));
+                c[j] = u.x, c[j + 1] = u.y, c[j + 2] = u.z, c[j + 3] = u.w;
+                s[j] = w.x, s[j + 1] = w.y, s[j + 2] = w.z, s[j + 3] = w.w;
             }
         }
-        if (h < a.Hq) {
-            if (known) __stcs(reinterpret_cast<uint4*>(a.q_out + t * a.q_out_stride + static_cast<long long>(h) * D + lane * 8), make_uint4(w[0], w[1], w[2], w[3]));
-            continue;
+        if (HALVES && first) {  // the first of a pair: a cos + b (-sin); the second: b cos + a sin
+#pragma unroll
+            for (int j = 0; j < NC; ++j) s[j] = -s[j];
         }
-        const bool val = h >= a.Hq + a.H;
-        const long long row = row0 + static_cast<long long>(h - a.Hq - (val ? a.H : 0)) * a.page_size;
+        const int base = threadIdx.x & 31 & ~(LANES - 1);
+        const int partner = base + (turns ? (first ? lane + half / 8 : lane - half / 8) : lane);
+#pragma unroll
+        for (int i = 0; i < HEADS; ++i) {
+            if (i >= heads) break;  // the same for the whole CTA
+            uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 p = attn::unpack2<F16>(w[j]);
+                float r0, r1;
+                if constexpr (HALVES) {
+                    const float2 o = attn::unpack2<F16>(__shfl_sync(kFullMask, w[j], partner));
+                    r0 = __fadd_rn(__fmul_rn(p.x, c[2 * j]), __fmul_rn(o.x, s[2 * j]));
+                    r1 = __fadd_rn(__fmul_rn(p.y, c[2 * j + 1]), __fmul_rn(o.y, s[2 * j + 1]));
+                } else {
+                    r0 = __fsub_rn(__fmul_rn(p.x, c[j]), __fmul_rn(p.y, s[j]));
+                    r1 = __fadd_rn(__fmul_rn(p.y, c[j]), __fmul_rn(p.x, s[j]));
+                }
+                if (turns) w[j] = attn::pack2<F16>(r0, r1);  // what is not turned keeps its bits
+            }
+            x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    if (kind == 0) {
+        uint16_t* dst = a.q_out + t * a.q_out_stride + h0 * D + lane * 8;
+#pragma unroll
+        for (int i = 0; i < HEADS; ++i)
+            if (known && i < heads) __stcs(reinterpret_cast<uint4*>(dst + i * D), x[i]);
+        return;
+    }
+    uint8_t* dst = static_cast<uint8_t*>(kind == 1 ? a.kc : a.vc) + (row0 * D + lane * 8) * (F8 ? 1 : 2);
+    const long long step = static_cast<long long>(a.page_size) * D * (F8 ? 1 : 2);
+    float* scales = (kind == 1 ? a.ks : a.vs) + row0;
+#pragma unroll
+    for (int i = 0; i < HEADS; ++i) {
+        if (i >= heads) break;
         if constexpr (F8) {
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
             float scale;
             const uint2 q = quantise8<LANES, F16>(w, scale);
-            if (row0 < 0) continue;
-            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(val ? a.vc : a.kc) + row * D + lane * 8) = q;
-            if (lane == 0) (val ? a.vs : a.ks)[row] = scale;
-        } else {
-            if (row0 < 0) continue;
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(val ? a.vc : a.kc) + row * D + lane * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (row0 >= 0) {
+                *reinterpret_cast<uint2*>(dst + i * step) = q;
+                if (lane == 0) scales[static_cast<long long>(i) * a.page_size] = scale;
+            }
+        } else if (row0 >= 0) {
+            *reinterpret_cast<uint4*>(dst + i * step) = x[i];
         }
     }
 }

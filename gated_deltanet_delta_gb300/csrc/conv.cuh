@@ -13,6 +13,7 @@
 #include "attn_mma.cuh"
 #include "common.cuh"
 #include "kernel_args.h"
+#include "tcgen05.cuh"
 #include "tile_util.cuh"
 
 namespace gdn {
@@ -21,6 +22,12 @@ namespace conv {
 constexpr int kThreads = 128;
 constexpr int kTokens = 32;
 constexpr int kStep = 8;  // tokens in registers, and as many on their way
+// the kernel for long calls
+constexpr int kTile = 128;
+constexpr int kStages = 4;
+constexpr int kRing = kStages * kStep * kThreads * 16;
+constexpr uint32_t kWaitPolls = 1u << 24;  // the limit of a wait for a copy (seconds)
+static_assert(kTile == kThreads, "a thread per token");
 
 // A token's sequence: which, where it begins and ends; n = -1 for a token of no (well-formed) sequence.
 struct Place {
@@ -130,6 +137,24 @@ __device__ __forceinline__ uint16_t* out_of(const ConvArgs& a, int c, int& width
     return a.out[i] + (c - (i > 0 ? a.width[0] : 0) - (i > 1 ? a.width[1] : 0));
 }
 
+// What is ahead of a tile: its first token's sequence's tokens (`ahead` of them), and before those the history.
+template <int TAPS, bool F16>
+__device__ __forceinline__ void ahead_of_tile(const ConvArgs& a, Past<TAPS>& p, const uint16_t* src, int c, long long slot, int ahead) {
+    if (slot >= 0 && ahead < TAPS - 1) {
+        p.load(a.hist + (slot * a.C + c) * (TAPS - 1));
+    } else {
+#pragma unroll
+        for (int j = 0; j < TAPS - 1; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p.v[j][i] = attn::pair(0.f, 0.f);
+    }
+    for (int j = slot >= 0 ? ahead : 0; j > 0; --j) {
+        f32x2 f[4];
+        widen8<F16>(*reinterpret_cast<const uint4*>(src - j * a.x_stride), f);
+        p.push(f);
+    }
+}
+
 // One token per sequence: outputs, and the history in place.
 template <int TAPS, bool F16>
 __global__ void __launch_bounds__(kThreads) short_conv_step_kernel(const __grid_constant__ ConvArgs a) {
@@ -194,23 +219,7 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(const __grid_const
     int width;
     uint16_t* out = out_of(a, c, width) + t0 * width;
     Past<TAPS> p;
-    {  // ahead of the tile: its first token's sequence's tokens, and before those the history
-        const int ahead = ahead_s[0];
-        const long long slot = slot_s[0];
-        if (slot >= 0 && ahead < TAPS - 1) {
-            p.load(a.hist + (slot * a.C + c) * (TAPS - 1));
-        } else {
-#pragma unroll
-            for (int j = 0; j < TAPS - 1; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) p.v[j][i] = attn::pair(0.f, 0.f);
-        }
-        for (int j = slot >= 0 ? ahead : 0; j > 0; --j) {
-            f32x2 f[4];
-            widen8<F16>(*reinterpret_cast<const uint4*>(src - j * a.x_stride), f);
-            p.push(f);
-        }
-    }
+    ahead_of_tile<TAPS, F16>(a, p, src, c, slot_s[0], ahead_s[0]);
     if (plain) {
 #pragma unroll 1
         for (int i0 = 0; i0 < kTokens; i0 += kStep) {
@@ -235,6 +244,97 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(const __grid_const
         if (slot >= 0) __stcs(reinterpret_cast<uint4*>(out + static_cast<long long>(i) * width), token<TAPS, F16>(w, p, f, a.silu));
         p.push(f);
     }
+}
+
+// The same for long calls: 128 tokens per CTA, whose rows come by bulk copies into a ring of kStages steps of eight tokens in shared memory.
+// With the rows in registers there is room for 12 warps with eight loads each on an SM, and 72 % of HBM's rate.  A copy that
+// does not arrive within the limit of a wait (seconds) is done without: the thread reads its rows directly.
+template <int TAPS, bool F16>
+__global__ void __launch_bounds__(kThreads) short_conv_ring_kernel(const __grid_constant__ ConvArgs a) {
+    extern __shared__ __align__(128) uint8_t ring[];  // [kStages][kStep][kThreads * 8] elements
+    __shared__ long long slot_s[kTile];
+    __shared__ int ahead_s[kTile];
+    __shared__ uint32_t odd_s[kTile / 32];  // tokens that begin a sequence, or belong to none
+    __shared__ uint64_t full[kStages];
+    constexpr uint32_t ROW = kThreads * 16, STAGE = kStep * ROW;
+    const int c0 = blockIdx.y * kThreads * 8, c = c0 + threadIdx.x * 8;
+    const long long t0 = static_cast<long long>(blockIdx.x) * kTile;
+    const int count = static_cast<int>(a.T - t0 < kTile ? a.T - t0 : kTile), steps = (count + kStep - 1) / kStep;
+    const bool on = c < a.C;
+    const uint16_t* src = a.x + t0 * a.x_stride + c;
+    const uint32_t bytes = static_cast<uint32_t>(min(kThreads * 8, a.C - c0)) * 2;
+    auto issue = [&](int k) {  // by thread 0
+        const int tokens = min(kStep, count - k * kStep), s = k % kStages;
+        tc::mbar_expect_tx(&full[s], tokens * bytes);
+        for (int i = 0; i < tokens; ++i)
+            tc::bulk_load(tc::smem_u32(ring) + s * STAGE + i * ROW, a.x + (t0 + k * kStep + i) * a.x_stride + c0, bytes, &full[s]);
+    };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) tc::mbar_init(&full[s], 1);
+        for (int k = 0; k < kStages && k < steps; ++k) issue(k);
+    }
+    {
+        const int i = threadIdx.x;
+        long long slot = -1;
+        int ahead = 0;
+        if (i < count) {
+            const Place p = place_of(a.cu, a.num_seqs, a.T, t0 + i);
+            if (p.n >= 0) {
+                slot = a.slots[p.n];
+                if (slot < 0 || slot >= a.pool_size) slot = -1;  // reported by the history's kernel
+                ahead = static_cast<int>(t0 + i - p.begin < TAPS - 1 ? t0 + i - p.begin : TAPS - 1);
+            }
+        }
+        slot_s[i] = slot;
+        ahead_s[i] = ahead;
+        const uint32_t odd = __ballot_sync(kFullMask, slot < 0 || (i > 0 && ahead == 0));
+        if (i % 32 == 0) odd_s[i / 32] = odd;
+    }
+    __syncthreads();
+    Weights<TAPS> w;
+    Past<TAPS> p;
+    int width = 0;
+    uint16_t* out = nullptr;
+    if (on) {
+        w.load(a, c);
+        out = out_of(a, c, width) + t0 * width;
+        ahead_of_tile<TAPS, F16>(a, p, src, c, slot_s[0], ahead_s[0]);
+    }
+    bool ok = true;
+#pragma unroll 1
+    for (int k = 0; k < steps; ++k) {
+        const int s = k % kStages, i0 = k * kStep;
+        if (ok) ok = tc::mbar_wait(&full[s], k / kStages & 1, kWaitPolls);
+        const uint8_t* held = ring + s * STAGE + threadIdx.x * 16;
+        auto row = [&](int i) {
+            return ok ? *reinterpret_cast<const uint4*>(held + i * ROW) : *reinterpret_cast<const uint4*>(src + (i0 + i) * a.x_stride);
+        };
+        if (on) {
+            if ((odd_s[i0 / 32] >> (i0 % 32) & 0xff) == 0) {
+#pragma unroll
+                for (int i = 0; i < kStep; ++i) {
+                    f32x2 f[4];
+                    widen8<F16>(row(i), f);
+                    __stcs(reinterpret_cast<uint4*>(out + static_cast<long long>(i0 + i) * width), token<TAPS, F16>(w, p, f, a.silu));
+                    p.push(f);
+                }
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < kStep && i0 + i < count; ++i) {
+                    const long long slot = slot_s[i0 + i];
+                    if (i0 + i > 0 && ahead_s[i0 + i] == 0 && slot >= 0) p.load(a.hist + (slot * a.C + c) * (TAPS - 1));
+                    f32x2 f[4];
+                    widen8<F16>(row(i), f);
+                    if (slot >= 0) __stcs(reinterpret_cast<uint4*>(out + static_cast<long long>(i0 + i) * width), token<TAPS, F16>(w, p, f, a.silu));
+                    p.push(f);
+                }
+            }
+        }
+        __syncthreads();  // the step's place has been read
+        if (threadIdx.x == 0 && ok && k + kStages < steps) issue(k + kStages);
+    }
+    if (threadIdx.x == 0 && !ok)  // gave up: leave what copies are in flight (microseconds) a millisecond
+        for (int i = 0; i < 100; ++i) __nanosleep(10000);
 }
 
 // The history behind each sequence's last token, and the report of malformed bounds and slots.

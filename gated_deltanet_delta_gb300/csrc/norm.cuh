@@ -131,7 +131,7 @@ __device__ __forceinline__ void row(const NormArgs& a, long long t, bool here, u
 }
 
 template <bool F16, bool F8, int R>
-__global__ void __launch_bounds__(R == 1 ? 256 : kMaxThreads, R == 1 ? 6 : R == 2 ? 3 : 1) add_rms_norm_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(R == 1 ? 256 : kMaxThreads, R == 1 ? 6 : R == 2 ? 4 : 1) add_rms_norm_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float buf[2][8][32];
     const long long t = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     const bool here = t < a.T;

@@ -65,7 +65,8 @@ def check(gdn, s, neighbours, q_out=None, kept=None):
 @pytest.mark.parametrize("neighbours", [False, True])
 @pytest.mark.parametrize("dtype,f8", [(torch.bfloat16, False), (torch.bfloat16, True), (torch.float16, False), (torch.float16, True)])
 @pytest.mark.parametrize("T,Hq,H,D,turned,page", [(1, 1, 1, 64, 64, 16), (7, 6, 2, 128, 128, 5), (33, 4, 4, 64, 32, 16), (150, 5, 1, 256, 64, 48),
-                                                  (9, 3, 3, 256, 256, 1), (65, 2, 1, 128, 16, 7), (40, 1, 2, 128, 112, 64)])
+                                                  (9, 3, 3, 256, 256, 1), (65, 2, 1, 128, 16, 7), (40, 1, 2, 128, 112, 64), (2051, 9, 3, 64, 64, 16), (2048, 10, 1, 128, 96, 48),
+                                                  (2500, 1, 9, 256, 128, 64)])
 def test_rotates_and_appends(gdn, T, Hq, H, D, turned, page, dtype, f8, neighbours):
     s = make(T, T, Hq, H, D, turned, page, dtype, f8)
     s["slots"][T // 2] = -1  # this token is not kept; its query is rotated

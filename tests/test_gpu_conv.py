@@ -96,6 +96,26 @@ def test_a_prompt_in_pieces(gdn):
     assert torch.equal(torch.cat(parts[0] + parts[1]).view(torch.int16), y.view(torch.int16)) and torch.equal(now, hist)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("taps,splits", [(4, [16]), (2, [8]), (3, [1032, 8])])
+def test_long_calls(gdn, taps, splits, dtype):
+    """Calls of so many tokens that another kernel takes them, against the same sequences in calls of a few, bit for bit."""
+    lens = [1, 2, 3, 500, 0, 128, 129, 127, 1, 1, 1, 9000, 7, 64, 8, 8, 8, 8, 8000, 31, 33, 6000, 5, 0, 12001, 3000, 1]
+    s = make(taps, lens, sum(splits), taps, dtype)
+    y, hist, status = run(gdn, s, splits)
+    assert status == 0 and bool((y[sum(lens):] == 9.0).all())
+    at, now = 0, s["hist"]
+    for n, k in enumerate(lens):
+        for a in range(0, k, 4000):
+            m = min(4000, k - a)
+            part = dict(s, wide=s["wide"][at + a:at + a + m], lens=[m], slots=s["slots"][n:n + 1], hist=now, cu=torch.tensor([0, m]))
+            part["x"] = part["wide"][:, 8:8 + sum(splits)]
+            got, now, status = run(gdn, part, splits)
+            assert status == 0 and torch.equal(got.view(torch.int16), y[at + a:at + a + m].view(torch.int16)), (n, a)
+        at += k
+    assert torch.equal(now, hist)
+
+
 def test_large_and_small_activations(gdn):
     s = make(2, [40], 16, 2, torch.bfloat16, pad=0)
     s["w"][:, 0], s["w"][:, 1], s["bias"][:] = 0.0, 1.0, 0.0
