@@ -308,9 +308,9 @@ struct SsmArgs {
     uint32_t polls;         // of a barrier, before a wait gives up
 };
 
-// x, B and C as rows of a token each.
+// x, B, C, z and out as rows of a token each.
 struct SsmMaps {
-    CUtensorMap x, B, C;
+    CUtensorMap x, B, C, z, y;
 };
 
 struct NormArgs {

@@ -12,13 +12,13 @@ namespace {
 
 constexpr int kSub = 8;  // chunks per piece of the launch ahead; segments are multiples of it
 
-// Tokens as rows of `width` elements: boxes of 64 columns and 128 rows, 128-byte swizzle, zero fill outside.
-bool encode_tokens(CUtensorMap* map, const void* base, long long T, long long width, long long stride) {
+// Tokens as rows of `width` elements: boxes of 64 columns and `rows` rows, 128-byte swizzle, zero fill outside.
+bool encode_tokens(CUtensorMap* map, const void* base, long long T, long long width, long long stride, unsigned rows = 128) {
     const auto fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(T)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
-    const cuuint32_t box[2] = {64, 128}, step[2] = {1, 1};
+    const cuuint32_t box[2] = {64, rows}, step[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -50,7 +50,8 @@ cudaError_t chunks(SsmArgs a, long long max_len, void* workspace, cudaStream_t s
     SsmMaps maps;
     const long long inner = static_cast<long long>(a.H) * P, gs = static_cast<long long>(a.G) * S;
     if (!encode_tokens(&maps.x, a.x, a.T, inner, a.x_stride) || !encode_tokens(&maps.B, a.B, a.T, gs, a.b_stride) ||
-        !encode_tokens(&maps.C, a.C, a.T, gs, a.c_stride))
+        !encode_tokens(&maps.C, a.C, a.T, gs, a.c_stride) || !encode_tokens(&maps.y, a.out, a.T, inner, inner) ||
+        !encode_tokens(&maps.z, a.z ? a.z : a.x, a.T, inner, a.z ? a.z_stride : a.x_stride, 32))
         return cudaErrorInvalidValue;
     // Segments.  In chunk times of one SM: `share` is the work over the SMs, a chain takes as long as it is, units that are
     // more than the SMs end unevenly by about half a unit, and the launch ahead costs two fifths of what it covers and a start.

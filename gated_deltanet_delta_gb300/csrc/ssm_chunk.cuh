@@ -57,14 +57,16 @@ struct ChunkCfg {
     // per chunk (two in turn) and head: the decays' sums within blocks of 32 tokens, the columns' factors, dt (in the
     // exponent it would be lost beside a large sum), the blocks' sums
     static constexpr int VEC = 3 * kChunk + 16;
-    static constexpr uint32_t USED = OFF_V + 2 * 2 * VEC * 4;
+    // the gate's rows, of the last three blocks of 32: there is no room for the first
+    static constexpr uint32_t OFF_Z = (OFF_V + 2 * 2 * VEC * 4 + 1023) / 1024 * 1024, ZBOX = 4096;
+    static constexpr uint32_t USED = OFF_Z + 6 * ZBOX;
     static constexpr uint32_t SMEM = USED + 1024;
     static constexpr uint32_t TM_S = 0, TM_G = 128, TM_M = 256, TM_Y = 384;
 };
 
 // Barriers, two of each for the chunks in turn.
 enum : int {
-    CK_X = 0, CK_BC, CK_XE, CK_G, CK_CS, CK_UPH, CK_UPD, CK_MX0, CK_MX1, CK_V, CK_S, CK_XL, CK_Y0, CK_Y1, CK_YF, CK_DRAIN, CK_N
+    CK_X = 0, CK_BC, CK_XE, CK_G, CK_CS, CK_UPH, CK_UPD, CK_MX0, CK_MX1, CK_V, CK_S, CK_XH, CK_XL, CK_Y0, CK_Y1, CK_YF, CK_O, CK_Z, CK_ZE, CK_DRAIN, CK_N
 };
 
 struct Unit {
@@ -77,14 +79,8 @@ struct Unit {
     int found;
 };
 
-// 32 bytes at an address that is a multiple of 32.
-__device__ __forceinline__ void ld32bytes(const void* p, uint4& x, uint4& y) {
-    asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w), "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
-                 : "l"(p));
-}
-__device__ __forceinline__ void st32bytes(void* p, const uint4& x, const uint4& y) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
+__device__ __forceinline__ void tma_store_2d(const void* map, int x, int y, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y), "r"(src) : "memory");
 }
 // 8 consecutive 32-bit TMEM columns of this thread's lane.
 __device__ __forceinline__ void st8(uint32_t taddr, const uint32_t (&r)[8]) {
@@ -167,8 +163,9 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
         for (int i = 0; i < 2 * CK_N; ++i) {
             const int id = i / 2;
             // B and C arrive one after the other; at the others but for the copies' and products' arrive warps
-            const int count = id == CK_BC ? (STATE ? 1 : 2) : id == CK_YF || (!STATE && id == CK_XE) || (P == 128 && id == CK_Y0) ? 16
-                              : id == CK_XE || id == CK_V || id == CK_S || id == CK_XL || id == CK_Y0 || id == CK_Y1 ? 8 : 1;
+            const int count = id == CK_BC ? (STATE ? 1 : 2) : id == CK_YF || id == CK_O || id == CK_ZE || (STATE && id == CK_XE) || (P == 128 && id == CK_Y0) ? 16
+                              : id == CK_V ? (P == 64 ? 4 : 2)
+                              : id == CK_XH || id == CK_S || id == CK_XL || id == CK_Y0 || id == CK_Y1 ? 8 : 1;
             tc::mbar_init(&bars[i], count);
         }
         most_polls = a.polls;
@@ -239,6 +236,14 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                 tc::mbar_expect_tx(bar, K::CB);
 #pragma unroll
                 for (int i = 0; i < S / 64; ++i) attn::tma_load_2d(sb + K::OFF_B + c % NCB * K::CB + i * 16384, &maps.B, g * S + 64 * i, row, bar);
+                if (!STATE && a.z) {
+                    if (c >= 1) ok = wait(CK_ZE, c - 1);
+                    if (!ok) break;
+                    bar = &bars[2 * CK_Z + (c & 1)];
+                    tc::mbar_expect_tx(bar, halves * 3 * K::ZBOX);
+                    for (int i = 0; i < halves; ++i)
+                        for (int j = 0; j < 3; ++j) attn::tma_load_2d(sb + K::OFF_Z + (3 * i + j) * K::ZBOX, &maps.z, h0 * P + 64 * i, row + 32 + 32 * j, bar);
+                }
             }
             if (!ok)  // gave up: leave what copies are in flight (microseconds) a millisecond
                 for (int i = 0; i < 100; ++i) __nanosleep(10000);
@@ -302,6 +307,23 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
             tc::commit(&bars[2 * CK_DRAIN]);
             tc::mbar_wait(&bars[2 * CK_DRAIN], 0, kPolls);
         }
+        if (!STATE && warp == 19 && attn::elect()) {
+            // -------------------------------------------------------- stores of whole chunks, from their x's place
+            bool ok = true;
+            for (int c = 0; c < u.chunks && ok; ++c) {
+                ok = wait(CK_O, c);
+                if (!ok) break;
+                if (u.len - c * kChunk >= kChunk) {
+                    const int halves = heads * P / 64;
+                    for (int i = 0; i < halves; ++i)
+                        tma_store_2d(&maps.y, h0 * P + 64 * i, static_cast<int>(u.begin) + c * kChunk, sb + K::OFF_X + (c & 1) * K::X + i * 16384);
+                    tc::bulk_commit();
+                    tc::bulk_wait_read();
+                }
+                tc::mbar_arrive(&bars[2 * CK_XE + (c & 1)]);
+            }
+            tc::bulk_wait_all();
+        }
         if (warp == 18 && attn::elect()) {
             // -------------------------------------------------------- the state
             constexpr uint32_t ID_UPD = tc::idesc_bf16(128, S, 1, 1, 0);
@@ -309,7 +331,7 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
             bool ok = true;
             for (int c = 0; c < u.chunks && ok; ++c) {
                 const uint64_t off = c % NCB * (K::CB >> 4);
-                ok = one_wait(CK_BC, c) && one_wait(CK_S, c);
+                ok = one_wait(CK_BC, c) && one_wait(CK_XH, c) && one_wait(CK_S, c);
                 if (!ok) break;
 #pragma unroll 1
                 for (uint32_t q = 0; q < 2; ++q)
@@ -416,23 +438,30 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
         };
         const long long col = static_cast<long long>(h0) * P + side * 64;  // the first feature of this half of the tile
         const uint32_t line = static_cast<uint32_t>(side * 16384 + t * 128);  // this row of that half
-        // A thread's 32 features are two sectors of global memory, taken whole where their address allows it.
-        const bool z32 = reinterpret_cast<uintptr_t>(a.z) % 32 == 0 && a.z_stride % 16 == 0, y32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
+        // A whole chunk goes out by TMA, from the place of its x, and the gate comes by TMA but for the first block of rows: a thread's own
+        // 64 bytes of a row of global memory, 32 lines per instruction, held up all that goes through the load and store unit.
         auto output = [&](int c) -> bool {
-            const bool live = t < u.len - c * kChunk && valid;
+            const bool live = t < u.len - c * kChunk && valid, whole = u.len - c * kChunk >= kChunk;
             const long long tok = u.begin + c * kChunk + t;
             uint4 z[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) z[i] = make_uint4(0, 0, 0, 0);
-            if (a.z && live) {
-                const uint16_t* src = a.z + tok * a.z_stride + col + (wg >> 1) * 32;
-                if (z32) ld32bytes(src, z[0], z[1]), ld32bytes(src + 16, z[2], z[3]);
-                else
+            if (a.z && w == 0 && live) {
+                const uint4* src = reinterpret_cast<const uint4*>(a.z + tok * a.z_stride + col) + (wg >> 1) * 4;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) z[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+                for (int i = 0; i < 4; ++i) z[i] = __ldg(src + i);
             }
             __syncwarp();
             if (!warp_wait(P == 64 ? CK_MX0 + side : CK_MX0, c) || !warp_wait(CK_X, c)) return false;
+            if (a.z) {
+                if (!warp_wait(CK_Z, c)) return false;
+                if (w > 0) {
+                    const uint32_t zt = sb + K::OFF_Z + (3 * side + w - 1) * K::ZBOX + lane * 128;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) z[i] = attn::lds128(zt + ((((wg >> 1) * 4 + i) ^ (lane & 7)) << 4));
+                }
+                warp_arrive(CK_ZE, c);
+            }
             const uint32_t at = sb + K::OFF_X + (c & 1) * K::X + line;
             const int t7 = anew(t) & 7;
             const float D = head_s[hh][2];
@@ -462,15 +491,14 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                     z[2 * i + q] = make_uint4(r[0], r[1], r[2], r[3]);
                 }
             }
-            warp_arrive(CK_XE, c);
-            if (live) {
-                uint16_t* dst = a.out + tok * a.H * P + col + (wg >> 1) * 32;
-                if (y32) st32bytes(dst, z[0], z[1]), st32bytes(dst + 16, z[2], z[3]);
-                else
+            uint4* dst = reinterpret_cast<uint4*>(a.out + tok * a.H * P + col) + (wg >> 1) * 4;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(dst)[i] = z[i];
+            for (int i = 0; i < 4; ++i) {
+                if (whole) attn::sts128(at + ((((wg >> 1) * 4 + i) ^ t7) << 4), z[i]);
+                else if (live) dst[i] = z[i];
             }
-            __syncwarp();
+            tc::fence_proxy_async();
+            warp_arrive(CK_O, c);
             return true;
         };
 
@@ -479,10 +507,6 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
         const bool there = ph < heads;
         auto srow = [&] { return (static_cast<long long>(h0 + (there ? ph : 0)) * P + (P == 64 ? t & 63 : t)) * S + side * (S / 2); };
         auto state = [&] { return static_cast<long long>(a.H) * P * S; };
-        auto raw_at = [&](int c) {
-            const int i = c * kChunk + t;
-            return valid && i < u.len ? a.dt[(u.begin + i) * a.dt_stride + h] : static_cast<uint16_t>(0);
-        };
         float gone = 0.f;  // the decay of the chunks so far
         if (isb) {  // the unit's first state
             const bool from_pool = STATE ? u.k == 0 : u.parts == 1;
@@ -517,63 +541,75 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
             }
             tc::wait_st();
         }
-        uint16_t raw = isb ? raw_at(0) : static_cast<uint16_t>(0);
-        float dt = 0.f, behind = 0.f, weight = 0.f;
+        // B, the warps of the first two blocks of M, which have the least of it: dt and the decays' sums of chunk c, of two blocks each
+        const bool sums = isb && w < 2 && (P == 64 || side == 0);
+        auto raw_at = [&](int c, int b) {
+            const int i = c * kChunk + (2 * w + b) * 32 + lane;
+            return sums && valid && i < u.len ? a.dt[(u.begin + i) * a.dt_stride + h] : static_cast<uint16_t>(0);
+        };
+        uint16_t raw[2] = {raw_at(0, 0), raw_at(0, 1)};
         auto decays = [&](int c) {
-            dt = valid && t < u.len - c * kChunk ? softplus(bf16_to_f32(raw) + head_s[hh][1]) : 0.f;
-            raw = raw_at(c + 1);
-            const float step = head_s[hh][0] * dt;
-            float upto = step;
-            behind = __shfl_down_sync(kFullMask, step, 1);
-            if (lane == 31) behind = 0.f;
-#pragma unroll
-            for (int o = 1; o < 32; o *= 2) {
-                const float x = __shfl_up_sync(kFullMask, upto, o), y = __shfl_down_sync(kFullMask, behind, o);
-                if (lane >= o) upto += x;
-                if (lane + o < 32) behind += y;
-            }
             float* V = vec(c, hh);
-            if (P == 64 || side == 0) {
-                V[t] = upto;
-                V[kChunk + t] = dt * ex2(behind);
-                V[2 * kChunk + t] = dt;
-                if (lane == 31) V[3 * kChunk + w] = upto;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int i = (2 * w + b) * 32 + lane;
+                const float dt = valid && i < u.len - c * kChunk ? softplus(bf16_to_f32(raw[b]) + head_s[hh][1]) : 0.f;
+                raw[b] = raw_at(c + 1, b);
+                const float step = head_s[hh][0] * dt;
+                float upto = step, behind = __shfl_down_sync(kFullMask, step, 1);
+                if (lane == 31) behind = 0.f;
+#pragma unroll
+                for (int o = 1; o < 32; o *= 2) {
+                    const float x = __shfl_up_sync(kFullMask, upto, o), y = __shfl_down_sync(kFullMask, behind, o);
+                    if (lane >= o) upto += x;
+                    if (lane + o < 32) behind += y;
+                }
+                V[i] = upto;
+                V[kChunk + i] = dt * ex2(behind);
+                V[2 * kChunk + i] = dt;
+                if (lane == 31) V[3 * kChunk + 2 * w + b] = upto;
             }
             warp_arrive(CK_V, c);
         };
-        // The row times its weight to X': in bf16 arithmetic, with the weight as w0 + w1.  h = x w0, rounded; x w0 - h is
-        // exact (16 bits less the first 8); with x w1 added it is the low part.
-        auto weigh = [&](int c, bool high, uint32_t to) {
-            const __nv_bfloat16 wh = __float2bfloat16(weight);
-            const int t7 = anew(t) & 7;
-            const __nv_bfloat162 w0 = __bfloat162bfloat162(wh), w1 = __bfloat162bfloat162(__float2bfloat16(weight - __bfloat162float(wh)));
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const uint32_t at = line + ((q ^ t7) << 4);
-                const uint4 p = attn::lds128(sb + K::OFF_X + (c & 1) * K::X + at);
-                uint32_t v[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const __nv_bfloat162 x2 = *reinterpret_cast<const __nv_bfloat162*>(&v[k]);
-                    __nv_bfloat162 r = __hmul2_rn(x2, w0);
-                    if (!high) r = __hfma2(x2, w1, __hfma2(x2, w0, __hneg2(r)));
-                    v[k] = *reinterpret_cast<const uint32_t*>(&r);
-                }
-                attn::sts128(sb + to + at, make_uint4(v[0], v[1], v[2], v[3]));
-            }
+        // this token's weight in the state behind the chunk
+        auto weight_of = [&](int c) {
+            const float* V = vec(c, hh);
+            float behind = 0.f;
+            for (int j = w + 1; j < 4; ++j) behind += V[3 * kChunk + j];
+            return V[kChunk + t] * ex2(behind);
         };
-        // X', high parts, and the state that chunk c begins with: a copy in bf16 for Y, and the decayed state
-        auto begin = [&](int c) -> bool {
+        // The row times its weight to X', as bf16 high parts or as what they leave.  In fp32: packed bf16 products took twice the time.
+        auto weigh = [&](int c, float weight, bool high, uint32_t to) {
+            const attn::f32x2 ww = attn::pair(weight, weight), minus = attn::pair(-1.f, -1.f);
+            const int t7 = anew(t) & 7;
+#pragma unroll
+            for (int q0 = 0; q0 < 8; q0 += 4) {
+                uint4 x[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) x[q] = attn::lds128(sb + K::OFF_X + (c & 1) * K::X + line + (((q0 + q) ^ t7) << 4));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t v[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const attn::f32x2 p = attn::mul2(attn::widen2(v[k]), ww);
+                        float f[2];
+                        attn::unpair(p, f);
+                        v[k] = pack_bf16x2(f[0], f[1]);
+                        if (!high) {
+                            attn::unpair(attn::fma2(attn::widen2(v[k]), minus, p), f);
+                            v[k] = pack_bf16x2(f[0], f[1]);
+                        }
+                    }
+                    attn::sts128(sb + to + line + (((q0 + q) ^ t7) << 4), make_uint4(v[0], v[1], v[2], v[3]));
+                }
+            }
+            tc::fence_proxy_async();
+        };
+        // A: X' of chunk c, high parts
+        auto high_parts = [&](int c) -> bool {
             const int rows = min(kChunk, u.len - c * kChunk);
             if (!warp_wait(CK_X, c) || !warp_wait(CK_V, c)) return false;
-            {
-                const float* W = vec(c, hh) + 3 * kChunk;
-                for (int j = w + 1; j < 4; ++j) behind += W[j];
-                weight = dt * ex2(behind);
-            }
-            const float* W = vec(c, ph) + 3 * kChunk;  // of this feature's head
-            const float all = (W[0] + W[1]) + (W[2] + W[3]), keep = ex2(all);
-            gone += all;
             if (rows < kChunk || !valid) {  // what a weight of zero meets must be finite: rows behind the sequence may hold anything
                 if (!warp_wait(CK_BC, c)) return false;
                 const uint4 none = make_uint4(0, 0, 0, 0);
@@ -584,7 +620,19 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                 }
             }
             if (c > 0 && !warp_wait(CK_UPH, c - 1)) return false;
-            weigh(c, true, K::OFF_XH);
+            weigh(c, weight_of(c), true, K::OFF_XH);
+            warp_arrive(CK_XH, c);
+            if (STATE) warp_arrive(CK_XE, c);
+            return true;
+        };
+        float weight = 0.f;
+        // B: the state that chunk c begins with: a copy in bf16 for Y, and the decayed state
+        auto begin = [&](int c) -> bool {
+            if (!warp_wait(CK_V, c)) return false;
+            weight = weight_of(c);
+            const float* W = vec(c, ph) + 3 * kChunk;  // of this feature's head
+            const float all = (W[0] + W[1]) + (W[2] + W[3]), keep = ex2(all);
+            gone += all;
             if (c > 0 && !warp_wait(CK_UPD, c - 1)) return false;
             const attn::f32x2 kk = attn::pair(keep, keep);
             const int ts = anew(t);
@@ -618,8 +666,9 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                 if (P == 64 || wg == 0) attn::tm_st16(tM + 16 * j, zero);
             }
         }
+        if (sums) decays(0);
 #pragma unroll 1
-        for (int c = -1; c < u.chunks && (isb || !STATE); ++c) {
+        for (int c = -1; c < u.chunks; ++c) {
             if (c >= 0) {
                 if constexpr (!STATE) {
                     ok = (isb || warp_wait(CK_V, c)) && weights(c);
@@ -627,17 +676,18 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                     ok = warp_wait(CK_CS, c);
                     if (!ok) break;
                 }
+                if (sums && c + 1 < u.chunks) decays(c + 1);
                 if (isb) {  // the state's copy has been read: its place is X's low parts' now
-                    weigh(c, false, K::OFF_SX);
-                    tc::fence_proxy_async();
+                    ok = warp_wait(CK_X, c) && warp_wait(CK_XH, c);
+                    if (!ok) break;
+                    weigh(c, weight, false, K::OFF_SX);
                     warp_arrive(CK_XL, c);
                     if (STATE) warp_arrive(CK_XE, c);
                 }
                 if constexpr (!STATE) scale_y(c);
             }
-            if (isb && c + 1 < u.chunks) {
-                decays(c + 1);
-                ok = begin(c + 1);
+            if (c + 1 < u.chunks) {
+                ok = isb ? begin(c + 1) : high_parts(c + 1);
             }
             if (!STATE && c >= 0) ok = ok && output(c);
             if (!ok) break;
