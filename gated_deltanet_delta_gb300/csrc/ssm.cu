@@ -50,7 +50,7 @@ cudaError_t chunks(SsmArgs a, long long max_len, void* workspace, cudaStream_t s
     SsmMaps maps;
     const long long inner = static_cast<long long>(a.H) * P, gs = static_cast<long long>(a.G) * S;
     if (!encode_tokens(&maps.x, a.x, a.T, inner, a.x_stride) || !encode_tokens(&maps.B, a.B, a.T, gs, a.b_stride) ||
-        !encode_tokens(&maps.C, a.C, a.T, gs, a.c_stride) || !encode_tokens(&maps.y, a.out, a.T, inner, inner) ||
+        !encode_tokens(&maps.C, a.C, a.T, gs, a.c_stride) || !encode_tokens(&maps.y, a.out, a.T, inner, inner, 32) ||
         !encode_tokens(&maps.z, a.z ? a.z : a.x, a.T, inner, a.z ? a.z_stride : a.x_stride, 32))
         return cudaErrorInvalidValue;
     // Segments.  In chunk times of one SM: `share` is the work over the SMs, a chain takes as long as it is, units that are

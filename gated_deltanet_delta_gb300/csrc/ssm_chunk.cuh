@@ -57,7 +57,7 @@ struct ChunkCfg {
     // per chunk (two in turn) and head: the decays' sums within blocks of 32 tokens, the columns' factors, dt (in the
     // exponent it would be lost beside a large sum), the blocks' sums
     static constexpr int VEC = 3 * kChunk + 16;
-    // the gate's rows, of the last three blocks of 32: there is no room for the first
+    // the gate's rows, and then the output's, of the last three blocks of 32: there is no room for the first
     static constexpr uint32_t OFF_Z = (OFF_V + 2 * 2 * VEC * 4 + 1023) / 1024 * 1024, ZBOX = 4096;
     static constexpr uint32_t USED = OFF_Z + 6 * ZBOX;
     static constexpr uint32_t SMEM = USED + 1024;
@@ -163,8 +163,8 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
         for (int i = 0; i < 2 * CK_N; ++i) {
             const int id = i / 2;
             // B and C arrive one after the other; at the others but for the copies' and products' arrive warps
-            const int count = id == CK_BC ? (STATE ? 1 : 2) : id == CK_YF || id == CK_O || id == CK_ZE || (STATE && id == CK_XE) || (P == 128 && id == CK_Y0) ? 16
-                              : id == CK_V ? (P == 64 ? 4 : 2)
+            const int count = id == CK_BC ? (STATE ? 1 : 2) : id == CK_YF || id == CK_O || id == CK_XE || (P == 128 && id == CK_Y0) ? 16
+                              : id == CK_V ? (P == 64 ? 8 : 4)
                               : id == CK_XH || id == CK_S || id == CK_XL || id == CK_Y0 || id == CK_Y1 ? 8 : 1;
             tc::mbar_init(&bars[i], count);
         }
@@ -236,14 +236,6 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                 tc::mbar_expect_tx(bar, K::CB);
 #pragma unroll
                 for (int i = 0; i < S / 64; ++i) attn::tma_load_2d(sb + K::OFF_B + c % NCB * K::CB + i * 16384, &maps.B, g * S + 64 * i, row, bar);
-                if (!STATE && a.z) {
-                    if (c >= 1) ok = wait(CK_ZE, c - 1);
-                    if (!ok) break;
-                    bar = &bars[2 * CK_Z + (c & 1)];
-                    tc::mbar_expect_tx(bar, halves * 3 * K::ZBOX);
-                    for (int i = 0; i < halves; ++i)
-                        for (int j = 0; j < 3; ++j) attn::tma_load_2d(sb + K::OFF_Z + (3 * i + j) * K::ZBOX, &maps.z, h0 * P + 64 * i, row + 32 + 32 * j, bar);
-                }
             }
             if (!ok)  // gave up: leave what copies are in flight (microseconds) a millisecond
                 for (int i = 0; i < 100; ++i) __nanosleep(10000);
@@ -308,21 +300,33 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
             tc::mbar_wait(&bars[2 * CK_DRAIN], 0, kPolls);
         }
         if (!STATE && warp == 19 && attn::elect()) {
-            // -------------------------------------------------------- stores of whole chunks, from their x's place
+            // -------------------------------------------------------- the gate's rows, and the stores of whole chunks, in one place
+            const int halves = heads * P / 64;
+            auto gate = [&](int c) {
+                uint64_t* bar = &bars[2 * CK_Z + (c & 1)];
+                tc::mbar_expect_tx(bar, halves * 3 * K::ZBOX);
+                for (int i = 0; i < halves; ++i)
+                    for (int j = 0; j < 3; ++j)
+                        attn::tma_load_2d(sb + K::OFF_Z + (3 * i + j) * K::ZBOX, &maps.z, h0 * P + 64 * i, static_cast<int>(u.begin) + c * kChunk + 32 + 32 * j, bar);
+            };
             bool ok = true;
+            if (a.z) gate(0);
             for (int c = 0; c < u.chunks && ok; ++c) {
                 ok = wait(CK_O, c);
                 if (!ok) break;
                 if (u.len - c * kChunk >= kChunk) {
-                    const int halves = heads * P / 64;
                     for (int i = 0; i < halves; ++i)
-                        tma_store_2d(&maps.y, h0 * P + 64 * i, static_cast<int>(u.begin) + c * kChunk, sb + K::OFF_X + (c & 1) * K::X + i * 16384);
+                        for (int j = 0; j < 3; ++j)
+                            tma_store_2d(&maps.y, h0 * P + 64 * i, static_cast<int>(u.begin) + c * kChunk + 32 + 32 * j, sb + K::OFF_Z + (3 * i + j) * K::ZBOX);
                     tc::bulk_commit();
                     tc::bulk_wait_read();
                 }
-                tc::mbar_arrive(&bars[2 * CK_XE + (c & 1)]);
+                if (!a.z) tc::mbar_arrive(&bars[2 * CK_ZE + (c & 1)]);
+                else if (c + 1 < u.chunks) gate(c + 1);
             }
             tc::bulk_wait_all();
+            if (!ok && a.z)
+                for (int i = 0; i < 100; ++i) __nanosleep(10000);
         }
         if (warp == 18 && attn::elect()) {
             // -------------------------------------------------------- the state
@@ -438,11 +442,12 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
         };
         const long long col = static_cast<long long>(h0) * P + side * 64;  // the first feature of this half of the tile
         const uint32_t line = static_cast<uint32_t>(side * 16384 + t * 128);  // this row of that half
-        // A whole chunk goes out by TMA, from the place of its x, and the gate comes by TMA but for the first block of rows: a thread's own
-        // 64 bytes of a row of global memory, 32 lines per instruction, held up all that goes through the load and store unit.
+        // The gate comes by TMA and a whole chunk goes out by TMA, from the same place, but for the first block of rows: a thread's own
+        // 64 bytes of a row of global memory, 32 lines per instruction, hold up all that goes through the load and store unit.
         auto output = [&](int c) -> bool {
-            const bool live = t < u.len - c * kChunk && valid, whole = u.len - c * kChunk >= kChunk;
+            const bool live = t < u.len - c * kChunk && valid, staged = w > 0 && u.len - c * kChunk >= kChunk;
             const long long tok = u.begin + c * kChunk + t;
+            const uint32_t zt = sb + K::OFF_Z + (3 * side + w - 1) * K::ZBOX + lane * 128;
             uint4 z[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) z[i] = make_uint4(0, 0, 0, 0);
@@ -456,11 +461,11 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
             if (a.z) {
                 if (!warp_wait(CK_Z, c)) return false;
                 if (w > 0) {
-                    const uint32_t zt = sb + K::OFF_Z + (3 * side + w - 1) * K::ZBOX + lane * 128;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) z[i] = attn::lds128(zt + ((((wg >> 1) * 4 + i) ^ (lane & 7)) << 4));
                 }
-                warp_arrive(CK_ZE, c);
+            } else if (c > 0 && !warp_wait(CK_ZE, c - 1)) {
+                return false;
             }
             const uint32_t at = sb + K::OFF_X + (c & 1) * K::X + line;
             const int t7 = anew(t) & 7;
@@ -491,10 +496,11 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                     z[2 * i + q] = make_uint4(r[0], r[1], r[2], r[3]);
                 }
             }
+            warp_arrive(CK_XE, c);
             uint4* dst = reinterpret_cast<uint4*>(a.out + tok * a.H * P + col) + (wg >> 1) * 4;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (whole) attn::sts128(at + ((((wg >> 1) * 4 + i) ^ t7) << 4), z[i]);
+                if (staged) attn::sts128(zt + ((((wg >> 1) * 4 + i) ^ (lane & 7)) << 4), z[i]);
                 else if (live) dst[i] = z[i];
             }
             tc::fence_proxy_async();
@@ -541,34 +547,32 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
             }
             tc::wait_st();
         }
-        // B, the warps of the first two blocks of M, which have the least of it: dt and the decays' sums of chunk c, of two blocks each
-        const bool sums = isb && w < 2 && (P == 64 || side == 0);
-        auto raw_at = [&](int c, int b) {
-            const int i = c * kChunk + (2 * w + b) * 32 + lane;
+        // dt and the decays' sums of chunk c, a block of 32 tokens each by the warps of M's first two blocks of rows, which have the least of it
+        const bool sums = w < 2 && (P == 64 || side == 0);
+        const int block = (isb ? 2 : 0) + w;
+        auto raw_at = [&](int c) {
+            const int i = c * kChunk + block * 32 + lane;
             return sums && valid && i < u.len ? a.dt[(u.begin + i) * a.dt_stride + h] : static_cast<uint16_t>(0);
         };
-        uint16_t raw[2] = {raw_at(0, 0), raw_at(0, 1)};
+        uint16_t raw = raw_at(0);
         auto decays = [&](int c) {
             float* V = vec(c, hh);
+            const int i = block * 32 + lane;
+            const float dt = valid && i < u.len - c * kChunk ? softplus(bf16_to_f32(raw) + head_s[hh][1]) : 0.f;
+            raw = raw_at(c + 1);
+            const float step = head_s[hh][0] * dt;
+            float upto = step, behind = __shfl_down_sync(kFullMask, step, 1);
+            if (lane == 31) behind = 0.f;
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int i = (2 * w + b) * 32 + lane;
-                const float dt = valid && i < u.len - c * kChunk ? softplus(bf16_to_f32(raw[b]) + head_s[hh][1]) : 0.f;
-                raw[b] = raw_at(c + 1, b);
-                const float step = head_s[hh][0] * dt;
-                float upto = step, behind = __shfl_down_sync(kFullMask, step, 1);
-                if (lane == 31) behind = 0.f;
-#pragma unroll
-                for (int o = 1; o < 32; o *= 2) {
-                    const float x = __shfl_up_sync(kFullMask, upto, o), y = __shfl_down_sync(kFullMask, behind, o);
-                    if (lane >= o) upto += x;
-                    if (lane + o < 32) behind += y;
-                }
-                V[i] = upto;
-                V[kChunk + i] = dt * ex2(behind);
-                V[2 * kChunk + i] = dt;
-                if (lane == 31) V[3 * kChunk + 2 * w + b] = upto;
+            for (int o = 1; o < 32; o *= 2) {
+                const float x = __shfl_up_sync(kFullMask, upto, o), y = __shfl_down_sync(kFullMask, behind, o);
+                if (lane >= o) upto += x;
+                if (lane + o < 32) behind += y;
             }
+            V[i] = upto;
+            V[kChunk + i] = dt * ex2(behind);
+            V[2 * kChunk + i] = dt;
+            if (lane == 31) V[3 * kChunk + block] = upto;
             warp_arrive(CK_V, c);
         };
         // this token's weight in the state behind the chunk
@@ -676,7 +680,7 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                     ok = warp_wait(CK_CS, c);
                     if (!ok) break;
                 }
-                if (sums && c + 1 < u.chunks) decays(c + 1);
+                if (isb && sums && c + 1 < u.chunks) decays(c + 1);
                 if (isb) {  // the state's copy has been read: its place is X's low parts' now
                     ok = warp_wait(CK_X, c) && warp_wait(CK_XH, c);
                     if (!ok) break;
@@ -685,6 +689,7 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                     if (STATE) warp_arrive(CK_XE, c);
                 }
                 if constexpr (!STATE) scale_y(c);
+                if (!isb && sums && c + 1 < u.chunks) decays(c + 1);
             }
             if (c + 1 < u.chunks) {
                 ok = isb ? begin(c + 1) : high_parts(c + 1);
