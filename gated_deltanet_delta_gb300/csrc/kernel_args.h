@@ -302,8 +302,8 @@ struct SsmArgs {
     int num_seqs, pool_size, H, P, G;
     int tiles;              // row tiles per head (token by token)
     // chunks of 128 tokens (ssm_chunk.cuh)
-    int seg, sub;           // chunks per segment and per piece of one
-    float* ws;              // states [.., H, P, S] of the pieces, and the logarithms (base 2) of their decays [.., H]
+    int seg;                // chunks per segment
+    float* ws;              // states [.., H, P, S] behind segments, and the logarithms (base 2) of their decays [.., H]
     float* ws_decay;
     uint32_t polls;         // of a barrier, before a wait gives up
 };

@@ -10,7 +10,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kSub = 8;  // chunks per piece of the launch ahead; segments are multiples of it
+constexpr int kSegment = 8;  // segments are multiples of so many chunks
 
 // Tokens as rows of `width` elements: boxes of 64 columns and `rows` rows, 128-byte swizzle, zero fill outside.
 bool encode_tokens(CUtensorMap* map, const void* base, long long T, long long width, long long stride, unsigned rows = 128) {
@@ -23,22 +23,32 @@ bool encode_tokens(CUtensorMap* map, const void* base, long long T, long long wi
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int P, int S, bool STATE>
+template <int P, int S>
 cudaError_t run(const SsmArgs& a, const SsmMaps& maps, unsigned grid, cudaStream_t stream) {
     using C = ssm::ChunkCfg<S>;
     static std::atomic<unsigned long long> done{0};
-    cudaError_t e = raise_smem(ssm::ssm_chunk_kernel<P, S, STATE>, C::SMEM, done);
+    cudaError_t e = raise_smem(ssm::ssm_chunk_kernel<P, S>, C::SMEM, done);
     if (e != cudaSuccess) return e;
     // the split of registers among roles waits forever where the launch has fewer than it adds up to
     static std::atomic<int> regs{0};
     if (regs.load(std::memory_order_relaxed) == 0) {
         cudaFuncAttributes fa;
-        e = cudaFuncGetAttributes(&fa, ssm::ssm_chunk_kernel<P, S, STATE>);
+        e = cudaFuncGetAttributes(&fa, ssm::ssm_chunk_kernel<P, S>);
         if (e != cudaSuccess) return e;
         regs.store(fa.numRegs, std::memory_order_relaxed);
     }
     if (regs.load(std::memory_order_relaxed) < ssm::kRegsLaunch) return cudaErrorInvalidConfiguration;
-    ssm::ssm_chunk_kernel<P, S, STATE><<<grid, ssm::kChunkNT, C::SMEM, stream>>>(a, maps);
+    ssm::ssm_chunk_kernel<P, S><<<grid, ssm::kChunkNT, C::SMEM, stream>>>(a, maps);
+    return cudaGetLastError();
+}
+
+template <int P, int S>
+cudaError_t ahead(const SsmArgs& a, const SsmMaps& maps, unsigned grid, cudaStream_t stream) {
+    using C = ssm::AheadCfg<S>;
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = raise_smem(ssm::ssm_ahead_kernel<P, S>, C::SMEM, done);
+    if (e != cudaSuccess) return e;
+    ssm::ssm_ahead_kernel<P, S><<<grid, ssm::kAheadNT, C::SMEM, stream>>>(a, maps);
     return cudaGetLastError();
 }
 
@@ -54,30 +64,32 @@ cudaError_t chunks(SsmArgs a, long long max_len, void* workspace, cudaStream_t s
         !encode_tokens(&maps.z, a.z ? a.z : a.x, a.T, inner, a.z ? a.z_stride : a.x_stride, 32))
         return cudaErrorInvalidValue;
     // Segments.  In chunk times of one SM: `share` is the work over the SMs, a chain takes as long as it is, units that are
-    // more than the SMs end unevenly by about half a unit, and the launch ahead costs two fifths of what it covers and a start.
+    // more than the SMs end unevenly by about half a unit, and the launch ahead costs two fifths of what it covers, its uneven end
+    // included, and a start.  (Four prompts of 64, 43, 22 and 56 chunks and 32 units each: 343 us
+    // whole, 362 to 428 in segments of 8 to 48; one of 128 chunks: 486 whole, 272, 234, 296, 228, 248, 290 in segments of 8, 16, .. 48.)
     const long long per_seg = static_cast<long long>(a.G) * ((a.H / a.G * P + 127) / 128);
     const double total = static_cast<double>((a.T + 127) / 128), share = total * per_seg / sms;
     const double longest = static_cast<double>((std::min(std::max(max_len, 1LL), a.T) + 127) / 128);
     auto cost = [&](double seg) {
         const double units = total / longest * std::max(1.0, static_cast<double>(static_cast<long long>((longest + seg - 1) / seg))) * per_seg;
-        const double ahead = seg < longest ? 0.4 * share * (longest - seg) / longest + 3.0 : 0.0;
-        return (units <= sms ? seg : std::max(seg, share + seg / 2)) + ahead;
+        const double start = seg < longest ? 0.4 * share * (longest - seg) / longest + 3.0 : 0.0;
+        return (units <= sms ? seg : std::max(seg, share + seg / 2)) + start;
     };
-    a.seg = a.sub = 1 << 24;  // one segment per sequence
+    a.seg = 1 << 24;  // one segment per sequence
     double best = 0.85 * cost(longest);
-    for (int seg = kSub; seg < longest; seg += kSub)
-        if (cost(seg) < best) best = cost(seg), a.seg = seg, a.sub = kSub;
-    const long long state = static_cast<long long>(a.H) * P * S, states = 2 * (a.T / (128 * kSub));
+    for (int seg = kSegment; seg < longest; seg += kSegment)
+        if (cost(seg) < best) best = cost(seg), a.seg = seg;
+    const long long state = static_cast<long long>(a.H) * P * S, states = 2 * (a.T / (128 * kSegment));
     a.ws = static_cast<float*>(workspace);
     a.ws_decay = a.ws + states * state;
     if (a.seg < 1 << 24) {
-        const long long grid = a.T / (128 * kSub) * per_seg;
-        e = run<P, S, true>(a, maps, static_cast<unsigned>(grid), stream);
+        const long long grid = a.T / 128 / a.seg * per_seg;
+        e = ahead<P, S>(a, maps, static_cast<unsigned>(grid), stream);
         if (e != cudaSuccess) return e;
     }
     const long long grid = (a.T / 128 / a.seg + a.num_seqs) * per_seg;
     if (grid >= 1LL << 31) return cudaErrorInvalidConfiguration;
-    return run<P, S, false>(a, maps, static_cast<unsigned>(grid), stream);
+    return run<P, S>(a, maps, static_cast<unsigned>(grid), stream);
 }
 
 }  // namespace
@@ -94,9 +106,9 @@ void launch_ssm_steps(SsmArgs a, int S, cudaStream_t stream) {
     }
 }
 
-// Two states for every piece that a call of T tokens can have, and their decays.
+// Two states for every segment that a call of T tokens can have, and their decays.
 size_t ssm_workspace_bytes(int, long long T, int H, int P, int S) {
-    return static_cast<size_t>(2 * (T / (128 * kSub))) * H * (static_cast<size_t>(P) * S + 1) * sizeof(float);
+    return static_cast<size_t>(2 * (T / (128 * kSegment))) * H * (static_cast<size_t>(P) * S + 1) * sizeof(float);
 }
 
 cudaError_t launch_ssm_prefill(const SsmArgs& args, int S, long long max_len, void* workspace, cudaStream_t stream) {

@@ -17,18 +17,19 @@
 // the copy of S that Y is made from are rounded to bf16 (2^-8 of each product, like the output's own rounding).
 //
 // Roles, 640 threads.  Sixteen workers' warps: a thread is a token (a TMEM lane) of M, of Y and of X', and a feature of the state.
-// Warpgroups 0 and 1 (A) have M's diagonal blocks and the next ones, 2 and 3 (B) the blocks further off, dt, the decays' sums, X' and
-// the state between two chunks; the output (D, the gate) is shared, 32 features each.  Warp 16 loads, a lane each of warps 17
-// and 18 issues the MMAs.  Per chunk c
-//     A: M, Y scaled | output        B: M, X' low, Y scaled | dt, sums, X' high, state of c + 1 | output.
-// Measured: prompts of up to 8192 tokens, four, 64 heads of 64, N = 128, gated: 382 us, 6.0 us per chunk of the longest chain (with A
-// alone for M and the outputs, B alone for the state, 6.9 us).  What bounds it is the chain of hand-overs within a chunk and the
-// latency of the workers' instructions, four warps per scheduler; HBM would take 104 us for the whole, the tensor core 1.6 us a chunk.
+// Warpgroups 0 and 1 (A) have M's diagonal blocks and the next ones and the high parts of X', 2 and 3 (B) the blocks further off, the
+// low parts and the state between two chunks; the output (D, the gate) is shared, 32 features each, and the decays' sums are made by
+// the warps that have the least of M.  Warp 16 loads x, B and C, a lane of warp 17 issues what the outputs are made of and one of warp
+// 18 the state's update, and warp 19 loads the gate and stores the output.  Per chunk c
+//     A: M, Y scaled | X' high of c + 1 | output        B: M, X' low, Y scaled | state of c + 1 | output.
+// Measured: four prompts of up to 8192 tokens, 64 heads of 64, N = 128, gated: 343 us, 5.3 us per chunk of the longest chain; one of
+// 16384 tokens, 32 heads of 128: 228 us, 486 without segments (3.8 us a chunk with 32 SMs at work).  What bounds it: all sixteen warps
+// are busy nearly all of a chunk and issue in two of five cycles, four warps per scheduler, the rest is the latency of their
+// instructions and the hand-overs.  HBM would take 104 and 42 us, the tensor core 1.6 us a chunk.
 //
 // Segments.  A sequence is a chain, and a call with few sequences and heads has fewer chains than the GPU has SMs.  Long sequences are
-// cut into segments that run side by side: a launch ahead (STATE) forms, over pieces of them, the states that
-// zero states (for the first piece the pool's) end in, without the outputs; a segment then starts from the sum of the
-// pieces ahead of it with their decays.  Its cost is the state's part (about two fifths) of all but the last segments.
+// cut into segments that run side by side: a launch ahead (ssm_ahead_kernel) forms the states that all segments but the last end in
+// from a zero state (the first from the pool's), and a segment starts from the sum of those ahead of it with their decays.
 //
 // Every wait is bounded (attn_tiles.cuh): one that runs out sets GDN_STATUS_TIMEOUT and the CTA's limit of polls to 0.
 #pragma once
@@ -96,48 +97,52 @@ __device__ __forceinline__ int anew(int x) {
 }
 __device__ __forceinline__ float ex2(float x) { return attn::fast_exp2(x); }
 
-// The unit with number `rank`: one warp walks the sequences.  A sequence of more than a.seg chunks has the states of its
-// pieces in the workspace: the first the pool's, then one behind each piece.
-template <bool STATE>
+// The unit with number `rank`: one warp walks the sequences, twice: segments of a.seg chunks come first, then what is left of the
+// sequences, so that the last to start are the short ones.  Ahead (AHEAD) are all segments but each sequence's last.  A sequence of
+// more than a.seg chunks has states in the workspace: the pool's, then one for each segment ahead.
+template <bool AHEAD>
 __device__ __forceinline__ void find_unit(const SsmArgs& a, int rank, Unit& u) {
     const int lane = threadIdx.x & 31;
-    const int per = a.seg / a.sub;  // pieces per segment
     int base = 0;
-    long long ws = 0;
     if (lane == 0) u.found = 0;
-    for (int n0 = 0; n0 < a.num_seqs; n0 += 32) {
-        const int n = n0 + lane;
-        long long b = 0, e = 0, slot = 0;
-        if (n >= a.num_seqs || !sequence(a, n, b, e, slot, false)) b = e = 0;
-        const int chunks = static_cast<int>((e - b + kChunk - 1) / kChunk), segs = (chunks + a.seg - 1) / a.seg;
-        const int pieces = segs > 1 ? (segs - 1) * per : 0, mine = STATE ? pieces : segs, states = pieces ? pieces + 1 : 0;
-        int upto = mine, held = states;
+#pragma unroll 1
+    for (int walk = 0; walk < (AHEAD ? 1 : 2); ++walk) {
+        long long ws = 0;
+        for (int n0 = 0; n0 < a.num_seqs; n0 += 32) {
+            const int n = n0 + lane;
+            long long b = 0, e = 0, slot = 0;
+            if (n >= a.num_seqs || !sequence(a, n, b, e, slot, false)) b = e = 0;
+            const int chunks = static_cast<int>((e - b + kChunk - 1) / kChunk), segs = (chunks + a.seg - 1) / a.seg;
+            const int whole = chunks / a.seg, mine = AHEAD ? max(segs - 1, 0) : walk == 0 ? whole : segs - whole;
+            int upto = mine, held = segs > 1 ? segs : 0;
+            const int states = held;
 #pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const int x = __shfl_up_sync(kFullMask, upto, o), y = __shfl_up_sync(kFullMask, held, o);
-            if (lane >= o) upto += x, held += y;
-        }
-        const unsigned hit = __ballot_sync(kFullMask, rank < base + upto);
-        if (hit) {
-            if (lane == __ffs(hit) - 1) {
-                const int k = rank - (base + upto - mine), c0 = k * (STATE ? a.sub : a.seg);
-                u.begin = b + static_cast<long long>(c0) * kChunk;
-                u.slot = slot;
-                u.ws = ws + held - states;
-                u.chunks = min(STATE ? a.sub : a.seg, chunks - c0);
-                u.len = static_cast<int>(min(e - u.begin, static_cast<long long>(u.chunks) * kChunk));
-                u.k = k;
-                u.parts = segs;
-                u.found = 1;
+            for (int o = 1; o < 32; o *= 2) {
+                const int x = __shfl_up_sync(kFullMask, upto, o), y = __shfl_up_sync(kFullMask, held, o);
+                if (lane >= o) upto += x, held += y;
             }
-            return;
+            const unsigned hit = __ballot_sync(kFullMask, rank < base + upto);
+            if (hit) {
+                if (lane == __ffs(hit) - 1) {
+                    const int k = rank - (base + upto - mine) + (walk == 0 ? 0 : whole);
+                    u.begin = b + static_cast<long long>(k) * a.seg * kChunk;
+                    u.slot = slot;
+                    u.ws = ws + held - states;
+                    u.chunks = min(a.seg, chunks - k * a.seg);
+                    u.len = static_cast<int>(min(e - u.begin, static_cast<long long>(u.chunks) * kChunk));
+                    u.k = k;
+                    u.parts = segs;
+                    u.found = 1;
+                }
+                return;
+            }
+            base += __shfl_sync(kFullMask, upto, 31);
+            ws += __shfl_sync(kFullMask, held, 31);
         }
-        base += __shfl_sync(kFullMask, upto, 31);
-        ws += __shfl_sync(kFullMask, held, 31);
     }
 }
 
-template <int P, int S, bool STATE>
+template <int P, int S>
 __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ SsmMaps maps) {
     using K = ChunkCfg<S>;
     constexpr int NCB = K::NCB;
@@ -153,17 +158,17 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
     const int in_group = a.H / a.G, per_group = (in_group * P + 127) / 128, per_seg = a.G * per_group;
     const int rank = blockIdx.x / per_seg, which = blockIdx.x % per_seg, g = which / per_group;
     const int h0 = g * in_group + which % per_group * (128 / P), heads = min(128 / P, (g + 1) * in_group - h0);
-    if (!STATE && blockIdx.x == 0)
+    if (blockIdx.x == 0)
         for (int n = tid; n < a.num_seqs; n += kChunkNT) {
             long long b, e, slot;
             sequence(a, n, b, e, slot, true);
         }
-    if (warp == 0) find_unit<STATE>(a, rank, us);
+    if (warp == 0) find_unit<false>(a, rank, us);
     if (tid == 32) {
         for (int i = 0; i < 2 * CK_N; ++i) {
             const int id = i / 2;
             // B and C arrive one after the other; at the others but for the copies' and products' arrive warps
-            const int count = id == CK_BC ? (STATE ? 1 : 2) : id == CK_YF || id == CK_O || id == CK_XE || (P == 128 && id == CK_Y0) ? 16
+            const int count = id == CK_BC ? 2 : id == CK_YF || id == CK_O || id == CK_XE || (P == 128 && id == CK_Y0) ? 16
                               : id == CK_V ? (P == 64 ? 8 : 4)
                               : id == CK_XH || id == CK_S || id == CK_XL || id == CK_Y0 || id == CK_Y1 ? 8 : 1;
             tc::mbar_init(&bars[i], count);
@@ -222,14 +227,12 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                 const int halves = heads * P / 64;
                 tc::mbar_expect_tx(bar, halves * 16384);
                 for (int i = 0; i < halves; ++i) attn::tma_load_2d(sb + K::OFF_X + (c & 1) * K::X + i * 16384, &maps.x, h0 * P + 64 * i, row, bar);
-                if constexpr (!STATE) {
-                    if (c >= NCB) ok = wait(CK_CS, c - NCB);
-                    if (!ok) break;
-                    bar = &bars[2 * CK_BC + (c & 1)];
-                    tc::mbar_expect_tx(bar, K::CB);
+                if (c >= NCB) ok = wait(CK_CS, c - NCB);
+                if (!ok) break;
+                bar = &bars[2 * CK_BC + (c & 1)];
+                tc::mbar_expect_tx(bar, K::CB);
 #pragma unroll
-                    for (int i = 0; i < S / 64; ++i) attn::tma_load_2d(sb + K::OFF_C + c % NCB * K::CB + i * 16384, &maps.C, g * S + 64 * i, row, bar);
-                }
+                for (int i = 0; i < S / 64; ++i) attn::tma_load_2d(sb + K::OFF_C + c % NCB * K::CB + i * 16384, &maps.C, g * S + 64 * i, row, bar);
                 if (c >= NCB) ok = wait(CK_UPD, c - NCB);
                 if (!ok) break;
                 bar = &bars[2 * CK_BC + (c & 1)];
@@ -237,14 +240,12 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
 #pragma unroll
                 for (int i = 0; i < S / 64; ++i) attn::tma_load_2d(sb + K::OFF_B + c % NCB * K::CB + i * 16384, &maps.B, g * S + 64 * i, row, bar);
             }
-            if (!ok)  // gave up: leave what copies are in flight (microseconds) a millisecond
-                for (int i = 0; i < 100; ++i) __nanosleep(10000);
         }
         // The products' loops are unrolled by four only: unrolled in full, their descriptors, which are the same from chunk to chunk,
         // were kept in more registers than there are.  Two lanes issue: one what the outputs are made of, the other the state's update, so that neither chain waits for the
         // other's barriers.  What must be in order between the two is so by those: a chunk's update ends behind its Y = C S^T, whose
         // copy's place the low parts take, and that behind its G.
-        if (!STATE && warp == 17 && attn::elect()) {
+        if (warp == 17 && attn::elect()) {
             // -------------------------------------------------------- G, Y
             constexpr uint32_t ID_G = tc::idesc_bf16(128, 128, 0, 0, 0), ID_MX = tc::idesc_bf16(128, P, 0, 1, 0);
             const uint64_t dC = tc::sdesc(sb + K::OFF_C, 16, 1024), dB = tc::sdesc(sb + K::OFF_B, 16, 1024), dS = tc::sdesc(sb + K::OFF_SX, 16, 1024);
@@ -299,7 +300,7 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
             tc::commit(&bars[2 * CK_DRAIN]);
             tc::mbar_wait(&bars[2 * CK_DRAIN], 0, kPolls);
         }
-        if (!STATE && warp == 19 && attn::elect()) {
+        if (warp == 19 && attn::elect()) {
             // -------------------------------------------------------- the gate's rows, and the stores of whole chunks, in one place
             const int halves = heads * P / 64;
             auto gate = [&](int c) {
@@ -325,8 +326,6 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                 else if (c + 1 < u.chunks) gate(c + 1);
             }
             tc::bulk_wait_all();
-            if (!ok && a.z)
-                for (int i = 0; i < 100; ++i) __nanosleep(10000);
         }
         if (warp == 18 && attn::elect()) {
             // -------------------------------------------------------- the state
@@ -513,37 +512,31 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
         const bool there = ph < heads;
         auto srow = [&] { return (static_cast<long long>(h0 + (there ? ph : 0)) * P + (P == 64 ? t & 63 : t)) * S + side * (S / 2); };
         auto state = [&] { return static_cast<long long>(a.H) * P * S; };
-        float gone = 0.f;  // the decay of the chunks so far
-        if (isb) {  // the unit's first state
-            const bool from_pool = STATE ? u.k == 0 : u.parts == 1;
-            const int pieces = STATE ? 0 : u.k * (a.seg / a.sub);
-            const float* src = (from_pool ? a.state + u.slot * state() : a.ws + u.ws * state()) + srow();
-#pragma unroll 1
+        if (isb) {  // the unit's first state: the pool's (for the first of several segments its copy), or what the segments ahead add up to
+            const float* src = (u.parts == 1 ? a.state + u.slot * state() : a.ws + u.ws * state()) + srow();
+            float s[S / 2];
+#pragma unroll
+            for (int q = 0; q < S / 2; q += 4) {
+                const float4 v = there && u.k == 0 ? *reinterpret_cast<const float4*>(src + q) : make_float4(0.f, 0.f, 0.f, 0.f);
+                s[q] = v.x, s[q + 1] = v.y, s[q + 2] = v.z, s[q + 3] = v.w;
+            }
+            for (int j = 0; j < u.k && there; ++j) {
+                const long long at = u.ws + 1 + j;
+                const float f = ex2(a.ws_decay[at * a.H + h0 + ph]);
+                const float* from = a.ws + at * state() + srow();
+#pragma unroll
+                for (int q = 0; q < S / 2; q += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(from + q);
+                    s[q] = fmaf(f, s[q], v.x), s[q + 1] = fmaf(f, s[q + 1], v.y), s[q + 2] = fmaf(f, s[q + 2], v.z), s[q + 3] = fmaf(f, s[q + 3], v.w);
+                }
+            }
+            __syncwarp();
+#pragma unroll
             for (int i = 0; i < S / 32; ++i) {
-                float s[16];
+                float v[16];
 #pragma unroll
-                for (int q = 0; q < 16; q += 4) {
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (there && (!STATE || u.k == 0) && pieces == 0) v = *reinterpret_cast<const float4*>(src + 16 * i + q);
-                    s[q] = v.x, s[q + 1] = v.y, s[q + 2] = v.z, s[q + 3] = v.w;
-                }
-                if (STATE && u.k == 0 && there) {  // the pool's state for the first segment: the last one may have replaced it by then
-                    float* to = a.ws + u.ws * state() + srow() + 16 * i;
-#pragma unroll
-                    for (int q = 0; q < 16; q += 4) *reinterpret_cast<float4*>(to + q) = make_float4(s[q], s[q + 1], s[q + 2], s[q + 3]);
-                }
-                for (int j = 0; j < pieces && there; ++j) {
-                    const long long at = u.ws + 1 + j;
-                    const float f = ex2(a.ws_decay[at * a.H + h0 + ph]);
-                    const float* from = a.ws + at * state() + srow() + 16 * i;
-#pragma unroll
-                    for (int q = 0; q < 16; q += 4) {
-                        const float4 v = *reinterpret_cast<const float4*>(from + q);
-                        s[q] = fmaf(f, s[q], v.x), s[q + 1] = fmaf(f, s[q + 1], v.y), s[q + 2] = fmaf(f, s[q + 2], v.z), s[q + 3] = fmaf(f, s[q + 3], v.w);
-                    }
-                }
-                __syncwarp();
-                tc::st16(trow + K::TM_S + side * (S / 2) + 16 * i, s);
+                for (int q = 0; q < 16; ++q) v[q] = s[16 * i + q];
+                tc::st16(trow + K::TM_S + side * (S / 2) + 16 * i, v);
             }
             tc::wait_st();
         }
@@ -626,7 +619,6 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
             if (c > 0 && !warp_wait(CK_UPH, c - 1)) return false;
             weigh(c, weight_of(c), true, K::OFF_XH);
             warp_arrive(CK_XH, c);
-            if (STATE) warp_arrive(CK_XE, c);
             return true;
         };
         float weight = 0.f;
@@ -635,8 +627,7 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
             if (!warp_wait(CK_V, c)) return false;
             weight = weight_of(c);
             const float* W = vec(c, ph) + 3 * kChunk;  // of this feature's head
-            const float all = (W[0] + W[1]) + (W[2] + W[3]), keep = ex2(all);
-            gone += all;
+            const float keep = ex2((W[0] + W[1]) + (W[2] + W[3]));
             if (c > 0 && !warp_wait(CK_UPD, c - 1)) return false;
             const attn::f32x2 kk = attn::pair(keep, keep);
             const int ts = anew(t);
@@ -646,13 +637,11 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                 const int n0 = side * (S / 2) + 16 * i;
                 tc::ld16(trow + K::TM_S + n0, s);
                 tc::wait_ld();
-                if constexpr (!STATE) {
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        attn::sts128(sb + K::OFF_SX + tc::sw_chunk(ts, n0 / 8 + q, 128),
-                                     make_uint4(pack_bf16x2(s[8 * q], s[8 * q + 1]), pack_bf16x2(s[8 * q + 2], s[8 * q + 3]), pack_bf16x2(s[8 * q + 4], s[8 * q + 5]),
-                                                pack_bf16x2(s[8 * q + 6], s[8 * q + 7])));
-                }
+                for (int q = 0; q < 2; ++q)
+                    attn::sts128(sb + K::OFF_SX + tc::sw_chunk(ts, n0 / 8 + q, 128),
+                                 make_uint4(pack_bf16x2(s[8 * q], s[8 * q + 1]), pack_bf16x2(s[8 * q + 2], s[8 * q + 3]), pack_bf16x2(s[8 * q + 4], s[8 * q + 5]),
+                                            pack_bf16x2(s[8 * q + 6], s[8 * q + 7])));
 #pragma unroll
                 for (int q = 0; q < 16; q += 2) attn::unpair(attn::mul2(attn::pair(s[q], s[q + 1]), kk), s + q);
                 tc::st16(trow + K::TM_S + n0, s);
@@ -664,7 +653,7 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
             return true;
         };
         bool ok = true;
-        if (!STATE && !isb) {
+        if (!isb) {
             for (int j = w + 1; j < 4; ++j) {  // tokens behind the row's: zero, once for all
                 const uint32_t zero[16] = {};
                 if (P == 64 || wg == 0) attn::tm_st16(tM + 16 * j, zero);
@@ -674,33 +663,29 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
 #pragma unroll 1
         for (int c = -1; c < u.chunks; ++c) {
             if (c >= 0) {
-                if constexpr (!STATE) {
-                    ok = (isb || warp_wait(CK_V, c)) && weights(c);
-                    if (!ok) break;
-                    ok = warp_wait(CK_CS, c);
-                    if (!ok) break;
-                }
+                ok = (isb || warp_wait(CK_V, c)) && weights(c);
+                if (!ok) break;
+                ok = warp_wait(CK_CS, c);
+                if (!ok) break;
                 if (isb && sums && c + 1 < u.chunks) decays(c + 1);
                 if (isb) {  // the state's copy has been read: its place is X's low parts' now
                     ok = warp_wait(CK_X, c) && warp_wait(CK_XH, c);
                     if (!ok) break;
                     weigh(c, weight, false, K::OFF_SX);
                     warp_arrive(CK_XL, c);
-                    if (STATE) warp_arrive(CK_XE, c);
                 }
-                if constexpr (!STATE) scale_y(c);
+                scale_y(c);
                 if (!isb && sums && c + 1 < u.chunks) decays(c + 1);
             }
             if (c + 1 < u.chunks) {
                 ok = isb ? begin(c + 1) : high_parts(c + 1);
             }
-            if (!STATE && c >= 0) ok = ok && output(c);
+            if (c >= 0) ok = ok && output(c);
             if (!ok) break;
         }
         ok = ok && isb && warp_wait(CK_UPD, u.chunks - 1);
-        if (ok && (STATE || u.k == u.parts - 1)) {
-            float* dst = (STATE ? a.ws + (u.ws + 1 + u.k) * state() : a.state + u.slot * state()) + srow();
-            if (STATE && side == 0 && there && (P == 64 ? t & 63 : t) == 0) a.ws_decay[(u.ws + 1 + u.k) * a.H + h0 + ph] = gone;
+        if (ok && u.k == u.parts - 1) {
+            float* dst = a.state + u.slot * state() + srow();
 #pragma unroll 1
             for (int i = 0; i < S / 32; ++i) {
                 float v[16];
@@ -717,7 +702,220 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
     tc::fence_before();
     __syncthreads();
     if (warp == 17) tc::tmem_dealloc(tm, 512);
-    if (tid == 0 && most_polls == 0) atomicOr(a.status, kStatusTimeout);
+    if (tid == 0 && most_polls == 0) {  // gave up: leave what copies are in flight (microseconds) a millisecond
+        for (int i = 0; i < 100; ++i) __nanosleep(10000);
+        atomicOr(a.status, kStatusTimeout);
+    }
+}
+
+// The states that the segments ahead end in, each from a zero state (the first of a sequence from the pool's, of which it also leaves a
+// copy), and the logarithms of their decays.  A token's weight is its decay to the segment's end, so nothing is carried from chunk to
+// chunk: the chunks are taken from the last to the first with the sum of the steps behind them, and sixteen warps make X' of one
+// (high parts in x's own tile, low parts beside it) while the products of the one before run.
+template <int S>
+struct AheadCfg {
+    static constexpr uint32_t X = 32768, CB = kChunk * S * 2, STAGE = 2 * X + CB;  // x (then its high parts), the low parts, B
+    static constexpr uint32_t SMEM = 2 * STAGE + 1024;
+};
+constexpr int kAheadNT = 576;
+
+template <int P, int S>
+__global__ void __launch_bounds__(kAheadNT, 1) ssm_ahead_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ SsmMaps maps) {
+    using K = AheadCfg<S>;
+    constexpr int BATCH = 8;  // chunks whose weights are made at once
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[2], ready[2], done[2], drain;
+    __shared__ Unit us;
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile uint32_t most_polls;
+    __shared__ alignas(16) float weight_s[2][2][BATCH * kChunk], block_s[2][2][BATCH * 4];  // block_s is read four at a time
+    __shared__ float total_s[2];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int in_group = a.H / a.G, per_group = (in_group * P + 127) / 128, per_seg = a.G * per_group;
+    const int which = blockIdx.x % per_seg, g = which / per_group;
+    const int h0 = g * in_group + which % per_group * (128 / P), heads = min(128 / P, (g + 1) * in_group - h0);
+    if (warp == 0) find_unit<true>(a, blockIdx.x / per_seg, us);
+    if (tid == 32) {
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&full[i], 1);
+            tc::mbar_init(&ready[i], 16);
+            tc::mbar_init(&done[i], 1);
+        }
+        tc::mbar_init(&drain, 1);
+        most_polls = a.polls;
+    }
+    __syncthreads();
+    if (!us.found) return;
+    if (warp == 17) tc::tmem_alloc(&tmem_slot, 128);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tm = tmem_slot;
+    const Unit& u = us;
+    const uint32_t sb = tc::smem_u32(smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u));
+    // i: the number of a chunk from the segment's end
+    auto wait = [&](uint64_t* bars, int i) -> bool {
+        if (tc::mbar_wait_most<kPolls>(&bars[i & 1], i >> 1 & 1, &most_polls)) return true;
+        most_polls = 0;
+        return false;
+    };
+
+    if (warp == 16) {
+        // ------------------------------------------------------------ loader
+        if (lane == 0) {
+            for (int i = 0; i < u.chunks; ++i) {
+                if (i >= 2 && !wait(done, i - 2)) break;
+                const int row = static_cast<int>(u.begin) + (u.chunks - 1 - i) * kChunk, halves = heads * P / 64;
+                const uint32_t to = sb + (i & 1) * K::STAGE;
+                tc::mbar_expect_tx(&full[i & 1], halves * 16384 + K::CB);
+                for (int j = 0; j < halves; ++j) attn::tma_load_2d(to + j * 16384, &maps.x, h0 * P + 64 * j, row, &full[i & 1]);
+#pragma unroll
+                for (int j = 0; j < S / 64; ++j) attn::tma_load_2d(to + 2 * K::X + j * 16384, &maps.B, g * S + 64 * j, row, &full[i & 1]);
+            }
+        }
+    } else if (warp == 17) {
+        // ------------------------------------------------------------ MMA issue
+        if (attn::elect()) {
+            constexpr uint32_t ID = tc::idesc_bf16(128, S, 1, 1, 0);
+            const uint64_t dX = tc::sdesc(sb, 16384, 1024);
+            for (int i = 0; i < u.chunks; ++i) {
+                if (!wait(full, i) || !wait(ready, i)) break;
+                tc::fence_after();
+                const uint64_t hi = dX + (i & 1) * (K::STAGE >> 4), lo = hi + (K::X >> 4), b = lo + (K::X >> 4);
+#pragma unroll 1
+                for (uint32_t q = 0; q < 4; ++q)
+#pragma unroll
+                    for (uint32_t j = 0; j < 4; ++j) {
+                        const uint32_t k = (4 * q + j) & 7;
+                        tc::mma_bf16(tm, (q < 2 ? hi : lo) + k * 128, b + k * 128, ID, i + q + j > 0);
+                    }
+                tc::commit(&done[i & 1]);
+            }
+            // nothing of this CTA's may be in flight when it ends, its barriers' arrivals included
+            tc::commit(&drain);
+            tc::mbar_wait(&drain, 0, kPolls);
+        }
+    } else {
+        // ------------------------------------------------------------ workers: a token's 32 features, then a quarter of a feature's state
+        const int wg = warp >> 2, w = warp & 3, t = tid & 127, side = wg & 1, hh = P == 64 ? side : 0;
+        const bool valid = hh < heads;
+        // the weights of a batch within blocks of 32 tokens, and the blocks' sums; blocks count from the batch's first token on
+        auto weights = [&](int batch) {
+            const int last = u.chunks - batch * BATCH, first = max(0, last - BATCH), blocks = 4 * (last - first);
+            const int head = warp & 1;
+            if (head >= heads) return;
+            const float A = -expf(a.A_log[h0 + head]) * 1.44269504f, bias = a.dt_bias[h0 + head];
+            float dt[BATCH / 2];
+#pragma unroll
+            for (int j = 0; j < BATCH / 2; ++j) {
+                const int b = 8 * j + (warp >> 1);
+                dt[j] = b < blocks ? bf16_to_f32(a.dt[(u.begin + first * kChunk + b * 32 + lane) * a.dt_stride + h0 + head]) : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < BATCH / 2; ++j) {
+                const int b = 8 * j + (warp >> 1);
+                if (b >= blocks) break;
+                const float d = softplus(dt[j] + bias), step = A * d;
+                float behind = __shfl_down_sync(kFullMask, step, 1);
+                if (lane == 31) behind = 0.f;
+#pragma unroll
+                for (int o = 1; o < 32; o *= 2) {
+                    const float y = __shfl_down_sync(kFullMask, behind, o);
+                    if (lane + o < 32) behind += y;
+                }
+                weight_s[batch & 1][head][b * 32 + lane] = d * ex2(behind);
+                if (lane == 0) block_s[batch & 1][head][b] = behind + step;
+            }
+        };
+        auto together = [] { asm volatile("bar.sync 1, 512;" ::: "memory"); };
+        weights(0);
+        together();
+        float gone = 0.f;  // the steps behind the chunk
+        bool ok = true;
+        for (int i = 0; i < u.chunks; ++i) {
+            const int batch = i / BATCH, left = u.chunks - batch * BATCH;  // this batch's first chunk is number max(0, left - BATCH)
+            if (i % BATCH == 0 && left > BATCH) weights(batch + 1);
+            if (ok) {
+                ok = __all_sync(kFullMask, wait(full, i));
+            }
+            if (ok) {
+                const int c = min(left, BATCH) - 1 - i % BATCH;  // in the batch
+                float weight = 0.f;
+                if (valid) {
+                    const float4 sums = *reinterpret_cast<const float4*>(&block_s[batch & 1][hh][4 * c]);
+                    const float behind = w == 0 ? sums.y + sums.z + sums.w : w == 1 ? sums.z + sums.w : w == 2 ? sums.w : 0.f;
+                    weight = weight_s[batch & 1][hh][c * kChunk + t] * ex2(gone + behind);
+                    gone += (sums.x + sums.y) + (sums.z + sums.w);
+                }
+                const attn::f32x2 ww = attn::pair(weight, weight), minus = attn::pair(-1.f, -1.f);
+                const uint32_t tile = sb + (i & 1) * K::STAGE + side * 16384 + t * 128;
+                uint4 x[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) x[q] = valid ? attn::lds128(tile + ((((wg >> 1) * 4 + q) ^ (t & 7)) << 4)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t v[4] = {x[q].x, x[q].y, x[q].z, x[q].w}, l[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const attn::f32x2 p = attn::mul2(attn::widen2(v[k]), ww);
+                        float f[2];
+                        attn::unpair(p, f);
+                        v[k] = pack_bf16x2(f[0], f[1]);
+                        attn::unpair(attn::fma2(attn::widen2(v[k]), minus, p), f);
+                        l[k] = pack_bf16x2(f[0], f[1]);
+                    }
+                    const uint32_t at = tile + ((((wg >> 1) * 4 + q) ^ (t & 7)) << 4);
+                    attn::sts128(at, make_uint4(v[0], v[1], v[2], v[3]));
+                    attn::sts128(at + K::X, make_uint4(l[0], l[1], l[2], l[3]));
+                }
+                tc::fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&ready[i & 1]);
+            }
+            if (i % BATCH == BATCH - 1) together();  // all warps come here, those that gave up too
+        }
+        if (w == 0 && wg < heads && lane == 0 && P == 64) total_s[wg] = gone;
+        if (P == 128 && tid == 0) total_s[0] = gone;
+        together();
+        ok = ok && __all_sync(kFullMask, wait(done, u.chunks - 1));
+        tc::fence_after();
+        if (ok) {
+            const int ph = P == 64 ? t >> 6 : 0;
+            const bool there = ph < heads;
+            const long long state = static_cast<long long>(a.H) * P * S;
+            const long long row = (static_cast<long long>(h0 + (there ? ph : 0)) * P + (P == 64 ? t & 63 : t)) * S + wg * (S / 4);
+            const float total = total_s[there ? ph : 0], f = ex2(total);
+            if (wg == 0 && there && (P == 64 ? t & 63 : t) == 0) a.ws_decay[(u.ws + 1 + u.k) * a.H + h0 + ph] = total;
+#pragma unroll
+            for (int i = 0; i < S / 64; ++i) {
+                float v[16];
+                tc::ld16(tm + (static_cast<uint32_t>(w * 32) << 16) + wg * (S / 4) + 16 * i, v);
+                tc::wait_ld();
+                if (there) {
+                    if (u.k == 0) {  // the pool's state, copied too: the last segment may have replaced it when the first one starts
+#pragma unroll
+                        for (int q = 0; q < 16; q += 4) {
+                            const float4 x = *reinterpret_cast<const float4*>(a.state + u.slot * state + row + 16 * i + q);
+                            *reinterpret_cast<float4*>(a.ws + u.ws * state + row + 16 * i + q) = x;
+                            v[q] = fmaf(x.x, f, v[q]), v[q + 1] = fmaf(x.y, f, v[q + 1]), v[q + 2] = fmaf(x.z, f, v[q + 2]), v[q + 3] = fmaf(x.w, f, v[q + 3]);
+                        }
+                    }
+                    float* dst = a.ws + (u.ws + 1 + u.k) * state + row + 16 * i;
+#pragma unroll
+                    for (int q = 0; q < 16; q += 4) *reinterpret_cast<float4*>(dst + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+                }
+                __syncwarp();
+            }
+        }
+    }
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 17) tc::tmem_dealloc(tm, 128);
+    if (tid == 0 && most_polls == 0) {  // gave up: leave what copies are in flight (microseconds) a millisecond
+        for (int i = 0; i < 100; ++i) __nanosleep(10000);
+        atomicOr(a.status, kStatusTimeout);
+    }
 }
 
 }  // namespace ssm
