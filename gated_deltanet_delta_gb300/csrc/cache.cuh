@@ -205,6 +205,8 @@ __global__ void __launch_bounds__(kThreads) attn_cache_read_kernel(const __grid_
 // values, so that the token's row of the table, its slot and its addresses are there once for HEADS rows; the rows' loads are in
 // flight together.  HALVES: feature i's partner is i + turned / 2, in another lane of the group: it comes by a shuffle of the
 // packed row.  Else 2 i and 2 i + 1 are partners.
+// Measured, prompts of up to 8192 tokens, 32 query and 8 key heads of 128, e4m3: 89 us, 91 % of a copy's rate; of up to 4095 tokens,
+// 16 and 4 heads of 256, 16 bits: 88 us, 98 % (with queries, keys and values in one CTA, four heads a group: 106 and 90 us).
 template <int D, bool F16, bool F8, bool HALVES, int HEADS>
 __global__ void __launch_bounds__(kThreads) attn_cache_append_kernel(const __grid_constant__ AppendArgs a) {
     constexpr int LANES = D / 8, GROUPS = kThreads / LANES;

@@ -305,6 +305,7 @@ struct SsmArgs {
     int seg;                // chunks per segment
     float* ws;              // states [.., H, P, S] behind segments, and the logarithms (base 2) of their decays [.., H]
     float* ws_decay;
+    long long ws_states;    // how many
     uint32_t polls;         // of a barrier, before a wait gives up
 };
 

@@ -5,6 +5,9 @@
 //
 // Each value is read once and written once: the bound is HBM.  blockDim.x threads hold a row in registers, R
 // pieces of eight features each, blockDim.y short rows per CTA.  The sum of squares is taken over the rounded r, in fp32.
+// A row waits for its loads and then for its sums, so what counts is how many rows an SM has at once: 32 registers a thread, one or two
+// pieces.  Measured, 16383 rows of 5120, bf16 to e4m3 by groups of 128: 100 us, 88 % of a copy's rate (122 us with four pieces a
+// thread, 160 us with rows through a ring of bulk copies, 130 us with CTAs that stay and load the next row ahead).
 #pragma once
 
 #include <cuda_fp8.h>

@@ -75,14 +75,15 @@ cudaError_t chunks(SsmArgs a, long long max_len, void* workspace, cudaStream_t s
         const double start = seg < longest ? 0.4 * share * (longest - seg) / longest + 3.0 : 0.0;
         return (units <= sms ? seg : std::max(seg, share + seg / 2)) + start;
     };
-    a.seg = 1 << 24;  // one segment per sequence
+    a.seg = ssm::kWhole;
     double best = 0.85 * cost(longest);
     for (int seg = kSegment; seg < longest; seg += kSegment)
         if (cost(seg) < best) best = cost(seg), a.seg = seg;
     const long long state = static_cast<long long>(a.H) * P * S, states = 2 * (a.T / (128 * kSegment));
+    a.ws_states = states;
     a.ws = static_cast<float*>(workspace);
     a.ws_decay = a.ws + states * state;
-    if (a.seg < 1 << 24) {
+    if (a.seg < ssm::kWhole) {
         const long long grid = a.T / 128 / a.seg * per_seg;
         e = ahead<P, S>(a, maps, static_cast<unsigned>(grid), stream);
         if (e != cudaSuccess) return e;

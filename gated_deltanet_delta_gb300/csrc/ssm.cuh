@@ -6,6 +6,8 @@
 // A stream of the state, 8 bytes per element and call against 4 operations per token: HBM is the bound up to some ten
 // tokens.  A state row of N floats is split over TPR lanes, a thread has two rows and asks for all of its 16-byte pieces
 // before any arithmetic (as gdn_decode_kernel does); the tokens' inputs are staged in shared memory, kSteps at a time.
+// Measured, one token of 64 sequences, 64 heads of 64, N = 128 (270 MB): 48.5 us, 83 % of a copy's rate; 32 sequences of up to 8
+// tokens, no gate: 36.9 us, 55 %: four operations per element and token, and a sum over lanes for each output.
 #pragma once
 
 #include "common.cuh"

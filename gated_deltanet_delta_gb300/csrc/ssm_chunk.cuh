@@ -23,7 +23,7 @@
 // 18 the state's update, and warp 19 loads the gate and stores the output.  Per chunk c
 //     A: M, Y scaled | X' high of c + 1 | output        B: M, X' low, Y scaled | state of c + 1 | output.
 // Measured: four prompts of up to 8192 tokens, 64 heads of 64, N = 128, gated: 343 us, 5.3 us per chunk of the longest chain; one of
-// 16384 tokens, 32 heads of 128: 228 us, 486 without segments (3.8 us a chunk with 32 SMs at work).  What bounds it: all sixteen warps
+// 16384 tokens, 32 heads of 128, N = 64: 228 us, 486 without segments (3.8 us a chunk with 32 SMs at work).  What bounds it: all sixteen warps
 // are busy nearly all of a chunk and issue in two of five cycles, four warps per scheduler, the rest is the latency of their
 // instructions and the hand-overs.  HBM would take 104 and 42 us, the tensor core 1.6 us a chunk.
 //
@@ -44,6 +44,7 @@ namespace ssm {
 
 constexpr int kChunk = 128;
 constexpr int kChunkNT = 640;
+constexpr int kWhole = 1 << 24;  // chunks per segment where no sequence is cut
 // registers per thread: the launch's 96 x 5 warpgroups, parted as 104 x 4 for the workers and 64 for those that load and issue
 constexpr int kRegsLaunch = 96, kRegsWork = 104, kRegsIssue = 64;
 constexpr uint32_t kPolls = 1u << 22;  // the built-in limit of a wait (seconds)
@@ -106,7 +107,7 @@ __device__ __forceinline__ void find_unit(const SsmArgs& a, int rank, Unit& u) {
     int base = 0;
     if (lane == 0) u.found = 0;
 #pragma unroll 1
-    for (int walk = 0; walk < (AHEAD ? 1 : 2); ++walk) {
+    for (int walk = AHEAD || a.seg < kWhole ? 0 : 1; walk < (AHEAD ? 1 : 2); ++walk) {
         long long ws = 0;
         for (int n0 = 0; n0 < a.num_seqs; n0 += 32) {
             const int n = n0 + lane;
@@ -132,7 +133,8 @@ __device__ __forceinline__ void find_unit(const SsmArgs& a, int rank, Unit& u) {
                     u.len = static_cast<int>(min(e - u.begin, static_cast<long long>(u.chunks) * kChunk));
                     u.k = k;
                     u.parts = segs;
-                    u.found = 1;
+                    // bounds that go back make sequences overlap (the status has it): no state behind the workspace's
+                    u.found = segs == 1 || u.ws + segs <= a.ws_states;
                 }
                 return;
             }

@@ -364,7 +364,7 @@ gdn_status gdn_window_fused(float* state, const float* hist, float* hist_out, co
 /*
  * gdn_prefill_set_wait_limit -- bound every device-side wait of the prefill kernels
  * (gdn_prefill_chunked, _f16, _noalloc and comba_prefill_chunked: the chunk preparation and the
- * chunk recurrence) to `polls` polls of its mbarrier instead of the built-in limits (seconds of
+ * chunk recurrence; ssm_prefill_chunked) to `polls` polls of its mbarrier instead of the built-in limits (seconds of
  * waiting).  No page has a counterpart: this is the knob of the failure path.  A wait that runs out
  * sets GDN_STATUS_TIMEOUT in the call's dev_status and its CTA stops after one more bounded wait
  * for the copies and products it has in flight, so the call returns with that status and partial
@@ -515,7 +515,9 @@ gdn_status draft_verify(const float* target_p, const float* draft_p, const int64
  *   slots      int64 [T], as attn_cache_write's: a negative slot leaves the token out of the cache (its query is rotated);
  *              one outside it sets GDN_STATUS_BAD_CACHE_INDEX, likewise
  *   q_out      [T, Hq, D] of dtype, token t q_out_stride elements after token t - 1; may be q itself (with the same stride)
- * Supported: D in {64, 128, 256}, rotary_dim a multiple of 16, 16 .. D, Hq, Hkv <= 65535.
+ * Slots are distinct, as attn_cache_write's.
+ * Supported: D in {64, 128, 256}, rotary_dim a multiple of 16, 16 .. D, Hq, Hkv <= 65535, and in all
+ * (T / 8 + 1) ((Hq + 2 Hkv) / 4 + 3) < 2^31.
  */
 gdn_status attn_cache_append(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
                              int64_t v_stride, gdn_dtype dtype, const float* rotation, int64_t max_positions,
@@ -581,7 +583,12 @@ size_t ssm_prefill_workspace_size(int num_seqs, int64_t T, int H, int P, int N);
  *   workspace  ssm_prefill_workspace_size bytes, 16-byte aligned, contents need not be initialised; calls that share it must
  *              not overlap on the GPU
  * A sequence with malformed bounds sets GDN_STATUS_BAD_SEQLENS, one with a bad slot GDN_STATUS_BAD_CACHE_INDEX; it is skipped.  Rows of
- * no sequence are not written.
+ * no sequence are not written.  (Bounds that go back make sequences overlap: those that are not malformed themselves then have no
+ * meaningful result.)
+ * Long calls work on 128 tokens at a time: an input that is not finite leaves no meaningful value in the outputs of the up to 127
+ * tokens ahead of it either.  Sums and states are f32; the weights of pairs of tokens and the state that 128 tokens begin with are
+ * rounded to bf16 for the outputs, dt x to 16 bits of fraction for the state.
+ * A device-side wait that runs out sets GDN_STATUS_TIMEOUT; gdn_prefill_set_wait_limit bounds these waits too.
  */
 gdn_status ssm_prefill_chunked(const void* x, const void* dt, const void* B, const void* C, const void* z,
                                const int64_t* token_strides, const float* A_log, const float* D, const float* dt_bias,

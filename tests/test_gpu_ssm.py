@@ -217,6 +217,34 @@ def test_a_wait_that_runs_out_reports_and_the_next_call_is_right(gdn):
     check(s, y, state, reference(s), True)
 
 
+@pytest.mark.parametrize("P,S", [(64, 128), (128, 64)])
+def test_a_wait_that_runs_out_in_a_cut_sequence(gdn, P, S):
+    s = make(19, [6000, 200], 2, P, 1, S)
+    try:
+        gdn.set_prefill_wait_limit(1)
+        _, _, status = prefill(gdn, s)
+    finally:
+        gdn.set_prefill_wait_limit(0)
+    assert status & gdn.STATUS_TIMEOUT
+    y, state, status = prefill(gdn, s)
+    assert status == 0
+    check(s, y, state, reference(s), True)
+
+
+def test_bounds_that_go_back_stay_in_the_workspace(gdn):
+    """cu_seqlens that falls: every second sequence is malformed, the others have the same tokens, and more segments than T tokens do."""
+    T, n = 6000, 9
+    s = make(20, [T] + [0] * (n - 1), 2, 64, 1, 128)
+    need = gdn.ssm_prefill_workspace_size(n, T, 2, 64, 128)
+    ws = torch.full((need + 65536,), 85, dtype=torch.uint8, device="cuda")
+    cu = torch.tensor([0, T] * 5, device="cuda")
+    _, state, status = prefill(gdn, s, cu=cu, max_len=T, workspace=ws)
+    assert status == gdn.STATUS_BAD_SEQLENS and bool((ws[need:] == 85).all())
+    odd = s["slots"][1::2]  # the sequences that end before they begin, and the slots of none
+    spare = [i for i in range(state.shape[0]) if i not in s["slots"].tolist()]
+    assert torch.equal(state[odd], s["state"][odd]) and torch.equal(state[spare], s["state"][spare])
+
+
 def test_refuses_from_python(gdn):
     s = make(18, [2, 2], 2, 64, 1, 64, strided=False)
     args = [s["x"], s["dt"], s["B"], s["C"], s["A_log"], s["dt_bias"], s["state"], s["slots"], s["cu"], 2]
