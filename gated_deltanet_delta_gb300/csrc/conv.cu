@@ -19,9 +19,9 @@ cudaError_t run(const ConvArgs& a, cudaStream_t stream) {
     cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
     const long long tiles = (a.T + conv::kTile - 1) / conv::kTile;
-    // A CTA of the ring takes 25 us for its 128 tokens and three are on an SM: with few of them per SM the kernel of 32 tokens is done
-    // sooner (8192 channels, us, that one / the ring: 0.8 CTAs per SM 22 / 29, 3.4: 61 / 68, 5.1: 85 / 83, 10: 155 / 146, 13: 202 / 182).
-    if (tiles * blocks >= 5 * sms) {
+    // A CTA of the ring takes 28 us for its 128 tokens and four are on an SM: with fewer than two per SM the kernel of 32 tokens is done
+    // sooner (8192 channels, us, that one / the ring: 0.8 CTAs per SM 21 / 28, 1.7: 35 / 36, 2.5: 49 / 45, 5.1: 85 / 84, 10: 154 / 141).
+    if (tiles * blocks >= 2 * sms) {
         static std::atomic<unsigned long long> done{0};
         e = raise_smem(conv::short_conv_ring_kernel<TAPS, F16>, conv::kRing, done);
         if (e != cudaSuccess) return e;

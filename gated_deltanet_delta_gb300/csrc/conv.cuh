@@ -7,8 +7,9 @@
 // with the weights in registers; the TAPS - 1 tokens ahead of its tile come from L2, where the tile before read them.  Short calls go
 // in tiles of 32 tokens, the next eight of them loaded ahead (short_conv_kernel); long ones in tiles of 128 whose rows arrive through
 // a ring of bulk copies, so that many bytes are on their way with few registers (short_conv_ring_kernel; 23508 tokens of 8192
-// channels, bf16: 145 us, 5.3 TB/s; 159 us with the loads of the other).  What is left above the 115 us of the bytes are the
-// activations: an exponential and a reciprocal per value, half of the issue slots.
+// channels, bf16: 140 us, 82 % of a copy's rate; 154 us with the loads of the other, 145 us with four stages and three CTAs per SM, 151
+// us with two stages and five).  What is left above the 115 us of the bytes is the latency of sixteen warps' arithmetic: 44 % of the
+// issue slots, a value's own dependences the largest stall.
 //
 // The new history is written by a kernel of its own behind the first: in the same one, the CTA that reaches a sequence's end would
 // overwrite what the CTA at its start has yet to read.  A step of one token per sequence has no such order to keep, and is one launch.
@@ -28,7 +29,7 @@ constexpr int kTokens = 32;
 constexpr int kStep = 8;  // tokens in registers, and as many on their way
 // the kernel for long calls
 constexpr int kTile = 128;
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 constexpr int kRing = kStages * kStep * kThreads * 16;
 constexpr uint32_t kWaitPolls = 1u << 24;  // the limit of a wait for a copy (seconds)
 static_assert(kTile == kThreads, "a thread per token");

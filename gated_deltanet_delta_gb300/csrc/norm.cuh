@@ -6,7 +6,7 @@
 // Each value is read once and written once: the bound is HBM.  blockDim.x threads hold a row in registers, R
 // pieces of eight features each, blockDim.y short rows per CTA.  The sum of squares is taken over the rounded r, in fp32.
 // A row waits for its loads and then for its sums, so what counts is how many rows an SM has at once: 32 registers a thread, one or two
-// pieces.  Measured, 16383 rows of 5120, bf16 to e4m3 by groups of 128: 100 us, 88 % of a copy's rate (122 us with four pieces a
+// pieces.  Measured, 16383 rows of 5120, bf16 to e4m3 by groups of 128: 97 us, 90 % of a copy's rate (122 us with four pieces a
 // thread, 160 us with rows through a ring of bulk copies, 130 us with CTAs that stay and load the next row ahead).
 #pragma once
 
@@ -15,6 +15,7 @@
 #include "attn_mma.cuh"
 #include "common.cuh"
 #include "kernel_args.h"
+#include "tile_util.cuh"
 
 namespace gdn {
 namespace norm {
@@ -42,6 +43,12 @@ __device__ __forceinline__ float row_join(float v, float* buf) {
     return v;
 }
 
+template <bool F16>
+__device__ __forceinline__ attn::f32x2 widen(uint32_t w) {
+    if constexpr (!F16) return attn::widen2(w);
+    const float2 f = attn::unpack2<F16>(w);
+    return attn::pair(f.x, f.y);
+}
 __device__ __forceinline__ float scale_of(float amax) { return amax > 0.f ? fmaxf(amax * (1.f / 448.f), 1.17549435e-38f) : 1.f; }
 // 1 / s by one step of Newton's iteration on the approximation: within 2^-23.
 __device__ __forceinline__ float inverse(float s) {
@@ -49,11 +56,15 @@ __device__ __forceinline__ float inverse(float s) {
     return fmaf(r, fmaf(-s, r, 1.f), r);
 }
 // Eight values to e4m3, times 1 / scale: with that rounded, a quotient within 2^-22 of the middle between two may go to either (divisions
-// took 22 of 122 us).
+// took 22 us more).
 __device__ __forceinline__ uint2 to_e4m3(const float (&f)[8], float up) {
     uint32_t q[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) q[j] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * j] * up, f[2 * j + 1] * up), __NV_SATFINITE, __NV_E4M3);
+    for (int j = 0; j < 4; ++j) {
+        float g[2];
+        attn::unpair(attn::mul2(attn::pair(f[2 * j], f[2 * j + 1]), attn::pair(up, up)), g);
+        q[j] = __nv_cvt_float2_to_fp8x2(make_float2(g[0], g[1]), __NV_SATFINITE, __NV_E4M3);
+    }
     return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
 }
 
@@ -63,7 +74,7 @@ template <bool F16, bool F8, int R>
 __device__ __forceinline__ void row(const NormArgs& a, long long t, bool here, uint4 (&x)[R], const uint4 (&r)[R], float* sums, float* tops) {
     const int pieces = a.C / 8;
     auto piece = [&](int i) { return static_cast<int>(threadIdx.x + i * blockDim.x); };
-    float sum = 0.f;
+    attn::f32x2 sums2 = attn::pair(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
@@ -71,16 +82,19 @@ __device__ __forceinline__ void row(const NormArgs& a, long long t, bool here, u
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (a.residual) {
-                const float2 b = attn::unpack2<F16>(v[j]), c = attn::unpack2<F16>(u[j]);
-                u[j] = attn::pack2<F16>(b.x + c.x, b.y + c.y);
+                float f[2];
+                attn::unpair(attn::add2(widen<F16>(v[j]), widen<F16>(u[j])), f);
+                u[j] = attn::pack2<F16>(f[0], f[1]);
             }
-            const float2 f = attn::unpack2<F16>(u[j]);
-            sum = fmaf(f.x, f.x, fmaf(f.y, f.y, sum));
+            const attn::f32x2 f = widen<F16>(u[j]);
+            sums2 = attn::fma2(f, f, sums2);
         }
         x[i] = make_uint4(u[0], u[1], u[2], u[3]);
         if (a.residual && here && piece(i) < pieces) *reinterpret_cast<uint4*>(a.residual + t * a.C + piece(i) * 8) = x[i];
     }
-    const float inv = rsqrtf(row_join<false>(sum, sums) / static_cast<float>(a.C) + a.eps);
+    float sum[2];
+    attn::unpair(sums2, sum);
+    const float inv = rsqrtf(row_join<false>(sum[0] + sum[1], sums) / static_cast<float>(a.C) + a.eps);
     auto normed = [&](int i, float (&f)[8]) {
         const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
         float4 p = make_float4(0.f, 0.f, 0.f, 0.f), q = p;
@@ -88,13 +102,10 @@ __device__ __forceinline__ void row(const NormArgs& a, long long t, bool here, u
             p = __ldg(reinterpret_cast<const float4*>(a.w + piece(i) * 8));
             q = __ldg(reinterpret_cast<const float4*>(a.w + piece(i) * 8 + 4));
         }
-        const float w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+        const attn::f32x2 w[4] = {attn::pair(p.x, p.y), attn::pair(p.z, p.w), attn::pair(q.x, q.y), attn::pair(q.z, q.w)};
+        const attn::f32x2 by = attn::pair(inv, inv);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 b = attn::unpack2<F16>(u[j]);
-            f[2 * j] = b.x * inv * w[2 * j];
-            f[2 * j + 1] = b.y * inv * w[2 * j + 1];
-        }
+        for (int j = 0; j < 4; ++j) attn::unpair(attn::mul2(attn::mul2(widen<F16>(u[j]), by), w[j]), f + 2 * j);
     };
     float amax = 0.f;  // of the row (one scale per row)
 #pragma unroll
