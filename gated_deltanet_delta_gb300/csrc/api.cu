@@ -970,8 +970,8 @@ static gdn_status ssm_check(const char* fn, gdn::SsmArgs* a, const void* x, cons
     REQUIRE(aligned(x, 16) && aligned(B, 16) && aligned(C, 16) && aligned(z, 16) && aligned(out, 16) && aligned(state_pool, 16) &&
                 aligned(dt, 2) && aligned(A_log, 4) && aligned(D, 4) && aligned(dt_bias, 4) && aligned(cache_indices, 8) && aligned(dev_status, 4),
             GDN_ERR_INVALID_ARG, "%s: x, B, C, z, out and state_pool must be 16-byte aligned", fn);
-    REQUIRE(T < (1LL << 31) && static_cast<long long>(num_seqs) * H * (P / 64) < (1LL << 31) && inner < (1LL << 31) && gn < (1LL << 31),
-            GDN_ERR_UNSUPPORTED, "%s: T and num_seqs * H must be below 2^31", fn);
+    REQUIRE(T < (1LL << 31) && static_cast<long long>(num_seqs) * H * (P / 32) < (1LL << 31) && inner < (1LL << 31) && gn < (1LL << 31),
+            GDN_ERR_UNSUPPORTED, "%s: T and num_seqs * H * P / 32 must be below 2^31", fn);
     const size_t ob = static_cast<size_t>(T) * inner * 2, sb = static_cast<size_t>(pool_size) * inner * N * 4;
     auto span = [&](int i) { return (static_cast<size_t>(T - 1) * strides[i] + least[i]) * 2; };
     const void* const in[5] = {x, dt, B, C, z};

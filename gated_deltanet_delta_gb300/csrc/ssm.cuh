@@ -6,18 +6,20 @@
 // A stream of the state, 8 bytes per element and call against 4 operations per token: HBM is the bound up to some ten
 // tokens.  A state row of N floats is split over TPR lanes, a thread has two rows and asks for all of its 16-byte pieces
 // before any arithmetic (as gdn_decode_kernel does); the tokens' inputs are staged in shared memory, kSteps at a time.
-// Measured, one token of 64 sequences, 64 heads of 64, N = 128 (270 MB): 48.5 us, 83 % of a copy's rate; 32 sequences of up to 8
-// tokens, no gate: 36.9 us, 55 %: four operations per element and token, and a sum over lanes for each output.
+// CTAs of 32 rows: while some load, others compute and store (of 64 rows: 48.9 and 36.9 us).  Measured, one token of 64 sequences, 64
+// heads of 64, N = 128 (270 MB): 45.1 us, 89 % of a copy's rate; 32 sequences of up to 8 tokens, no gate: 32.8 us, 62 %: the
+// arithmetic, and a sum over lanes for each output.
 #pragma once
 
 #include "common.cuh"
 #include "kernel_args.h"
+#include "tile_util.cuh"
 
 namespace gdn {
 namespace ssm {
 
 constexpr int kSteps = 8;    // tokens staged at a time
-constexpr int kRows = 64;    // state rows per CTA
+constexpr int kRows = 32;    // state rows per CTA
 
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
 // z / (1 + e^-z)
@@ -74,15 +76,32 @@ __global__ void __launch_bounds__(kRows / 2 * TPR, 768 / (kRows / 2 * TPR)) ssm_
                 const int row = r * RPP + rw;
                 const float x = xs[k][row], add = dt * x;
                 float y = 0.f;
+                attn::f32x2 yy = attn::pair(0.f, 0.f);
 #pragma unroll
                 for (int m = 0; m < NV; ++m) {
-                    const float4 b = Bs[k][lr + TPR * m];
+                    const float4 b = Bs[k][lr + TPR * m], c = Cs[k][lr + TPR * m];
                     float4& v = s[r][m];
-                    v.x = fmaf(keep, v.x, add * b.x);
-                    v.y = fmaf(keep, v.y, add * b.y);
-                    v.z = fmaf(keep, v.z, add * b.z);
-                    v.w = fmaf(keep, v.w, add * b.w);
-                    y += dot4(v, Cs[k][lr + TPR * m]);
+                    if constexpr (ONE) {
+                        v.x = fmaf(keep, v.x, add * b.x);
+                        v.y = fmaf(keep, v.y, add * b.y);
+                        v.z = fmaf(keep, v.z, add * b.z);
+                        v.w = fmaf(keep, v.w, add * b.w);
+                        y += dot4(v, c);
+                    } else {  // in pairs: the arithmetic of several tokens counts
+                        const attn::f32x2 kk = attn::pair(keep, keep), aa = attn::pair(add, add);
+                        const attn::f32x2 p = attn::fma2(kk, attn::pair(v.x, v.y), attn::mul2(aa, attn::pair(b.x, b.y)));
+                        const attn::f32x2 q = attn::fma2(kk, attn::pair(v.z, v.w), attn::mul2(aa, attn::pair(b.z, b.w)));
+                        yy = attn::fma2(p, attn::pair(c.x, c.y), attn::fma2(q, attn::pair(c.z, c.w), yy));
+                        float f[4];
+                        attn::unpair(p, f);
+                        attn::unpair(q, f + 2);
+                        v = make_float4(f[0], f[1], f[2], f[3]);
+                    }
+                }
+                if constexpr (!ONE) {
+                    float f[2];
+                    attn::unpair(yy, f);
+                    y = f[0] + f[1];
                 }
                 y = fmaf(D, x, group_sum<TPR>(y));
                 if (lr == 0) {
