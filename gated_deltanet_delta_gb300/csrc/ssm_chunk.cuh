@@ -68,7 +68,7 @@ struct ChunkCfg {
 
 // Barriers, two of each for the chunks in turn.
 enum : int {
-    CK_X = 0, CK_BC, CK_XE, CK_G, CK_CS, CK_UPH, CK_UPD, CK_MX0, CK_MX1, CK_V, CK_S, CK_XH, CK_XL, CK_Y0, CK_Y1, CK_YF, CK_O, CK_Z, CK_ZE, CK_DRAIN, CK_N
+    CK_X = 0, CK_BC, CK_XE, CK_G, CK_CS, CK_UPH, CK_UPD, CK_MX0, CK_MX1, CK_V, CK_S, CK_XH, CK_XL, CK_M, CK_YF, CK_O, CK_Z, CK_ZE, CK_DRAIN, CK_N
 };
 
 struct Unit {
@@ -170,9 +170,9 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
         for (int i = 0; i < 2 * CK_N; ++i) {
             const int id = i / 2;
             // B and C arrive one after the other; at the others but for the copies' and products' arrive warps
-            const int count = id == CK_BC ? 2 : id == CK_YF || id == CK_O || id == CK_XE || (P == 128 && id == CK_Y0) ? 16
+            const int count = id == CK_BC ? 2 : id == CK_YF || id == CK_O || id == CK_XE || id == CK_M ? 16
                               : id == CK_V ? (P == 64 ? 8 : 4)
-                              : id == CK_XH || id == CK_S || id == CK_XL || id == CK_Y0 || id == CK_Y1 ? 8 : 1;
+                              : id == CK_XH || id == CK_S || id == CK_XL ? 8 : 1;
             tc::mbar_init(&bars[i], count);
         }
         most_polls = a.polls;
@@ -262,41 +262,31 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                 tc::commit(&bars[2 * CK_G + (c & 1)]);
                 return true;
             };
-            bool ok = pairs(0);
+            bool ok = true;
             for (int c = 0; c < u.chunks && ok; ++c) {
                 const uint64_t off = c % NCB * (K::CB >> 4), xoff = (c & 1) * (K::X >> 4);
-                ok = (c == 0 || one_wait(CK_YF, c - 1)) && one_wait(CK_S, c);
+                ok = (c == 0 || one_wait(CK_YF, c - 1)) && pairs(c) && one_wait(CK_S, c);
                 if (!ok) break;
 #pragma unroll 1
                 for (uint32_t q = 0; q < S / 64; ++q)
 #pragma unroll
                     for (uint32_t k = 0; k < 4; ++k) tc::mma_bf16(tm + K::TM_Y, dC + off + q * 1024 + 2 * k, dS + q * 1024 + 2 * k, ID_G, q + k > 0);
                 tc::commit(&bars[2 * CK_CS + (c & 1)]);
-                if constexpr (P == 64) {
-#pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        ok = ok && one_wait(CK_Y0 + h, c);
-                        if (!ok) break;
-                        if (h < heads) {
-#pragma unroll 1
-                            for (uint32_t q = 0; q < 2; ++q)
-#pragma unroll
-                                for (uint32_t k = 4 * q, i = 0; i < 4; ++k, ++i)
-                                    tc::mma_bf16_ts(tm + K::TM_Y + 64 * h, tm + K::TM_M + 64 * h + 8 * k, dX + xoff + h * 1024 + k * 128, ID_MX, 1);
-                        }
-                        tc::commit(&bars[2 * (CK_MX0 + h) + (c & 1)]);
-                    }
-                } else {
-                    ok = one_wait(CK_Y0, c);
-                    if (!ok) break;
-#pragma unroll 1
-                    for (uint32_t q = 0; q < 2; ++q)
-#pragma unroll
-                        for (uint32_t k = 4 * q, i = 0; i < 4; ++k, ++i) tc::mma_bf16_ts(tm + K::TM_Y, tm + K::TM_M + 8 * k, dX + xoff + k * 128, ID_MX, 1);
-                    tc::commit(&bars[2 * CK_MX0 + (c & 1)]);
-                }
+                ok = one_wait(CK_M, c);
                 if (!ok) break;
-                if (c + 1 < u.chunks) ok = pairs(c + 1);
+                // M X in the place of G, which all have read
+                constexpr int HEADS = 128 / P;
+#pragma unroll 1
+                for (int h = 0; h < HEADS; ++h) {
+                    if (h < heads) {
+#pragma unroll 1
+                        for (uint32_t q = 0; q < 2; ++q)
+#pragma unroll
+                            for (uint32_t k = 4 * q, i = 0; i < 4; ++k, ++i)
+                                tc::mma_bf16_ts(tm + K::TM_G + 64 * h, tm + K::TM_M + 64 * h + 8 * k, dX + xoff + h * 1024 + k * 128, ID_MX, k > 0);
+                    }
+                    tc::commit(&bars[2 * (CK_MX0 + h) + (c & 1)]);
+                }
             }
             // nothing of this CTA's may be in flight when it ends, its barriers' arrivals included
             tc::commit(&bars[2 * CK_DRAIN]);
@@ -369,7 +359,7 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
             if (P == 64) return isb ? j <= w - 2 : j >= w - 1;
             return j == w - wg;
         };
-        const uint32_t tM = trow + K::TM_M + (P == 64 ? side * 64 : 0), tY = trow + K::TM_Y + side * 64 + (wg >> 1) * 32;
+        const uint32_t tM = trow + K::TM_M + (P == 64 ? side * 64 : 0), tY = side * 64 + (wg >> 1) * 32;
         auto weights = [&](int c) -> bool {
             const float* V = vec(c, hh);
             const float pre = V[t];
@@ -420,27 +410,6 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
             }
             return true;
         };
-        auto scale_y = [&](int c) {
-            const float* V = vec(c, hh);
-            float sum = V[t];  // the decay from the chunk's start
-            for (int j = 0; j < w; ++j) sum += V[3 * kChunk + j];
-            const float from = ex2(sum);
-            const attn::f32x2 ff = attn::pair(from, from);
-            float y0[16], y1[16];
-            tc::ld16(tY, y0);
-            tc::ld16(tY + 16, y1);
-            tc::wait_ld();
-#pragma unroll
-            for (int q = 0; q < 16; q += 2) {
-                attn::unpair(attn::mul2(attn::pair(y0[q], y0[q + 1]), ff), y0 + q);
-                attn::unpair(attn::mul2(attn::pair(y1[q], y1[q + 1]), ff), y1 + q);
-            }
-            tc::st16(tY, y0);
-            tc::st16(tY + 16, y1);
-            tc::wait_st();
-            tc::fence_before();
-            warp_arrive(P == 64 ? CK_Y0 + side : CK_Y0, c);
-        };
         const long long col = static_cast<long long>(h0) * P + side * 64;  // the first feature of this half of the tile
         const uint32_t line = static_cast<uint32_t>(side * 16384 + t * 128);  // this row of that half
         // The gate comes by TMA and a whole chunk goes out by TMA, from the same place, but for the first block of rows: a thread's own
@@ -470,12 +439,16 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
             }
             const uint32_t at = sb + K::OFF_X + (c & 1) * K::X + line;
             const int t7 = anew(t) & 7;
-            const float D = head_s[hh][2];
-            const attn::f32x2 dd = attn::pair(D, D);
+            const float* V = vec(c, hh);
+            float sum = V[t];  // the decay from the chunk's start
+            for (int j = 0; j < w; ++j) sum += V[3 * kChunk + j];
+            const float D = head_s[hh][2], from = ex2(sum);
+            const attn::f32x2 dd = attn::pair(D, D), ff = attn::pair(from, from);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float y[16];
-                tc::ld16(tY + 16 * i, y);
+                float s[16], y[16];
+                tc::ld16(trow + K::TM_Y + tY + 16 * i, s);
+                tc::ld16(trow + K::TM_G + tY + 16 * i, y);
                 tc::wait_ld();
                 if (i == 1) {
                     tc::fence_before();
@@ -488,7 +461,8 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                     uint32_t r[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        attn::f32x2 o = attn::fma2(attn::widen2(xs[k]), dd, attn::pair(y[8 * q + 2 * k], y[8 * q + 2 * k + 1]));
+                        const int j = 8 * q + 2 * k;
+                        attn::f32x2 o = attn::fma2(attn::widen2(xs[k]), dd, attn::fma2(ff, attn::pair(s[j], s[j + 1]), attn::pair(y[j], y[j + 1])));
                         if (a.z) o = attn::mul2(o, attn::silu2(attn::widen2(zs[k])));
                         float f[2];
                         attn::unpair(o, f);
@@ -667,16 +641,20 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
             if (c >= 0) {
                 ok = (isb || warp_wait(CK_V, c)) && weights(c);
                 if (!ok) break;
-                ok = warp_wait(CK_CS, c);
-                if (!ok) break;
-                if (isb && sums && c + 1 < u.chunks) decays(c + 1);
-                if (isb) {  // the state's copy has been read: its place is X's low parts' now
-                    ok = warp_wait(CK_X, c) && warp_wait(CK_XH, c);
+                tc::wait_st();
+                tc::fence_before();
+                warp_arrive(CK_M, c);
+                // The sums of c + 1 go where those of c - 1 were: what is waited for here (B) or for the weights (A) stands behind the last
+                // reading of those, in the output of c - 1.
+                if (isb) {  // once the state's copy has been read its place is X's low parts'
+                    ok = warp_wait(CK_CS, c) && warp_wait(CK_X, c);
+                    if (!ok) break;
+                    if (sums && c + 1 < u.chunks) decays(c + 1);
+                    ok = warp_wait(CK_XH, c);
                     if (!ok) break;
                     weigh(c, weight, false, K::OFF_SX);
                     warp_arrive(CK_XL, c);
                 }
-                scale_y(c);
                 if (!isb && sums && c + 1 < u.chunks) decays(c + 1);
             }
             if (c + 1 < u.chunks) {
