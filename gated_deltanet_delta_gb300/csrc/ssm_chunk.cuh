@@ -4,10 +4,10 @@
 //     y_t = sum_s (C_t . B_s) e^(a_(s+1) + .. + a_t) dt_s x_s + e^(a_1 + .. + a_t) C_t S^T + D x_t,
 //     S' = e^(a_1 + .. + a_Q) S + sum_s e^(a_(s+1) + .. + a_Q) dt_s x_s (x) B_s.
 // A CTA has 128 features of one segment of a sequence (two heads of 64 that share B and C, or one of 128) and walks its chunks:
-//     G = C B^T (128 x 128 x N),  Y = C S^T (128 x 128 x N),  Y = e^(..) Y + M X (128 x 64 x 128 per head of 64),
+//     G = C B^T (128 x 128 x N),  Y = C S^T (128 x 128 x N),  M X (128 x 64 x 128 per head of 64),
 //     S = e^(..) S + X'^T B (128 x N x 128, twice),
-// M = G with the weights of its pairs and X' = the rows of x with theirs, made by threads.  S, G, M and Y fill TMEM (512 columns for
-// N = 128); tiles of x, B and C come by TMA.
+// M = G with the weights of its pairs and X' = the rows of x with theirs, made by threads, which also join the output, e^(..) Y + M X + D x.
+// S, G, M and Y fill TMEM (512 columns for N = 128; M X takes G's place); tiles of x, B and C come by TMA.
 //
 // No decay is the exponential of a difference of running sums, which would lose as many bits as the sum has: the sums run
 // over blocks of 32 tokens, and a pair of tokens in two blocks has the product of two factors, the one of the row and
@@ -21,9 +21,10 @@
 // low parts and the state between two chunks; the output (D, the gate) is shared, 32 features each, and the decays' sums are made by
 // the warps that have the least of M.  Warp 16 loads x, B and C, a lane of warp 17 issues what the outputs are made of and one of warp
 // 18 the state's update, and warp 19 loads the gate and stores the output.  Per chunk c
-//     A: M, Y scaled | X' high of c + 1 | output        B: M, X' low, Y scaled | state of c + 1 | output.
-// Measured: four prompts of up to 8192 tokens, 64 heads of 64, N = 128, gated: 343 us, 5.3 us per chunk of the longest chain; one of
-// 16384 tokens, 32 heads of 128, N = 64: 228 us, 486 without segments (3.8 us a chunk with 32 SMs at work).  What bounds it: all sixteen warps
+//     A: M | X' high of c + 1 | output        B: M, X' low | state of c + 1 | output.
+// (B's output ahead of the state: 2 to 4 % less without a gate, 4 % more with one, whose rows come late in the place of the output.)
+// Measured: four prompts of up to 8192 tokens, 64 heads of 64, N = 128, gated: 337 us, 5.2 us per chunk of the longest chain; one of
+// 16384 tokens, 32 heads of 128, N = 64: 230 us, 486 without segments (3.8 us a chunk with 32 SMs at work).  What bounds it: all sixteen warps
 // are busy nearly all of a chunk and issue in two of five cycles, four warps per scheduler, the rest is the latency of their
 // instructions and the hand-overs.  HBM would take 104 and 42 us, the tensor core 1.6 us a chunk.
 //
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
         const bool valid = hh < heads;
         const int h = h0 + (valid ? hh : 0);
 
-        // ---- what all do: the weights of pairs in M, the scaling of Y, the output
+        // ---- what all do: the weights of pairs in M, the output
         // blocks of 32 columns of M: an A warp has the diagonal one (and the one ahead of it), a B warp those further ahead
         auto mine = [&](int j) {
             if (P == 64) return isb ? j <= w - 2 : j >= w - 1;
