@@ -859,8 +859,15 @@ extern "C" gdn_status attn_cache_append(const void* q, const void* k, const void
     const size_t rb = static_cast<size_t>(max_positions) * rotary_dim * 4;
     // q_out may be q itself; then its rows may stand among the rows of k and v, as those of a fused projection do
     const bool in_place = Hq > 0 && q_out == q && q_out_stride == q_stride;
-    REQUIRE(in_place || (!any_overlap(q_out, ob, q, qb) && !any_overlap(q_out, ob, k, kb) && !any_overlap(q_out, ob, v, vb)),
-            GDN_ERR_INVALID_ARG, "%s: q_out overlaps a source (it may be q itself, with the same stride)", fn);
+    auto apart = [&](const void* p, size_t bytes, int64_t stride) {
+        if (!any_overlap(q_out, ob, p, bytes)) return true;
+        if (!in_place || stride != q_stride) return false;
+        const long long d = (static_cast<long long>(reinterpret_cast<uintptr_t>(p)) - static_cast<long long>(reinterpret_cast<uintptr_t>(q))) / 2 % q_stride;
+        const long long behind = d < 0 ? d + q_stride : d;
+        return behind >= qrow && behind + row <= q_stride;
+    };
+    REQUIRE((in_place || !any_overlap(q_out, ob, q, qb)) && apart(k, kb, k_stride) && apart(v, vb, v_stride), GDN_ERR_INVALID_ARG,
+            "%s: q_out overlaps a source (it may be q itself, with the same stride)", fn);
     REQUIRE(!any_overlap(q_out, ob, rotation, rb) && !any_overlap(k_cache, cb, rotation, rb) && !any_overlap(v_cache, cb, rotation, rb),
             GDN_ERR_INVALID_ARG, "%s: rotation overlaps an output", fn);
     const size_t sb = k_scale ? static_cast<size_t>(num_pages) * Hkv * page_size * 4 : 0;

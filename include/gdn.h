@@ -514,7 +514,8 @@ gdn_status draft_verify(const float* target_p, const float* draft_p, const int64
  *   positions  int64 [T]; one outside the table sets GDN_STATUS_BAD_POSITION, and nothing of its token is written
  *   slots      int64 [T], as attn_cache_write's: a negative slot leaves the token out of the cache (its query is rotated);
  *              one outside it sets GDN_STATUS_BAD_CACHE_INDEX, likewise
- *   q_out      [T, Hq, D] of dtype, token t q_out_stride elements after token t - 1; may be q itself (with the same stride)
+ *   q_out      [T, Hq, D] of dtype, token t q_out_stride elements after token t - 1; may be q itself (with the same stride); keys
+ *              and values may then stand beside the queries in the same rows
  * Slots are distinct, as attn_cache_write's.
  * Supported: D in {64, 128, 256}, rotary_dim a multiple of 16, 16 .. D, Hq, Hkv <= 65535, and in all
  * (T / 8 + 1) ((Hq + 2 Hkv) / 4 + 3) < 2^31.

@@ -31,6 +31,17 @@ APPEND = dict(q=at(0), k=at(1), v=at(2), qs=1024, ks=256, vs=256, dt=BF16, rot=a
               qo=at(6), qos=1024, kc=at(7), vc=at(8), ksc=N, vsc=N, cdt=BF16, pages=10, page=16, hq=8, h=2, D=128, st=at(9))
 
 
+@pytest.mark.parametrize("kw,want", [
+    (dict(k=at(0), ks=1024), INVALID), (dict(k=at(0, 512), ks=1024), INVALID), (dict(k=at(0, 2 * 1024), ks=1536), INVALID),
+    (dict(v=at(0, 2 * 1400), vs=1536, qs=1536, qos=1536), INVALID), (dict(k=at(0, 2 * 1024), ks=1536, qs=1536, qos=1536, T=0), OK),
+])
+def test_append_in_place_refuses_rows_that_overlap(lib, kw, want):
+    """q_out is q: the keys and values may stand behind the queries in the same rows, not among them."""
+    assert call(lib.attn_cache_append, APPEND, APPEND, dict(kw, qo=at(0))) == want
+    if want != OK:
+        assert "overlap" in gdn.last_error()
+
+
 @pytest.mark.parametrize("kw,want,word", [
     (dict(D=96), UNSUPPORTED, "64, 128 or 256"), (dict(R=8), UNSUPPORTED, "rotary_dim"), (dict(R=144), UNSUPPORTED, "rotary_dim"),
     (dict(R=24), UNSUPPORTED, "rotary_dim"), (dict(dt=F32), INVALID, "dtype"), (dict(cdt=F16), INVALID, "cache_dtype"), (dict(cdt=E4M3), INVALID, "k_scale"),
