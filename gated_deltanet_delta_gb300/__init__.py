@@ -729,14 +729,15 @@ def attn_cache_append(q, k, v, rotation, positions, slots, k_cache, v_cache, k_s
 def _row_stride(t, name: str, dtype, shape):
     """A [T, C] tensor whose rows may stand apart; returns the distance between them."""
     torch = _torch_module or _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.shape == shape):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     T, C = shape
     if T == 0:
         return C
@@ -773,20 +774,18 @@ def short_conv(x, weight, hist_pool, cache_indices, cu_seqlens=None, bias=None, 
     _want(cache_indices, "cache_indices", torch.int64, (N,))
     if cu_seqlens is not None:
         _want(cu_seqlens, "cu_seqlens", torch.int64, (N + 1,))
-    widths = [C] if splits is None else list(splits)
+    widths = [C] if splits is None else splits
     if not 1 <= len(widths) <= 3 or sum(widths) != C or min(widths) < 1:
         raise ValueError(f"splits must be one to three widths that add up to {C}, got {widths}")
     if outs is None:
-        outs = tuple([torch.empty((T, w), dtype=dtype, device=device) for w in widths])
+        outs = [torch.empty((T, w), dtype=dtype, device=device) for w in widths]
     elif len(outs) != len(widths):
         raise ValueError(f"{len(widths)} outs wanted, got {len(outs)}")
     else:
         for i, w in enumerate(widths):
             _want(outs[i], f"outs[{i}]", dtype, (T, w))
     dev_status = _want_status(dev_status, device)
-    parts = []
-    for i in range(3):
-        parts += [outs[i].data_ptr(), widths[i]] if i < len(widths) else [None, 0]
+    parts = [p for o, w in zip(outs, widths) for p in (o.data_ptr(), w)] + [None, 0] * (3 - len(widths))
     _check(load().short_conv(x.data_ptr(), stride, code, weight.data_ptr(), _ptr(bias), hist_pool.data_ptr(), hist_pool.shape[0],
                              cache_indices.data_ptr(), _ptr(cu_seqlens), N, T, C, taps, int(silu), *parts, dev_status.data_ptr(),
                              _stream(device)), "short_conv")
