@@ -26,7 +26,7 @@
 //     A: M | X' high of c + 1 | output        B: M, X' low | state of c + 1 | output.
 // (B's output ahead of the state: 2 to 4 % less without a gate, 4 % more with one, whose rows come late in the place of the output.)
 // Measured: four prompts of up to 8192 tokens, 64 heads of 64, N = 128, gated: 337 us, 5.2 us per chunk of the longest chain; one of
-// 16384 tokens, 32 heads of 128, N = 64: 230 us, 486 without segments (3.8 us a chunk with 32 SMs at work).  What bounds it: all sixteen warps
+// 16384 tokens, 32 heads of 128, N = 64: 227 us, 486 without segments (3.8 us a chunk with 32 SMs at work).  What bounds it: all sixteen warps
 // are busy nearly all of a chunk and issue in two of five cycles, four warps per scheduler, the rest is the latency of their
 // instructions and the hand-overs.  HBM would take 104 and 42 us, the tensor core 1.6 us a chunk.
 //
@@ -91,6 +91,17 @@ __device__ __forceinline__ void tma_store_2d(const void* map, int x, int y, uint
 __device__ __forceinline__ void st8(uint32_t taddr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
                  "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// Eight floats at once, 32-byte aligned: a lane has a row of the state to itself, so that an instruction touches 32 lines whatever its width.
+__device__ __forceinline__ void ld_state(const float* p, float* v) {
+    asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "l"(p));
+}
+__device__ __forceinline__ void st_state(float* p, const float* v) {
+    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]),
+                 "f"(v[6]), "f"(v[7])
                  : "memory");
 }
 // x, which the compiler does not know to be the same from chunk to chunk: what depends on it is computed where it is used, and does
@@ -495,18 +506,24 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
             const float* src = (u.parts == 1 ? a.state + u.slot * state() : a.ws + u.ws * state()) + srow();
             float s[S / 2];
 #pragma unroll
-            for (int q = 0; q < S / 2; q += 4) {
-                const float4 v = there && u.k == 0 ? *reinterpret_cast<const float4*>(src + q) : make_float4(0.f, 0.f, 0.f, 0.f);
-                s[q] = v.x, s[q + 1] = v.y, s[q + 2] = v.z, s[q + 3] = v.w;
+            for (int q = 0; q < S / 2; q += 8) {
+                if (there && u.k == 0) {
+                    ld_state(src + q, s + q);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s[q + i] = 0.f;
+                }
             }
             for (int j = 0; j < u.k && there; ++j) {
                 const long long at = u.ws + 1 + j;
                 const float f = ex2(a.ws_decay[at * a.H + h0 + ph]);
                 const float* from = a.ws + at * state() + srow();
 #pragma unroll
-                for (int q = 0; q < S / 2; q += 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(from + q);
-                    s[q] = fmaf(f, s[q], v.x), s[q + 1] = fmaf(f, s[q + 1], v.y), s[q + 2] = fmaf(f, s[q + 2], v.z), s[q + 3] = fmaf(f, s[q + 3], v.w);
+                for (int q = 0; q < S / 2; q += 8) {
+                    float v[8];
+                    ld_state(from + q, v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s[q + i] = fmaf(f, s[q + i], v[i]);
                 }
             }
             __syncwarp();
@@ -674,9 +691,7 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                 float v[16];
                 tc::ld16(trow + K::TM_S + side * (S / 2) + 16 * i, v);
                 tc::wait_ld();
-                if (there)
-#pragma unroll
-                    for (int q = 0; q < 16; q += 4) *reinterpret_cast<float4*>(dst + 16 * i + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+                if (there) st_state(dst + 16 * i, v), st_state(dst + 16 * i + 8, v + 8);
                 __syncwarp();
             }
         }
@@ -877,15 +892,17 @@ __global__ void __launch_bounds__(kAheadNT, 1) ssm_ahead_kernel(const __grid_con
                 if (there) {
                     if (u.k == 0) {  // the pool's state, copied too: the last segment may have replaced it when the first one starts
 #pragma unroll
-                        for (int q = 0; q < 16; q += 4) {
-                            const float4 x = *reinterpret_cast<const float4*>(a.state + u.slot * state + row + 16 * i + q);
-                            *reinterpret_cast<float4*>(a.ws + u.ws * state + row + 16 * i + q) = x;
-                            v[q] = fmaf(x.x, f, v[q]), v[q + 1] = fmaf(x.y, f, v[q + 1]), v[q + 2] = fmaf(x.z, f, v[q + 2]), v[q + 3] = fmaf(x.w, f, v[q + 3]);
+                        for (int q = 0; q < 16; q += 8) {
+                            float x[8];
+                            ld_state(a.state + u.slot * state + row + 16 * i + q, x);
+                            st_state(a.ws + u.ws * state + row + 16 * i + q, x);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) v[q + k] = fmaf(x[k], f, v[q + k]);
                         }
                     }
                     float* dst = a.ws + (u.ws + 1 + u.k) * state + row + 16 * i;
-#pragma unroll
-                    for (int q = 0; q < 16; q += 4) *reinterpret_cast<float4*>(dst + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+                    st_state(dst, v);
+                    st_state(dst + 8, v + 8);
                 }
                 __syncwarp();
             }

@@ -112,7 +112,7 @@ def test_step_refuses(lib, kw, want, word):
 
 @pytest.mark.parametrize("kw,want,word", BOTH + [
     (dict(T=-1), INVALID, "sizes"), (dict(T=1 << 31), UNSUPPORTED, "2^31"), (dict(cu=N), INVALID, "cu_seqlens"), (dict(max_len=-1), INVALID, "max_len"),
-    (dict(ws=at(13, 8)), INVALID, "aligned"),
+    (dict(ws=at(13, 8)), INVALID, "aligned"), (dict(ws=at(13, 16)), INVALID, "32-byte"), (dict(state=at(8, 16)), INVALID, "32-byte"),
 ])
 def test_prefill_refuses(lib, kw, want, word):
     assert call(lib.ssm_prefill_chunked, SCAN, SCAN_ORDER, kw) == want
