@@ -34,7 +34,8 @@
 // cut into segments that run side by side: a launch ahead (ssm_ahead_kernel) forms the states that all segments but the last end in
 // from a zero state (the first from the pool's), and a segment starts from the sum of those ahead of it with their decays.
 //
-// Every wait is bounded (attn_tiles.cuh): one that runs out sets GDN_STATUS_TIMEOUT and the CTA's limit of polls to 0.
+// Every wait is bounded (attn_tiles.cuh): one that runs out sets GDN_STATUS_TIMEOUT and the CTA's limit of polls to 0.  A CTA that gave
+// up ends behind one more bounded wait for each product and copy that it has in flight.
 #pragma once
 
 #include "attn_mma.cuh"
@@ -230,8 +231,11 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
     auto vec = [&](int c, int hh) { return reinterpret_cast<float*>(sm + K::OFF_V) + ((c & 1) * 2 + hh) * K::VEC; };
     const uint32_t trow = tm + (static_cast<uint32_t>((warp & 3) * 32) << 16);
 
+    auto all_left = [] { asm volatile("bar.sync 1, 640;" ::: "memory"); };  // every role has left its loop
+
     if (warp >= 16) {
         attn::regs_down<kRegsIssue>();  // by the whole warpgroup, then its warps part
+        int nx = 0, nbc = 0, nz = 0;    // loads that this lane has issued: chunks of x, tiles of C and B in turn, chunks of the gate
         if (warp == 16 && attn::elect()) {
             // -------------------------------------------------------- loader
             bool ok = true;
@@ -243,18 +247,21 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                 const int halves = heads * P / 64;
                 tc::mbar_expect_tx(bar, halves * 16384);
                 for (int i = 0; i < halves; ++i) attn::tma_load_2d(sb + K::OFF_X + (c & 1) * K::X + i * 16384, &maps.x, h0 * P + 64 * i, row, bar);
+                ++nx;
                 if (c >= NCB) ok = wait(CK_CS, c - NCB);
                 if (!ok) break;
                 bar = &bars[2 * CK_BC + (c & 1)];
                 tc::mbar_expect_tx(bar, K::CB);
 #pragma unroll
                 for (int i = 0; i < S / 64; ++i) attn::tma_load_2d(sb + K::OFF_C + c % NCB * K::CB + i * 16384, &maps.C, g * S + 64 * i, row, bar);
+                ++nbc;
                 if (c >= NCB) ok = wait(CK_UPD, c - NCB);
                 if (!ok) break;
                 bar = &bars[2 * CK_BC + (c & 1)];
                 tc::mbar_expect_tx(bar, K::CB);
 #pragma unroll
                 for (int i = 0; i < S / 64; ++i) attn::tma_load_2d(sb + K::OFF_B + c % NCB * K::CB + i * 16384, &maps.B, g * S + 64 * i, row, bar);
+                ++nbc;
             }
         }
         // The products' loops are unrolled by four only: unrolled in full, their descriptors, which are the same from chunk to chunk,
@@ -315,6 +322,7 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                 for (int i = 0; i < halves; ++i)
                     for (int j = 0; j < 3; ++j)
                         attn::tma_load_2d(sb + K::OFF_Z + (3 * i + j) * K::ZBOX, &maps.z, h0 * P + 64 * i, static_cast<int>(u.begin) + c * kChunk + 32 + 32 * j, bar);
+                ++nz;
             };
             bool ok = true;
             if (a.z) gate(0);
@@ -357,6 +365,17 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
             }
             tc::commit(&bars[2 * CK_DRAIN + 1]);
             tc::mbar_wait(&bars[2 * CK_DRAIN + 1], 0, kPolls);
+        }
+        __syncwarp();
+        all_left();
+        if (most_polls == 0) {  // gave up: the copies that nobody waited for land before the CTA ends
+            auto land = [&](int id, int n) {
+                for (int c = max(n - 2, 0); c < n; ++c) tc::mbar_wait(&bars[2 * id + (c & 1)], c >> 1 & 1, kPolls);
+            };
+            if (nbc & 1) tc::mbar_arrive(&bars[2 * CK_BC + (nbc >> 1 & 1)]);  // in the place of the last C's B, which nobody expects any more
+            land(CK_X, nx);
+            land(CK_BC, (nbc + 1) / 2);
+            land(CK_Z, nz);
         }
     } else {
         // ------------------------------------------------------------ workers: warpgroups 0, 1 (A) and 2, 3 (B)
@@ -695,15 +714,14 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                 __syncwarp();
             }
         }
+        __syncwarp();
+        all_left();
     }
     __syncwarp();
     tc::fence_before();
     __syncthreads();
     if (warp == 17) tc::tmem_dealloc(tm, 512);
-    if (tid == 0 && most_polls == 0) {  // gave up: leave what copies are in flight (microseconds) a millisecond
-        for (int i = 0; i < 100; ++i) __nanosleep(10000);
-        atomicOr(a.status, kStatusTimeout);
-    }
+    if (tid == 0 && most_polls == 0) atomicOr(a.status, kStatusTimeout);
 }
 
 // The states that the segments ahead end in, each from a zero state (the first of a sequence from the pool's, of which it also leaves a
@@ -761,7 +779,8 @@ __global__ void __launch_bounds__(kAheadNT, 1) ssm_ahead_kernel(const __grid_con
     if (warp == 16) {
         // ------------------------------------------------------------ loader
         if (lane == 0) {
-            for (int i = 0; i < u.chunks; ++i) {
+            int i = 0;
+            for (; i < u.chunks; ++i) {
                 if (i >= 2 && !wait(done, i - 2)) break;
                 const int row = static_cast<int>(u.begin) + (u.chunks - 1 - i) * kChunk, halves = heads * P / 64;
                 const uint32_t to = sb + (i & 1) * K::STAGE;
@@ -770,6 +789,7 @@ __global__ void __launch_bounds__(kAheadNT, 1) ssm_ahead_kernel(const __grid_con
 #pragma unroll
                 for (int j = 0; j < S / 64; ++j) attn::tma_load_2d(to + 2 * K::X + j * 16384, &maps.B, g * S + 64 * j, row, &full[i & 1]);
             }
+            for (int j = max(i - 2, 0); j < i; ++j) tc::mbar_wait(&full[j & 1], j >> 1 & 1, kPolls);  // where others gave up nobody else does
         }
     } else if (warp == 17) {
         // ------------------------------------------------------------ MMA issue
@@ -912,10 +932,7 @@ __global__ void __launch_bounds__(kAheadNT, 1) ssm_ahead_kernel(const __grid_con
     tc::fence_before();
     __syncthreads();
     if (warp == 17) tc::tmem_dealloc(tm, 128);
-    if (tid == 0 && most_polls == 0) {  // gave up: leave what copies are in flight (microseconds) a millisecond
-        for (int i = 0; i < 100; ++i) __nanosleep(10000);
-        atomicOr(a.status, kStatusTimeout);
-    }
+    if (tid == 0 && most_polls == 0) atomicOr(a.status, kStatusTimeout);
 }
 
 }  // namespace ssm
