@@ -957,6 +957,7 @@ extern "C" gdn_status short_conv(const void* x, int64_t x_stride, gdn_dtype dtyp
     a.num_seqs = num_seqs;
     a.pool_size = pool_size;
     a.silu = silu != 0;
+    a.polls = g_prefill_wait_polls.load(std::memory_order_relaxed);
     const cudaError_t e = gdn::launch_conv(a, taps, dtype == GDN_F16, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
     return launched(fn);

@@ -42,7 +42,8 @@ cudaError_t run_taps(const ConvArgs& a, bool f16, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_conv(const ConvArgs& a, int taps, bool f16, cudaStream_t stream) {
+cudaError_t launch_conv(ConvArgs a, int taps, bool f16, cudaStream_t stream) {
+    if (a.polls == 0 || a.polls > conv::kWaitPolls) a.polls = conv::kWaitPolls;
     if (taps == 2) return run_taps<2>(a, f16, stream);
     if (taps == 3) return run_taps<3>(a, f16, stream);
     return run_taps<4>(a, f16, stream);

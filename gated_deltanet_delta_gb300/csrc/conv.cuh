@@ -31,7 +31,7 @@ constexpr int kStep = 8;  // tokens in registers, and as many on their way
 constexpr int kTile = 128;
 constexpr int kStages = 3;
 constexpr int kRing = kStages * kStep * kThreads * 16;
-constexpr uint32_t kWaitPolls = 1u << 24;  // the limit of a wait for a copy (seconds)
+constexpr uint32_t kWaitPolls = 1u << 24;  // the built-in limit of a wait for a copy (seconds)
 static_assert(kTile == kThreads, "a thread per token");
 
 // A token's sequence: which, where it begins and ends; n = -1 for a token of no (well-formed) sequence.
@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(const __grid_const
 
 // The same for long calls: 128 tokens per CTA, whose rows come by bulk copies into a ring of kStages steps of eight tokens in shared memory.
 // With the rows in registers there is room for 12 warps with eight loads each on an SM, and 72 % of HBM's rate.  A copy that
-// does not arrive within the limit of a wait (seconds) is done without: the thread reads its rows directly.
+// does not arrive within the limit of a wait is done without: the thread reads its rows directly, and the CTA ends behind one more bounded
+// wait for each copy that is still to come.
 template <int TAPS, bool F16>
 __global__ void __launch_bounds__(kThreads) short_conv_ring_kernel(const __grid_constant__ ConvArgs a) {
     extern __shared__ __align__(128) uint8_t ring[];  // [kStages][kStep][kThreads * 8] elements
@@ -306,10 +307,11 @@ __global__ void __launch_bounds__(kThreads) short_conv_ring_kernel(const __grid_
         ahead_of_tile<TAPS, F16>(a, p, src, c, slot_s[0], ahead_s[0]);
     }
     bool ok = true;
+    int unseen = steps;  // the first step whose copies this thread has not seen arrive
 #pragma unroll 1
     for (int k = 0; k < steps; ++k) {
         const int s = k % kStages, i0 = k * kStep;
-        if (ok) ok = tc::mbar_wait(&full[s], k / kStages & 1, kWaitPolls);
+        if (ok && !tc::mbar_wait(&full[s], k / kStages & 1, a.polls)) ok = false, unseen = k;
         const uint8_t* held = ring + s * STAGE + threadIdx.x * 16;
         auto row = [&](int i) {
             return ok ? *reinterpret_cast<const uint4*>(held + i * ROW) : *reinterpret_cast<const uint4*>(src + (i0 + i) * a.x_stride);
@@ -338,8 +340,8 @@ __global__ void __launch_bounds__(kThreads) short_conv_ring_kernel(const __grid_
         __syncthreads();  // the step's place has been read
         if (threadIdx.x == 0 && ok && k + kStages < steps) issue(k + kStages);
     }
-    if (threadIdx.x == 0 && !ok)  // gave up: leave what copies are in flight (microseconds) a millisecond
-        for (int i = 0; i < 100; ++i) __nanosleep(10000);
+    if (threadIdx.x == 0)  // thread 0 issued no more once it had given up
+        for (int k = unseen; k < min(unseen + kStages, steps); ++k) tc::mbar_wait(&full[k % kStages], k / kStages & 1, kWaitPolls);
 }
 
 // The history behind each sequence's last token, and the report of malformed bounds and slots.

@@ -280,6 +280,7 @@ struct ConvArgs {
     int32_t* status;
     long long T;
     int C, num_seqs, pool_size, silu;
+    uint32_t polls;         // of a barrier, before a wait gives up (0: the built-in limit)
 };
 
 // The selective state space scan.

@@ -52,7 +52,7 @@ void launch_cache_append(const AppendArgs& a, int D, bool f16, bool f8, bool nei
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream);
 
 // taps in 2 .. 4.
-cudaError_t launch_conv(const ConvArgs& a, int taps, bool f16, cudaStream_t stream);
+cudaError_t launch_conv(ConvArgs a, int taps, bool f16, cudaStream_t stream);
 // One token per sequence, or sequences of few tokens each: the recurrence as it stands.  S in {64, 128}.
 void launch_ssm_steps(SsmArgs a, int S, cudaStream_t stream);
 // Sequences of any length; max_len (the longest) only chooses the kernel.

@@ -364,7 +364,8 @@ gdn_status gdn_window_fused(float* state, const float* hist, float* hist_out, co
 /*
  * gdn_prefill_set_wait_limit -- bound every device-side wait of the prefill kernels
  * (gdn_prefill_chunked, _f16, _noalloc and comba_prefill_chunked: the chunk preparation and the
- * chunk recurrence; ssm_prefill_chunked) to `polls` polls of its mbarrier instead of the built-in limits (seconds of
+ * chunk recurrence; ssm_prefill_chunked, and the copies of short_conv, whose wait that runs out sets no status, as the
+ * values are read without them) to `polls` polls of its mbarrier instead of the built-in limits (seconds of
  * waiting).  No page has a counterpart: this is the knob of the failure path.  A wait that runs out
  * sets GDN_STATUS_TIMEOUT in the call's dev_status and its CTA stops after one more bounded wait
  * for the copies and products it has in flight, so the call returns with that status and partial
