@@ -366,9 +366,6 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
             if (!advance<T>(a, p)) break;
         }
         cp_async_wait<0>();
-        if (!ok) {  // gave up: leave what TMA copies are in flight (microseconds) a millisecond
-            for (int i = 0; i < 100; ++i) __nanosleep(10000);
-        }
     } else if (wg == 3) {
         regs_down<kRegsOther>();  // by the whole warpgroup, then its warps part
         if (F8 && (warp == 13 || (C::DUAL && warp == 14))) {
@@ -417,9 +414,6 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
                     }
                 }
                 if (!ok || !advance<T>(a, p)) break;
-            }
-            if (!ok) {  // gave up: leave what TMA copies are in flight (microseconds) a millisecond
-                for (int i = 0; i < 100; ++i) __nanosleep(10000);
             }
         } else if (F8 && warp == 15) {
             // ------------------------------------------------------------ 8 bits: the keys' scales, for the softmax
@@ -848,7 +842,11 @@ __global__ void __launch_bounds__(kTilesNT, 1) attn_tiles_kernel(const __grid_co
     tc::fence_before();
     __syncthreads();
     if (warp == 12) tc::tmem_dealloc(tm, 512);
-    if (tid == 0 && most_polls == 0) atomicOr(a.status, kStatusTimeout);
+    if (tid == 0 && most_polls == 0) {
+        // Gave up: the loaders may have left TMA copies in flight that nobody waits for, those that came to their end among them.
+        tc::let_pass(1000);  // such copies take microseconds
+        atomicOr(a.status, kStatusTimeout);
+    }
 }
 
 }  // namespace attn

@@ -140,6 +140,18 @@ __device__ __forceinline__ bool mbar_sleep_wait(uint64_t* mbar, uint32_t parity,
     return false;
 }
 
+// At least `us` microseconds by the GPU's clock, and at most 2^20 looks at it: for copies in flight that no barrier will tell of.
+// (A sleep alone may take anything from nothing to twice its length.)
+__device__ __forceinline__ void let_pass(uint32_t us) {
+    uint64_t begin, now;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(begin));
+    for (uint32_t i = 0; i < 1u << 20; ++i) {
+        asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
+        if (now - begin >= us * 1000ull) return;
+        __nanosleep(1000);
+    }
+}
+
 // Non-blocking: has the phase with parity `parity` completed?
 __device__ __forceinline__ bool mbar_test(uint64_t* mbar, uint32_t parity) {
     uint32_t done;
