@@ -306,12 +306,13 @@ __global__ void __launch_bounds__(kThreads) short_conv_ring_kernel(const __grid_
         out = out_of(a, c, width) + t0 * width;
         ahead_of_tile<TAPS, F16>(a, p, src, c, slot_s[0], ahead_s[0]);
     }
+    const bool tight = a.polls < kWaitPolls;  // with the limit a variable in every wait: 141 us instead of 139
     bool ok = true;
     int unseen = steps;  // the first step whose copies this thread has not seen arrive
 #pragma unroll 1
     for (int k = 0; k < steps; ++k) {
         const int s = k % kStages, i0 = k * kStep;
-        if (ok && !tc::mbar_wait(&full[s], k / kStages & 1, a.polls)) ok = false, unseen = k;
+        if (ok && !(tight ? tc::mbar_wait(&full[s], k / kStages & 1, a.polls) : tc::mbar_wait(&full[s], k / kStages & 1, kWaitPolls))) ok = false, unseen = k;
         const uint8_t* held = ring + s * STAGE + threadIdx.x * 16;
         auto row = [&](int i) {
             return ok ? *reinterpret_cast<const uint4*>(held + i * ROW) : *reinterpret_cast<const uint4*>(src + (i0 + i) * a.x_stride);
