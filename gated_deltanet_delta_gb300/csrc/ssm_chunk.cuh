@@ -35,7 +35,8 @@
 // from a zero state (the first from the pool's), and a segment starts from the sum of those ahead of it with their decays.
 //
 // Every wait is bounded (attn_tiles.cuh): one that runs out sets GDN_STATUS_TIMEOUT and the CTA's limit of polls to 0.  A CTA that gave
-// up ends behind one more bounded wait for each product and copy that it has in flight.
+// up ends behind one more bounded wait for each product and copy that it has in flight, and leaves the pool's state as it is; one whose
+// segment starts from what another did not come to write gives up too.
 #pragma once
 
 #include "attn_mma.cuh"
@@ -51,6 +52,7 @@ constexpr int kChunkNT = 640;
 constexpr int kWhole = 1 << 24;  // chunks per segment where no sequence is cut
 // registers per thread: the launch's 96 x 5 warpgroups, parted as 104 x 4 for the workers and 64 for those that load and issue
 constexpr int kRegsLaunch = 96, kRegsWork = 104, kRegsIssue = 64;
+constexpr float kNoState = 1.f;        // in the place of a decay's logarithm, which is never positive: the state was not written
 constexpr uint32_t kPolls = 1u << 22;  // the built-in limit of a wait (seconds)
 
 template <int S>
@@ -521,8 +523,12 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
         const bool there = ph < heads;
         auto srow = [&] { return (static_cast<long long>(h0 + (there ? ph : 0)) * P + (P == 64 ? t & 63 : t)) * S + side * (S / 2); };
         auto state = [&] { return static_cast<long long>(a.H) * P * S; };
+        bool ok = true;
         if (isb) {  // the unit's first state: the pool's (for the first of several segments its copy), or what the segments ahead add up to
             const float* src = (u.parts == 1 ? a.state + u.slot * state() : a.ws + u.ws * state()) + srow();
+            // The first segment's copy is there if its own state is.  The same for all of the CTA's heads, which one CTA ahead has.
+            for (int j = 0; j < (u.k == 0 && u.parts > 1 ? 1 : u.k); ++j) ok = ok && a.ws_decay[(u.ws + 1 + j) * a.H + h0] != kNoState;
+            if (!ok) most_polls = 0;
             float s[S / 2];
 #pragma unroll
             for (int q = 0; q < S / 2; q += 8) {
@@ -667,7 +673,6 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
             warp_arrive(CK_S, c);
             return true;
         };
-        bool ok = true;
         if (!isb) {
             for (int j = w + 1; j < 4; ++j) {  // tokens behind the row's: zero, once for all
                 const uint32_t zero[16] = {};
@@ -676,7 +681,7 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
         }
         if (sums) decays(0);
 #pragma unroll 1
-        for (int c = -1; c < u.chunks; ++c) {
+        for (int c = -1; ok && c < u.chunks; ++c) {
             if (c >= 0) {
                 ok = (isb || warp_wait(CK_V, c)) && weights(c);
                 if (!ok) break;
@@ -700,10 +705,11 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                 ok = isb ? begin(c + 1) : high_parts(c + 1);
             }
             if (c >= 0) ok = ok && output(c);
-            if (!ok) break;
         }
-        ok = ok && isb && warp_wait(CK_UPD, u.chunks - 1);
-        if (ok && u.k == u.parts - 1) {
+        if (ok && isb) warp_wait(CK_UPD, u.chunks - 1);
+        __syncwarp();
+        all_left();
+        if (isb && most_polls != 0 && u.k == u.parts - 1) {
             float* dst = a.state + u.slot * state() + srow();
 #pragma unroll 1
             for (int i = 0; i < S / 32; ++i) {
@@ -714,8 +720,6 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                 __syncwarp();
             }
         }
-        __syncwarp();
-        all_left();
     }
     __syncwarp();
     tc::fence_before();
@@ -725,7 +729,7 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
 }
 
 // The states that the segments ahead end in, each from a zero state (the first of a sequence from the pool's, of which it also leaves a
-// copy), and the logarithms of their decays.  A token's weight is its decay to the segment's end, so nothing is carried from chunk to
+// copy), and the logarithms of their decays (kNoState: gave up).  A token's weight is its decay to the segment's end, so nothing is carried from chunk to
 // chunk: the chunks are taken from the last to the first with the sum of the steps behind them, and sixteen warps make X' of one
 // (high parts in x's own tile, low parts beside it) while the products of the one before run.
 template <int S>
@@ -932,7 +936,10 @@ __global__ void __launch_bounds__(kAheadNT, 1) ssm_ahead_kernel(const __grid_con
     tc::fence_before();
     __syncthreads();
     if (warp == 17) tc::tmem_dealloc(tm, 128);
-    if (tid == 0 && most_polls == 0) atomicOr(a.status, kStatusTimeout);
+    if (tid == 0 && most_polls == 0) {
+        for (int i = 0; i < heads; ++i) a.ws_decay[(u.ws + 1 + u.k) * a.H + h0 + i] = kNoState;
+        atomicOr(a.status, kStatusTimeout);
+    }
 }
 
 }  // namespace ssm
