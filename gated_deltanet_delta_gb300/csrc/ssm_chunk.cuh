@@ -9,8 +9,10 @@
 // M = G with the weights of its pairs and X' = the rows of x with theirs, made by threads, which also join the output, e^(..) Y + M X + D x.
 // S, G, M and Y fill TMEM (512 columns for N = 128; M X takes G's place); tiles of x, B and C come by TMA.
 //
-// No decay is the exponential of a difference of running sums, which would lose as many bits as the sum has: the sums run
-// over blocks of 32 tokens, and a pair of tokens in two blocks has the product of two factors, the one of the row and
+// A difference of running sums loses as many bits as the sums have, so they run over blocks of 32 tokens only, in which a pair's decay is the
+// exponential of such a difference, and a step counts as at most 2^-128, which is zero here: a sum is at most 4096, its five levels of additions
+// are off by less than 2^-12 together, and a weight by 2^-11 ln 2 (3.4e-4) where a block is full of such steps, a twelfth of what its
+// rounding to bf16 may take.  A pair of tokens in two blocks has the product of two factors, the one of the row and
 // its block, the other of the column, which also saves the exponentials: one per pair only inside the blocks.
 //
 // The state is an fp32 result and is carried for thousands of chunks, so X' is held in two bf16 parts (2^-16 of each product at most); M and
@@ -107,6 +109,12 @@ __device__ __forceinline__ void st_state(float* p, const float* v) {
                  "f"(v[6]), "f"(v[7])
                  : "memory");
 }
+// A weight of a pair beyond bf16's range becomes its largest number: it may stand for an x of zero.
+__device__ __forceinline__ uint32_t pack_weights(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 // x, which the compiler does not know to be the same from chunk to chunk: what depends on it is computed where it is used, and does
 // not take registers in between (they were spilled, and each reload from memory took some 300 clocks).
 __device__ __forceinline__ int anew(int x) {
@@ -114,6 +122,9 @@ __device__ __forceinline__ int anew(int x) {
     return x;
 }
 __device__ __forceinline__ float ex2(float x) { return attn::fast_exp2(x); }
+// The logarithm (base 2) of a token's decay, for A to that base: not below -128, as ex2 is zero from there on (without the limit one step of
+// thousands takes the digits of its block's other decays, and one that is no longer a number of fp32 makes them NaN); 0 for no token.
+__device__ __forceinline__ float log_decay(float A, float dt) { return dt > 0.f ? fmaxf(A * dt, -128.f) : 0.f; }
 
 // The unit with number `rank`: one warp walks the sequences, twice: segments of a.seg chunks come first, then what is left of the
 // sequences, so that the last to start are the short ones.  Ahead (AHEAD) are all segments but each sequence's last.  A sequence of
@@ -422,12 +433,13 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                             float f[4], e[4];
                             attn::unpair(attn::fma2(attn::pair(p.x, p.y), minus, pp), f);
                             attn::unpair(attn::fma2(attn::pair(p.z, p.w), minus, pp), f + 2);
-                            attn::unpair(attn::mul2(attn::pair(x[i], x[i + 1]), attn::pair(d.x, d.y)), e);
-                            attn::unpair(attn::mul2(attn::pair(x[i + 2], x[i + 3]), attn::pair(d.z, d.w)), e + 2);
+                            // dt times its decay first: times G it may leave the range
+                            attn::unpair(attn::mul2(attn::pair(ex2(f[0]), ex2(f[1])), attn::pair(d.x, d.y)), e);
+                            attn::unpair(attn::mul2(attn::pair(ex2(f[2]), ex2(f[3])), attn::pair(d.z, d.w)), e + 2);
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) x[i + q] = i0 + i + q <= lane ? e[q] * ex2(f[q]) : 0.f;
-                            m[i / 2] = pack_bf16x2(x[i], x[i + 1]);
-                            m[i / 2 + 1] = pack_bf16x2(x[i + 2], x[i + 3]);
+                            for (int q = 0; q < 4; ++q) x[i + q] = i0 + i + q <= lane ? e[q] * x[i + q] : 0.f;
+                            m[i / 2] = pack_weights(x[i], x[i + 1]);
+                            m[i / 2 + 1] = pack_weights(x[i + 2], x[i + 3]);
                         }
                     } else {
 #pragma unroll
@@ -436,8 +448,8 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                             float y[4];
                             attn::unpair(attn::mul2(attn::mul2(attn::pair(f.x, f.y), rr), attn::pair(x[i], x[i + 1])), y);
                             attn::unpair(attn::mul2(attn::mul2(attn::pair(f.z, f.w), rr), attn::pair(x[i + 2], x[i + 3])), y + 2);
-                            m[i / 2] = pack_bf16x2(y[0], y[1]);
-                            m[i / 2 + 1] = pack_bf16x2(y[2], y[3]);
+                            m[i / 2] = pack_weights(y[0], y[1]);
+                            m[i / 2 + 1] = pack_weights(y[2], y[3]);
                         }
                     }
                     st8(tM + 16 * j + i0 / 2, m);
@@ -574,7 +586,7 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
             const int i = block * 32 + lane;
             const float dt = valid && i < u.len - c * kChunk ? softplus(bf16_to_f32(raw) + head_s[hh][1]) : 0.f;
             raw = raw_at(c + 1);
-            const float step = head_s[hh][0] * dt;
+            const float step = log_decay(head_s[hh][0], dt);
             float upto = step, behind = __shfl_down_sync(kFullMask, step, 1);
             if (lane == 31) behind = 0.f;
 #pragma unroll
@@ -837,7 +849,7 @@ __global__ void __launch_bounds__(kAheadNT, 1) ssm_ahead_kernel(const __grid_con
             for (int j = 0; j < BATCH / 2; ++j) {
                 const int b = 8 * j + (warp >> 1);
                 if (b >= blocks) break;
-                const float d = softplus(dt[j] + bias), step = A * d;
+                const float d = softplus(dt[j] + bias), step = log_decay(A, d);
                 float behind = __shfl_down_sync(kFullMask, step, 1);
                 if (lane == 31) behind = 0.f;
 #pragma unroll
