@@ -127,7 +127,7 @@ __device__ __forceinline__ uint4 token(const Weights<TAPS>& w, const Past<TAPS>&
 #pragma unroll
         for (int j = 0; j < TAPS - 1; ++j) y = attn::fma2(w.w[j][i], p.v[j][i], y);
         y = attn::fma2(w.w[TAPS - 1][i], x[i], y);
-        if (silu) y = attn::silu2(y);
+        if (silu) y = attn::silu2_joint(y);
         float f[2];
         attn::unpair(y, f);
         r[i] = attn::pack2<F16>(f[0], f[1]);

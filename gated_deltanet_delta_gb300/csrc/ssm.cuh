@@ -22,8 +22,11 @@ constexpr int kSteps = 8;    // tokens staged at a time
 constexpr int kRows = 32;    // state rows per CTA
 
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
-// z / (1 + e^-z)
-__device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.f + __expf(fminf(-z, 80.f))); }
+// z / (1 + e^-z) as z e^z / (1 + e^z), e^z held at e^40: both ends of z's range stay in it, and go to 0 and to z.
+__device__ __forceinline__ float silu(float z) {
+    const float t = __expf(fminf(z, 40.f));
+    return z * __fdividef(t, 1.f + t);
+}
 
 // The bounds and the slot of sequence n; false (and the status) if they are malformed.
 __device__ __forceinline__ bool sequence(const SsmArgs& a, int n, long long& begin, long long& end, long long& slot, bool report) {
