@@ -872,6 +872,11 @@ extern "C" gdn_status attn_cache_append(const void* q, const void* k, const void
             GDN_ERR_INVALID_ARG, "%s: rotation overlaps an output", fn);
     const size_t sb = k_scale ? static_cast<size_t>(num_pages) * Hkv * page_size * 4 : 0;
     REQUIRE(!any_overlap(k_scale, sb, v_scale, sb), GDN_ERR_INVALID_ARG, "%s: k_scale and v_scale overlap", fn);
+    for (const float* scale : {k_scale, v_scale})
+        REQUIRE(!any_overlap(scale, sb, k_cache, cb) && !any_overlap(scale, sb, v_cache, cb) && !any_overlap(scale, sb, k, kb) &&
+                    !any_overlap(scale, sb, v, vb) && !any_overlap(scale, sb, q, qb) && !any_overlap(scale, sb, q_out, ob) &&
+                    !any_overlap(scale, sb, rotation, rb),
+                GDN_ERR_INVALID_ARG, "%s: a scale overlaps another buffer", fn);
     gdn::AppendArgs a;
     std::memset(&a, 0, sizeof(a));
     a.q = static_cast<const uint16_t*>(q);
@@ -990,8 +995,9 @@ static gdn_status ssm_check(const char* fn, gdn::SsmArgs* a, const void* x, cons
     }
     const size_t hb = static_cast<size_t>(H) * 4;
     REQUIRE(!any_overlap(out, ob, state_pool, sb) && !any_overlap(out, ob, A_log, hb) && !any_overlap(out, ob, dt_bias, hb) &&
-                !any_overlap(out, ob, D, D ? hb : 0),
-            GDN_ERR_INVALID_ARG, "%s: out overlaps another buffer", fn);
+                !any_overlap(out, ob, D, D ? hb : 0) && !any_overlap(state_pool, sb, A_log, hb) && !any_overlap(state_pool, sb, dt_bias, hb) &&
+                !any_overlap(state_pool, sb, D, D ? hb : 0),
+            GDN_ERR_INVALID_ARG, "%s: out or state_pool overlaps another buffer", fn);
     std::memset(a, 0, sizeof(*a));
     a->x = static_cast<const uint16_t*>(x);
     a->dt = static_cast<const uint16_t*>(dt);
@@ -1067,6 +1073,16 @@ extern "C" gdn_status ssm_prefill_chunked(const void* x, const void* dt, const v
     REQUIRE(aligned(workspace, 32) && aligned(state_pool, 32), GDN_ERR_INVALID_ARG, "%s: workspace and state_pool must be 32-byte aligned", fn);
     const size_t inner = static_cast<size_t>(H) * P, sb = static_cast<size_t>(pool_size) * inner * N * 4;
     REQUIRE(!any_overlap(workspace, need, out, static_cast<size_t>(T) * inner * 2) && !any_overlap(workspace, need, state_pool, sb),
+            GDN_ERR_INVALID_ARG, "%s: workspace overlaps another buffer", fn);
+    const size_t gn = static_cast<size_t>(G) * N * 2, hb = static_cast<size_t>(H) * 4;
+    const void* const in[5] = {x, dt, B, C, z};
+    const size_t least[5] = {inner * 2, static_cast<size_t>(H) * 2, gn, gn, inner * 2};
+    for (int i = 0; i < 5; ++i)
+        REQUIRE(!in[i] || !any_overlap(workspace, need, in[i], static_cast<size_t>(T - 1) * token_strides[i] * 2 + least[i]), GDN_ERR_INVALID_ARG,
+                "%s: workspace overlaps an input", fn);
+    REQUIRE(!any_overlap(workspace, need, A_log, hb) && !any_overlap(workspace, need, dt_bias, hb) && !any_overlap(workspace, need, D, D ? hb : 0) &&
+                !any_overlap(workspace, need, cu_seqlens, (static_cast<size_t>(num_seqs) + 1) * 8) &&
+                !any_overlap(workspace, need, cache_indices, static_cast<size_t>(num_seqs) * 8) && !any_overlap(workspace, need, dev_status, 4),
             GDN_ERR_INVALID_ARG, "%s: workspace overlaps another buffer", fn);
     a.cu = cu_seqlens;
     a.polls = g_prefill_wait_polls.load(std::memory_order_relaxed);
