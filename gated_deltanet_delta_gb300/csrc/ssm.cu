@@ -10,8 +10,6 @@
 namespace gdn {
 namespace {
 
-constexpr int kSegment = 8;  // segments are multiples of so many chunks
-
 // Tokens as rows of `width` elements: boxes of 64 columns and `rows` rows, 128-byte swizzle, zero fill outside.
 bool encode_tokens(CUtensorMap* map, const void* base, long long T, long long width, long long stride, unsigned rows = 128) {
     const auto fn = encode_fn();
@@ -77,9 +75,9 @@ cudaError_t chunks(SsmArgs a, long long max_len, void* workspace, cudaStream_t s
     };
     a.seg = ssm::kWhole;
     double best = 0.85 * cost(longest);
-    for (int seg = kSegment; seg < longest; seg += kSegment)
+    for (int seg = ssm::kSegment; seg < longest; seg += ssm::kSegment)
         if (cost(seg) < best) best = cost(seg), a.seg = seg;
-    const long long state = static_cast<long long>(a.H) * P * S, states = 2 * (a.T / (128 * kSegment));
+    const long long state = static_cast<long long>(a.H) * P * S, states = 2 * (a.T / (128 * ssm::kSegment));
     a.ws_states = states;
     a.ws = static_cast<float*>(workspace);
     a.ws_decay = a.ws + states * state;
@@ -109,7 +107,7 @@ void launch_ssm_steps(SsmArgs a, int S, cudaStream_t stream) {
 
 // Two states for every segment that a call of T tokens can have, and their decays.
 size_t ssm_workspace_bytes(int, long long T, int H, int P, int S) {
-    return static_cast<size_t>(2 * (T / (128 * kSegment))) * H * (static_cast<size_t>(P) * S + 1) * sizeof(float);
+    return static_cast<size_t>(2 * (T / (128 * ssm::kSegment))) * H * (static_cast<size_t>(P) * S + 1) * sizeof(float);
 }
 
 cudaError_t launch_ssm_prefill(const SsmArgs& args, int S, long long max_len, void* workspace, cudaStream_t stream) {

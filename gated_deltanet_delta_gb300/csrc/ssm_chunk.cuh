@@ -51,6 +51,7 @@ namespace ssm {
 
 constexpr int kChunk = 128;
 constexpr int kChunkNT = 640;
+constexpr int kSegment = 8;      // segments are multiples of so many chunks
 constexpr int kWhole = 1 << 24;  // chunks per segment where no sequence is cut
 // registers per thread: the launch's 96 x 5 warpgroups, parted as 104 x 4 for the workers and 64 for those that load and issue
 constexpr int kRegsLaunch = 96, kRegsWork = 104, kRegsIssue = 64;
@@ -754,7 +755,7 @@ constexpr int kAheadNT = 576;
 template <int P, int S>
 __global__ void __launch_bounds__(kAheadNT, 1) ssm_ahead_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ SsmMaps maps) {
     using K = AheadCfg<S>;
-    constexpr int BATCH = 8;  // chunks whose weights are made at once
+    constexpr int BATCH = kSegment;  // chunks whose weights are made at once: a segment ahead is whole, a number of batches
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[2], ready[2], done[2], drain;
     __shared__ Unit us;
@@ -835,20 +836,18 @@ __global__ void __launch_bounds__(kAheadNT, 1) ssm_ahead_kernel(const __grid_con
         const bool valid = hh < heads;
         // the weights of a batch within blocks of 32 tokens, and the blocks' sums; blocks count from the batch's first token on
         auto weights = [&](int batch) {
-            const int last = u.chunks - batch * BATCH, first = max(0, last - BATCH), blocks = 4 * (last - first);
-            const int head = warp & 1;
+            const int first = u.chunks - (batch + 1) * BATCH, head = warp & 1;
             if (head >= heads) return;
             const float A = -expf(a.A_log[h0 + head]) * 1.44269504f, bias = a.dt_bias[h0 + head];
             float dt[BATCH / 2];
 #pragma unroll
             for (int j = 0; j < BATCH / 2; ++j) {
                 const int b = 8 * j + (warp >> 1);
-                dt[j] = b < blocks ? bf16_to_f32(a.dt[(u.begin + first * kChunk + b * 32 + lane) * a.dt_stride + h0 + head]) : 0.f;
+                dt[j] = bf16_to_f32(a.dt[(u.begin + first * kChunk + b * 32 + lane) * a.dt_stride + h0 + head]);
             }
 #pragma unroll
             for (int j = 0; j < BATCH / 2; ++j) {
                 const int b = 8 * j + (warp >> 1);
-                if (b >= blocks) break;
                 const float d = softplus(dt[j] + bias), step = log_decay(A, d);
                 float behind = __shfl_down_sync(kFullMask, step, 1);
                 if (lane == 31) behind = 0.f;
@@ -867,13 +866,13 @@ __global__ void __launch_bounds__(kAheadNT, 1) ssm_ahead_kernel(const __grid_con
         float gone = 0.f;  // the steps behind the chunk
         bool ok = true;
         for (int i = 0; i < u.chunks; ++i) {
-            const int batch = i / BATCH, left = u.chunks - batch * BATCH;  // this batch's first chunk is number max(0, left - BATCH)
-            if (i % BATCH == 0 && left > BATCH) weights(batch + 1);
+            const int batch = i / BATCH;
+            if (i % BATCH == 0 && i + BATCH < u.chunks) weights(batch + 1);
             if (ok) {
                 ok = __all_sync(kFullMask, wait(full, i));
             }
             if (ok) {
-                const int c = min(left, BATCH) - 1 - i % BATCH;  // in the batch
+                const int c = BATCH - 1 - i % BATCH;  // in the batch
                 float weight = 0.f;
                 if (valid) {
                     const float4 sums = *reinterpret_cast<const float4*>(&block_s[batch & 1][hh][4 * c]);
