@@ -1070,7 +1070,8 @@ extern "C" gdn_status ssm_prefill_chunked(const void* x, const void* dt, const v
     const size_t need = gdn::ssm_workspace_bytes(num_seqs, T, H, P, N);
     REQUIRE(need == 0 || (workspace && workspace_bytes >= need), GDN_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed (got %zu)", fn, need,
             workspace ? workspace_bytes : size_t(0));
-    REQUIRE(aligned(workspace, 32) && aligned(state_pool, 32), GDN_ERR_INVALID_ARG, "%s: workspace and state_pool must be 32-byte aligned", fn);
+    REQUIRE(max_len <= gdn::kSsmSteps || (aligned(workspace, 32) && aligned(state_pool, 32)), GDN_ERR_INVALID_ARG,
+            "%s: workspace and state_pool must be 32-byte aligned where max_len is over %d", fn, gdn::kSsmSteps);
     const size_t inner = static_cast<size_t>(H) * P, sb = static_cast<size_t>(pool_size) * inner * N * 4;
     REQUIRE(!any_overlap(workspace, need, out, static_cast<size_t>(T) * inner * 2) && !any_overlap(workspace, need, state_pool, sb),
             GDN_ERR_INVALID_ARG, "%s: workspace overlaps another buffer", fn);

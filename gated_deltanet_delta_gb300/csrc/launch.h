@@ -55,7 +55,9 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream);
 cudaError_t launch_conv(ConvArgs a, int taps, bool f16, cudaStream_t stream);
 // One token per sequence, or sequences of few tokens each: the recurrence as it stands.  S in {64, 128}.
 void launch_ssm_steps(SsmArgs a, int S, cudaStream_t stream);
-// Sequences of any length; max_len (the longest) only chooses the kernel.
+// Sequences of any length; max_len (the longest) only chooses the kernel: token by token up to kSsmSteps tokens, in chunks (whose state pool
+// and workspace are 32-byte aligned) from there on.
+constexpr int kSsmSteps = 16;
 size_t ssm_workspace_bytes(int num_seqs, long long T, int H, int P, int S);
 cudaError_t launch_ssm_prefill(const SsmArgs& a, int S, long long max_len, void* workspace, cudaStream_t stream);
 void launch_norm(const NormArgs& a, bool f16, bool f8, cudaStream_t stream);

@@ -111,9 +111,9 @@ size_t ssm_workspace_bytes(int, long long T, int H, int P, int S) {
 }
 
 cudaError_t launch_ssm_prefill(const SsmArgs& args, int S, long long max_len, void* workspace, cudaStream_t stream) {
-    // Token by token up to 16 tokens: a chunk's time does not depend on its tokens, a step's does.  64 heads of 64, N = 128, gated, us,
+    // Up to 16 tokens: a chunk's time does not depend on its tokens, a step's does.  64 heads of 64, N = 128, gated, us,
     // steps / chunks: 32 sequences of 12 tokens 80 / 109, of 16 101 / 109, of 20 125 / 109; 128 of 16 443 / 450; 1 of 16 21 / 19.
-    if (max_len <= 16) {
+    if (max_len <= kSsmSteps) {
         launch_ssm_steps(args, S, stream);
         return cudaGetLastError();
     }

@@ -582,8 +582,8 @@ size_t ssm_prefill_workspace_size(int num_seqs, int64_t T, int H, int P, int N);
  *   x, z, dt, B, C, out   as above with T tokens
  *   cu_seqlens int64 [num_seqs + 1]
  *   max_len    the longest sequence, as far as the caller knows it: it chooses the kernel and changes no result beyond rounding
- *   workspace  ssm_prefill_workspace_size bytes, 32-byte aligned (and so is state_pool), contents need not be initialised; calls that share it must
- *              not overlap on the GPU
+ *   workspace  ssm_prefill_workspace_size bytes, contents need not be initialised; it overlaps no other argument, and calls that share it do not
+ *              overlap on the GPU.  With a max_len over 16 it and state_pool are 32-byte aligned
  * A sequence with malformed bounds sets GDN_STATUS_BAD_SEQLENS, one with a bad slot GDN_STATUS_BAD_CACHE_INDEX; it is skipped.  Rows of
  * no sequence are not written.  (Bounds that go back make sequences overlap: those that are not malformed themselves then have no
  * meaningful result.)
