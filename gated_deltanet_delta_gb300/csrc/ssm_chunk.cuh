@@ -124,8 +124,12 @@ __device__ __forceinline__ int anew(int x) {
 }
 __device__ __forceinline__ float ex2(float x) { return attn::fast_exp2(x); }
 // The logarithm (base 2) of a token's decay, for A to that base: not below -128, as ex2 is zero from there on (without the limit one step of
-// thousands takes the digits of its block's other decays, and one that is no longer a number of fp32 makes them NaN); 0 for no token.
-__device__ __forceinline__ float log_decay(float A, float dt) { return dt > 0.f ? fmaxf(A * dt, -128.f) : 0.f; }
+// thousands takes the digits of its block's other decays, and one that is no longer a number of fp32 makes them NaN); 0 for no token.  A NaN stays one.
+__device__ __forceinline__ float log_decay(float A, float dt) {
+    float a;
+    asm("max.NaN.f32 %0, %1, 0fC3000000;" : "=f"(a) : "f"(A * dt));
+    return dt > 0.f ? a : 0.f;
+}
 
 // The unit with number `rank`: one warp walks the sequences, twice: segments of a.seg chunks come first, then what is left of the
 // sequences, so that the last to start are the short ones.  Ahead (AHEAD) are all segments but each sequence's last.  A sequence of

@@ -71,3 +71,19 @@ def test_a_large_step_in_a_cut_sequence(gdn):
     y, state, status = prefill(gdn, s, max_len=5000)
     assert status == 0
     check(s, y, state, ref, True)
+
+
+@pytest.mark.parametrize("max_len", [3000, 1])
+@pytest.mark.parametrize("name", ["A_log", "dt_bias", "dt"])
+def test_what_is_no_number_shows(gdn, name, max_len):
+    """One head's decay, or one token's step, is no number: the head's outputs from there on are none, and the other head's are as they were."""
+    s = make(42, [3000], 2, 64, 1, 128)
+    clean = prefill(gdn, s, max_len=max_len)
+    s[name] = s[name].clone()
+    first = 1500 if name == "dt" else 0
+    s[name][(slice(1500, 1501), 1) if name == "dt" else 1] = float("nan")
+    y, state, status = prefill(gdn, s, max_len=max_len)
+    slot = int(s["slots"][0])
+    assert status == 0 and bool(y[first:, 1].isnan().all()) and bool(state[slot, 1].isnan().all())
+    assert torch.equal(y[:, 0], clean[0][:, 0]) and torch.equal(state[slot, 0], clean[1][slot, 0])
+    assert torch.equal(y[:first // 128 * 128], clean[0][:first // 128 * 128])
