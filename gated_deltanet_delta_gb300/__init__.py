@@ -840,7 +840,7 @@ def ssm_prefill_workspace_size(N: int, T: int, H: int, P: int, S: int) -> int:
 def ssm_prefill_chunked(x, dt, B, C, A_log, dt_bias, state_pool, cache_indices, cu_seqlens, max_len: int, D=None, z=None, out=None,
                         workspace=None, dev_status=None):
     """The scan of ssm_decode_step over packed sequences: x, z bf16 [T,H,P]; dt bf16 [T,H]; B, C bf16 [T,G,S]; cu_seqlens
-    int64 [N+1]; max_len: the longest sequence (it only chooses the kernel).  Returns out bf16 [T,H,P]."""
+    int64 [N+1]; max_len: the longest sequence (it chooses the kernel: up to 16 token by token in f32, over 16 in chunks of 128).  Returns out bf16 [T,H,P]."""
     torch = _torch_module or _torch()
     args, sizes, out, dev_status = _ssm_args(x, dt, B, C, A_log, dt_bias, state_pool, cache_indices, D, z, out, dev_status)
     T, N = x.shape[0], cache_indices.shape[0]

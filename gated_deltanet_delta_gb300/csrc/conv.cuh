@@ -8,7 +8,7 @@
 // in tiles of 32 tokens, the next eight of them loaded ahead (short_conv_kernel); long ones in tiles of 128 whose rows arrive through
 // a ring of bulk copies, so that many bytes are on their way with few registers (short_conv_ring_kernel; 23508 tokens of 8192
 // channels, bf16: 140 us, 82 % of a copy's rate; 154 us with the loads of the other, 145 us with four stages and three CTAs per SM, 151
-// us with two stages and five).  What is left above the 115 us of the bytes is the latency of sixteen warps' arithmetic: 44 % of the
+// us with two stages and five).  What is left above the 115 us of the bytes is the latency of sixteen warps' arithmetic: 47 % of the
 // issue slots, a value's own dependences the largest stall.
 //
 // The new history is written by a kernel of its own behind the first: in the same one, the CTA that reaches a sequence's end would

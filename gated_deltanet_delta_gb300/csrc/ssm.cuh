@@ -7,8 +7,9 @@
 // tokens.  A state row of N floats is split over TPR lanes, a thread has two rows and asks for all of its 16-byte pieces
 // before any arithmetic (as gdn_decode_kernel does); the tokens' inputs are staged in shared memory, kSteps at a time.
 // CTAs of 32 rows: while some load, others compute and store (of 64 rows: 48.9 and 36.9 us).  Measured, one token of 64 sequences, 64
-// heads of 64, N = 128 (270 MB): 45.1 us, 89 % of a copy's rate; 32 sequences of up to 8 tokens, no gate: 32.8 us, 62 %: the
-// arithmetic, and a sum over lanes for each output.
+// heads of 64, N = 128 (270 MB): 45.1 us, 89 % of a copy's rate; 32 sequences of up to 8 tokens, no gate: 32.8 us, 62 %, where no unit is
+// the limit: a scheduler issues in 49 % of the cycles, and its warps wait for the state, for shared memory and shuffles (a sum over lanes
+// for each output), and for the instruction before, in about equal parts.
 #pragma once
 
 #include "common.cuh"

@@ -543,7 +543,8 @@ gdn_status attn_cache_append(const void* q, const void* k, const void* v, int64_
  *   out0..2    [T, c0], [T, c1], [T, c2] of dtype, 16-byte aligned: channels 0 .. c0 - 1, the next c1, the next c2 (queries, keys
  *              and values for gdn_prefill_chunked; x, B and C for the scan).  c0 + c1 + c2 = C; c1, c2 may be 0
  * A sequence with malformed bounds (GDN_STATUS_BAD_SEQLENS) or a bad slot (GDN_STATUS_BAD_CACHE_INDEX) is skipped: its history stays
- * and, where the bounds tell which they are, its rows are not written.  Rows of no sequence are not written.
+ * and, where the bounds tell which they are, its rows are not written.  Rows of no sequence are not written.  (Where bounds go back, sequences that
+ * are not malformed themselves have no meaningful result either.)
  * Supported: taps 2, 3 or 4; c0, c1, c2 multiples of 8, C <= 2^24.
  */
 gdn_status short_conv(const void* x, int64_t x_stride, gdn_dtype dtype, const float* weight, const float* bias,
@@ -581,16 +582,21 @@ size_t ssm_prefill_workspace_size(int num_seqs, int64_t T, int H, int P, int N);
  * sequence n's, its state goes from slot to slot in place, so that a prompt may come in pieces.
  *   x, z, dt, B, C, out   as above with T tokens
  *   cu_seqlens int64 [num_seqs + 1]
- *   max_len    the longest sequence, as far as the caller knows it: it chooses the kernel and changes no result beyond rounding
+ *   max_len    the longest sequence, as far as the caller knows it: it chooses the kernel, for sequences of any length.  Up to 16 the call goes
+ *              token by token in f32 throughout, as ssm_decode_step does; over 16 it takes 128 tokens at a time, which differs for finite
+ *              inputs by the roundings below, and for others in the tokens ahead of one.  A long prompt is some 30 times faster so, a single
+ *              token slower: single tokens and prompts are best not packed in one call
  *   workspace  ssm_prefill_workspace_size bytes, contents need not be initialised; it overlaps no other argument, and calls that share it do not
  *              overlap on the GPU.  With a max_len over 16 it and state_pool are 32-byte aligned
  * A sequence with malformed bounds sets GDN_STATUS_BAD_SEQLENS, one with a bad slot GDN_STATUS_BAD_CACHE_INDEX; it is skipped.  Rows of
  * no sequence are not written.  (Bounds that go back make sequences overlap: those that are not malformed themselves then have no
  * meaningful result.)
- * Long calls work on 128 tokens at a time: an input that is not finite leaves no meaningful value in the outputs of the up to 127
- * tokens ahead of it either.  Sums and states are f32; the weights of pairs of tokens and the state that 128 tokens begin with are
- * rounded to bf16 for the outputs, dt x to 16 bits of fraction for the state.
- * A device-side wait that runs out sets GDN_STATUS_TIMEOUT; gdn_prefill_set_wait_limit bounds these waits too.
+ * 128 tokens at a time: an input that is not finite leaves no meaningful value in the outputs of the up to 127 tokens ahead of it either.
+ * Sums and states are f32; the weights of pairs of tokens (dt, the decay between them, C . B) and the state that 128 tokens begin with are rounded to
+ * bf16 for the outputs, dt x to 16 bits of fraction for the state.  A token's decay counts as 2^-128 at least, and the decay between
+ * two tokens of 32 is off by 3.4e-4 of itself at most.
+ * A device-side wait that runs out sets GDN_STATUS_TIMEOUT; gdn_prefill_set_wait_limit bounds these waits too.  A head's state is then as it was,
+ * or right.
  */
 gdn_status ssm_prefill_chunked(const void* x, const void* dt, const void* B, const void* C, const void* z,
                                const int64_t* token_strides, const float* A_log, const float* D, const float* dt_bias,
@@ -604,10 +610,12 @@ gdn_status ssm_prefill_chunked(const void* x, const void* dt, const void* B, con
  *              multiple of 8
  *   residual   [T, C] of dtype, updated in place; or NULL: r = x
  *   weight     f32 [C], 16-byte aligned
- *   out        [T, C] of out_dtype: dtype (then it may be x itself, where x is dense), or GDN_E4M3: y / s to nearest even, with
- *              s = max |y| / 448 over each group of features (1 where all are zero; at least 2^-126)
+ *   out        [T, C] of out_dtype: dtype (then it may be x itself, where x is dense), or GDN_E4M3: y (1 / s) to nearest even, with
+ *              s = max |y| / 448 over each group of features (1 where all are zero; at least 2^-126) and 1 / s rounded: where y / s is within
+ *              2^-22 of the middle between two values, either may be taken
  *   scale      f32 [T, C / group], or [T] for group 0 (one scale per row); NULL for a 16-bit out
- * Sums and y are f32.  A row with an element that is not finite has no meaningful y.
+ * Sums and y are f32.  A row with an element that is not finite has no meaningful y, nor has one whose sum of squares leaves f32's normal numbers
+ * (as it may with elements of 2^55 and more, or, with an eps of 0, where all are below 2^-55).
  * Supported: C a multiple of 8, at most 32768; group 0, 32, 64, 128 or 256, a divisor of C.
  */
 gdn_status add_rms_norm(const void* x, int64_t x_stride, void* residual, gdn_dtype dtype, const float* weight, float eps,
