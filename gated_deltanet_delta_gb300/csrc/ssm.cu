@@ -23,7 +23,7 @@ bool encode_tokens(CUtensorMap* map, const void* base, long long T, long long wi
 
 template <int P, int S>
 cudaError_t run(const SsmArgs& a, const SsmMaps& maps, unsigned grid, cudaStream_t stream) {
-    using C = ssm::ChunkCfg<S>;
+    using C = ssm::ChunkCfg<P, S>;
     static std::atomic<unsigned long long> done{0};
     cudaError_t e = raise_smem(ssm::ssm_chunk_kernel<P, S>, C::SMEM, done);
     if (e != cudaSuccess) return e;
@@ -42,7 +42,7 @@ cudaError_t run(const SsmArgs& a, const SsmMaps& maps, unsigned grid, cudaStream
 
 template <int P, int S>
 cudaError_t ahead(const SsmArgs& a, const SsmMaps& maps, unsigned grid, cudaStream_t stream) {
-    using C = ssm::AheadCfg<S>;
+    using C = ssm::AheadCfg<P, S>;
     static std::atomic<unsigned long long> done{0};
     const cudaError_t e = raise_smem(ssm::ssm_ahead_kernel<P, S>, C::SMEM, done);
     if (e != cudaSuccess) return e;

@@ -5,7 +5,7 @@
 //     S' = e^(a_1 + .. + a_Q) S + sum_s e^(a_(s+1) + .. + a_Q) dt_s x_s (x) B_s.
 // A CTA has 128 features of one segment of a sequence (two heads of 64 that share B and C, or one of 128) and walks its chunks:
 //     G = C B^T (128 x 128 x N),  Y = C S^T (128 x 128 x N),  M X (128 x 64 x 128 per head of 64),
-//     S = e^(..) S + X'^T B (128 x N x 128, twice),
+//     S = e^(..) S + X'^T B (128 x N x 128, three times),
 // M = G with the weights of its pairs and X' = the rows of x with theirs, made by threads, which also join the output, e^(..) Y + M X + D x.
 // S, G, M and Y fill TMEM (512 columns for N = 128; M X takes G's place); tiles of x, B and C come by TMA.
 //
@@ -15,22 +15,21 @@
 // rounding to bf16 may take.  A pair of tokens in two blocks has the product of two factors, the one of the row and
 // its block, the other of the column, which also saves the exponentials: one per pair only inside the blocks.
 //
-// The state is an fp32 result and is carried for thousands of chunks, so X' is held in two bf16 parts (2^-16 of each product at most); M and
-// the copy of S that Y is made from are rounded to bf16 (2^-8 of each product at most, like the output's own rounding).  Measured against 64
-// bits the state is off by 2.1e-6 to 2.5e-6 of its norm, from the two parts, and where decays are so weak that it holds a thousand tokens by
-// 3e-6, from the accumulation on the tensor core.  A third part takes the first of these away and is not worth its time here: over the pools of the
-// two prompts below, 1.2e-6 and 6e-7 become 2.4e-7 and 8e-8, 333 and 227 us become 348 and 246 (token by token, where decays are as weak,
-// rounded decays cost as much as the two parts).
+// The state is an fp32 result and is carried for thousands of chunks, so X' is held in three bf16 parts, which leave nothing of fp32 out; M and
+// the copy of S that Y is made from are rounded to bf16 (2^-8 of each product at most, like the output's own rounding).  With two parts a
+// state is off by 2.5e-6 of its norm.  Over the pools of the two prompts below, against 64 bits: 3.2e-7 and 8e-8 (two parts: 1.0e-6 and
+// 5.4e-7, in 333 and 227 us; token by token: 3.8e-7 and 3e-8).  Where one head has the tile to itself and B is half as wide, B takes the
+// weights instead of x (B' below, also in three parts): half the threads' work, and room for all of the parts.
 //
 // Roles, 640 threads.  Sixteen workers' warps: a thread is a token (a TMEM lane) of M, of Y and of X', and a feature of the state.
 // Warpgroups 0 and 1 (A) have M's diagonal blocks and the next ones and the high parts of X', 2 and 3 (B) the blocks further off, the
-// low parts and the state between two chunks; the output (D, the gate) is shared, 32 features each, and the decays' sums are made by
+// others, and the state between two chunks; the output (D, the gate) is shared, 32 features each, and the decays' sums are made by
 // the warps that have the least of M.  Warp 16 loads x, B and C, a lane of warp 17 issues what the outputs are made of and one of warp
 // 18 the state's update, and warp 19 loads the gate and stores the output.  Per chunk c
-//     A: M | X' high of c + 1 | output        B: M, X' low | state of c + 1 | output.
+//     A: M | X' high of c + 1 | output        B: M, X' middle and low | state of c + 1 | output.
 // (B's output ahead of the state: 2 to 4 % less without a gate, 4 % more with one, whose rows come late in the place of the output.)
-// Measured: four prompts of up to 8192 tokens, 64 heads of 64, N = 128, gated: 333 us, 5.2 us per chunk of the longest chain; one of
-// 16384 tokens, 32 heads of 128, N = 64: 227 us, 486 without segments (3.8 us a chunk with 32 SMs at work).  No unit bounds it: a scheduler
+// Measured: four prompts of up to 8192 tokens, 64 heads of 64, N = 128, gated: 350 us, 5.5 us per chunk of the longest chain; one of
+// 16384 tokens, 32 heads of 128, N = 64: 216 us.  No unit bounds it: a scheduler
 // issues in 48 % of the cycles, the tensor core is at work in 21 %, the rest is the latency of four warps' instructions per scheduler and
 // the hand-overs.  HBM would take 104 and 42 us, the tensor core 1.6 us a chunk.
 //
@@ -61,13 +60,16 @@ constexpr int kRegsLaunch = 96, kRegsWork = 104, kRegsIssue = 64;
 constexpr float kNoState = 1.f;        // in the place of a decay's logarithm, which is never positive: the state was not written
 constexpr uint32_t kPolls = 1u << 22;  // the built-in limit of a wait (seconds)
 
-template <int S>
+template <int P, int S>
 struct ChunkCfg {
     static constexpr uint32_t X = 32768, CB = kChunk * S * 2;  // bytes of a tile of x, of B or C
-    static constexpr int NCB = S == 64 ? 2 : 1;                // buffers of B and of C each; x has two
-    static constexpr uint32_t OFF_XH = 0;                      // X', high parts
-    static constexpr uint32_t OFF_SX = X;                      // the state's copy, then X', low parts
-    static constexpr uint32_t OFF_C = 2 * X, OFF_B = OFF_C + NCB * CB, OFF_X = OFF_B + NCB * CB, OFF_V = OFF_X + 2 * X;
+    // Whether B takes the weights of the state's products instead of x: where one head has the tile to itself and B is half as wide.
+    static constexpr bool WB = P == 128 && S == 64;
+    static constexpr int NB = S == 64 ? 2 : 1, NC = WB ? 2 : 1;  // buffers of B and of C; x has two
+    static constexpr uint32_t OFF_H = 0, OFF_S = X;              // high parts; the state's copy
+    // The middle parts come in the place of the state's copy and the low ones in C's, once those have been read; B's have places of their own.
+    static constexpr uint32_t OFF_M = WB ? X + CB : X, OFF_L = WB ? CB : 2 * X;
+    static constexpr uint32_t OFF_C = 2 * X, OFF_B = 3 * X, OFF_X = OFF_B + NB * CB, OFF_V = OFF_X + 2 * X;
     // per chunk (two in turn) and head: the decays' sums within blocks of 32 tokens, the columns' factors, dt (in the
     // exponent it would be lost beside a large sum), the blocks' sums
     static constexpr int VEC = 3 * kChunk + 16;
@@ -96,6 +98,9 @@ struct Unit {
 __device__ __forceinline__ void tma_store_2d(const void* map, int x, int y, uint32_t src) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y), "r"(src) : "memory");
 }
+__device__ __forceinline__ void tma_prefetch_2d(const void* map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+}
 // 8 consecutive 32-bit TMEM columns of this thread's lane.
 __device__ __forceinline__ void st8(uint32_t taddr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
@@ -118,6 +123,13 @@ __device__ __forceinline__ uint32_t pack_weights(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+// WB: of a row of B times its weight, which may stand for an x of zero too.
+template <bool WB>
+__device__ __forceinline__ uint32_t pack_part(attn::f32x2 p) {
+    float f[2];
+    attn::unpair(p, f);
+    return WB ? pack_weights(f[0], f[1]) : pack_bf16x2(f[0], f[1]);
 }
 // x, which the compiler does not know to be the same from chunk to chunk: what depends on it is computed where it is used, and does
 // not take registers in between (they were spilled, and each reload from memory took some 300 clocks).
@@ -183,8 +195,9 @@ __device__ __forceinline__ void find_unit(const SsmArgs& a, int rank, Unit& u) {
 
 template <int P, int S>
 __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ SsmMaps maps) {
-    using K = ChunkCfg<S>;
-    constexpr int NCB = K::NCB;
+    using K = ChunkCfg<P, S>;
+    constexpr int NB = K::NB, NC = K::NC;
+    constexpr bool WB = K::WB;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bars[2 * CK_N];
     __shared__ Unit us;
@@ -257,7 +270,7 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
 
     if (warp >= 16) {
         attn::regs_down<kRegsIssue>();  // by the whole warpgroup, then its warps part
-        int nx = 0, nbc = 0, nz = 0;    // loads that this lane has issued: chunks of x, tiles of C and B in turn, chunks of the gate
+        int nx = 0, nbc = 0, nz = 0;    // loads that this lane has issued: chunks of x, tiles of B and C in turn, chunks of the gate
         if (warp == 16 && attn::elect()) {
             // -------------------------------------------------------- loader
             bool ok = true;
@@ -270,20 +283,26 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                 tc::mbar_expect_tx(bar, halves * 16384);
                 for (int i = 0; i < halves; ++i) attn::tma_load_2d(sb + K::OFF_X + (c & 1) * K::X + i * 16384, &maps.x, h0 * P + 64 * i, row, bar);
                 ++nx;
-                if (c >= NCB) ok = wait(CK_CS, c - NCB);
+                if (c >= NB) ok = wait(CK_UPD, c - NB);
                 if (!ok) break;
                 bar = &bars[2 * CK_BC + (c & 1)];
                 tc::mbar_expect_tx(bar, K::CB);
 #pragma unroll
-                for (int i = 0; i < S / 64; ++i) attn::tma_load_2d(sb + K::OFF_C + c % NCB * K::CB + i * 16384, &maps.C, g * S + 64 * i, row, bar);
+                for (int i = 0; i < S / 64; ++i) attn::tma_load_2d(sb + K::OFF_B + c % NB * K::CB + i * 16384, &maps.B, g * S + 64 * i, row, bar);
                 ++nbc;
-                if (c >= NCB) ok = wait(CK_UPD, c - NCB);
+                if (NB > NC && c >= 1) ok = wait(CK_UPD, c - 1);  // C's own chunk before, the low parts in its place included
                 if (!ok) break;
-                bar = &bars[2 * CK_BC + (c & 1)];
                 tc::mbar_expect_tx(bar, K::CB);
 #pragma unroll
-                for (int i = 0; i < S / 64; ++i) attn::tma_load_2d(sb + K::OFF_B + c % NCB * K::CB + i * 16384, &maps.B, g * S + 64 * i, row, bar);
+                for (int i = 0; i < S / 64; ++i) attn::tma_load_2d(sb + K::OFF_C + c % NC * K::CB + i * 16384, &maps.C, g * S + 64 * i, row, bar);
                 ++nbc;
+                if (NB == 1 && c + 1 < u.chunks) {  // the next ones can start late only: from L2, then (four prompts 353 -> 348 us)
+#pragma unroll
+                    for (int i = 0; i < S / 64; ++i) {
+                        tma_prefetch_2d(&maps.B, g * S + 64 * i, row + kChunk);
+                        tma_prefetch_2d(&maps.C, g * S + 64 * i, row + kChunk);
+                    }
+                }
             }
         }
         // The products' loops are unrolled by four only: unrolled in full, their descriptors, which are the same from chunk to chunk,
@@ -293,27 +312,27 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
         if (warp == 17 && attn::elect()) {
             // -------------------------------------------------------- G, Y
             constexpr uint32_t ID_G = tc::idesc_bf16(128, 128, 0, 0, 0), ID_MX = tc::idesc_bf16(128, P, 0, 1, 0);
-            const uint64_t dC = tc::sdesc(sb + K::OFF_C, 16, 1024), dB = tc::sdesc(sb + K::OFF_B, 16, 1024), dS = tc::sdesc(sb + K::OFF_SX, 16, 1024);
+            const uint64_t dC = tc::sdesc(sb + K::OFF_C, 16, 1024), dB = tc::sdesc(sb + K::OFF_B, 16, 1024), dS = tc::sdesc(sb + K::OFF_S, 16, 1024);
             const uint64_t dX = tc::sdesc(sb + K::OFF_X, 16384, 1024);
             auto pairs = [&](int c) -> bool {  // G of chunk c
                 if (!one_wait(CK_BC, c)) return false;
-                const uint64_t off = c % NCB * (K::CB >> 4);
+                const uint64_t off = c % NB * (K::CB >> 4), coff = c % NC * (K::CB >> 4);
 #pragma unroll 1
                 for (uint32_t q = 0; q < S / 64; ++q)
 #pragma unroll
-                    for (uint32_t k = 0; k < 4; ++k) tc::mma_bf16(tm + K::TM_G, dC + off + q * 1024 + 2 * k, dB + off + q * 1024 + 2 * k, ID_G, q + k > 0);
+                    for (uint32_t k = 0; k < 4; ++k) tc::mma_bf16(tm + K::TM_G, dC + coff + q * 1024 + 2 * k, dB + off + q * 1024 + 2 * k, ID_G, q + k > 0);
                 tc::commit(&bars[2 * CK_G + (c & 1)]);
                 return true;
             };
             bool ok = true;
             for (int c = 0; c < u.chunks && ok; ++c) {
-                const uint64_t off = c % NCB * (K::CB >> 4), xoff = (c & 1) * (K::X >> 4);
+                const uint64_t coff = c % NC * (K::CB >> 4), xoff = (c & 1) * (K::X >> 4);
                 ok = (c == 0 || one_wait(CK_YF, c - 1)) && pairs(c) && one_wait(CK_S, c);
                 if (!ok) break;
 #pragma unroll 1
                 for (uint32_t q = 0; q < S / 64; ++q)
 #pragma unroll
-                    for (uint32_t k = 0; k < 4; ++k) tc::mma_bf16(tm + K::TM_Y, dC + off + q * 1024 + 2 * k, dS + q * 1024 + 2 * k, ID_G, q + k > 0);
+                    for (uint32_t k = 0; k < 4; ++k) tc::mma_bf16(tm + K::TM_Y, dC + coff + q * 1024 + 2 * k, dS + q * 1024 + 2 * k, ID_G, q + k > 0);
                 tc::commit(&bars[2 * CK_CS + (c & 1)]);
                 ok = one_wait(CK_M, c);
                 if (!ok) break;
@@ -366,23 +385,27 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
         if (warp == 18 && attn::elect()) {
             // -------------------------------------------------------- the state
             constexpr uint32_t ID_UPD = tc::idesc_bf16(128, S, 1, 1, 0);
-            const uint64_t dBm = tc::sdesc(sb + K::OFF_B, 16384, 1024), dXH = tc::sdesc(sb + K::OFF_XH, 16384, 1024), dXL = tc::sdesc(sb + K::OFF_SX, 16384, 1024);
+            const uint64_t dBm = tc::sdesc(sb + K::OFF_B, 16384, 1024), dX = tc::sdesc(sb + K::OFF_X, 16384, 1024);
+            const uint64_t dH = tc::sdesc(sb + K::OFF_H, 16384, 1024), dM = tc::sdesc(sb + K::OFF_M, 16384, 1024), dL = tc::sdesc(sb + K::OFF_L, 16384, 1024);
             bool ok = true;
             for (int c = 0; c < u.chunks && ok; ++c) {
-                const uint64_t off = c % NCB * (K::CB >> 4);
+                const uint64_t off = WB ? (c & 1) * (K::X >> 4) : c % NB * (K::CB >> 4);
+                auto update = [&](uint64_t part, uint32_t k) {
+                    tc::mma_bf16(tm + K::TM_S, (WB ? dX + off : part) + k * 128, (WB ? part : dBm + off) + k * 128, ID_UPD, 1);
+                };
                 ok = one_wait(CK_BC, c) && one_wait(CK_XH, c) && one_wait(CK_S, c);
                 if (!ok) break;
 #pragma unroll 1
                 for (uint32_t q = 0; q < 2; ++q)
 #pragma unroll
-                    for (uint32_t k = 4 * q, i = 0; i < 4; ++k, ++i) tc::mma_bf16(tm + K::TM_S, dXH + k * 128, dBm + off + k * 128, ID_UPD, 1);
+                    for (uint32_t k = 4 * q, i = 0; i < 4; ++k, ++i) update(dH, k);
                 tc::commit(&bars[2 * CK_UPH + (c & 1)]);
                 ok = one_wait(CK_XL, c);
                 if (!ok) break;
 #pragma unroll 1
-                for (uint32_t q = 0; q < 2; ++q)
+                for (uint32_t q = 0; q < 4; ++q)
 #pragma unroll
-                    for (uint32_t k = 4 * q, i = 0; i < 4; ++k, ++i) tc::mma_bf16(tm + K::TM_S, dXL + k * 128, dBm + off + k * 128, ID_UPD, 1);
+                    for (uint32_t i = 0; i < 4; ++i) update(q < 2 ? dM : dL, (4 * q + i) & 7);
                 tc::commit(&bars[2 * CK_UPD + (c & 1)]);
             }
             tc::commit(&bars[2 * CK_DRAIN + 1]);
@@ -394,7 +417,7 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
             auto land = [&](int id, int n) {
                 for (int c = max(n - 2, 0); c < n; ++c) tc::mbar_wait(&bars[2 * id + (c & 1)], c >> 1 & 1, kPolls);
             };
-            if (nbc & 1) tc::mbar_arrive(&bars[2 * CK_BC + (nbc >> 1 & 1)]);  // in the place of the last C's B, which nobody expects any more
+            if (nbc & 1) tc::mbar_arrive(&bars[2 * CK_BC + (nbc >> 1 & 1)]);  // in the place of the last B's C, which nobody expects any more
             land(CK_X, nx);
             land(CK_BC, (nbc + 1) / 2);
             land(CK_Z, nz);
@@ -617,30 +640,32 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
             for (int j = w + 1; j < 4; ++j) behind += V[3 * kChunk + j];
             return V[kChunk + t] * ex2(behind);
         };
-        // The row times its weight to X', as bf16 high parts or as what they leave.  In fp32: packed bf16 products took twice the time.
-        auto weigh = [&](int c, float weight, bool high, uint32_t to) {
+        // The row (of x, or of B) times its weight, as bf16 high parts or as the two parts of what they leave.  In fp32: packed bf16 products took twice the time.
+        auto weigh = [&](int c, float weight, bool high) {
             const attn::f32x2 ww = attn::pair(weight, weight), minus = attn::pair(-1.f, -1.f);
             const int t7 = anew(t) & 7;
+            const uint32_t from = sb + (WB ? K::OFF_B + c % NB * K::CB : K::OFF_X + (c & 1) * K::X), row = WB ? t * 128 : line;
 #pragma unroll
-            for (int q0 = 0; q0 < 8; q0 += 4) {
+            for (int q0 = WB ? side * 4 : 0, n = 0; n < (WB ? 1 : 2); q0 += 4, ++n) {
                 uint4 x[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) x[q] = attn::lds128(sb + K::OFF_X + (c & 1) * K::X + line + (((q0 + q) ^ t7) << 4));
+                for (int q = 0; q < 4; ++q) x[q] = attn::lds128(from + row + (((q0 + q) ^ t7) << 4));
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    uint32_t v[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+                    uint32_t v[4] = {x[q].x, x[q].y, x[q].z, x[q].w}, l[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const attn::f32x2 p = attn::mul2(attn::widen2(v[k]), ww);
-                        float f[2];
-                        attn::unpair(p, f);
-                        v[k] = pack_bf16x2(f[0], f[1]);
+                        attn::f32x2 p = attn::mul2(attn::widen2(v[k]), ww);
+                        v[k] = pack_part<WB>(p);
                         if (!high) {
-                            attn::unpair(attn::fma2(attn::widen2(v[k]), minus, p), f);
-                            v[k] = pack_bf16x2(f[0], f[1]);
+                            p = attn::fma2(attn::widen2(v[k]), minus, p);
+                            v[k] = pack_part<WB>(p);
+                            l[k] = pack_part<WB>(attn::fma2(attn::widen2(v[k]), minus, p));
                         }
                     }
-                    attn::sts128(sb + to + line + (((q0 + q) ^ t7) << 4), make_uint4(v[0], v[1], v[2], v[3]));
+                    const uint32_t at = sb + row + (((q0 + q) ^ t7) << 4);
+                    attn::sts128(at + (high ? K::OFF_H : K::OFF_M), make_uint4(v[0], v[1], v[2], v[3]));
+                    if (!high) attn::sts128(at + K::OFF_L, make_uint4(l[0], l[1], l[2], l[3]));
                 }
             }
             tc::fence_proxy_async();
@@ -649,17 +674,19 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
         auto high_parts = [&](int c) -> bool {
             const int rows = min(kChunk, u.len - c * kChunk);
             if (!warp_wait(CK_X, c) || !warp_wait(CK_V, c)) return false;
+            if (WB && !warp_wait(CK_BC, c)) return false;
             if (rows < kChunk || !valid) {  // what a weight of zero meets must be finite: rows behind the sequence may hold anything
-                if (!warp_wait(CK_BC, c)) return false;
+                if (!WB && !warp_wait(CK_BC, c)) return false;
                 const uint4 none = make_uint4(0, 0, 0, 0);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     if (t >= rows || !valid) attn::sts128(sb + K::OFF_X + (c & 1) * K::X + line + (q << 4), none);
-                    if (t >= rows && (S == 128 || side == 0)) attn::sts128(sb + K::OFF_B + c % NCB * K::CB + line + (q << 4), none);
+                    // of B: this thread's half of the row
+                    if (t >= rows && (S == 128 || (q ^ t & 7) >> 2 == side)) attn::sts128(sb + K::OFF_B + c % NB * K::CB + (S == 128 ? line : t * 128) + (q << 4), none);
                 }
             }
             if (c > 0 && !warp_wait(CK_UPH, c - 1)) return false;
-            weigh(c, weight_of(c), true, K::OFF_XH);
+            weigh(c, weight_of(c), true);
             warp_arrive(CK_XH, c);
             return true;
         };
@@ -681,7 +708,7 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                 tc::wait_ld();
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
-                    attn::sts128(sb + K::OFF_SX + tc::sw_chunk(ts, n0 / 8 + q, 128),
+                    attn::sts128(sb + K::OFF_S + tc::sw_chunk(ts, n0 / 8 + q, 128),
                                  make_uint4(pack_bf16x2(s[8 * q], s[8 * q + 1]), pack_bf16x2(s[8 * q + 2], s[8 * q + 3]), pack_bf16x2(s[8 * q + 4], s[8 * q + 5]),
                                             pack_bf16x2(s[8 * q + 6], s[8 * q + 7])));
 #pragma unroll
@@ -711,13 +738,13 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                 warp_arrive(CK_M, c);
                 // The sums of c + 1 go where those of c - 1 were: what is waited for here (B) or for the weights (A) stands behind the last
                 // reading of those, in the output of c - 1.
-                if (isb) {  // once the state's copy has been read its place is X's low parts'
+                if (isb) {  // once the state's copy and C have been read their places are those of the other parts of X'
                     ok = warp_wait(CK_CS, c) && warp_wait(CK_X, c);
                     if (!ok) break;
                     if (sums && c + 1 < u.chunks) decays(c + 1);
                     ok = warp_wait(CK_XH, c);
                     if (!ok) break;
-                    weigh(c, weight, false, K::OFF_SX);
+                    weigh(c, weight, false);
                     warp_arrive(CK_XL, c);
                 }
                 if (!isb && sums && c + 1 < u.chunks) decays(c + 1);
@@ -752,17 +779,22 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
 // The states that the segments ahead end in, each from a zero state (the first of a sequence from the pool's, of which it also leaves a
 // copy), and the logarithms of their decays (kNoState: gave up).  A token's weight is its decay to the segment's end, so nothing is carried from chunk to
 // chunk: the chunks are taken from the last to the first with the sum of the steps behind them, and sixteen warps make X' of one
-// (high parts in x's own tile, low parts beside it) while the products of the one before run.
-template <int S>
+// (high parts in x's own tile, middle ones beside it, low ones in the other stage's place for those) while the products of the one before run.
+template <int P, int S>
 struct AheadCfg {
-    static constexpr uint32_t X = 32768, CB = kChunk * S * 2, STAGE = 2 * X + CB;  // x (then its high parts), the low parts, B
+    static constexpr bool WB = ChunkCfg<P, S>::WB;
+    // x, its middle parts, B, with x's high parts in its own place and the low ones in that of the other stage's middle ones; or x, B, B's middle and
+    // low parts, with its high ones in its own place.
+    static constexpr uint32_t X = 32768, CB = kChunk * S * 2, STAGE = WB ? X + 3 * CB : 2 * X + CB;
+    static constexpr uint32_t OFF_B = WB ? X : 2 * X, OFF_H = WB ? X : 0, OFF_M = WB ? X + CB : X, OFF_L = WB ? X + 2 * CB : X;
     static constexpr uint32_t SMEM = 2 * STAGE + 1024;
 };
 constexpr int kAheadNT = 576;
 
 template <int P, int S>
 __global__ void __launch_bounds__(kAheadNT, 1) ssm_ahead_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ SsmMaps maps) {
-    using K = AheadCfg<S>;
+    using K = AheadCfg<P, S>;
+    constexpr bool WB = K::WB;
     constexpr int BATCH = kSegment;  // chunks whose weights are made at once: a segment ahead is whole, a number of batches
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[2], ready[2], done[2], drain;
@@ -812,7 +844,7 @@ __global__ void __launch_bounds__(kAheadNT, 1) ssm_ahead_kernel(const __grid_con
                 tc::mbar_expect_tx(&full[i & 1], halves * 16384 + K::CB);
                 for (int j = 0; j < halves; ++j) attn::tma_load_2d(to + j * 16384, &maps.x, h0 * P + 64 * j, row, &full[i & 1]);
 #pragma unroll
-                for (int j = 0; j < S / 64; ++j) attn::tma_load_2d(to + 2 * K::X + j * 16384, &maps.B, g * S + 64 * j, row, &full[i & 1]);
+                for (int j = 0; j < S / 64; ++j) attn::tma_load_2d(to + K::OFF_B + j * 16384, &maps.B, g * S + 64 * j, row, &full[i & 1]);
             }
             for (int j = max(i - 2, 0); j < i; ++j) tc::mbar_wait(&full[j & 1], j >> 1 & 1, kPolls);  // where others gave up nobody else does
         }
@@ -824,13 +856,14 @@ __global__ void __launch_bounds__(kAheadNT, 1) ssm_ahead_kernel(const __grid_con
             for (int i = 0; i < u.chunks; ++i) {
                 if (!wait(full, i) || !wait(ready, i)) break;
                 tc::fence_after();
-                const uint64_t hi = dX + (i & 1) * (K::STAGE >> 4), lo = hi + (K::X >> 4), b = lo + (K::X >> 4);
+                const uint64_t stage = dX + (i & 1) * (K::STAGE >> 4), low = (WB ? stage : dX + (~i & 1) * (K::STAGE >> 4)) + (K::OFF_L >> 4);
 #pragma unroll 1
-                for (uint32_t q = 0; q < 4; ++q)
+                for (uint32_t q = 0; q < 6; ++q)
 #pragma unroll
                     for (uint32_t j = 0; j < 4; ++j) {
                         const uint32_t k = (4 * q + j) & 7;
-                        tc::mma_bf16(tm, (q < 2 ? hi : lo) + k * 128, b + k * 128, ID, i + q + j > 0);
+                        const uint64_t part = (q < 2 ? stage + (K::OFF_H >> 4) : q < 4 ? stage + (K::OFF_M >> 4) : low) + k * 128;
+                        tc::mma_bf16(tm, WB ? stage + k * 128 : part, WB ? part : stage + (K::OFF_B >> 4) + k * 128, ID, i + q + j > 0);
                     }
                 tc::commit(&done[i & 1]);
             }
@@ -889,29 +922,40 @@ __global__ void __launch_bounds__(kAheadNT, 1) ssm_ahead_kernel(const __grid_con
                     gone += (sums.x + sums.y) + (sums.z + sums.w);
                 }
                 const attn::f32x2 ww = attn::pair(weight, weight), minus = attn::pair(-1.f, -1.f);
-                const uint32_t tile = sb + (i & 1) * K::STAGE + side * 16384 + t * 128;
-                uint4 x[4];
+                constexpr int NQ = WB ? 2 : 4;  // pieces of 16 bytes: of half a row of x, of a quarter of B's
+                const int q0 = WB ? wg * 2 : (wg >> 1) * 4;
+                const uint32_t line = sb + (WB ? 0 : side * 16384) + t * 128, tile = line + (i & 1) * K::STAGE;
+                uint4 x[NQ], low[NQ];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) x[q] = valid ? attn::lds128(tile + ((((wg >> 1) * 4 + q) ^ (t & 7)) << 4)) : make_uint4(0, 0, 0, 0);
+                for (int q = 0; q < NQ; ++q) x[q] = valid ? attn::lds128(tile + K::OFF_H + (((q0 + q) ^ (t & 7)) << 4)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t v[4] = {x[q].x, x[q].y, x[q].z, x[q].w}, l[4];
+                for (int q = 0; q < NQ; ++q) {
+                    uint32_t v[4] = {x[q].x, x[q].y, x[q].z, x[q].w}, l[4], r[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const attn::f32x2 p = attn::mul2(attn::widen2(v[k]), ww);
-                        float f[2];
-                        attn::unpair(p, f);
-                        v[k] = pack_bf16x2(f[0], f[1]);
-                        attn::unpair(attn::fma2(attn::widen2(v[k]), minus, p), f);
-                        l[k] = pack_bf16x2(f[0], f[1]);
+                        attn::f32x2 p = attn::mul2(attn::widen2(v[k]), ww);
+                        v[k] = pack_part<WB>(p);
+                        p = attn::fma2(attn::widen2(v[k]), minus, p);
+                        l[k] = pack_part<WB>(p);
+                        r[k] = pack_part<WB>(attn::fma2(attn::widen2(l[k]), minus, p));
                     }
-                    const uint32_t at = tile + ((((wg >> 1) * 4 + q) ^ (t & 7)) << 4);
-                    attn::sts128(at, make_uint4(v[0], v[1], v[2], v[3]));
-                    attn::sts128(at + K::X, make_uint4(l[0], l[1], l[2], l[3]));
+                    attn::sts128(tile + K::OFF_H + (((q0 + q) ^ (t & 7)) << 4), make_uint4(v[0], v[1], v[2], v[3]));
+                    x[q] = make_uint4(l[0], l[1], l[2], l[3]);
+                    low[q] = make_uint4(r[0], r[1], r[2], r[3]);
                 }
-                tc::fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&ready[i & 1]);
+                // The products of the chunk before have its middle parts and, in the place of this one's, its low parts.
+                if (!WB && i > 0) ok = __all_sync(kFullMask, wait(done, i - 1));
+                if (ok) {
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) {
+                        const uint32_t at = ((q0 + q) ^ (t & 7)) << 4;
+                        attn::sts128(tile + K::OFF_M + at, x[q]);
+                        attn::sts128((WB ? tile : line + (~i & 1) * K::STAGE) + K::OFF_L + at, low[q]);
+                    }
+                    tc::fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&ready[i & 1]);
+                }
             }
             if (i % BATCH == BATCH - 1) together();  // all warps come here, those that gave up too
         }

@@ -593,7 +593,7 @@ size_t ssm_prefill_workspace_size(int num_seqs, int64_t T, int H, int P, int N);
  * meaningful result.)
  * 128 tokens at a time: an input that is not finite leaves no meaningful value in the outputs of the up to 127 tokens ahead of it either.
  * Sums and states are f32; the weights of pairs of tokens (dt, the decay between them, C . B) and the state that 128 tokens begin with are rounded to
- * bf16 for the outputs, dt x to 16 bits of fraction for the state.  A token's decay counts as 2^-128 at least, and the decay between
+ * bf16 for the outputs, for the state nothing is.  A token's decay counts as 2^-128 at least, and the decay between
  * two tokens of 32 is off by 3.4e-4 of itself at most.
  * A device-side wait that runs out sets GDN_STATUS_TIMEOUT; gdn_prefill_set_wait_limit bounds these waits too.  A head's state is then as it was,
  * or right.
