@@ -6,7 +6,7 @@
 // Each value is read once and written once: the bound is HBM.  blockDim.x threads hold a row in registers, R
 // pieces of eight features each, blockDim.y short rows per CTA.  The sum of squares is taken over the rounded r, in fp32.
 // A row waits for its loads and then for its sums, so what counts is how many rows an SM has at once: 32 registers a thread, one or two
-// pieces.  Measured, 16383 rows of 5120, bf16 to e4m3 by groups of 128: 97 us, 90 % of a copy's rate (122 us with four pieces a
+// pieces.  Measured, 16383 rows of 5120, bf16 to e4m3 by groups of 128: 100 us, 88 % of a copy's rate (122 us with four pieces a
 // thread, 160 us with rows through a ring of bulk copies, 130 us with CTAs that stay and load the next row ahead).
 #pragma once
 
@@ -49,20 +49,21 @@ __device__ __forceinline__ attn::f32x2 widen(uint32_t w) {
     const float2 f = attn::unpack2<F16>(w);
     return attn::pair(f.x, f.y);
 }
-__device__ __forceinline__ float scale_of(float amax) { return amax > 0.f ? fmaxf(amax * (1.f / 448.f), 1.17549435e-38f) : 1.f; }
-// 1 / s by one step of Newton's iteration on the approximation: within 2^-23.
-__device__ __forceinline__ float inverse(float s) {
-    const float r = attn::fast_rcp(s);
-    return fmaf(r, fmaf(-s, r, 1.f), r);
+// amax / 448: the product with 1 / 448 and what that leaves.
+__device__ __forceinline__ float scale_of(float amax) {
+    const float q = amax * (1.f / 448.f);
+    return amax > 0.f ? fmaxf(fmaf(fmaf(-448.f, q, amax), 1.f / 448.f, q), 1.17549435e-38f) : 1.f;
 }
-// Eight values to e4m3, times 1 / scale: with that rounded, a quotient within 2^-22 of the middle between two may go to either (divisions
-// took 22 us more).
-__device__ __forceinline__ uint2 to_e4m3(const float (&f)[8], float up) {
+// Eight values over the scale to e4m3: the quotient is the product with up, about 1 / scale, and what that leaves times up again, which makes it fp32's
+// (by the product alone a quotient within 2^-22 of the middle between two went to either; divisions took 22 us more).
+__device__ __forceinline__ uint2 to_e4m3(const float (&f)[8], float scale, float up) {
     uint32_t q[4];
+    const attn::f32x2 ss = attn::pair(-scale, -scale), uu = attn::pair(up, up);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         float g[2];
-        attn::unpair(attn::mul2(attn::pair(f[2 * j], f[2 * j + 1]), attn::pair(up, up)), g);
+        const attn::f32x2 y = attn::pair(f[2 * j], f[2 * j + 1]), p = attn::mul2(y, uu);
+        attn::unpair(attn::fma2(attn::fma2(p, ss, y), uu, p), g);
         q[j] = __nv_cvt_float2_to_fp8x2(make_float2(g[0], g[1]), __NV_SATFINITE, __NV_E4M3);
     }
     return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
@@ -128,7 +129,7 @@ __device__ __forceinline__ void row(const NormArgs& a, long long t, bool here, u
                 for (int o = a.lanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
                 const float scale = scale_of(m);
                 if (on) {
-                    __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + t * a.C + p * 8), to_e4m3(f, inverse(scale)));
+                    __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + t * a.C + p * 8), to_e4m3(f, scale, attn::fast_rcp(scale)));
                     if (p % a.lanes == 0) a.scale[t * (pieces / a.lanes) + p / a.lanes] = scale;
                 }
             }
@@ -137,14 +138,14 @@ __device__ __forceinline__ void row(const NormArgs& a, long long t, bool here, u
     if constexpr (F8) {
         if (a.lanes == 0) {
             amax = row_join<true>(amax, tops);
-            const float scale = scale_of(amax), up = inverse(scale);
+            const float scale = scale_of(amax), up = attn::fast_rcp(scale);
             if (here && threadIdx.x == 0) a.scale[t] = scale;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 if (!here || piece(i) >= pieces) continue;
                 float f[8];
                 normed(i, f);
-                __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + t * a.C + piece(i) * 8), to_e4m3(f, up));
+                __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + t * a.C + piece(i) * 8), to_e4m3(f, scale, up));
             }
         }
     }

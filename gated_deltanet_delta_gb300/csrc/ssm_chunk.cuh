@@ -31,7 +31,7 @@
 // Measured: four prompts of up to 8192 tokens, 64 heads of 64, N = 128, gated: 350 us, 5.5 us per chunk of the longest chain; one of
 // 16384 tokens, 32 heads of 128, N = 64: 216 us.  No unit bounds it: a scheduler
 // issues in 48 % of the cycles, the tensor core is at work in 21 %, the rest is the latency of four warps' instructions per scheduler and
-// the hand-overs.  HBM would take 104 and 42 us, the tensor core 1.6 us a chunk.
+// the hand-overs.  HBM would take 104 and 42 us, the tensor core 1.9 us a chunk.
 //
 // Segments.  A sequence is a chain, and a call with few sequences and heads has fewer chains than the GPU has SMs.  Long sequences are
 // cut into segments that run side by side: a launch ahead (ssm_ahead_kernel) forms the states that all segments but the last end in

@@ -610,9 +610,8 @@ gdn_status ssm_prefill_chunked(const void* x, const void* dt, const void* B, con
  *              multiple of 8
  *   residual   [T, C] of dtype, updated in place; or NULL: r = x
  *   weight     f32 [C], 16-byte aligned
- *   out        [T, C] of out_dtype: dtype (then it may be x itself, where x is dense), or GDN_E4M3: y (1 / s) to nearest even, with
- *              s = max |y| / 448 over each group of features (1 where all are zero; at least 2^-126) and 1 / s rounded: where y / s is within
- *              2^-22 of the middle between two values, either may be taken
+ *   out        [T, C] of out_dtype: dtype (then it may be x itself, where x is dense), or GDN_E4M3: y / s, s and the quotient to f32, to nearest even, with
+ *              s = max |y| / 448 over each group of features (1 where all are zero; at least 2^-126)
  *   scale      f32 [T, C / group], or [T] for group 0 (one scale per row); NULL for a 16-bit out
  * Sums and y are f32.  A row with an element that is not finite has no meaningful y, nor has one whose sum of squares leaves f32's normal numbers
  * (as it may with elements of 2^55 and more, or, with an eps of 0, where all are below 2^-55).
