@@ -66,7 +66,7 @@ cudaError_t chunks(SsmArgs a, long long max_len, void* workspace, cudaStream_t s
     // included, and a start.  (Four prompts of 64, 43, 22 and 56 chunks and 32 units each: 343 us
     // whole, 362 to 428 in segments of 8 to 48; one of 128 chunks: 486 whole, 272, 234, 296, 228, 248, 290 in segments of 8, 16, .. 48.
     // That is the range that it is measured in.  The sum of the states that a segment starts from is not in it, and counts from 192 chunks on:
-    // one prompt of 64 heads of 64, N = 128, of 128, 192, 256, 512, 1024 chunks takes 247, 602, 778, 2250, 6810 us.)
+    // one prompt of 64 heads of 64, N = 128, of 128, 192, 256, 512, 1024 chunks takes 273, 628, 818, 2310, 6900 us.)
     const long long per_seg = static_cast<long long>(a.G) * ((a.H / a.G * P + 127) / 128);
     const double total = static_cast<double>((a.T + 127) / 128), share = total * per_seg / sms;
     const double longest = static_cast<double>((std::min(std::max(max_len, 1LL), a.T) + 127) / 128);

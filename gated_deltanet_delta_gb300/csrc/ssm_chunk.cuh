@@ -30,13 +30,13 @@
 // (B's output ahead of the state: 2 to 4 % less without a gate, 4 % more with one, whose rows come late in the place of the output.)
 // Measured: four prompts of up to 8192 tokens, 64 heads of 64, N = 128, gated: 350 us, 5.5 us per chunk of the longest chain; one of
 // 16384 tokens, 32 heads of 128, N = 64: 216 us.  No unit bounds it: a scheduler
-// issues in 48 % of the cycles, the tensor core is at work in 21 %, the rest is the latency of four warps' instructions per scheduler and
+// issues in 49 % of the cycles, the tensor core is at work in 24 %, the rest is the latency of four warps' instructions per scheduler and
 // the hand-overs.  HBM would take 104 and 42 us, the tensor core 1.9 us a chunk.
 //
 // Segments.  A sequence is a chain, and a call with few sequences and heads has fewer chains than the GPU has SMs.  Long sequences are
 // cut into segments that run side by side: a launch ahead (ssm_ahead_kernel) forms the states that all segments but the last end in
 // from a zero state (the first from the pool's), and a segment starts from the sum of those ahead of it with their decays.  Those sums
-// grow with the square of the segments: one prompt of 16384, 32768 and 131072 tokens, 64 heads of 64, N = 128: 247, 778 and 6810 us.
+// grow with the square of the segments: one prompt of 16384, 32768 and 131072 tokens, 64 heads of 64, N = 128: 273, 818 and 6900 us.
 //
 // Every wait is bounded (attn_tiles.cuh): one that runs out sets GDN_STATUS_TIMEOUT and the CTA's limit of polls to 0.  A CTA that gave
 // up ends behind one more bounded wait for each product and copy that it has in flight, and leaves the pool's state as it is; one whose
@@ -148,7 +148,7 @@ __device__ __forceinline__ float log_decay(float A, float dt) {
 
 // The unit with number `rank`: one warp walks the sequences, twice: segments of a.seg chunks come first, then what is left of the
 // sequences, so that the last to start are the short ones.  The walk has 32 sequences at a time and all of its SM wait: of 32 tokens each (64 heads
-// of 64, N = 128) 256, 1024 and 4096 sequences take 0.83, 4.4 and 35 ms.  Ahead (AHEAD) are all segments but each sequence's last.  A sequence of
+// of 64, N = 128) 256, 1024 and 4096 sequences take 0.84, 4.4 and 36 ms.  Ahead (AHEAD) are all segments but each sequence's last.  A sequence of
 // more than a.seg chunks has states in the workspace: the pool's, then one for each segment ahead.
 template <bool AHEAD>
 __device__ __forceinline__ void find_unit(const SsmArgs& a, int rank, Unit& u) {
