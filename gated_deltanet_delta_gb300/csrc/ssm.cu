@@ -62,18 +62,19 @@ cudaError_t chunks(SsmArgs a, long long max_len, void* workspace, cudaStream_t s
         !encode_tokens(&maps.z, a.z ? a.z : a.x, a.T, inner, a.z ? a.z_stride : a.x_stride, 32))
         return cudaErrorInvalidValue;
     // Segments.  In chunk times of one SM: `share` is the work over the SMs, a chain takes as long as it is, units that are
-    // more than the SMs end unevenly by about half a unit, and the launch ahead costs two fifths of what it covers, its uneven end
-    // included, and a start.  (Four prompts of 64, 43, 22 and 56 chunks and 32 units each: 343 us
-    // whole, 362 to 428 in segments of 8 to 48; one of 128 chunks: 486 whole, 272, 234, 296, 228, 248, 290 in segments of 8, 16, .. 48.
-    // That is the range that it is measured in.  The sum of the states that a segment starts from is not in it, and counts from 192 chunks on:
-    // one prompt of 64 heads of 64, N = 128, of 128, 192, 256, 512, 1024 chunks takes 273, 628, 818, 2310, 6900 us.)
+    // more than the SMs end unevenly by about half a unit, the launch ahead costs two fifths of what it covers, its uneven end
+    // included, and a start, and a segment starts from as many states as there are segments ahead, a third of a chunk time each where all SMs read
+    // (N = 128), a quarter else.  Measured, us: four prompts of 64, 43, 22 and 56 chunks and 32 units each: 348 whole, 381 to 449 in segments of 8
+    // to 48; one of 128 chunks, N = 64: 479 whole, 260, 221, 293, 220, 242, 283, 367 in segments of 8, 16, .. 48, 64; N = 128, one of 192: 930
+    // whole, 633, 455, 416, 508, 467, 391, 481; of 256: 1237 whole, 818, 623, 602, 542, 616, 725, 510; of 512: 2459 whole, 2310, 1237,
+    // 1082, 1076, 987, 1105, 1008, and 989 in segments of 128.
     const long long per_seg = static_cast<long long>(a.G) * ((a.H / a.G * P + 127) / 128);
     const double total = static_cast<double>((a.T + 127) / 128), share = total * per_seg / sms;
     const double longest = static_cast<double>((std::min(std::max(max_len, 1LL), a.T) + 127) / 128);
     auto cost = [&](double seg) {
-        const double units = total / longest * std::max(1.0, static_cast<double>(static_cast<long long>((longest + seg - 1) / seg))) * per_seg;
-        const double start = seg < longest ? 0.4 * share * (longest - seg) / longest + 3.0 : 0.0;
-        return (units <= sms ? seg : std::max(seg, share + seg / 2)) + start;
+        const double parts = std::max(1.0, static_cast<double>(static_cast<long long>((longest + seg - 1) / seg))), units = total / longest * parts * per_seg;
+        const double start = seg < longest ? 0.4 * share * (longest - seg) / longest + 3.0 : 0.0, states = (parts - 1) * S / 128;
+        return (units <= sms ? seg + 0.25 * states : std::max(seg, share + seg / 2) + 0.35 * states * units / sms) + start;
     };
     a.seg = ssm::kWhole;
     double best = 0.85 * cost(longest);

@@ -36,7 +36,8 @@
 // Segments.  A sequence is a chain, and a call with few sequences and heads has fewer chains than the GPU has SMs.  Long sequences are
 // cut into segments that run side by side: a launch ahead (ssm_ahead_kernel) forms the states that all segments but the last end in
 // from a zero state (the first from the pool's), and a segment starts from the sum of those ahead of it with their decays.  Those sums
-// grow with the square of the segments: one prompt of 16384, 32768 and 131072 tokens, 64 heads of 64, N = 128: 273, 818 and 6900 us.
+// grow with the square of the segments, which ssm.cu keeps few: one prompt of 16384, 32768 and 131072 tokens, 64 heads of 64, N = 128, takes 271,
+// 506 and 1901 us.
 //
 // Every wait is bounded (attn_tiles.cuh): one that runs out sets GDN_STATUS_TIMEOUT and the CTA's limit of polls to 0.  A CTA that gave
 // up ends behind one more bounded wait for each product and copy that it has in flight, and leaves the pool's state as it is; one whose

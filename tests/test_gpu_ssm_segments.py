@@ -95,3 +95,16 @@ def test_captured_with_two_workspaces_that_both_use(gdn):
     for _, out, state, want, status, ws, state_bytes, _ in calls:
         assert status.item() == 0 and torch.equal(out, want[0]) and torch.equal(state, want[1])
         assert states_left(ws, state_bytes) >= 5
+
+
+def test_long_prompts_have_few_segments(gdn):
+    """A segment starts from the sum of the states of all segments ahead of it: in 64 segments these sums took two thirds of the call."""
+    T, H, P, S = 65536, 64, 64, 64
+    z = lambda *d: torch.zeros(d, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    s = {"lens": [T], "x": z(T, H, P), "B": z(T, 1, S)}
+    ws, state_bytes = workspace(gdn, s)
+    state, status = torch.ones((1, H, P, S), device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = gdn.ssm_prefill_chunked(s["x"], z(T, H), s["B"], z(T, 1, S), torch.full((H,), -30.0, device="cuda"), torch.full((H,), -30.0, device="cuda"), state,
+                                torch.zeros(1, dtype=torch.int64, device="cuda"), torch.tensor([0, T], device="cuda"), T, workspace=ws, dev_status=status)
+    assert status.item() == 0 and not bool(y.any()) and bool((state == 1).all())  # steps of e^-30, of which nothing is seen in fp32
+    assert 2 <= states_left(ws, state_bytes) <= 24
