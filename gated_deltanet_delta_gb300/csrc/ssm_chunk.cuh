@@ -308,8 +308,8 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
         }
         // The products' loops are unrolled by four only: unrolled in full, their descriptors, which are the same from chunk to chunk,
         // were kept in more registers than there are.  Two lanes issue: one what the outputs are made of, the other the state's update, so that neither chain waits for the
-        // other's barriers.  What must be in order between the two is so by those: a chunk's update ends behind its Y = C S^T, whose
-        // copy's place the low parts take, and that behind its G.
+        // other's barriers.  What must be in order between the two is so by those: a chunk's update ends behind its Y = C S^T, whose operands'
+        // places the middle and low parts take, and that behind its G.
         if (warp == 17 && attn::elect()) {
             // -------------------------------------------------------- G, Y
             constexpr uint32_t ID_G = tc::idesc_bf16(128, 128, 0, 0, 0), ID_MX = tc::idesc_bf16(128, P, 0, 1, 0);
@@ -571,9 +571,8 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
         bool ok = true;
         if (isb) {  // the unit's first state: the pool's (for the first of several segments its copy), or what the segments ahead add up to
             const float* src = (u.parts == 1 ? a.state + u.slot * state() : a.ws + u.ws * state()) + srow();
-            // The first segment's copy is there if its own state is.  The same for all of the CTA's heads, which one CTA ahead has.
-            for (int j = 0; j < (u.k == 0 && u.parts > 1 ? 1 : u.k); ++j) ok = ok && a.ws_decay[(u.ws + 1 + j) * a.H + h0] != kNoState;
-            if (!ok) most_polls = 0;
+            // The first segment's copy is there if its own state is.  (The same for all of the CTA's heads, which one CTA ahead has.)
+            if (u.k == 0 && u.parts > 1) ok = a.ws_decay[(u.ws + 1) * a.H + h0] != kNoState;
             float s[S / 2];
 #pragma unroll
             for (int q = 0; q < S / 2; q += 8) {
@@ -584,9 +583,11 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                     for (int i = 0; i < 8; ++i) s[q + i] = 0.f;
                 }
             }
-            for (int j = 0; j < u.k && there; ++j) {
+            for (int j = 0; j < u.k; ++j) {
                 const long long at = u.ws + 1 + j;
-                const float f = ex2(a.ws_decay[at * a.H + h0 + ph]);
+                const float decay = a.ws_decay[at * a.H + h0 + (there ? ph : 0)], f = ex2(decay);
+                ok = ok && decay != kNoState;
+                if (!there) continue;
                 const float* from = a.ws + at * state() + srow();
 #pragma unroll
                 for (int q = 0; q < S / 2; q += 8) {
@@ -596,6 +597,7 @@ __global__ void __launch_bounds__(kChunkNT, 1) ssm_chunk_kernel(const __grid_con
                     for (int i = 0; i < 8; ++i) s[q + i] = fmaf(f, s[q + i], v[i]);
                 }
             }
+            if (!ok) most_polls = 0;
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < S / 32; ++i) {
